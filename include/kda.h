@@ -63,7 +63,8 @@ typedef enum {
     KDA_ERR_UNSUPPORTED = 2,  /* valid but not implemented (e.g. dk = 96)          */
     KDA_ERR_CUDA = 3,         /* a CUDA launch or runtime call failed               */
     KDA_ERR_TIMEOUT = 4,      /* a bounded device-side wait gave up                 */
-    KDA_ERR_DEVICE = 5        /* the device reported malformed input (cu_seqlens)   */
+    KDA_ERR_DEVICE = 5        /* the device reported malformed input (cu_seqlens,
+                                 slots, positions)                              */
 } kda_status_t;
 
 typedef enum { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype_t;
@@ -208,6 +209,119 @@ kda_status_t kda_decode_step_gated(const void *q, const void *k, const void *v,
                                    float g_min, float *S, const void *gate, const float *norm_w,
                                    float eps, int N, int H, int dk, int dv, kda_dtype_t io_dt,
                                    void *y, kda_stream_t stream);
+
+/*
+ * Linear attention with one decay per head (the sibling of KDA without the delta rule and with
+ * a scalar decay), per sequence and head:
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T        o_t = S_t^T q_t        (no scale on q)
+ * The log decay g is fp32, read as [T, H] (one value a token and head) when g_per_token is
+ * nonzero, else as [H] (one fixed value a head).  g = -inf is a decay of exactly zero: the
+ * state forgets everything before that token.  g is meant to be <= 0; larger values are
+ * computed as written while e^{sums of g} stay in the fp32 range.
+ * Additional conventions of these entry points:
+ *   - q, k, v and dout are [T, H, d] with the heads of a token contiguous and a token stride of
+ *     ld elements (ld >= H d, a multiple of 16 bytes), so a view of a fused projection's output
+ *     can be passed as it is; every tensor written is contiguous.
+ *   - g, dg, slots and positions need 4-byte alignment only.
+ *   - No output may overlap an input, except S_out, which may be the same buffer as S0.
+ */
+
+/*
+ * kda_linear_fwd_chunked -- the forward over N packed sequences.
+ *   S0     : [N, H, dk, dv] fp32 initial states, or NULL for zeros
+ *   S_out  : [N, H, dk, dv] fp32 final states (written), or NULL
+ *   cu_seqlens, N, T_total : as kda_fwd_chunked (a sequence may be empty: its S_out is its S0)
+ *   o      : [T_total, H, dv] io_dt (written)
+ *   workspace : device scratch of kda_linear_fwd_workspace_size(...) bytes (NULL when 0)
+ * Long sequences are cut into segments that run in parallel: one launch forms each segment's
+ * contribution to the state, one the states at the segment starts, one the outputs.
+ */
+size_t kda_linear_fwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv,
+                                     kda_dtype_t io_dt);
+kda_status_t kda_linear_fwd_chunked(const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                                    const void *v, int64_t v_ld, const float *g, int g_per_token,
+                                    const float *S0, float *S_out, const int32_t *cu_seqlens,
+                                    int N, int64_t T_total, int H, int dk, int dv,
+                                    kda_dtype_t io_dt, void *o, void *workspace, size_t ws_bytes,
+                                    kda_stream_t stream);
+
+/*
+ * kda_linear_bwd -- gradients of kda_linear_fwd_chunked's outputs.  For a loss with gradient
+ * dout [T_total, H, dv] io_dt on o and dS_out [N, H, dk, dv] fp32 (or NULL) on S_out, with
+ * D_t = dL/dS_t running backwards (D_t = e^{g_{t+1}} D_{t+1} + q_t do_t^T, dS_out added at the
+ * end), writes
+ *   dq = S_t do_t, dk = D_t v_t : [T_total, H, dk] io_dt      dv = D_t^T k_t : [T_total, H, dv]
+ *   dg  : fp32, [T_total, H] when g_per_token, else [H] (summed over all tokens), or NULL
+ *   dS0 : [N, H, dk, dv] fp32, or NULL when not wanted
+ * Deterministic.  Gradients with respect to g = -inf are computed as for any other g.
+ */
+size_t kda_linear_bwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv,
+                                     kda_dtype_t io_dt);
+kda_status_t kda_linear_bwd(const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                            const void *v, int64_t v_ld, const float *g, int g_per_token,
+                            const float *S0, const int32_t *cu_seqlens, int N, int64_t T_total,
+                            int H, int dk, int dv, kda_dtype_t io_dt, const void *dout,
+                            int64_t dout_ld, const float *dS_out, void *dq, void *dk_out,
+                            void *dv_out, float *dg, float *dS0, void *workspace,
+                            size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * kda_linear_decode_step -- one token of the recurrence for N requests, states in place.
+ *   q, k, v, g : one token a request ([N, H, d] with token strides; g as above, [N, H] or [H])
+ *   S      : [n_slots, H, dk, dv] fp32 pool of states, read and overwritten
+ *   slots  : device int32 [N], the pool row of each request, or NULL for row n = request n
+ *            (then n_slots >= N).  A negative slot marks an unused row of the batch: no state is
+ *            touched and its o is zero.  No two requests may name the same slot.  A slot
+ *            >= n_slots counts as unused and kda_device_status() returns KDA_ERR_DEVICE.
+ *   o      : [N, H, dv] io_dt (written)
+ */
+kda_status_t kda_linear_decode_step(const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                                    const void *v, int64_t v_ld, const float *g, int g_per_token,
+                                    float *S, const int32_t *slots, int n_slots, int N, int H,
+                                    int dk, int dv, kda_dtype_t io_dt, void *o,
+                                    kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope -- RMS norm of every query and key head and the rotation of its first
+ * rot_dim channels by the token's position, in one pass:
+ *     n = w x / sqrt(mean(x^2) + eps)                    over the d channels of a head
+ *     (y_a, y_b) = (n_a cos - n_b sin, n_a sin + n_b cos)  for each pair (a, b) of channels
+ * Pair p < rot_dim / 2 is (p, p + rot_dim / 2), or (2p, 2p + 1) when interleaved is nonzero, and
+ * its angle is row positions[t] of the table.  (An L2 norm is this norm with w = 1 / sqrt(d)
+ * and eps divided by d.)
+ *   q : [T, Hq, d], k : [T, Hk, d] io_dt with token strides q_ld, k_ld (as above); Hk may be 0
+ *   wq, wk   : [d] fp32 weights, or NULL for ones
+ *   cos_sin  : [n_pos, rot_dim] fp32, a row holding rot_dim / 2 cosines then as many sines;
+ *              NULL when rot_dim = 0
+ *   positions: device int32 [T], each in [0, n_pos); NULL for positions 0 .. T - 1 (n_pos >= T).
+ *              A token whose position is outside is not rotated and kda_device_status() returns
+ *              KDA_ERR_DEVICE.
+ *   q_out, k_out : [T, Hq, d], [T, Hk, d] contiguous (written); may be q, k where those are
+ *              contiguous.
+ * d must be 64 or 128; rot_dim a multiple of 16 from 0 to d.
+ */
+kda_status_t kda_qk_norm_rope(const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                              const float *wq, const float *wk, float eps, const float *cos_sin,
+                              int64_t n_pos, const int32_t *positions, int rot_dim,
+                              int interleaved, void *q_out, void *k_out, int64_t T, int Hq,
+                              int Hk, int d, kda_dtype_t io_dt, kda_stream_t stream);
+
+/*
+ * kda_qk_norm_rope_bwd -- its gradients, from the inputs q, k and the upstream gradients
+ * dyq [T, Hq, d], dyk [T, Hk, d] (contiguous, io_dt) on q_out, k_out:
+ *   dq, dk   : [T, Hq, d], [T, Hk, d] io_dt, contiguous (written); may be dyq, dyk
+ *   dwq, dwk : [d] fp32, summed over tokens and heads, or NULL when not wanted
+ *   workspace: device scratch of kda_qk_norm_rope_bwd_workspace_size(d) bytes
+ */
+size_t kda_qk_norm_rope_bwd_workspace_size(int d);
+kda_status_t kda_qk_norm_rope_bwd(const void *q, int64_t q_ld, const void *k, int64_t k_ld,
+                                  const void *dyq, const void *dyk, const float *wq,
+                                  const float *wk, float eps, const float *cos_sin,
+                                  int64_t n_pos, const int32_t *positions, int rot_dim,
+                                  int interleaved, void *dq, void *dk_out, float *dwq,
+                                  float *dwk, int64_t T, int Hq, int Hk, int d,
+                                  kda_dtype_t io_dt, void *workspace, size_t ws_bytes,
+                                  kda_stream_t stream);
 
 /*
  * kda_quantile_balance -- quantile-balancing update of a mixture-of-experts router's expert

@@ -46,6 +46,14 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
         if (!aligned16(p)) return fail(KDA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name); \
     } while (0)
 
+// Arrays of 4-byte values read one by one (so that a slice of a longer one can be passed).
+#define KDA_REQUIRE_WORDS(p, name)                                                      \
+    do {                                                                                \
+        if ((p) == nullptr) return fail(KDA_ERR_INVALID_ARG, "%s is NULL", name);       \
+        if (reinterpret_cast<uintptr_t>(p) & 3u)                                        \
+            return fail(KDA_ERR_INVALID_ARG, "%s is not 4-byte aligned", name);         \
+    } while (0)
+
 #define KDA_OPTIONAL_PTR(p, name)                                                  \
     do {                                                                           \
         if ((p) != nullptr && !aligned16(p))                                       \
@@ -91,7 +99,7 @@ kda_status_t set_last_error(kda_status_t s, const char* msg) {
 
 extern "C" {
 
-int kda_version(void) { return 200; /* 0.2.0: backward, softplus variant, output step, quantile balancing */ }
+int kda_version(void) { return 300; /* 0.3.0: per-head-decay linear attention, query/key norm with rotation */ }
 
 const char* kda_status_string(kda_status_t s) {
     switch (s) {
@@ -407,6 +415,267 @@ kda_status_t kda_decode_step_gated(const void* q, const void* k, const void* v,
     return KDA_OK;
 }
 
+// Checks shared by the entry points of the per-head-decay linear attention.  A token stride is
+// at least a token's heads and a whole number of 16-byte pieces.
+static kda_status_t check_linear(int H, int dk, int dv, kda_dtype_t io_dt, int64_t q_ld,
+                                 int64_t k_ld, int64_t v_ld) {
+    KDA_REQUIRE(io_dt == KDA_F32 || io_dt == KDA_BF16, "io_dt=%d is not a kda_dtype_t", (int)io_dt);
+    KDA_REQUIRE(H > 0 && H <= 65535, "H=%d must be in [1, 65535]", H);
+    if (kda_status_t s = check_dims(dk, dv)) return s;
+    const int per16 = io_dt == KDA_BF16 ? 8 : 4;
+    KDA_REQUIRE(q_ld >= (int64_t)H * dk && q_ld % per16 == 0,
+                "q_ld=%lld must be a multiple of %d and at least H dk", (long long)q_ld, per16);
+    KDA_REQUIRE(k_ld >= (int64_t)H * dk && k_ld % per16 == 0,
+                "k_ld=%lld must be a multiple of %d and at least H dk", (long long)k_ld, per16);
+    KDA_REQUIRE(v_ld >= (int64_t)H * dv && v_ld % per16 == 0,
+                "v_ld=%lld must be a multiple of %d and at least H dv", (long long)v_ld, per16);
+    return KDA_OK;
+}
+
+static kda_status_t check_packed(int64_t T_total, int N, int H, const int32_t* cu_seqlens) {
+    KDA_REQUIRE(N >= 0, "N=%d must be >= 0", N);
+    KDA_REQUIRE(T_total >= 0 && T_total < (int64_t)1 << 31, "T_total=%lld must be in [0, 2^31)",
+                (long long)T_total);
+    KDA_REQUIRE(N > 0 || T_total == 0, "N=0 requires T_total=0");
+    KDA_REQUIRE(cu_seqlens != nullptr || N == 0 || T_total % N == 0,
+                "without cu_seqlens T_total=%lld must be a multiple of N=%d", (long long)T_total,
+                N);
+    KDA_REQUIRE((int64_t)N * H * 4 < (int64_t)1 << 31, "N*H=%lld is too large",
+                (long long)N * H);
+    KDA_OPTIONAL_PTR(cu_seqlens, "cu_seqlens");
+    return KDA_OK;
+}
+
+size_t kda_linear_fwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv,
+                                     kda_dtype_t io_dt) {
+    if (T_total < 0 || N <= 0 || H <= 0 || check_dims(dk, dv) != KDA_OK) return 0;
+    return kda::linear_fwd_workspace_size(T_total, N, H, dk, dv, io_dt == KDA_BF16);
+}
+
+size_t kda_linear_bwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv,
+                                     kda_dtype_t io_dt) {
+    if (T_total < 0 || N <= 0 || H <= 0 || check_dims(dk, dv) != KDA_OK) return 0;
+    return kda::linear_bwd_workspace_size(T_total, N, H, dk, dv, io_dt == KDA_BF16);
+}
+
+kda_status_t kda_linear_fwd_chunked(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                    const void* v, int64_t v_ld, const float* g, int g_per_token,
+                                    const float* S0, float* S_out, const int32_t* cu_seqlens,
+                                    int N, int64_t T_total, int H, int dk, int dv,
+                                    kda_dtype_t io_dt, void* o, void* workspace, size_t ws_bytes,
+                                    kda_stream_t stream) {
+    t_last_error.clear();
+    if (kda_status_t s = check_linear(H, dk, dv, io_dt, q_ld, k_ld, v_ld)) return s;
+    if (kda_status_t s = check_packed(T_total, N, H, cu_seqlens)) return s;
+    if (N == 0) return KDA_OK;
+    if (T_total > 0) {
+        KDA_REQUIRE_PTR(q, "q");
+        KDA_REQUIRE_PTR(k, "k");
+        KDA_REQUIRE_PTR(v, "v");
+        KDA_REQUIRE_WORDS(g, "g");
+        KDA_REQUIRE_PTR(o, "o");
+    }
+    KDA_OPTIONAL_PTR(S0, "S0");
+    KDA_OPTIONAL_PTR(S_out, "S_out");
+    const size_t need = kda_linear_fwd_workspace_size(T_total, N, H, dk, dv, io_dt);
+    if (need > 0) {
+        KDA_REQUIRE_PTR(workspace, "workspace");
+        KDA_REQUIRE(ws_bytes >= need, "workspace of %zu bytes is smaller than the %zu needed",
+                    ws_bytes, need);
+    }
+    kda::LinearArgs a{};
+    a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.v = v; a.v_ld = v_ld;
+    a.g = g; a.g_per_token = g_per_token != 0; a.S0 = S0; a.S_out = S_out;
+    a.cu_seqlens = cu_seqlens; a.N = N; a.T_total = T_total; a.H = H; a.dk = dk; a.dv = dv;
+    a.io_bf16 = io_dt == KDA_BF16; a.o = o; a.workspace = workspace;
+    a.dev_err = device_error_ptr();
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_linear_fwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_linear_fwd_chunked launch");
+    return KDA_OK;
+}
+
+kda_status_t kda_linear_bwd(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                            const void* v, int64_t v_ld, const float* g, int g_per_token,
+                            const float* S0, const int32_t* cu_seqlens, int N, int64_t T_total,
+                            int H, int dk, int dv, kda_dtype_t io_dt, const void* dout,
+                            int64_t dout_ld, const float* dS_out, void* dq, void* dk_out,
+                            void* dv_out, float* dg, float* dS0, void* workspace,
+                            size_t ws_bytes, kda_stream_t stream) {
+    t_last_error.clear();
+    if (kda_status_t s = check_linear(H, dk, dv, io_dt, q_ld, k_ld, v_ld)) return s;
+    if (kda_status_t s = check_packed(T_total, N, H, cu_seqlens)) return s;
+    const int per16 = io_dt == KDA_BF16 ? 8 : 4;
+    KDA_REQUIRE(dout_ld >= (int64_t)H * dv && dout_ld % per16 == 0,
+                "dout_ld=%lld must be a multiple of %d and at least H dv", (long long)dout_ld,
+                per16);
+    KDA_REQUIRE(N > 0, "N=%d must be positive", N);
+    if (T_total > 0) {
+        KDA_REQUIRE_PTR(q, "q");
+        KDA_REQUIRE_PTR(k, "k");
+        KDA_REQUIRE_PTR(v, "v");
+        KDA_REQUIRE_WORDS(g, "g");
+        KDA_REQUIRE_PTR(dout, "dout");
+        KDA_REQUIRE_PTR(dq, "dq");
+        KDA_REQUIRE_PTR(dk_out, "dk");
+        KDA_REQUIRE_PTR(dv_out, "dv");
+    }
+    KDA_OPTIONAL_PTR(S0, "S0");
+    KDA_OPTIONAL_PTR(dS_out, "dS_out");
+    if (dg) KDA_REQUIRE_WORDS(dg, "dg");
+    KDA_OPTIONAL_PTR(dS0, "dS0");
+    const size_t need = kda_linear_bwd_workspace_size(T_total, N, H, dk, dv, io_dt);
+    if (need > 0) {
+        KDA_REQUIRE_PTR(workspace, "workspace");
+        KDA_REQUIRE(ws_bytes >= need, "workspace of %zu bytes is smaller than the %zu needed",
+                    ws_bytes, need);
+    }
+    kda::LinearArgs a{};
+    a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.v = v; a.v_ld = v_ld;
+    a.g = g; a.g_per_token = g_per_token != 0; a.S0 = S0;
+    a.cu_seqlens = cu_seqlens; a.N = N; a.T_total = T_total; a.H = H; a.dk = dk; a.dv = dv;
+    a.io_bf16 = io_dt == KDA_BF16; a.dout = dout; a.dout_ld = dout_ld; a.dS_out = dS_out;
+    a.dq = dq; a.dk_ = dk_out; a.dv_ = dv_out; a.dg = dg; a.dS0 = dS0;
+    a.workspace = workspace; a.dev_err = device_error_ptr();
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_linear_bwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_linear_bwd launch");
+    return KDA_OK;
+}
+
+kda_status_t kda_linear_decode_step(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                    const void* v, int64_t v_ld, const float* g, int g_per_token,
+                                    float* S, const int32_t* slots, int n_slots, int N, int H,
+                                    int dk, int dv, kda_dtype_t io_dt, void* o,
+                                    kda_stream_t stream) {
+    t_last_error.clear();
+    if (kda_status_t s = check_linear(H, dk, dv, io_dt, q_ld, k_ld, v_ld)) return s;
+    KDA_REQUIRE(N >= 0, "N=%d must be >= 0", N);
+    KDA_REQUIRE((int64_t)N * H < (int64_t)1 << 31, "N*H=%lld is too large", (long long)N * H);
+    KDA_REQUIRE(n_slots >= 0, "n_slots=%d must be >= 0", n_slots);
+    KDA_REQUIRE(slots != nullptr || n_slots >= N, "n_slots=%d must be at least N=%d without slots",
+                n_slots, N);
+    if (N == 0) return KDA_OK;
+    KDA_REQUIRE_PTR(q, "q");
+    KDA_REQUIRE_PTR(k, "k");
+    KDA_REQUIRE_PTR(v, "v");
+    KDA_REQUIRE_WORDS(g, "g");
+    KDA_REQUIRE_PTR(S, "S");
+    KDA_REQUIRE_PTR(o, "o");
+    if (slots) KDA_REQUIRE_WORDS(slots, "slots");
+    unsigned* err = device_error_ptr();
+    if (err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_linear_decode(q, q_ld, k, k_ld, v, v_ld, g, g_per_token != 0, S,
+                                              slots, n_slots, N, H, dk, dv, io_dt == KDA_BF16, o,
+                                              err, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kda_linear_decode_step launch");
+    return KDA_OK;
+}
+
+static kda_status_t check_qk_norm(const kda::QkNormArgs& a, kda_dtype_t io_dt, bool bwd) {
+    KDA_REQUIRE(io_dt == KDA_F32 || io_dt == KDA_BF16, "io_dt=%d is not a kda_dtype_t", (int)io_dt);
+    KDA_REQUIRE(a.T >= 0 && a.T < (int64_t)1 << 31, "T=%lld must be in [0, 2^31)", (long long)a.T);
+    KDA_REQUIRE(a.Hq > 0 && a.Hq <= 65535, "Hq=%d must be in [1, 65535]", a.Hq);
+    KDA_REQUIRE(a.Hk >= 0 && a.Hk <= 65535, "Hk=%d must be in [0, 65535]", a.Hk);
+    if (a.d != 64 && a.d != 128)
+        return fail(KDA_ERR_UNSUPPORTED, "d=%d: only 64 and 128 are supported", a.d);
+    KDA_REQUIRE(a.rot_dim >= 0 && a.rot_dim <= a.d, "rot_dim=%d must be in [0, %d]", a.rot_dim,
+                a.d);
+    if (a.rot_dim % 16 != 0)
+        return fail(KDA_ERR_UNSUPPORTED, "rot_dim=%d: only multiples of 16 are supported",
+                    a.rot_dim);
+    KDA_REQUIRE(a.eps >= 0.f && std::isfinite(a.eps), "eps=%g must be finite and >= 0",
+                (double)a.eps);
+    const int per16 = io_dt == KDA_BF16 ? 8 : 4;
+    KDA_REQUIRE(a.q_ld >= (int64_t)a.Hq * a.d && a.q_ld % per16 == 0,
+                "q_ld=%lld must be a multiple of %d and at least Hq d", (long long)a.q_ld, per16);
+    KDA_REQUIRE(a.Hk == 0 || (a.k_ld >= (int64_t)a.Hk * a.d && a.k_ld % per16 == 0),
+                "k_ld=%lld must be a multiple of %d and at least Hk d", (long long)a.k_ld, per16);
+    KDA_OPTIONAL_PTR(a.wq, "wq");
+    KDA_OPTIONAL_PTR(a.wk, "wk");
+    if (a.rot_dim > 0) {
+        KDA_REQUIRE_PTR(a.cos_sin, "cos_sin");
+        if (a.positions) KDA_REQUIRE_WORDS(a.positions, "positions");
+        KDA_REQUIRE(a.n_pos >= 0, "n_pos=%lld must be >= 0", (long long)a.n_pos);
+        KDA_REQUIRE(a.positions != nullptr || a.n_pos >= a.T,
+                    "n_pos=%lld must be at least T=%lld without positions", (long long)a.n_pos,
+                    (long long)a.T);
+    }
+    if (a.T > 0) {
+        KDA_REQUIRE_PTR(a.q, "q");
+        if (bwd) KDA_REQUIRE_PTR(a.dyq, "dyq");
+        KDA_REQUIRE_PTR(a.q_out, bwd ? "dq" : "q_out");
+        if (a.Hk > 0) {
+            KDA_REQUIRE_PTR(a.k, "k");
+            if (bwd) KDA_REQUIRE_PTR(a.dyk, "dyk");
+            KDA_REQUIRE_PTR(a.k_out, bwd ? "dk" : "k_out");
+        }
+    }
+    return KDA_OK;
+}
+
+kda_status_t kda_qk_norm_rope(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                              const float* wq, const float* wk, float eps, const float* cos_sin,
+                              int64_t n_pos, const int32_t* positions, int rot_dim,
+                              int interleaved, void* q_out, void* k_out, int64_t T, int Hq,
+                              int Hk, int d, kda_dtype_t io_dt, kda_stream_t stream) {
+    t_last_error.clear();
+    kda::QkNormArgs a{};
+    a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.wq = wq; a.wk = wk; a.eps = eps;
+    a.cos_sin = cos_sin; a.n_pos = n_pos; a.positions = positions; a.rot_dim = rot_dim;
+    a.interleaved = interleaved != 0; a.q_out = q_out; a.k_out = k_out; a.T = T; a.Hq = Hq;
+    a.Hk = Hk; a.d = d; a.io_bf16 = io_dt == KDA_BF16;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (kda_status_t s = check_qk_norm(a, io_dt, false)) return s;
+    KDA_REQUIRE(q_out != q || q_ld == (int64_t)Hq * d, "q_out may be q only where q is contiguous");
+    KDA_REQUIRE(Hk == 0 || k_out != k || k_ld == (int64_t)Hk * d,
+                "k_out may be k only where k is contiguous");
+    if (T == 0) return KDA_OK;
+    a.dev_err = device_error_ptr();
+    if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_qk_norm(a);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_qk_norm_rope launch");
+    return KDA_OK;
+}
+
+size_t kda_qk_norm_rope_bwd_workspace_size(int d) {
+    return d == 64 || d == 128 ? kda::qk_norm_bwd_workspace_size(d) : 0;
+}
+
+kda_status_t kda_qk_norm_rope_bwd(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                  const void* dyq, const void* dyk, const float* wq,
+                                  const float* wk, float eps, const float* cos_sin,
+                                  int64_t n_pos, const int32_t* positions, int rot_dim,
+                                  int interleaved, void* dq, void* dk_out, float* dwq,
+                                  float* dwk, int64_t T, int Hq, int Hk, int d,
+                                  kda_dtype_t io_dt, void* workspace, size_t ws_bytes,
+                                  kda_stream_t stream) {
+    t_last_error.clear();
+    kda::QkNormArgs a{};
+    a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.dyq = dyq; a.dyk = dyk; a.wq = wq;
+    a.wk = wk; a.eps = eps; a.cos_sin = cos_sin; a.n_pos = n_pos; a.positions = positions;
+    a.rot_dim = rot_dim; a.interleaved = interleaved != 0; a.q_out = dq; a.k_out = dk_out;
+    a.dwq = dwq; a.dwk = dwk; a.T = T; a.Hq = Hq; a.Hk = Hk; a.d = d;
+    a.io_bf16 = io_dt == KDA_BF16; a.workspace = workspace;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (kda_status_t s = check_qk_norm(a, io_dt, true)) return s;
+    KDA_OPTIONAL_PTR(dwq, "dwq");
+    KDA_OPTIONAL_PTR(dwk, "dwk");
+    if (dwq || dwk) {
+        const size_t need = kda::qk_norm_bwd_workspace_size(d);
+        KDA_REQUIRE_PTR(workspace, "workspace");
+        KDA_REQUIRE(ws_bytes >= need, "workspace of %zu bytes is smaller than the %zu needed",
+                    ws_bytes, need);
+    }
+    a.dev_err = device_error_ptr();
+    if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_qk_norm_bwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_qk_norm_rope_bwd launch");
+    return KDA_OK;
+}
+
 size_t kda_quantile_balance_workspace_size(int64_t m, int n) {
     if (m <= 0 || n <= 0) return 0;
     return kda::qb_workspace_size(m, n);
@@ -462,6 +731,12 @@ kda_status_t kda_device_status(kda_stream_t stream) {
     if (word & kda::kDevErrBadSeqlens)
         return fail(KDA_ERR_DEVICE, "malformed cu_seqlens met on the device (error word 0x%x)",
                     word);
+    if (word & kda::kDevErrBadSlot)
+        return fail(KDA_ERR_DEVICE, "a slot outside the pool met on the device (error word 0x%x)",
+                    word);
+    if (word & kda::kDevErrBadPosition)
+        return fail(KDA_ERR_DEVICE,
+                    "a position outside the table met on the device (error word 0x%x)", word);
     return KDA_OK;
 }
 

@@ -8,7 +8,12 @@
 namespace kda {
 
 // Bits of the device error word (see kda_device_status in kda.h).
-enum : unsigned { kDevErrBadSeqlens = 1u, kDevErrTimeout = 2u };
+enum : unsigned {
+    kDevErrBadSeqlens = 1u,
+    kDevErrTimeout = 2u,
+    kDevErrBadSlot = 4u,
+    kDevErrBadPosition = 8u
+};
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }

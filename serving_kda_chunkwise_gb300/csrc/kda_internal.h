@@ -89,6 +89,64 @@ cudaError_t launch_quantile_balance(const float* s, const float* b, int64_t m, i
                                     float* b_new, float* bhat, float* alpha, void* workspace,
                                     cudaStream_t stream);
 
+// Linear attention with one decay per head (linear.cu; the tensor-core outputs linear_tc.cu).
+struct LinearArgs {
+    const void *q, *k, *v;
+    int64_t q_ld, k_ld, v_ld;
+    const float* g;
+    int g_per_token;
+    const float* S0;
+    float* S_out;  // backward: unused
+    const int32_t* cu_seqlens;
+    int N;
+    int64_t T_total;
+    int H, dk, dv;
+    int io_bf16;
+    void* o;
+    // backward only
+    const void* dout;
+    int64_t dout_ld;
+    const float* dS_out;
+    void *dq, *dk_, *dv_;
+    float *dg, *dS0;
+    void* workspace;
+    unsigned* dev_err;
+    cudaStream_t stream;
+};
+size_t linear_fwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv, int io_bf16);
+size_t linear_bwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv, int io_bf16);
+cudaError_t launch_linear_fwd(const LinearArgs& a);
+cudaError_t launch_linear_bwd(const LinearArgs& a);
+cudaError_t launch_linear_decode(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                 const void* v, int64_t v_ld, const float* g, int g_per_token,
+                                 float* S, const int32_t* slots, int n_slots, int N, int H, int dk,
+                                 int dv, int io_bf16, void* o, unsigned* dev_err,
+                                 cudaStream_t stream);
+
+// Norm of the query and key heads with the position rotation (qk_norm.cu).
+struct QkNormArgs {
+    const void *q, *k;
+    int64_t q_ld, k_ld;
+    const void *dyq, *dyk;  // backward only
+    const float *wq, *wk;
+    float eps;
+    const float* cos_sin;
+    int64_t n_pos;
+    const int32_t* positions;
+    int rot_dim, interleaved;
+    void *q_out, *k_out;  // backward: dq, dk
+    float *dwq, *dwk;     // backward only
+    int64_t T;
+    int Hq, Hk, d;
+    int io_bf16;
+    void* workspace;
+    unsigned* dev_err;
+    cudaStream_t stream;
+};
+size_t qk_norm_bwd_workspace_size(int d);
+cudaError_t launch_qk_norm(const QkNormArgs& a);
+cudaError_t launch_qk_norm_bwd(const QkNormArgs& a);
+
 // Chunked forward on CUDA cores in fp32 (any dtype, dk/dv in {64,128}).
 cudaError_t launch_fwd_generic(const FwdArgs& a);
 

@@ -1,0 +1,558 @@
+// linear.cu -- linear attention with one decay per head (declared in include/kda.h):
+//     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t
+// its gradients and its single-token step.  linear_common.cuh says how the forward and the
+// three gradients are instances of one call and how sequences are cut into segments.
+//
+// Launches of a call over sequences longer than a segment:
+//   1. segment sums: each segment's own contribution to the state, and its summed log decay;
+//   2. edges: the state at every segment's edge (a scan over a sequence's segments);
+//   3. outputs: every segment from its edge state.
+// When no sequence can be longer than a segment, launch 3 alone.
+//
+// The gradient of g:  dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_out>.  Taken over
+// a long sequence that sum would gather the rounding of every later token, so it runs over the
+// segment only, from the exact anchor <S, D> at the segment's end (both states are at hand).
+#include "linear_common.cuh"
+
+namespace kda {
+namespace {
+
+using lin::Call;
+using lin::Calls;
+using lin::Problem;
+using lin::Segment;
+
+// -------------------------------------------------- token by token, CUDA cores --
+// A CTA of 128 threads holds a da x 32 block of the state in registers (lane = column, warp =
+// a quarter of the rows) and walks the segment's tokens; x, y, w come in tiles of 16 tokens.
+// fp32 throughout, so that fp32 inputs keep fp32 accuracy: e^{g} multiplies the state as the
+// definition says.  Bound by its three fp32 operations per state element and token.
+constexpr int kCols = 32;
+constexpr int kTile = 16;
+
+template <int DA, typename IO, bool kOut>
+__global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Problem p,
+                                                    const __grid_constant__ Calls calls,
+                                                    float* dec,
+                                                    int blocks_per_call) {
+    constexpr int R = DA / 4;
+    __shared__ float xs[kTile][DA], ys[kTile][DA], ws[kTile][kCols], es[kTile];
+    __shared__ float part[4][kTile][kCols];
+    if (kOut && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) lin::check_seqlens(p);
+    const Call& c = calls.c[blockIdx.z / blocks_per_call];
+    const int cb = blockIdx.z % blocks_per_call;
+    if (c.da != DA || cb * kCols >= c.db) return;
+    const Segment sg = lin::find_segment(p, blockIdx.x);
+    const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = cb * kCols + lane, row0 = warp * R;
+    const int64_t E = (int64_t)c.da * c.db;
+    const int64_t rs = c.tr ? 1 : c.db, cs = c.tr ? c.da : 1;
+    const int64_t own = ((int64_t)blockIdx.x * p.H + h) * E;
+    const int64_t seq = ((int64_t)sg.n * p.H + h) * E;
+
+    float S[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) S[i] = 0.f;
+    if (!sg.live) {
+        // an empty sequence owns its first slot: its final state is its initial one
+        if (kOut && c.S_out && sg.count == 0 && sg.s == 0)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                c.S_out[seq + (row0 + i) * rs + col * cs] =
+                    c.edge ? c.edge[seq + (row0 + i) * rs + col * cs] : 0.f;
+        return;
+    }
+    const bool last = c.reverse ? sg.s == 0 : sg.s == sg.count - 1;
+    if (!kOut && last) return;  // no edge state follows from it
+    if (kOut) {
+        // the edges launch also put the sequence's own edge state into its first slot, so that
+        // with S_out in S0's place no segment reads what another has overwritten
+        const float* from = sg.count > 1 ? c.seg + own : c.edge ? c.edge + seq : nullptr;
+        if (from)
+#pragma unroll
+            for (int i = 0; i < R; ++i) S[i] = from[(row0 + i) * rs + col * cs];
+    }
+
+    const int64_t len = sg.end - sg.begin;
+    float gsum = 0.f;
+    for (int64_t t0 = 0; t0 < len; t0 += kTile) {
+        const int m = (int)(len - t0 < kTile ? len - t0 : kTile);
+        // token i of the tile, in the order of the walk
+        auto token = [&](int i) { return c.reverse ? sg.end - 1 - t0 - i : sg.begin + t0 + i; };
+        __syncthreads();
+        for (int e = threadIdx.x; e < m * DA; e += 128) {
+            const int i = e / DA, d = e % DA;
+            const int64_t t = token(i);
+            if (kOut) xs[i][d] = to_f32(static_cast<const IO*>(c.x)[t * c.x_ld + h * DA + d]);
+            ys[i][d] = to_f32(static_cast<const IO*>(c.y)[t * c.y_ld + h * DA + d]);
+        }
+        for (int e = threadIdx.x; e < m * kCols; e += 128) {
+            const int i = e / kCols, d = e % kCols;
+            ws[i][d] = to_f32(static_cast<const IO*>(c.w)[token(i) * c.w_ld + (int64_t)h * c.db +
+                                                          cb * kCols + d]);
+        }
+        if (threadIdx.x < m) es[threadIdx.x] = lin::log_decay(p, token(threadIdx.x), h);
+        __syncthreads();
+        for (int i = 0; i < m; ++i) {
+            const float a = expf(es[i]), w = ws[i][lane];
+            gsum += es[i];
+            float acc = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (c.reverse) {
+                    S[r] = fmaf(ys[i][row0 + r], w, S[r]);
+                    if (kOut) acc = fmaf(xs[i][row0 + r], S[r], acc);
+                    S[r] *= a;
+                } else {
+                    S[r] = fmaf(ys[i][row0 + r], w, a * S[r]);
+                    if (kOut) acc = fmaf(xs[i][row0 + r], S[r], acc);
+                }
+            }
+            if (kOut) part[warp][i][lane] = acc;
+        }
+        if (!kOut) continue;
+        __syncthreads();
+        for (int i = warp; i < m; i += 4) {
+            const int64_t t = token(i);
+            const float o = part[0][i][lane] + part[1][i][lane] + part[2][i][lane] +
+                            part[3][i][lane];
+            static_cast<IO*>(c.out)[(t * p.H + h) * c.db + col] = from_f32<IO>(o);
+            if (c.dot) {
+                float x = o * to_f32(static_cast<const IO*>(c.dot)[t * c.dot_ld +
+                                                                   (int64_t)h * c.db + col]);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+                if (lane == 0) c.dots[((int64_t)cb * p.T + t) * p.H + h] = x;
+            }
+        }
+    }
+    float* to = kOut ? (last && c.S_out ? c.S_out + seq : nullptr)
+                     : const_cast<float*>(c.seg) + own;
+    if (to)
+#pragma unroll
+        for (int i = 0; i < R; ++i) to[(row0 + i) * rs + col * cs] = S[i];
+    if (!kOut && cb == 0 && threadIdx.x == 0)
+        dec[((int64_t)c.reverse * gridDim.x + blockIdx.x) * p.H + h] = gsum;
+}
+
+// ------------------------------------------------------------------------ edges --
+// A thread carries four state elements over a sequence's segments, the contributions loaded
+// four segments ahead.
+struct Edges {
+    const float* add[2];    // [slots][H][E] contributions: forward, reversed
+    float* seg[2];          // [slots][H][E] edge states (written)
+    const float* edge[2];   // [N][H][E] or nullptr
+    const float* dec[2];    // [slots][H] summed log decays
+    int E;
+};
+
+__global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Problem p,
+                                                   const __grid_constant__ Edges e) {
+    constexpr int kAhead = 4;
+    const int dir = blockIdx.z;
+    const int per_head = e.E / 4 / 256;
+    const int h = blockIdx.x / per_head;
+    const int at = (blockIdx.x % per_head) * 256 + threadIdx.x;  // float4 within the state
+    const int64_t stride = (int64_t)p.H * (e.E / 4), own = (int64_t)h * (e.E / 4) + at;
+    const float4* add = reinterpret_cast<const float4*>(e.add[dir]);
+    float4* seg = reinterpret_cast<float4*>(e.seg[dir]);
+    for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+        int64_t a, b;
+        seq_range(p.cu, n, p.N, p.T, p.err, a, b);
+        const int count = (int)((b - a + p.L - 1) / p.L);
+        if (count < 2) continue;
+        const int64_t base = a / p.L + n;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (e.edge[dir])
+            acc = reinterpret_cast<const float4*>(e.edge[dir])[(int64_t)n * stride + own];
+        seg[(base + (dir ? count - 1 : 0)) * stride + own] = acc;
+        // step i takes segment s(i)'s contribution and leaves the edge state of segment s(i + 1)
+        auto slot = [&](int i) { return base + (dir ? count - 1 - i : i); };
+        for (int i0 = 0; i0 < count - 1; i0 += kAhead) {
+            float4 in[kAhead];
+            float d[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (i0 + u < count - 1) {
+                    in[u] = __ldcs(add + slot(i0 + u) * stride + own);
+                    d[u] = __ldg(e.dec[dir] + slot(i0 + u) * p.H + h);
+                }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                if (i0 + u < count - 1) {
+                    const float f = expf(d[u]);
+                    acc.x = fmaf(f, acc.x, in[u].x);
+                    acc.y = fmaf(f, acc.y, in[u].y);
+                    acc.z = fmaf(f, acc.z, in[u].z);
+                    acc.w = fmaf(f, acc.w, in[u].w);
+                    seg[slot(i0 + u + 1) * stride + own] = acc;
+                }
+        }
+    }
+}
+
+// ----------------------------------------------------------- gradient of the decay --
+// One CTA a (segment, head): the anchor <S, D> at the segment's end, then the suffix sums of
+// q.dq - k.dk over its tokens, 256 at a time from the end.
+struct DecayGrad {
+    const float *segS, *segD;   // [slots][H][E] edge states, or nullptr where none exist
+    const float *S_T, *dS_out;  // [N][H][E], both or neither
+    const float *dots_q, *dots_k;  // [nq][T][H], [nk][T][H]
+    int nq, nk;
+    float* dg;                  // [T][H]
+    int E;
+};
+
+__global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__ Problem p,
+                                                         const __grid_constant__ DecayGrad d) {
+    __shared__ float red[8];
+    const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Segment sg = lin::find_segment(p, blockIdx.x);
+    if (!sg.live) return;
+    const bool last = sg.s == sg.count - 1;
+    const float *A = nullptr, *B = nullptr;
+    if (!last) {
+        A = d.segS + ((int64_t)(blockIdx.x + 1) * p.H + h) * d.E;
+        B = d.segD + ((int64_t)blockIdx.x * p.H + h) * d.E;
+    } else if (d.dS_out) {
+        A = d.S_T + ((int64_t)sg.n * p.H + h) * d.E;
+        B = d.dS_out + ((int64_t)sg.n * p.H + h) * d.E;
+    }
+    auto block_sum = [&](float x) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        __syncthreads();
+        if (lane == 0) red[warp] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) x += red[w];
+        return x;
+    };
+    float carry = 0.f;
+    if (A) {
+        float x = 0.f;
+        for (int i = threadIdx.x; i < d.E / 4; i += 256) {
+            const float4 u = reinterpret_cast<const float4*>(A)[i];
+            const float4 v = reinterpret_cast<const float4*>(B)[i];
+            x = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, x))));
+        }
+        carry = block_sum(x);
+    }
+    // thread i holds the i-th token from the end, so the suffix sum is a running sum
+    for (int64_t t0 = sg.end - 1; t0 >= sg.begin; t0 -= 256) {
+        const int64_t t = t0 - threadIdx.x;
+        float x = 0.f;
+        if (t >= sg.begin) {
+            for (int b = 0; b < d.nq; ++b) x += d.dots_q[((int64_t)b * p.T + t) * p.H + h];
+            for (int b = 0; b < d.nk; ++b) x -= d.dots_k[((int64_t)b * p.T + t) * p.H + h];
+        }
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) red[warp] = x;
+        __syncthreads();
+        float before = 0.f, all = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w < warp) before += red[w];
+            all += red[w];
+        }
+        if (t >= sg.begin) d.dg[t * p.H + h] = carry + before + x;
+        carry += all;
+    }
+}
+
+// dg of a decay that all tokens of a head share: the sum over tokens, in a fixed order.
+__global__ void __launch_bounds__(256) decay_sum_kernel(const float* dg, int64_t T, int H,
+                                                        float* out) {
+    __shared__ float red[256];
+    const int h = blockIdx.x;
+    float x = 0.f;
+    for (int64_t t = threadIdx.x; t < T; t += 256) x += dg[t * H + h];
+    red[threadIdx.x] = x;
+    for (int n = 128; n > 0; n >>= 1) {
+        __syncthreads();
+        if (threadIdx.x < n) red[threadIdx.x] += red[threadIdx.x + n];
+    }
+    if (threadIdx.x == 0) out[h] = red[0];
+}
+
+// ------------------------------------------------------------------------- host --
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Tokens a segment: short enough that the segments of all heads fill the GPU a few times, no
+// shorter than the edge states' traffic (two fp32 states a segment) is worth.
+int segment_length(int64_t T, int H) {
+    int L = 64;
+    while (L < 1024 && T / L * H > 4 * 152) L *= 2;
+    return L;
+}
+
+struct Layout {
+    int L;
+    int64_t slots;
+    bool segments;  // some sequence may be longer than a segment
+    size_t add[2], seg[2], dec, S_T, dots_q, dots_k, dg, bytes;
+};
+
+Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool equal) {
+    Layout l{};
+    l.L = segment_length(T, H);
+    l.slots = lin::slot_count(T, N, l.L);
+    l.segments = (equal && N > 0 ? T / N : T) > l.L;
+    const size_t state = (size_t)H * dk * dv * sizeof(float);
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t r = at;
+        at += align256(n);
+        return r;
+    };
+    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+        l.add[i] = take(l.segments ? (size_t)l.slots * state : 0);
+        l.seg[i] = take(l.segments ? (size_t)l.slots * state : 0);
+    }
+    l.dec = take(l.segments ? (size_t)2 * l.slots * H * sizeof(float) : 0);
+    if (bwd) {
+        l.S_T = take((size_t)N * state);
+        l.dots_q = take((size_t)(dk / kCols) * T * H * sizeof(float));
+        l.dots_k = take((size_t)(dk / kCols) * T * H * sizeof(float));
+        l.dg = take((size_t)T * H * sizeof(float));
+    }
+    l.bytes = at;
+    return l;
+}
+
+Problem problem(const LinearArgs& a, int L) {
+    Problem p{};
+    p.cu = a.cu_seqlens; p.N = a.N; p.T = a.T_total; p.H = a.H; p.g = a.g;
+    p.g_per_token = a.g_per_token; p.L = L; p.err = a.dev_err;
+    return p;
+}
+
+template <typename IO, bool kOut>
+void launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, float* dec,
+                  const char* name, cudaStream_t s) {
+    const int blocks = 4;
+    const dim3 grid((unsigned)slots, p.H, n * blocks);
+    bool any[2] = {};
+    for (int i = 0; i < n; ++i) any[calls.c[i].da == 128] = true;
+    ProfScope prof(name, s);
+    if (any[0]) token_kernel<64, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
+    if (any[1]) token_kernel<128, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
+}
+
+template <bool kOut>
+void launch_token(const LinearArgs& a, const Problem& p, const Calls& calls, int n, int64_t slots,
+                  float* dec, const char* name) {
+    if (a.io_bf16)
+        launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream);
+    else
+        launch_token<float, kOut>(p, calls, n, slots, dec, name, a.stream);
+}
+
+// Segment sums and edges of the forward states and, in a backward pass, of the reversed ones.
+void launch_segments(const LinearArgs& a, const Problem& p, const Layout& l, bool bwd) {
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    float* dec = reinterpret_cast<float*>(ws + l.dec);
+    Calls calls{};
+    Edges e{};
+    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+        Call& c = calls.c[i];
+        c.y = i ? a.q : a.k; c.y_ld = i ? a.q_ld : a.k_ld;
+        c.w = i ? a.dout : a.v; c.w_ld = i ? a.dout_ld : a.v_ld;
+        c.da = a.dk; c.db = a.dv; c.reverse = i;
+        c.seg = reinterpret_cast<float*>(ws + l.add[i]);
+        e.add[i] = c.seg;
+        e.seg[i] = reinterpret_cast<float*>(ws + l.seg[i]);
+        e.edge[i] = i ? a.dS_out : a.S0;
+        e.dec[i] = dec + (size_t)i * l.slots * a.H;
+    }
+    e.E = a.dk * a.dv;
+    launch_token<false>(a, p, calls, bwd ? 2 : 1, l.slots, dec, "linear_segment_kernel");
+    ProfScope prof("linear_edge_kernel", a.stream);
+    const dim3 grid(a.H * (e.E / 1024), a.N < 64 ? a.N : 64, bwd ? 2 : 1);
+    edge_kernel<<<grid, 256, 0, a.stream>>>(p, e);
+}
+
+}  // namespace
+
+size_t linear_fwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int) {
+    return layout(T, N, H, dk, dv, false, false).bytes;
+}
+size_t linear_bwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int) {
+    return layout(T, N, H, dk, dv, true, false).bytes;
+}
+
+cudaError_t launch_linear_fwd(const LinearArgs& a) {
+    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, false, a.cu_seqlens == nullptr);
+    const Problem p = problem(a, l.L);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    if (l.segments) launch_segments(a, p, l, false);
+    Calls calls{};
+    Call& c = calls.c[0];
+    c.x = a.q; c.x_ld = a.q_ld; c.y = a.k; c.y_ld = a.k_ld; c.w = a.v; c.w_ld = a.v_ld;
+    c.da = a.dk; c.db = a.dv; c.edge = a.S0; c.S_out = a.S_out; c.out = a.o;
+    c.seg = reinterpret_cast<float*>(ws + l.seg[0]);
+    launch_token<true>(a, p, calls, 1, l.slots, nullptr, "linear_out_kernel");
+    return cudaGetLastError();
+}
+
+cudaError_t launch_linear_bwd(const LinearArgs& a) {
+    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, true, a.cu_seqlens == nullptr);
+    const Problem p = problem(a, l.L);
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    if (l.segments) launch_segments(a, p, l, true);
+    const bool anchor = a.dg && a.dS_out;
+    Calls calls{};
+    Call &q = calls.c[0], &k = calls.c[1], &v = calls.c[2];
+    q.x = a.dout; q.x_ld = a.dout_ld; q.y = a.v; q.y_ld = a.v_ld; q.w = a.k; q.w_ld = a.k_ld;
+    q.da = a.dv; q.db = a.dk; q.tr = 1; q.edge = a.S0; q.seg = at(l.seg[0]);
+    q.S_out = anchor ? at(l.S_T) : nullptr; q.out = a.dq;
+    if (a.dg) { q.dot = a.q; q.dot_ld = a.q_ld; q.dots = at(l.dots_q); }
+    k.x = a.v; k.x_ld = a.v_ld; k.y = a.dout; k.y_ld = a.dout_ld; k.w = a.q; k.w_ld = a.q_ld;
+    k.da = a.dv; k.db = a.dk; k.reverse = 1; k.tr = 1; k.edge = a.dS_out; k.seg = at(l.seg[1]);
+    k.out = a.dk_;
+    if (a.dg) { k.dot = a.k; k.dot_ld = a.k_ld; k.dots = at(l.dots_k); }
+    v.x = a.k; v.x_ld = a.k_ld; v.y = a.q; v.y_ld = a.q_ld; v.w = a.dout; v.w_ld = a.dout_ld;
+    v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = at(l.seg[1]);
+    v.S_out = a.dS0; v.out = a.dv_;
+    launch_token<true>(a, p, calls, 3, l.slots, nullptr, "linear_grad_kernel");
+    if (a.dg) {
+        DecayGrad d{};
+        d.segS = at(l.seg[0]); d.segD = at(l.seg[1]);
+        d.S_T = at(l.S_T); d.dS_out = a.dS_out;
+        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kCols;
+        d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
+        if (a.T_total > 0) {
+            ProfScope prof("linear_decay_grad_kernel", a.stream);
+            decay_grad_kernel<<<dim3((unsigned)l.slots, a.H), 256, 0, a.stream>>>(p, d);
+        }
+        if (!a.g_per_token) {
+            ProfScope prof("linear_decay_sum_kernel", a.stream);
+            decay_sum_kernel<<<a.H, 256, 0, a.stream>>>(d.dg, a.T_total, a.H, a.dg);
+        }
+    }
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------ decode --
+// One CTA a (request, head): a state row of dv fp32 is covered by dv / 4 lanes with a float4
+// each, the dk rows spread over 8 warps; every element is read once, updated, written once and
+// added to its column's output:  S <- e^g S + k v^T,  o = S^T q.
+namespace {
+
+template <int DK, int DV, typename IO>
+__global__ void __launch_bounds__(256) step_kernel(const IO* __restrict__ q, int64_t q_ld,
+                                                   const IO* __restrict__ k, int64_t k_ld,
+                                                   const IO* __restrict__ v, int64_t v_ld,
+                                                   const float* __restrict__ g, int g_per_token,
+                                                   float* __restrict__ S,
+                                                   const int32_t* __restrict__ slots, int n_slots,
+                                                   int H, IO* __restrict__ o, unsigned* err) {
+    constexpr int kLanesPerRow = DV / 4;
+    constexpr int kRowsPerPass = 256 / kLanesPerRow;
+    constexpr int kRows = DK / kRowsPerPass;
+    __shared__ float s_k[DK], s_q[DK];
+    __shared__ float4 s_red[8][kLanesPerRow];
+    const int n = blockIdx.x / H, h = blockIdx.x % H;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int col = tid % kLanesPerRow, row0 = tid / kLanesPerRow;
+    const int slot = slots ? __ldg(slots + n) : n;
+    if (slot < 0 || slot >= n_slots) {
+        if (slot >= n_slots && tid == 0) atomicOr(err, kDevErrBadSlot);
+        if (tid < DV) o[(size_t)blockIdx.x * DV + tid] = from_f32<IO>(0.f);
+        return;
+    }
+    float4* Sp = reinterpret_cast<float4*>(S + ((size_t)slot * H + h) * DK * DV);
+    float4 s[kRows];
+#pragma unroll
+    for (int m = 0; m < kRows; ++m)
+        s[m] = __ldcs(Sp + (row0 + m * kRowsPerPass) * kLanesPerRow + col);
+    const float a = expf(g_per_token ? __ldg(g + blockIdx.x) : __ldg(g + h));
+    for (int c = tid; c < DK; c += 256) {
+        s_k[c] = to_f32(k[n * k_ld + h * DK + c]);
+        s_q[c] = to_f32(q[n * q_ld + h * DK + c]);
+    }
+    const IO* vp = v + n * v_ld + h * DV + 4 * col;
+    const float4 w = make_float4(to_f32(vp[0]), to_f32(vp[1]), to_f32(vp[2]), to_f32(vp[3]));
+    __syncthreads();
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int m = 0; m < kRows; ++m) {
+        const int row = row0 + m * kRowsPerPass;
+        const float kr = s_k[row], qr = s_q[row];
+        float4 r;
+        r.x = fmaf(a, s[m].x, kr * w.x);
+        r.y = fmaf(a, s[m].y, kr * w.y);
+        r.z = fmaf(a, s[m].z, kr * w.z);
+        r.w = fmaf(a, s[m].w, kr * w.w);
+        __stcs(Sp + row * kLanesPerRow + col, r);
+        acc.x = fmaf(qr, r.x, acc.x);
+        acc.y = fmaf(qr, r.y, acc.y);
+        acc.z = fmaf(qr, r.z, acc.z);
+        acc.w = fmaf(qr, r.w, acc.w);
+    }
+    if (kLanesPerRow < 32) {
+        acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+        acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+        acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+        acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+    }
+    if (lane < kLanesPerRow) s_red[warp][lane] = acc;
+    __syncthreads();
+    if (tid < DV) {
+        float x = 0.f;
+#pragma unroll
+        for (int w8 = 0; w8 < 8; ++w8) x += reinterpret_cast<const float*>(s_red[w8])[tid];
+        o[(size_t)blockIdx.x * DV + tid] = from_f32<IO>(x);
+    }
+}
+
+struct StepArgs {
+    const void *q, *k, *v;
+    int64_t q_ld, k_ld, v_ld;
+    const float* g;
+    int g_per_token;
+    float* S;
+    const int32_t* slots;
+    int n_slots, N, H;
+    void* o;
+    unsigned* err;
+    cudaStream_t stream;
+};
+
+template <int DK, int DV, typename IO>
+cudaError_t step_t(const StepArgs& a) {
+    ProfScope prof("linear_step_kernel", a.stream);
+    step_kernel<DK, DV, IO><<<a.N * a.H, 256, 0, a.stream>>>(
+        static_cast<const IO*>(a.q), a.q_ld, static_cast<const IO*>(a.k), a.k_ld,
+        static_cast<const IO*>(a.v), a.v_ld, a.g, a.g_per_token, a.S, a.slots, a.n_slots, a.H,
+        static_cast<IO*>(a.o), a.err);
+    return cudaGetLastError();
+}
+
+template <typename IO>
+cudaError_t step_dims(const StepArgs& a, int dk, int dv) {
+    if (dk == 128) return dv == 128 ? step_t<128, 128, IO>(a) : step_t<128, 64, IO>(a);
+    return dv == 128 ? step_t<64, 128, IO>(a) : step_t<64, 64, IO>(a);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_decode(const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                 const void* v, int64_t v_ld, const float* g, int g_per_token,
+                                 float* S, const int32_t* slots, int n_slots, int N, int H, int dk,
+                                 int dv, int io_bf16, void* o, unsigned* dev_err,
+                                 cudaStream_t stream) {
+    const StepArgs a{q, k, v, q_ld, k_ld, v_ld, g, g_per_token, S, slots, n_slots, N, H, o,
+                     dev_err, stream};
+    return io_bf16 ? step_dims<__nv_bfloat16>(a, dk, dv) : step_dims<float>(a, dk, dv);
+}
+
+}  // namespace kda

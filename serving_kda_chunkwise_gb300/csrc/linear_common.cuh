@@ -1,0 +1,108 @@
+// linear_common.cuh -- what the kernels of the per-head-decay linear attention share: the
+// problem, the linear-attention call that the forward and all three gradients are instances of,
+// and the map from segment slots to token ranges.
+//
+// One call, with rows x, y of da channels and w of db channels, computes per sequence and head
+//     forward:  S_t = e^{g_t} S_{t-1} + y_t w_t^T,                out_t = S_t^T x_t
+//     reversed: D_t = e^{g_{t+1}} D_{t+1} + y_t w_t^T,            out_t = D_t^T x_t
+//   o  = forward (x, y, w) = (q, k, v)          dq = forward (do, v, k)  (states transposed)
+//   dv = reversed (k, q, do)                    dk = reversed (v, do, q) (states transposed)
+//
+// Segments.  The recurrence is linear, so a sequence is cut into segments of L tokens that run
+// in parallel once the state at each segment's edge is known.  Slot base(n) + s holds segment
+// s of sequence n, with base(n) = floor(cu[n] / L) + n: consecutive bases are at least
+// ceil(len / L) apart, so a slot finds its sequence from cu_seqlens alone and no launch has to
+// lay out a table.  Slots past a sequence's last segment are empty.
+#pragma once
+
+#include "kda_common.cuh"
+#include "kda_internal.h"
+
+namespace kda {
+namespace lin {
+
+struct Problem {
+    const int32_t* cu;
+    int N;
+    int64_t T;
+    int H;
+    const float* g;
+    int g_per_token;
+    int L;
+    unsigned* err;
+};
+
+struct Call {
+    const void *x, *y, *w;
+    int64_t x_ld, y_ld, w_ld;
+    int da, db;
+    int reverse;
+    int tr;              // states in memory are [db][da] instead of [da][db]
+    const float* edge;   // [N][H][...] state before the first (reversed: after the last) token
+    const float* seg;    // [slots][H][...] state at the other segments' edges
+    float* S_out;        // [N][H][...] state after the sequence (reversed: before it), or nullptr
+    void* out;           // [T][H][db]
+    const void* dot;     // [T][H][db] rows, or nullptr: dots[b][t][h] = sum over column block b
+    int64_t dot_ld;      //   of out * dot in fp32, before out is rounded
+    float* dots;
+};
+
+constexpr int kMaxCalls = 3;
+struct Calls {
+    Call c[kMaxCalls];
+};
+
+__host__ __device__ inline int64_t slot_count(int64_t T, int N, int L) { return T / L + N; }
+
+struct Segment {
+    int n;                // sequence
+    int s, count;         // segment of the sequence, and how many it has
+    int64_t begin, end;   // its tokens
+    bool live;
+};
+
+__device__ __forceinline__ int64_t seq_start(const Problem& p, int n) {
+    return p.cu ? (int64_t)__ldg(p.cu + n) : (int64_t)n * (p.T / p.N);
+}
+
+// Called by whole warps: the segment in slot j.
+__device__ __forceinline__ Segment find_segment(const Problem& p, int64_t j) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = p.N;  // the sequence is in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int n = lo + (lane + 1) * step;
+        const bool at = n < hi && seq_start(p, n) / p.L + n <= j;
+        const unsigned mask = __ballot_sync(0xffffffffu, at);
+        const int c = mask == 0xffffffffu ? 32 : __ffs(~mask) - 1;
+        lo += c * step;
+        hi = min(hi, lo + step);
+    }
+    Segment r;
+    r.n = lo;
+    int64_t a, b;
+    seq_range(p.cu, lo, p.N, p.T, p.err, a, b);
+    r.count = (int)((b - a + p.L - 1) / p.L);
+    const int64_t s = j - ((p.cu ? a : seq_start(p, lo)) / p.L + lo);
+    r.live = s >= 0 && s < r.count;
+    r.s = (int)s;
+    r.begin = a + s * p.L;
+    r.end = r.begin + p.L < b ? r.begin + p.L : b;
+    return r;
+}
+
+// The launch's first CTA reports any malformed offset: find_segment() looks at some only.
+__device__ __forceinline__ void check_seqlens(const Problem& p) {
+    if (p.cu == nullptr) return;
+    for (int n = threadIdx.x; n < p.N; n += blockDim.x) {
+        int64_t a, b;
+        seq_range(p.cu, n, p.N, p.T, p.err, a, b);
+    }
+}
+
+__device__ __forceinline__ float log_decay(const Problem& p, int64_t t, int h) {
+    return p.g_per_token ? __ldg(p.g + t * p.H + h) : __ldg(p.g + h);
+}
+
+}  // namespace lin
+}  // namespace kda

@@ -74,6 +74,27 @@ def _load():
     lib.kda_bwd.restype = ctypes.c_int
     lib.kda_bwd.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, vp, i32, i64, i32, i32, i32, i32,
                             vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_linear_fwd_workspace_size.restype = sz
+    lib.kda_linear_fwd_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32]
+    lib.kda_linear_fwd_chunked.restype = ctypes.c_int
+    lib.kda_linear_fwd_chunked.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, vp, i32,
+                                           i64, i32, i32, i32, i32, vp, vp, sz, vp]
+    lib.kda_linear_bwd_workspace_size.restype = sz
+    lib.kda_linear_bwd_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32]
+    lib.kda_linear_bwd.restype = ctypes.c_int
+    lib.kda_linear_bwd.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, i32, i64, i32, i32,
+                                   i32, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_linear_decode_step.restype = ctypes.c_int
+    lib.kda_linear_decode_step.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, i32, i32,
+                                           i32, i32, i32, i32, vp, vp]
+    lib.kda_qk_norm_rope.restype = ctypes.c_int
+    lib.kda_qk_norm_rope.argtypes = [vp, i64, vp, i64, vp, vp, f32, vp, i64, vp, i32, i32, vp, vp,
+                                     i64, i32, i32, i32, i32, vp]
+    lib.kda_qk_norm_rope_bwd_workspace_size.restype = sz
+    lib.kda_qk_norm_rope_bwd_workspace_size.argtypes = [i32]
+    lib.kda_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.kda_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, f32, vp, i64, vp, i32,
+                                         i32, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp]
     lib.kda_selftest_timeout.restype = ctypes.c_int
     lib.kda_selftest_timeout.argtypes = [ctypes.c_uint, vp]
     lib.kda_device_status.restype = ctypes.c_int
@@ -407,6 +428,228 @@ def decode_step_gated(q, k, v, beta, z, A_log, g_min: float, S, gate, norm_w=Non
                                       _ptr(norm_w), float(eps), int(N), int(H), int(dk), int(dv),
                                       _dt(q), _ptr(y), _stream(stream)), "kda_decode_step_gated")
     return y
+
+
+def _rows(t: torch.Tensor, name: str, dtype) -> int:
+    """Token stride of a [T, H, d] tensor whose heads are contiguous (T may be a strided view)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got {t.dim()}")
+    T, H, d = t.shape
+    s = t.stride()
+    if T == 0 or t.is_contiguous():
+        return H * d
+    if s[2] != 1 or (H > 1 and s[1] != d):
+        raise ValueError(f"{name} must have contiguous heads")
+    return s[0] if T > 1 else H * d
+
+
+def _shape(t: torch.Tensor, name: str, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _decay(g: torch.Tensor, T: int, H: int) -> int:
+    """1 for a log decay [T, H], 0 for one fixed value a head [H]."""
+    _need(g, "g", torch.float32)
+    if g.dim() == 1:
+        _shape(g, "g", (H,))
+        return 0
+    _shape(g, "g", (T, H))
+    return 1
+
+
+def _scratch(workspace, need: int, device):
+    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _packed(q, k, v, cu_seqlens, N):
+    """Shared shape checks of the linear attention: (T, N, H, dk, dv)."""
+    T, H, dk = q.shape
+    dv = v.shape[2]
+    _shape(k, "k", (T, H, dk))
+    _shape(v, "v", (T, H, dv))
+    if cu_seqlens is not None:
+        _need(cu_seqlens, "cu_seqlens", torch.int32)
+        n = cu_seqlens.numel() - 1
+        if N is not None and N != n:
+            raise ValueError(f"N={N} does not match cu_seqlens of {n} sequences")
+        N = n
+    elif N is None:
+        N = 1
+    return T, N, H, dk, dv
+
+
+def linear_fwd_chunked(q, k, v, g, S0=None, cu_seqlens=None, N=None, o=None, S_out=None,
+                       want_state: bool = True, workspace=None, stream=None):
+    """Linear attention with one decay per head over packed sequences:
+    S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+
+    q, k: [T, H, dk]; v: [T, H, dv] (bf16 or fp32; the token stride is free); g: fp32 log decay,
+    [T, H] or [H]; S0: fp32 [N, H, dk, dv] or None; cu_seqlens: int32 [N+1] on the device, or
+    None with N equal sequences (N defaults to 1).
+    Returns (o [T, H, dv], S_out [N, H, dk, dv] or None); S_out may be S0.
+    """
+    lq, lk, lv = _rows(q, "q", q.dtype), _rows(k, "k", q.dtype), _rows(v, "v", q.dtype)
+    T, N, H, dk, dv = _packed(q, k, v, cu_seqlens, N)
+    per_token = _decay(g, T, H)
+    dt = _dt(q)
+    if o is None:
+        o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+    _need(o, "o", q.dtype)
+    _shape(o, "o", (T, H, dv))
+    if S_out is None and want_state:
+        S_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+    for t, nm in ((S0, "S0"), (S_out, "S_out")):
+        if t is not None:
+            _need(t, nm, torch.float32)
+            _shape(t, nm, (N, H, dk, dv))
+    workspace, ws_bytes = _scratch(
+        workspace, _lib.kda_linear_fwd_workspace_size(T, N, H, dk, dv, dt), q.device)
+    _check(_lib.kda_linear_fwd_chunked(_ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(g), per_token,
+                                       _ptr(S0), _ptr(S_out), _ptr(cu_seqlens), N, T, H, dk, dv,
+                                       dt, _ptr(o), _ptr(workspace), ws_bytes, _stream(stream)),
+           "kda_linear_fwd_chunked")
+    return o, S_out
+
+
+def linear_bwd(q, k, v, g, dout, S0=None, dS_out=None, cu_seqlens=None, N=None,
+               want_dg: bool = True, want_dS0: bool = True, workspace=None, stream=None):
+    """Gradients of linear_fwd_chunked's (o, S_out) for upstream gradients dout (and dS_out).
+
+    Returns a dict: dq, dk, dv (io dtype), dg (fp32, g's shape) and dS0 [N, H, dk, dv] fp32
+    (None where not wanted).
+    """
+    lq, lk, lv = _rows(q, "q", q.dtype), _rows(k, "k", q.dtype), _rows(v, "v", q.dtype)
+    ldo = _rows(dout, "dout", q.dtype)
+    T, N, H, dk, dv = _packed(q, k, v, cu_seqlens, N)
+    _shape(dout, "dout", (T, H, dv))
+    per_token = _decay(g, T, H)
+    for t, nm in ((S0, "S0"), (dS_out, "dS_out")):
+        if t is not None:
+            _need(t, nm, torch.float32)
+            _shape(t, nm, (N, H, dk, dv))
+    dt, dev = _dt(q), q.device
+    out = {"dq": torch.empty((T, H, dk), dtype=q.dtype, device=dev),
+           "dk": torch.empty((T, H, dk), dtype=q.dtype, device=dev),
+           "dv": torch.empty((T, H, dv), dtype=q.dtype, device=dev),
+           "dg": torch.empty_like(g) if want_dg else None,
+           "dS0": (torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+                   if want_dS0 else None)}
+    workspace, ws_bytes = _scratch(
+        workspace, _lib.kda_linear_bwd_workspace_size(T, N, H, dk, dv, dt), dev)
+    _check(_lib.kda_linear_bwd(_ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(g), per_token,
+                               _ptr(S0), _ptr(cu_seqlens), N, T, H, dk, dv, dt, _ptr(dout), ldo,
+                               _ptr(dS_out), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
+                               _ptr(out["dg"]), _ptr(out["dS0"]), _ptr(workspace), ws_bytes,
+                               _stream(stream)), "kda_linear_bwd")
+    return out
+
+
+def linear_decode_step(q, k, v, g, S, slots=None, o=None, stream=None):
+    """One token of linear_fwd_chunked's recurrence for N requests, states updated in place.
+
+    q, k: [N, H, dk]; v: [N, H, dv]; g: fp32 [N, H] or [H]; S: fp32 pool [n_slots, H, dk, dv];
+    slots: int32 [N], each request's row of the pool (negative: unused, its o is zero), or None
+    for row n.  Returns o [N, H, dv].
+    """
+    lq, lk, lv = _rows(q, "q", q.dtype), _rows(k, "k", q.dtype), _rows(v, "v", q.dtype)
+    N, _, H, dk, dv = _packed(q, k, v, None, None)
+    per_token = _decay(g, N, H)
+    _need(S, "S", torch.float32)
+    n_slots = S.shape[0]
+    _shape(S, "S", (n_slots, H, dk, dv))
+    if slots is not None:
+        _need(slots, "slots", torch.int32)
+        _shape(slots, "slots", (N,))
+    if o is None:
+        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+    _need(o, "o", q.dtype)
+    _shape(o, "o", (N, H, dv))
+    _check(_lib.kda_linear_decode_step(_ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(g), per_token,
+                                       _ptr(S), _ptr(slots), n_slots, N, H, dk, dv, _dt(q),
+                                       _ptr(o), _stream(stream)), "kda_linear_decode_step")
+    return o
+
+
+def _qk(q, k, wq, wk, cos_sin, positions):
+    """Shared checks of the query/key norm: (q_ld, k_ld, n_pos, rot_dim)."""
+    lq, lk = _rows(q, "q", q.dtype), _rows(k, "k", q.dtype)
+    T, _, d = q.shape
+    _shape(k, "k", (T, k.shape[1], d))
+    for w, nm in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _need(w, nm, torch.float32)
+            _shape(w, nm, (d,))
+    n_pos = rot = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32)
+        n_pos, rot = cos_sin.shape
+    if positions is not None:
+        _need(positions, "positions", torch.int32)
+        _shape(positions, "positions", (T,))
+    return lq, lk, n_pos, rot
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, eps: float = 1e-6, cos_sin=None, positions=None,
+                 interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head and the rotation of its first channels by the
+    token's position, in one pass.
+
+    q: [T, Hq, d], k: [T, Hk, d] (bf16 or fp32; the token stride is free); wq, wk: fp32 [d] or
+    None; cos_sin: fp32 [n_pos, rot_dim], rot_dim/2 cosines then as many sines a row, or None
+    for no rotation; positions: int32 [T], or None for 0 .. T-1.  interleaved pairs channels
+    (2p, 2p + 1), otherwise (p, p + rot_dim/2).  Returns (q_out, k_out), contiguous; they may be
+    q and k where those are contiguous.
+    """
+    lq, lk, n_pos, rot = _qk(q, k, wq, wk, cos_sin, positions)
+    T, Hq, d = q.shape
+    Hk = k.shape[1]
+    if q_out is None:
+        q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, d), dtype=q.dtype, device=q.device)
+    for t, nm, H in ((q_out, "q_out", Hq), (k_out, "k_out", Hk)):
+        _need(t, nm, q.dtype)
+        _shape(t, nm, (T, H, d))
+    _check(_lib.kda_qk_norm_rope(_ptr(q), lq, _ptr(k), lk, _ptr(wq), _ptr(wk), eps,
+                                 _ptr(cos_sin), n_pos, _ptr(positions), rot, int(interleaved),
+                                 _ptr(q_out), _ptr(k_out), T, Hq, Hk, d, _dt(q),
+                                 _stream(stream)), "kda_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, cos_sin=None,
+                     positions=None, interleaved: bool = False, workspace=None, stream=None):
+    """Gradients of qk_norm_rope for upstream gradients dyq [T, Hq, d], dyk [T, Hk, d].
+
+    Returns a dict: dq, dk (io dtype), dwq, dwk [d] fp32 (None where the weight is None).
+    """
+    lq, lk, n_pos, rot = _qk(q, k, wq, wk, cos_sin, positions)
+    T, Hq, d = q.shape
+    Hk = k.shape[1]
+    for t, nm, H in ((dyq, "dyq", Hq), (dyk, "dyk", Hk)):
+        _need(t, nm, q.dtype)
+        _shape(t, nm, (T, H, d))
+    dev = q.device
+    out = {"dq": torch.empty((T, Hq, d), dtype=q.dtype, device=dev),
+           "dk": torch.empty((T, Hk, d), dtype=q.dtype, device=dev),
+           "dwq": None if wq is None else torch.empty(d, dtype=torch.float32, device=dev),
+           "dwk": None if wk is None else torch.empty(d, dtype=torch.float32, device=dev)}
+    need = 0 if wq is None and wk is None else _lib.kda_qk_norm_rope_bwd_workspace_size(d)
+    workspace, ws_bytes = _scratch(workspace, need, dev)
+    _check(_lib.kda_qk_norm_rope_bwd(_ptr(q), lq, _ptr(k), lk, _ptr(dyq), _ptr(dyk), _ptr(wq),
+                                     _ptr(wk), eps, _ptr(cos_sin), n_pos, _ptr(positions), rot,
+                                     int(interleaved), _ptr(out["dq"]), _ptr(out["dk"]),
+                                     _ptr(out["dwq"]), _ptr(out["dwk"]), T, Hq, Hk, d, _dt(q),
+                                     _ptr(workspace), ws_bytes, _stream(stream)),
+           "kda_qk_norm_rope_bwd")
+    return out
 
 
 def quantile_balance(scores, bias, k: int, want_bhat=False, want_alpha=False, workspace=None,
