@@ -10,9 +10,15 @@
 // When no sequence can be longer than a segment, launch 3 alone.
 //
 // The gradient of g:  dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_out>.  Taken over
-// a long sequence that sum would gather the rounding of every later token, so it runs over the
-// segment only, from the exact anchor <S, D> at the segment's end (both states are at hand).
+// a long sequence that sum would gather the rounding of every later token.  At every segment's
+// edges it is <S, D>, from states that are at hand, so the sums run inside a segment, from the
+// anchor at its end; what they miss the anchor at its start by is their rounding, and is taken
+// back token by token in proportion to the terms' sizes.
+#include <cstdlib>
+#include <cstring>
+
 #include "linear_common.cuh"
+#include "linear_tc.h"
 
 namespace kda {
 namespace {
@@ -132,7 +138,7 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
 #pragma unroll
         for (int i = 0; i < R; ++i) to[(row0 + i) * rs + col * cs] = S[i];
     if (!kOut && cb == 0 && threadIdx.x == 0)
-        dec[((int64_t)c.reverse * gridDim.x + blockIdx.x) * p.H + h] = gsum;
+        dec[((int64_t)c.reverse * gridDim.x + blockIdx.x) * p.H + h] = gsum * 1.4426950408889634f;
 }
 
 // ------------------------------------------------------------------------ edges --
@@ -142,7 +148,7 @@ struct Edges {
     const float* add[2];    // [slots][H][E] contributions: forward, reversed
     float* seg[2];          // [slots][H][E] edge states (written)
     const float* edge[2];   // [N][H][E] or nullptr
-    const float* dec[2];    // [slots][H] summed log decays
+    const float* dec[2];    // [slots][H] summed log2 decays
     int E;
 };
 
@@ -180,7 +186,7 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
                 if (i0 + u < count - 1) {
-                    const float f = expf(d[u]);
+                    const float f = exp2f(d[u]);
                     acc.x = fmaf(f, acc.x, in[u].x);
                     acc.y = fmaf(f, acc.y, in[u].y);
                     acc.z = fmaf(f, acc.z, in[u].z);
@@ -192,11 +198,12 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
 }
 
 // ----------------------------------------------------------- gradient of the decay --
-// One CTA a (segment, head): the anchor <S, D> at the segment's end, then the suffix sums of
-// q.dq - k.dk over its tokens, 256 at a time from the end.
+// One CTA a (segment, head): the anchors <S, D> at the segment's two edges, then the suffix sums
+// of q.dq - k.dk over its tokens, 256 at a time from the end.
 struct DecayGrad {
-    const float *segS, *segD;   // [slots][H][E] edge states, or nullptr where none exist
-    const float *S_T, *dS_out;  // [N][H][E], both or neither
+    const float *segS, *segD;   // [slots][H][E] edge states (where sequences have segments)
+    const float *S0, *dS0;      // [N][H][E] at the sequences' starts; S0 may be nullptr (zeros)
+    const float *S_T, *dS_out;  // at their ends; dS_out may be nullptr (zeros)
     const float *dots_q, *dots_k;  // [nq][T][H], [nk][T][H]
     int nq, nk;
     float* dg;                  // [T][H]
@@ -205,63 +212,84 @@ struct DecayGrad {
 
 __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__ Problem p,
                                                          const __grid_constant__ DecayGrad d) {
-    __shared__ float red[8];
+    __shared__ float red[2][8];
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Segment sg = lin::find_segment(p, blockIdx.x);
     if (!sg.live) return;
-    const bool last = sg.s == sg.count - 1;
-    const float *A = nullptr, *B = nullptr;
-    if (!last) {
-        A = d.segS + ((int64_t)(blockIdx.x + 1) * p.H + h) * d.E;
-        B = d.segD + ((int64_t)blockIdx.x * p.H + h) * d.E;
-    } else if (d.dS_out) {
-        A = d.S_T + ((int64_t)sg.n * p.H + h) * d.E;
-        B = d.dS_out + ((int64_t)sg.n * p.H + h) * d.E;
-    }
-    auto block_sum = [&](float x) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        __syncthreads();
-        if (lane == 0) red[warp] = x;
-        __syncthreads();
-        x = 0.f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w) x += red[w];
+    const int64_t seq = ((int64_t)sg.n * p.H + h) * d.E;
+    const int64_t own = ((int64_t)blockIdx.x * p.H + h) * d.E, step = (int64_t)p.H * d.E;
+    auto dot = [&](const float* A, const float* B) {
+        float x = 0.f;
+        if (A && B)
+            for (int i = threadIdx.x; i < d.E / 4; i += 256) {
+                const float4 u = reinterpret_cast<const float4*>(A)[i];
+                const float4 v = reinterpret_cast<const float4*>(B)[i];
+                x = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, x))));
+            }
         return x;
     };
-    float carry = 0.f;
-    if (A) {
-        float x = 0.f;
-        for (int i = threadIdx.x; i < d.E / 4; i += 256) {
-            const float4 u = reinterpret_cast<const float4*>(A)[i];
-            const float4 v = reinterpret_cast<const float4*>(B)[i];
-            x = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, x))));
+    // sums of x and of y over the block, the same in every thread
+    auto block_sum = [&](float& x, float& y) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, off);
+            y += __shfl_xor_sync(0xffffffffu, y, off);
         }
-        carry = block_sum(x);
+        __syncthreads();
+        if (lane == 0) { red[0][warp] = x; red[1][warp] = y; }
+        __syncthreads();
+        x = y = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) { x += red[0][w]; y += red[1][w]; }
+    };
+    // segment s's slot holds S at its start and D at its end
+    const bool first = sg.s == 0, last = sg.s == sg.count - 1;
+    float head = first ? dot(d.S0 ? d.S0 + seq : nullptr, d.dS0 + seq)
+                       : dot(d.segS + own, d.segD + own - step);
+    float tail = last ? dot(d.S_T + seq, d.dS_out ? d.dS_out + seq : nullptr)
+                      : dot(d.segS + own + step, d.segD + own);
+    block_sum(head, tail);
+    auto term = [&](int64_t t, float& x, float& size) {
+        x = size = 0.f;
+        if (t < sg.begin) return;
+        float a = 0.f, b = 0.f;
+        for (int i = 0; i < d.nq; ++i) a += d.dots_q[((int64_t)i * p.T + t) * p.H + h];
+        for (int i = 0; i < d.nk; ++i) b += d.dots_k[((int64_t)i * p.T + t) * p.H + h];
+        x = a - b;
+        size = fabsf(a) + fabsf(b);
+    };
+    float sum = 0.f, weight = 0.f;
+    for (int64_t t0 = sg.end - 1; t0 >= sg.begin; t0 -= 256) {
+        float x, size;
+        term(t0 - threadIdx.x, x, size);
+        sum += x;
+        weight += size;
     }
+    block_sum(sum, weight);
+    const float miss = (tail - head) + sum;
+    const float share = weight > 0.f ? miss / weight : 0.f;
+    float carry = tail;
     // thread i holds the i-th token from the end, so the suffix sum is a running sum
     for (int64_t t0 = sg.end - 1; t0 >= sg.begin; t0 -= 256) {
         const int64_t t = t0 - threadIdx.x;
-        float x = 0.f;
-        if (t >= sg.begin) {
-            for (int b = 0; b < d.nq; ++b) x += d.dots_q[((int64_t)b * p.T + t) * p.H + h];
-            for (int b = 0; b < d.nk; ++b) x -= d.dots_k[((int64_t)b * p.T + t) * p.H + h];
-        }
+        float x, size;
+        term(t, x, size);
+        x -= share * size;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const float y = __shfl_up_sync(0xffffffffu, x, off);
             if (lane >= off) x += y;
         }
         __syncthreads();
-        if (lane == 31) red[warp] = x;
+        if (lane == 31) red[0][warp] = x;
         __syncthreads();
         float before = 0.f, all = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-            if (w < warp) before += red[w];
-            all += red[w];
+            if (w < warp) before += red[0][w];
+            all += red[0][w];
         }
-        if (t >= sg.begin) d.dg[t * p.H + h] = carry + before + x;
+        if (t >= sg.begin) d.dg[t * p.H + h] = carry + (before + x);
         carry += all;
     }
 }
@@ -285,10 +313,17 @@ __global__ void __launch_bounds__(256) decay_sum_kernel(const float* dg, int64_t
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// bf16 runs on the tensor cores, fp32 (whose operands they would round) token by token.
+// KDA_FWD_PATH=generic in the environment forces the latter (the tests cross-check the two).
+bool use_tc(int io_bf16) {
+    const char* env = getenv("KDA_FWD_PATH");
+    return io_bf16 && !(env && strcmp(env, "generic") == 0);
+}
+
 // Tokens a segment: short enough that the segments of all heads fill the GPU a few times, no
 // shorter than the edge states' traffic (two fp32 states a segment) is worth.
-int segment_length(int64_t T, int H) {
-    int L = 64;
+int segment_length(int64_t T, int H, bool tc) {
+    int L = tc ? 128 : 64;
     while (L < 1024 && T / L * H > 4 * 152) L *= 2;
     return L;
 }
@@ -297,12 +332,12 @@ struct Layout {
     int L;
     int64_t slots;
     bool segments;  // some sequence may be longer than a segment
-    size_t add[2], seg[2], dec, S_T, dots_q, dots_k, dg, bytes;
+    size_t add[2], seg[2], dec, S_T, dS0, dots_q, dots_k, dg, bytes;
 };
 
-Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool equal) {
+Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool equal) {
     Layout l{};
-    l.L = segment_length(T, H);
+    l.L = segment_length(T, H, tc);
     l.slots = lin::slot_count(T, N, l.L);
     l.segments = (equal && N > 0 ? T / N : T) > l.L;
     const size_t state = (size_t)H * dk * dv * sizeof(float);
@@ -319,6 +354,7 @@ Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool equal) {
     l.dec = take(l.segments ? (size_t)2 * l.slots * H * sizeof(float) : 0);
     if (bwd) {
         l.S_T = take((size_t)N * state);
+        l.dS0 = take((size_t)N * state);
         l.dots_q = take((size_t)(dk / kCols) * T * H * sizeof(float));
         l.dots_k = take((size_t)(dk / kCols) * T * H * sizeof(float));
         l.dg = take((size_t)T * H * sizeof(float));
@@ -347,16 +383,20 @@ void launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, fl
 }
 
 template <bool kOut>
-void launch_token(const LinearArgs& a, const Problem& p, const Calls& calls, int n, int64_t slots,
-                  float* dec, const char* name) {
+cudaError_t launch_calls(const LinearArgs& a, const Problem& p, const Calls& calls, int n,
+                         int64_t slots, float* dec, const char* name) {
+    if (use_tc(a.io_bf16))
+        return kOut ? lintc::launch_outputs(p, calls, n, slots, name, a.stream)
+                    : lintc::launch_sums(p, calls, n, slots, dec, name, a.stream);
     if (a.io_bf16)
         launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream);
     else
         launch_token<float, kOut>(p, calls, n, slots, dec, name, a.stream);
+    return cudaGetLastError();
 }
 
 // Segment sums and edges of the forward states and, in a backward pass, of the reversed ones.
-void launch_segments(const LinearArgs& a, const Problem& p, const Layout& l, bool bwd) {
+cudaError_t launch_segments(const LinearArgs& a, const Problem& p, const Layout& l, bool bwd) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     float* dec = reinterpret_cast<float*>(ws + l.dec);
     Calls calls{};
@@ -373,41 +413,47 @@ void launch_segments(const LinearArgs& a, const Problem& p, const Layout& l, boo
         e.dec[i] = dec + (size_t)i * l.slots * a.H;
     }
     e.E = a.dk * a.dv;
-    launch_token<false>(a, p, calls, bwd ? 2 : 1, l.slots, dec, "linear_segment_kernel");
+    if (cudaError_t err = launch_calls<false>(a, p, calls, bwd ? 2 : 1, l.slots, dec,
+                                              "linear_segment_kernel"))
+        return err;
     ProfScope prof("linear_edge_kernel", a.stream);
     const dim3 grid(a.H * (e.E / 1024), a.N < 64 ? a.N : 64, bwd ? 2 : 1);
     edge_kernel<<<grid, 256, 0, a.stream>>>(p, e);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-size_t linear_fwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int) {
-    return layout(T, N, H, dk, dv, false, false).bytes;
+size_t linear_fwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int io_bf16) {
+    return layout(T, N, H, dk, dv, false, use_tc(io_bf16), false).bytes;
 }
-size_t linear_bwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int) {
-    return layout(T, N, H, dk, dv, true, false).bytes;
+size_t linear_bwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int io_bf16) {
+    return layout(T, N, H, dk, dv, true, use_tc(io_bf16), false).bytes;
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a) {
-    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, false, a.cu_seqlens == nullptr);
+    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, false, use_tc(a.io_bf16),
+                            a.cu_seqlens == nullptr);
     const Problem p = problem(a, l.L);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    if (l.segments) launch_segments(a, p, l, false);
+    if (l.segments)
+        if (cudaError_t e = launch_segments(a, p, l, false)) return e;
     Calls calls{};
     Call& c = calls.c[0];
     c.x = a.q; c.x_ld = a.q_ld; c.y = a.k; c.y_ld = a.k_ld; c.w = a.v; c.w_ld = a.v_ld;
     c.da = a.dk; c.db = a.dv; c.edge = a.S0; c.S_out = a.S_out; c.out = a.o;
     c.seg = reinterpret_cast<float*>(ws + l.seg[0]);
-    launch_token<true>(a, p, calls, 1, l.slots, nullptr, "linear_out_kernel");
-    return cudaGetLastError();
+    return launch_calls<true>(a, p, calls, 1, l.slots, nullptr, "linear_out_kernel");
 }
 
 cudaError_t launch_linear_bwd(const LinearArgs& a) {
-    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, true, a.cu_seqlens == nullptr);
+    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, true, use_tc(a.io_bf16),
+                            a.cu_seqlens == nullptr);
     const Problem p = problem(a, l.L);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
-    if (l.segments) launch_segments(a, p, l, true);
+    if (l.segments)
+        if (cudaError_t e = launch_segments(a, p, l, true)) return e;
     const bool anchor = a.dg && a.dS_out;
     Calls calls{};
     Call &q = calls.c[0], &k = calls.c[1], &v = calls.c[2];
@@ -421,12 +467,14 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
     if (a.dg) { k.dot = a.k; k.dot_ld = a.k_ld; k.dots = at(l.dots_k); }
     v.x = a.k; v.x_ld = a.k_ld; v.y = a.q; v.y_ld = a.q_ld; v.w = a.dout; v.w_ld = a.dout_ld;
     v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = at(l.seg[1]);
-    v.S_out = a.dS0; v.out = a.dv_;
-    launch_token<true>(a, p, calls, 3, l.slots, nullptr, "linear_grad_kernel");
+    v.S_out = a.dS0 ? a.dS0 : a.dg && a.S0 ? at(l.dS0) : nullptr; v.out = a.dv_;
+    if (cudaError_t e =
+            launch_calls<true>(a, p, calls, 3, l.slots, nullptr, "linear_grad_kernel"))
+        return e;
     if (a.dg) {
         DecayGrad d{};
         d.segS = at(l.seg[0]); d.segD = at(l.seg[1]);
-        d.S_T = at(l.S_T); d.dS_out = a.dS_out;
+        d.S_T = at(l.S_T); d.dS_out = a.dS_out; d.S0 = a.S0; d.dS0 = v.S_out;
         d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kCols;
         d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
         if (a.T_total > 0) {
