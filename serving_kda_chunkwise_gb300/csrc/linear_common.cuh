@@ -57,7 +57,7 @@ __host__ __device__ inline int64_t slot_count(int64_t T, int N, int L) { return 
 struct Segment {
     int n;                // sequence
     int s, count;         // segment of the sequence, and how many it has
-    int64_t begin, end;   // its tokens
+    int begin, end;       // its tokens (there are fewer than 2^31)
     bool live;
 };
 
@@ -86,8 +86,8 @@ __device__ __forceinline__ Segment find_segment(const Problem& p, int64_t j) {
     const int64_t s = j - ((p.cu ? a : seq_start(p, lo)) / p.L + lo);
     r.live = s >= 0 && s < r.count;
     r.s = (int)s;
-    r.begin = a + s * p.L;
-    r.end = r.begin + p.L < b ? r.begin + p.L : b;
+    r.begin = (int)(a + s * p.L);
+    r.end = (int)(a + (s + 1) * p.L < b ? a + (s + 1) * p.L : b);
     return r;
 }
 

@@ -52,22 +52,27 @@ __device__ __forceinline__ void landed(float (&v)[16]) {
                  :
                  : "memory");
 }
-template <int N>
-__device__ __forceinline__ void landed(float (&v)[N]) {
-    static_assert(N == 32, "16 or 32 columns");
-    landed(reinterpret_cast<float(&)[16]>(v[0]));
-    landed(reinterpret_cast<float(&)[16]>(v[16]));
+__device__ __forceinline__ void landed(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                   "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                   "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                   "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[30]), "+f"(v[31]) : : "memory");
 }
 
 // ---------------------------------------------------------------- decays --
-// log2 decays of the chunk's tokens 32 b + lane, b = 0..3; tokens past the segment do not decay.
-__device__ __forceinline__ void load_decays(const Problem& p, int64_t t0, int len, int h, int lane,
+// Log decays of the chunk's tokens 32 b + lane, b = 0..3, as they are in memory (loaded a chunk
+// ahead); tokens past the segment do not decay.
+__device__ __forceinline__ void load_decays(const Problem& p, int t0, int len, int h, int lane,
                                             float (&e)[4]) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         const int i = 32 * b + lane;
-        float x = i < len ? lin::log_decay(p, t0 + i, h) * kLog2e : 0.f;
-        e[b] = x < -2000.f ? -2000.f : x;
+        e[b] = i < len ? lin::log_decay(p, t0 + i, h) : 0.f;
     }
 }
 
@@ -82,8 +87,14 @@ struct Sums {
 };
 
 template <bool kTwo>
-__device__ __forceinline__ Sums sums(const float (&e)[4], int q, int lane) {
+__device__ __forceinline__ Sums sums(const float (&g)[4], int q, int lane) {
     Sums r;
+    float e[4];  // log2 decays
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float x = g[b] * kLog2e;
+        e[b] = x < -2000.f ? -2000.f : x;
+    }
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         float x = e[b];
@@ -92,25 +103,24 @@ __device__ __forceinline__ Sums sums(const float (&e)[4], int q, int lane) {
         r.B[b] = x;
     }
     const float own = pick(e, q);
-    if (kTwo) {
-        double x = own;
+    float x = own, lo = 0.f;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
+    for (int off = 1; off < 32; off <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, x, off);
+        if (kTwo) {  // (x, lo) += (y, ylo), the rounding of x + y kept in lo
+            const float ylo = __shfl_up_sync(0xffffffffu, lo, off);
+            if (lane >= off) {
+                const float s = __fadd_rn(x, y), d = __fsub_rn(s, x);
+                const float err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, d)), __fsub_rn(y, d));
+                x = s;
+                lo = __fadd_rn(__fadd_rn(lo, ylo), err);
+            }
+        } else if (lane >= off) {
+            x += y;
         }
-        r.P = (float)x;
-        r.Plo = (float)(x - (double)r.P);
-    } else {
-        float x = own;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
-        }
-        r.P = x;
-        r.Plo = 0.f;
     }
+    r.P = x;
+    r.Plo = lo;
     float u = __shfl_down_sync(0xffffffffu, own, 1);
     if (lane == 31) u = 0.f;
 #pragma unroll
@@ -141,7 +151,7 @@ __device__ __forceinline__ float after(const Sums& s, int q) {
 // calls of one (slot, head) next to each other so that they share the rows through L2.
 struct Item {
     Segment sg;
-    int64_t slot;
+    int slot;
     int call, h, half, chunks;
     bool live;
 };
@@ -166,7 +176,7 @@ __device__ __forceinline__ Item item_at(const OutParams& o, int64_t i) {
     t.call = (int)(i % o.n_calls);
     i /= o.n_calls;
     t.h = (int)(i % o.p.H);
-    t.slot = i / o.p.H;
+    t.slot = (int)(i / o.p.H);
     t.sg = lin::find_segment(o.p, t.slot);
     t.live = t.sg.live && t.half * 64 < o.calls.c[t.call].db;
     t.chunks = t.live ? (int)((t.sg.end - t.sg.begin + kC - 1) / kC) : 0;
@@ -174,22 +184,21 @@ __device__ __forceinline__ Item item_at(const OutParams& o, int64_t i) {
 }
 
 // First token and length of the c-th chunk of the walk.
-__device__ __forceinline__ void chunk_at(const Item& t, int reverse, int c, int64_t& t0, int& len) {
+__device__ __forceinline__ void chunk_at(const Item& t, int reverse, int c, int& t0, int& len) {
     const int i = reverse ? t.chunks - 1 - c : c;
-    t0 = t.sg.begin + (int64_t)i * kC;
-    const int64_t rest = t.sg.end - t0;
-    len = rest < kC ? (int)rest : kC;
+    t0 = t.sg.begin + i * kC;
+    len = min(t.sg.end - t0, kC);
 }
 
 // -------------------------------------------------------------- outputs --
-// Persistent, one CTA an SM.  Roles: warp 0 issues the TMA loads (two stages), warp 1 the MMAs,
-// warps 4..11 turn X Y^T into A (hi + lo over the product's own TMEM columns, so that A never
-// leaves tensor memory), warps 12..19 decay W, convert the state and write the outputs.  Warp w
+// Persistent, one CTA an SM.  Roles: warps 0..3 turn X Y^T into A (hi + lo over the product's own
+// TMEM columns, so that A never leaves tensor memory), warp 12 issues the TMA loads (two stages),
+// warp 13 the MMAs, and warps 4..11 decay W, convert the state and write the outputs.  Warp w
 // reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in fp32; X S reads its bf16
 // hi + lo copy in shared memory.
 // A CTA takes 64 of the db columns: two full stages of X, Y and W then fit beside the decayed W
 // and the state, at the price of forming A twice for db = 128.
-constexpr int kThreads = 640;
+constexpr int kThreads = 448;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536, kStage = 81920;  // two stages
 constexpr uint32_t kSWd = 2 * kStage;       // decayed W: hi, lo (16 KB each)
 constexpr uint32_t kSS = kSWd + 32768;      // state: hi, lo (16 KB each)
@@ -203,8 +212,8 @@ constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = 320, kTS = 448;
 
 struct OutBars {
     uint64_t full[2], done[2];   // stage loaded; every MMA of the stage's chunk complete
-    uint64_t sc[2], a[2];        // X Y^T complete; A written (8 arrivals)
-    uint64_t col[2];             // column factors written (8 arrivals)
+    uint64_t sc[2], a[2];        // X Y^T complete; A written (4 arrivals)
+    uint64_t col[2];             // column factors written (4 arrivals)
     uint64_t s, wd;              // state and its copy written; decayed W written (8 arrivals each)
     uint64_t upd, qs;            // state update complete; X S complete
     uint64_t o_full, o_free;     // chunk's outputs complete; read (8 arrivals)
@@ -227,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.done[i], 1);
             mbar_init(&bar.sc[i], 1);
-            mbar_init(&bar.a[i], 8);
-            mbar_init(&bar.col[i], 8);
+            mbar_init(&bar.a[i], 4);
+            mbar_init(&bar.col[i], 4);
         }
         mbar_init(&bar.s, 8);
         mbar_init(&bar.wd, 8);
@@ -249,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     const int64_t items = item_count(o);
     int loaded[2] = {-1, -1};  // phase of each stage's last load (for the way out of an abort)
 
-    if (warp == 0) {
+    if (warp == 12) {
         // --------------------------------------------------------- TMA warp
         uint32_t g = 0;
         bool ok = true;
@@ -263,24 +272,24 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     ok = false;
                     break;
                 }
-                int64_t t0;
+                int t0;
                 int len;
                 chunk_at(t, c.reverse, k, t0, len);
                 if (lane == 0) {
                     uint8_t* s = sm + st * kStage;
                     mbar_expect_tx(&bar.full[st], blocks * 32768 + 16384);
                     for (int b = 0; b < blocks; ++b) {
-                        tma_load_3d(s + kSX + b * 16384, &o.x[t.call], 64 * b, t.h, (int)t0,
+                        tma_load_3d(s + kSX + b * 16384, &o.x[t.call], 64 * b, t.h, t0,
                                     &bar.full[st]);
-                        tma_load_3d(s + kSY + b * 16384, &o.y[t.call], 64 * b, t.h, (int)t0,
+                        tma_load_3d(s + kSY + b * 16384, &o.y[t.call], 64 * b, t.h, t0,
                                     &bar.full[st]);
                     }
-                    tma_load_3d(s + kSW, &o.w[t.call], 64 * t.half, t.h, (int)t0, &bar.full[st]);
+                    tma_load_3d(s + kSW, &o.w[t.call], 64 * t.half, t.h, t0, &bar.full[st]);
                 }
                 loaded[st] = (int)((g >> 1) & 1);
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 13) {
         // --------------------------------------------------------- MMA warp
         constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
         constexpr uint32_t id_aw = idesc_bf16(128, 64, false, true);    // A W, X S
@@ -367,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 __syncwarp();
             }
         }
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp < 4) {
         // ------------------------------------------------------------ A warps
-        const int q = warp & 3, wg = (warp - 4) >> 2;
+        const int q = warp;
         const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
         float* col = reinterpret_cast<float*>(sm + kSCol);
         float* diag = reinterpret_cast<float*>(sm + kSDiag);
@@ -379,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             const Item t = item_at(o, i);
             const int rev = o.calls.c[t.call].reverse;
             const bool dots = o.calls.c[t.call].dot != nullptr;
-            int64_t t0;
+            int t0;
             int len;
             float e[4];
             if (t.chunks) {
@@ -390,21 +399,19 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 const uint32_t st = g & 1;
                 const Sums s = sums<true>(e, q, lane);
                 const int this_len = len;
-                if (wg == 0) col[128 * st + 32 * q + lane] = ex2f(rev ? s.P : s.U);
+                col[128 * st + 32 * q + lane] = ex2f(rev ? s.P : s.U);
                 if (k + 1 < t.chunks) {
                     chunk_at(t, rev, k + 1, t0, len);
                     load_decays(p, t0, len, t.h, lane, e);
                 }
-                // all eight warps are past the previous chunk and their column factors written
+                // all four warps are past the previous chunk and their column factors written
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.col[st]);
                 if (!wait(&bar.col[st], (g >> 1) & 1, p.err, abort) ||
                     !wait(&bar.sc[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-                // this warp's column blocks: 0 and 3, or 1 and 2 (at most two with work in any row)
-#pragma unroll
-                for (int b2 = 0; b2 < 2; ++b2) {
-                    const int j = wg == 0 ? 3 * b2 : 1 + b2;
+#pragma unroll 1
+                for (int j = 0; j < 4; ++j) {
                     const uint32_t at = tmem + lb + kTA + 128 * st + 32 * j;
                     const bool off = rev ? j < q : j > q;
                     float rf = 0.f;  // the row's decay up to the block
@@ -415,16 +422,21 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                             x += (rev ? b > q && b < j : b < q && b > j) ? s.B[b] : 0.f;
                         rf = ex2f(x);
                     }
+                    float w[2][16];
+                    if (!off) {
+                        tmem_ld16(at, w[0]);
+                        tmem_ld16(at + 16, w[1]);
+                        landed(w[0]);
+                        landed(w[1]);
+                    }
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
                         uint32_t hi[8], lo[8];
+                        float(&v)[16] = w[hf];
                         if (off) {
 #pragma unroll
                             for (int c = 0; c < 8; ++c) hi[c] = lo[c] = 0u;
                         } else {
-                            float v[16];
-                            tmem_ld16(at + 16 * hf, v);
-                            landed(v);
                             if (j == q) {
 #pragma unroll
                                 for (int c = 0; c < 16; ++c) {
@@ -475,9 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 if (lane == 0) mbar_arrive(&bar.a[st]);
             }
         }
-    } else if (warp >= 12) {
+    } else {
         // --------------------------------------- state, decayed W and outputs
-        const int q = warp & 3, wg = (warp - 12) >> 2;
+        const int q = warp & 3, wg = (warp - 4) >> 2;
         const int row = 32 * q + lane;  // token, or state row
         const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
         uint32_t g = 0;
@@ -499,13 +511,27 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 continue;
             }
             const float* from =
-                t.sg.count > 1 ? c.seg + (t.slot * p.H + t.h) * E + mine
+                t.sg.count > 1 ? c.seg + ((int64_t)t.slot * p.H + t.h) * E + mine
                                : c.edge ? c.edge + seq : nullptr;
             float S[32];
 #pragma unroll
-            for (int x = 0; x < 32; ++x) S[x] = from && sv ? from[x * cs] : 0.f;
-            int64_t t0, t0_prev = 0;
-            int len, len_prev = 0;
+            for (int x = 0; x < 32; ++x) S[x] = 0.f;
+            if (from && sv) {
+                if (c.tr) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) S[x] = __ldcg(from + x * cs);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const float4 f = __ldcg(reinterpret_cast<const float4*>(from) + x);
+                        S[4 * x] = f.x;
+                        S[4 * x + 1] = f.y;
+                        S[4 * x + 2] = f.z;
+                        S[4 * x + 3] = f.w;
+                    }
+                }
+            }
+            int t0, t0_prev = 0, len, len_prev = 0;
             float rowf_prev = 0.f;
             float e[4];
             chunk_at(t, rev, 0, t0, len);
@@ -516,17 +542,17 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             // diagonal's term x_r . y_r w_r, which is added here in fp32 and left out of the
             // dot: it is the same number in both of the decay's gradient's sums, where under
             // strong decays everything else is far below its rounding.
-            auto write_out = [&](uint32_t gg, int64_t tt, int n, float rowf) -> bool {
+            auto write_out = [&](uint32_t gg, int tt, int n, float rowf) -> bool {
                 if (!wait(&bar.o_full, gg & 1, p.err, abort)) return false;
                 tc_fence_after();
-                const int64_t at = ((tt + row) * p.H + t.h) * c.db + 64 * t.half + 32 * wg;
+                const int64_t at = ((int64_t)(tt + row) * p.H + t.h) * c.db + 64 * t.half + 32 * wg;
                 __nv_bfloat16* out = static_cast<__nv_bfloat16*>(c.out) + at;
                 const __nv_bfloat16* dot =
-                    c.dot ? static_cast<const __nv_bfloat16*>(c.dot) + (tt + row) * c.dot_ld +
+                    c.dot ? static_cast<const __nv_bfloat16*>(c.dot) + (int64_t)(tt + row) * c.dot_ld +
                                 (int64_t)t.h * c.db + 64 * t.half + 32 * wg
                           : nullptr;
                 const __nv_bfloat16* wrow =
-                    static_cast<const __nv_bfloat16*>(c.w) + (tt + row) * c.w_ld +
+                    static_cast<const __nv_bfloat16*>(c.w) + (int64_t)(tt + row) * c.w_ld +
                     (int64_t)t.h * c.db + 64 * t.half + 32 * wg;
                 const float dg =
                     dot ? reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg % 3) + row] : 0.f;
@@ -582,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 const float rowf = ex2f(rev ? tail : head);
                 const float wf = row < len ? ex2f(rev ? head : tail) : 0.f;
                 const float all = ex2f((s.B[0] + s.B[1]) + (s.B[2] + s.B[3]));
-                const int64_t t0_now = t0;
+                const int t0_now = t0;
                 const int len_now = len;
                 if (k + 1 < t.chunks) {
                     chunk_at(t, rev, k + 1, t0, len);
@@ -675,10 +701,10 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     __syncthreads();
     if (bar.abort) {
         // let copies and MMAs still in flight land before leaving
-        if (warp == 0)
+        if (warp == 12)
             for (int st = 0; st < 2; ++st)
                 if (loaded[st] >= 0) mbar_wait(&bar.full[st], loaded[st], nullptr);
-        if (tid == 32) {
+        if (tid == 13 * 32) {
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, nullptr);
         }
@@ -753,17 +779,17 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                     ok = false;
                     break;
                 }
-                int64_t t0;
+                int t0;
                 int len;
                 chunk_at(t, !c.reverse, k, t0, len);
                 if (lane == 0) {
                     uint8_t* s = sm + st * kUStage;
                     mbar_expect_tx(&bar.full[st], (c.da + c.db) / 64 * 16384);
                     for (int b = 0; b < c.da / 64; ++b)
-                        tma_load_3d(s + kUY + b * 16384, &o.y[t.call], 64 * b, t.h, (int)t0,
+                        tma_load_3d(s + kUY + b * 16384, &o.y[t.call], 64 * b, t.h, t0,
                                     &bar.full[st]);
                     for (int b = 0; b < c.db / 64; ++b)
-                        tma_load_3d(s + kUW + b * 16384, &o.w[t.call], 64 * b, t.h, (int)t0,
+                        tma_load_3d(s + kUW + b * 16384, &o.w[t.call], 64 * b, t.h, t0,
                                     &bar.full[st]);
                 }
                 loaded[st] = (int)((g >> 1) & 1);
@@ -807,7 +833,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             const Call& c = o.calls.c[t.call];
             const int rev = c.reverse;
             float between = 0.f;  // log2 decay between the edge and the chunk
-            int64_t t0;
+            int t0;
             int len;
             float e[4];
             chunk_at(t, !rev, 0, t0, len);
@@ -859,7 +885,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             const uint32_t gl = g - 1;
             if (!wait(&bar.done[gl & 1], (gl >> 1) & 1, p.err, abort)) { ok = false; break; }
             tc_fence_after();
-            const int64_t at = ((t.slot * p.H + t.h) * c.da + row) * c.db + 64 * wg;
+            const int64_t at = (((int64_t)t.slot * p.H + t.h) * c.da + row) * c.db + 64 * wg;
             if (64 * wg < c.db) {
                 float* to = const_cast<float*>(c.seg) + at;
 #pragma unroll
