@@ -37,10 +37,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ---------------------------------------------------------------- waits --
 // A whole warp waits, and all of its lanes agree on whether it did: after an abort no lane is
-// left behind at a later warp-wide step.
+// left behind at a later warp-wide step.  The polling loop is kept out of line: each role runs its
+// code once a chunk, beside the other roles', and what does not fit the instruction cache costs.
+__device__ __noinline__ bool wait_poll(uint64_t* bar, uint32_t parity, unsigned* err,
+                                       volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_ab(bar, parity, err, abort));
+}
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned* err,
                                      volatile int* abort) {
-    return __all_sync(0xffffffffu, mbar_wait_ab(bar, parity, err, abort));
+    if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
+    return wait_poll(bar, parity, err, abort);
 }
 
 // The registers of earlier TMEM loads are ready (tied to the wait, so that no use moves above it).
@@ -256,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
     const int64_t items = item_count(o);
-    int loaded[2] = {-1, -1};  // phase of each stage's last load (for the way out of an abort)
+    int loads = 0;  // stages loaded by the TMA warp (for the way out of an abort)
 
     if (warp == 12) {
         // --------------------------------------------------------- TMA warp
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     }
                     tma_load_3d(s + kSW, &o.w[t.call], 64 * t.half, t.h, t0, &bar.full[st]);
                 }
-                loaded[st] = (int)((g >> 1) & 1);
+                loads = (int)g + 1;
             }
         }
     } else if (warp == 13) {
@@ -296,14 +302,11 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         constexpr uint32_t id_up = idesc_bf16(128, 64, true, true);     // Y^T W
         const uint64_t dWd = sdesc_sw128(sbase + kSWd, 0, 1024);
         const uint64_t dS = sdesc_sw128(sbase + kSS, 0, 1024);
-        uint64_t dX[2], dYk[2], dYm[2], dW[2];
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            dX[st] = sdesc_sw128(sbase + st * kStage + kSX, 0, 1024);
-            dYk[st] = sdesc_sw128(sbase + st * kStage + kSY, 0, 1024);
-            dYm[st] = sdesc_sw128(sbase + st * kStage + kSY, 16384, 1024);
-            dW[st] = sdesc_sw128(sbase + st * kStage + kSW, 0, 1024);
-        }
+        // of stage 0; stage 1 is kStage bytes on
+        const uint64_t dX = sdesc_sw128(sbase + kSX, 0, 1024);
+        const uint64_t dYk = sdesc_sw128(sbase + kSY, 0, 1024);
+        const uint64_t dYm = sdesc_sw128(sbase + kSY, 16384, 1024);
+        const uint64_t dW = sdesc_sw128(sbase + kSW, 0, 1024);
         // chunks ahead of the current one: where the walk of X Y^T stands
         int64_t next_i = blockIdx.x;
         int next_left = 0, next_da = 0;
@@ -321,8 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             tc_fence_after();
             if (lane == 0) {
                 for (int ks = 0; ks < next_da / 16; ++ks) {
-                    const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                    mma_bf16(tmem + kTA + 128 * st, dX[st] + off, dYk[st] + off, id_sc, ks > 0);
+                    const uint32_t off = (st * kStage + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                    mma_bf16(tmem + kTA + 128 * st, dX + off, dYk + off, id_sc, ks > 0);
                 }
                 mma_commit(&bar.sc[st]);
             }
@@ -345,14 +348,14 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     // S += Y^T Wd: 128 tokens in 8 steps, hi then lo (da = 64: the second 64
                     // lanes take whatever the block's second half holds and are never read)
                     for (int ks = 0; ks < 16; ++ks)
-                        mma_bf16(tmem + kTS, dYm[st] + ((ks & 7) * 2048 >> 4),
+                        mma_bf16(tmem + kTS, dYm + ((st * kStage + (ks & 7) * 2048) >> 4),
                                  dWd + (((ks >> 3) * 16384 + (ks & 7) * 2048) >> 4), id_up, 1);
                     mma_commit(&bar.upd);
                     // X S
                     for (int ks = 0; ks < da / 8; ++ks) {
                         const int half = ks >= da / 16, kk = ks - half * (da / 16);
                         mma_bf16(tmem + kTO2 + 64 * st,
-                                 dX[st] + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                                 dX + ((st * kStage + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
                                  dS + ((half * 16384 + kk * 2048) >> 4), id_aw, ks > 0);
                     }
                     mma_commit(&bar.qs);
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     for (int ks = 0; ks < 16; ++ks) {
                         const int kk = ks & 7;
                         mma_bf16_ts(tmem + kTO1, tmem + kTA + 128 * st + 16 * kk + 8 * (ks >> 3),
-                                    dW[st] + (kk * 2048 >> 4), id_aw, ks > 0);
+                                    dW + ((st * kStage + kk * 2048) >> 4), id_aw, ks > 0);
                     }
                     mma_commit(&bar.o_full);
                     mma_commit(&bar.done[st]);
@@ -408,78 +411,72 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.col[st]);
                 if (!wait(&bar.col[st], (g >> 1) & 1, p.err, abort) ||
-                    !wait(&bar.sc[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
+                    !wait(&bar.sc[st], (g >> 1) & 1, p.err, abort)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
+                const uint32_t at = tmem + lb + kTA + 128 * st;
+                float to_block = rev ? s.U : s.P;  // log2 decay between the row and block j
 #pragma unroll 1
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t at = tmem + lb + kTA + 128 * st + 32 * j;
-                    const bool off = rev ? j < q : j > q;
-                    float rf = 0.f;  // the row's decay up to the block
-                    if (!off && j != q) {
-                        float x = rev ? s.U : s.P;
+                for (int n = 0; n < 4; ++n) {  // blocks at distance n from the diagonal
+                    const int j = rev ? q + n : q - n, z = rev ? q - n : q + n;
+                    if (n > 0 && z >= 0 && z < 4) {  // outside the triangle
+                        uint32_t zero[32];
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            x += (rev ? b > q && b < j : b < q && b > j) ? s.B[b] : 0.f;
-                        rf = ex2f(x);
+                        for (int c = 0; c < 32; ++c) zero[c] = 0u;
+                        tmem_st32(at + 32 * z, zero);
                     }
-                    float w[2][16];
-                    if (!off) {
-                        tmem_ld16(at, w[0]);
-                        tmem_ld16(at + 16, w[1]);
-                        landed(w[0]);
-                        landed(w[1]);
-                    }
+                    if (j < 0 || j > 3) continue;
+                    float v[32];
+                    tmem_ld32(at + 32 * j, v);
+                    landed(v);
+                    if (n == 0) {
+                        // columns of the triangle that are tokens of the segment
+                        uint32_t in = rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
+                        if (rev && this_len - 32 * q < 32)
+                            in &= this_len > 32 * q ? (1u << (this_len - 32 * q)) - 1u : 0u;
+                        if (dots) {
+                            float own = 0.f;
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t hi[8], lo[8];
-                        float(&v)[16] = w[hf];
-                        if (off) {
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) hi[c] = lo[c] = 0u;
-                        } else {
-                            if (j == q) {
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) {
-                                    const int ci = 16 * hf + c;  // token of the block
-                                    const float ph = __shfl_sync(0xffffffffu, s.P, ci);
-                                    const float pl = __shfl_sync(0xffffffffu, s.Plo, ci);
-                                    float x = (s.P - ph) + (s.Plo - pl);
-                                    if (rev) x = -x;
-                                    bool in = rev ? ci >= lane && 32 * q + ci < this_len
-                                                  : ci <= lane;
-                                    if (dots && ci == lane) {
-                                        diag[128 * (g % 3) + 32 * q + lane] = v[c];
-                                        in = false;
-                                    }
-                                    v[c] = in ? v[c] * ex2f(x) : 0.f;
-                                }
-                            } else {
-                                const float4* cf = reinterpret_cast<const float4*>(
-                                    col + 128 * st + 32 * j + 16 * hf);
-#pragma unroll
-                                for (int c4 = 0; c4 < 4; ++c4) {
-                                    const float4 f = cf[c4];
-                                    v[4 * c4] *= rf * f.x;
-                                    v[4 * c4 + 1] *= rf * f.y;
-                                    v[4 * c4 + 2] *= rf * f.z;
-                                    v[4 * c4 + 3] *= rf * f.w;
-                                }
-                                if (rev && this_len < kC)
-#pragma unroll
-                                    for (int c = 0; c < 16; ++c)
-                                        if (32 * j + 16 * hf + c >= this_len) v[c] = 0.f;
-                            }
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) {
-                                hi[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
-                                lo[c] = pack_bf16x2(
-                                    v[2 * c] - __uint_as_float(hi[c] << 16),
-                                    v[2 * c + 1] - __uint_as_float(hi[c] & 0xffff0000u));
-                            }
+                            for (int c = 0; c < 32; ++c) own = c == lane ? v[c] : own;
+                            diag[128 * (g % 3) + 32 * q + lane] = own;
+                            in &= ~(1u << lane);
                         }
-                        tmem_st8(at + 16 * hf, hi);
-                        tmem_st8(at + 16 * hf + 8, lo);
+                        const float ph = rev ? -s.P : s.P, pl = rev ? -s.Plo : s.Plo;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float x = (ph - __shfl_sync(0xffffffffu, ph, c)) +
+                                            (pl - __shfl_sync(0xffffffffu, pl, c));
+                            v[c] = in & (1u << c) ? v[c] * ex2f(x) : 0.f;
+                        }
+                    } else {
+                        const float rf = ex2f(to_block);
+                        to_block += pick(s.B, j);
+                        const float4* cf = reinterpret_cast<const float4*>(col + 128 * st + 32 * j);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const float4 f = cf[c];
+                            v[4 * c] *= rf * f.x;
+                            v[4 * c + 1] *= rf * f.y;
+                            v[4 * c + 2] *= rf * f.z;
+                            v[4 * c + 3] *= rf * f.w;
+                        }
+                        if (rev && this_len - 32 * j < 32)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c)
+                                if (32 * j + c >= this_len) v[c] = 0.f;
                     }
+                    uint32_t u[32];  // each 16-token step: 8 columns of hi, 8 of lo
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const int k2 = 16 * (c >> 3) + (c & 7);
+                        u[k2] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+                        u[k2 + 8] =
+                            pack_bf16x2(v[2 * c] - __uint_as_float(u[k2] << 16),
+                                        v[2 * c + 1] - __uint_as_float(u[k2] & 0xffff0000u));
+                    }
+                    tmem_st32(at + 32 * j, u);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -513,66 +510,163 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             const float* from =
                 t.sg.count > 1 ? c.seg + ((int64_t)t.slot * p.H + t.h) * E + mine
                                : c.edge ? c.edge + seq : nullptr;
-            float S[32];
-#pragma unroll
-            for (int x = 0; x < 32; ++x) S[x] = 0.f;
-            if (from && sv) {
-                if (c.tr) {
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) S[x] = __ldcg(from + x * cs);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const float4 f = __ldcg(reinterpret_cast<const float4*>(from) + x);
-                        S[4 * x] = f.x;
-                        S[4 * x + 1] = f.y;
-                        S[4 * x + 2] = f.z;
-                        S[4 * x + 3] = f.w;
-                    }
-                }
-            }
-            int t0, t0_prev = 0, len, len_prev = 0;
-            float rowf_prev = 0.f;
+            int t0, len;
             float e[4];
             chunk_at(t, rev, 0, t0, len);
             load_decays(p, t0, len, t.h, lane, e);
-
-            // Outputs of chunk gg (first token tt, n tokens): rowf * (X S) + A W.  Where the
-            // outputs' dot products with another row are wanted, A W comes without the
-            // diagonal's term x_r . y_r w_r, which is added here in fp32 and left out of the
-            // dot: it is the same number in both of the decay's gradient's sums, where under
-            // strong decays everything else is far below its rounding.
-            auto write_out = [&](uint32_t gg, int tt, int n, float rowf) -> bool {
-                if (!wait(&bar.o_full, gg & 1, p.err, abort)) return false;
+            {
+                // the segment's edge state into TMEM, once the last segment's is done with
+                float S[32];
+#pragma unroll
+                for (int x = 0; x < 32; ++x) S[x] = 0.f;
+                if (from && sv) {
+                    if (c.tr) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) S[x] = __ldcg(from + x * cs);
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            const float4 f = __ldcg(reinterpret_cast<const float4*>(from) + x);
+                            S[4 * x] = f.x;
+                            S[4 * x + 1] = f.y;
+                            S[4 * x + 2] = f.z;
+                            S[4 * x + 3] = f.w;
+                        }
+                    }
+                }
+                if (g > 0 && !wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-                const int64_t at = ((int64_t)(tt + row) * p.H + t.h) * c.db + 64 * t.half + 32 * wg;
-                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(c.out) + at;
-                const __nv_bfloat16* dot =
-                    c.dot ? static_cast<const __nv_bfloat16*>(c.dot) + (int64_t)(tt + row) * c.dot_ld +
-                                (int64_t)t.h * c.db + 64 * t.half + 32 * wg
-                          : nullptr;
-                const __nv_bfloat16* wrow =
-                    static_cast<const __nv_bfloat16*>(c.w) + (int64_t)(tt + row) * c.w_ld +
-                    (int64_t)t.h * c.db + 64 * t.half + 32 * wg;
-                const float dg =
-                    dot ? reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg % 3) + row] : 0.f;
-                float acc = 0.f;
+                uint32_t u[32];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float o1[16], o2[16];
-                    tmem_ld16(tmem + lb + kTO1 + 32 * wg + 16 * b, o1);
-                    tmem_ld16(tmem + lb + kTO2 + 64 * (gg & 1) + 32 * wg + 16 * b, o2);
-                    landed(o1);
-                    landed(o2);
+                for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(S[x]);
+                tmem_st32(tmem + lb + kTS + 32 * wg, u);
+                tmem_st_wait();
+            }
+            int t0_prev = 0, len_prev = 0;
+            float rowf_prev = 0.f;
+            // step k: the state's copy and the decayed W of chunk k, then the outputs of chunk
+            // k - 1 while the tensor cores work on chunk k
+#pragma unroll 1
+            for (int k = 0; k <= t.chunks; ++k) {
+                const int t0_now = t0, len_now = len;
+                float rowf = 0.f;
+                if (k < t.chunks) {
+                    const uint32_t st = g & 1;
+                    const Sums s = sums<false>(e, q, lane);
+                    const float head = s.P + before(s, q), tail = s.U + after(s, q);
+                    rowf = ex2f(rev ? tail : head);
+                    const float wf = row < len ? ex2f(rev ? head : tail) : 0.f;
+                    const float all = ex2f((s.B[0] + s.B[1]) + (s.B[2] + s.B[3]));
+                    if (k + 1 < t.chunks) {
+                        chunk_at(t, rev, k + 1, t0, len);
+                        load_decays(p, t0, len, t.h, lane, e);
+                    }
+                    // the last update of the state, the last read of its copy and of the decayed
+                    // W's buffer are complete
+                    if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
+                                  !wait(&bar.qs, (g - 1) & 1, p.err, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    uint8_t* sr = sm + kSS + row * 128;
+#pragma unroll 1
+                    for (int b = 0; b < 2; ++b) {
+                        float S[16];
+                        tmem_ld16(tmem + lb + kTS + 32 * wg + 16 * b, S);
+                        landed(S);
+                        if (sv)
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) o1[x] = fmaf(rowf, o2[x], o1[x]);
-                    if (row < n) {
-                        if (dot) {
+                            for (int x = 0; x < 2; ++x) {
+                                float v[8];
+#pragma unroll
+                                for (int y = 0; y < 8; ++y) v[y] = S[8 * x + y];
+                                uint4 hi, lo;
+                                pk8_hilo(v, hi, lo);
+                                const uint32_t at = ((4 * wg + 2 * b + x) ^ (row & 7)) << 4;
+                                *reinterpret_cast<uint4*>(sr + at) = hi;
+                                *reinterpret_cast<uint4*>(sr + 16384 + at) = lo;
+                            }
+                        uint32_t u[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(S[x] * all);
+                        tmem_st16(tmem + lb + kTS + 32 * wg + 16 * b, u);
+                    }
+                    tmem_st_wait();
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.s);
+
+                    if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
+                    uint8_t* stage = sm + st * kStage;
+                    uint8_t* wr = stage + kSW + row * 128;
+                    uint8_t* wd = sm + kSWd + row * 128;
+                    const bool dead = row >= len_now;
+#pragma unroll 2
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t at = ((4 * wg + x) ^ (row & 7)) << 4;
+                        uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
+                        if (!dead) {
+                            float v[8];
+                            ld8(wr + at, v);
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) v[y] *= wf;
+                            pk8_hilo(v, hi, lo);
+                        } else {
+                            // rows past the segment hold another sequence's tokens (or zeros):
+                            // they must not reach a product even as 0 * inf
+                            *reinterpret_cast<uint4*>(wr + at) = hi;
+                        }
+                        *reinterpret_cast<uint4*>(wd + at) = hi;
+                        *reinterpret_cast<uint4*>(wd + 16384 + at) = lo;
+                    }
+                    if (dead && 64 * wg < c.da) {
+                        uint4* yr = reinterpret_cast<uint4*>(stage + kSY + wg * 16384 + row * 128);
+#pragma unroll 1
+                        for (int x = 0; x < 8; ++x) yr[x] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.wd);
+                    ++g;
+                }
+                if (k > 0) {
+                    // Outputs of chunk k - 1: rowf (X S) + A W.  Where their dot products with
+                    // another row are wanted, A W comes without the diagonal's term
+                    // x_r . y_r w_r, which is added here in fp32 and left out of the dot: it is
+                    // the same number in both of the decay's gradient's sums, where under strong
+                    // decays everything else is far below its rounding.
+                    const uint32_t gg = k < t.chunks ? g - 2 : g - 1;
+                    if (!wait(&bar.o_full, gg & 1, p.err, abort)) { ok = false; break; }
+                    tc_fence_after();
+                    const int tr = t0_prev + row;
+                    const int off = t.h * c.db + 64 * t.half + 32 * wg;
+                    const bool in = row < len_prev;
+                    uint8_t* out = static_cast<uint8_t*>(c.out) +
+                                   ((int64_t)tr * p.H * c.db + off) * 2;
+                    float acc = 0.f;
+#pragma unroll 1
+                    for (int b = 0; b < 2; ++b) {
+                        float o1[16], o2[16];
+                        tmem_ld16(tmem + lb + kTO1 + 32 * wg + 16 * b, o1);
+                        tmem_ld16(tmem + lb + kTO2 + 64 * (gg & 1) + 32 * wg + 16 * b, o2);
+                        landed(o1);
+                        landed(o2);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) o1[x] = fmaf(rowf_prev, o2[x], o1[x]);
+                        if (in && c.dot) {
+                            const uint8_t* dr = static_cast<const uint8_t*>(c.dot) +
+                                                ((int64_t)tr * c.dot_ld + off) * 2 + 32 * b;
+                            const uint8_t* wr = static_cast<const uint8_t*>(c.w) +
+                                                ((int64_t)tr * c.w_ld + off) * 2 + 32 * b;
+                            const float dg =
+                                reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg % 3) + row];
 #pragma unroll
                             for (int h8 = 0; h8 < 2; ++h8) {
                                 float d[8], w[8];
-                                ld8(reinterpret_cast<const uint8_t*>(dot) + 32 * b + 16 * h8, d);
-                                ld8(reinterpret_cast<const uint8_t*>(wrow) + 32 * b + 16 * h8, w);
+                                ld8(dr + 16 * h8, d);
+                                ld8(wr + 16 * h8, w);
 #pragma unroll
                                 for (int x = 0; x < 8; ++x) {
                                     acc = fmaf(o1[8 * h8 + x], d[x], acc);
@@ -580,115 +674,36 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                                 }
                             }
                         }
-                        uint4 u[2];
-                        u[0] = make_uint4(pack_bf16x2(o1[0], o1[1]), pack_bf16x2(o1[2], o1[3]),
-                                          pack_bf16x2(o1[4], o1[5]), pack_bf16x2(o1[6], o1[7]));
-                        u[1] = make_uint4(pack_bf16x2(o1[8], o1[9]), pack_bf16x2(o1[10], o1[11]),
-                                          pack_bf16x2(o1[12], o1[13]), pack_bf16x2(o1[14], o1[15]));
-                        if (o.wide_store) {
-                            st_global_32(out + 16 * b, u[0], u[1]);
-                        } else {
-                            reinterpret_cast<uint4*>(out)[2 * b] = u[0];
-                            reinterpret_cast<uint4*>(out)[2 * b + 1] = u[1];
+                        if (in) {
+                            uint4 u[2];
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                u[x] = make_uint4(pack_bf16x2(o1[8 * x], o1[8 * x + 1]),
+                                                  pack_bf16x2(o1[8 * x + 2], o1[8 * x + 3]),
+                                                  pack_bf16x2(o1[8 * x + 4], o1[8 * x + 5]),
+                                                  pack_bf16x2(o1[8 * x + 6], o1[8 * x + 7]));
+                            if (o.wide_store) {
+                                st_global_32(out + 32 * b, u[0], u[1]);
+                            } else {
+                                reinterpret_cast<uint4*>(out)[2 * b] = u[0];
+                                reinterpret_cast<uint4*>(out)[2 * b + 1] = u[1];
+                            }
                         }
                     }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.o_free);
+                    if (in && c.dot)
+                        c.dots[((int64_t)(2 * t.half + wg) * p.T + tr) * p.H + t.h] = acc;
                 }
-                if (dot && row < n)
-                    c.dots[((int64_t)(2 * t.half + wg) * p.T + tt + row) * p.H + t.h] = acc;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.o_free);
-                return true;
-            };
-
-            for (int k = 0; k < t.chunks; ++k, ++g) {
-                const uint32_t st = g & 1;
-                const Sums s = sums<false>(e, q, lane);
-                const float head = s.P + before(s, q), tail = s.U + after(s, q);
-                const float rowf = ex2f(rev ? tail : head);
-                const float wf = row < len ? ex2f(rev ? head : tail) : 0.f;
-                const float all = ex2f((s.B[0] + s.B[1]) + (s.B[2] + s.B[3]));
-                const int t0_now = t0;
-                const int len_now = len;
-                if (k + 1 < t.chunks) {
-                    chunk_at(t, rev, k + 1, t0, len);
-                    load_decays(p, t0, len, t.h, lane, e);
-                }
-                // the last update of the state and of the decayed W's buffer is complete
-                if (g > 0 && !wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
-                tc_fence_after();
-                if (k > 0) {
-                    tmem_ld32(tmem + lb + kTS + 32 * wg, S);
-                    landed(S);
-                }
-                if (g > 0 && !wait(&bar.qs, (g - 1) & 1, p.err, abort)) { ok = false; break; }
-                if (sv) {
-                    uint8_t* r = sm + kSS + row * 128;
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        float v[8];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) v[y] = S[8 * x + y];
-                        uint4 hi, lo;
-                        pk8_hilo(v, hi, lo);
-                        const uint32_t at = ((4 * wg + x) ^ (row & 7)) << 4;
-                        *reinterpret_cast<uint4*>(r + at) = hi;
-                        *reinterpret_cast<uint4*>(r + 16384 + at) = lo;
-                    }
-                }
-                {
-                    uint32_t u[32];
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(S[x] * all);
-                    tmem_st32(tmem + lb + kTS + 32 * wg, u);
-                    tmem_st_wait();
-                }
-                fence_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.s);
-
-                if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
-                uint8_t* stage = sm + st * kStage;
-                uint8_t* wr = stage + kSW + row * 128;
-                uint8_t* wd = sm + kSWd + row * 128;
-                const bool dead = row >= len_now;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const uint32_t at = ((4 * wg + x) ^ (row & 7)) << 4;
-                    uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-                    if (!dead) {
-                        float v[8];
-                        ld8(wr + at, v);
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) v[y] *= wf;
-                        pk8_hilo(v, hi, lo);
-                    } else {
-                        // rows past the segment hold another sequence's tokens (or zeros): they
-                        // must not reach a product even as 0 * inf
-                        *reinterpret_cast<uint4*>(wr + at) = hi;
-                    }
-                    *reinterpret_cast<uint4*>(wd + at) = hi;
-                    *reinterpret_cast<uint4*>(wd + 16384 + at) = lo;
-                }
-                if (dead && 64 * wg < c.da) {
-                    uint4* yr = reinterpret_cast<uint4*>(stage + kSY + wg * 16384 + row * 128);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) yr[x] = make_uint4(0u, 0u, 0u, 0u);
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.wd);
-
-                if (k > 0 && !write_out(g - 1, t0_prev, len_prev, rowf_prev)) { ok = false; break; }
                 t0_prev = t0_now;
                 len_prev = len_now;
                 rowf_prev = rowf;
             }
             if (!ok) break;
-            if (!write_out(g - 1, t0_prev, len_prev, rowf_prev)) { ok = false; break; }
             const bool last = rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1;
             if (last && c.S_out) {  // (the chunk's outputs are complete, so its update is too)
+                float S[32];
                 tmem_ld32(tmem + lb + kTS + 32 * wg, S);
                 landed(S);
                 if (sv)
@@ -702,8 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     if (bar.abort) {
         // let copies and MMAs still in flight land before leaving
         if (warp == 12)
-            for (int st = 0; st < 2; ++st)
-                if (loaded[st] >= 0) mbar_wait(&bar.full[st], loaded[st], nullptr);
+            for (int x = max(loads - 2, 0); x < loads; ++x)
+                mbar_wait(&bar.full[x & 1], (x >> 1) & 1, nullptr);
         if (tid == 13 * 32) {
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, nullptr);
@@ -764,7 +779,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         const int rev = o.calls.c[t.call].reverse;
         return !t.live || (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1);
     };
-    int loaded[2] = {-1, -1};
+    int loads = 0;
 
     if (warp == 0) {
         uint32_t g = 0;
@@ -792,7 +807,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                         tma_load_3d(s + kUW + b * 16384, &o.w[t.call], 64 * b, t.h, t0,
                                     &bar.full[st]);
                 }
-                loaded[st] = (int)((g >> 1) & 1);
+                loads = (int)g + 1;
             }
         }
     } else if (warp == 1) {
@@ -909,8 +924,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
     __syncthreads();
     if (bar.abort) {
         if (warp == 0)
-            for (int st = 0; st < 2; ++st)
-                if (loaded[st] >= 0) mbar_wait(&bar.full[st], loaded[st], nullptr);
+            for (int x = max(loads - 2, 0); x < loads; ++x)
+                mbar_wait(&bar.full[x & 1], (x >> 1) & 1, nullptr);
         if (tid == 32) {
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, nullptr);
