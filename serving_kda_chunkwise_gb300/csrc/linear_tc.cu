@@ -70,6 +70,42 @@ __device__ __forceinline__ void landed(float (&v)[32]) {
     asm volatile("" : "+f"(v[30]), "+f"(v[31]) : : "memory");
 }
 
+// ---------------------------------------------------------------- MMAs --
+// Issued by the one lane with `lead` set out of warp-uniform code: loop control and descriptors
+// then stay in uniform registers (from a branch on the lane every operand of every MMA is moved
+// there first, which held the issue to one MMA in 150 cycles).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
+                                       uint32_t accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
+                                       uint32_t accumulate, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"(accumulate), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(lead)
+        : "memory");
+}
+// The same value in every lane, known as such to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // ---------------------------------------------------------------- decays --
 // Log decays of the chunk's tokens 32 b + lane, b = 0..3, as they are in memory (loaded a chunk
 // ahead); tokens past the segment do not decay.
@@ -307,28 +343,30 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         const uint64_t dYk = sdesc_sw128(sbase + kSY, 0, 1024);
         const uint64_t dYm = sdesc_sw128(sbase + kSY, 16384, 1024);
         const uint64_t dW = sdesc_sw128(sbase + kSW, 0, 1024);
+        const uint32_t lead = lane == 0;
+        const uint32_t tm = uniform(tmem);
         // chunks ahead of the current one: where the walk of X Y^T stands
         int64_t next_i = blockIdx.x;
-        int next_left = 0, next_da = 0;
+        uint32_t next_left = 0, next_blocks = 0;
         uint32_t gn = 0;
         auto issue_sc = [&]() -> bool {  // X Y^T of chunk gn, if there is one
             while (next_left == 0) {
                 if (next_i >= items) return true;
                 const Item t = item_at(o, next_i);
                 next_i += gridDim.x;
-                next_left = t.chunks;
-                next_da = o.calls.c[t.call].da;
+                next_left = uniform(t.chunks);
+                next_blocks = uniform(o.calls.c[t.call].da / 64);
             }
             const uint32_t st = gn & 1;
             if (!wait(&bar.full[st], (gn >> 1) & 1, p.err, abort)) return false;
             tc_fence_after();
-            if (lane == 0) {
-                for (int ks = 0; ks < next_da / 16; ++ks) {
-                    const uint32_t off = (st * kStage + (ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                    mma_bf16(tmem + kTA + 128 * st, dX + off, dYk + off, id_sc, ks > 0);
-                }
-                mma_commit(&bar.sc[st]);
-            }
+            uint64_t x = dX + (st * kStage >> 4), y = dYk + (st * kStage >> 4);
+            for (uint32_t b = 0; b < next_blocks; ++b, x += 16384 >> 4, y += 16384 >> 4)
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    mma_ss(tm + kTA + 128 * st, x + (ks * 32 >> 4), y + (ks * 32 >> 4), id_sc,
+                           b > 0 || ks > 0, lead);
+            commit(&bar.sc[st], lead);
             --next_left;
             ++gn;
             return true;
@@ -337,46 +375,47 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         bool ok = issue_sc();
         for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item t = item_at(o, i);
-            const int da = o.calls.c[t.call].da;
-            for (int k = 0; k < t.chunks; ++k, ++g) {
+            const uint32_t blocks = uniform(o.calls.c[t.call].da / 64);
+            const uint32_t chunks = uniform(t.chunks);
+            for (uint32_t k = 0; k < chunks; ++k, ++g) {
                 const uint32_t st = g & 1, ph = (g >> 1) & 1;
-                ok = wait(&bar.s, g & 1, p.err, abort) &&
-                     wait(&bar.wd, g & 1, p.err, abort);
+                const uint32_t stage = st * kStage >> 4;
+                ok = wait(&bar.s, g & 1, p.err, abort) && wait(&bar.wd, g & 1, p.err, abort);
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    // S += Y^T Wd: 128 tokens in 8 steps, hi then lo (da = 64: the second 64
-                    // lanes take whatever the block's second half holds and are never read)
-                    for (int ks = 0; ks < 16; ++ks)
-                        mma_bf16(tmem + kTS, dYm + ((st * kStage + (ks & 7) * 2048) >> 4),
-                                 dWd + (((ks >> 3) * 16384 + (ks & 7) * 2048) >> 4), id_up, 1);
-                    mma_commit(&bar.upd);
-                    // X S
-                    for (int ks = 0; ks < da / 8; ++ks) {
-                        const int half = ks >= da / 16, kk = ks - half * (da / 16);
-                        mma_bf16(tmem + kTO2 + 64 * st,
-                                 dX + ((st * kStage + (kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                                 dS + ((half * 16384 + kk * 2048) >> 4), id_aw, ks > 0);
-                    }
-                    mma_commit(&bar.qs);
-                }
-                __syncwarp();
+                // S += Y^T Wd: 128 tokens in 8 steps, hi and lo (da = 64: the second 64 lanes
+                // take whatever the block's second half holds and are never read)
+#pragma unroll 4
+                for (uint32_t ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (uint32_t part = 0; part < 2; ++part)
+                        mma_ss(tm + kTS, dYm + stage + (ks * 2048 >> 4),
+                               dWd + ((part * 16384 + ks * 2048) >> 4), id_up, 1, lead);
+                commit(&bar.upd, lead);
+                // X S
+                for (uint32_t b = 0; b < blocks; ++b)
+#pragma unroll
+                    for (uint32_t ks = 0; ks < 4; ++ks)
+#pragma unroll
+                        for (uint32_t part = 0; part < 2; ++part)
+                            mma_ss(tm + kTO2 + 64 * st, dX + stage + ((b * 16384 + ks * 32) >> 4),
+                                   dS + ((part * 16384 + (4 * b + ks) * 2048) >> 4), id_aw,
+                                   b + ks + part > 0, lead);
+                commit(&bar.qs, lead);
                 if (!(ok = issue_sc())) break;
                 ok = wait(&bar.a[st], ph, p.err, abort) &&
                      (g == 0 || wait(&bar.o_free, (g - 1) & 1, p.err, abort));
                 if (!ok) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    // A W: A's 16-token steps are 8 columns of hi and 8 of lo
-                    for (int ks = 0; ks < 16; ++ks) {
-                        const int kk = ks & 7;
-                        mma_bf16_ts(tmem + kTO1, tmem + kTA + 128 * st + 16 * kk + 8 * (ks >> 3),
-                                    dW + ((st * kStage + kk * 2048) >> 4), id_aw, ks > 0);
-                    }
-                    mma_commit(&bar.o_full);
-                    mma_commit(&bar.done[st]);
-                }
-                __syncwarp();
+                // A W: A's 16-token steps are 8 columns of hi and 8 of lo
+#pragma unroll 4
+                for (uint32_t ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (uint32_t part = 0; part < 2; ++part)
+                        mma_ts(tm + kTO1, tm + kTA + 128 * st + 16 * ks + 8 * part,
+                               dW + stage + (ks * 2048 >> 4), id_aw, ks + part > 0, lead);
+                commit(&bar.o_full, lead);
+                commit(&bar.done[st], lead);
             }
         }
     } else if (warp < 4) {
@@ -811,29 +850,32 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             }
         }
     } else if (warp == 1) {
+        const uint32_t lead = lane == 0;
+        const uint32_t tm = uniform(tmem);
+        const uint64_t dY = sdesc_sw128(sbase + kUY, 16384, 1024);
+        const uint64_t dHi = sdesc_sw128(sbase + kUW, 16384, 1024);
+        const uint64_t dLo = sdesc_sw128(sbase + kULo, 16384, 1024);
         uint32_t g = 0;
         bool ok = true;
         for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item t = item_at(o, i);
             if (skip(t)) continue;
             const Call& c = o.calls.c[t.call];
-            const uint32_t id = idesc_bf16(128, 64, true, true) +
-                                (c.db == 128 ? (64u >> 3) << 17 : 0u);  // N = db
-            for (int k = 0; k < t.chunks; ++k, ++g) {
+            const uint32_t id = uniform(idesc_bf16(128, 64, true, true) +
+                                        (c.db == 128 ? (64u >> 3) << 17 : 0u));  // N = db
+            const uint32_t chunks = uniform(t.chunks);
+            for (uint32_t k = 0; k < chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
                 if (!wait(&bar.wd[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t s = sbase + st * kUStage;
-                    const uint64_t dy = sdesc_sw128(s + kUY, 16384, 1024);
-                    const uint64_t dh = sdesc_sw128(s + kUW, 16384, 1024);
-                    const uint64_t dl = sdesc_sw128(s + kULo, 16384, 1024);
-                    for (int ks = 0; ks < 16; ++ks)
-                        mma_bf16(tmem, dy + ((ks & 7) * 2048 >> 4),
-                                 (ks < 8 ? dh : dl) + ((ks & 7) * 2048 >> 4), id, k > 0 || ks > 0);
-                    mma_commit(&bar.done[st]);
+                const uint32_t stage = st * kUStage >> 4;
+#pragma unroll 4
+                for (uint32_t ks = 0; ks < 8; ++ks) {
+                    const uint32_t at = stage + (ks * 2048 >> 4);
+                    mma_ss(tm, dY + at, dHi + at, id, k + ks > 0, lead);
+                    mma_ss(tm, dY + at, dLo + at, id, 1, lead);
                 }
-                __syncwarp();
+                commit(&bar.done[st], lead);
             }
         }
     } else if (warp >= 4) {
