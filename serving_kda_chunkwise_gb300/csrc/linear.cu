@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
     const Call& c = calls.c[blockIdx.z / blocks_per_call];
     const int cb = blockIdx.z % blocks_per_call;
     if (c.da != DA || cb * kCols >= c.db) return;
-    const Segment sg = lin::find_segment(p, blockIdx.x);
+    const Segment sg = lin::find_segment(p, (int)blockIdx.x);
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = cb * kCols + lane, row0 = warp * R;
     const int64_t E = (int64_t)c.da * c.db;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
                                                          const __grid_constant__ DecayGrad d) {
     __shared__ float red[2][8];
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Segment sg = lin::find_segment(p, blockIdx.x);
+    const Segment sg = lin::find_segment(p, (int)blockIdx.x);
     if (!sg.live) return;
     const int64_t seq = ((int64_t)sg.n * p.H + h) * d.E;
     const int64_t own = ((int64_t)blockIdx.x * p.H + h) * d.E, step = (int64_t)p.H * d.E;
@@ -332,7 +332,7 @@ struct Layout {
     int L;
     int64_t slots;
     bool segments;  // some sequence may be longer than a segment
-    size_t add[2], seg[2], dec, S_T, dS0, dots_q, dots_k, dg, bytes;
+    size_t rec, add[2], seg[2], dec, S_T, dS0, dots_q, dots_k, dg, bytes;
 };
 
 Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool equal) {
@@ -347,6 +347,7 @@ Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool e
         at += align256(n);
         return r;
     };
+    l.rec = take(tc ? lintc::record_bytes(l.slots, l.L, H) : 0);
     for (int i = 0; i < (bwd ? 2 : 1); ++i) {
         l.add[i] = take(l.segments ? (size_t)l.slots * state : 0);
         l.seg[i] = take(l.segments ? (size_t)l.slots * state : 0);
@@ -384,10 +385,12 @@ void launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, fl
 
 template <bool kOut>
 cudaError_t launch_calls(const LinearArgs& a, const Problem& p, const Calls& calls, int n,
-                         int64_t slots, float* dec, const char* name) {
+                         const Layout& l, float* dec, const char* name) {
+    const int64_t slots = l.slots;
+    const float* rec = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + l.rec);
     if (use_tc(a.io_bf16))
-        return kOut ? lintc::launch_outputs(p, calls, n, slots, name, a.stream)
-                    : lintc::launch_sums(p, calls, n, slots, dec, name, a.stream);
+        return kOut ? lintc::launch_outputs(p, calls, n, slots, rec, name, a.stream)
+                    : lintc::launch_sums(p, calls, n, slots, rec, dec, name, a.stream);
     if (a.io_bf16)
         launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream);
     else
@@ -413,7 +416,7 @@ cudaError_t launch_segments(const LinearArgs& a, const Problem& p, const Layout&
         e.dec[i] = dec + (size_t)i * l.slots * a.H;
     }
     e.E = a.dk * a.dv;
-    if (cudaError_t err = launch_calls<false>(a, p, calls, bwd ? 2 : 1, l.slots, dec,
+    if (cudaError_t err = launch_calls<false>(a, p, calls, bwd ? 2 : 1, l, dec,
                                               "linear_segment_kernel"))
         return err;
     ProfScope prof("linear_edge_kernel", a.stream);
@@ -436,6 +439,10 @@ cudaError_t launch_linear_fwd(const LinearArgs& a) {
                             a.cu_seqlens == nullptr);
     const Problem p = problem(a, l.L);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    if (use_tc(a.io_bf16))
+        if (cudaError_t e = lintc::launch_decays(
+                p, l.slots, reinterpret_cast<float*>(ws + l.rec), a.stream))
+            return e;
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, false)) return e;
     Calls calls{};
@@ -443,7 +450,7 @@ cudaError_t launch_linear_fwd(const LinearArgs& a) {
     c.x = a.q; c.x_ld = a.q_ld; c.y = a.k; c.y_ld = a.k_ld; c.w = a.v; c.w_ld = a.v_ld;
     c.da = a.dk; c.db = a.dv; c.edge = a.S0; c.S_out = a.S_out; c.out = a.o;
     c.seg = reinterpret_cast<float*>(ws + l.seg[0]);
-    return launch_calls<true>(a, p, calls, 1, l.slots, nullptr, "linear_out_kernel");
+    return launch_calls<true>(a, p, calls, 1, l, nullptr, "linear_out_kernel");
 }
 
 cudaError_t launch_linear_bwd(const LinearArgs& a) {
@@ -452,6 +459,10 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
     const Problem p = problem(a, l.L);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+    if (use_tc(a.io_bf16))
+        if (cudaError_t e = lintc::launch_decays(
+                p, l.slots, reinterpret_cast<float*>(ws + l.rec), a.stream))
+            return e;
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, true)) return e;
     const bool anchor = a.dg && a.dS_out;
@@ -469,13 +480,13 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
     v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = at(l.seg[1]);
     v.S_out = a.dS0 ? a.dS0 : a.dg && a.S0 ? at(l.dS0) : nullptr; v.out = a.dv_;
     if (cudaError_t e =
-            launch_calls<true>(a, p, calls, 3, l.slots, nullptr, "linear_grad_kernel"))
+            launch_calls<true>(a, p, calls, 3, l, nullptr, "linear_grad_kernel"))
         return e;
     if (a.dg) {
         DecayGrad d{};
         d.segS = at(l.seg[0]); d.segD = at(l.seg[1]);
         d.S_T = at(l.S_T); d.dS_out = a.dS_out; d.S0 = a.S0; d.dS0 = v.S_out;
-        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kCols;
+        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / (use_tc(a.io_bf16) ? 64 : kCols);
         d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
         if (a.T_total > 0) {
             ProfScope prof("linear_decay_grad_kernel", a.stream);

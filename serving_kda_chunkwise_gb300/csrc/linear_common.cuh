@@ -61,33 +61,44 @@ struct Segment {
     bool live;
 };
 
-__device__ __forceinline__ int64_t seq_start(const Problem& p, int n) {
-    return p.cu ? (int64_t)__ldg(p.cu + n) : (int64_t)n * (p.T / p.N);
+__device__ __forceinline__ uint32_t seq_start(const Problem& p, int n) {
+    return p.cu ? (uint32_t)__ldg(p.cu + n) : (uint32_t)n * ((uint32_t)p.T / (uint32_t)p.N);
 }
 
-// Called by whole warps: the segment in slot j.
-__device__ __forceinline__ Segment find_segment(const Problem& p, int64_t j) {
+// The segment in slot j.  kWarp: called by whole warps, whose lanes search together; else by one
+// thread on its own.
+template <bool kWarp = true>
+__device__ __forceinline__ Segment find_segment(const Problem& p, int j) {
     const int lane = threadIdx.x & 31;
+    const uint32_t L = p.L;
     int lo = 0, hi = p.N;  // the sequence is in [lo, hi)
-    while (hi - lo > 1) {
+    while (!kWarp && hi - lo > 1) {
+        const int n = (lo + hi) / 2;
+        if (seq_start(p, n) / L + (uint32_t)n <= (uint32_t)j) lo = n;
+        else hi = n;
+    }
+    while (kWarp && hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int n = lo + (lane + 1) * step;
-        const bool at = n < hi && seq_start(p, n) / p.L + n <= j;
+        const bool at = n < hi && seq_start(p, n) / L + (uint32_t)n <= (uint32_t)j;
         const unsigned mask = __ballot_sync(0xffffffffu, at);
         const int c = mask == 0xffffffffu ? 32 : __ffs(~mask) - 1;
         lo += c * step;
         hi = min(hi, lo + step);
     }
+    // (as seq_range(), in 32 bits; a malformed range reads as empty)
+    const uint32_t a = seq_start(p, lo);
+    const uint32_t b = p.cu ? seq_start(p, lo + 1) : a + (uint32_t)p.T / (uint32_t)p.N;
+    const uint32_t T = (uint32_t)p.T;
+    const bool bad = p.cu && ((int)a < 0 || b < a || b > T || (lo == 0 && a != 0) ||
+                              (lo == p.N - 1 && b != T));
     Segment r;
     r.n = lo;
-    int64_t a, b;
-    seq_range(p.cu, lo, p.N, p.T, p.err, a, b);
-    r.count = (int)((b - a + p.L - 1) / p.L);
-    const int64_t s = j - ((p.cu ? a : seq_start(p, lo)) / p.L + lo);
-    r.live = s >= 0 && s < r.count;
-    r.s = (int)s;
-    r.begin = (int)(a + s * p.L);
-    r.end = (int)(a + (s + 1) * p.L < b ? a + (s + 1) * p.L : b);
+    r.count = bad ? 0 : (int)((b - a + L - 1) / L);
+    r.s = j - (int)((bad ? 0u : a) / L) - lo;
+    r.live = r.s >= 0 && r.s < r.count;
+    r.begin = (int)(a + (uint32_t)r.s * L);
+    r.end = (int)min((uint32_t)r.begin + L, b);
     return r;
 }
 

@@ -48,6 +48,11 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, unsigned* e
     if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(bar), parity))) return true;
     return wait_poll(bar, parity, err, abort);
 }
+// The same by one thread.
+__device__ __noinline__ bool wait1(uint64_t* bar, uint32_t parity, unsigned* err,
+                                   volatile int* abort) {
+    return mbar_wait_ab(bar, parity, err, abort);
+}
 
 // The registers of earlier TMEM loads are ready (tied to the wait, so that no use moves above it).
 __device__ __forceinline__ void landed(float (&v)[16]) {
@@ -70,200 +75,215 @@ __device__ __forceinline__ void landed(float (&v)[32]) {
     asm volatile("" : "+f"(v[30]), "+f"(v[31]) : : "memory");
 }
 
-// ---------------------------------------------------------------- MMAs --
-// Issued by the one lane with `lead` set out of warp-uniform code: loop control and descriptors
-// then stay in uniform registers (from a branch on the lane every operand of every MMA is moved
-// there first, which held the issue to one MMA in 150 cycles).
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id,
-                                       uint32_t accumulate, uint32_t lead) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(id), "r"(accumulate), "r"(lead)
-        : "memory");
+// ---------------------------------------------------------- descriptors --
+// Operand descriptors (128-byte swizzle, 1024 bytes between 8-row groups) as a constant upper
+// word and a lower word that steps by constants.
+__device__ __forceinline__ uint32_t dlow(uint32_t saddr, uint32_t lbo) {
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id,
-                                       uint32_t accumulate, uint32_t lead) {
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"(accumulate), "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "setp.ne.b32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
-            smem_u32(bar)),
-        "r"(lead)
-        : "memory");
-}
-// The same value in every lane, known as such to the compiler.
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-// ---------------------------------------------------------------- decays --
-// Log decays of the chunk's tokens 32 b + lane, b = 0..3, as they are in memory (loaded a chunk
-// ahead); tokens past the segment do not decay.
-__device__ __forceinline__ void load_decays(const Problem& p, int t0, int len, int h, int lane,
-                                            float (&e)[4]) {
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const int i = 32 * b + lane;
-        e[b] = i < len ? lin::log_decay(p, t0 + i, h) : 0.f;
-    }
+__device__ __forceinline__ uint64_t desc(uint32_t low) {
+    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return (static_cast<uint64_t>(kHigh) << 32) | low;
 }
 
-__device__ __forceinline__ float pick(const float (&x)[4], int q) {
-    return q == 0 ? x[0] : q == 1 ? x[1] : q == 2 ? x[2] : x[3];
+// ------------------------------------------------- pairs of fp32 numbers --
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1));
 }
-
-struct Sums {
-    float B[4];  // block sums
-    float P, U;  // of this lane's token of block q: inclusive prefix, exclusive suffix
-    float Plo;   // P's rounding error (filled by sums<true>)
-};
-
-template <bool kTwo>
-__device__ __forceinline__ Sums sums(const float (&g)[4], int q, int lane) {
-    Sums r;
-    float e[4];  // log2 decays
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const float x = g[b] * kLog2e;
-        e[b] = x < -2000.f ? -2000.f : x;
-    }
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        float x = e[b];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        r.B[b] = x;
-    }
-    const float own = pick(e, q);
-    float x = own, lo = 0.f;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const float y = __shfl_up_sync(0xffffffffu, x, off);
-        if (kTwo) {  // (x, lo) += (y, ylo), the rounding of x + y kept in lo
-            const float ylo = __shfl_up_sync(0xffffffffu, lo, off);
-            if (lane >= off) {
-                const float s = __fadd_rn(x, y), d = __fsub_rn(s, x);
-                const float err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, d)), __fsub_rn(y, d));
-                x = s;
-                lo = __fadd_rn(__fadd_rn(lo, ylo), err);
-            }
-        } else if (lane >= off) {
-            x += y;
-        }
-    }
-    r.P = x;
-    r.Plo = lo;
-    float u = __shfl_down_sync(0xffffffffu, own, 1);
-    if (lane == 31) u = 0.f;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, u, off);
-        if (lane + off < 32) u += y;
-    }
-    r.U = u;
-    return r;
-}
-
-// Sum of the blocks before (after) block q, nearest first.
-__device__ __forceinline__ float before(const Sums& s, int q) {
-    float x = 0.f;
-#pragma unroll
-    for (int b = 2; b >= 0; --b) x += b < q ? s.B[b] : 0.f;
-    return x;
-}
-__device__ __forceinline__ float after(const Sums& s, int q) {
-    float x = 0.f;
-#pragma unroll
-    for (int b = 1; b < 4; ++b) x += b > q ? s.B[b] : 0.f;
-    return x;
+// bf16 hi of (a0, a1) and of what hi leaves of them
+__device__ __forceinline__ void split2(float a0, float a1, uint32_t& hi, uint32_t& lo) {
+    hi = pack_bf16x2(a0, a1);
+    float l0, l1;
+    asm("{\n\t.reg .b64 a, h, m;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 h, {%4, %5};\n\t"
+        "mov.b64 m, {%6, %6};\n\tfma.rn.f32x2 a, h, m, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(l0), "=f"(l1)
+        : "f"(a0), "f"(a1), "f"(__uint_as_float(hi << 16)),
+          "f"(__uint_as_float(hi & 0xffff0000u)), "f"(-1.f));
+    lo = pack_bf16x2(l0, l1);
 }
 
 // ------------------------------------------------------------- work items --
-// Items: slots x heads x calls x halves of the call's db columns (64 each), the halves and the
-// calls of one (slot, head) next to each other so that they share the rows through L2.
+// Items: slots x heads x calls, the calls of one (slot, head) next to each other so that they
+// share the rows through L2.
 struct Item {
     Segment sg;
-    int slot;
-    int call, h, half, chunks;
-    bool live;
+    int slot, call, h, chunks;
 };
 
 struct OutParams {
     Problem p;
     lin::Calls calls;
     CUtensorMap x[lin::kMaxCalls], y[lin::kMaxCalls], w[lin::kMaxCalls];
-    int n_calls, halves;
-    int64_t slots;
-    int wide_store;  // every output row piece is 32-byte aligned
+    int n_calls;
+    int slots;
+    const float* rec;  // decay records, see decay_kernel
+    int wide_store;    // every output row piece is 32-byte aligned
 };
 
-__device__ __forceinline__ int64_t item_count(const OutParams& o) {
-    return o.slots * o.p.H * o.n_calls * o.halves;
+__device__ __forceinline__ uint32_t item_count(const OutParams& o) {
+    return (uint32_t)o.slots * o.p.H * o.n_calls;
 }
 
-__device__ __forceinline__ Item item_at(const OutParams& o, int64_t i) {
+// Out of line: once an item and in every role.  kWarp: called by whole warps; else by one thread.
+template <bool kWarp>
+__device__ __noinline__ Item item_at(const OutParams& o, uint32_t i) {
     Item t;
-    t.half = (int)(i % o.halves);
-    i /= o.halves;
     t.call = (int)(i % o.n_calls);
     i /= o.n_calls;
     t.h = (int)(i % o.p.H);
     t.slot = (int)(i / o.p.H);
-    t.sg = lin::find_segment(o.p, t.slot);
-    t.live = t.sg.live && t.half * 64 < o.calls.c[t.call].db;
-    t.chunks = t.live ? (int)((t.sg.end - t.sg.begin + kC - 1) / kC) : 0;
+    t.sg = lin::find_segment<kWarp>(o.p, t.slot);
+    t.chunks = t.sg.live ? (t.sg.end - t.sg.begin + kC - 1) / kC : 0;
     return t;
 }
 
-// First token and length of the c-th chunk of the walk.
-__device__ __forceinline__ void chunk_at(const Item& t, int reverse, int c, int& t0, int& len) {
-    const int i = reverse ? t.chunks - 1 - c : c;
-    t0 = t.sg.begin + i * kC;
-    len = min(t.sg.end - t0, kC);
+// The c-th chunk of the walk: its place in the segment, first token and length.
+struct Chunk {
+    int i, t0, len;
+};
+__device__ __forceinline__ Chunk chunk_at(const Item& t, int reverse, int c) {
+    Chunk k;
+    k.i = reverse ? t.chunks - 1 - c : c;
+    k.t0 = t.sg.begin + k.i * kC;
+    k.len = min(t.sg.end - k.t0, kC);
+    return k;
+}
+
+// ---------------------------------------------------------------- decays --
+// What a chunk's decays are needed as, formed once for all calls and roles: a record of floats a
+// (chunk, head), arrays of 128 tokens.
+constexpr int kRP = 0, kRPlo = 128;   // prefix sum inside the block of 32 (log2), its rounding
+constexpr int kRU = 256;              // exclusive suffix sum inside the block
+constexpr int kRHead = 384;           // 2^(sum from the chunk's start, inclusive)
+constexpr int kRTail = 512;           // 2^(sum to the chunk's end, exclusive)
+constexpr int kRCol = 640;            // 2^U, then 2^P: column factors, forward and reversed
+constexpr int kRB = 896;              // the four blocks' sums, their total
+constexpr int kRec = 928;
+
+__device__ __forceinline__ const float* record(const OutParams& o, const Item& t, int chunk) {
+    return o.rec + ((size_t)(t.slot * (o.p.L / kC) + chunk) * o.p.H + t.h) * kRec;
+}
+
+// One warp a (chunk, head); a CTA's warps take neighbouring heads, whose decays share sectors.
+__global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Problem p, float* rec) {
+    const int lane = threadIdx.x & 31, per = p.L / kC;
+    const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int slot = blockIdx.x / per, chunk = blockIdx.x % per;
+    const Segment sg = lin::find_segment(p, slot);
+    const int t0 = sg.begin + chunk * kC;
+    if (h >= p.H || !sg.live || t0 >= sg.end) return;
+    float* r = rec + ((size_t)blockIdx.x * p.H + h) * kRec;
+    float e[4], P[4], Plo[4], U[4], B[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const int t = t0 + 32 * b + lane;
+        const float x = t < sg.end ? lin::log_decay(p, t, h) * kLog2e : 0.f;
+        e[b] = x < -2000.f ? -2000.f : x;  // (a NaN stays one)
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        float x = e[b], lo = 0.f;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, x, off);
+            const float ylo = __shfl_up_sync(0xffffffffu, lo, off);
+            if (lane >= off) {  // (x, lo) += (y, ylo), the rounding of x + y kept in lo
+                const float s = __fadd_rn(x, y), d = __fsub_rn(s, x);
+                const float err = __fadd_rn(__fsub_rn(x, __fsub_rn(s, d)), __fsub_rn(y, d));
+                x = s;
+                lo = __fadd_rn(__fadd_rn(lo, ylo), err);
+            }
+        }
+        P[b] = x;
+        Plo[b] = lo;
+        B[b] = __shfl_sync(0xffffffffu, x, 31);
+        float u = __shfl_down_sync(0xffffffffu, e[b], 1);
+        if (lane == 31) u = 0.f;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const float y = __shfl_down_sync(0xffffffffu, u, off);
+            if (lane + off < 32) u += y;
+        }
+        U[b] = u;
+    }
+    const float before[4] = {0.f, B[0], B[0] + B[1], B[0] + B[1] + B[2]};
+    const float after[4] = {B[1] + B[2] + B[3], B[2] + B[3], B[3], 0.f};
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const int i = 32 * b + lane;
+        r[kRP + i] = P[b];
+        r[kRPlo + i] = Plo[b];
+        r[kRU + i] = U[b];
+        r[kRHead + i] = ex2f(P[b] + before[b]);
+        r[kRTail + i] = ex2f(U[b] + after[b]);
+        r[kRCol + i] = ex2f(U[b]);
+        r[kRCol + 128 + i] = ex2f(P[b]);
+    }
+    if (lane == 0) {
+        *reinterpret_cast<float4*>(r + kRB) = make_float4(B[0], B[1], B[2], B[3]);
+        r[kRB + 4] = (B[0] + B[1]) + (B[2] + B[3]);
+    }
 }
 
 // -------------------------------------------------------------- outputs --
 // Persistent, one CTA an SM.  Roles: warps 0..3 turn X Y^T into A (hi + lo over the product's own
-// TMEM columns, so that A never leaves tensor memory), warp 12 issues the TMA loads (two stages),
-// warp 13 the MMAs, and warps 4..11 decay W, convert the state and write the outputs.  Warp w
-// reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in fp32; X S reads its bf16
-// hi + lo copy in shared memory.
-// A CTA takes 64 of the db columns: two full stages of X, Y and W then fit beside the decayed W
-// and the state, at the price of forming A twice for db = 128.
-constexpr int kThreads = 448;
-constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536, kStage = 81920;  // two stages
-constexpr uint32_t kSWd = 2 * kStage;       // decayed W: hi, lo (16 KB each)
-constexpr uint32_t kSS = kSWd + 32768;      // state: hi, lo (16 KB each)
-constexpr uint32_t kSCol = kSS + 32768;     // column factors, two chunks of 128 floats
-constexpr uint32_t kSDiag = kSCol + 1024;   // diagonals of X Y^T, three chunks of 128 floats
+// TMEM columns, so that A never leaves tensor memory); warps 4..11 decay W, keep the state's copy
+// and write the outputs; single threads of warps 12, 14 and 15 load X, Y and W by TMA, one of warp
+// 13 issues the MMAs.  Warp w reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in
+// fp32; X S reads its bf16 hi + lo copy in shared memory.
+// Shared memory holds one chunk of X, Y and W (32 KB each), the decayed W and the state's copy (64
+// KB each): no second stage fits, but each operand is reloaded as soon as its last product is
+// done, and while one waits the others' products run.  (Two stages fit with 64 of the db columns
+// to a CTA; that form made A twice and its N = 64 products run at 75 % of N = 128's rate, and was
+// slower.)
+constexpr int kThreads = 512;
+constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
+constexpr uint32_t kSWd = 98304;             // decayed W: hi, lo
+constexpr uint32_t kSS = kSWd + 65536;       // state: hi, lo
+constexpr uint32_t kSDiag = kSS + 65536;     // diagonals of X Y^T, three chunks of 128 floats
 constexpr uint32_t kSBar = kSDiag + 1536;
 constexpr uint32_t kOutSmem = kSBar + 256;
 static_assert(kOutSmem <= 232448, "shared-memory limit");
-// TMEM columns: X Y^T / A two buffers of 128, A W 64, X S two of 64, state 64
-constexpr uint32_t kTA = 0, kTO1 = 256, kTO2 = 320, kTS = 448;
+// TMEM columns (all 512 are allocated, so the base address is 0): X Y^T / A, A W, X S, state
+constexpr uint32_t kTA = 0, kTO1 = 128, kTO2 = 256, kTS = 384;
 
 struct OutBars {
-    uint64_t full[2], done[2];   // stage loaded; every MMA of the stage's chunk complete
-    uint64_t sc[2], a[2];        // X Y^T complete; A written (4 arrivals)
-    uint64_t col[2];             // column factors written (4 arrivals)
-    uint64_t s, wd;              // state and its copy written; decayed W written (8 arrivals each)
-    uint64_t upd, qs;            // state update complete; X S complete
-    uint64_t o_full, o_free;     // chunk's outputs complete; read (8 arrivals)
+    uint64_t x, y, w;        // operands loaded
+    uint64_t sc, a;          // X Y^T complete; A written (4 arrivals)
+    uint64_t s, wd;          // state and its copy written; decayed W written (8 arrivals each)
+    uint64_t upd, xs;        // state update complete; X S complete
+    uint64_t out, read;      // A W (so the chunk's outputs) complete; outputs read (8 arrivals)
     uint64_t drain;
     uint32_t tmem;
     int abort;
 };
 static_assert(sizeof(OutBars) <= 256, "barrier area");
+
+// One operand's loads, by one thread: chunk after chunk, each once `freed` says that the last
+// chunk's products have read the buffer.  Returns the number of loads issued.
+__device__ __noinline__ int load_operand(const OutParams& o, const CUtensorMap* maps, int which,
+                                         uint8_t* dst, uint64_t* full, uint64_t* freed,
+                                         volatile int* abort) {
+    const uint32_t items = item_count(o);
+    int g = 0;
+    for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const Item t = item_at<false>(o, i);
+        const Call& c = o.calls.c[t.call];
+        const int blocks = (which == 2 ? c.db : c.da) / 64;
+        for (int k = 0; k < t.chunks; ++k, ++g) {
+            if (g > 0 && !wait1(freed, (g - 1) & 1, o.p.err, abort)) return g;
+            const Chunk ch = chunk_at(t, c.reverse, k);
+            mbar_expect_tx(full, blocks * 16384);
+#pragma unroll 1
+            for (int b = 0; b < blocks; ++b)
+                tma_load_3d(dst + b * 16384, maps + t.call, 64 * b, t.h, ch.t0, full);
+        }
+    }
+    return g;
+}
 
 __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant__ OutParams o) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -272,22 +292,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     const Problem& p = o.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &bar.abort;
-    static_assert(kC == 128, "a chunk is the 128 lanes of a TMEM tile");
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.done[i], 1);
-            mbar_init(&bar.sc[i], 1);
-            mbar_init(&bar.a[i], 4);
-            mbar_init(&bar.col[i], 4);
-        }
+        uint64_t* one[] = {&bar.x, &bar.y, &bar.w, &bar.sc, &bar.upd, &bar.xs, &bar.out, &bar.drain};
+        for (uint64_t* b : one) mbar_init(b, 1);
+        mbar_init(&bar.a, 4);
         mbar_init(&bar.s, 8);
         mbar_init(&bar.wd, 8);
-        mbar_init(&bar.upd, 1);
-        mbar_init(&bar.qs, 1);
-        mbar_init(&bar.o_full, 1);
-        mbar_init(&bar.o_free, 8);
-        mbar_init(&bar.drain, 1);
+        mbar_init(&bar.read, 8);
         fence_mbar_init();
         bar.abort = 0;
     }
@@ -296,167 +307,106 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bar.tmem;
-    const int64_t items = item_count(o);
-    int loads = 0;  // stages loaded by the TMA warp (for the way out of an abort)
+    const uint32_t items = item_count(o);
+    int loads = 0;  // of this thread (for the way out of an abort)
+    uint64_t* load_bar = nullptr;
 
-    if (warp == 12) {
-        // --------------------------------------------------------- TMA warp
+    if (tid == 12 * 32) {
+        load_bar = &bar.x;
+        loads = load_operand(o, o.x, 0, sm + kSX, &bar.x, &bar.xs, abort);
+    } else if (tid == 14 * 32) {
+        load_bar = &bar.y;
+        loads = load_operand(o, o.y, 1, sm + kSY, &bar.y, &bar.upd, abort);
+    } else if (tid == 15 * 32) {
+        load_bar = &bar.w;
+        loads = load_operand(o, o.w, 2, sm + kSW, &bar.w, &bar.out, abort);
+    } else if (tid == 13 * 32) {
+        // ------------------------------------------------------- MMA thread
+        constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
+        const uint32_t lX = dlow(sbase + kSX, 0), lYk = dlow(sbase + kSY, 0);
+        const uint32_t lYm = dlow(sbase + kSY, 16384), lW = dlow(sbase + kSW, 16384);
+        const uint32_t lWd = dlow(sbase + kSWd, 16384), lS = dlow(sbase + kSS, 16384);
         uint32_t g = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at(o, i);
-            const Call& c = o.calls.c[t.call];
-            const int blocks = c.da / 64;
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item t = item_at<false>(o, i);
+            const int da = o.calls.c[t.call].da;
+            const uint32_t n = (uint32_t)(o.calls.c[t.call].db >> 3) << 17;  // N = db
+            const uint32_t id_out = (idesc_bf16(128, 0, false, true)) | n;   // A W, X S
+            const uint32_t id_up = (idesc_bf16(128, 0, true, true)) | n;     // Y^T W
             for (int k = 0; k < t.chunks; ++k, ++g) {
-                const uint32_t st = g & 1;
-                if (g >= 2 && !wait(&bar.done[st], ((g - 2) >> 1) & 1, p.err, abort)) {
-                    ok = false;
-                    break;
-                }
-                int t0;
-                int len;
-                chunk_at(t, c.reverse, k, t0, len);
-                if (lane == 0) {
-                    uint8_t* s = sm + st * kStage;
-                    mbar_expect_tx(&bar.full[st], blocks * 32768 + 16384);
-                    for (int b = 0; b < blocks; ++b) {
-                        tma_load_3d(s + kSX + b * 16384, &o.x[t.call], 64 * b, t.h, t0,
-                                    &bar.full[st]);
-                        tma_load_3d(s + kSY + b * 16384, &o.y[t.call], 64 * b, t.h, t0,
-                                    &bar.full[st]);
-                    }
-                    tma_load_3d(s + kSW, &o.w[t.call], 64 * t.half, t.h, t0, &bar.full[st]);
-                }
-                loads = (int)g + 1;
-            }
-        }
-    } else if (warp == 13) {
-        // --------------------------------------------------------- MMA warp
-        constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
-        constexpr uint32_t id_aw = idesc_bf16(128, 64, false, true);    // A W, X S
-        constexpr uint32_t id_up = idesc_bf16(128, 64, true, true);     // Y^T W
-        const uint64_t dWd = sdesc_sw128(sbase + kSWd, 0, 1024);
-        const uint64_t dS = sdesc_sw128(sbase + kSS, 0, 1024);
-        // of stage 0; stage 1 is kStage bytes on
-        const uint64_t dX = sdesc_sw128(sbase + kSX, 0, 1024);
-        const uint64_t dYk = sdesc_sw128(sbase + kSY, 0, 1024);
-        const uint64_t dYm = sdesc_sw128(sbase + kSY, 16384, 1024);
-        const uint64_t dW = sdesc_sw128(sbase + kSW, 0, 1024);
-        const uint32_t lead = lane == 0;
-        const uint32_t tm = uniform(tmem);
-        // chunks ahead of the current one: where the walk of X Y^T stands
-        int64_t next_i = blockIdx.x;
-        uint32_t next_left = 0, next_blocks = 0;
-        uint32_t gn = 0;
-        auto issue_sc = [&]() -> bool {  // X Y^T of chunk gn, if there is one
-            while (next_left == 0) {
-                if (next_i >= items) return true;
-                const Item t = item_at(o, next_i);
-                next_i += gridDim.x;
-                next_left = uniform(t.chunks);
-                next_blocks = uniform(o.calls.c[t.call].da / 64);
-            }
-            const uint32_t st = gn & 1;
-            if (!wait(&bar.full[st], (gn >> 1) & 1, p.err, abort)) return false;
-            tc_fence_after();
-            uint64_t x = dX + (st * kStage >> 4), y = dYk + (st * kStage >> 4);
-            for (uint32_t b = 0; b < next_blocks; ++b, x += 16384 >> 4, y += 16384 >> 4)
+                const uint32_t ph = g & 1;
+                ok = wait1(&bar.x, ph, p.err, abort) && wait1(&bar.y, ph, p.err, abort);
+                if (!ok) break;
+                tc_fence_after();
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_ss(tm + kTA + 128 * st, x + (ks * 32 >> 4), y + (ks * 32 >> 4), id_sc,
-                           b > 0 || ks > 0, lead);
-            commit(&bar.sc[st], lead);
-            --next_left;
-            ++gn;
-            return true;
-        };
-        uint32_t g = 0;
-        bool ok = issue_sc();
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at(o, i);
-            const uint32_t blocks = uniform(o.calls.c[t.call].da / 64);
-            const uint32_t chunks = uniform(t.chunks);
-            for (uint32_t k = 0; k < chunks; ++k, ++g) {
-                const uint32_t st = g & 1, ph = (g >> 1) & 1;
-                const uint32_t stage = st * kStage >> 4;
-                ok = wait(&bar.s, g & 1, p.err, abort) && wait(&bar.wd, g & 1, p.err, abort);
+                for (int ks = 0; ks < 8; ++ks) {
+                    if (ks == 4 && da == 64) break;
+                    const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                    mma_bf16(kTA, desc(lX + off), desc(lYk + off), id_sc, ks > 0);
+                }
+                mma_commit(&bar.sc);
+                ok = wait1(&bar.s, ph, p.err, abort) && wait1(&bar.wd, ph, p.err, abort);
                 if (!ok) break;
                 tc_fence_after();
                 // S += Y^T Wd: 128 tokens in 8 steps, hi and lo (da = 64: the second 64 lanes
-                // take whatever the block's second half holds and are never read)
-#pragma unroll 4
-                for (uint32_t ks = 0; ks < 8; ++ks)
+                // take whatever the buffer's second half holds and are never read)
 #pragma unroll
-                    for (uint32_t part = 0; part < 2; ++part)
-                        mma_ss(tm + kTS, dYm + stage + (ks * 2048 >> 4),
-                               dWd + ((part * 16384 + ks * 2048) >> 4), id_up, 1, lead);
-                commit(&bar.upd, lead);
+                for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                        mma_bf16(kTS, desc(lYm + (ks * 2048 >> 4)),
+                                 desc(lWd + ((part * 32768 + ks * 2048) >> 4)), id_up, 1);
+                mma_commit(&bar.upd);
+                if (g > 0 && !(ok = wait1(&bar.read, ph ^ 1, p.err, abort))) break;
+                tc_fence_after();
                 // X S
-                for (uint32_t b = 0; b < blocks; ++b)
 #pragma unroll
-                    for (uint32_t ks = 0; ks < 4; ++ks)
+                for (int ks = 0; ks < 8; ++ks) {
+                    if (ks == 4 && da == 64) break;
 #pragma unroll
-                        for (uint32_t part = 0; part < 2; ++part)
-                            mma_ss(tm + kTO2 + 64 * st, dX + stage + ((b * 16384 + ks * 32) >> 4),
-                                   dS + ((part * 16384 + (4 * b + ks) * 2048) >> 4), id_aw,
-                                   b + ks + part > 0, lead);
-                commit(&bar.qs, lead);
-                if (!(ok = issue_sc())) break;
-                ok = wait(&bar.a[st], ph, p.err, abort) &&
-                     (g == 0 || wait(&bar.o_free, (g - 1) & 1, p.err, abort));
+                    for (int part = 0; part < 2; ++part)
+                        mma_bf16(kTO2, desc(lX + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4)),
+                                 desc(lS + ((part * 32768 + ks * 2048) >> 4)), id_out,
+                                 ks + part > 0);
+                }
+                mma_commit(&bar.xs);
+                ok = wait1(&bar.a, ph, p.err, abort) && wait1(&bar.w, ph, p.err, abort);
                 if (!ok) break;
                 tc_fence_after();
                 // A W: A's 16-token steps are 8 columns of hi and 8 of lo
-#pragma unroll 4
-                for (uint32_t ks = 0; ks < 8; ++ks)
 #pragma unroll
-                    for (uint32_t part = 0; part < 2; ++part)
-                        mma_ts(tm + kTO1, tm + kTA + 128 * st + 16 * ks + 8 * part,
-                               dW + stage + (ks * 2048 >> 4), id_aw, ks + part > 0, lead);
-                commit(&bar.o_full, lead);
-                commit(&bar.done[st], lead);
+                for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+                        mma_bf16_ts(kTO1, kTA + 16 * ks + 8 * part, desc(lW + (ks * 2048 >> 4)),
+                                    id_out, ks + part > 0);
+                mma_commit(&bar.out);
             }
         }
     } else if (warp < 4) {
         // ------------------------------------------------------------ A warps
         const int q = warp;
-        const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
-        float* col = reinterpret_cast<float*>(sm + kSCol);
-        float* diag = reinterpret_cast<float*>(sm + kSDiag);
+        const uint32_t at = static_cast<uint32_t>(32 * q) << 16 | kTA;
+        float* diag = reinterpret_cast<float*>(sm + kSDiag) + 32 * q + lane;
         uint32_t g = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at(o, i);
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item t = item_at<true>(o, i);
             const int rev = o.calls.c[t.call].reverse;
             const bool dots = o.calls.c[t.call].dot != nullptr;
-            int t0;
-            int len;
-            float e[4];
-            if (t.chunks) {
-                chunk_at(t, rev, 0, t0, len);
-                load_decays(p, t0, len, t.h, lane, e);
-            }
             for (int k = 0; k < t.chunks; ++k, ++g) {
-                const uint32_t st = g & 1;
-                const Sums s = sums<true>(e, q, lane);
-                const int this_len = len;
-                col[128 * st + 32 * q + lane] = ex2f(rev ? s.P : s.U);
-                if (k + 1 < t.chunks) {
-                    chunk_at(t, rev, k + 1, t0, len);
-                    load_decays(p, t0, len, t.h, lane, e);
-                }
-                // all four warps are past the previous chunk and their column factors written
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.col[st]);
-                if (!wait(&bar.col[st], (g >> 1) & 1, p.err, abort) ||
-                    !wait(&bar.sc[st], (g >> 1) & 1, p.err, abort)) {
-                    ok = false;
-                    break;
-                }
+                const Chunk ch = chunk_at(t, rev, k);
+                const float* r = record(o, t, ch.i);
+                const float* rP = r + kRP + 32 * q;
+                const float* rPlo = r + kRPlo + 32 * q;
+                const float4 B = __ldg(reinterpret_cast<const float4*>(r + kRB));
+                // (of the reversed walk every sign of a diagonal block's difference changes)
+                const float sgn = rev ? -1.f : 1.f;
+                const float p_hi = sgn * __ldg(rP + lane), p_lo = sgn * __ldg(rPlo + lane);
+                float to_block = rev ? __ldg(r + kRU + 32 * q + lane) : sgn * p_hi;
+                if (!wait(&bar.sc, g & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t at = tmem + lb + kTA + 128 * st;
-                float to_block = rev ? s.U : s.P;  // log2 decay between the row and block j
 #pragma unroll 1
                 for (int n = 0; n < 4; ++n) {  // blocks at distance n from the diagonal
                     const int j = rev ? q + n : q - n, z = rev ? q - n : q + n;
@@ -469,201 +419,224 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (j < 0 || j > 3) continue;
                     float v[32];
                     tmem_ld32(at + 32 * j, v);
-                    landed(v);
                     if (n == 0) {
                         // columns of the triangle that are tokens of the segment
                         uint32_t in = rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
-                        if (rev && this_len - 32 * q < 32)
-                            in &= this_len > 32 * q ? (1u << (this_len - 32 * q)) - 1u : 0u;
+                        const int rest = ch.len - 32 * q;
+                        if (rev && rest < 32) in &= rest > 0 ? (1u << rest) - 1u : 0u;
+                        landed(v);
                         if (dots) {
                             float own = 0.f;
 #pragma unroll
                             for (int c = 0; c < 32; ++c) own = c == lane ? v[c] : own;
-                            diag[128 * (g % 3) + 32 * q + lane] = own;
+                            diag[128 * (g % 3)] = own;
                             in &= ~(1u << lane);
                         }
-                        const float ph = rev ? -s.P : s.P, pl = rev ? -s.Plo : s.Plo;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float x = (ph - __shfl_sync(0xffffffffu, ph, c)) +
-                                            (pl - __shfl_sync(0xffffffffu, pl, c));
-                            v[c] = in & (1u << c) ? v[c] * ex2f(x) : 0.f;
+                        for (int c4 = 0; c4 < 8; ++c4) {
+                            const float4 a = __ldg(reinterpret_cast<const float4*>(rP) + c4);
+                            const float4 b = __ldg(reinterpret_cast<const float4*>(rPlo) + c4);
+                            const float hi[4] = {a.x, a.y, a.z, a.w}, lo[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const int c = 4 * c4 + x;
+                                const float d = fmaf(-sgn, hi[x], p_hi) + fmaf(-sgn, lo[x], p_lo);
+                                v[c] = in & (1u << c) ? v[c] * ex2f(d) : 0.f;
+                            }
                         }
                     } else {
                         const float rf = ex2f(to_block);
-                        to_block += pick(s.B, j);
-                        const float4* cf = reinterpret_cast<const float4*>(col + 128 * st + 32 * j);
+                        to_block += j == 0 ? B.x : j == 1 ? B.y : j == 2 ? B.z : B.w;
+                        const float4* cf = reinterpret_cast<const float4*>(
+                            r + kRCol + (rev ? 128 : 0) + 32 * j);
+                        float4 f[8];
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            const float4 f = cf[c];
-                            v[4 * c] *= rf * f.x;
-                            v[4 * c + 1] *= rf * f.y;
-                            v[4 * c + 2] *= rf * f.z;
-                            v[4 * c + 3] *= rf * f.w;
+                            f[c] = __ldg(cf + c);
+                            mul2(f[c].x, f[c].y, rf, rf);
+                            mul2(f[c].z, f[c].w, rf, rf);
                         }
-                        if (rev && this_len - 32 * j < 32)
+                        landed(v);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            mul2(v[4 * c], v[4 * c + 1], f[c].x, f[c].y);
+                            mul2(v[4 * c + 2], v[4 * c + 3], f[c].z, f[c].w);
+                        }
+                        if (rev && ch.len - 32 * j < 32)
 #pragma unroll
                             for (int c = 0; c < 32; ++c)
-                                if (32 * j + c >= this_len) v[c] = 0.f;
+                                if (32 * j + c >= ch.len) v[c] = 0.f;
                     }
                     uint32_t u[32];  // each 16-token step: 8 columns of hi, 8 of lo
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
                         const int k2 = 16 * (c >> 3) + (c & 7);
-                        u[k2] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
-                        u[k2 + 8] =
-                            pack_bf16x2(v[2 * c] - __uint_as_float(u[k2] << 16),
-                                        v[2 * c + 1] - __uint_as_float(u[k2] & 0xffff0000u));
+                        split2(v[2 * c], v[2 * c + 1], u[k2], u[k2 + 8]);
                     }
                     tmem_st32(at + 32 * j, u);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.a[st]);
+                if (lane == 0) mbar_arrive(&bar.a);
             }
         }
-    } else {
+    } else if (warp < 12) {
         // --------------------------------------- state, decayed W and outputs
         const int q = warp & 3, wg = (warp - 4) >> 2;
         const int row = 32 * q + lane;  // token, or state row
-        const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
+        const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + 64 * wg;  // this warp's columns
         uint32_t g = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at(o, i);
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item t = item_at<true>(o, i);
             const Call& c = o.calls.c[t.call];
             const int rev = c.reverse;
+            const bool cols = 64 * wg < c.db;  // this warp has columns
             const int64_t E = (int64_t)c.da * c.db;
             const int64_t rs = c.tr ? 1 : c.db, cs = c.tr ? c.da : 1;
-            const int64_t mine = (int64_t)row * rs + (int64_t)(64 * t.half + 32 * wg) * cs;
+            const int64_t mine = (int64_t)row * rs + (int64_t)(64 * wg) * cs;
             const int64_t seq = ((int64_t)t.sg.n * p.H + t.h) * E + mine;
-            const bool sv = row < c.da;  // this lane holds a state row
-            if (!t.live) {
+            const bool holds = cols && row < c.da;  // this lane has a state row
+            if (!t.sg.live) {
                 // an empty sequence owns its first slot: its final state is its initial one
-                if (c.S_out && t.sg.count == 0 && t.sg.s == 0 && t.half * 64 < c.db && sv)
-                    for (int x = 0; x < 32; ++x)
+                if (c.S_out && t.sg.count == 0 && t.sg.s == 0 && holds)
+#pragma unroll 1
+                    for (int x = 0; x < 64; ++x)
                         c.S_out[seq + x * cs] = c.edge ? c.edge[seq + x * cs] : 0.f;
                 continue;
             }
             const float* from =
                 t.sg.count > 1 ? c.seg + ((int64_t)t.slot * p.H + t.h) * E + mine
                                : c.edge ? c.edge + seq : nullptr;
-            int t0, len;
-            float e[4];
-            chunk_at(t, rev, 0, t0, len);
-            load_decays(p, t0, len, t.h, lane, e);
-            {
-                // the segment's edge state into TMEM, once the last segment's is done with
-                float S[32];
+            // the segment's edge state into TMEM, once the last segment's is done with
+            if (g > 0 && !wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
+                uint32_t u[32];
 #pragma unroll
-                for (int x = 0; x < 32; ++x) S[x] = 0.f;
-                if (from && sv) {
+                for (int x = 0; x < 32; ++x) u[x] = 0u;
+                if (from && holds) {
                     if (c.tr) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x) S[x] = __ldcg(from + x * cs);
+                        for (int x = 0; x < 32; ++x)
+                            u[x] = __float_as_uint(__ldcg(from + (32 * b + x) * cs));
                     } else {
 #pragma unroll
                         for (int x = 0; x < 8; ++x) {
-                            const float4 f = __ldcg(reinterpret_cast<const float4*>(from) + x);
-                            S[4 * x] = f.x;
-                            S[4 * x + 1] = f.y;
-                            S[4 * x + 2] = f.z;
-                            S[4 * x + 3] = f.w;
+                            const uint4 f = __ldcg(reinterpret_cast<const uint4*>(from) + 8 * b + x);
+                            u[4 * x] = f.x;
+                            u[4 * x + 1] = f.y;
+                            u[4 * x + 2] = f.z;
+                            u[4 * x + 3] = f.w;
                         }
                     }
                 }
-                if (g > 0 && !wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
-                tc_fence_after();
-                uint32_t u[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(S[x]);
-                tmem_st32(tmem + lb + kTS + 32 * wg, u);
-                tmem_st_wait();
+                tmem_st32(at + kTS + 32 * b, u);
             }
-            int t0_prev = 0, len_prev = 0;
+            tmem_st_wait();
+
             float rowf_prev = 0.f;
+            Chunk prev{};
             // step k: the state's copy and the decayed W of chunk k, then the outputs of chunk
             // k - 1 while the tensor cores work on chunk k
 #pragma unroll 1
             for (int k = 0; k <= t.chunks; ++k) {
-                const int t0_now = t0, len_now = len;
                 float rowf = 0.f;
+                Chunk ch{};
                 if (k < t.chunks) {
-                    const uint32_t st = g & 1;
-                    const Sums s = sums<false>(e, q, lane);
-                    const float head = s.P + before(s, q), tail = s.U + after(s, q);
-                    rowf = ex2f(rev ? tail : head);
-                    const float wf = row < len ? ex2f(rev ? head : tail) : 0.f;
-                    const float all = ex2f((s.B[0] + s.B[1]) + (s.B[2] + s.B[3]));
-                    if (k + 1 < t.chunks) {
-                        chunk_at(t, rev, k + 1, t0, len);
-                        load_decays(p, t0, len, t.h, lane, e);
-                    }
+                    ch = chunk_at(t, rev, k);
+                    const float* r = record(o, t, ch.i);
+                    const float head = __ldg(r + kRHead + row), tail = __ldg(r + kRTail + row);
+                    const float all = ex2f(__ldg(r + kRB + 4));
+                    rowf = rev ? tail : head;
+                    const float wf = rev ? head : tail;
                     // the last update of the state, the last read of its copy and of the decayed
                     // W's buffer are complete
                     if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
-                                  !wait(&bar.qs, (g - 1) & 1, p.err, abort))) {
+                                  !wait(&bar.xs, (g - 1) & 1, p.err, abort))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    uint8_t* sr = sm + kSS + row * 128;
+                    if (cols) {
+                        uint8_t* sr = sm + kSS + wg * 16384 + row * 128;
 #pragma unroll 1
-                    for (int b = 0; b < 2; ++b) {
-                        float S[16];
-                        tmem_ld16(tmem + lb + kTS + 32 * wg + 16 * b, S);
-                        landed(S);
-                        if (sv)
+                        for (int b = 0; b < 2; ++b) {
+                            float S[32];
+                            tmem_ld32(at + kTS + 32 * b, S);
+                            landed(S);
+                            if (holds)
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                float v[8];
+                                for (int x = 0; x < 4; ++x) {
+                                    uint4 hi, lo;
+                                    split2(S[8 * x], S[8 * x + 1], hi.x, lo.x);
+                                    split2(S[8 * x + 2], S[8 * x + 3], hi.y, lo.y);
+                                    split2(S[8 * x + 4], S[8 * x + 5], hi.z, lo.z);
+                                    split2(S[8 * x + 6], S[8 * x + 7], hi.w, lo.w);
+                                    const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
+                                    *reinterpret_cast<uint4*>(sr + to) = hi;
+                                    *reinterpret_cast<uint4*>(sr + 32768 + to) = lo;
+                                }
+                            uint32_t u[32];
 #pragma unroll
-                                for (int y = 0; y < 8; ++y) v[y] = S[8 * x + y];
-                                uint4 hi, lo;
-                                pk8_hilo(v, hi, lo);
-                                const uint32_t at = ((4 * wg + 2 * b + x) ^ (row & 7)) << 4;
-                                *reinterpret_cast<uint4*>(sr + at) = hi;
-                                *reinterpret_cast<uint4*>(sr + 16384 + at) = lo;
+                            for (int x = 0; x < 32; x += 2) {
+                                mul2(S[x], S[x + 1], all, all);
+                                u[x] = __float_as_uint(S[x]);
+                                u[x + 1] = __float_as_uint(S[x + 1]);
                             }
-                        uint32_t u[16];
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) u[x] = __float_as_uint(S[x] * all);
-                        tmem_st16(tmem + lb + kTS + 32 * wg + 16 * b, u);
+                            tmem_st32(at + kTS + 32 * b, u);
+                        }
+                        tmem_st_wait();
+                        fence_async_smem();
                     }
-                    tmem_st_wait();
-                    fence_async_smem();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.s);
 
-                    if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
-                    uint8_t* stage = sm + st * kStage;
-                    uint8_t* wr = stage + kSW + row * 128;
-                    uint8_t* wd = sm + kSWd + row * 128;
-                    const bool dead = row >= len_now;
-#pragma unroll 2
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t at = ((4 * wg + x) ^ (row & 7)) << 4;
-                        uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-                        if (!dead) {
-                            float v[8];
-                            ld8(wr + at, v);
-#pragma unroll
-                            for (int y = 0; y < 8; ++y) v[y] *= wf;
-                            pk8_hilo(v, hi, lo);
-                        } else {
-                            // rows past the segment hold another sequence's tokens (or zeros):
-                            // they must not reach a product even as 0 * inf
-                            *reinterpret_cast<uint4*>(wr + at) = hi;
-                        }
-                        *reinterpret_cast<uint4*>(wd + at) = hi;
-                        *reinterpret_cast<uint4*>(wd + 16384 + at) = lo;
-                    }
-                    if (dead && 64 * wg < c.da) {
-                        uint4* yr = reinterpret_cast<uint4*>(stage + kSY + wg * 16384 + row * 128);
+                    if (!wait(&bar.w, g & 1, p.err, abort)) { ok = false; break; }
+                    const bool dead = row >= ch.len;
+                    if (cols) {
+                        uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
+                        uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
 #pragma unroll 1
-                        for (int x = 0; x < 8; ++x) yr[x] = make_uint4(0u, 0u, 0u, 0u);
+                        for (int b = 0; b < 2; ++b) {
+                            uint4 in[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                in[x] = *reinterpret_cast<const uint4*>(
+                                    wr + (((4 * b + x) ^ (row & 7)) << 4));
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    float a0 = __uint_as_float(w[y] << 16);
+                                    float a1 = __uint_as_float(w[y] & 0xffff0000u);
+                                    mul2(a0, a1, wf, wf);
+                                    split2(a0, a1, hi[y], lo[y]);
+                                    if (dead) hi[y] = lo[y] = 0u;
+                                }
+                                const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
+                                *reinterpret_cast<uint4*>(wd + to) =
+                                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                *reinterpret_cast<uint4*>(wd + 32768 + to) =
+                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            }
+                        }
+                    }
+                    if (ch.len < kC) {
+                        // rows past the segment hold another sequence's tokens (or zeros): they
+                        // must not reach a product even as 0 * inf.  (X Y^T is masked instead.)
+                        if (!wait(&bar.y, g & 1, p.err, abort)) { ok = false; break; }
+                        if (dead) {
+                            uint4* wr = reinterpret_cast<uint4*>(sm + kSW + wg * 16384 + row * 128);
+                            uint4* yr = reinterpret_cast<uint4*>(sm + kSY + wg * 16384 + row * 128);
+#pragma unroll 1
+                            for (int x = 0; x < 8; ++x) wr[x] = yr[x] = make_uint4(0u, 0u, 0u, 0u);
+                        }
                     }
                     fence_async_smem();
                     __syncwarp();
@@ -677,77 +650,82 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     // the same number in both of the decay's gradient's sums, where under strong
                     // decays everything else is far below its rounding.
                     const uint32_t gg = k < t.chunks ? g - 2 : g - 1;
-                    if (!wait(&bar.o_full, gg & 1, p.err, abort)) { ok = false; break; }
+                    if (!wait(&bar.out, gg & 1, p.err, abort)) { ok = false; break; }
                     tc_fence_after();
-                    const int tr = t0_prev + row;
-                    const int off = t.h * c.db + 64 * t.half + 32 * wg;
-                    const bool in = row < len_prev;
-                    uint8_t* out = static_cast<uint8_t*>(c.out) +
-                                   ((int64_t)tr * p.H * c.db + off) * 2;
-                    float acc = 0.f;
+                    if (cols) {
+                        const int tr = prev.t0 + row;
+                        const int off = t.h * c.db + 64 * wg;
+                        const bool in = row < prev.len;
+                        uint8_t* out = static_cast<uint8_t*>(c.out) +
+                                       ((int64_t)tr * p.H * c.db + off) * 2;
+                        const uint8_t* dr = static_cast<const uint8_t*>(c.dot) +
+                                            ((int64_t)tr * c.dot_ld + off) * 2;
+                        const uint8_t* wr =
+                            static_cast<const uint8_t*>(c.w) + ((int64_t)tr * c.w_ld + off) * 2;
+                        const float dg =
+                            reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg % 3) + row];
+                        float acc = 0.f;
 #pragma unroll 1
-                    for (int b = 0; b < 2; ++b) {
-                        float o1[16], o2[16];
-                        tmem_ld16(tmem + lb + kTO1 + 32 * wg + 16 * b, o1);
-                        tmem_ld16(tmem + lb + kTO2 + 64 * (gg & 1) + 32 * wg + 16 * b, o2);
-                        landed(o1);
-                        landed(o2);
+                        for (int b = 0; b < 4; ++b) {
+                            float o1[16], o2[16];
+                            tmem_ld16(at + kTO1 + 16 * b, o1);
+                            tmem_ld16(at + kTO2 + 16 * b, o2);
+                            landed(o1);
+                            landed(o2);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) o1[x] = fmaf(rowf_prev, o2[x], o1[x]);
-                        if (in && c.dot) {
-                            const uint8_t* dr = static_cast<const uint8_t*>(c.dot) +
-                                                ((int64_t)tr * c.dot_ld + off) * 2 + 32 * b;
-                            const uint8_t* wr = static_cast<const uint8_t*>(c.w) +
-                                                ((int64_t)tr * c.w_ld + off) * 2 + 32 * b;
-                            const float dg =
-                                reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg % 3) + row];
+                            for (int x = 0; x < 16; ++x) o1[x] = fmaf(rowf_prev, o2[x], o1[x]);
+                            if (in && c.dot) {
 #pragma unroll
-                            for (int h8 = 0; h8 < 2; ++h8) {
-                                float d[8], w[8];
-                                ld8(dr + 16 * h8, d);
-                                ld8(wr + 16 * h8, w);
+                                for (int h8 = 0; h8 < 2; ++h8) {
+                                    float d[8], w[8];
+                                    ld8(dr + 32 * b + 16 * h8, d);
+                                    ld8(wr + 32 * b + 16 * h8, w);
 #pragma unroll
-                                for (int x = 0; x < 8; ++x) {
-                                    acc = fmaf(o1[8 * h8 + x], d[x], acc);
-                                    o1[8 * h8 + x] = fmaf(dg, w[x], o1[8 * h8 + x]);
+                                    for (int x = 0; x < 8; ++x) {
+                                        acc = fmaf(o1[8 * h8 + x], d[x], acc);
+                                        o1[8 * h8 + x] = fmaf(dg, w[x], o1[8 * h8 + x]);
+                                    }
+                                }
+                            }
+                            if (in) {
+                                uint4 u[2];
+#pragma unroll
+                                for (int x = 0; x < 2; ++x)
+                                    u[x] = make_uint4(pack_bf16x2(o1[8 * x], o1[8 * x + 1]),
+                                                      pack_bf16x2(o1[8 * x + 2], o1[8 * x + 3]),
+                                                      pack_bf16x2(o1[8 * x + 4], o1[8 * x + 5]),
+                                                      pack_bf16x2(o1[8 * x + 6], o1[8 * x + 7]));
+                                if (o.wide_store) {
+                                    st_global_32(out + 32 * b, u[0], u[1]);
+                                } else {
+                                    reinterpret_cast<uint4*>(out)[2 * b] = u[0];
+                                    reinterpret_cast<uint4*>(out)[2 * b + 1] = u[1];
                                 }
                             }
                         }
-                        if (in) {
-                            uint4 u[2];
-#pragma unroll
-                            for (int x = 0; x < 2; ++x)
-                                u[x] = make_uint4(pack_bf16x2(o1[8 * x], o1[8 * x + 1]),
-                                                  pack_bf16x2(o1[8 * x + 2], o1[8 * x + 3]),
-                                                  pack_bf16x2(o1[8 * x + 4], o1[8 * x + 5]),
-                                                  pack_bf16x2(o1[8 * x + 6], o1[8 * x + 7]));
-                            if (o.wide_store) {
-                                st_global_32(out + 32 * b, u[0], u[1]);
-                            } else {
-                                reinterpret_cast<uint4*>(out)[2 * b] = u[0];
-                                reinterpret_cast<uint4*>(out)[2 * b + 1] = u[1];
-                            }
-                        }
+                        if (in && c.dot)
+                            c.dots[((int64_t)wg * p.T + tr) * p.H + t.h] = acc;
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.o_free);
-                    if (in && c.dot)
-                        c.dots[((int64_t)(2 * t.half + wg) * p.T + tr) * p.H + t.h] = acc;
+                    if (lane == 0) mbar_arrive(&bar.read);
                 }
-                t0_prev = t0_now;
-                len_prev = len_now;
+                prev = ch;
                 rowf_prev = rowf;
             }
             if (!ok) break;
             const bool last = rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1;
-            if (last && c.S_out) {  // (the chunk's outputs are complete, so its update is too)
-                float S[32];
-                tmem_ld32(tmem + lb + kTS + 32 * wg, S);
-                landed(S);
-                if (sv)
+            if (last && c.S_out && cols) {  // (the outputs are complete, so the update is too)
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    float S[16];
+                    tmem_ld16(at + kTS + 16 * b, S);
+                    landed(S);
+                    if (holds)
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) c.S_out[seq + x * cs] = S[x];
+                        for (int x = 0; x < 16; ++x) c.S_out[seq + (16 * b + x) * cs] = S[x];
+                }
+                tc_fence_before();
             }
         }
     }
@@ -755,9 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     __syncthreads();
     if (bar.abort) {
         // let copies and MMAs still in flight land before leaving
-        if (warp == 12)
-            for (int x = max(loads - 2, 0); x < loads; ++x)
-                mbar_wait(&bar.full[x & 1], (x >> 1) & 1, nullptr);
+        if (loads > 0) mbar_wait(load_bar, (loads - 1) & 1, nullptr);
         if (tid == 13 * 32) {
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, nullptr);
@@ -767,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(0, 512);
     }
 }
 
@@ -796,7 +772,6 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
     const Problem& p = o.p;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &bar.abort;
-    static_assert(kC == 128, "a chunk is the 128 lanes of a TMEM tile");
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
@@ -812,70 +787,62 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int64_t items = item_count(o);
+    const uint32_t items = item_count(o);
     // an item whose sum no edge needs: the last segment of a walk
     auto skip = [&](const Item& t) {
         const int rev = o.calls.c[t.call].reverse;
-        return !t.live || (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1);
+        return !t.sg.live || (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1);
     };
-    int loads = 0;
+    int loads = 0;  // stages loaded by the TMA thread (for the way out of an abort)
 
-    if (warp == 0) {
+    if (tid == 0) {
         uint32_t g = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at(o, i);
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item t = item_at<false>(o, i);
             if (skip(t)) continue;
             const Call& c = o.calls.c[t.call];
             for (int k = 0; k < t.chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
-                if (g >= 2 && !wait(&bar.done[st], ((g - 2) >> 1) & 1, p.err, abort)) {
+                if (g >= 2 && !wait1(&bar.done[st], ((g - 2) >> 1) & 1, p.err, abort)) {
                     ok = false;
                     break;
                 }
-                int t0;
-                int len;
-                chunk_at(t, !c.reverse, k, t0, len);
-                if (lane == 0) {
-                    uint8_t* s = sm + st * kUStage;
-                    mbar_expect_tx(&bar.full[st], (c.da + c.db) / 64 * 16384);
-                    for (int b = 0; b < c.da / 64; ++b)
-                        tma_load_3d(s + kUY + b * 16384, &o.y[t.call], 64 * b, t.h, t0,
-                                    &bar.full[st]);
-                    for (int b = 0; b < c.db / 64; ++b)
-                        tma_load_3d(s + kUW + b * 16384, &o.w[t.call], 64 * b, t.h, t0,
-                                    &bar.full[st]);
-                }
+                const Chunk ch = chunk_at(t, !c.reverse, k);
+                uint8_t* s = sm + st * kUStage;
+                mbar_expect_tx(&bar.full[st], (c.da + c.db) / 64 * 16384);
+#pragma unroll 1
+                for (int b = 0; b < c.da / 64; ++b)
+                    tma_load_3d(s + kUY + b * 16384, &o.y[t.call], 64 * b, t.h, ch.t0, &bar.full[st]);
+#pragma unroll 1
+                for (int b = 0; b < c.db / 64; ++b)
+                    tma_load_3d(s + kUW + b * 16384, &o.w[t.call], 64 * b, t.h, ch.t0, &bar.full[st]);
                 loads = (int)g + 1;
             }
         }
-    } else if (warp == 1) {
-        const uint32_t lead = lane == 0;
-        const uint32_t tm = uniform(tmem);
-        const uint64_t dY = sdesc_sw128(sbase + kUY, 16384, 1024);
-        const uint64_t dHi = sdesc_sw128(sbase + kUW, 16384, 1024);
-        const uint64_t dLo = sdesc_sw128(sbase + kULo, 16384, 1024);
+    } else if (tid == 32) {
+        const uint32_t lY = dlow(sbase + kUY, 16384), lHi = dlow(sbase + kUW, 16384);
+        const uint32_t lLo = dlow(sbase + kULo, 16384);
         uint32_t g = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at(o, i);
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item t = item_at<false>(o, i);
             if (skip(t)) continue;
-            const Call& c = o.calls.c[t.call];
-            const uint32_t id = uniform(idesc_bf16(128, 64, true, true) +
-                                        (c.db == 128 ? (64u >> 3) << 17 : 0u));  // N = db
-            const uint32_t chunks = uniform(t.chunks);
-            for (uint32_t k = 0; k < chunks; ++k, ++g) {
+            const uint32_t id =
+                idesc_bf16(128, 0, true, true) | (uint32_t)(o.calls.c[t.call].db >> 3) << 17;
+            for (int k = 0; k < t.chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
-                if (!wait(&bar.wd[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
+                if (!wait1(&bar.wd[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t stage = st * kUStage >> 4;
-#pragma unroll 4
-                for (uint32_t ks = 0; ks < 8; ++ks) {
-                    const uint32_t at = stage + (ks * 2048 >> 4);
-                    mma_ss(tm, dY + at, dHi + at, id, k + ks > 0, lead);
-                    mma_ss(tm, dY + at, dLo + at, id, 1, lead);
+                uint32_t at = st * kUStage >> 4;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    mma_bf16(tmem, desc(lY + at + (ks * 2048 >> 4)),
+                             desc(lHi + at + (ks * 2048 >> 4)), id, k + ks > 0);
+                    mma_bf16(tmem, desc(lY + at + (ks * 2048 >> 4)),
+                             desc(lLo + at + (ks * 2048 >> 4)), id, 1);
                 }
-                commit(&bar.done[st], lead);
+                mma_commit(&bar.done[st]);
             }
         }
     } else if (warp >= 4) {
@@ -884,52 +851,56 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
         uint32_t g = 0;
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at(o, i);
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            const Item t = item_at<true>(o, i);
             if (skip(t)) continue;
             const Call& c = o.calls.c[t.call];
             const int rev = c.reverse;
+            const bool cols = 64 * wg < c.db;
             float between = 0.f;  // log2 decay between the edge and the chunk
-            int t0;
-            int len;
-            float e[4];
-            chunk_at(t, !rev, 0, t0, len);
-            load_decays(p, t0, len, t.h, lane, e);
+#pragma unroll 1
             for (int k = 0; k < t.chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
-                const Sums s = sums<false>(e, q, lane);
-                const float head = s.P + before(s, q), tail = s.U + after(s, q);
-                const float wf = ex2f((rev ? head : tail) + between);
-                between += (s.B[0] + s.B[1]) + (s.B[2] + s.B[3]);
-                const int len_now = len;
-                if (k + 1 < t.chunks) {
-                    chunk_at(t, !rev, k + 1, t0, len);
-                    load_decays(p, t0, len, t.h, lane, e);
-                }
+                const Chunk ch = chunk_at(t, !rev, k);
+                const float* r = record(o, t, ch.i);
+                const float wf = __ldg(r + (rev ? kRHead : kRTail) + row) * ex2f(between);
+                between += __ldg(r + kRB + 4);
                 if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 uint8_t* stage = sm + st * kUStage;
-                const bool dead = row >= len_now;
-                if (64 * wg < c.db) {
+                const bool dead = row >= ch.len;
+                if (cols) {
                     uint8_t* wr = stage + kUW + wg * 16384 + row * 128;
                     uint8_t* lr = stage + kULo + wg * 16384 + row * 128;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const uint32_t at = (x ^ (row & 7)) << 4;
-                        uint4 hi = make_uint4(0u, 0u, 0u, 0u), lo = hi;
-                        if (!dead) {
-                            float v[8];
-                            ld8(wr + at, v);
+                    for (int b = 0; b < 2; ++b) {
+                        uint4 in[4];
 #pragma unroll
-                            for (int y = 0; y < 8; ++y) v[y] *= wf;
-                            pk8_hilo(v, hi, lo);
+                        for (int x = 0; x < 4; ++x)
+                            in[x] = *reinterpret_cast<const uint4*>(
+                                wr + (((4 * b + x) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                            uint32_t hi[4], lo[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) {
+                                float a0 = __uint_as_float(w[y] << 16);
+                                float a1 = __uint_as_float(w[y] & 0xffff0000u);
+                                mul2(a0, a1, wf, wf);
+                                split2(a0, a1, hi[y], lo[y]);
+                                if (dead) hi[y] = lo[y] = 0u;
+                            }
+                            const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
+                            *reinterpret_cast<uint4*>(wr + to) =
+                                make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(lr + to) =
+                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
                         }
-                        *reinterpret_cast<uint4*>(wr + at) = hi;
-                        *reinterpret_cast<uint4*>(lr + at) = lo;
                     }
                 }
-                if (dead && 64 * wg < c.da) {
+                if (dead) {
                     uint4* yr = reinterpret_cast<uint4*>(stage + kUY + wg * 16384 + row * 128);
-#pragma unroll
+#pragma unroll 1
                     for (int x = 0; x < 8; ++x) yr[x] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_smem();
@@ -942,9 +913,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             const uint32_t gl = g - 1;
             if (!wait(&bar.done[gl & 1], (gl >> 1) & 1, p.err, abort)) { ok = false; break; }
             tc_fence_after();
-            const int64_t at = (((int64_t)t.slot * p.H + t.h) * c.da + row) * c.db + 64 * wg;
-            if (64 * wg < c.db) {
-                float* to = const_cast<float*>(c.seg) + at;
+            if (cols) {
+                float* to = const_cast<float*>(c.seg) +
+                            (((int64_t)t.slot * p.H + t.h) * c.da + row) * c.db + 64 * wg;
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     float v[32];
@@ -965,7 +936,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
 
     __syncthreads();
     if (bar.abort) {
-        if (warp == 0)
+        if (tid == 0)
             for (int x = max(loads - 2, 0); x < loads; ++x)
                 mbar_wait(&bar.full[x & 1], (x >> 1) & 1, nullptr);
         if (tid == 32) {
@@ -1022,15 +993,15 @@ int sm_count() {
 }
 
 cudaError_t fill(OutParams& o, const Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                 bool out) {
+                 const float* rec, bool out) {
     o.p = p;
     o.calls = calls;
     o.n_calls = n;
-    o.slots = slots;
+    o.slots = (int)slots;
+    o.rec = rec;
     o.wide_store = 1;
     for (int i = 0; i < n; ++i) {
         const Call& c = calls.c[i];
-        if (out && c.db == 128) o.halves = 2;
         if (reinterpret_cast<uintptr_t>(c.out) & 31) o.wide_store = 0;
         if (p.T == 0) continue;
         if ((out && !make_map(&o.x[i], c.x, p.T, p.H, c.da, c.x_ld)) ||
@@ -1043,25 +1014,34 @@ cudaError_t fill(OutParams& o, const Problem& p, const lin::Calls& calls, int n,
 
 }  // namespace
 
+size_t record_bytes(int64_t slots, int L, int H) {
+    return (size_t)slots * (L / kC) * H * kRec * sizeof(float);
+}
+
+cudaError_t launch_decays(const Problem& p, int64_t slots, float* rec, cudaStream_t s) {
+    if (p.T == 0) return cudaSuccess;
+    ProfScope prof("linear_decay_kernel", s);
+    decay_kernel<<<dim3((unsigned)(slots * (p.L / kC)), (p.H + 7) / 8), 256, 0, s>>>(p, rec);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_outputs(const Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                           const char* name, cudaStream_t s) {
+                           const float* rec, const char* name, cudaStream_t s) {
     OutParams o{};
-    o.halves = 1;
-    if (cudaError_t e = fill(o, p, calls, n, slots, true)) return e;
+    if (cudaError_t e = fill(o, p, calls, n, slots, rec, true)) return e;
     if (cudaError_t e = cudaFuncSetAttribute(
             out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem))
         return e;
-    const int64_t items = slots * p.H * n * o.halves, sms = sm_count();
+    const int64_t items = slots * p.H * n, sms = sm_count();
     ProfScope prof(name, s);
     out_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, kOutSmem, s>>>(o);
     return cudaGetLastError();
 }
 
 cudaError_t launch_sums(const Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                        float* dec, const char* name, cudaStream_t s) {
+                        const float* rec, float* dec, const char* name, cudaStream_t s) {
     OutParams o{};
-    o.halves = 1;
-    if (cudaError_t e = fill(o, p, calls, n, slots, false)) return e;
+    if (cudaError_t e = fill(o, p, calls, n, slots, rec, false)) return e;
     if (cudaError_t e = cudaFuncSetAttribute(
             sum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSumSmem))
         return e;
