@@ -322,9 +322,9 @@ bool use_tc(int io_bf16) {
 
 // Tokens a segment: short enough that the segments of all heads fill the GPU a few times, no
 // shorter than the edge states' traffic (two fp32 states a segment) is worth.
-int segment_length(int64_t T, int H, bool tc) {
+int segment_length(int64_t T, int H, bool tc, bool bwd) {
     int L = tc ? 128 : 64;
-    while (L < 1024 && T / L * H > 4 * 152) L *= 2;
+    while (L < (tc && !bwd ? 2048 : 1024) && T / L * H > 4 * 152) L *= 2;
     return L;
 }
 
@@ -337,7 +337,7 @@ struct Layout {
 
 Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool equal) {
     Layout l{};
-    l.L = segment_length(T, H, tc);
+    l.L = segment_length(T, H, tc, bwd);
     l.slots = lin::slot_count(T, N, l.L);
     l.segments = (equal && N > 0 ? T / N : T) > l.L;
     const size_t state = (size_t)H * dk * dv * sizeof(float);

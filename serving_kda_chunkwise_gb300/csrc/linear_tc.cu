@@ -54,6 +54,19 @@ __device__ __noinline__ bool wait1(uint64_t* bar, uint32_t parity, unsigned* err
     return mbar_wait_ab(bar, parity, err, abort);
 }
 
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
 // The registers of earlier TMEM loads are ready (tied to the wait, so that no use moves above it).
 __device__ __forceinline__ void landed(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -229,44 +242,48 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
 }
 
 // -------------------------------------------------------------- outputs --
-// Persistent, one CTA an SM.  Roles: warps 0..3 turn X Y^T into A (hi + lo over the product's own
-// TMEM columns, so that A never leaves tensor memory); warps 4..11 decay W, keep the state's copy
-// and write the outputs; single threads of warps 12, 14 and 15 load X, Y and W by TMA, one of warp
-// 13 issues the MMAs.  Warp w reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in
-// fp32; X S reads its bf16 hi + lo copy in shared memory.
+// Persistent, one CTA an SM.  Roles: warps 0..7 turn X Y^T into A (hi + lo over the product's own
+// TMEM columns, so that A never leaves tensor memory); warps 8..15 decay W, keep the state's copy
+// and write the outputs; lanes of warp 16 load X, Y, W and the decays, one thread of warp 17
+// issues the MMAs, each chunk's three sets in the order in which their operands get ready.  Warp w
+// reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in fp32; X S reads its bf16
+// hi + lo copy in shared memory.
 // Shared memory holds one chunk of X, Y and W (32 KB each), the decayed W and the state's copy (64
 // KB each): no second stage fits, but each operand is reloaded as soon as its last product is
 // done, and while one waits the others' products run.  (Two stages fit with 64 of the db columns
 // to a CTA; that form made A twice and its N = 64 products run at 75 % of N = 128's rate, and was
 // slower.)
-constexpr int kThreads = 512;
+constexpr int kThreads = 576;
+constexpr int kTmaWarp = 16, kMmaT = 17 * 32;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
 constexpr uint32_t kSWd = 98304;             // decayed W: hi, lo
 constexpr uint32_t kSS = kSWd + 65536;       // state: hi, lo
-constexpr uint32_t kSDiag = kSS + 65536;     // diagonals of X Y^T, three chunks of 128 floats
-constexpr uint32_t kSBar = kSDiag + 1536;
+constexpr uint32_t kSRec = kSS + 65536;      // the record's P, Plo and column factors
+constexpr uint32_t kSDiag = kSRec + 1536;    // diagonals of X Y^T, two chunks of 128 floats
+constexpr uint32_t kSBar = kSDiag + 1024;
 constexpr uint32_t kOutSmem = kSBar + 256;
 static_assert(kOutSmem <= 232448, "shared-memory limit");
 // TMEM columns (all 512 are allocated, so the base address is 0): X Y^T / A, A W, X S, state
 constexpr uint32_t kTA = 0, kTO1 = 128, kTO2 = 256, kTS = 384;
 
 struct OutBars {
-    uint64_t x, y, w;        // operands loaded
-    uint64_t sc, a;          // X Y^T complete; A written (4 arrivals)
+    uint64_t x, y, w, rec;   // operands and decays loaded
+    uint64_t sc, a;          // X Y^T complete; A written (8 arrivals)
     uint64_t s, wd;          // state and its copy written; decayed W written (8 arrivals each)
-    uint64_t upd, xs;        // state update complete; X S complete
-    uint64_t out, read;      // A W (so the chunk's outputs) complete; outputs read (8 arrivals)
+    uint64_t upd, xs, aw;    // state update, X S, A W complete
+    uint64_t read;           // the chunk's outputs read (8 arrivals)
     uint64_t drain;
     uint32_t tmem;
     int abort;
 };
 static_assert(sizeof(OutBars) <= 256, "barrier area");
 
-// One operand's loads, by one thread: chunk after chunk, each once `freed` says that the last
-// chunk's products have read the buffer.  Returns the number of loads issued.
+// One operand's loads (0: X, 1: Y, 2: W, 3: decays), by one thread: chunk after chunk, each once
+// `freed` (and `freed2`) say that the last chunk's buffer has been read.  Returns the number of
+// chunks loaded.
 __device__ __noinline__ int load_operand(const OutParams& o, const CUtensorMap* maps, int which,
                                          uint8_t* dst, uint64_t* full, uint64_t* freed,
-                                         volatile int* abort) {
+                                         uint64_t* freed2, volatile int* abort) {
     const uint32_t items = item_count(o);
     int g = 0;
     for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
@@ -274,8 +291,17 @@ __device__ __noinline__ int load_operand(const OutParams& o, const CUtensorMap* 
         const Call& c = o.calls.c[t.call];
         const int blocks = (which == 2 ? c.db : c.da) / 64;
         for (int k = 0; k < t.chunks; ++k, ++g) {
-            if (g > 0 && !wait1(freed, (g - 1) & 1, o.p.err, abort)) return g;
+            if (g > 0 && (!wait1(freed, (g - 1) & 1, o.p.err, abort) ||
+                          (freed2 && !wait1(freed2, (g - 1) & 1, o.p.err, abort))))
+                return g;
             const Chunk ch = chunk_at(t, c.reverse, k);
+            if (which == 3) {
+                const float* r = record(o, t, ch.i);
+                mbar_expect_tx(full, 1536);
+                bulk_g2s(dst, r + kRP, 1024, full);
+                bulk_g2s(dst + 1024, r + kRCol + (c.reverse ? 128 : 0), 512, full);
+                continue;
+            }
             mbar_expect_tx(full, blocks * 16384);
 #pragma unroll 1
             for (int b = 0; b < blocks; ++b)
@@ -293,12 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int* abort = &bar.abort;
     if (tid == 0) {
-        uint64_t* one[] = {&bar.x, &bar.y, &bar.w, &bar.sc, &bar.upd, &bar.xs, &bar.out, &bar.drain};
+        uint64_t* one[] = {&bar.x,  &bar.y,   &bar.w,  &bar.rec, &bar.sc,
+                           &bar.upd, &bar.xs, &bar.aw, &bar.drain};
         for (uint64_t* b : one) mbar_init(b, 1);
-        mbar_init(&bar.a, 4);
-        mbar_init(&bar.s, 8);
-        mbar_init(&bar.wd, 8);
-        mbar_init(&bar.read, 8);
+        uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd, &bar.read};
+        for (uint64_t* b : eight) mbar_init(b, 8);
         fence_mbar_init();
         bar.abort = 0;
     }
@@ -311,16 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     int loads = 0;  // of this thread (for the way out of an abort)
     uint64_t* load_bar = nullptr;
 
-    if (tid == 12 * 32) {
-        load_bar = &bar.x;
-        loads = load_operand(o, o.x, 0, sm + kSX, &bar.x, &bar.xs, abort);
-    } else if (tid == 14 * 32) {
-        load_bar = &bar.y;
-        loads = load_operand(o, o.y, 1, sm + kSY, &bar.y, &bar.upd, abort);
-    } else if (tid == 15 * 32) {
-        load_bar = &bar.w;
-        loads = load_operand(o, o.w, 2, sm + kSW, &bar.w, &bar.out, abort);
-    } else if (tid == 13 * 32) {
+    if (warp == kTmaWarp) {
+        if (lane < 4) {
+            load_bar = lane == 0 ? &bar.x : lane == 1 ? &bar.y : lane == 2 ? &bar.w : &bar.rec;
+            loads = load_operand(
+                o, lane == 0 ? o.x : lane == 1 ? o.y : o.w, lane,
+                sm + (lane == 0 ? kSX : lane == 1 ? kSY : lane == 2 ? kSW : kSRec), load_bar,
+                lane == 0 ? &bar.xs : lane == 1 ? &bar.upd : lane == 2 ? &bar.aw : &bar.a,
+                lane == 2 ? &bar.wd : nullptr, abort);
+        }
+    } else if (tid == kMmaT) {
         // ------------------------------------------------------- MMA thread
         constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
         const uint32_t lX = dlow(sbase + kSX, 0), lYk = dlow(sbase + kSY, 0);
@@ -334,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             const uint32_t n = (uint32_t)(o.calls.c[t.call].db >> 3) << 17;  // N = db
             const uint32_t id_out = (idesc_bf16(128, 0, false, true)) | n;   // A W, X S
             const uint32_t id_up = (idesc_bf16(128, 0, true, true)) | n;     // Y^T W
-            for (int k = 0; k < t.chunks; ++k, ++g) {
+            for (int k = 0; ok && k < t.chunks; ++k, ++g) {
                 const uint32_t ph = g & 1;
                 ok = wait1(&bar.x, ph, p.err, abort) && wait1(&bar.y, ph, p.err, abort);
                 if (!ok) break;
@@ -346,48 +371,75 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     mma_bf16(kTA, desc(lX + off), desc(lYk + off), id_sc, ks > 0);
                 }
                 mma_commit(&bar.sc);
-                ok = wait1(&bar.s, ph, p.err, abort) && wait1(&bar.wd, ph, p.err, abort);
-                if (!ok) break;
-                tc_fence_after();
-                // S += Y^T Wd: 128 tokens in 8 steps, hi and lo (da = 64: the second 64 lanes
-                // take whatever the buffer's second half holds and are never read)
+                // the other three, each as soon as its operands are there
+                uint32_t todo = 7;
+                uint64_t since = 0;
+                while (todo) {
+                    uint32_t now = 0;
+                    const bool s = test(&bar.s, ph);
+                    if ((todo & 1) && s && test(&bar.wd, ph)) {
+                        now = 1;
+                    } else if (g == 0 || test(&bar.read, ph ^ 1)) {
+                        if ((todo & 2) && s) now = 2;
+                        else if ((todo & 4) && test(&bar.a, ph) && test(&bar.w, ph)) now = 4;
+                    }
+                    if (now == 0) {
+                        if (since == 0) since = globaltimer();
+                        if (*abort) { ok = false; break; }
+                        if (globaltimer() - since > kWaitLimitNs) {
+                            atomicOr(p.err, kDevErrTimeout);
+                            *abort = 1;
+                            ok = false;
+                            break;
+                        }
+                        continue;
+                    }
+                    todo &= ~now;
+                    since = 0;
+                    tc_fence_after();
+                    if (now == 1) {
+                        // S += Y^T Wd: 128 tokens in 8 steps, hi and lo (da = 64: the second 64
+                        // lanes take whatever the buffer's second half holds, never read)
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
+                        for (int ks = 0; ks < 8; ++ks)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mma_bf16(kTS, desc(lYm + (ks * 2048 >> 4)),
-                                 desc(lWd + ((part * 32768 + ks * 2048) >> 4)), id_up, 1);
-                mma_commit(&bar.upd);
-                if (g > 0 && !(ok = wait1(&bar.read, ph ^ 1, p.err, abort))) break;
-                tc_fence_after();
-                // X S
+                            for (int part = 0; part < 2; ++part)
+                                mma_bf16(kTS, desc(lYm + (ks * 2048 >> 4)),
+                                         desc(lWd + ((part * 32768 + ks * 2048) >> 4)), id_up, 1);
+                        mma_commit(&bar.upd);
+                    } else if (now == 2) {
+                        // X S
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    if (ks == 4 && da == 64) break;
+                        for (int ks = 0; ks < 8; ++ks) {
+                            if (ks == 4 && da == 64) break;
 #pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mma_bf16(kTO2, desc(lX + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4)),
-                                 desc(lS + ((part * 32768 + ks * 2048) >> 4)), id_out,
-                                 ks + part > 0);
+                            for (int part = 0; part < 2; ++part)
+                                mma_bf16(kTO2,
+                                         desc(lX + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4)),
+                                         desc(lS + ((part * 32768 + ks * 2048) >> 4)), id_out,
+                                         ks + part > 0);
+                        }
+                        mma_commit(&bar.xs);
+                    } else {
+                        // A W: A's 16-token steps are 8 columns of hi and 8 of lo
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+                            for (int part = 0; part < 2; ++part)
+                                mma_bf16_ts(kTO1, kTA + 16 * ks + 8 * part,
+                                            desc(lW + (ks * 2048 >> 4)), id_out, ks + part > 0);
+                        mma_commit(&bar.aw);
+                    }
                 }
-                mma_commit(&bar.xs);
-                ok = wait1(&bar.a, ph, p.err, abort) && wait1(&bar.w, ph, p.err, abort);
-                if (!ok) break;
-                tc_fence_after();
-                // A W: A's 16-token steps are 8 columns of hi and 8 of lo
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-                        mma_bf16_ts(kTO1, kTA + 16 * ks + 8 * part, desc(lW + (ks * 2048 >> 4)),
-                                    id_out, ks + part > 0);
-                mma_commit(&bar.out);
             }
         }
-    } else if (warp < 4) {
+    } else if (warp < 8) {
         // ------------------------------------------------------------ A warps
-        const int q = warp;
+        const int q = warp & 3, wg = warp >> 2;
         const uint32_t at = static_cast<uint32_t>(32 * q) << 16 | kTA;
+        const float* rP = reinterpret_cast<const float*>(sm + kSRec) + 32 * q;
+        const float* rPlo = rP + 128;
+        const float* rCol = reinterpret_cast<const float*>(sm + kSRec) + 256;
         float* diag = reinterpret_cast<float*>(sm + kSDiag) + 32 * q + lane;
         uint32_t g = 0;
         bool ok = true;
@@ -395,20 +447,27 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             const Item t = item_at<true>(o, i);
             const int rev = o.calls.c[t.call].reverse;
             const bool dots = o.calls.c[t.call].dot != nullptr;
+            // (of the reversed walk every sign of a diagonal block's difference changes)
+            const float sgn = rev ? -1.f : 1.f;
             for (int k = 0; k < t.chunks; ++k, ++g) {
                 const Chunk ch = chunk_at(t, rev, k);
                 const float* r = record(o, t, ch.i);
-                const float* rP = r + kRP + 32 * q;
-                const float* rPlo = r + kRPlo + 32 * q;
                 const float4 B = __ldg(reinterpret_cast<const float4*>(r + kRB));
-                // (of the reversed walk every sign of a diagonal block's difference changes)
-                const float sgn = rev ? -1.f : 1.f;
-                const float p_hi = sgn * __ldg(rP + lane), p_lo = sgn * __ldg(rPlo + lane);
-                float to_block = rev ? __ldg(r + kRU + 32 * q + lane) : sgn * p_hi;
-                if (!wait(&bar.sc, g & 1, p.err, abort)) { ok = false; break; }
+                const float mine = __ldg(r + (rev ? kRU : kRP) + 32 * q + lane);
+                // decays of the blocks at distance 1 and 2, on the side the rows look to
+                const float b1 = rev ? (q == 0 ? B.y : B.z) : (q == 3 ? B.z : B.y);
+                const float b2 = rev ? B.z : B.y;
+                if (!wait(&bar.rec, g & 1, p.err, abort) || !wait(&bar.sc, g & 1, p.err, abort)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
+                const float p_hi = sgn * rP[lane], p_lo = sgn * rPlo[lane];
+                // blocks at distance n from the diagonal: 0 and 3, or 1 and 2 (no warp has more
+                // than two inside the triangle)
 #pragma unroll 1
-                for (int n = 0; n < 4; ++n) {  // blocks at distance n from the diagonal
+                for (int m = 0; m < 2; ++m) {
+                    const int n = wg == 0 ? 3 * m : 1 + m;
                     const int j = rev ? q + n : q - n, z = rev ? q - n : q + n;
                     if (n > 0 && z >= 0 && z < 4) {  // outside the triangle
                         uint32_t zero[32];
@@ -429,13 +488,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                             float own = 0.f;
 #pragma unroll
                             for (int c = 0; c < 32; ++c) own = c == lane ? v[c] : own;
-                            diag[128 * (g % 3)] = own;
+                            diag[128 * (g & 1)] = own;
                             in &= ~(1u << lane);
                         }
 #pragma unroll
                         for (int c4 = 0; c4 < 8; ++c4) {
-                            const float4 a = __ldg(reinterpret_cast<const float4*>(rP) + c4);
-                            const float4 b = __ldg(reinterpret_cast<const float4*>(rPlo) + c4);
+                            const float4 a = reinterpret_cast<const float4*>(rP)[c4];
+                            const float4 b = reinterpret_cast<const float4*>(rPlo)[c4];
                             const float hi[4] = {a.x, a.y, a.z, a.w}, lo[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
@@ -445,22 +504,17 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                             }
                         }
                     } else {
-                        const float rf = ex2f(to_block);
-                        to_block += j == 0 ? B.x : j == 1 ? B.y : j == 2 ? B.z : B.w;
-                        const float4* cf = reinterpret_cast<const float4*>(
-                            r + kRCol + (rev ? 128 : 0) + 32 * j);
-                        float4 f[8];
-#pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            f[c] = __ldg(cf + c);
-                            mul2(f[c].x, f[c].y, rf, rf);
-                            mul2(f[c].z, f[c].w, rf, rf);
-                        }
+                        // the row's decay up to the block, times the columns' inside it
+                        const float rf =
+                            ex2f(n == 1 ? mine : n == 2 ? mine + b1 : mine + b1 + b2);
                         landed(v);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            mul2(v[4 * c], v[4 * c + 1], f[c].x, f[c].y);
-                            mul2(v[4 * c + 2], v[4 * c + 3], f[c].z, f[c].w);
+                            float4 f = reinterpret_cast<const float4*>(rCol + 32 * j)[c];
+                            mul2(f.x, f.y, rf, rf);
+                            mul2(f.z, f.w, rf, rf);
+                            mul2(v[4 * c], v[4 * c + 1], f.x, f.y);
+                            mul2(v[4 * c + 2], v[4 * c + 3], f.z, f.w);
                         }
                         if (rev && ch.len - 32 * j < 32)
 #pragma unroll
@@ -481,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 if (lane == 0) mbar_arrive(&bar.a);
             }
         }
-    } else if (warp < 12) {
+    } else if (warp < 16) {
         // --------------------------------------- state, decayed W and outputs
-        const int q = warp & 3, wg = (warp - 4) >> 2;
+        const int q = warp & 3, wg = (warp - 8) >> 2;
         const int row = 32 * q + lane;  // token, or state row
         const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + 64 * wg;  // this warp's columns
         uint32_t g = 0;
@@ -538,20 +592,24 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             tmem_st_wait();
 
             float rowf_prev = 0.f;
-            Chunk prev{};
-            // step k: the state's copy and the decayed W of chunk k, then the outputs of chunk
-            // k - 1 while the tensor cores work on chunk k
+            Chunk prev{}, ch = chunk_at(t, rev, 0);
+            const float* r = record(o, t, ch.i);
+            float head = __ldg(r + kRHead + row), tail = __ldg(r + kRTail + row);
+            float total = __ldg(r + kRB + 4);
+            // step k: the state's copy of chunk k, the outputs of chunk k - 1 (whose products were
+            // the last to read W's buffer: chunk k's load runs meanwhile), the decayed W of chunk k
 #pragma unroll 1
             for (int k = 0; k <= t.chunks; ++k) {
-                float rowf = 0.f;
-                Chunk ch{};
+                const Chunk now = ch;
+                const float rowf = rev ? tail : head, wf = rev ? head : tail, all = ex2f(total);
                 if (k < t.chunks) {
-                    ch = chunk_at(t, rev, k);
-                    const float* r = record(o, t, ch.i);
-                    const float head = __ldg(r + kRHead + row), tail = __ldg(r + kRTail + row);
-                    const float all = ex2f(__ldg(r + kRB + 4));
-                    rowf = rev ? tail : head;
-                    const float wf = rev ? head : tail;
+                    if (k + 1 < t.chunks) {  // the next chunk's, early
+                        ch = chunk_at(t, rev, k + 1);
+                        r = record(o, t, ch.i);
+                        head = __ldg(r + kRHead + row);
+                        tail = __ldg(r + kRTail + row);
+                        total = __ldg(r + kRB + 4);
+                    }
                     // the last update of the state, the last read of its copy and of the decayed
                     // W's buffer are complete
                     if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
@@ -563,30 +621,30 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (cols) {
                         uint8_t* sr = sm + kSS + wg * 16384 + row * 128;
 #pragma unroll 1
-                        for (int b = 0; b < 2; ++b) {
-                            float S[32];
-                            tmem_ld32(at + kTS + 32 * b, S);
+                        for (int b = 0; b < 4; ++b) {
+                            float S[16];
+                            tmem_ld16(at + kTS + 16 * b, S);
                             landed(S);
                             if (holds)
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) {
+                                for (int x = 0; x < 2; ++x) {
                                     uint4 hi, lo;
                                     split2(S[8 * x], S[8 * x + 1], hi.x, lo.x);
                                     split2(S[8 * x + 2], S[8 * x + 3], hi.y, lo.y);
                                     split2(S[8 * x + 4], S[8 * x + 5], hi.z, lo.z);
                                     split2(S[8 * x + 6], S[8 * x + 7], hi.w, lo.w);
-                                    const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
+                                    const uint32_t to = ((2 * b + x) ^ (row & 7)) << 4;
                                     *reinterpret_cast<uint4*>(sr + to) = hi;
                                     *reinterpret_cast<uint4*>(sr + 32768 + to) = lo;
                                 }
-                            uint32_t u[32];
+                            uint32_t u[16];
 #pragma unroll
-                            for (int x = 0; x < 32; x += 2) {
+                            for (int x = 0; x < 16; x += 2) {
                                 mul2(S[x], S[x + 1], all, all);
                                 u[x] = __float_as_uint(S[x]);
                                 u[x + 1] = __float_as_uint(S[x + 1]);
                             }
-                            tmem_st32(at + kTS + 32 * b, u);
+                            tmem_st16(at + kTS + 16 * b, u);
                         }
                         tmem_st_wait();
                         fence_async_smem();
@@ -595,53 +653,6 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.s);
 
-                    if (!wait(&bar.w, g & 1, p.err, abort)) { ok = false; break; }
-                    const bool dead = row >= ch.len;
-                    if (cols) {
-                        uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
-                        uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
-#pragma unroll 1
-                        for (int b = 0; b < 2; ++b) {
-                            uint4 in[4];
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                in[x] = *reinterpret_cast<const uint4*>(
-                                    wr + (((4 * b + x) ^ (row & 7)) << 4));
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
-                                uint32_t hi[4], lo[4];
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) {
-                                    float a0 = __uint_as_float(w[y] << 16);
-                                    float a1 = __uint_as_float(w[y] & 0xffff0000u);
-                                    mul2(a0, a1, wf, wf);
-                                    split2(a0, a1, hi[y], lo[y]);
-                                    if (dead) hi[y] = lo[y] = 0u;
-                                }
-                                const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
-                                *reinterpret_cast<uint4*>(wd + to) =
-                                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                                *reinterpret_cast<uint4*>(wd + 32768 + to) =
-                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                            }
-                        }
-                    }
-                    if (ch.len < kC) {
-                        // rows past the segment hold another sequence's tokens (or zeros): they
-                        // must not reach a product even as 0 * inf.  (X Y^T is masked instead.)
-                        if (!wait(&bar.y, g & 1, p.err, abort)) { ok = false; break; }
-                        if (dead) {
-                            uint4* wr = reinterpret_cast<uint4*>(sm + kSW + wg * 16384 + row * 128);
-                            uint4* yr = reinterpret_cast<uint4*>(sm + kSY + wg * 16384 + row * 128);
-#pragma unroll 1
-                            for (int x = 0; x < 8; ++x) wr[x] = yr[x] = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.wd);
-                    ++g;
                 }
                 if (k > 0) {
                     // Outputs of chunk k - 1: rowf (X S) + A W.  Where their dot products with
@@ -649,8 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     // x_r . y_r w_r, which is added here in fp32 and left out of the dot: it is
                     // the same number in both of the decay's gradient's sums, where under strong
                     // decays everything else is far below its rounding.
-                    const uint32_t gg = k < t.chunks ? g - 2 : g - 1;
-                    if (!wait(&bar.out, gg & 1, p.err, abort)) { ok = false; break; }
+                    const uint32_t gg = g - 1;
+                    if (!wait(&bar.aw, gg & 1, p.err, abort) ||
+                        !wait(&bar.xs, gg & 1, p.err, abort)) {
+                        ok = false;
+                        break;
+                    }
                     tc_fence_after();
                     if (cols) {
                         const int tr = prev.t0 + row;
@@ -663,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                         const uint8_t* wr =
                             static_cast<const uint8_t*>(c.w) + ((int64_t)tr * c.w_ld + off) * 2;
                         const float dg =
-                            reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg % 3) + row];
+                            reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg & 1) + row];
                         float acc = 0.f;
 #pragma unroll 1
                         for (int b = 0; b < 4; ++b) {
@@ -710,12 +725,63 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.read);
                 }
-                prev = ch;
+                if (k < t.chunks) {
+                    if (!wait(&bar.w, g & 1, p.err, abort)) { ok = false; break; }
+                    const bool dead = row >= now.len;
+                    if (cols) {
+                        uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
+                        uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
+#pragma unroll 1
+                        for (int b = 0; b < 2; ++b) {
+                            uint4 in[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                in[x] = *reinterpret_cast<const uint4*>(
+                                    wr + (((4 * b + x) ^ (row & 7)) << 4));
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    float a0 = __uint_as_float(w[y] << 16);
+                                    float a1 = __uint_as_float(w[y] & 0xffff0000u);
+                                    mul2(a0, a1, wf, wf);
+                                    split2(a0, a1, hi[y], lo[y]);
+                                    if (dead) hi[y] = lo[y] = 0u;
+                                }
+                                const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
+                                *reinterpret_cast<uint4*>(wd + to) =
+                                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                *reinterpret_cast<uint4*>(wd + 32768 + to) =
+                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            }
+                        }
+                    }
+                    if (now.len < kC) {
+                        // rows past the segment hold another sequence's tokens (or zeros): they
+                        // must not reach a product even as 0 * inf.  (X Y^T is masked instead.)
+                        if (!wait(&bar.y, g & 1, p.err, abort)) { ok = false; break; }
+                        if (dead) {
+                            uint4* wr = reinterpret_cast<uint4*>(sm + kSW + wg * 16384 + row * 128);
+                            uint4* yr = reinterpret_cast<uint4*>(sm + kSY + wg * 16384 + row * 128);
+#pragma unroll 1
+                            for (int x = 0; x < 8; ++x) wr[x] = yr[x] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.wd);
+                    ++g;
+                }
+                prev = now;
                 rowf_prev = rowf;
             }
             if (!ok) break;
             const bool last = rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1;
-            if (last && c.S_out && cols) {  // (the outputs are complete, so the update is too)
+            if (last && c.S_out && cols) {
+                if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+                tc_fence_after();
 #pragma unroll 1
                 for (int b = 0; b < 4; ++b) {
                     float S[16];
@@ -734,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     if (bar.abort) {
         // let copies and MMAs still in flight land before leaving
         if (loads > 0) mbar_wait(load_bar, (loads - 1) & 1, nullptr);
-        if (tid == 13 * 32) {
+        if (tid == kMmaT) {
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, nullptr);
         }
