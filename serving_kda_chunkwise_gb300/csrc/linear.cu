@@ -486,7 +486,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
         DecayGrad d{};
         d.segS = at(l.seg[0]); d.segD = at(l.seg[1]);
         d.S_T = at(l.S_T); d.dS_out = a.dS_out; d.S0 = a.S0; d.dS0 = v.S_out;
-        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / (use_tc(a.io_bf16) ? 64 : kCols);
+        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kCols;
         d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
         if (a.T_total > 0) {
             ProfScope prof("linear_decay_grad_kernel", a.stream);

@@ -172,9 +172,11 @@ constexpr int kRP = 0, kRPlo = 128;   // prefix sum inside the block of 32 (log2
 constexpr int kRU = 256;              // exclusive suffix sum inside the block
 constexpr int kRHead = 384;           // 2^(sum from the chunk's start, inclusive)
 constexpr int kRTail = 512;           // 2^(sum to the chunk's end, exclusive)
-constexpr int kRCol = 640;            // 2^U, then 2^P: column factors, forward and reversed
-constexpr int kRB = 896;              // the four blocks' sums, their total
-constexpr int kRec = 928;
+// column factors, forward then reversed: for the blocks beside the diagonal (2^U, 2^P) and for
+// the diagonal's (2^-P, 2^P)
+constexpr int kRCol = 640;
+constexpr int kRB = 1152;             // the four blocks' sums, their total
+constexpr int kRec = 1184;
 
 __device__ __forceinline__ const float* record(const OutParams& o, const Item& t, int chunk) {
     return o.rec + ((size_t)(t.slot * (o.p.L / kC) + chunk) * o.p.H + t.h) * kRec;
@@ -233,7 +235,8 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
         r[kRHead + i] = ex2f(P[b] + before[b]);
         r[kRTail + i] = ex2f(U[b] + after[b]);
         r[kRCol + i] = ex2f(U[b]);
-        r[kRCol + 128 + i] = ex2f(P[b]);
+        r[kRCol + 128 + i] = ex2f(-P[b]);
+        r[kRCol + 256 + i] = r[kRCol + 384 + i] = ex2f(P[b]);
     }
     if (lane == 0) {
         *reinterpret_cast<float4*>(r + kRB) = make_float4(B[0], B[1], B[2], B[3]);
@@ -258,9 +261,8 @@ constexpr int kTmaWarp = 16, kMmaT = 17 * 32;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
 constexpr uint32_t kSWd = 98304;             // decayed W: hi, lo
 constexpr uint32_t kSS = kSWd + 65536;       // state: hi, lo
-constexpr uint32_t kSRec = kSS + 65536;      // the record's P, Plo and column factors
-constexpr uint32_t kSDiag = kSRec + 1536;    // diagonals of X Y^T, two chunks of 128 floats
-constexpr uint32_t kSBar = kSDiag + 1024;
+constexpr uint32_t kSRec = kSS + 65536;      // the record's column factors
+constexpr uint32_t kSBar = kSRec + 1024;
 constexpr uint32_t kOutSmem = kSBar + 256;
 static_assert(kOutSmem <= 232448, "shared-memory limit");
 // TMEM columns (all 512 are allocated, so the base address is 0): X Y^T / A, A W, X S, state
@@ -271,7 +273,7 @@ struct OutBars {
     uint64_t sc, a;          // X Y^T complete; A written (8 arrivals)
     uint64_t s, wd;          // state and its copy written; decayed W written (8 arrivals each)
     uint64_t upd, xs, aw;    // state update, X S, A W complete
-    uint64_t read;           // the chunk's outputs read (8 arrivals)
+    uint64_t read;           // the chunk's outputs read (16 arrivals)
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -297,9 +299,8 @@ __device__ __noinline__ int load_operand(const OutParams& o, const CUtensorMap* 
             const Chunk ch = chunk_at(t, c.reverse, k);
             if (which == 3) {
                 const float* r = record(o, t, ch.i);
-                mbar_expect_tx(full, 1536);
-                bulk_g2s(dst, r + kRP, 1024, full);
-                bulk_g2s(dst + 1024, r + kRCol + (c.reverse ? 128 : 0), 512, full);
+                mbar_expect_tx(full, 1024);
+                bulk_g2s(dst, r + kRCol + (c.reverse ? 256 : 0), 1024, full);
                 continue;
             }
             mbar_expect_tx(full, blocks * 16384);
@@ -309,6 +310,74 @@ __device__ __noinline__ int load_operand(const OutParams& o, const CUtensorMap* 
         }
     }
     return g;
+}
+
+// Outputs of one chunk (t0, len), 32 columns from `col` of one row a lane: rowf (X S) + A W, and
+// their dot products with another row where wanted.  A warp's 32 rows are its TMEM lanes; out of
+// line, for both groups of warps call it.
+__device__ __noinline__ bool write_out(const OutParams& o, OutBars& bar, uint32_t phase, int call,
+                                       int h, int t0, int len, float rowf, int col) {
+    const Call& c = o.calls.c[call];
+    const int row = threadIdx.x & 127;
+    const int tr = t0 + row;
+    const bool cols = col < c.db;
+    const bool in = cols && row < len, dots = c.dot != nullptr;
+    uint4 d[4];
+    if (in && dots) {  // on the way while the products are waited for
+        const uint4* dr = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(c.dot) + (int64_t)tr * c.dot_ld + h * c.db + col);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) d[x] = __ldg(dr + x);
+    }
+    if (!wait(&bar.aw, phase, o.p.err, &bar.abort) || !wait(&bar.xs, phase, o.p.err, &bar.abort))
+        return false;
+    tc_fence_after();
+    if (cols) {
+        __nv_bfloat16* out =
+            static_cast<__nv_bfloat16*>(c.out) + ((int64_t)tr * o.p.H + h) * c.db + col;
+        const uint32_t at = (static_cast<uint32_t>(row & 96) << 16) + col;
+        float acc = 0.f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            float o1[16], o2[16];
+            tmem_ld16(at + kTO1 + 16 * b, o1);
+            tmem_ld16(at + kTO2 + 16 * b, o2);
+            landed(o1);
+            landed(o2);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) o1[x] = fmaf(rowf, o2[x], o1[x]);
+            if (!in) continue;
+            uint4 u[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float* v = o1 + 8 * x;
+                u[x] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+            }
+            if (o.wide_store) {
+                st_global_32(out + 16 * b, u[0], u[1]);
+            } else {
+                reinterpret_cast<uint4*>(out)[2 * b] = u[0];
+                reinterpret_cast<uint4*>(out)[2 * b + 1] = u[1];
+            }
+            if (dots)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint4 e = d[2 * b + x];
+                    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        acc = fmaf(o1[8 * x + 2 * y], __uint_as_float(w[y] << 16), acc);
+                        acc = fmaf(o1[8 * x + 2 * y + 1], __uint_as_float(w[y] & 0xffff0000u), acc);
+                    }
+                }
+        }
+        if (in && dots) c.dots[((int64_t)(col >> 5) * o.p.T + tr) * o.p.H + h] = acc;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.read);
+    return true;
 }
 
 __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant__ OutParams o) {
@@ -322,8 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         uint64_t* one[] = {&bar.x,  &bar.y,   &bar.w,  &bar.rec, &bar.sc,
                            &bar.upd, &bar.xs, &bar.aw, &bar.drain};
         for (uint64_t* b : one) mbar_init(b, 1);
-        uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd, &bar.read};
+        uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd};
         for (uint64_t* b : eight) mbar_init(b, 8);
+        mbar_init(&bar.read, 16);
         fence_mbar_init();
         bar.abort = 0;
     }
@@ -437,32 +507,29 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         // ------------------------------------------------------------ A warps
         const int q = warp & 3, wg = warp >> 2;
         const uint32_t at = static_cast<uint32_t>(32 * q) << 16 | kTA;
-        const float* rP = reinterpret_cast<const float*>(sm + kSRec) + 32 * q;
-        const float* rPlo = rP + 128;
-        const float* rCol = reinterpret_cast<const float*>(sm + kSRec) + 256;
-        float* diag = reinterpret_cast<float*>(sm + kSDiag) + 32 * q + lane;
+        const float* rCol = reinterpret_cast<const float*>(sm + kSRec);
+        const int row = 32 * q + lane;
         uint32_t g = 0;
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item t = item_at<true>(o, i);
             const int rev = o.calls.c[t.call].reverse;
-            const bool dots = o.calls.c[t.call].dot != nullptr;
-            // (of the reversed walk every sign of a diagonal block's difference changes)
-            const float sgn = rev ? -1.f : 1.f;
             for (int k = 0; k < t.chunks; ++k, ++g) {
                 const Chunk ch = chunk_at(t, rev, k);
                 const float* r = record(o, t, ch.i);
                 const float4 B = __ldg(reinterpret_cast<const float4*>(r + kRB));
-                const float mine = __ldg(r + (rev ? kRU : kRP) + 32 * q + lane);
+                const float mine = __ldg(r + (rev ? kRU : kRP) + row);
+                const float p_hi = __ldg(r + kRP + row), p_lo = __ldg(r + kRPlo + row);
+                const float rowf = __ldg(r + (rev ? kRTail : kRHead) + row);
                 // decays of the blocks at distance 1 and 2, on the side the rows look to
                 const float b1 = rev ? (q == 0 ? B.y : B.z) : (q == 3 ? B.z : B.y);
                 const float b2 = rev ? B.z : B.y;
+                const float bq = q == 0 ? B.x : q == 1 ? B.y : q == 2 ? B.z : B.w;
                 if (!wait(&bar.rec, g & 1, p.err, abort) || !wait(&bar.sc, g & 1, p.err, abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float p_hi = sgn * rP[lane], p_lo = sgn * rPlo[lane];
                 // blocks at distance n from the diagonal: 0 and 3, or 1 and 2 (no warp has more
                 // than two inside the triangle)
 #pragma unroll 1
@@ -478,49 +545,45 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (j < 0 || j > 3) continue;
                     float v[32];
                     tmem_ld32(at + 32 * j, v);
-                    if (n == 0) {
-                        // columns of the triangle that are tokens of the segment
-                        uint32_t in = rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
-                        const int rest = ch.len - 32 * q;
-                        if (rev && rest < 32) in &= rest > 0 ? (1u << rest) - 1u : 0u;
-                        landed(v);
-                        if (dots) {
-                            float own = 0.f;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) own = c == lane ? v[c] : own;
-                            diag[128 * (g & 1)] = own;
-                            in &= ~(1u << lane);
-                        }
-#pragma unroll
-                        for (int c4 = 0; c4 < 8; ++c4) {
-                            const float4 a = reinterpret_cast<const float4*>(rP)[c4];
-                            const float4 b = reinterpret_cast<const float4*>(rPlo)[c4];
-                            const float hi[4] = {a.x, a.y, a.z, a.w}, lo[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                const int c = 4 * c4 + x;
-                                const float d = fmaf(-sgn, hi[x], p_hi) + fmaf(-sgn, lo[x], p_lo);
-                                v[c] = in & (1u << c) ? v[c] * ex2f(d) : 0.f;
-                            }
-                        }
-                    } else {
-                        // the row's decay up to the block, times the columns' inside it
-                        const float rf =
-                            ex2f(n == 1 ? mine : n == 2 ? mine + b1 : mine + b1 + b2);
+                    // Columns that count: all of a block beside the diagonal but those past the
+                    // segment, on the diagonal those of the triangle.
+                    uint32_t in = 0xffffffffu;
+                    if (rev && ch.len - 32 * j < 32)
+                        in = ch.len > 32 * j ? (1u << (ch.len - 32 * j)) - 1u : 0u;
+                    if (n == 0) in &= rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
+                    if (n > 0 || bq > -24.f) {
+                        // The row's decay up to the block times the columns' inside it.  On the
+                        // diagonal these are 2^P_r and 2^-P_i (reversed: 2^-P_r, 2^P_i), at most
+                        // 2^24, whose errors (2^-23 times the exponents) stay below 2e-6.
+                        const float rf = n == 0 ? ex2f(rev ? -p_hi : p_hi)
+                                                : ex2f(n == 1   ? mine
+                                                       : n == 2 ? mine + b1
+                                                                : mine + b1 + b2);
+                        const float4* cf =
+                            reinterpret_cast<const float4*>(rCol + (n == 0 ? 128 : 0) + 32 * j);
                         landed(v);
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
-                            float4 f = reinterpret_cast<const float4*>(rCol + 32 * j)[c];
+                            float4 f = cf[c];
                             mul2(f.x, f.y, rf, rf);
                             mul2(f.z, f.w, rf, rf);
                             mul2(v[4 * c], v[4 * c + 1], f.x, f.y);
                             mul2(v[4 * c + 2], v[4 * c + 3], f.z, f.w);
                         }
-                        if (rev && ch.len - 32 * j < 32)
+                    } else {
+                        // strong decays: the difference of the prefix sums, kept in two floats
+                        landed(v);
+                        const float sgn = rev ? -1.f : 1.f;
 #pragma unroll
-                            for (int c = 0; c < 32; ++c)
-                                if (32 * j + c >= ch.len) v[c] = 0.f;
+                        for (int c = 0; c < 32; ++c) {
+                            const float hi = __shfl_sync(0xffffffffu, p_hi, c);
+                            const float lo = __shfl_sync(0xffffffffu, p_lo, c);
+                            v[c] *= ex2f(sgn * ((p_hi - hi) + (p_lo - lo)));
+                        }
                     }
+                    if (n == 0 || in != 0xffffffffu)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) v[c] = in & (1u << c) ? v[c] : 0.f;
                     uint32_t u[32];  // each 16-token step: 8 columns of hi, 8 of lo
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
@@ -533,6 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.a);
+                // the second half of its 64 output columns (the state warps write the first)
+                ok = write_out(o, bar, g & 1, t.call, t.h, ch.t0, ch.len, rowf, 64 * wg + 32);
+                if (!ok) break;
             }
         }
     } else if (warp < 16) {
@@ -655,75 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 
                 }
                 if (k > 0) {
-                    // Outputs of chunk k - 1: rowf (X S) + A W.  Where their dot products with
-                    // another row are wanted, A W comes without the diagonal's term
-                    // x_r . y_r w_r, which is added here in fp32 and left out of the dot: it is
-                    // the same number in both of the decay's gradient's sums, where under strong
-                    // decays everything else is far below its rounding.
-                    const uint32_t gg = g - 1;
-                    if (!wait(&bar.aw, gg & 1, p.err, abort) ||
-                        !wait(&bar.xs, gg & 1, p.err, abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    if (cols) {
-                        const int tr = prev.t0 + row;
-                        const int off = t.h * c.db + 64 * wg;
-                        const bool in = row < prev.len;
-                        uint8_t* out = static_cast<uint8_t*>(c.out) +
-                                       ((int64_t)tr * p.H * c.db + off) * 2;
-                        const uint8_t* dr = static_cast<const uint8_t*>(c.dot) +
-                                            ((int64_t)tr * c.dot_ld + off) * 2;
-                        const uint8_t* wr =
-                            static_cast<const uint8_t*>(c.w) + ((int64_t)tr * c.w_ld + off) * 2;
-                        const float dg =
-                            reinterpret_cast<const float*>(sm + kSDiag)[128 * (gg & 1) + row];
-                        float acc = 0.f;
-#pragma unroll 1
-                        for (int b = 0; b < 4; ++b) {
-                            float o1[16], o2[16];
-                            tmem_ld16(at + kTO1 + 16 * b, o1);
-                            tmem_ld16(at + kTO2 + 16 * b, o2);
-                            landed(o1);
-                            landed(o2);
-#pragma unroll
-                            for (int x = 0; x < 16; ++x) o1[x] = fmaf(rowf_prev, o2[x], o1[x]);
-                            if (in && c.dot) {
-#pragma unroll
-                                for (int h8 = 0; h8 < 2; ++h8) {
-                                    float d[8], w[8];
-                                    ld8(dr + 32 * b + 16 * h8, d);
-                                    ld8(wr + 32 * b + 16 * h8, w);
-#pragma unroll
-                                    for (int x = 0; x < 8; ++x) {
-                                        acc = fmaf(o1[8 * h8 + x], d[x], acc);
-                                        o1[8 * h8 + x] = fmaf(dg, w[x], o1[8 * h8 + x]);
-                                    }
-                                }
-                            }
-                            if (in) {
-                                uint4 u[2];
-#pragma unroll
-                                for (int x = 0; x < 2; ++x)
-                                    u[x] = make_uint4(pack_bf16x2(o1[8 * x], o1[8 * x + 1]),
-                                                      pack_bf16x2(o1[8 * x + 2], o1[8 * x + 3]),
-                                                      pack_bf16x2(o1[8 * x + 4], o1[8 * x + 5]),
-                                                      pack_bf16x2(o1[8 * x + 6], o1[8 * x + 7]));
-                                if (o.wide_store) {
-                                    st_global_32(out + 32 * b, u[0], u[1]);
-                                } else {
-                                    reinterpret_cast<uint4*>(out)[2 * b] = u[0];
-                                    reinterpret_cast<uint4*>(out)[2 * b + 1] = u[1];
-                                }
-                            }
-                        }
-                        if (in && c.dot)
-                            c.dots[((int64_t)wg * p.T + tr) * p.H + t.h] = acc;
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.read);
+                    ok = write_out(o, bar, (g - 1) & 1, t.call, t.h, prev.t0, prev.len, rowf_prev,
+                                   64 * wg);
+                    if (!ok) break;
                 }
                 if (k < t.chunks) {
                     if (!wait(&bar.w, g & 1, p.err, abort)) { ok = false; break; }
