@@ -323,6 +323,7 @@ bool use_tc(int io_bf16) {
 // Tokens a segment: short enough that the segments of all heads fill the GPU a few times, no
 // shorter than the edge states' traffic (two fp32 states a segment) is worth.
 int segment_length(int64_t T, int H, bool tc, bool bwd) {
+    if (tc && T <= 512) return 512;  // one launch: four chunks take less than two more launches
     int L = tc ? 128 : 64;
     while (L < (tc && !bwd ? 2048 : 1024) && T / L * H > 4 * 152) L *= 2;
     return L;

@@ -247,17 +247,17 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
 // -------------------------------------------------------------- outputs --
 // Persistent, one CTA an SM.  Roles: warps 0..7 turn X Y^T into A (hi + lo over the product's own
 // TMEM columns, so that A never leaves tensor memory); warps 8..15 decay W, keep the state's copy
-// and write the outputs; lanes of warp 16 load X, Y, W and the decays, one thread of warp 17
-// issues the MMAs, each chunk's three sets in the order in which their operands get ready.  Warp w
-// reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in fp32; X S reads its bf16
+// and write the outputs; a thread each of warps 16..18 loads X and the decays, Y, and W (as lanes
+// of one warp they held each other up by up to 2500 cycles), one of warp 19 issues the MMAs, each
+// chunk's three sets in the order in which their operands get ready.  Warp w reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in fp32; X S reads its bf16
 // hi + lo copy in shared memory.
 // Shared memory holds one chunk of X, Y and W (32 KB each), the decayed W and the state's copy (64
 // KB each): no second stage fits, but each operand is reloaded as soon as its last product is
 // done, and while one waits the others' products run.  (Two stages fit with 64 of the db columns
 // to a CTA; that form made A twice and its N = 64 products run at 75 % of N = 128's rate, and was
 // slower.)
-constexpr int kThreads = 576;
-constexpr int kTmaWarp = 16, kMmaT = 17 * 32;
+constexpr int kThreads = 640;
+constexpr int kMmaT = 19 * 32;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
 constexpr uint32_t kSWd = 98304;             // decayed W: hi, lo
 constexpr uint32_t kSS = kSWd + 65536;       // state: hi, lo
@@ -280,12 +280,15 @@ struct OutBars {
 };
 static_assert(sizeof(OutBars) <= 256, "barrier area");
 
-// One operand's loads (0: X, 1: Y, 2: W, 3: decays), by one thread: chunk after chunk, each once
-// `freed` (and `freed2`) say that the last chunk's buffer has been read.  Returns the number of
-// chunks loaded.
-__device__ __noinline__ int load_operand(const OutParams& o, const CUtensorMap* maps, int which,
-                                         uint8_t* dst, uint64_t* full, uint64_t* freed,
-                                         uint64_t* freed2, volatile int* abort) {
+// One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each once
+// the last chunk's buffer has been read.  Returns the number of chunks loaded.
+__device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int which, uint8_t* sm) {
+    const CUtensorMap* maps = which == 0 ? o.x : which == 1 ? o.y : o.w;
+    uint8_t* dst = sm + (which == 0 ? kSX : which == 1 ? kSY : kSW);
+    uint64_t* full = which == 0 ? &bar.x : which == 1 ? &bar.y : &bar.w;
+    uint64_t* freed = which == 0 ? &bar.xs : which == 1 ? &bar.upd : &bar.aw;
+    volatile int* abort = &bar.abort;
+    unsigned* err = o.p.err;
     const uint32_t items = item_count(o);
     int g = 0;
     for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
@@ -293,20 +296,24 @@ __device__ __noinline__ int load_operand(const OutParams& o, const CUtensorMap* 
         const Call& c = o.calls.c[t.call];
         const int blocks = (which == 2 ? c.db : c.da) / 64;
         for (int k = 0; k < t.chunks; ++k, ++g) {
-            if (g > 0 && (!wait1(freed, (g - 1) & 1, o.p.err, abort) ||
-                          (freed2 && !wait1(freed2, (g - 1) & 1, o.p.err, abort))))
-                return g;
+            const uint32_t last = (g - 1) & 1;
+            if (g > 0 && !wait1(freed, last, err, abort)) return g;
+            if (which == 2 && g > 0 && !wait1(&bar.wd, last, err, abort)) return g;
             const Chunk ch = chunk_at(t, c.reverse, k);
-            if (which == 3) {
-                const float* r = record(o, t, ch.i);
-                mbar_expect_tx(full, 1024);
-                bulk_g2s(dst, r + kRCol + (c.reverse ? 256 : 0), 1024, full);
-                continue;
-            }
             mbar_expect_tx(full, blocks * 16384);
+            // (the next chunk's on its way into L2)
+            const int ahead = chunk_at(t, c.reverse, k + 1).t0;
 #pragma unroll 1
-            for (int b = 0; b < blocks; ++b)
+            for (int b = 0; b < blocks; ++b) {
                 tma_load_3d(dst + b * 16384, maps + t.call, 64 * b, t.h, ch.t0, full);
+                if (k + 1 < t.chunks) tma_prefetch_3d(maps + t.call, 64 * b, t.h, ahead);
+            }
+            if (which == 0) {
+                if (g > 0 && !wait1(&bar.a, last, err, abort)) return g + 1;
+                mbar_expect_tx(&bar.rec, 1024);
+                bulk_g2s(sm + kSRec, record(o, t, ch.i) + kRCol + (c.reverse ? 256 : 0), 1024,
+                         &bar.rec);
+            }
         }
     }
     return g;
@@ -403,18 +410,10 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t items = item_count(o);
-    int loads = 0;  // of this thread (for the way out of an abort)
-    uint64_t* load_bar = nullptr;
+    int loads = 0;  // chunks loaded by this thread (for the way out of an abort)
 
-    if (warp == kTmaWarp) {
-        if (lane < 4) {
-            load_bar = lane == 0 ? &bar.x : lane == 1 ? &bar.y : lane == 2 ? &bar.w : &bar.rec;
-            loads = load_operand(
-                o, lane == 0 ? o.x : lane == 1 ? o.y : o.w, lane,
-                sm + (lane == 0 ? kSX : lane == 1 ? kSY : lane == 2 ? kSW : kSRec), load_bar,
-                lane == 0 ? &bar.xs : lane == 1 ? &bar.upd : lane == 2 ? &bar.aw : &bar.a,
-                lane == 2 ? &bar.wd : nullptr, abort);
-        }
+    if (warp >= 16 && warp < 19) {
+        if (lane == 0) loads = load_operand(o, bar, warp - 16, sm);
     } else if (tid == kMmaT) {
         // ------------------------------------------------------- MMA thread
         constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
@@ -729,7 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (!wait(&bar.w, g & 1, p.err, abort)) { ok = false; break; }
                     const bool dead = row >= now.len;
                     if (cols) {
-                        uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
+                        const uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
                         uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
 #pragma unroll 1
                         for (int b = 0; b < 2; ++b) {
@@ -738,6 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                             for (int x = 0; x < 4; ++x)
                                 in[x] = *reinterpret_cast<const uint4*>(
                                     wr + (((4 * b + x) ^ (row & 7)) << 4));
+                            if (dead)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) in[x] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
@@ -748,7 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                                     float a1 = __uint_as_float(w[y] & 0xffff0000u);
                                     mul2(a0, a1, wf, wf);
                                     split2(a0, a1, hi[y], lo[y]);
-                                    if (dead) hi[y] = lo[y] = 0u;
                                 }
                                 const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
                                 *reinterpret_cast<uint4*>(wd + to) =
@@ -799,7 +800,12 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     __syncthreads();
     if (bar.abort) {
         // let copies and MMAs still in flight land before leaving
-        if (loads > 0) mbar_wait(load_bar, (loads - 1) & 1, nullptr);
+        if (loads > 0) {
+            mbar_wait(warp == 16 ? &bar.x : warp == 17 ? &bar.y : &bar.w, (loads - 1) & 1, nullptr);
+            // (where the abort came before the last chunk's decays were asked for, this wait runs
+            // out, by when those of the chunk before have landed)
+            if (warp == 16) mbar_wait(&bar.rec, (loads - 1) & 1, nullptr);
+        }
         if (tid == kMmaT) {
             mma_commit(&bar.drain);
             mbar_wait(&bar.drain, 0, nullptr);
