@@ -76,6 +76,23 @@ __device__ __forceinline__ void landed(float (&v)[16]) {
                  :
                  : "memory");
 }
+__device__ __forceinline__ void landed(float (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                   "+f"(v[6]), "+f"(v[7])
+                 :
+                 : "memory");
+}
+// Warp-collective: 8 consecutive fp32 columns of this warp's 32 TMEM lanes.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+    uint32_t r[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void landed(float (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
@@ -129,11 +146,10 @@ struct Item {
 struct OutParams {
     Problem p;
     lin::Calls calls;
-    CUtensorMap x[lin::kMaxCalls], y[lin::kMaxCalls], w[lin::kMaxCalls];
+    CUtensorMap x[lin::kMaxCalls], y[lin::kMaxCalls], w[lin::kMaxCalls], out[lin::kMaxCalls];
     int n_calls;
     int slots;
     const float* rec;  // decay records, see decay_kernel
-    int wide_store;    // every output row piece is 32-byte aligned
 };
 
 __device__ __forceinline__ uint32_t item_count(const OutParams& o) {
@@ -172,10 +188,9 @@ constexpr int kRP = 0, kRPlo = 128;   // prefix sum inside the block of 32 (log2
 constexpr int kRU = 256;              // exclusive suffix sum inside the block
 constexpr int kRHead = 384;           // 2^(sum from the chunk's start, inclusive)
 constexpr int kRTail = 512;           // 2^(sum to the chunk's end, exclusive)
-// column factors, forward then reversed: for the blocks beside the diagonal (2^U, 2^P) and for
-// the diagonal's (2^-P, 2^P)
-constexpr int kRCol = 640;
-constexpr int kRB = 1152;             // the four blocks' sums, their total
+// forward, then reversed: column factors for the blocks beside the diagonal (2^U, 2^P) and for
+// the diagonal's (2^-P, 2^P), the four blocks' sums, their total
+constexpr int kRCol = 640, kRB = 256, kRDir = 264;
 constexpr int kRec = 1184;
 
 __device__ __forceinline__ const float* record(const OutParams& o, const Item& t, int chunk) {
@@ -236,11 +251,12 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
         r[kRTail + i] = ex2f(U[b] + after[b]);
         r[kRCol + i] = ex2f(U[b]);
         r[kRCol + 128 + i] = ex2f(-P[b]);
-        r[kRCol + 256 + i] = r[kRCol + 384 + i] = ex2f(P[b]);
+        r[kRCol + kRDir + i] = r[kRCol + kRDir + 128 + i] = ex2f(P[b]);
     }
-    if (lane == 0) {
-        *reinterpret_cast<float4*>(r + kRB) = make_float4(B[0], B[1], B[2], B[3]);
-        r[kRB + 4] = (B[0] + B[1]) + (B[2] + B[3]);
+    if (lane < 2) {
+        float* s = r + kRCol + lane * kRDir + kRB;
+        *reinterpret_cast<float4*>(s) = make_float4(B[0], B[1], B[2], B[3]);
+        s[4] = (B[0] + B[1]) + (B[2] + B[3]);
     }
 }
 
@@ -261,8 +277,9 @@ constexpr int kMmaT = 19 * 32;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
 constexpr uint32_t kSWd = 98304;             // decayed W: hi, lo
 constexpr uint32_t kSS = kSWd + 65536;       // state: hi, lo
-constexpr uint32_t kSRec = kSS + 65536;      // the record's column factors
-constexpr uint32_t kSBar = kSRec + 1024;
+constexpr uint32_t kSRec = kSS + 65536;      // the record's part for the call's direction
+constexpr uint32_t kSItem = kSRec + 1088;    // the 16 warps' items, 12 words each
+constexpr uint32_t kSBar = kSItem + 768;
 constexpr uint32_t kOutSmem = kSBar + 256;
 static_assert(kOutSmem <= 232448, "shared-memory limit");
 // TMEM columns (all 512 are allocated, so the base address is 0): X Y^T / A, A W, X S, state
@@ -273,7 +290,8 @@ struct OutBars {
     uint64_t sc, a;          // X Y^T complete; A written (8 arrivals)
     uint64_t s, wd;          // state and its copy written; decayed W written (8 arrivals each)
     uint64_t upd, xs, aw;    // state update, X S, A W complete
-    uint64_t read;           // the chunk's outputs read (16 arrivals)
+    uint64_t read;           // the chunk's outputs read from TMEM (16 arrivals)
+    uint64_t staged, stored; // ... and staged (16 arrivals); the stage read by the store
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -281,7 +299,8 @@ struct OutBars {
 static_assert(sizeof(OutBars) <= 256, "barrier area");
 
 // One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each once
-// the last chunk's buffer has been read.  Returns the number of chunks loaded.
+// the last chunk's buffer has been read.  W's also stores the outputs, for it is idle then.
+// Returns the number of chunks loaded.
 __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int which, uint8_t* sm) {
     const CUtensorMap* maps = which == 0 ? o.x : which == 1 ? o.y : o.w;
     uint8_t* dst = sm + (which == 0 ? kSX : which == 1 ? kSY : kSW);
@@ -290,6 +309,19 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
     volatile int* abort = &bar.abort;
     unsigned* err = o.p.err;
     const uint32_t items = item_count(o);
+    int call = 0, h = 0, t0 = -1;  // the last chunk's outputs: t0 < 0 where rows were written
+    auto store = [&](uint32_t phase) {
+        if (!wait1(&bar.staged, phase, err, abort)) return false;
+        if (t0 >= 0) {
+#pragma unroll 1
+            for (int b = 0; b < o.calls.c[call].db / 64; ++b)
+                tma_store_3d(&o.out[call], sm + kSWd + b * 16384, 64 * b, h, t0);
+            bulk_commit();
+            bulk_wait_read0();
+        }
+        mbar_arrive(&bar.stored);
+        return true;
+    };
     int g = 0;
     for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
         const Item t = item_at<false>(o, i);
@@ -301,89 +333,223 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
             if (which == 2 && g > 0 && !wait1(&bar.wd, last, err, abort)) return g;
             const Chunk ch = chunk_at(t, c.reverse, k);
             mbar_expect_tx(full, blocks * 16384);
-            // (the next chunk's on its way into L2)
-            const int ahead = chunk_at(t, c.reverse, k + 1).t0;
 #pragma unroll 1
-            for (int b = 0; b < blocks; ++b) {
+            for (int b = 0; b < blocks; ++b)
                 tma_load_3d(dst + b * 16384, maps + t.call, 64 * b, t.h, ch.t0, full);
-                if (k + 1 < t.chunks) tma_prefetch_3d(maps + t.call, 64 * b, t.h, ahead);
+            if (which == 2) {
+                if (g > 0 && !store(last)) return g + 1;
+                call = t.call;
+                h = t.h;
+                t0 = ch.len == kC ? ch.t0 : -1;
             }
             if (which == 0) {
                 if (g > 0 && !wait1(&bar.a, last, err, abort)) return g + 1;
-                mbar_expect_tx(&bar.rec, 1024);
-                bulk_g2s(sm + kSRec, record(o, t, ch.i) + kRCol + (c.reverse ? 256 : 0), 1024,
-                         &bar.rec);
+                mbar_expect_tx(&bar.rec, 4 * kRDir);
+                bulk_g2s(sm + kSRec, record(o, t, ch.i) + kRCol + (c.reverse ? kRDir : 0),
+                         4 * kRDir, &bar.rec);
             }
         }
     }
+    if (which == 2 && g > 0) store((g - 1) & 1);
     return g;
 }
 
-// Outputs of one chunk (t0, len), 32 columns from `col` of one row a lane: rowf (X S) + A W, and
-// their dot products with another row where wanted.  A warp's 32 rows are its TMEM lanes; out of
-// line, for both groups of warps call it.
-__device__ __noinline__ bool write_out(const OutParams& o, OutBars& bar, uint32_t phase, int call,
-                                       int h, int t0, int len, float rowf, int col) {
-    const Call& c = o.calls.c[call];
+// States in memory and in TMEM, 64 columns from `col` by a warp; out of line, once an item.
+struct StateAt {
+    int64_t at, cs;  // this lane's row from column col, the step between columns
+    bool holds;
+};
+__device__ __forceinline__ StateAt state_at(const OutParams& o, const Call& c, int which, int h,
+                                            int col) {
     const int row = threadIdx.x & 127;
-    const int tr = t0 + row;
-    const bool cols = col < c.db;
-    const bool in = cols && row < len, dots = c.dot != nullptr;
-    uint4 d[4];
-    if (in && dots) {  // on the way while the products are waited for
-        const uint4* dr = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(c.dot) + (int64_t)tr * c.dot_ld + h * c.db + col);
+    StateAt s;
+    s.cs = c.tr ? c.da : 1;
+    s.at = ((int64_t)which * o.p.H + h) * c.da * c.db + (int64_t)row * (c.tr ? 1 : c.db) +
+           col * s.cs;
+    s.holds = col < c.db && row < c.da;
+    return s;
+}
+// which >= 0: sequence `which`'s own state at its edge (zeros without one), else the edge state
+// of the segment in slot -1 - which.
+__device__ __noinline__ void load_state(const OutParams& o, int call, int which, int h, int col) {
+    const Call& c = o.calls.c[call];
+    const StateAt s = state_at(o, c, which < 0 ? -1 - which : which, h, col);
+    const float* from = which < 0 ? c.seg : c.edge;
+    const uint32_t to = ((threadIdx.x & 96u) << 16) + kTS + col;
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {
+        uint32_t u[32];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) d[x] = __ldg(dr + x);
+        for (int x = 0; x < 32; ++x) u[x] = 0u;
+        if (from && s.holds) {
+            const float* f = from + s.at + 32 * b * s.cs;
+            if (c.tr) {
+#pragma unroll
+                for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(__ldcg(f + x * s.cs));
+            } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(f) + x);
+                    u[4 * x] = v.x;
+                    u[4 * x + 1] = v.y;
+                    u[4 * x + 2] = v.z;
+                    u[4 * x + 3] = v.w;
+                }
+            }
+        }
+        tmem_st32(to + 32 * b, u);
     }
-    if (!wait(&bar.aw, phase, o.p.err, &bar.abort) || !wait(&bar.xs, phase, o.p.err, &bar.abort))
+    tmem_st_wait();
+}
+__device__ __noinline__ void store_state(const OutParams& o, int call, int n, int h, int col) {
+    const Call& c = o.calls.c[call];
+    if (c.S_out == nullptr) return;
+    const StateAt s = state_at(o, c, n, h, col);
+    const uint32_t from = ((threadIdx.x & 96u) << 16) + kTS + col;
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        float v[16];
+        tmem_ld16(from + 16 * b, v);
+        landed(v);
+        if (s.holds)
+#pragma unroll
+            for (int x = 0; x < 16; ++x) c.S_out[s.at + (16 * b + x) * s.cs] = v[x];
+    }
+}
+__device__ __noinline__ void pass_state(const OutParams& o, int call, int n, int h, int col) {
+    const Call& c = o.calls.c[call];
+    const StateAt s = state_at(o, c, n, h, col);
+    if (c.S_out && s.holds)
+#pragma unroll 1
+        for (int x = 0; x < 64; ++x)
+            c.S_out[s.at + x * s.cs] = c.edge ? c.edge[s.at + x * s.cs] : 0.f;
+}
+
+// What a warp's chunks need of its item, kept in shared memory: the roles' registers are few, and
+// what the compiler would put into local memory comes back from L2 (shared memory takes all of L1).
+struct View {
+    volatile int* v;
+    enum { kBegin, kEnd, kChunks, kCall, kH, kRev, kRecord, kEdge, kFinal, kWords };
+    __device__ __forceinline__ int chunks() const { return v[kChunks]; }
+    __device__ __forceinline__ int call() const { return v[kCall]; }
+    __device__ __forceinline__ int h() const { return v[kH]; }
+    __device__ __forceinline__ int rev() const { return v[kRev]; }
+    __device__ __forceinline__ Chunk chunk(int k) const {
+        Chunk c;
+        c.i = v[kRev] ? v[kChunks] - 1 - k : k;
+        c.t0 = v[kBegin] + c.i * kC;
+        c.len = min(v[kEnd] - c.t0, kC);
+        return c;
+    }
+    __device__ __forceinline__ const float* record(const OutParams& o, int k) const {
+        const int i = v[kRev] ? v[kChunks] - 1 - k : k;
+        return o.rec + ((size_t)(v[kRecord] + i) * o.p.H + v[kH]) * kRec;
+    }
+};
+// Whole warps: the item's facts for the warp's chunks.
+__device__ __noinline__ void open_item(const OutParams& o, uint32_t i, View w) {
+    const Item t = item_at<true>(o, i);
+    const int rev = o.calls.c[t.call].reverse;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        w.v[View::kBegin] = t.sg.begin;
+        w.v[View::kEnd] = t.sg.end;
+        w.v[View::kChunks] = t.chunks;
+        w.v[View::kCall] = t.call;
+        w.v[View::kH] = t.h;
+        w.v[View::kRev] = rev;
+        w.v[View::kRecord] = t.slot * (o.p.L / kC);
+        // where the state comes from: load_state()'s argument; an empty sequence's first slot
+        // passes the state on (kChunks = 0, kFinal >= 0)
+        w.v[View::kEdge] = t.sg.count > 1 ? -1 - t.slot : t.sg.n;
+        const bool last = t.sg.live ? (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1)
+                                    : t.sg.count == 0 && t.sg.s == 0;
+        w.v[View::kFinal] = last ? t.sg.n : -1;  // whose final state follows, if any
+    }
+    __syncwarp();
+}
+
+// Outputs of one chunk, 32 columns from `col` of one row a lane: rowf (X S) + A W, and
+// their dot products with another row where wanted.  Whole chunks are staged in the decayed W's
+// buffer (whose product is complete, and which the next chunk's overwrites only once its W is
+// there) and stored by TMA: written row by row from the lanes they kept the load/store unit busy
+// for 2000 cycles.  A warp's 32 rows are its TMEM lanes; out of
+// line, for both groups of warps call it.
+__device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint8_t* sm,
+                                          uint32_t phase, View it, int k, float rowf, int col) {
+    const int row = threadIdx.x & 127;
+    if (!wait(&bar.aw, phase, o.p.err, &bar.abort) ||
+        !wait(&bar.xs, phase, o.p.err, &bar.abort) ||
+        !wait(&bar.upd, phase, o.p.err, &bar.abort))
         return false;
     tc_fence_after();
-    if (cols) {
-        __nv_bfloat16* out =
-            static_cast<__nv_bfloat16*>(c.out) + ((int64_t)tr * o.p.H + h) * c.db + col;
-        const uint32_t at = (static_cast<uint32_t>(row & 96) << 16) + col;
-        float acc = 0.f;
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            float o1[16], o2[16];
-            tmem_ld16(at + kTO1 + 16 * b, o1);
-            tmem_ld16(at + kTO2 + 16 * b, o2);
+    const Call& c = o.calls.c[it.call()];
+    const int db = c.db, h = it.h();
+    const Chunk ch = it.chunk(k);
+    const int tr = ch.t0 + row;
+    const bool cols = col < db;
+    const bool in = cols && row < ch.len, dots = c.dot != nullptr;
+    const uint32_t from = (static_cast<uint32_t>(row & 96) << 16) + col;
+    float acc = 0.f;
+#pragma unroll 1
+    for (int b = 0; b < 2; ++b) {  // 16 columns at a time, to stay within the registers
+        uint4 d[2];
+        if (in && dots) {
+            const uint4* dr = reinterpret_cast<const uint4*>(
+                static_cast<const __nv_bfloat16*>(c.dot) + (int64_t)tr * c.dot_ld + h * db + col);
+            d[0] = __ldg(dr + 2 * b);
+            d[1] = __ldg(dr + 2 * b + 1);
+        }
+        float o1[16];
+        if (cols) {
+            float o2[8];
+            tmem_ld16(from + kTO1 + 16 * b, o1);
+            tmem_ld8(from + kTO2 + 16 * b, o2);
             landed(o1);
             landed(o2);
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o1[x] = fmaf(rowf, o2[x], o1[x]);
-            if (!in) continue;
-            uint4 u[2];
+            for (int x = 0; x < 8; ++x) o1[x] = fmaf(rowf, o2[x], o1[x]);
+            tmem_ld8(from + kTO2 + 16 * b + 8, o2);
+            landed(o2);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o1[8 + x] = fmaf(rowf, o2[x], o1[8 + x]);
+        }
+        if (b == 1) {  // the accumulators may be written again
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.read);
+        }
+        if (!in) continue;
+        uint8_t* stage = sm + kSWd + (col >> 6) * 16384 + row * 128;
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.out) +
+                                              ((int64_t)tr * o.p.H + h) * db + col + 16 * b);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const float* w = o1 + 8 * x;
+            const uint4 u = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
+                                       pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
+            if (ch.len < kC)  // (a stored tile would reach into the next sequence)
+                out[x] = u;
+            else
+                *reinterpret_cast<uint4*>(
+                    stage + ((((col & 32) >> 3) + 2 * b + x) ^ (row & 7)) * 16) = u;
+        }
+        if (dots) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const float* v = o1 + 8 * x;
-                u[x] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-            }
-            if (o.wide_store) {
-                st_global_32(out + 16 * b, u[0], u[1]);
-            } else {
-                reinterpret_cast<uint4*>(out)[2 * b] = u[0];
-                reinterpret_cast<uint4*>(out)[2 * b + 1] = u[1];
-            }
-            if (dots)
+                const uint32_t w[4] = {d[x].x, d[x].y, d[x].z, d[x].w};
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint4 e = d[2 * b + x];
-                    const uint32_t w[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        acc = fmaf(o1[8 * x + 2 * y], __uint_as_float(w[y] << 16), acc);
-                        acc = fmaf(o1[8 * x + 2 * y + 1], __uint_as_float(w[y] & 0xffff0000u), acc);
-                    }
+                for (int y = 0; y < 4; ++y) {
+                    acc = fmaf(o1[8 * x + 2 * y], __uint_as_float(w[y] << 16), acc);
+                    acc = fmaf(o1[8 * x + 2 * y + 1], __uint_as_float(w[y] & 0xffff0000u), acc);
                 }
+            }
         }
-        if (in && dots) c.dots[((int64_t)(col >> 5) * o.p.T + tr) * o.p.H + h] = acc;
     }
-    tc_fence_before();
+    if (in && dots) c.dots[((int64_t)(col >> 5) * o.p.T + tr) * o.p.H + h] = acc;
+    fence_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.read);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.staged);
     return true;
 }
 
@@ -401,6 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd};
         for (uint64_t* b : eight) mbar_init(b, 8);
         mbar_init(&bar.read, 16);
+        mbar_init(&bar.staged, 16);
+        mbar_init(&bar.stored, 1);
         fence_mbar_init();
         bar.abort = 0;
     }
@@ -413,7 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     int loads = 0;  // chunks loaded by this thread (for the way out of an abort)
 
     if (warp >= 16 && warp < 19) {
-        if (lane == 0) loads = load_operand(o, bar, warp - 16, sm);
+        if (lane == 0) {
+            loads = load_operand(o, bar, warp - 16, sm);
+            bulk_wait0();  // (its stores, if any, are complete)
+        }
     } else if (tid == kMmaT) {
         // ------------------------------------------------------- MMA thread
         constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
@@ -508,22 +679,30 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         const uint32_t at = static_cast<uint32_t>(32 * q) << 16 | kTA;
         const float* rCol = reinterpret_cast<const float*>(sm + kSRec);
         const int row = 32 * q + lane;
+        const View it{reinterpret_cast<volatile int*>(sm + kSItem) + 12 * warp};
         uint32_t g = 0;
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at<true>(o, i);
-            const int rev = o.calls.c[t.call].reverse;
-            for (int k = 0; k < t.chunks; ++k, ++g) {
-                const Chunk ch = chunk_at(t, rev, k);
-                const float* r = record(o, t, ch.i);
-                const float4 B = __ldg(reinterpret_cast<const float4*>(r + kRB));
-                const float mine = __ldg(r + (rev ? kRU : kRP) + row);
-                const float p_hi = __ldg(r + kRP + row), p_lo = __ldg(r + kRPlo + row);
-                const float rowf = __ldg(r + (rev ? kRTail : kRHead) + row);
-                // decays of the blocks at distance 1 and 2, on the side the rows look to
-                const float b1 = rev ? (q == 0 ? B.y : B.z) : (q == 3 ? B.z : B.y);
-                const float b2 = rev ? B.z : B.y;
-                const float bq = q == 0 ? B.x : q == 1 ? B.y : q == 2 ? B.z : B.w;
+            open_item(o, i, it);
+            // the row's prefix sum inside its block and its sum to the edge of the block that it
+            // looks to, loaded a chunk ahead (from memory they take 2500 cycles)
+            float hi_next = 0.f, edge_next = 0.f;
+            if (it.chunks()) {
+                const float* r = it.record(o, 0);
+                hi_next = __ldg(r + kRP + row);
+                edge_next = __ldg(r + (it.rev() ? kRU : kRP) + row);
+            }
+#pragma unroll 1
+            for (int k = 0; k < it.chunks(); ++k, ++g) {
+                const int rev = it.rev();
+                const int len = it.chunk(k).len;
+                const float p_hi = hi_next, edge = edge_next;
+                const float rowf = __ldg(it.record(o, k) + (rev ? kRTail : kRHead) + row);
+                if (k + 1 < it.chunks()) {
+                    const float* r = it.record(o, k + 1);
+                    hi_next = __ldg(r + kRP + row);
+                    edge_next = __ldg(r + (rev ? kRU : kRP) + row);
+                }
                 if (!wait(&bar.rec, g & 1, p.err, abort) || !wait(&bar.sc, g & 1, p.err, abort)) {
                     ok = false;
                     break;
@@ -547,17 +726,17 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     // Columns that count: all of a block beside the diagonal but those past the
                     // segment, on the diagonal those of the triangle.
                     uint32_t in = 0xffffffffu;
-                    if (rev && ch.len - 32 * j < 32)
-                        in = ch.len > 32 * j ? (1u << (ch.len - 32 * j)) - 1u : 0u;
+                    if (rev && len - 32 * j < 32)
+                        in = len > 32 * j ? (1u << (len - 32 * j)) - 1u : 0u;
                     if (n == 0) in &= rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
-                    if (n > 0 || bq > -24.f) {
+                    if (n > 0 || rCol[kRB + q] > -24.f) {
                         // The row's decay up to the block times the columns' inside it.  On the
                         // diagonal these are 2^P_r and 2^-P_i (reversed: 2^-P_r, 2^P_i), at most
                         // 2^24, whose errors (2^-23 times the exponents) stay below 2e-6.
-                        const float rf = n == 0 ? ex2f(rev ? -p_hi : p_hi)
-                                                : ex2f(n == 1   ? mine
-                                                       : n == 2 ? mine + b1
-                                                                : mine + b1 + b2);
+                        float x = n == 0 ? (rev ? -p_hi : p_hi) : edge;
+                        if (n > 1) x += rCol[kRB + (rev ? q + 1 : q - 1)];
+                        if (n > 2) x += rCol[kRB + (rev ? q + 2 : q - 2)];
+                        const float rf = ex2f(x);
                         const float4* cf =
                             reinterpret_cast<const float4*>(rCol + (n == 0 ? 128 : 0) + 32 * j);
                         landed(v);
@@ -572,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     } else {
                         // strong decays: the difference of the prefix sums, kept in two floats
                         landed(v);
-                        const float sgn = rev ? -1.f : 1.f;
+                        const float sgn = rev ? -1.f : 1.f, p_lo = __ldg(it.record(o, k) + kRPlo + row);
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
                             const float hi = __shfl_sync(0xffffffffu, p_hi, c);
@@ -583,20 +762,21 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (n == 0 || in != 0xffffffffu)
 #pragma unroll
                         for (int c = 0; c < 32; ++c) v[c] = in & (1u << c) ? v[c] : 0.f;
-                    uint32_t u[32];  // each 16-token step: 8 columns of hi, 8 of lo
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int k2 = 16 * (c >> 3) + (c & 7);
-                        split2(v[2 * c], v[2 * c + 1], u[k2], u[k2 + 8]);
+                    for (int hf = 0; hf < 2; ++hf) {  // a 16-token step: 8 columns of hi, 8 of lo
+                        uint32_t u[16];
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            split2(v[16 * hf + 2 * c], v[16 * hf + 2 * c + 1], u[c], u[c + 8]);
+                        tmem_st16(at + 32 * j + 16 * hf, u);
                     }
-                    tmem_st32(at + 32 * j, u);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.a);
                 // the second half of its 64 output columns (the state warps write the first)
-                ok = write_out(o, bar, g & 1, t.call, t.h, ch.t0, ch.len, rowf, 64 * wg + 32);
+                ok = write_out(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32);
                 if (!ok) break;
             }
         }
@@ -604,76 +784,48 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         // --------------------------------------- state, decayed W and outputs
         const int q = warp & 3, wg = (warp - 8) >> 2;
         const int row = 32 * q + lane;  // token, or state row
+        const View it{reinterpret_cast<volatile int*>(sm + kSItem) + 12 * warp};
         const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + 64 * wg;  // this warp's columns
         uint32_t g = 0;
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at<true>(o, i);
-            const Call& c = o.calls.c[t.call];
-            const int rev = c.reverse;
-            const bool cols = 64 * wg < c.db;  // this warp has columns
-            const int64_t E = (int64_t)c.da * c.db;
-            const int64_t rs = c.tr ? 1 : c.db, cs = c.tr ? c.da : 1;
-            const int64_t mine = (int64_t)row * rs + (int64_t)(64 * wg) * cs;
-            const int64_t seq = ((int64_t)t.sg.n * p.H + t.h) * E + mine;
-            const bool holds = cols && row < c.da;  // this lane has a state row
-            if (!t.sg.live) {
+            open_item(o, i, it);
+            if (it.chunks() == 0) {
                 // an empty sequence owns its first slot: its final state is its initial one
-                if (c.S_out && t.sg.count == 0 && t.sg.s == 0 && holds)
-#pragma unroll 1
-                    for (int x = 0; x < 64; ++x)
-                        c.S_out[seq + x * cs] = c.edge ? c.edge[seq + x * cs] : 0.f;
+                if (it.v[View::kFinal] >= 0)
+                    pass_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg);
                 continue;
             }
-            const float* from =
-                t.sg.count > 1 ? c.seg + ((int64_t)t.slot * p.H + t.h) * E + mine
-                               : c.edge ? c.edge + seq : nullptr;
+            const bool cols = 64 * wg < o.calls.c[it.call()].db;          // this warp has columns
+            const bool holds = cols && row < o.calls.c[it.call()].da;     // this lane a state row
             // the segment's edge state into TMEM, once the last segment's is done with
             if (g > 0 && !wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
             tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
-                uint32_t u[32];
-#pragma unroll
-                for (int x = 0; x < 32; ++x) u[x] = 0u;
-                if (from && holds) {
-                    if (c.tr) {
-#pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            u[x] = __float_as_uint(__ldcg(from + (32 * b + x) * cs));
-                    } else {
-#pragma unroll
-                        for (int x = 0; x < 8; ++x) {
-                            const uint4 f = __ldcg(reinterpret_cast<const uint4*>(from) + 8 * b + x);
-                            u[4 * x] = f.x;
-                            u[4 * x + 1] = f.y;
-                            u[4 * x + 2] = f.z;
-                            u[4 * x + 3] = f.w;
-                        }
-                    }
-                }
-                tmem_st32(at + kTS + 32 * b, u);
-            }
-            tmem_st_wait();
+            load_state(o, it.call(), it.v[View::kEdge], it.h(), 64 * wg);
 
-            float rowf_prev = 0.f;
-            Chunk prev{}, ch = chunk_at(t, rev, 0);
-            const float* r = record(o, t, ch.i);
-            float head = __ldg(r + kRHead + row), tail = __ldg(r + kRTail + row);
-            float total = __ldg(r + kRB + 4);
-            // step k: the state's copy of chunk k, the outputs of chunk k - 1 (whose products were
-            // the last to read W's buffer: chunk k's load runs meanwhile), the decayed W of chunk k
+            float rowf_prev = 0.f, head, tail, total;
+            {
+                const float* r = it.record(o, 0);
+                head = __ldg(r + kRHead + row);
+                tail = __ldg(r + kRTail + row);
+                total = __ldg(r + kRCol + kRB + 4);
+            }
+            // step k: the outputs of chunk k - 1 (its products were the last to read W's buffer, so
+            // chunk k's load runs meanwhile), the state's copy and the decayed W of chunk k
 #pragma unroll 1
-            for (int k = 0; k <= t.chunks; ++k) {
-                const Chunk now = ch;
+            for (int k = 0; k <= it.chunks(); ++k) {
+                const int rev = it.rev();
                 const float rowf = rev ? tail : head, wf = rev ? head : tail, all = ex2f(total);
-                if (k < t.chunks) {
-                    if (k + 1 < t.chunks) {  // the next chunk's, early
-                        ch = chunk_at(t, rev, k + 1);
-                        r = record(o, t, ch.i);
+                if (k > 0) {
+                    ok = write_out(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev, 64 * wg);
+                    if (!ok) break;
+                }
+                if (k < it.chunks()) {
+                    if (k + 1 < it.chunks()) {  // the next chunk's, early
+                        const float* r = it.record(o, k + 1);
                         head = __ldg(r + kRHead + row);
                         tail = __ldg(r + kRTail + row);
-                        total = __ldg(r + kRB + 4);
+                        total = __ldg(r + kRCol + kRB + 4);
                     }
                     // the last update of the state, the last read of its copy and of the decayed
                     // W's buffer are complete
@@ -719,14 +871,14 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (lane == 0) mbar_arrive(&bar.s);
 
                 }
-                if (k > 0) {
-                    ok = write_out(o, bar, (g - 1) & 1, t.call, t.h, prev.t0, prev.len, rowf_prev,
-                                   64 * wg);
-                    if (!ok) break;
-                }
-                if (k < t.chunks) {
-                    if (!wait(&bar.w, g & 1, p.err, abort)) { ok = false; break; }
-                    const bool dead = row >= now.len;
+                if (k < it.chunks()) {
+                    if (!wait(&bar.w, g & 1, p.err, abort) ||
+                        (g > 0 && !wait(&bar.stored, (g - 1) & 1, p.err, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    const int len = it.chunk(k).len;
+                    const bool dead = row >= len;
                     if (cols) {
                         const uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
                         uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
@@ -759,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                             }
                         }
                     }
-                    if (now.len < kC) {
+                    if (len < kC) {
                         // rows past the segment hold another sequence's tokens (or zeros): they
                         // must not reach a product even as 0 * inf.  (X Y^T is masked instead.)
                         if (!wait(&bar.y, g & 1, p.err, abort)) { ok = false; break; }
@@ -775,23 +927,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (lane == 0) mbar_arrive(&bar.wd);
                     ++g;
                 }
-                prev = now;
                 rowf_prev = rowf;
             }
             if (!ok) break;
-            const bool last = rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1;
-            if (last && c.S_out && cols) {
+            if (it.v[View::kFinal] >= 0) {
                 if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-#pragma unroll 1
-                for (int b = 0; b < 4; ++b) {
-                    float S[16];
-                    tmem_ld16(at + kTS + 16 * b, S);
-                    landed(S);
-                    if (holds)
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) c.S_out[seq + (16 * b + x) * cs] = S[x];
-                }
+                store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg);
                 tc_fence_before();
             }
         }
@@ -936,7 +1078,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                 const Chunk ch = chunk_at(t, !rev, k);
                 const float* r = record(o, t, ch.i);
                 const float wf = __ldg(r + (rev ? kRHead : kRTail) + row) * ex2f(between);
-                between += __ldg(r + kRB + 4);
+                between += __ldg(r + kRCol + kRB + 4);
                 if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 uint8_t* stage = sm + st * kUStage;
                 const bool dead = row >= ch.len;
@@ -1071,12 +1213,11 @@ cudaError_t fill(OutParams& o, const Problem& p, const lin::Calls& calls, int n,
     o.n_calls = n;
     o.slots = (int)slots;
     o.rec = rec;
-    o.wide_store = 1;
     for (int i = 0; i < n; ++i) {
         const Call& c = calls.c[i];
-        if (reinterpret_cast<uintptr_t>(c.out) & 31) o.wide_store = 0;
         if (p.T == 0) continue;
-        if ((out && !make_map(&o.x[i], c.x, p.T, p.H, c.da, c.x_ld)) ||
+        if ((out && (!make_map(&o.x[i], c.x, p.T, p.H, c.da, c.x_ld) ||
+                     !make_map(&o.out[i], c.out, p.T, p.H, c.db, (int64_t)p.H * c.db))) ||
             !make_map(&o.y[i], c.y, p.T, p.H, c.da, c.y_ld) ||
             !make_map(&o.w[i], c.w, p.T, p.H, c.db, c.w_ld))
             return cudaErrorInvalidValue;
