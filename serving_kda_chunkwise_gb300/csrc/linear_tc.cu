@@ -336,6 +336,12 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
 #pragma unroll 1
             for (int b = 0; b < blocks; ++b)
                 tma_load_3d(dst + b * 16384, maps + t.call, 64 * b, t.h, ch.t0, full);
+            if (which == 2 && k + 1 < t.chunks) {  // its load is waited for longest: into L2 early
+                const int ahead = chunk_at(t, c.reverse, k + 1).t0;
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b)
+                    tma_prefetch_3d(maps + t.call, 64 * b, t.h, ahead);
+            }
             if (which == 2) {
                 if (g > 0 && !store(last)) return g + 1;
                 call = t.call;
@@ -697,7 +703,6 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 const int rev = it.rev();
                 const int len = it.chunk(k).len;
                 const float p_hi = hi_next, edge = edge_next;
-                const float rowf = __ldg(it.record(o, k) + (rev ? kRTail : kRHead) + row);
                 if (k + 1 < it.chunks()) {
                     const float* r = it.record(o, k + 1);
                     hi_next = __ldg(r + kRP + row);
@@ -721,53 +726,55 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                         tmem_st32(at + 32 * z, zero);
                     }
                     if (j < 0 || j > 3) continue;
-                    float v[32];
-                    tmem_ld32(at + 32 * j, v);
                     // Columns that count: all of a block beside the diagonal but those past the
                     // segment, on the diagonal those of the triangle.
                     uint32_t in = 0xffffffffu;
                     if (rev && len - 32 * j < 32)
                         in = len > 32 * j ? (1u << (len - 32 * j)) - 1u : 0u;
                     if (n == 0) in &= rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
-                    if (n > 0 || rCol[kRB + q] > -24.f) {
-                        // The row's decay up to the block times the columns' inside it.  On the
-                        // diagonal these are 2^P_r and 2^-P_i (reversed: 2^-P_r, 2^P_i), at most
-                        // 2^24, whose errors (2^-23 times the exponents) stay below 2e-6.
-                        float x = n == 0 ? (rev ? -p_hi : p_hi) : edge;
-                        if (n > 1) x += rCol[kRB + (rev ? q + 1 : q - 1)];
-                        if (n > 2) x += rCol[kRB + (rev ? q + 2 : q - 2)];
-                        const float rf = ex2f(x);
-                        const float4* cf =
-                            reinterpret_cast<const float4*>(rCol + (n == 0 ? 128 : 0) + 32 * j);
+                    // The row's decay up to the block times the columns' inside it.  On the
+                    // diagonal these are 2^P_r and 2^-P_i (reversed: 2^-P_r, 2^P_i), at most 2^24,
+                    // whose errors (2^-23 times the exponents) stay below 2e-6.
+                    const bool strong = n == 0 && !(rCol[kRB + q] > -24.f);
+                    float x = n == 0 ? (rev ? -p_hi : p_hi) : edge;
+                    if (n > 1) x += rCol[kRB + (rev ? q + 1 : q - 1)];
+                    if (n > 2) x += rCol[kRB + (rev ? q + 2 : q - 2)];
+                    const float rf = ex2f(x);
+                    const float* cf = rCol + (n == 0 ? 128 : 0) + 32 * j;
+#pragma unroll 1
+                    for (int hf = 0; hf < 2; ++hf) {  // 16 columns, a step of A W
+                        float v[16];
+                        tmem_ld16(at + 32 * j + 16 * hf, v);
                         landed(v);
+                        if (!strong) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            float4 f = cf[c];
-                            mul2(f.x, f.y, rf, rf);
-                            mul2(f.z, f.w, rf, rf);
-                            mul2(v[4 * c], v[4 * c + 1], f.x, f.y);
-                            mul2(v[4 * c + 2], v[4 * c + 3], f.z, f.w);
+                            for (int c = 0; c < 4; ++c) {
+                                float4 f = reinterpret_cast<const float4*>(cf + 16 * hf)[c];
+                                mul2(f.x, f.y, rf, rf);
+                                mul2(f.z, f.w, rf, rf);
+                                mul2(v[4 * c], v[4 * c + 1], f.x, f.y);
+                                mul2(v[4 * c + 2], v[4 * c + 3], f.z, f.w);
+                            }
+                        } else {
+                            // strong decays: the difference of the prefix sums, kept in two floats
+                            const float sgn = rev ? -1.f : 1.f;
+                            const float p_lo = __ldg(it.record(o, k) + kRPlo + row);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const float hi = __shfl_sync(0xffffffffu, p_hi, 16 * hf + c);
+                                const float lo = __shfl_sync(0xffffffffu, p_lo, 16 * hf + c);
+                                v[c] *= ex2f(sgn * ((p_hi - hi) + (p_lo - lo)));
+                            }
                         }
-                    } else {
-                        // strong decays: the difference of the prefix sums, kept in two floats
-                        landed(v);
-                        const float sgn = rev ? -1.f : 1.f, p_lo = __ldg(it.record(o, k) + kRPlo + row);
+                        if (n == 0 || in != 0xffffffffu) {
+                            const uint32_t part = in >> (16 * hf);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float hi = __shfl_sync(0xffffffffu, p_hi, c);
-                            const float lo = __shfl_sync(0xffffffffu, p_lo, c);
-                            v[c] *= ex2f(sgn * ((p_hi - hi) + (p_lo - lo)));
+                            for (int c = 0; c < 16; ++c) v[c] = part & (1u << c) ? v[c] : 0.f;
                         }
-                    }
-                    if (n == 0 || in != 0xffffffffu)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) v[c] = in & (1u << c) ? v[c] : 0.f;
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {  // a 16-token step: 8 columns of hi, 8 of lo
-                        uint32_t u[16];
+                        uint32_t u[16];  // 8 columns of hi, 8 of lo
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
-                            split2(v[16 * hf + 2 * c], v[16 * hf + 2 * c + 1], u[c], u[c + 8]);
+                            split2(v[2 * c], v[2 * c + 1], u[c], u[c + 8]);
                         tmem_st16(at + 32 * j + 16 * hf, u);
                     }
                 }
@@ -776,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.a);
                 // the second half of its 64 output columns (the state warps write the first)
+                const float rowf = __ldg(it.record(o, k) + (it.rev() ? kRTail : kRHead) + row);
                 ok = write_out(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32);
                 if (!ok) break;
             }
@@ -810,23 +818,31 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 tail = __ldg(r + kRTail + row);
                 total = __ldg(r + kRCol + kRB + 4);
             }
-            // step k: the outputs of chunk k - 1 (its products were the last to read W's buffer, so
-            // chunk k's load runs meanwhile), the state's copy and the decayed W of chunk k
+            // step k: the outputs of chunk k - 1 and the state's copy of chunk k, then chunk k's
+            // decayed W (the outputs' products were the last to read W's buffer, so its load runs
+            // meanwhile)
 #pragma unroll 1
             for (int k = 0; k <= it.chunks(); ++k) {
                 const int rev = it.rev();
                 const float rowf = rev ? tail : head, wf = rev ? head : tail, all = ex2f(total);
-                if (k > 0) {
-                    ok = write_out(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev, 64 * wg);
-                    if (!ok) break;
+                if (k + 1 < it.chunks()) {  // the next chunk's, early
+                    const float* r = it.record(o, k + 1);
+                    head = __ldg(r + kRHead + row);
+                    tail = __ldg(r + kRTail + row);
+                    total = __ldg(r + kRCol + kRB + 4);
                 }
-                if (k < it.chunks()) {
-                    if (k + 1 < it.chunks()) {  // the next chunk's, early
-                        const float* r = it.record(o, k + 1);
-                        head = __ldg(r + kRHead + row);
-                        tail = __ldg(r + kRTail + row);
-                        total = __ldg(r + kRCol + kRB + 4);
+                // first whichever of the two has its products complete
+                const bool outputs_first =
+                    k == it.chunks() ||
+                    (k > 0 && __all_sync(0xffffffffu, test(&bar.aw, (g - 1) & 1)));
+#pragma unroll 1
+                for (int part = 0; ok && part < 2; ++part) {
+                    if ((part == 0) == outputs_first) {
+                        if (k > 0)
+                            ok = write_out(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev, 64 * wg);
+                        continue;
                     }
+                    if (k == it.chunks()) continue;
                     // the last update of the state, the last read of its copy and of the decayed
                     // W's buffer are complete
                     if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
@@ -869,8 +885,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.s);
-
                 }
+                if (!ok) break;
                 if (k < it.chunks()) {
                     if (!wait(&bar.w, g & 1, p.err, abort) ||
                         (g > 0 && !wait(&bar.stored, (g - 1) & 1, p.err, abort))) {
