@@ -8,10 +8,12 @@
 // Streaming work: each element is read and written once (backward: x and dy read, dx written).
 // A row (one token and head) of d channels is covered by d / 8 lanes with 8 channels each
 // (16-byte loads for bf16), so a warp holds 2 (d = 128) or 4 (d = 64) rows at a time and the
-// row sums are shuffle reductions.  A warp's task is one token and up to kUnroll row groups of
-// that token's heads, so the token's cosines and sines are loaded once a task.  The partner of
-// a channel in the (p, p + rot/2) pairing sits in another lane (rot is a multiple of 16, so
-// whole lanes pair up) and comes by shuffle; in the interleaved pairing it sits in the same lane.
+// row sums are shuffle reductions.  A warp's task is one token's queries or keys, some or all of
+// its heads, in groups of 1 or 2 times that many rows, the next group's rows on their way while
+// one is worked on: the token's position and its row of the table, two dependent loads, are then
+// paid once a task.  The partner of a channel
+// in the (p, p + rot/2) pairing sits in another lane (rot is a multiple of 16, so whole lanes pair
+// up) and comes by shuffle; in the interleaved pairing it sits in the same lane.
 // All sums and the rotation are fp32; the only rounding to fewer bits is that of the result.
 // y may be x: a lane reads its 8 channels before it writes them and no other lane reads them.
 #include "kda_common.cuh"
@@ -21,27 +23,47 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kUnroll = 4;
 constexpr int kMaxBwdBlocks = 152 * 4;
 
-template <typename IO>
-__device__ __forceinline__ void load8(const IO* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(w[e] << 16);
-        v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-    }
-}
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+
+// 8 channels as they are in memory, loaded ahead of their use.
+template <typename IO>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        a = __ldcs(reinterpret_cast<const uint4*>(p));
+    }
+    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
 
 template <typename IO>
 __device__ __forceinline__ void store8(IO* p, const float (&v)[8]);
@@ -139,125 +161,131 @@ __device__ __forceinline__ float row_sum(float x) {
     return x;
 }
 
+struct Side {  // queries or keys
+    const void *x, *dy;
+    int64_t ld;
+    const float* w;
+    void* out;     // backward: dx
+    int H;
+    int parts;     // warps a token's rows are split over
+    int64_t warps; // of the launch that work on this side
+};
+
 struct NormArgs {
-    const void *q, *k, *dyq, *dyk;
-    int64_t q_ld, k_ld;
-    const float *wq, *wk;
+    Side side[2];
     float eps;
     const float* cos_sin;
     int64_t n_pos;
     const int32_t* positions;
     int rot;
-    void *q_out, *k_out;  // backward: dq, dk
     float* part;          // backward: [blocks][2][D] partial weight gradients, or nullptr
     int64_t T;
-    int Hq, Hk;
     unsigned* err;
 };
 
 template <int D, typename IO, bool kInter, bool kBwd>
-__global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
+    const __grid_constant__ NormArgs a) {
     constexpr int kLanes = D / 8;
     constexpr int kRows = 32 / kLanes;         // rows a warp holds at a time
-    constexpr int kGroup = kRows * kUnroll;    // rows of a task
+    constexpr int kUnroll = kBwd ? 1 : 2;
+    constexpr int kGroup = kRows * kUnroll;    // rows of a group
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % kLanes, sub = lane / kLanes;
-    const int nq = (a.Hq + kGroup - 1) / kGroup;
-    const int per_token = nq + (a.Hk + kGroup - 1) / kGroup;
-    const int64_t tasks = a.T * per_token;
-    float dwq[8], dwk[8];
+    int64_t id = (int64_t)blockIdx.x * kWarps + warp;
+    const bool is_k = id >= a.side[0].warps;
+    const Side& s = a.side[is_k ? 1 : 0];
+    if (is_k) id -= a.side[0].warps;
+    const int H = s.H, groups = (H + kGroup - 1) / kGroup;
+    const int per_part = (groups + s.parts - 1) / s.parts;
+    const int64_t tasks = id < s.warps ? a.T * s.parts : 0;
+    float dw[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
+    for (int e = 0; e < 8; ++e) dw[e] = 0.f;
 
-    for (int64_t task = (int64_t)blockIdx.x * kWarps + warp; task < tasks;
-         task += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = task / per_token;
-        const int grp = (int)(task - t * per_token);
-        const bool is_k = grp >= nq;
-        const int H = is_k ? a.Hk : a.Hq;
-        const int h0 = (is_k ? grp - nq : grp) * kGroup + sub;
-        const IO* x = static_cast<const IO*>(is_k ? a.k : a.q) + t * (is_k ? a.k_ld : a.q_ld) + 8 * l;
-        const IO* dy = static_cast<const IO*>(is_k ? a.dyk : a.dyq) + t * H * D + 8 * l;
-        IO* y = static_cast<IO*>(is_k ? a.k_out : a.q_out) + t * H * D + 8 * l;
-        const float* wp = is_k ? a.wk : a.wq;
+    for (int64_t task = id; task < tasks; task += s.warps) {
+        const int64_t t = s.parts == 1 ? task : task / s.parts;
+        const int g0 = s.parts == 1 ? 0 : (int)(task - t * s.parts) * per_part;
+        const int g1 = min(g0 + per_part, groups);
+        const IO* xp = static_cast<const IO*>(s.x) + t * s.ld + 8 * l;
+        const int64_t own = t * H * D + 8 * l;
 
-        float v[kUnroll][8], u[kBwd ? kUnroll : 1][8];
+        Raw<IO> x[kUnroll], dy[kBwd ? kUnroll : 1];
+        auto fetch = [&](int g) {
 #pragma unroll
-        for (int m = 0; m < kUnroll; ++m) {
-            const int h = h0 + m * kRows;
-            if (h < H) {
-                load8(x + (int64_t)h * D, v[m]);
-                if (kBwd) load8(dy + (int64_t)h * D, u[m]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[m][e] = 0.f;
-                    if (kBwd) u[m][e] = 0.f;
+            for (int m = 0; m < kUnroll; ++m) {
+                const int h = g * kGroup + m * kRows + sub;
+                x[m].zero();
+                if (kBwd) dy[m].zero();
+                if (h < H) {
+                    x[m].load(xp + h * D);
+                    if (kBwd) dy[m].load(static_cast<const IO*>(s.dy) + own + h * D);
                 }
             }
-        }
+        };
+        if (g0 < g1) fetch(g0);
         const Turn r = load_turn<D, kInter>(a.cos_sin, a.n_pos, a.positions, a.rot, t, lane, a.err);
-        float w[8];
-        if (wp)
-            load8(wp + 8 * l, w);
-        else
+        for (int g = g0; g < g1; ++g) {
+            float v[kUnroll][8], u[kBwd ? kUnroll : 1][8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.f;
-        float add[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) add[e] = 0.f;
-#pragma unroll
-        for (int m = 0; m < kUnroll; ++m) {
-            const int h = h0 + m * kRows;
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(v[m][e], v[m][e], ss);
-            const float rms = sqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-            const float rinv = 1.f / rms;
-            if (!kBwd) {
-                float n[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) n[e] = v[m][e] * rinv * w[e];
-                turn<kInter>(r, 1.f, a.rot, n);
-                if (h < H) store8(y + (int64_t)h * D, n);
-            } else {
-                turn<kInter>(r, -1.f, a.rot, u[m]);
-                float dot = 0.f;
-                const bool live = h < H;  // (a dead row with eps = 0 would give 0 * inf)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float hat = v[m][e] * rinv;
-                    if (live) add[e] = fmaf(u[m][e], hat, add[e]);
-                    u[m][e] *= w[e];
-                    dot = fmaf(u[m][e], hat, dot);
-                }
-                dot = row_sum<D>(dot) * (1.f / D);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) u[m][e] = rinv * (u[m][e] - v[m][e] * rinv * dot);
-                if (live) store8(y + (int64_t)h * D, u[m]);
+            for (int m = 0; m < kUnroll; ++m) {
+                x[m].get(v[m]);
+                if (kBwd) dy[m].get(u[m]);
             }
-        }
-        if (kBwd) {
-            if (is_k)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) dwk[e] += add[e];
+            if (g + 1 < g1) fetch(g + 1);
+            float w[8];
+            if (s.w)
+                load8(s.w + 8 * l, w);
             else
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dwq[e] += add[e];
+                for (int e = 0; e < 8; ++e) w[e] = 1.f;
+#pragma unroll
+            for (int m = 0; m < kUnroll; ++m) {
+                const int h = g * kGroup + m * kRows + sub;
+                IO* y = static_cast<IO*>(s.out) + own + h * D;
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(v[m][e], v[m][e], ss);
+                const float rms = sqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
+                const float rinv = 1.f / rms;
+                if (!kBwd) {
+                    float n[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) n[e] = v[m][e] * rinv * w[e];
+                    turn<kInter>(r, 1.f, a.rot, n);
+                    if (h < H) store8(y, n);
+                } else {
+                    turn<kInter>(r, -1.f, a.rot, u[m]);
+                    float dot = 0.f;
+                    const bool live = h < H;  // (a dead row with eps = 0 would give 0 * inf)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float hat = v[m][e] * rinv;
+                        if (live) dw[e] = fmaf(u[m][e], hat, dw[e]);
+                        u[m][e] *= w[e];
+                        dot = fmaf(u[m][e], hat, dot);
+                    }
+                    dot = row_sum<D>(dot) * (1.f / D);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) u[m][e] = rinv * (u[m][e] - v[m][e] * rinv * dot);
+                    if (live) store8(y, u[m]);
+                }
+            }
         }
     }
 
     if (kBwd && a.part) {
         __shared__ float red[kWarps][2][D];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int e = 0; e < 8; ++e) {
+            float x = dw[e];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float x = i ? dwk[e] : dwq[e];
-#pragma unroll
-                for (int off = kLanes; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-                if (sub == 0) red[warp][i][8 * l + e] = x;
+            for (int off = kLanes; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+            if (sub == 0) {
+                red[warp][is_k ? 1 : 0][8 * l + e] = x;
+                red[warp][is_k ? 0 : 1][8 * l + e] = 0.f;
             }
+        }
         __syncthreads();
         for (int c = threadIdx.x; c < 2 * D; c += blockDim.x) {
             float x = 0.f;
@@ -292,46 +320,54 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int bl
 }
 
 template <int D, typename IO, bool kBwd>
-cudaError_t launch_t(NormArgs a, int interleaved, float* dwq, float* dwk, cudaStream_t s) {
-    constexpr int kGroup = 32 / (D / 8) * kUnroll;
-    const int64_t per_token = (a.Hq + kGroup - 1) / kGroup + (a.Hk + kGroup - 1) / kGroup;
-    const int64_t want = (a.T * per_token + kWarps - 1) / kWarps;
-    // the forward runs one task a warp; the backward keeps the weight gradients in registers
-    // over a grid-stride loop
-    const int64_t cap = kBwd ? (int64_t)kMaxBwdBlocks : ((int64_t)1 << 30);
-    const int grid = (int)(want < cap ? want : cap);
-    if (grid > 0) {
-        ProfScope prof(kBwd ? "qk_norm_bwd_kernel" : "qk_norm_kernel", s);
-        if (interleaved)
-            norm_kernel<D, IO, true, kBwd><<<grid, 32 * kWarps, 0, s>>>(a);
-        else
-            norm_kernel<D, IO, false, kBwd><<<grid, 32 * kWarps, 0, s>>>(a);
+cudaError_t launch_t(const QkNormArgs& p) {
+    constexpr int kGroup = 32 / (D / 8) * (kBwd ? 1 : 2);
+    NormArgs a{};
+    a.side[0] = Side{p.q, p.dyq, p.q_ld, p.wq, p.q_out, p.Hq, 1, 0};
+    a.side[1] = Side{p.k, p.dyk, p.k_ld, p.wk, p.k_out, p.Hk, 1, 0};
+    a.eps = p.eps; a.cos_sin = p.cos_sin; a.n_pos = p.n_pos; a.positions = p.positions;
+    a.rot = p.rot_dim; a.T = p.T; a.err = p.dev_err;
+    a.part = (p.dwq || p.dwk) ? static_cast<float*>(p.workspace) : nullptr;
+    // A token's rows go to one warp, unless that leaves an SM fewer than some 32 warps.  The forward
+    // runs one task a warp; the backward keeps the weight gradients in registers over a
+    // grid-stride loop, its warps shared out by the two sides' rows.
+    const int64_t fill = 152 * 32;
+    const int64_t groups[2] = {(p.Hq + kGroup - 1) / kGroup, (p.Hk + kGroup - 1) / kGroup};
+    const int64_t all = groups[0] + groups[1];
+    int64_t tasks[2];
+    for (int i = 0; i < 2; ++i) {
+        const int64_t want = p.T > 0 ? (fill * groups[i] + p.T * all - 1) / (p.T * all) : 1;
+        a.side[i].parts = (int)(want < 1 ? 1 : want > groups[i] ? (groups[i] ? groups[i] : 1) : want);
+        tasks[i] = groups[i] ? p.T * a.side[i].parts : 0;
+        a.side[i].warps = tasks[i];
     }
-    if (kBwd && (dwq || dwk)) {
-        ProfScope prof("qk_norm_dw_kernel", s);
-        norm_dw_kernel<D><<<1, 1024, 0, s>>>(a.part, grid, dwq, dwk);
+    if (kBwd && tasks[0] + tasks[1] > (int64_t)kMaxBwdBlocks * kWarps) {
+        const int64_t most = (int64_t)kMaxBwdBlocks * kWarps;
+        int64_t k = most * groups[1] / all;
+        if (groups[1] > 0 && k < 1) k = 1;
+        a.side[0].warps = most - k;
+        a.side[1].warps = k;
+    }
+    const int grid = (int)((a.side[0].warps + a.side[1].warps + kWarps - 1) / kWarps);
+    if (grid > 0) {
+        ProfScope prof(kBwd ? "qk_norm_bwd_kernel" : "qk_norm_kernel", p.stream);
+        if (p.interleaved)
+            norm_kernel<D, IO, true, kBwd><<<grid, 32 * kWarps, 0, p.stream>>>(a);
+        else
+            norm_kernel<D, IO, false, kBwd><<<grid, 32 * kWarps, 0, p.stream>>>(a);
+    }
+    if (kBwd && (p.dwq || p.dwk)) {
+        ProfScope prof("qk_norm_dw_kernel", p.stream);
+        norm_dw_kernel<D><<<1, 1024, 0, p.stream>>>(a.part, grid, p.dwq, p.dwk);
     }
     return cudaGetLastError();
 }
 
-NormArgs to_args(const QkNormArgs& p) {
-    NormArgs a{};
-    a.q = p.q; a.k = p.k; a.dyq = p.dyq; a.dyk = p.dyk; a.q_ld = p.q_ld; a.k_ld = p.k_ld;
-    a.wq = p.wq; a.wk = p.wk; a.eps = p.eps; a.cos_sin = p.cos_sin; a.n_pos = p.n_pos;
-    a.positions = p.positions; a.rot = p.rot_dim; a.q_out = p.q_out; a.k_out = p.k_out;
-    a.part = (p.dwq || p.dwk) ? static_cast<float*>(p.workspace) : nullptr;
-    a.T = p.T; a.Hq = p.Hq; a.Hk = p.Hk; a.err = p.dev_err;
-    return a;
-}
-
 template <bool kBwd>
 cudaError_t dispatch(const QkNormArgs& p) {
-    const NormArgs a = to_args(p);
     if (p.d == 128)
-        return p.io_bf16 ? launch_t<128, __nv_bfloat16, kBwd>(a, p.interleaved, p.dwq, p.dwk, p.stream)
-                         : launch_t<128, float, kBwd>(a, p.interleaved, p.dwq, p.dwk, p.stream);
-    return p.io_bf16 ? launch_t<64, __nv_bfloat16, kBwd>(a, p.interleaved, p.dwq, p.dwk, p.stream)
-                     : launch_t<64, float, kBwd>(a, p.interleaved, p.dwq, p.dwk, p.stream);
+        return p.io_bf16 ? launch_t<128, __nv_bfloat16, kBwd>(p) : launch_t<128, float, kBwd>(p);
+    return p.io_bf16 ? launch_t<64, __nv_bfloat16, kBwd>(p) : launch_t<64, float, kBwd>(p);
 }
 
 }  // namespace
