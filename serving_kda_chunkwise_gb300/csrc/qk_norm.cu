@@ -6,14 +6,15 @@
 //   dw = sum over rows of u x r,   dx = r (w u) - x r^3 mean(w u x),   r = 1 / sqrt(mean x^2 + eps)
 //
 // Streaming work: each element is read and written once (backward: x and dy read, dx written).
-// A row (one token and head) of d channels is covered by d / 8 lanes with 8 channels each
-// (16-byte loads for bf16), so a warp holds 2 (d = 128) or 4 (d = 64) rows at a time and the
-// row sums are shuffle reductions.  A warp's task is one token's queries or keys, some or all of
-// its heads, in groups of 1 or 2 times that many rows, the next group's rows on their way while
-// one is worked on: the token's position and its row of the table, two dependent loads, are then
-// paid once a task.  The partner of a channel
-// in the (p, p + rot/2) pairing sits in another lane (rot is a multiple of 16, so whole lanes pair
-// up) and comes by shuffle; in the interleaved pairing it sits in the same lane.
+// A row (one token and head) of d channels is covered by d / 8 lanes with two pieces of 4
+// channels each, so a warp holds 2 (d = 128) or 4 (d = 64) rows at a time and the row sums are
+// shuffle reductions.  The pieces of a lane are 8 neighbouring channels, but in the
+// (p, p + rot/2) pairing lanes of rotated channels take channels 4 l .. and rot/2 + 4 l .., so that
+// both members of every pair sit in one lane (with whole 16-byte pieces the partner came by 8
+// shuffles a row).  A warp's task is one token's queries or keys, some or all of its heads, in
+// groups of 1 or 2 times that many rows, the next group's rows on their way while one is worked
+// on: the token's position and its row of the table, two dependent loads, are then paid once a
+// task.
 // All sums and the rotation are fp32; the only rounding to fewer bits is that of the result.
 // y may be x: a lane reads its 8 channels before it writes them and no other lane reads them.
 #include "kda_common.cuh"
@@ -25,25 +26,24 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kMaxBwdBlocks = 152 * 4;
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+__device__ __forceinline__ void load4(const float* p, float* v) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// 8 channels as they are in memory, loaded ahead of their use.
+// Two pieces of 4 channels as they are in memory, loaded ahead of their use.
 template <typename IO>
 struct Raw;
 template <>
 struct Raw<__nv_bfloat16> {
-    uint4 a;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-        a = __ldcs(reinterpret_cast<const uint4*>(p));
+    uint2 a, b;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, int second) {
+        a = __ldcs(reinterpret_cast<const uint2*>(p));
+        b = __ldcs(reinterpret_cast<const uint2*>(p + second));
     }
-    __device__ __forceinline__ void zero() { a = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void zero() { a = b = make_uint2(0u, 0u); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[2 * e] = __uint_as_float(w[e] << 16);
@@ -54,9 +54,9 @@ struct Raw<__nv_bfloat16> {
 template <>
 struct Raw<float> {
     float4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
+    __device__ __forceinline__ void load(const float* p, int second) {
         a = __ldcs(reinterpret_cast<const float4*>(p));
-        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        b = __ldcs(reinterpret_cast<const float4*>(p + second));
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -65,40 +65,33 @@ struct Raw<float> {
     }
 };
 
-template <typename IO>
-__device__ __forceinline__ void store8(IO* p, const float (&v)[8]);
-template <>
-__device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&v)[8]) {
+__device__ __forceinline__ void store(__nv_bfloat16* p, int second, const float (&v)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
         w[e] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+    __stcs(reinterpret_cast<uint2*>(p + second), make_uint2(w[2], w[3]));
 }
-template <>
-__device__ __forceinline__ void store8<float>(float* p, const float (&v)[8]) {
+__device__ __forceinline__ void store(float* p, int second, const float (&v)[8]) {
     __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    __stcs(reinterpret_cast<float4*>(p + second), make_float4(v[4], v[5], v[6], v[7]));
 }
 
-// What one lane rotates with: its 8 channels' cosines and signed sines (half pairing) or its 4
-// pairs' (interleaved, in the first 4 entries).
+// The cosines and sines of a lane's four pairs.
 struct Turn {
-    float c[8], s[8];
-    int partner;  // lane holding the other members of this lane's pairs (half pairing)
-    bool on;      // this lane's channels are rotated
+    float c[4], s[4];
+    bool on;  // the lane's channels are rotated
 };
 
-template <int D, bool kInter>
+template <int D>
 __device__ __forceinline__ Turn load_turn(const float* cos_sin, int64_t n_pos,
                                           const int32_t* positions, int rot, int64_t t, int lane,
                                           unsigned* err) {
-    constexpr int kLanes = D / 8;
-    const int l = lane % kLanes;
+    const int l = lane % (D / 8);
     Turn r;
-    r.partner = lane;
     r.on = 8 * l < rot;
     if (rot == 0) return r;
     const int64_t p = positions ? (int64_t)__ldg(positions + t) : t;
@@ -107,51 +100,24 @@ __device__ __forceinline__ Turn load_turn(const float* cos_sin, int64_t n_pos,
         r.on = false;
         return r;
     }
-    const float* row = cos_sin + p * rot;
-    if (kInter) {
-        if (r.on) {
-            const float4 c = __ldg(reinterpret_cast<const float4*>(row) + l);
-            const float4 s = __ldg(reinterpret_cast<const float4*>(row + rot / 2) + l);
-            r.c[0] = c.x; r.c[1] = c.y; r.c[2] = c.z; r.c[3] = c.w;
-            r.s[0] = s.x; r.s[1] = s.y; r.s[2] = s.z; r.s[3] = s.w;
-        }
-    } else {
-        const int half = rot / 16;  // lanes a half of the rotated channels covers
-        const bool second = l >= half;
-        if (r.on) {
-            r.partner = second ? lane - half : lane + half;
-            const int at = second ? l - half : l;
-            load8(row + 8 * at, r.c);
-            load8(row + rot / 2 + 8 * at, r.s);
-            // channel a of a pair takes -sin of its partner, channel b takes +sin
-            if (!second)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) r.s[e] = -r.s[e];
-        }
+    if (r.on) {
+        load4(cos_sin + p * rot + 4 * l, r.c);
+        load4(cos_sin + p * rot + rot / 2 + 4 * l, r.s);
     }
     return r;
 }
 
-// Rotates the lane's channels (sign -1: the transposed rotation).  Called by whole warps.
+// Rotates the lane's pairs (sign -1: the transposed rotation).
 template <bool kInter>
-__device__ __forceinline__ void turn(const Turn& r, float sign, int rot, float (&v)[8]) {
-    if (rot == 0) return;
-    if (kInter) {
-        if (r.on)
+__device__ __forceinline__ void turn(const Turn& r, float sign, float (&v)[8]) {
+    if (r.on)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = v[2 * e], b = v[2 * e + 1], s = sign * r.s[e];
-                v[2 * e] = a * r.c[e] - b * s;
-                v[2 * e + 1] = a * s + b * r.c[e];
-            }
-    } else {
-        float o[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = __shfl_sync(0xffffffffu, v[e], r.partner);
-        if (r.on)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = v[e] * r.c[e] + o[e] * (sign * r.s[e]);
-    }
+        for (int e = 0; e < 4; ++e) {
+            const int i = kInter ? 2 * e : e, j = kInter ? 2 * e + 1 : 4 + e;
+            const float a = v[i], b = v[j], s = sign * r.s[e];
+            v[i] = a * r.c[e] - b * s;
+            v[j] = a * s + b * r.c[e];
+        }
 }
 
 template <int D>
@@ -159,6 +125,27 @@ __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
     for (int off = D / 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     return x;
+}
+
+// The row's sum from the lanes' two pieces.  A lane's pieces are neighbours, or `apart` lanes apart
+// (a power of two) where they are split: then each is summed over its neighbours first, which is
+// the order in which a row without a rotation is summed, so that its norm has the same bits.
+template <int D>
+__device__ __forceinline__ float piece_sum(float x, float y, bool split, int apart) {
+    if (!split) {
+        x += y;
+        y = 0.f;
+    }
+#pragma unroll
+    for (int off = 1; off < D / 8; off <<= 1) {
+        if (off < apart) y += __shfl_xor_sync(0xffffffffu, y, off);
+        if (off == apart) {
+            x += y;
+            y = 0.f;
+        }
+        x += __shfl_xor_sync(0xffffffffu, x, off);
+    }
+    return x + y;
 }
 
 struct Side {  // queries or keys
@@ -199,6 +186,12 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
     const int H = s.H, groups = (H + kGroup - 1) / kGroup;
     const int per_part = (groups + s.parts - 1) / s.parts;
     const int64_t tasks = id < s.warps ? a.T * s.parts : 0;
+    // the lane's two pieces of a row
+    const bool split = !kInter && 8 * l < a.rot;
+    const int first = split ? 4 * l : 8 * l, second = split ? a.rot / 2 : 4;
+    // (lanes between a split lane's pieces; other widths sum a lane's pieces first)
+    const int wide = kInter ? 0 : a.rot / 8;
+    const int apart = (wide & (wide - 1)) == 0 ? wide : 0;
     float dw[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[e] = 0.f;
@@ -207,8 +200,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
         const int64_t t = s.parts == 1 ? task : task / s.parts;
         const int g0 = s.parts == 1 ? 0 : (int)(task - t * s.parts) * per_part;
         const int g1 = min(g0 + per_part, groups);
-        const IO* xp = static_cast<const IO*>(s.x) + t * s.ld + 8 * l;
-        const int64_t own = t * H * D + 8 * l;
+        const IO* xp = static_cast<const IO*>(s.x) + t * s.ld + first;
+        const int64_t own = t * H * D + first;
 
         Raw<IO> x[kUnroll], dy[kBwd ? kUnroll : 1];
         auto fetch = [&](int g) {
@@ -218,13 +211,13 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
                 x[m].zero();
                 if (kBwd) dy[m].zero();
                 if (h < H) {
-                    x[m].load(xp + h * D);
-                    if (kBwd) dy[m].load(static_cast<const IO*>(s.dy) + own + h * D);
+                    x[m].load(xp + h * D, second);
+                    if (kBwd) dy[m].load(static_cast<const IO*>(s.dy) + own + h * D, second);
                 }
             }
         };
         if (g0 < g1) fetch(g0);
-        const Turn r = load_turn<D, kInter>(a.cos_sin, a.n_pos, a.positions, a.rot, t, lane, a.err);
+        const Turn r = load_turn<D>(a.cos_sin, a.n_pos, a.positions, a.rot, t, lane, a.err);
         for (int g = g0; g < g1; ++g) {
             float v[kUnroll][8], u[kBwd ? kUnroll : 1][8];
 #pragma unroll
@@ -234,28 +227,32 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
             }
             if (g + 1 < g1) fetch(g + 1);
             float w[8];
-            if (s.w)
-                load8(s.w + 8 * l, w);
-            else
+            if (s.w) {
+                load4(s.w + first, w);
+                load4(s.w + first + second, w + 4);
+            } else
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = 1.f;
 #pragma unroll
             for (int m = 0; m < kUnroll; ++m) {
                 const int h = g * kGroup + m * kRows + sub;
                 IO* y = static_cast<IO*>(s.out) + own + h * D;
-                float ss = 0.f;
+                float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(v[m][e], v[m][e], ss);
-                const float rms = sqrtf(row_sum<D>(ss) * (1.f / D) + a.eps);
-                const float rinv = 1.f / rms;
+                for (int e = 0; e < 4; ++e) {
+                    s0 = fmaf(v[m][e], v[m][e], s0);
+                    s1 = fmaf(v[m][4 + e], v[m][4 + e], s1);
+                }
+                const float ss = piece_sum<D>(s0, s1, split && apart > 0, apart);
+                const float rinv = rsqrtf(ss * (1.f / D) + a.eps);
                 if (!kBwd) {
                     float n[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) n[e] = v[m][e] * rinv * w[e];
-                    turn<kInter>(r, 1.f, a.rot, n);
-                    if (h < H) store8(y, n);
+                    turn<kInter>(r, 1.f, n);
+                    if (h < H) store(y, second, n);
                 } else {
-                    turn<kInter>(r, -1.f, a.rot, u[m]);
+                    turn<kInter>(r, -1.f, u[m]);
                     float dot = 0.f;
                     const bool live = h < H;  // (a dead row with eps = 0 would give 0 * inf)
 #pragma unroll
@@ -268,7 +265,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
                     dot = row_sum<D>(dot) * (1.f / D);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) u[m][e] = rinv * (u[m][e] - v[m][e] * rinv * dot);
-                    if (live) store8(y, u[m]);
+                    if (live) store(y, second, u[m]);
                 }
             }
         }
@@ -282,8 +279,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
 #pragma unroll
             for (int off = kLanes; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
             if (sub == 0) {
-                red[warp][is_k ? 1 : 0][8 * l + e] = x;
-                red[warp][is_k ? 0 : 1][8 * l + e] = 0.f;
+                const int c = first + (e < 4 ? e : second + e - 4);
+                red[warp][is_k ? 1 : 0][c] = x;
+                red[warp][is_k ? 0 : 1][c] = 0.f;
             }
         }
         __syncthreads();
