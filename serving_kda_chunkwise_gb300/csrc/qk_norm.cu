@@ -24,6 +24,11 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8;
+// Row groups loaded at a time: what keeps some 30 KB a SM on the way within the registers.
+template <typename IO>
+__host__ __device__ constexpr int unroll(bool bwd) {
+    return bwd ? (sizeof(IO) == 2 ? 2 : 1) : (sizeof(IO) == 2 ? 4 : 2);
+}
 constexpr int kMaxBwdBlocks = 152 * 4;
 
 __device__ __forceinline__ void load4(const float* p, float* v) {
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
     const __grid_constant__ NormArgs a) {
     constexpr int kLanes = D / 8;
     constexpr int kRows = 32 / kLanes;         // rows a warp holds at a time
-    constexpr int kUnroll = kBwd ? 1 : 2;
+    constexpr int kUnroll = unroll<IO>(kBwd);
     constexpr int kGroup = kRows * kUnroll;    // rows of a group
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane % kLanes, sub = lane / kLanes;
@@ -219,11 +224,11 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
         if (g0 < g1) fetch(g0);
         const Turn r = load_turn<D>(a.cos_sin, a.n_pos, a.positions, a.rot, t, lane, a.err);
         for (int g = g0; g < g1; ++g) {
-            float v[kUnroll][8], u[kBwd ? kUnroll : 1][8];
+            Raw<IO> xc[kUnroll], dc[kBwd ? kUnroll : 1];
 #pragma unroll
             for (int m = 0; m < kUnroll; ++m) {
-                x[m].get(v[m]);
-                if (kBwd) dy[m].get(u[m]);
+                xc[m] = x[m];
+                if (kBwd) dc[m] = dy[m];
             }
             if (g + 1 < g1) fetch(g + 1);
             float w[8];
@@ -237,35 +242,38 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
             for (int m = 0; m < kUnroll; ++m) {
                 const int h = g * kGroup + m * kRows + sub;
                 IO* y = static_cast<IO*>(s.out) + own + h * D;
+                float v[8], u[8];
+                xc[m].get(v);
+                if (kBwd) dc[m].get(u);
                 float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s0 = fmaf(v[m][e], v[m][e], s0);
-                    s1 = fmaf(v[m][4 + e], v[m][4 + e], s1);
+                    s0 = fmaf(v[e], v[e], s0);
+                    s1 = fmaf(v[4 + e], v[4 + e], s1);
                 }
                 const float ss = piece_sum<D>(s0, s1, split && apart > 0, apart);
                 const float rinv = rsqrtf(ss * (1.f / D) + a.eps);
                 if (!kBwd) {
                     float n[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) n[e] = v[m][e] * rinv * w[e];
+                    for (int e = 0; e < 8; ++e) n[e] = v[e] * rinv * w[e];
                     turn<kInter>(r, 1.f, n);
                     if (h < H) store(y, second, n);
                 } else {
-                    turn<kInter>(r, -1.f, u[m]);
+                    turn<kInter>(r, -1.f, u);
                     float dot = 0.f;
                     const bool live = h < H;  // (a dead row with eps = 0 would give 0 * inf)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float hat = v[m][e] * rinv;
-                        if (live) dw[e] = fmaf(u[m][e], hat, dw[e]);
-                        u[m][e] *= w[e];
-                        dot = fmaf(u[m][e], hat, dot);
+                        const float hat = v[e] * rinv;
+                        if (live) dw[e] = fmaf(u[e], hat, dw[e]);
+                        u[e] *= w[e];
+                        dot = fmaf(u[e], hat, dot);
                     }
                     dot = row_sum<D>(dot) * (1.f / D);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) u[m][e] = rinv * (u[m][e] - v[m][e] * rinv * dot);
-                    if (live) store(y, second, u[m]);
+                    for (int e = 0; e < 8; ++e) u[e] = rinv * (u[e] - v[e] * rinv * dot);
+                    if (live) store(y, second, u);
                 }
             }
         }
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int bl
 
 template <int D, typename IO, bool kBwd>
 cudaError_t launch_t(const QkNormArgs& p) {
-    constexpr int kGroup = 32 / (D / 8) * (kBwd ? 1 : 2);
+    constexpr int kGroup = 32 / (D / 8) * unroll<IO>(kBwd);
     NormArgs a{};
     a.side[0] = Side{p.q, p.dyq, p.q_ld, p.wq, p.q_out, p.Hq, 1, 0};
     a.side[1] = Side{p.k, p.dyk, p.k_ld, p.wk, p.k_out, p.Hk, 1, 0};
