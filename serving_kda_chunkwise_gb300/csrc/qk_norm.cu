@@ -31,6 +31,24 @@ __host__ __device__ constexpr int unroll(bool bwd) {
 }
 constexpr int kMaxBwdBlocks = 152 * 4;
 
+// Pairs of fp32 numbers: the kernels are bound by the instructions they issue.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
 __device__ __forceinline__ void load4(const float* p, float* v) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p));
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -47,13 +65,11 @@ struct Raw<__nv_bfloat16> {
         b = __ldcs(reinterpret_cast<const uint2*>(p + second));
     }
     __device__ __forceinline__ void zero() { a = b = make_uint2(0u, 0u); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
         const uint32_t w[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-        }
+        for (int e = 0; e < 4; ++e)
+            v[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
     }
 };
 template <>
@@ -64,25 +80,25 @@ struct Raw<float> {
         b = __ldcs(reinterpret_cast<const float4*>(p + second));
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    __device__ __forceinline__ void get(float2 (&v)[4]) const {
+        v[0] = make_float2(a.x, a.y); v[1] = make_float2(a.z, a.w);
+        v[2] = make_float2(b.x, b.y); v[3] = make_float2(b.z, b.w);
     }
 };
 
-__device__ __forceinline__ void store(__nv_bfloat16* p, int second, const float (&v)[8]) {
+__device__ __forceinline__ void store(__nv_bfloat16* p, int second, const float2 (&v)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[e].x, v[e].y);
         w[e] = *reinterpret_cast<const uint32_t*>(&b);
     }
     __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
     __stcs(reinterpret_cast<uint2*>(p + second), make_uint2(w[2], w[3]));
 }
-__device__ __forceinline__ void store(float* p, int second, const float (&v)[8]) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(p + second), make_float4(v[4], v[5], v[6], v[7]));
+__device__ __forceinline__ void store(float* p, int second, const float2 (&v)[4]) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+    __stcs(reinterpret_cast<float4*>(p + second), make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
 }
 
 // The cosines and sines of a lane's four pairs.
@@ -112,17 +128,26 @@ __device__ __forceinline__ Turn load_turn(const float* cos_sin, int64_t n_pos,
     return r;
 }
 
-// Rotates the lane's pairs (sign -1: the transposed rotation).
-template <bool kInter>
-__device__ __forceinline__ void turn(const Turn& r, float sign, float (&v)[8]) {
-    if (r.on)
+// Rotates the lane's pairs (the transposed rotation for kBack).
+template <bool kInter, bool kBack>
+__device__ __forceinline__ void turn(const Turn& r, float2 (&v)[4]) {
+    if (!r.on) return;
+    if (kInter) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = kInter ? 2 * e : e, j = kInter ? 2 * e + 1 : 4 + e;
-            const float a = v[i], b = v[j], s = sign * r.s[e];
-            v[i] = a * r.c[e] - b * s;
-            v[j] = a * s + b * r.c[e];
+            const float s = kBack ? -r.s[e] : r.s[e], a = v[e].x, b = v[e].y;
+            v[e] = make_float2(a * r.c[e] - b * s, a * s + b * r.c[e]);
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 c = make_float2(r.c[2 * e], r.c[2 * e + 1]);
+            const float2 s = make_float2(r.s[2 * e], r.s[2 * e + 1]);
+            const float2 n = make_float2(-s.x, -s.y), a = v[e], b = v[2 + e];
+            v[e] = fma2(b, kBack ? s : n, mul2(a, c));
+            v[2 + e] = fma2(a, kBack ? n : s, mul2(b, c));
+        }
+    }
 }
 
 template <int D>
@@ -137,9 +162,22 @@ __device__ __forceinline__ float row_sum(float x) {
 // the order in which a row without a rotation is summed, so that its norm has the same bits.
 template <int D>
 __device__ __forceinline__ float piece_sum(float x, float y, bool split, int apart) {
+    if (apart >= D / 8) {  // every lane is split, and to the last step
+#pragma unroll
+        for (int off = 1; off < D / 8; off <<= 1) {
+            x += __shfl_xor_sync(0xffffffffu, x, off);
+            y += __shfl_xor_sync(0xffffffffu, y, off);
+        }
+        return x + y;
+    }
     if (!split) {
         x += y;
         y = 0.f;
+    }
+    if (apart == 0) {
+#pragma unroll
+        for (int off = 1; off < D / 8; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        return x;
     }
 #pragma unroll
     for (int off = 1; off < D / 8; off <<= 1) {
@@ -197,9 +235,9 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
     // (lanes between a split lane's pieces; other widths sum a lane's pieces first)
     const int wide = kInter ? 0 : a.rot / 8;
     const int apart = (wide & (wide - 1)) == 0 ? wide : 0;
-    float dw[8];
+    float2 dw[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[e] = 0.f;
+    for (int e = 0; e < 4; ++e) dw[e] = make_float2(0.f, 0.f);
 
     for (int64_t task = id; task < tasks; task += s.warps) {
         const int64_t t = s.parts == 1 ? task : task / s.parts;
@@ -207,6 +245,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
         const int g1 = min(g0 + per_part, groups);
         const IO* xp = static_cast<const IO*>(s.x) + t * s.ld + first;
         const int64_t own = t * H * D + first;
+        const IO* up = static_cast<const IO*>(s.dy) + own;
+        IO* out = static_cast<IO*>(s.out) + own;
 
         Raw<IO> x[kUnroll], dy[kBwd ? kUnroll : 1];
         auto fetch = [&](int g) {
@@ -217,7 +257,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
                 if (kBwd) dy[m].zero();
                 if (h < H) {
                     x[m].load(xp + h * D, second);
-                    if (kBwd) dy[m].load(static_cast<const IO*>(s.dy) + own + h * D, second);
+                    if (kBwd) dy[m].load(up + h * D, second);
                 }
             }
         };
@@ -241,38 +281,37 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
 #pragma unroll
             for (int m = 0; m < kUnroll; ++m) {
                 const int h = g * kGroup + m * kRows + sub;
-                IO* y = static_cast<IO*>(s.out) + own + h * D;
-                float v[8], u[8];
+                IO* y = out + h * D;
+                float2 v[4];
                 xc[m].get(v);
-                if (kBwd) dc[m].get(u);
-                float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s0 = fmaf(v[e], v[e], s0);
-                    s1 = fmaf(v[4 + e], v[4 + e], s1);
-                }
-                const float ss = piece_sum<D>(s0, s1, split && apart > 0, apart);
+                const float2 q0 = fma2(v[1], v[1], mul2(v[0], v[0]));
+                const float2 q1 = fma2(v[3], v[3], mul2(v[2], v[2]));
+                const float ss = piece_sum<D>(q0.x + q0.y, q1.x + q1.y, split && apart > 0, apart);
                 const float rinv = rsqrtf(ss * (1.f / D) + a.eps);
+                const float2 r2 = make_float2(rinv, rinv);
                 if (!kBwd) {
-                    float n[8];
+                    float2 n[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) n[e] = v[e] * rinv * w[e];
-                    turn<kInter>(r, 1.f, n);
+                    for (int e = 0; e < 4; ++e)
+                        n[e] = mul2(mul2(v[e], r2), make_float2(w[2 * e], w[2 * e + 1]));
+                    turn<kInter, false>(r, n);
                     if (h < H) store(y, second, n);
                 } else {
-                    turn<kInter>(r, -1.f, u);
-                    float dot = 0.f;
+                    float2 u[4], d2 = make_float2(0.f, 0.f);
+                    dc[m].get(u);
+                    turn<kInter, true>(r, u);
                     const bool live = h < H;  // (a dead row with eps = 0 would give 0 * inf)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float hat = v[e] * rinv;
-                        if (live) dw[e] = fmaf(u[e], hat, dw[e]);
-                        u[e] *= w[e];
-                        dot = fmaf(u[e], hat, dot);
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = mul2(v[e], r2);
+                        if (live) dw[e] = fma2(u[e], v[e], dw[e]);
+                        u[e] = mul2(u[e], make_float2(w[2 * e], w[2 * e + 1]));
+                        d2 = fma2(u[e], v[e], d2);
                     }
-                    dot = row_sum<D>(dot) * (1.f / D);
+                    const float dot = -row_sum<D>(d2.x + d2.y) * (1.f / D);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) u[e] = rinv * (u[e] - v[e] * rinv * dot);
+                    for (int e = 0; e < 4; ++e)
+                        u[e] = mul2(r2, fma2(v[e], make_float2(dot, dot), u[e]));
                     if (live) store(y, second, u);
                 }
             }
@@ -283,7 +322,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
         __shared__ float red[kWarps][2][D];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float x = dw[e];
+            float x = e & 1 ? dw[e / 2].y : dw[e / 2].x;
 #pragma unroll
             for (int off = kLanes; off < 32; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
             if (sub == 0) {
