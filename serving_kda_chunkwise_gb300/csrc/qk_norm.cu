@@ -341,21 +341,22 @@ __global__ void __launch_bounds__(32 * kWarps, kBwd ? 2 : 3) norm_kernel(
     }
 }
 
-// dw[c] = the sum of the blocks' partials in a fixed order: 1024 / (2 D) threads a channel.
+// dw[c] = the sum of the blocks' partials in a fixed order: a CTA takes 32 channels, its 32 warps
+// every 32nd block.
 template <int D>
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int blocks, float* dwq,
                                                        float* dwk) {
-    constexpr int kParts = 1024 / (2 * D);
-    __shared__ float red[kParts][2 * D];
-    const int c = threadIdx.x % (2 * D), j = threadIdx.x / (2 * D);
+    __shared__ float red[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float x = 0.f;
-    for (int b = j; b < blocks; b += kParts) x += part[(int64_t)b * 2 * D + c];
-    red[j][c] = x;
+#pragma unroll 4
+    for (int b = warp; b < blocks; b += 32) x += part[(int64_t)b * 2 * D + c];
+    red[warp][lane] = x;
     __syncthreads();
-    if (j == 0) {
+    if (warp == 0) {
         x = 0.f;
 #pragma unroll
-        for (int i = 0; i < kParts; ++i) x += red[i][c];
+        for (int i = 0; i < 32; ++i) x += red[i][lane];
         if (c < D) {
             if (dwq) dwq[c] = x;
         } else if (dwk) {
@@ -403,7 +404,7 @@ cudaError_t launch_t(const QkNormArgs& p) {
     }
     if (kBwd && (p.dwq || p.dwk)) {
         ProfScope prof("qk_norm_dw_kernel", p.stream);
-        norm_dw_kernel<D><<<1, 1024, 0, p.stream>>>(a.part, grid, p.dwq, p.dwk);
+        norm_dw_kernel<D><<<2 * D / 32, 1024, 0, p.stream>>>(a.part, grid, p.dwq, p.dwk);
     }
     return cudaGetLastError();
 }
