@@ -983,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 // the edge and the chunk carried along, and the accumulator in TMEM is never rescaled.  W is
 // decayed in place (hi over W itself, lo beside it), so two stages of all operands fit.  Bound by
 // reading Y and W.
-constexpr int kSumThreads = 384;
+constexpr int kSumThreads = 640;
 constexpr uint32_t kUY = 0, kUW = 32768, kULo = 65536, kUStage = 98304;  // two stages
 constexpr uint32_t kUBar = 2 * kUStage;
 constexpr uint32_t kSumSmem = kUBar + 256;
@@ -1006,7 +1006,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.done[i], 1);
-            mbar_init(&bar.wd[i], 8);
+            mbar_init(&bar.wd[i], 16);
         }
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
@@ -1076,7 +1076,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             }
         }
     } else if (warp >= 4) {
-        const int q = warp & 3, wg = (warp - 4) >> 2;
+        // 16 warps decay W, each 32 tokens of 32 columns (8 warps took longer than the loads)
+        const int q = warp & 3, cg = (warp - 4) >> 2;
         const int row = 32 * q + lane;
         const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
         uint32_t g = 0;
@@ -1086,52 +1087,56 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             if (skip(t)) continue;
             const Call& c = o.calls.c[t.call];
             const int rev = c.reverse;
-            const bool cols = 64 * wg < c.db;
+            const bool cols = 32 * cg < c.db;
             float between = 0.f;  // log2 decay between the edge and the chunk
+            const int mine = (rev ? kRHead : kRTail) + row;
+            const float* r = record(o, t, chunk_at(t, !rev, 0).i);
+            float next = __ldg(r + mine), total = __ldg(r + kRCol + kRB + 4);
 #pragma unroll 1
             for (int k = 0; k < t.chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
                 const Chunk ch = chunk_at(t, !rev, k);
-                const float* r = record(o, t, ch.i);
-                const float wf = __ldg(r + (rev ? kRHead : kRTail) + row) * ex2f(between);
-                between += __ldg(r + kRCol + kRB + 4);
+                const float wf = next * ex2f(between);
+                between += total;
+                if (k + 1 < t.chunks) {  // the next chunk's, early
+                    r = record(o, t, chunk_at(t, !rev, k + 1).i);
+                    next = __ldg(r + mine);
+                    total = __ldg(r + kRCol + kRB + 4);
+                }
                 if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 uint8_t* stage = sm + st * kUStage;
                 const bool dead = row >= ch.len;
                 if (cols) {
-                    uint8_t* wr = stage + kUW + wg * 16384 + row * 128;
-                    uint8_t* lr = stage + kULo + wg * 16384 + row * 128;
+                    uint8_t* wr = stage + kUW + (cg >> 1) * 16384 + row * 128;
+                    uint8_t* lr = stage + kULo + (cg >> 1) * 16384 + row * 128;
+                    uint4 in[4];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        uint4 in[4];
+                    for (int x = 0; x < 4; ++x)
+                        in[x] = *reinterpret_cast<const uint4*>(
+                            wr + (((4 * (cg & 1) + x) ^ (row & 7)) << 4));
+                    if (dead)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            in[x] = *reinterpret_cast<const uint4*>(
-                                wr + (((4 * b + x) ^ (row & 7)) << 4));
+                        for (int x = 0; x < 4; ++x) in[x] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
-                            uint32_t hi[4], lo[4];
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                float a0 = __uint_as_float(w[y] << 16);
-                                float a1 = __uint_as_float(w[y] & 0xffff0000u);
-                                mul2(a0, a1, wf, wf);
-                                split2(a0, a1, hi[y], lo[y]);
-                                if (dead) hi[y] = lo[y] = 0u;
-                            }
-                            const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
-                            *reinterpret_cast<uint4*>(wr + to) =
-                                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(lr + to) =
-                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        for (int y = 0; y < 4; ++y) {
+                            float a0 = __uint_as_float(w[y] << 16);
+                            float a1 = __uint_as_float(w[y] & 0xffff0000u);
+                            mul2(a0, a1, wf, wf);
+                            split2(a0, a1, hi[y], lo[y]);
                         }
+                        const uint32_t to = ((4 * (cg & 1) + x) ^ (row & 7)) << 4;
+                        *reinterpret_cast<uint4*>(wr + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(lr + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
                 }
                 if (dead) {
-                    uint4* yr = reinterpret_cast<uint4*>(stage + kUY + wg * 16384 + row * 128);
+                    uint4* yr = reinterpret_cast<uint4*>(stage + kUY + (cg >> 1) * 16384 + row * 128);
 #pragma unroll 1
-                    for (int x = 0; x < 8; ++x) yr[x] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int x = 0; x < 4; ++x) yr[4 * (cg & 1) + x] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -1145,18 +1150,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             tc_fence_after();
             if (cols) {
                 float* to = const_cast<float*>(c.seg) +
-                            (((int64_t)t.slot * p.H + t.h) * c.da + row) * c.db + 64 * wg;
+                            (((int64_t)t.slot * p.H + t.h) * c.da + row) * c.db + 32 * cg;
+                float v[32];
+                tmem_ld32(tmem + lb + 32 * cg, v);
+                landed(v);
+                if (row < c.da)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float v[32];
-                    tmem_ld32(tmem + lb + 64 * wg + 32 * b, v);
-                    landed(v);
-                    if (row < c.da)
-#pragma unroll
-                        for (int x = 0; x < 8; ++x)
-                            reinterpret_cast<float4*>(to)[8 * b + x] =
-                                make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                }
+                    for (int x = 0; x < 8; ++x)
+                        reinterpret_cast<float4*>(to)[x] =
+                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
             }
             tc_fence_before();
             if (warp == 4 && lane == 0)
