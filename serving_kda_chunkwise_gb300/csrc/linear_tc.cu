@@ -292,6 +292,7 @@ struct OutBars {
     uint64_t upd, xs, aw;    // state update, X S, A W complete
     uint64_t read;           // the chunk's outputs read from TMEM (16 arrivals)
     uint64_t staged, stored; // ... and staged (16 arrivals); the stage read by the store
+    uint64_t open;           // the item's state loaded (8 arrivals)
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -375,27 +376,52 @@ __device__ __forceinline__ StateAt state_at(const OutParams& o, const Call& c, i
     s.holds = col < c.db && row < c.da;
     return s;
 }
+// A [da][db] state's rows lie 4 db bytes apart, one a lane: read or written from the lanes, each
+// access would touch 32 lines (an item's 64 KB took 20,000 cycles).  The warp's 32 x 64 piece goes
+// through 8 KB of shared memory instead, 16-byte pieces permuted by the row.
+__device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 256 + ((c ^ (r & 15)) << 4); }
+
 // which >= 0: sequence `which`'s own state at its edge (zeros without one), else the edge state
-// of the segment in slot -1 - which.
-__device__ __noinline__ void load_state(const OutParams& o, int call, int which, int h, int col) {
+// of the segment in slot -1 - which.  `stage`: the warp's 8 KB.
+__device__ __noinline__ void load_state(const OutParams& o, int call, int which, int h, int col,
+                                        uint8_t* stage) {
     const Call& c = o.calls.c[call];
+    const int lane = threadIdx.x & 31, row0 = threadIdx.x & 96;
     const StateAt s = state_at(o, c, which < 0 ? -1 - which : which, h, col);
     const float* from = which < 0 ? c.seg : c.edge;
-    const uint32_t to = ((threadIdx.x & 96u) << 16) + kTS + col;
+    const uint32_t to = (static_cast<uint32_t>(row0) << 16) + kTS + col;
+    const bool rows = col < c.db && row0 < c.da;  // (da is a multiple of a warp's rows)
+    if (from && rows && !c.tr) {
+        const float* f = from + s.at - (int64_t)lane * c.db;
+#pragma unroll 1
+        for (int b = 0; b < 2; ++b) {
+            float4 v[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                v[x] = __ldcg(reinterpret_cast<const float4*>(
+                                  f + (int64_t)(16 * b + 2 * x + (lane >> 4)) * c.db) +
+                              (lane & 15));
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                *reinterpret_cast<float4*>(stage + piece_at(16 * b + 2 * x + (lane >> 4),
+                                                            lane & 15)) = v[x];
+        }
+        __syncwarp();
+    }
 #pragma unroll 1
     for (int b = 0; b < 2; ++b) {
         uint32_t u[32];
 #pragma unroll
         for (int x = 0; x < 32; ++x) u[x] = 0u;
-        if (from && s.holds) {
-            const float* f = from + s.at + 32 * b * s.cs;
+        if (from && rows) {
             if (c.tr) {
 #pragma unroll
-                for (int x = 0; x < 32; ++x) u[x] = __float_as_uint(__ldcg(f + x * s.cs));
+                for (int x = 0; x < 32; ++x)
+                    u[x] = __float_as_uint(__ldcg(from + s.at + (32 * b + x) * s.cs));
             } else {
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(f) + x);
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + piece_at(lane, 8 * b + x));
                     u[4 * x] = v.x;
                     u[4 * x + 1] = v.y;
                     u[4 * x + 2] = v.z;
@@ -406,21 +432,39 @@ __device__ __noinline__ void load_state(const OutParams& o, int call, int which,
         tmem_st32(to + 32 * b, u);
     }
     tmem_st_wait();
+    __syncwarp();
 }
-__device__ __noinline__ void store_state(const OutParams& o, int call, int n, int h, int col) {
+__device__ __noinline__ void store_state(const OutParams& o, int call, int n, int h, int col,
+                                         uint8_t* stage) {
     const Call& c = o.calls.c[call];
-    if (c.S_out == nullptr) return;
+    const int lane = threadIdx.x & 31, row0 = threadIdx.x & 96;
+    const bool rows = col < c.db && row0 < c.da;
+    if (c.S_out == nullptr || !rows) return;
     const StateAt s = state_at(o, c, n, h, col);
-    const uint32_t from = ((threadIdx.x & 96u) << 16) + kTS + col;
+    const uint32_t from = (static_cast<uint32_t>(row0) << 16) + kTS + col;
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
         float v[16];
         tmem_ld16(from + 16 * b, v);
         landed(v);
-        if (s.holds)
+        if (c.tr) {
 #pragma unroll
             for (int x = 0; x < 16; ++x) c.S_out[s.at + (16 * b + x) * s.cs] = v[x];
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                *reinterpret_cast<float4*>(stage + piece_at(lane, 4 * b + x)) =
+                    make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+        }
     }
+    if (c.tr) return;
+    __syncwarp();
+    float* f = c.S_out + s.at - (int64_t)lane * c.db;
+#pragma unroll 4
+    for (int x = 0; x < 16; ++x)
+        reinterpret_cast<float4*>(f + (int64_t)(2 * x + (lane >> 4)) * c.db)[lane & 15] =
+            *reinterpret_cast<const float4*>(stage + piece_at(2 * x + (lane >> 4), lane & 15));
+    __syncwarp();
 }
 __device__ __noinline__ void pass_state(const OutParams& o, int call, int n, int h, int col) {
     const Call& c = o.calls.c[call];
@@ -570,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         uint64_t* one[] = {&bar.x,  &bar.y,   &bar.w,  &bar.rec, &bar.sc,
                            &bar.upd, &bar.xs, &bar.aw, &bar.drain};
         for (uint64_t* b : one) mbar_init(b, 1);
-        uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd};
+        uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd, &bar.open};
         for (uint64_t* b : eight) mbar_init(b, 8);
         mbar_init(&bar.read, 16);
         mbar_init(&bar.staged, 16);
@@ -794,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         const int row = 32 * q + lane;  // token, or state row
         const View it{reinterpret_cast<volatile int*>(sm + kSItem) + 12 * warp};
         const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + 64 * wg;  // this warp's columns
-        uint32_t g = 0;
+        uint32_t g = 0, opened = 0;
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             open_item(o, i, it);
@@ -806,10 +850,20 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             }
             const bool cols = 64 * wg < o.calls.c[it.call()].db;          // this warp has columns
             const bool holds = cols && row < o.calls.c[it.call()].da;     // this lane a state row
-            // the segment's edge state into TMEM, once the last segment's is done with
-            if (g > 0 && !wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+            // the segment's edge state into TMEM, once the last segment's is done with (and so is
+            // its copy, whose buffer the state passes through)
+            if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
+                          !wait(&bar.xs, (g - 1) & 1, p.err, abort))) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
-            load_state(o, it.call(), it.v[View::kEdge], it.h(), 64 * wg);
+            uint8_t* stage = sm + kSS + (warp - 8) * 8192;
+            load_state(o, it.call(), it.v[View::kEdge], it.h(), 64 * wg, stage);
+            // no warp writes the copy while another's state is still on its way through the buffer
+            if (lane == 0) mbar_arrive(&bar.open);
+            if (!wait(&bar.open, opened & 1, p.err, abort)) { ok = false; break; }
+            ++opened;
 
             float rowf_prev = 0.f, head, tail, total;
             {
@@ -949,7 +1003,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             if (it.v[View::kFinal] >= 0) {
                 if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-                store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg);
+                store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg, stage);
                 tc_fence_before();
             }
         }
@@ -989,7 +1043,7 @@ constexpr uint32_t kUBar = 2 * kUStage;
 constexpr uint32_t kSumSmem = kUBar + 256;
 
 struct SumBars {
-    uint64_t full[2], done[2], wd[2], drain;
+    uint64_t full[2], done[2], wd[2], stored, drain;
     uint32_t tmem;
     int abort;
 };
@@ -1008,6 +1062,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             mbar_init(&bar.done[i], 1);
             mbar_init(&bar.wd[i], 16);
         }
+        mbar_init(&bar.stored, 16);
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
         bar.abort = 0;
@@ -1080,7 +1135,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         const int q = warp & 3, cg = (warp - 4) >> 2;
         const int row = 32 * q + lane;
         const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
-        uint32_t g = 0;
+        uint32_t g = 0, stored = 0;
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item t = item_at<true>(o, i);
@@ -1149,18 +1204,35 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             if (!wait(&bar.done[gl & 1], (gl >> 1) & 1, p.err, abort)) { ok = false; break; }
             tc_fence_after();
             if (cols) {
-                float* to = const_cast<float*>(c.seg) +
-                            (((int64_t)t.slot * p.H + t.h) * c.da + row) * c.db + 32 * cg;
+                // (through shared memory, as in load_state(): both lo buffers are free now, for
+                // every product is complete and these warps write them next)
                 float v[32];
                 tmem_ld32(tmem + lb + 32 * cg, v);
                 landed(v);
-                if (row < c.da)
+                const int w16 = warp - 4;
+                uint8_t* own = sm + (w16 >> 3) * kUStage + kULo + (w16 & 7) * 4096;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        reinterpret_cast<float4*>(to)[x] =
-                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                for (int x = 0; x < 8; ++x)
+                    *reinterpret_cast<float4*>(own + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+                        make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                __syncwarp();
+                float* to = const_cast<float*>(c.seg) +
+                            (((int64_t)t.slot * p.H + t.h) * c.da + 32 * q) * c.db + 32 * cg;
+                if (32 * q < c.da)
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int r8 = 4 * x + (lane >> 3), c8 = lane & 7;
+                        reinterpret_cast<float4*>(to + (int64_t)r8 * c.db)[c8] =
+                            *reinterpret_cast<const float4*>(own + r8 * 128 +
+                                                             ((c8 ^ (r8 & 7)) << 4));
+                    }
             }
             tc_fence_before();
+            // no warp decays the next item's W over another's sums
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.stored);
+            if (!wait(&bar.stored, stored & 1, p.err, abort)) { ok = false; break; }
+            ++stored;
             if (warp == 4 && lane == 0)
                 dec[((int64_t)rev * o.slots + t.slot) * p.H + t.h] = between;
         }
