@@ -525,6 +525,7 @@ __device__ __noinline__ void open_item(const OutParams& o, uint32_t i, View w) {
 // there) and stored by TMA: written row by row from the lanes they kept the load/store unit busy
 // for 2000 cycles.  A warp's 32 rows are its TMEM lanes; out of
 // line, for both groups of warps call it.
+template <bool kDots>
 __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint8_t* sm,
                                           uint32_t phase, View it, int k, float rowf, int col) {
     const int row = threadIdx.x & 127;
@@ -538,7 +539,7 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
     const Chunk ch = it.chunk(k);
     const int tr = ch.t0 + row;
     const bool cols = col < db;
-    const bool in = cols && row < ch.len, dots = c.dot != nullptr;
+    const bool in = cols && row < ch.len, dots = kDots && c.dot != nullptr;
     const uint32_t from = (static_cast<uint32_t>(row & 96) << 16) + col;
     float acc = 0.f;
 #pragma unroll 1
@@ -603,6 +604,8 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
     return true;
 }
 
+// kDots: some call wants its outputs' dot products (a forward has the registers they take to spare).
+template <bool kDots>
 __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant__ OutParams o) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sbase = smem_u32(sm);
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 if (lane == 0) mbar_arrive(&bar.a);
                 // the second half of its 64 output columns (the state warps write the first)
                 const float rowf = __ldg(it.record(o, k) + (it.rev() ? kRTail : kRHead) + row);
-                ok = write_out(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32);
+                ok = write_out<kDots>(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32);
                 if (!ok) break;
             }
         }
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 for (int part = 0; ok && part < 2; ++part) {
                     if ((part == 0) == outputs_first) {
                         if (k > 0)
-                            ok = write_out(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev, 64 * wg);
+                            ok = write_out<kDots>(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev, 64 * wg);
                         continue;
                     }
                     if (k == it.chunks()) continue;
@@ -1332,12 +1335,15 @@ cudaError_t launch_outputs(const Problem& p, const lin::Calls& calls, int n, int
                            const float* rec, const char* name, cudaStream_t s) {
     OutParams o{};
     if (cudaError_t e = fill(o, p, calls, n, slots, rec, true)) return e;
+    bool dots = false;
+    for (int i = 0; i < n; ++i) dots = dots || calls.c[i].dot != nullptr;
+    const auto kernel = dots ? out_kernel<true> : out_kernel<false>;
     if (cudaError_t e = cudaFuncSetAttribute(
-            out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem))
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem))
         return e;
     const int64_t items = slots * p.H * n, sms = sm_count();
     ProfScope prof(name, s);
-    out_kernel<<<(unsigned)(items < sms ? items : sms), kThreads, kOutSmem, s>>>(o);
+    kernel<<<(unsigned)(items < sms ? items : sms), kThreads, kOutSmem, s>>>(o);
     return cudaGetLastError();
 }
 
