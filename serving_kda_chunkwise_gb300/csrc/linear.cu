@@ -29,116 +29,234 @@ using lin::Problem;
 using lin::Segment;
 
 // -------------------------------------------------- token by token, CUDA cores --
-// A CTA of 128 threads holds a da x 32 block of the state in registers (lane = column, warp =
-// a quarter of the rows) and walks the segment's tokens; x, y, w come in tiles of 16 tokens.
-// fp32 throughout, so that fp32 inputs keep fp32 accuracy: e^{g} multiplies the state as the
-// definition says.  Bound by its three fp32 operations per state element and token.
-constexpr int kCols = 32;
+// A CTA of 128 threads holds a da x 64 block of the state in registers (a lane two columns, a warp
+// a quarter of the rows, in pairs) and walks the segment's tokens, 16 at a time through shared
+// memory, the next 16 on their way in registers meanwhile.  fp32 throughout, so that fp32 inputs
+// keep fp32 accuracy.  The state decays by S += S (e^g - 1) unless g is far below 0: e^g itself
+// rounds near 1, and one decay for all tokens would round the same way at every one of them.
+// Bound by its three (sums: two) fp32 operations per state element and token, then by the
+// instructions around them.
+constexpr int kCols = 64;
+constexpr int kDotCols = 32;
 constexpr int kTile = 16;
+constexpr float kNear = -0.5f;  // below it e^g - 1 has no more bits of e^g than e^g itself
+
+template <typename IO>
+__device__ __forceinline__ float4 load_row4(const IO* p) {
+    if constexpr (sizeof(IO) == 4) {
+        return __ldg(reinterpret_cast<const float4*>(p));
+    } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        const float2 a = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.x));
+        const float2 b = __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(u.y));
+        return make_float4(a.x, a.y, b.x, b.y);
+    }
+}
 
 template <int DA, typename IO, bool kOut>
 __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Problem p,
                                                     const __grid_constant__ Calls calls,
                                                     float* dec,
                                                     int blocks_per_call) {
-    constexpr int R = DA / 4;
-    __shared__ float xs[kTile][DA], ys[kTile][DA], ws[kTile][kCols], es[kTile];
-    __shared__ float part[4][kTile][kCols];
+    constexpr int R = DA / 4, kPer = kTile * DA / 4 / 128, kPerW = kTile * kCols / 4 / 128;
+    __shared__ __align__(16) float xs[kOut ? kTile : 1][DA], ys[kTile][DA], ws[kTile][kCols];
+    __shared__ float2 fs[kTile];  // how the state decays before the token: factor, near
+    __shared__ float2 part[kOut ? 4 : 1][kTile][kCols / 2];
     if (kOut && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) lin::check_seqlens(p);
     const Call& c = calls.c[blockIdx.z / blocks_per_call];
     const int cb = blockIdx.z % blocks_per_call;
     if (c.da != DA || cb * kCols >= c.db) return;
     const Segment sg = lin::find_segment(p, (int)blockIdx.x);
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = cb * kCols + lane, row0 = warp * R;
+    const int col = cb * kCols + 2 * lane, row0 = warp * R;
     const int64_t E = (int64_t)c.da * c.db;
-    const int64_t rs = c.tr ? 1 : c.db, cs = c.tr ? c.da : 1;
     const int64_t own = ((int64_t)blockIdx.x * p.H + h) * E;
     const int64_t seq = ((int64_t)sg.n * p.H + h) * E;
 
-    float S[R];
+    float2 S[2][R / 2];  // [column][row pair]
+    auto load_state = [&](const float* from) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) S[i] = 0.f;
+        for (int r = 0; r < R / 2; ++r) {
+            const int row = row0 + 2 * r;
+            if (from == nullptr) {
+                S[0][r] = S[1][r] = make_float2(0.f, 0.f);
+            } else if (c.tr) {
+                S[0][r] = *reinterpret_cast<const float2*>(from + col * DA + row);
+                S[1][r] = *reinterpret_cast<const float2*>(from + (col + 1) * DA + row);
+            } else {
+                const float2 a = *reinterpret_cast<const float2*>(from + row * c.db + col);
+                const float2 b = *reinterpret_cast<const float2*>(from + (row + 1) * c.db + col);
+                S[0][r] = make_float2(a.x, b.x);
+                S[1][r] = make_float2(a.y, b.y);
+            }
+        }
+    };
+    auto store_state = [&](float* to) {
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) {
+            const int row = row0 + 2 * r;
+            const float2 a = S[0][r], b = S[1][r];
+            if (c.tr) {
+                *reinterpret_cast<float2*>(to + col * DA + row) = a;
+                *reinterpret_cast<float2*>(to + (col + 1) * DA + row) = b;
+            } else {
+                *reinterpret_cast<float2*>(to + row * c.db + col) = make_float2(a.x, b.x);
+                *reinterpret_cast<float2*>(to + (row + 1) * c.db + col) = make_float2(a.y, b.y);
+            }
+        }
+    };
     if (!sg.live) {
         // an empty sequence owns its first slot: its final state is its initial one
-        if (kOut && c.S_out && sg.count == 0 && sg.s == 0)
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                c.S_out[seq + (row0 + i) * rs + col * cs] =
-                    c.edge ? c.edge[seq + (row0 + i) * rs + col * cs] : 0.f;
+        if (kOut && c.S_out && sg.count == 0 && sg.s == 0) {
+            load_state(c.edge ? c.edge + seq : nullptr);
+            store_state(c.S_out + seq);
+        }
         return;
     }
     const bool last = c.reverse ? sg.s == 0 : sg.s == sg.count - 1;
     if (!kOut && last) return;  // no edge state follows from it
-    if (kOut) {
-        // the edges launch also put the sequence's own edge state into its first slot, so that
-        // with S_out in S0's place no segment reads what another has overwritten
-        const float* from = sg.count > 1 ? c.seg + own : c.edge ? c.edge + seq : nullptr;
-        if (from)
-#pragma unroll
-            for (int i = 0; i < R; ++i) S[i] = from[(row0 + i) * rs + col * cs];
-    }
+    // the edges launch also put the sequence's own edge state into its first slot, so that
+    // with S_out in S0's place no segment reads what another has overwritten
+    load_state(!kOut ? nullptr : sg.count > 1 ? c.seg + own : c.edge ? c.edge + seq : nullptr);
 
-    const int64_t len = sg.end - sg.begin;
-    float gsum = 0.f;
-    for (int64_t t0 = 0; t0 < len; t0 += kTile) {
-        const int m = (int)(len - t0 < kTile ? len - t0 : kTile);
-        // token i of the tile, in the order of the walk
-        auto token = [&](int i) { return c.reverse ? sg.end - 1 - t0 - i : sg.begin + t0 + i; };
-        __syncthreads();
-        for (int e = threadIdx.x; e < m * DA; e += 128) {
-            const int i = e / DA, d = e % DA;
-            const int64_t t = token(i);
-            if (kOut) xs[i][d] = to_f32(static_cast<const IO*>(c.x)[t * c.x_ld + h * DA + d]);
-            ys[i][d] = to_f32(static_cast<const IO*>(c.y)[t * c.y_ld + h * DA + d]);
-        }
-        for (int e = threadIdx.x; e < m * kCols; e += 128) {
-            const int i = e / kCols, d = e % kCols;
-            ws[i][d] = to_f32(static_cast<const IO*>(c.w)[token(i) * c.w_ld + (int64_t)h * c.db +
-                                                          cb * kCols + d]);
-        }
-        if (threadIdx.x < m) es[threadIdx.x] = lin::log_decay(p, token(threadIdx.x), h);
-        __syncthreads();
-        for (int i = 0; i < m; ++i) {
-            const float a = expf(es[i]), w = ws[i][lane];
-            gsum += es[i];
-            float acc = 0.f;
+    const int len = sg.end - sg.begin;
+    const int e = threadIdx.x;
+    float4 nx[kPer], ny[kPer], nw[kPerW];
+    float ng = 0.f, gsum = 0.f;
+    // tile t0's rows, in the order of the walk, zeros past its end
+    auto load_tile = [&](int t0) {
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto at = [&](int i) { return c.reverse ? sg.end - 1 - t0 - i : sg.begin + t0 + i; };
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                if (c.reverse) {
-                    S[r] = fmaf(ys[i][row0 + r], w, S[r]);
-                    if (kOut) acc = fmaf(xs[i][row0 + r], S[r], acc);
-                    S[r] *= a;
-                } else {
-                    S[r] = fmaf(ys[i][row0 + r], w, a * S[r]);
-                    if (kOut) acc = fmaf(xs[i][row0 + r], S[r], acc);
+        for (int j = 0; j < kPer; ++j) {
+            const int i = (e + 128 * j) / (DA / 4), d = (e + 128 * j) % (DA / 4) * 4;
+            const bool in = t0 + i < len;
+            const int64_t t = at(i);
+            if (kOut)
+                nx[j] = in ? load_row4(static_cast<const IO*>(c.x) + t * c.x_ld + h * DA + d)
+                           : zero;
+            ny[j] = in ? load_row4(static_cast<const IO*>(c.y) + t * c.y_ld + h * DA + d) : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < kPerW; ++j) {
+            const int i = (e + 128 * j) / (kCols / 4), d = (e + 128 * j) % (kCols / 4) * 4;
+            nw[j] = t0 + i < len ? load_row4(static_cast<const IO*>(c.w) + at(i) * c.w_ld +
+                                             h * c.db + cb * kCols + d)
+                                 : zero;
+        }
+        // reversed, a token's state has decayed by the token's before it in the walk
+        if (e < kTile) {
+            ng = 0.f;
+            if (t0 + e < len && (!c.reverse || t0 + e > 0))
+                ng = lin::log_decay(p, at(c.reverse ? e - 1 : e), h);
+        }
+    };
+    auto factor = [](float g) {
+        return g > kNear ? make_float2(expm1f(g), 1.f) : make_float2(expf(g), 0.f);
+    };
+    auto decay = [&](float2 f) {
+        const float2 a = make_float2(f.x, f.x);
+        if (f.y != 0.f) {
+#pragma unroll
+            for (int r = 0; r < R / 2; ++r) {
+                S[0][r] = fma2(S[0][r], a, S[0][r]);
+                S[1][r] = fma2(S[1][r], a, S[1][r]);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < R / 2; ++r) {
+                S[0][r] = mul2(S[0][r], a);
+                S[1][r] = mul2(S[1][r], a);
+            }
+        }
+    };
+    // outputs of tile t0, of which `part` holds the four warps' shares
+    auto write_out = [&](int t0) {
+        for (int i = warp; i < min(kTile, len - t0); i += 4) {
+            const int64_t t = c.reverse ? sg.end - 1 - t0 - i : sg.begin + t0 + i;
+            float2 o = part[0][i][lane];
+#pragma unroll
+            for (int u = 1; u < 4; ++u) {
+                o.x += part[u][i][lane].x;
+                o.y += part[u][i][lane].y;
+            }
+            IO* to = static_cast<IO*>(c.out) + (t * p.H + h) * c.db + col;
+            if constexpr (sizeof(IO) == 4)
+                *reinterpret_cast<float2*>(to) = o;
+            else
+                *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(o.x, o.y);
+            if (c.dot) {
+                const IO* y = static_cast<const IO*>(c.dot) + t * c.dot_ld + h * c.db + col;
+                float x = fmaf(o.x, to_f32(y[0]), o.y * to_f32(y[1]));
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+                if ((lane & 15) == 0)
+                    c.dots[((int64_t)(col / kDotCols) * p.T + t) * p.H + h] = x;
+            }
+        }
+    };
+    load_tile(0);
+    for (int t0 = 0; t0 < len; t0 += kTile) {
+        __syncthreads();
+        if (kOut && t0 > 0) write_out(t0 - kTile);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            if (kOut) reinterpret_cast<float4*>(xs)[e + 128 * j] = nx[j];
+            reinterpret_cast<float4*>(ys)[e + 128 * j] = ny[j];
+        }
+#pragma unroll
+        for (int j = 0; j < kPerW; ++j) reinterpret_cast<float4*>(ws)[e + 128 * j] = nw[j];
+        if (e < kTile) {
+            fs[e] = factor(ng);
+            gsum += ng;
+        }
+        __syncthreads();
+        if (t0 + kTile < len) load_tile(t0 + kTile);
+        const int m = min(kTile, len - t0);
+        for (int i = 0; i < m; ++i) {
+            decay(fs[i]);
+            const float2 w = *reinterpret_cast<const float2*>(&ws[i][2 * lane]);
+            const float2 w0 = make_float2(w.x, w.x), w1 = make_float2(w.y, w.y);
+            float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+#pragma unroll
+            for (int r = 0; r < R / 4; ++r) {
+                const float4 y = *reinterpret_cast<const float4*>(&ys[i][row0 + 4 * r]);
+                const float2 ya = make_float2(y.x, y.y), yb = make_float2(y.z, y.w);
+                S[0][2 * r] = fma2(ya, w0, S[0][2 * r]);
+                S[1][2 * r] = fma2(ya, w1, S[1][2 * r]);
+                S[0][2 * r + 1] = fma2(yb, w0, S[0][2 * r + 1]);
+                S[1][2 * r + 1] = fma2(yb, w1, S[1][2 * r + 1]);
+                if (kOut) {
+                    const float4 x = *reinterpret_cast<const float4*>(&xs[i][row0 + 4 * r]);
+                    const float2 xa = make_float2(x.x, x.y), xb = make_float2(x.z, x.w);
+                    a0 = fma2(xa, S[0][2 * r], a0);
+                    a1 = fma2(xa, S[1][2 * r], a1);
+                    a0 = fma2(xb, S[0][2 * r + 1], a0);
+                    a1 = fma2(xb, S[1][2 * r + 1], a1);
                 }
             }
-            if (kOut) part[warp][i][lane] = acc;
+            if (kOut) part[warp][i][lane] = make_float2(a0.x + a0.y, a1.x + a1.y);
         }
-        if (!kOut) continue;
+    }
+    if (kOut) {
         __syncthreads();
-        for (int i = warp; i < m; i += 4) {
-            const int64_t t = token(i);
-            const float o = part[0][i][lane] + part[1][i][lane] + part[2][i][lane] +
-                            part[3][i][lane];
-            static_cast<IO*>(c.out)[(t * p.H + h) * c.db + col] = from_f32<IO>(o);
-            if (c.dot) {
-                float x = o * to_f32(static_cast<const IO*>(c.dot)[t * c.dot_ld +
-                                                                   (int64_t)h * c.db + col]);
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-                if (lane == 0) c.dots[((int64_t)cb * p.T + t) * p.H + h] = x;
-            }
-        }
+        write_out((len - 1) / kTile * kTile);
+    }
+    if (c.reverse) {
+        const float g = lin::log_decay(p, sg.begin, h);
+        decay(factor(g));
+        if (e == 0) gsum += g;
     }
     float* to = kOut ? (last && c.S_out ? c.S_out + seq : nullptr)
                      : const_cast<float*>(c.seg) + own;
-    if (to)
+    if (to) store_state(to);
+    if (!kOut && cb == 0 && warp == 0) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) to[(row0 + i) * rs + col * cs] = S[i];
-    if (!kOut && cb == 0 && threadIdx.x == 0)
-        dec[((int64_t)c.reverse * gridDim.x + blockIdx.x) * p.H + h] = gsum * 1.4426950408889634f;
+        for (int off = 8; off > 0; off >>= 1) gsum += __shfl_xor_sync(0xffffffffu, gsum, off);
+        if (lane == 0)
+            dec[((int64_t)c.reverse * gridDim.x + blockIdx.x) * p.H + h] =
+                gsum * 1.4426950408889634f;
+    }
 }
 
 // ------------------------------------------------------------------------ edges --
@@ -357,8 +475,8 @@ Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool e
     if (bwd) {
         l.S_T = take((size_t)N * state);
         l.dS0 = take((size_t)N * state);
-        l.dots_q = take((size_t)(dk / kCols) * T * H * sizeof(float));
-        l.dots_k = take((size_t)(dk / kCols) * T * H * sizeof(float));
+        l.dots_q = take((size_t)(dk / kDotCols) * T * H * sizeof(float));
+        l.dots_k = take((size_t)(dk / kDotCols) * T * H * sizeof(float));
         l.dg = take((size_t)T * H * sizeof(float));
     }
     l.bytes = at;
@@ -375,7 +493,7 @@ Problem problem(const LinearArgs& a, int L) {
 template <typename IO, bool kOut>
 void launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, float* dec,
                   const char* name, cudaStream_t s) {
-    const int blocks = 4;
+    const int blocks = 128 / kCols;
     const dim3 grid((unsigned)slots, p.H, n * blocks);
     bool any[2] = {};
     for (int i = 0; i < n; ++i) any[calls.c[i].da == 128] = true;
@@ -487,7 +605,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
         DecayGrad d{};
         d.segS = at(l.seg[0]); d.segD = at(l.seg[1]);
         d.S_T = at(l.S_T); d.dS_out = a.dS_out; d.S0 = a.S0; d.dS0 = v.S_out;
-        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kCols;
+        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kDotCols;
         d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
         if (a.T_total > 0) {
             ProfScope prof("linear_decay_grad_kernel", a.stream);
