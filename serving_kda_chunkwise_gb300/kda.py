@@ -128,12 +128,14 @@ def _dt(t: torch.Tensor) -> int:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the handle alone: a torch.cuda.Stream object costs more than a short kernel's launch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _need(t: torch.Tensor, name: str, dtype=None):
@@ -448,8 +450,8 @@ def _rows(t: torch.Tensor, name: str, dtype) -> int:
 
 
 def _shape(t: torch.Tensor, name: str, shape):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
 def _decay(g: torch.Tensor, T: int, H: int) -> int:
@@ -501,8 +503,9 @@ def linear_fwd_chunked(q, k, v, g, S0=None, cu_seqlens=None, N=None, o=None, S_o
     dt = _dt(q)
     if o is None:
         o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
-    _need(o, "o", q.dtype)
-    _shape(o, "o", (T, H, dv))
+    else:
+        _need(o, "o", q.dtype)
+        _shape(o, "o", (T, H, dv))
     if S_out is None and want_state:
         S_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
     for t, nm in ((S0, "S0"), (S_out, "S_out")):
@@ -569,8 +572,9 @@ def linear_decode_step(q, k, v, g, S, slots=None, o=None, stream=None):
         _shape(slots, "slots", (N,))
     if o is None:
         o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
-    _need(o, "o", q.dtype)
-    _shape(o, "o", (N, H, dv))
+    else:
+        _need(o, "o", q.dtype)
+        _shape(o, "o", (N, H, dv))
     _check(_lib.kda_linear_decode_step(_ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(g), per_token,
                                        _ptr(S), _ptr(slots), n_slots, N, H, dk, dv, _dt(q),
                                        _ptr(o), _stream(stream)), "kda_linear_decode_step")
@@ -610,13 +614,14 @@ def qk_norm_rope(q, k, wq=None, wk=None, eps: float = 1e-6, cos_sin=None, positi
     lq, lk, n_pos, rot = _qk(q, k, wq, wk, cos_sin, positions)
     T, Hq, d = q.shape
     Hk = k.shape[1]
+    for t, nm, H in ((q_out, "q_out", Hq), (k_out, "k_out", Hk)):
+        if t is not None:
+            _need(t, nm, q.dtype)
+            _shape(t, nm, (T, H, d))
     if q_out is None:
         q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
     if k_out is None:
         k_out = torch.empty((T, Hk, d), dtype=q.dtype, device=q.device)
-    for t, nm, H in ((q_out, "q_out", Hq), (k_out, "k_out", Hk)):
-        _need(t, nm, q.dtype)
-        _shape(t, nm, (T, H, d))
     _check(_lib.kda_qk_norm_rope(_ptr(q), lq, _ptr(k), lk, _ptr(wq), _ptr(wk), eps,
                                  _ptr(cos_sin), n_pos, _ptr(positions), rot, int(interleaved),
                                  _ptr(q_out), _ptr(k_out), T, Hq, Hk, d, _dt(q),
