@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item t = item_at<false>(o, i);
-            const int da = o.calls.c[t.call].da;
+            const int da = o.calls.c[t.call].da, rev = o.calls.c[t.call].reverse;
             const uint32_t n = (uint32_t)(o.calls.c[t.call].db >> 3) << 17;  // N = db
             const uint32_t id_out = (idesc_bf16(128, 0, false, true)) | n;   // A W, X S
             const uint32_t id_up = (idesc_bf16(128, 0, true, true)) | n;     // Y^T W
@@ -664,7 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     mma_bf16(kTA, desc(lX + off), desc(lYk + off), id_sc, ks > 0);
                 }
                 mma_commit(&bar.sc);
-                // the other three, each as soon as its operands are there
+                // the other three, each as soon as its operands are there (A W of a chunk that
+                // ends inside its tile: once the rows past it are cleared, with the decayed W)
+                const bool whole = chunk_at(t, rev, k).len == kC;
                 uint32_t todo = 7;
                 uint64_t since = 0;
                 while (todo) {
@@ -674,7 +676,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                         now = 1;
                     } else if (g == 0 || test(&bar.read, ph ^ 1)) {
                         if ((todo & 2) && s) now = 2;
-                        else if ((todo & 4) && test(&bar.a, ph) && test(&bar.w, ph)) now = 4;
+                        else if ((todo & 4) && test(&bar.a, ph) &&
+                                 test(whole ? &bar.w : &bar.wd, ph))
+                            now = 4;
                     }
                     if (now == 0) {
                         if (since == 0) since = globaltimer();

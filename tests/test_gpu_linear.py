@@ -329,3 +329,63 @@ def test_binding_refusals(kda):
     with pytest.raises(kda.KdaError) as e:
         kda.linear_decode_step(q, k, v, g, torch.zeros(19, 2, 64, 64, device="cuda"))
     assert "n_slots" in str(e.value)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lengths", [[70, 45, 60], [300, 45, 1000]], ids=str)
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")], ids=str)
+def test_not_finite_stays_in_its_sequence(kda, dtype, lengths, bad):
+    """A sequence of NaN or infinities, tokens, decays and state, leaves the others' results as
+    they were, bit for bit; fp32 outputs before the token too."""
+    import torch
+    x = _inputs(21, lengths, 2, 128, 64, dtype)
+
+    def run():
+        o, S = kda.linear_fwd_chunked(x["q"], x["k"], x["v"], x["g"], S0=x["S0"],
+                                      cu_seqlens=x["cu"])
+        b = kda.linear_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS_out=x["dS"],
+                           cu_seqlens=x["cu"])
+        return dict(b, o=o, S=S)
+
+    first = run()
+    a, b = lengths[0], lengths[0] + lengths[1]
+    for n in ("q", "k", "v", "do", "g"):
+        x[n][a:b] = bad
+    x["S0"][1] = x["dS"][1] = bad
+    second = run()
+    kda.device_status()
+    for n, t in second.items():
+        if n in ("S", "dS0"):
+            assert torch.equal(t[[0, 2]], first[n][[0, 2]]), n
+        else:
+            assert torch.equal(t[:a], first[n][:a]) and torch.equal(t[b:], first[n][b:]), n
+    assert not bool(torch.isfinite(second["o"][a:b]).any())
+    if dtype == "f32":
+        x = _inputs(22, lengths, 2, 128, 64, dtype)
+        first, _ = kda.linear_fwd_chunked(x["q"], x["k"], x["v"], x["g"], cu_seqlens=x["cu"])
+        x["k"][40] = bad
+        second, _ = kda.linear_fwd_chunked(x["q"], x["k"], x["v"], x["g"], cu_seqlens=x["cu"])
+        assert torch.equal(second[:40], first[:40])
+
+
+def test_bf16_token_by_token(kda, monkeypatch):
+    """bf16 on CUDA cores (the path of fp32), which the environment can ask for."""
+    monkeypatch.setenv("KDA_FWD_PATH", "generic")
+    for lengths in ([40, 0, 300], [700, 129]):
+        x = _inputs(23, lengths, 3, 64, 128, "bf16")
+        _check_fwd(kda, x)
+        _check_bwd(kda, x)
+
+
+@pytest.mark.parametrize("decay", [0.003, 0.49, 0.51, 9.0])
+def test_f32_fixed_decay_over_many_tokens(kda, decay):
+    """One decay for all of 4000 tokens: its own rounding must not add up."""
+    import linear_ref
+    import torch
+    x = _inputs(24, [4000], 2, 64, 64, "f32", per_token=False)
+    x["g"] = torch.full((2,), -decay, device="cuda")
+    o, S = kda.linear_fwd_chunked(x["q"], x["k"], x["v"], x["g"], S0=x["S0"], cu_seqlens=x["cu"])
+    ro, rS = linear_ref.forward(x["q"], x["k"], x["v"], x["g"], x["S0"], x["lengths"])
+    # fp32 sums of some hundred terms, 2^-24 each in quadrature: below 2e-6
+    assert float((o.double() - ro).norm()) <= 2e-6 * float(ro.norm())
+    assert float((S.double() - rS).norm()) <= 2e-6 * float(rS.norm())
