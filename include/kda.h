@@ -234,7 +234,10 @@ kda_status_t kda_decode_step_gated(const void *q, const void *k, const void *v,
  *   o      : [T_total, H, dv] io_dt (written)
  *   workspace : device scratch of kda_linear_fwd_workspace_size(...) bytes (NULL when 0)
  * Long sequences are cut into segments that run in parallel: one launch forms each segment's
- * contribution to the state, one the states at the segment starts, one the outputs.
+ * contribution to the state, one the states at the segment starts, one the outputs (for bf16
+ * after a short one that sums the log decays).
+ * A token whose q, k, v or g is not finite spoils its sequence from there on, for bf16 also up
+ * to 127 tokens before it (masked products are formed); other sequences stay as they are.
  */
 size_t kda_linear_fwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv,
                                      kda_dtype_t io_dt);
@@ -253,7 +256,8 @@ kda_status_t kda_linear_fwd_chunked(const void *q, int64_t q_ld, const void *k, 
  *   dq = S_t do_t, dk = D_t v_t : [T_total, H, dk] io_dt      dv = D_t^T k_t : [T_total, H, dv]
  *   dg  : fp32, [T_total, H] when g_per_token, else [H] (summed over all tokens), or NULL
  *   dS0 : [N, H, dk, dv] fp32, or NULL when not wanted
- * Deterministic.  Gradients with respect to g = -inf are computed as for any other g.
+ * Deterministic.  Gradients with respect to g = -inf are computed as for any other g.  Inputs
+ * that are not finite spoil their own sequence only (and dg [H], which sums over all).
  */
 size_t kda_linear_bwd_workspace_size(int64_t T_total, int N, int H, int dk, int dv,
                                      kda_dtype_t io_dt);
