@@ -833,10 +833,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.a);
+                // the second half of its 64 output columns (the state warps write the first)
                 const float rowf = __ldg(it.record(o, k) + (it.rev() ? kRTail : kRHead) + row);
-#pragma unroll 1
-                for (int hf = 0; ok && hf < 2; ++hf)
-                    ok = write_out<kDots>(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32 * hf);
+                ok = write_out<kDots>(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32);
                 if (!ok) break;
             }
         }
@@ -873,126 +872,143 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             if (!wait(&bar.open, opened & 1, p.err, abort)) { ok = false; break; }
             ++opened;
 
-            const int own = it.rev() ? kRHead : kRTail;
-            float next, total;
+            float rowf_prev = 0.f, head, tail, total;
             {
                 const float* r = it.record(o, 0);
-                next = __ldg(r + own + row);
+                head = __ldg(r + kRHead + row);
+                tail = __ldg(r + kRTail + row);
                 total = __ldg(r + kRCol + kRB + 4);
             }
-            // the state's copy, then the decayed W
+            // step k: the outputs of chunk k - 1 and the state's copy of chunk k, then chunk k's
+            // decayed W (the outputs' products were the last to read W's buffer, so its load runs
+            // meanwhile)
 #pragma unroll 1
-            for (int k = 0; k < it.chunks(); ++k, ++g) {
-                const float wf = next, all = ex2f(total);
+            for (int k = 0; k <= it.chunks(); ++k) {
+                const int rev = it.rev();
+                const float rowf = rev ? tail : head, wf = rev ? head : tail, all = ex2f(total);
                 if (k + 1 < it.chunks()) {  // the next chunk's, early
                     const float* r = it.record(o, k + 1);
-                    next = __ldg(r + own + row);
+                    head = __ldg(r + kRHead + row);
+                    tail = __ldg(r + kRTail + row);
                     total = __ldg(r + kRCol + kRB + 4);
                 }
-                // the last update of the state, the last read of its copy and of the decayed
-                // W's buffer are complete
-                if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
-                              !wait(&bar.xs, (g - 1) & 1, p.err, abort))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (cols) {
-                    uint8_t* sr = sm + kSS + wg * 16384 + row * 128;
+                // first whichever of the two has its products complete
+                const bool outputs_first =
+                    k == it.chunks() ||
+                    (k > 0 && __all_sync(0xffffffffu, test(&bar.aw, (g - 1) & 1)));
 #pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
-                        float S[16];
-                        tmem_ld16(at + kTS + 16 * b, S);
-                        landed(S);
-                        if (holds)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                uint4 hi, lo;
-                                split2(S[8 * x], S[8 * x + 1], hi.x, lo.x);
-                                split2(S[8 * x + 2], S[8 * x + 3], hi.y, lo.y);
-                                split2(S[8 * x + 4], S[8 * x + 5], hi.z, lo.z);
-                                split2(S[8 * x + 6], S[8 * x + 7], hi.w, lo.w);
-                                const uint32_t to = ((2 * b + x) ^ (row & 7)) << 4;
-                                *reinterpret_cast<uint4*>(sr + to) = hi;
-                                *reinterpret_cast<uint4*>(sr + 32768 + to) = lo;
-                            }
-                        uint32_t u[16];
-#pragma unroll
-                        for (int x = 0; x < 16; x += 2) {
-                            mul2(S[x], S[x + 1], all, all);
-                            u[x] = __float_as_uint(S[x]);
-                            u[x + 1] = __float_as_uint(S[x + 1]);
-                        }
-                        tmem_st16(at + kTS + 16 * b, u);
+                for (int part = 0; ok && part < 2; ++part) {
+                    if ((part == 0) == outputs_first) {
+                        if (k > 0)
+                            ok = write_out<kDots>(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev, 64 * wg);
+                        continue;
                     }
-                    tmem_st_wait();
+                    if (k == it.chunks()) continue;
+                    // the last update of the state, the last read of its copy and of the decayed
+                    // W's buffer are complete
+                    if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
+                                  !wait(&bar.xs, (g - 1) & 1, p.err, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (cols) {
+                        uint8_t* sr = sm + kSS + wg * 16384 + row * 128;
+#pragma unroll 1
+                        for (int b = 0; b < 4; ++b) {
+                            float S[16];
+                            tmem_ld16(at + kTS + 16 * b, S);
+                            landed(S);
+                            if (holds)
+#pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    uint4 hi, lo;
+                                    split2(S[8 * x], S[8 * x + 1], hi.x, lo.x);
+                                    split2(S[8 * x + 2], S[8 * x + 3], hi.y, lo.y);
+                                    split2(S[8 * x + 4], S[8 * x + 5], hi.z, lo.z);
+                                    split2(S[8 * x + 6], S[8 * x + 7], hi.w, lo.w);
+                                    const uint32_t to = ((2 * b + x) ^ (row & 7)) << 4;
+                                    *reinterpret_cast<uint4*>(sr + to) = hi;
+                                    *reinterpret_cast<uint4*>(sr + 32768 + to) = lo;
+                                }
+                            uint32_t u[16];
+#pragma unroll
+                            for (int x = 0; x < 16; x += 2) {
+                                mul2(S[x], S[x + 1], all, all);
+                                u[x] = __float_as_uint(S[x]);
+                                u[x + 1] = __float_as_uint(S[x + 1]);
+                            }
+                            tmem_st16(at + kTS + 16 * b, u);
+                        }
+                        tmem_st_wait();
+                        fence_async_smem();
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.s);
+                }
+                if (!ok) break;
+                if (k < it.chunks()) {
+                    if (!wait(&bar.w, g & 1, p.err, abort) ||
+                        (g > 0 && !wait(&bar.stored, (g - 1) & 1, p.err, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    const int len = it.chunk(k).len;
+                    const bool dead = row >= len;
+                    if (cols) {
+                        const uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
+                        uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
+#pragma unroll 1
+                        for (int b = 0; b < 2; ++b) {
+                            uint4 in[4];
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                in[x] = *reinterpret_cast<const uint4*>(
+                                    wr + (((4 * b + x) ^ (row & 7)) << 4));
+                            if (dead)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) in[x] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                                uint32_t hi[4], lo[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    float a0 = __uint_as_float(w[y] << 16);
+                                    float a1 = __uint_as_float(w[y] & 0xffff0000u);
+                                    mul2(a0, a1, wf, wf);
+                                    split2(a0, a1, hi[y], lo[y]);
+                                }
+                                const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
+                                *reinterpret_cast<uint4*>(wd + to) =
+                                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                *reinterpret_cast<uint4*>(wd + 32768 + to) =
+                                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            }
+                        }
+                    }
+                    if (len < kC) {
+                        // rows past the segment hold another sequence's tokens (or zeros): they
+                        // must not reach a product even as 0 * inf.  (X Y^T is masked instead.)
+                        if (!wait(&bar.y, g & 1, p.err, abort)) { ok = false; break; }
+                        if (dead) {
+                            uint4* wr = reinterpret_cast<uint4*>(sm + kSW + wg * 16384 + row * 128);
+                            uint4* yr = reinterpret_cast<uint4*>(sm + kSY + wg * 16384 + row * 128);
+#pragma unroll 1
+                            for (int x = 0; x < 8; ++x) wr[x] = yr[x] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                    }
                     fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.wd);
+                    ++g;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.s);
-                if (!wait(&bar.w, g & 1, p.err, abort) ||
-                    (g > 0 && !wait(&bar.stored, (g - 1) & 1, p.err, abort))) {
-                    ok = false;
-                    break;
-                }
-                const int len = it.chunk(k).len;
-                const bool dead = row >= len;
-                if (cols) {
-                    const uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
-                    uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
-#pragma unroll 1
-                    for (int b = 0; b < 2; ++b) {
-                        uint4 in[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            in[x] = *reinterpret_cast<const uint4*>(
-                                wr + (((4 * b + x) ^ (row & 7)) << 4));
-                        if (dead)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) in[x] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
-                            uint32_t hi[4], lo[4];
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) {
-                                float a0 = __uint_as_float(w[y] << 16);
-                                float a1 = __uint_as_float(w[y] & 0xffff0000u);
-                                mul2(a0, a1, wf, wf);
-                                split2(a0, a1, hi[y], lo[y]);
-                            }
-                            const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
-                            *reinterpret_cast<uint4*>(wd + to) =
-                                make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(wd + 32768 + to) =
-                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        }
-                    }
-                }
-                if (len < kC) {
-                    // rows past the segment hold another sequence's tokens (or zeros): they
-                    // must not reach a product even as 0 * inf.  (X Y^T is masked instead.)
-                    if (!wait(&bar.y, g & 1, p.err, abort)) { ok = false; break; }
-                    if (dead) {
-                        uint4* wr = reinterpret_cast<uint4*>(sm + kSW + wg * 16384 + row * 128);
-                        uint4* yr = reinterpret_cast<uint4*>(sm + kSY + wg * 16384 + row * 128);
-#pragma unroll 1
-                        for (int x = 0; x < 8; ++x) wr[x] = yr[x] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.wd);
+                rowf_prev = rowf;
             }
             if (!ok) break;
             if (it.v[View::kFinal] >= 0) {
-                // (it passes through the copy's buffer)
-                if (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
-                    !wait(&bar.xs, (g - 1) & 1, p.err, abort)) {
-                    ok = false;
-                    break;
-                }
+                if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
                 store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg, stage);
                 tc_fence_before();
