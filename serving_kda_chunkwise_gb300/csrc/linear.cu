@@ -568,7 +568,7 @@ cudaError_t launch_linear_fwd(const LinearArgs& a) {
     Call& c = calls.c[0];
     c.x = a.q; c.x_ld = a.q_ld; c.y = a.k; c.y_ld = a.k_ld; c.w = a.v; c.w_ld = a.v_ld;
     c.da = a.dk; c.db = a.dv; c.edge = a.S0; c.S_out = a.S_out; c.out = a.o;
-    c.seg = reinterpret_cast<float*>(ws + l.seg[0]);
+    c.seg = l.segments ? reinterpret_cast<float*>(ws + l.seg[0]) : nullptr;
     return launch_calls<true>(a, p, calls, 1, l, nullptr, "linear_out_kernel");
 }
 
@@ -585,25 +585,26 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, true)) return e;
     const bool anchor = a.dg && a.dS_out;
+    float* const seg[2] = {l.segments ? at(l.seg[0]) : nullptr, l.segments ? at(l.seg[1]) : nullptr};
     Calls calls{};
     Call &q = calls.c[0], &k = calls.c[1], &v = calls.c[2];
     q.x = a.dout; q.x_ld = a.dout_ld; q.y = a.v; q.y_ld = a.v_ld; q.w = a.k; q.w_ld = a.k_ld;
-    q.da = a.dv; q.db = a.dk; q.tr = 1; q.edge = a.S0; q.seg = at(l.seg[0]);
+    q.da = a.dv; q.db = a.dk; q.tr = 1; q.edge = a.S0; q.seg = seg[0];
     q.S_out = anchor ? at(l.S_T) : nullptr; q.out = a.dq;
     if (a.dg) { q.dot = a.q; q.dot_ld = a.q_ld; q.dots = at(l.dots_q); }
     k.x = a.v; k.x_ld = a.v_ld; k.y = a.dout; k.y_ld = a.dout_ld; k.w = a.q; k.w_ld = a.q_ld;
-    k.da = a.dv; k.db = a.dk; k.reverse = 1; k.tr = 1; k.edge = a.dS_out; k.seg = at(l.seg[1]);
+    k.da = a.dv; k.db = a.dk; k.reverse = 1; k.tr = 1; k.edge = a.dS_out; k.seg = seg[1];
     k.out = a.dk_;
     if (a.dg) { k.dot = a.k; k.dot_ld = a.k_ld; k.dots = at(l.dots_k); }
     v.x = a.k; v.x_ld = a.k_ld; v.y = a.q; v.y_ld = a.q_ld; v.w = a.dout; v.w_ld = a.dout_ld;
-    v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = at(l.seg[1]);
+    v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = seg[1];
     v.S_out = a.dS0 ? a.dS0 : a.dg && a.S0 ? at(l.dS0) : nullptr; v.out = a.dv_;
     if (cudaError_t e =
             launch_calls<true>(a, p, calls, 3, l, nullptr, "linear_grad_kernel"))
         return e;
     if (a.dg) {
         DecayGrad d{};
-        d.segS = at(l.seg[0]); d.segD = at(l.seg[1]);
+        d.segS = seg[0]; d.segD = seg[1];
         d.S_T = at(l.S_T); d.dS_out = a.dS_out; d.S0 = a.S0; d.dS0 = v.S_out;
         d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kDotCols;
         d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;

@@ -39,7 +39,7 @@ struct Call {
     int reverse;
     int tr;              // states in memory are [db][da] instead of [da][db]
     const float* edge;   // [N][H][...] state before the first (reversed: after the last) token
-    const float* seg;    // [slots][H][...] state at the other segments' edges
+    const float* seg;    // [slots][H][...] state at the other segments' edges, or nullptr
     float* S_out;        // [N][H][...] state after the sequence (reversed: before it), or nullptr
     void* out;           // [T][H][db]
     const void* dot;     // [T][H][db] rows, or nullptr: dots[b][t][h] = sum over column block b

@@ -146,7 +146,8 @@ struct Item {
 struct OutParams {
     Problem p;
     lin::Calls calls;
-    CUtensorMap x[lin::kMaxCalls], y[lin::kMaxCalls], w[lin::kMaxCalls], out[lin::kMaxCalls];
+    CUtensorMap x[lin::kMaxCalls], y[lin::kMaxCalls], w[lin::kMaxCalls];
+    CUtensorMap seg[lin::kMaxCalls], edge[lin::kMaxCalls];  // states (outputs only)
     int n_calls;
     int slots;
     const float* rec;  // decay records, see decay_kernel
@@ -278,8 +279,8 @@ constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
 constexpr uint32_t kSWd = 98304;             // decayed W: hi, lo
 constexpr uint32_t kSS = kSWd + 65536;       // state: hi, lo
 constexpr uint32_t kSRec = kSS + 65536;      // the record's part for the call's direction
-constexpr uint32_t kSItem = kSRec + 1088;    // the 16 warps' items, 12 words each
-constexpr uint32_t kSBar = kSItem + 768;
+constexpr uint32_t kSItem = kSRec + 1088;    // this item's facts and the next one's
+constexpr uint32_t kSBar = kSItem + 128;
 constexpr uint32_t kOutSmem = kSBar + 256;
 static_assert(kOutSmem <= 232448, "shared-memory limit");
 // TMEM columns (all 512 are allocated, so the base address is 0): X Y^T / A, A W, X S, state
@@ -291,17 +292,61 @@ struct OutBars {
     uint64_t s, wd;          // state and its copy written; decayed W written (8 arrivals each)
     uint64_t upd, xs, aw;    // state update, X S, A W complete
     uint64_t read;           // the chunk's outputs read from TMEM (16 arrivals)
-    uint64_t staged, stored; // ... and staged (16 arrivals); the stage read by the store
-    uint64_t open;           // the item's state loaded (8 arrivals)
+    uint64_t stored;         // ... and read from their stage (16 arrivals)
+    uint64_t item[2];        // an item's facts are there
+    uint64_t used[2];        // ... and done with (16 arrivals)
+    uint64_t idle;           // the last item's state is done with (8 arrivals)
+    uint64_t open, taken;    // the item's state loaded; all of it taken over (8 arrivals)
     uint64_t drain;
     uint32_t tmem;
     int abort;
 };
 static_assert(sizeof(OutBars) <= 256, "barrier area");
 
+// What the warps need of an item, kept in shared memory: their registers are few, and what the
+// compiler would put into local memory comes back from L2 (shared memory takes all of L1).  One
+// thread finds it, an item ahead: by each warp for itself an item began 4000 cycles later.
+struct View {
+    volatile int* v;
+    enum { kBegin, kEnd, kChunks, kCall, kH, kRev, kRecord, kZero, kFinal, kWords };
+    __device__ __forceinline__ int chunks() const { return v[kChunks]; }
+    __device__ __forceinline__ int call() const { return v[kCall]; }
+    __device__ __forceinline__ int h() const { return v[kH]; }
+    __device__ __forceinline__ int rev() const { return v[kRev]; }
+    __device__ __forceinline__ Chunk chunk(int k) const {
+        Chunk c;
+        c.i = v[kRev] ? v[kChunks] - 1 - k : k;
+        c.t0 = v[kBegin] + c.i * kC;
+        c.len = min(v[kEnd] - c.t0, kC);
+        return c;
+    }
+    __device__ __forceinline__ const float* record(const OutParams& o, int k) const {
+        const int i = v[kRev] ? v[kChunks] - 1 - k : k;
+        return o.rec + ((size_t)(v[kRecord] + i) * o.p.H + v[kH]) * kRec;
+    }
+};
+__device__ __forceinline__ View view(uint8_t* sm, uint32_t n) {
+    return View{reinterpret_cast<volatile int*>(sm + kSItem) + 12 * (n & 1)};
+}
+static_assert(2 * 12 * 4 <= kSBar - kSItem && View::kWords <= 12, "items' facts");
+__device__ __forceinline__ void put_item(const OutParams& o, const Item& t, View w) {
+    const int rev = o.calls.c[t.call].reverse;
+    w.v[View::kBegin] = t.sg.begin;
+    w.v[View::kEnd] = t.sg.end;
+    w.v[View::kChunks] = t.chunks;
+    w.v[View::kCall] = t.call;
+    w.v[View::kH] = t.h;
+    w.v[View::kRev] = rev;
+    w.v[View::kRecord] = t.slot * (o.p.L / kC);
+    w.v[View::kZero] = t.sg.count <= 1 && o.calls.c[t.call].edge == nullptr;
+    // (an empty sequence's first slot passes the state on: kChunks = 0, kFinal >= 0)
+    const bool last = t.sg.live ? (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1)
+                                : t.sg.count == 0 && t.sg.s == 0;
+    w.v[View::kFinal] = last ? t.sg.n : -1;  // whose final state follows, if any
+}
+
 // One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each once
-// the last chunk's buffer has been read.  W's also stores the outputs, for it is idle then.
-// Returns the number of chunks loaded.
+// the last chunk's buffer has been read.  Returns the number of chunks loaded.
 __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int which, uint8_t* sm) {
     const CUtensorMap* maps = which == 0 ? o.x : which == 1 ? o.y : o.w;
     uint8_t* dst = sm + (which == 0 ? kSX : which == 1 ? kSY : kSW);
@@ -310,26 +355,37 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
     volatile int* abort = &bar.abort;
     unsigned* err = o.p.err;
     const uint32_t items = item_count(o);
-    int call = 0, h = 0, t0 = -1;  // the last chunk's outputs: t0 < 0 where rows were written
-    auto store = [&](uint32_t phase) {
-        if (!wait1(&bar.staged, phase, err, abort)) return false;
-        if (t0 >= 0) {
-#pragma unroll 1
-            for (int b = 0; b < o.calls.c[call].db / 64; ++b)
-                tma_store_3d(&o.out[call], sm + kSWd + b * 16384, 64 * b, h, t0);
-            bulk_commit();
-            bulk_wait_read0();
-        }
-        mbar_arrive(&bar.stored);
-        return true;
-    };
     int g = 0;
-    for (uint32_t i = blockIdx.x; i < items; i += gridDim.x) {
+    uint32_t states = 0, n = 0;
+    for (uint32_t i = blockIdx.x; i < items; i += gridDim.x, ++n) {
         const Item t = item_at<false>(o, i);
         const Call& c = o.calls.c[t.call];
+        if (which == 0) {
+            if (n > 1 && !wait1(&bar.used[n & 1], ((n >> 1) - 1) & 1, err, abort)) return g;
+            put_item(o, t, view(sm, n));
+            mbar_arrive(&bar.item[n & 1]);
+        }
         const int blocks = (which == 2 ? c.db : c.da) / 64;
         for (int k = 0; k < t.chunks; ++k, ++g) {
             const uint32_t last = (g - 1) & 1;
+            if (which == 2 && k == 0) {  // the item's state, through its copy's buffer
+                if (states > 0 && !wait1(&bar.idle, (states - 1) & 1, err, abort)) return g;
+                const bool own = t.sg.count <= 1;
+                const CUtensorMap* m = (own ? o.edge : o.seg) + t.call;
+                if (!own || c.edge) {
+                    const int inner = c.tr ? c.da : c.db, bytes = (c.tr ? c.db : c.da) * 128;
+                    mbar_expect_tx(&bar.open, inner / 32 * bytes);
+#pragma unroll 1
+                    for (int b = 0; b < inner / 32; ++b)
+                        tma_load_3d(sm + kSS + b * bytes, m, 32 * b, 0,
+                                    (own ? t.sg.n : t.slot) * o.p.H + t.h, &bar.open);
+                } else {
+                    mbar_arrive(&bar.open);
+                }
+                // (it has landed before this thread can come to any way out)
+                mbar_wait(&bar.open, states & 1, nullptr);
+                ++states;
+            }
             if (g > 0 && !wait1(freed, last, err, abort)) return g;
             if (which == 2 && g > 0 && !wait1(&bar.wd, last, err, abort)) return g;
             const Chunk ch = chunk_at(t, c.reverse, k);
@@ -343,12 +399,6 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
                 for (int b = 0; b < blocks; ++b)
                     tma_prefetch_3d(maps + t.call, 64 * b, t.h, ahead);
             }
-            if (which == 2) {
-                if (g > 0 && !store(last)) return g + 1;
-                call = t.call;
-                h = t.h;
-                t0 = ch.len == kC ? ch.t0 : -1;
-            }
             if (which == 0) {
                 if (g > 0 && !wait1(&bar.a, last, err, abort)) return g + 1;
                 mbar_expect_tx(&bar.rec, 4 * kRDir);
@@ -357,7 +407,6 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
             }
         }
     }
-    if (which == 2 && g > 0) store((g - 1) & 1);
     return g;
 }
 
@@ -376,60 +425,39 @@ __device__ __forceinline__ StateAt state_at(const OutParams& o, const Call& c, i
     s.holds = col < c.db && row < c.da;
     return s;
 }
-// A [da][db] state's rows lie 4 db bytes apart, one a lane: read or written from the lanes, each
-// access would touch 32 lines (an item's 64 KB took 20,000 cycles).  The warp's 32 x 64 piece goes
-// through 8 KB of shared memory instead, 16-byte pieces permuted by the row.
+// A [da][db] state's rows lie 4 db bytes apart, one a lane: written from the lanes, each access
+// would touch 32 lines.  The warp's 32 x 64 piece goes through 8 KB of shared memory instead,
+// 16-byte pieces permuted by the row.  (States are read by TMA: by the warps themselves an item's
+// 64 KB took 15,000 cycles.)
 __device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 256 + ((c ^ (r & 15)) << 4); }
 
-// which >= 0: sequence `which`'s own state at its edge (zeros without one), else the edge state
-// of the segment in slot -1 - which.  `stage`: the warp's 8 KB.
-__device__ __noinline__ void load_state(const OutParams& o, int call, int which, int h, int col,
-                                        uint8_t* stage) {
+// The item's state from the buffer that the copy is to have, where 32-float boxes of its rows in
+// memory lie (128 bytes a row, 16-byte pieces permuted by the row), into TMEM.
+__device__ __noinline__ void load_state(const OutParams& o, int call, bool zero, int col,
+                                        const uint8_t* buf) {
     const Call& c = o.calls.c[call];
-    const int lane = threadIdx.x & 31, row0 = threadIdx.x & 96;
-    const StateAt s = state_at(o, c, which < 0 ? -1 - which : which, h, col);
-    const float* from = which < 0 ? c.seg : c.edge;
-    const uint32_t to = (static_cast<uint32_t>(row0) << 16) + kTS + col;
-    const bool rows = col < c.db && row0 < c.da;  // (da is a multiple of a warp's rows)
-    if (from && rows && !c.tr) {
-        const float* f = from + s.at - (int64_t)lane * c.db;
+    const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    const uint32_t to = (static_cast<uint32_t>(row & 96) << 16) + kTS + col;
+    zero = zero || col >= c.db || (row & 96) >= c.da;
 #pragma unroll 1
-        for (int b = 0; b < 2; ++b) {
-            float4 v[8];
+    for (int b = 0; b < 4; ++b) {
+        uint32_t u[16];
+        if (zero) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                v[x] = __ldcg(reinterpret_cast<const float4*>(
-                                  f + (int64_t)(16 * b + 2 * x + (lane >> 4)) * c.db) +
-                              (lane & 15));
+            for (int x = 0; x < 16; ++x) u[x] = 0u;
+        } else if (c.tr) {
+            const uint8_t* f = buf + (row >> 5) * c.db * 128 + (col + 16 * b) * 128 + (lane & 3) * 4;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                *reinterpret_cast<float4*>(stage + piece_at(16 * b + 2 * x + (lane >> 4),
-                                                            lane & 15)) = v[x];
+            for (int x = 0; x < 16; ++x)
+                u[x] = *reinterpret_cast<const uint32_t*>(f + x * 128 + ((lane >> 2 ^ (x & 7)) << 4));
+        } else {
+            const uint8_t* f = buf + ((col >> 5) + (b >> 1)) * c.da * 128 + row * 128;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                reinterpret_cast<uint4*>(u)[x] = *reinterpret_cast<const uint4*>(
+                    f + ((4 * (b & 1) + x ^ (row & 7)) << 4));
         }
-        __syncwarp();
-    }
-#pragma unroll 1
-    for (int b = 0; b < 2; ++b) {
-        uint32_t u[32];
-#pragma unroll
-        for (int x = 0; x < 32; ++x) u[x] = 0u;
-        if (from && rows) {
-            if (c.tr) {
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    u[x] = __float_as_uint(__ldcg(from + s.at + (32 * b + x) * s.cs));
-            } else {
-#pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(stage + piece_at(lane, 8 * b + x));
-                    u[4 * x] = v.x;
-                    u[4 * x + 1] = v.y;
-                    u[4 * x + 2] = v.z;
-                    u[4 * x + 3] = v.w;
-                }
-            }
-        }
-        tmem_st32(to + 32 * b, u);
+        tmem_st16(to + 16 * b, u);
     }
     tmem_st_wait();
     __syncwarp();
@@ -475,82 +503,39 @@ __device__ __noinline__ void pass_state(const OutParams& o, int call, int n, int
             c.S_out[s.at + x * s.cs] = c.edge ? c.edge[s.at + x * s.cs] : 0.f;
 }
 
-// What a warp's chunks need of its item, kept in shared memory: the roles' registers are few, and
-// what the compiler would put into local memory comes back from L2 (shared memory takes all of L1).
-struct View {
-    volatile int* v;
-    enum { kBegin, kEnd, kChunks, kCall, kH, kRev, kRecord, kEdge, kFinal, kWords };
-    __device__ __forceinline__ int chunks() const { return v[kChunks]; }
-    __device__ __forceinline__ int call() const { return v[kCall]; }
-    __device__ __forceinline__ int h() const { return v[kH]; }
-    __device__ __forceinline__ int rev() const { return v[kRev]; }
-    __device__ __forceinline__ Chunk chunk(int k) const {
-        Chunk c;
-        c.i = v[kRev] ? v[kChunks] - 1 - k : k;
-        c.t0 = v[kBegin] + c.i * kC;
-        c.len = min(v[kEnd] - c.t0, kC);
-        return c;
-    }
-    __device__ __forceinline__ const float* record(const OutParams& o, int k) const {
-        const int i = v[kRev] ? v[kChunks] - 1 - k : k;
-        return o.rec + ((size_t)(v[kRecord] + i) * o.p.H + v[kH]) * kRec;
-    }
-};
-// Whole warps: the item's facts for the warp's chunks.
-__device__ __noinline__ void open_item(const OutParams& o, uint32_t i, View w) {
-    const Item t = item_at<true>(o, i);
-    const int rev = o.calls.c[t.call].reverse;
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-        w.v[View::kBegin] = t.sg.begin;
-        w.v[View::kEnd] = t.sg.end;
-        w.v[View::kChunks] = t.chunks;
-        w.v[View::kCall] = t.call;
-        w.v[View::kH] = t.h;
-        w.v[View::kRev] = rev;
-        w.v[View::kRecord] = t.slot * (o.p.L / kC);
-        // where the state comes from: load_state()'s argument; an empty sequence's first slot
-        // passes the state on (kChunks = 0, kFinal >= 0)
-        w.v[View::kEdge] = t.sg.count > 1 ? -1 - t.slot : t.sg.n;
-        const bool last = t.sg.live ? (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1)
-                                    : t.sg.count == 0 && t.sg.s == 0;
-        w.v[View::kFinal] = last ? t.sg.n : -1;  // whose final state follows, if any
-    }
-    __syncwarp();
-}
-
 // Outputs of one chunk, 32 columns from `col` of one row a lane: rowf (X S) + A W, and
-// their dot products with another row where wanted.  Whole chunks are staged in the decayed W's
-// buffer (whose product is complete, and which the next chunk's overwrites only once its W is
-// there) and stored by TMA: written row by row from the lanes they kept the load/store unit busy
-// for 2000 cycles.  A warp's 32 rows are its TMEM lanes; out of
-// line, for both groups of warps call it.
+// their dot products with another row where wanted.  A warp's 32 rows are its TMEM lanes: stored
+// from there, each access would touch 32 lines and keep the load/store unit busy for 2000 cycles,
+// so a warp passes its 2 KB through the decayed W's buffer (whose product is complete, and which
+// the next chunk's overwrites only then).  A TMA store of the whole tile kept that buffer for
+// 2200 cycles.
 template <bool kDots>
 __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint8_t* sm,
                                           uint32_t phase, View it, int k, float rowf, int col) {
-    const int row = threadIdx.x & 127;
+    const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
+    const Call& c = o.calls.c[it.call()];
+    const int db = c.db, h = it.h();
+    const Chunk ch = it.chunk(k);
+    const bool cols = col < db, dots = kDots && cols && row < ch.len && c.dot != nullptr;
+    uint4 d[kDots ? 4 : 1];
+    if (dots) {
+        const uint4* dr = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(c.dot) + (int64_t)(ch.t0 + row) * c.dot_ld + h * db +
+            col);
+#pragma unroll
+        for (int x = 0; x < (kDots ? 4 : 0); ++x) d[x] = __ldg(dr + x);
+    }
     if (!wait(&bar.aw, phase, o.p.err, &bar.abort) ||
         !wait(&bar.xs, phase, o.p.err, &bar.abort) ||
         !wait(&bar.upd, phase, o.p.err, &bar.abort))
         return false;
     tc_fence_after();
-    const Call& c = o.calls.c[it.call()];
-    const int db = c.db, h = it.h();
-    const Chunk ch = it.chunk(k);
-    const int tr = ch.t0 + row;
-    const bool cols = col < db;
-    const bool in = cols && row < ch.len, dots = kDots && c.dot != nullptr;
     const uint32_t from = (static_cast<uint32_t>(row & 96) << 16) + col;
+    uint8_t* stage = sm + kSWd + (col >> 6) * 16384;
+    const int piece = (col & 32) >> 3;  // of 16 bytes, within the 128 of a row
     float acc = 0.f;
-#pragma unroll 1
+#pragma unroll
     for (int b = 0; b < 2; ++b) {  // 16 columns at a time, to stay within the registers
-        uint4 d[2];
-        if (in && dots) {
-            const uint4* dr = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(c.dot) + (int64_t)tr * c.dot_ld + h * db + col);
-            d[0] = __ldg(dr + 2 * b);
-            d[1] = __ldg(dr + 2 * b + 1);
-        }
         float o1[16];
         if (cols) {
             float o2[8];
@@ -568,27 +553,21 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
         if (b == 1) {  // the accumulators may be written again
             tc_fence_before();
             __syncwarp();
-            if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.read);
+            if (lane == 0) mbar_arrive(&bar.read);
         }
-        if (!in) continue;
-        uint8_t* stage = sm + kSWd + (col >> 6) * 16384 + row * 128;
-        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.out) +
-                                              ((int64_t)tr * o.p.H + h) * db + col + 16 * b);
+        if (!cols) continue;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const float* w = o1 + 8 * x;
-            const uint4 u = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
-                                       pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
-            if (ch.len < kC)  // (a stored tile would reach into the next sequence)
-                out[x] = u;
-            else
-                *reinterpret_cast<uint4*>(
-                    stage + ((((col & 32) >> 3) + 2 * b + x) ^ (row & 7)) * 16) = u;
+            *reinterpret_cast<uint4*>(stage + row * 128 + ((piece + 2 * b + x) ^ (row & 7)) * 16) =
+                make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
+                           pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
         }
         if (dots) {
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const uint32_t w[4] = {d[x].x, d[x].y, d[x].z, d[x].w};
+                const uint4 e = d[kDots ? 2 * b + x : 0];
+                const uint32_t w[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     acc = fmaf(o1[8 * x + 2 * y], __uint_as_float(w[y] << 16), acc);
@@ -597,10 +576,28 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
             }
         }
     }
-    if (in && dots) c.dots[((int64_t)(col >> 5) * o.p.T + tr) * o.p.H + h] = acc;
-    fence_async_smem();
+    if (dots) c.dots[((int64_t)(col >> 5) * o.p.T + ch.t0 + row) * o.p.H + h] = acc;
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar.staged);
+    // four lanes a row; rows 4 apart share a phase, for their pieces lie in different banks
+    const int r0 = (row & 96) + (lane >> 3) + (lane & 4);
+    uint4 u[4];
+    if (cols)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = r0 + 8 * j;
+            u[j] = *reinterpret_cast<const uint4*>(stage + r * 128 +
+                                                   ((piece + (lane & 3)) ^ (r & 7)) * 16);
+        }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.stored);
+    if (cols) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(c.out) +
+                             ((int64_t)(ch.t0 + r0) * o.p.H + h) * db + col + 8 * (lane & 3);
+        const int64_t step = (int64_t)8 * o.p.H * db;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (r0 + 8 * j < ch.len) *reinterpret_cast<uint4*>(out + j * step) = u[j];
+    }
     return true;
 }
 
@@ -617,11 +614,15 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         uint64_t* one[] = {&bar.x,  &bar.y,   &bar.w,  &bar.rec, &bar.sc,
                            &bar.upd, &bar.xs, &bar.aw, &bar.drain};
         for (uint64_t* b : one) mbar_init(b, 1);
-        uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd, &bar.open};
+        mbar_init(&bar.open, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bar.item[b], 1);
+            mbar_init(&bar.used[b], 16);
+        }
+        uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd, &bar.idle, &bar.taken};
         for (uint64_t* b : eight) mbar_init(b, 8);
         mbar_init(&bar.read, 16);
-        mbar_init(&bar.staged, 16);
-        mbar_init(&bar.stored, 1);
+        mbar_init(&bar.stored, 16);
         fence_mbar_init();
         bar.abort = 0;
     }
@@ -634,10 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     int loads = 0;  // chunks loaded by this thread (for the way out of an abort)
 
     if (warp >= 16 && warp < 19) {
-        if (lane == 0) {
-            loads = load_operand(o, bar, warp - 16, sm);
-            bulk_wait0();  // (its stores, if any, are complete)
-        }
+        if (lane == 0) loads = load_operand(o, bar, warp - 16, sm);
     } else if (tid == kMmaT) {
         // ------------------------------------------------------- MMA thread
         constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
@@ -648,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         bool ok = true;
         for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
             const Item t = item_at<false>(o, i);
-            const int da = o.calls.c[t.call].da, rev = o.calls.c[t.call].reverse;
+            const int da = o.calls.c[t.call].da;
             const uint32_t n = (uint32_t)(o.calls.c[t.call].db >> 3) << 17;  // N = db
             const uint32_t id_out = (idesc_bf16(128, 0, false, true)) | n;   // A W, X S
             const uint32_t id_up = (idesc_bf16(128, 0, true, true)) | n;     // Y^T W
@@ -664,22 +662,21 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     mma_bf16(kTA, desc(lX + off), desc(lYk + off), id_sc, ks > 0);
                 }
                 mma_commit(&bar.sc);
-                // the other three, each as soon as its operands are there (A W of a chunk that
-                // ends inside its tile: once the rows past it are cleared, with the decayed W)
-                const bool whole = chunk_at(t, rev, k).len == kC;
+                // X S and the state's update as soon as their operands are there, then A W: the
+                // longest way round is from the update through the next Y and X Y^T to A (A W
+                // first: 9.8k cycles a chunk).  With the decayed W the rows past a chunk that
+                // ends inside its tile are cleared, too.
                 uint32_t todo = 7;
                 uint64_t since = 0;
                 while (todo) {
                     uint32_t now = 0;
-                    const bool s = test(&bar.s, ph);
-                    if ((todo & 1) && s && test(&bar.wd, ph)) {
-                        now = 1;
-                    } else if (g == 0 || test(&bar.read, ph ^ 1)) {
-                        if ((todo & 2) && s) now = 2;
-                        else if ((todo & 4) && test(&bar.a, ph) &&
-                                 test(whole ? &bar.w : &bar.wd, ph))
-                            now = 4;
+                    const bool free = g == 0 || test(&bar.read, ph ^ 1);
+                    if ((todo & 3) && test(&bar.s, ph)) {
+                        if ((todo & 1) && test(&bar.wd, ph)) now = 1;
+                        else if ((todo & 2) && free) now = 2;
                     }
+                    if (now == 0 && (todo & 5) == 4 && free && test(&bar.a, ph))
+                        now = 4;
                     if (now == 0) {
                         if (since == 0) since = globaltimer();
                         if (*abort) { ok = false; break; }
@@ -736,11 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         const uint32_t at = static_cast<uint32_t>(32 * q) << 16 | kTA;
         const float* rCol = reinterpret_cast<const float*>(sm + kSRec);
         const int row = 32 * q + lane;
-        const View it{reinterpret_cast<volatile int*>(sm + kSItem) + 12 * warp};
-        uint32_t g = 0;
+        uint32_t g = 0, n = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            open_item(o, i, it);
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
+            if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
+            const View it = view(sm, n);
             // the row's prefix sum inside its block and its sum to the edge of the block that it
             // looks to, loaded a chunk ahead (from memory they take 2500 cycles)
             float hi_next = 0.f, edge_next = 0.f;
@@ -838,40 +835,29 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 ok = write_out<kDots>(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32);
                 if (!ok) break;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.used[n & 1]);
         }
     } else if (warp < 16) {
         // --------------------------------------- state, decayed W and outputs
         const int q = warp & 3, wg = (warp - 8) >> 2;
         const int row = 32 * q + lane;  // token, or state row
-        const View it{reinterpret_cast<volatile int*>(sm + kSItem) + 12 * warp};
         const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + 64 * wg;  // this warp's columns
-        uint32_t g = 0, opened = 0;
+        uint32_t g = 0, opened = 0, n = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            open_item(o, i, it);
+        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
+            if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
+            const View it = view(sm, n);
+            const bool final = it.v[View::kFinal] >= 0;
             if (it.chunks() == 0) {
                 // an empty sequence owns its first slot: its final state is its initial one
-                if (it.v[View::kFinal] >= 0)
-                    pass_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg);
+                if (final) pass_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.used[n & 1]);
                 continue;
             }
             const bool cols = 64 * wg < o.calls.c[it.call()].db;          // this warp has columns
             const bool holds = cols && row < o.calls.c[it.call()].da;     // this lane a state row
-            // the segment's edge state into TMEM, once the last segment's is done with (and so is
-            // its copy, whose buffer the state passes through)
-            if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
-                          !wait(&bar.xs, (g - 1) & 1, p.err, abort))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint8_t* stage = sm + kSS + (warp - 8) * 8192;
-            load_state(o, it.call(), it.v[View::kEdge], it.h(), 64 * wg, stage);
-            // no warp writes the copy while another's state is still on its way through the buffer
-            if (lane == 0) mbar_arrive(&bar.open);
-            if (!wait(&bar.open, opened & 1, p.err, abort)) { ok = false; break; }
-            ++opened;
-
             float rowf_prev = 0.f, head, tail, total;
             {
                 const float* r = it.record(o, 0);
@@ -879,6 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 tail = __ldg(r + kRTail + row);
                 total = __ldg(r + kRCol + kRB + 4);
             }
+            if (!wait(&bar.open, opened & 1, p.err, abort)) { ok = false; break; }
+            tc_fence_after();
+            load_state(o, it.call(), it.v[View::kZero], 64 * wg, sm + kSS);
+            // no warp writes the copy while another still reads the buffer
+            if (lane == 0) mbar_arrive(&bar.taken);
+            if (!wait(&bar.taken, opened & 1, p.err, abort)) { ok = false; break; }
+            ++opened;
             // step k: the outputs of chunk k - 1 and the state's copy of chunk k, then chunk k's
             // decayed W (the outputs' products were the last to read W's buffer, so its load runs
             // meanwhile)
@@ -892,18 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     tail = __ldg(r + kRTail + row);
                     total = __ldg(r + kRCol + kRB + 4);
                 }
-                // first whichever of the two has its products complete
-                const bool outputs_first =
-                    k == it.chunks() ||
-                    (k > 0 && __all_sync(0xffffffffu, test(&bar.aw, (g - 1) & 1)));
-#pragma unroll 1
-                for (int part = 0; ok && part < 2; ++part) {
-                    if ((part == 0) == outputs_first) {
-                        if (k > 0)
-                            ok = write_out<kDots>(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev, 64 * wg);
-                        continue;
-                    }
-                    if (k == it.chunks()) continue;
+                if (k < it.chunks()) {
                     // the last update of the state, the last read of its copy and of the decayed
                     // W's buffer are complete
                     if (g > 0 && (!wait(&bar.upd, (g - 1) & 1, p.err, abort) ||
@@ -947,7 +929,16 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.s);
                 }
-                if (!ok) break;
+                if (k == it.chunks() && !final) {
+                    // the copy's last read is complete: the next item's state may come
+                    if (!wait(&bar.xs, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+                    if (lane == 0) mbar_arrive(&bar.idle);
+                }
+                if (k > 0 && !write_out<kDots>(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev,
+                                               64 * wg)) {
+                    ok = false;
+                    break;
+                }
                 if (k < it.chunks()) {
                     if (!wait(&bar.w, g & 1, p.err, abort) ||
                         (g > 0 && !wait(&bar.stored, (g - 1) & 1, p.err, abort))) {
@@ -1007,12 +998,18 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 rowf_prev = rowf;
             }
             if (!ok) break;
-            if (it.v[View::kFinal] >= 0) {
-                if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+            if (final) {
+                if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) break;
                 tc_fence_after();
-                store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg, stage);
+                store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg,
+                            sm + kSS + (warp - 8) * 8192);
                 tc_fence_before();
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.idle);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.used[n & 1]);
         }
     }
 
@@ -1296,6 +1293,19 @@ bool make_map(CUtensorMap* m, const void* base, int64_t T, int H, int d, int64_t
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// fp32 states [count][rows][inner]: boxes of 32 columns x all rows (64 or 128) of one
+bool make_state_map(CUtensorMap* m, const void* base, int64_t count, int rows, int inner) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)count};
+    const cuuint64_t strides[2] = {(cuuint64_t)inner * 4, (cuuint64_t)rows * inner * 4};
+    const cuuint32_t box[3] = {32, (cuuint32_t)rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int sm_count() {
     int dev = 0, n = 0;
     cudaGetDevice(&dev);
@@ -1313,10 +1323,14 @@ cudaError_t fill(OutParams& o, const Problem& p, const lin::Calls& calls, int n,
     for (int i = 0; i < n; ++i) {
         const Call& c = calls.c[i];
         if (p.T == 0) continue;
-        if ((out && (!make_map(&o.x[i], c.x, p.T, p.H, c.da, c.x_ld) ||
-                     !make_map(&o.out[i], c.out, p.T, p.H, c.db, (int64_t)p.H * c.db))) ||
+        if ((out && !make_map(&o.x[i], c.x, p.T, p.H, c.da, c.x_ld)) ||
             !make_map(&o.y[i], c.y, p.T, p.H, c.da, c.y_ld) ||
             !make_map(&o.w[i], c.w, p.T, p.H, c.db, c.w_ld))
+            return cudaErrorInvalidValue;
+        const int rows = c.tr ? c.db : c.da, inner = c.tr ? c.da : c.db;
+        if (out && ((c.seg && !make_state_map(&o.seg[i], c.seg, slots * p.H, rows, inner)) ||
+                    (c.edge && !make_state_map(&o.edge[i], c.edge, (int64_t)p.N * p.H, rows,
+                                               inner))))
             return cudaErrorInvalidValue;
     }
     return cudaSuccess;
