@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
 #pragma unroll
                 for (int off = 8; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
                 if ((lane & 15) == 0)
-                    c.dots[((int64_t)(col / kDotCols) * p.T + t) * p.H + h] = x;
+                    c.dots[((int64_t)(col / kDotCols) * p.H + h) * p.T + t] = x;
             }
         }
     };
@@ -322,7 +322,7 @@ struct DecayGrad {
     const float *segS, *segD;   // [slots][H][E] edge states (where sequences have segments)
     const float *S0, *dS0;      // [N][H][E] at the sequences' starts; S0 may be nullptr (zeros)
     const float *S_T, *dS_out;  // at their ends; dS_out may be nullptr (zeros)
-    const float *dots_q, *dots_k;  // [nq][T][H], [nk][T][H]
+    const float *dots_q, *dots_k;  // [nq][H][T], [nk][H][T]
     int nq, nk;
     float* dg;                  // [T][H]
     int E;
@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
         x = size = 0.f;
         if (t < sg.begin) return;
         float a = 0.f, b = 0.f;
-        for (int i = 0; i < d.nq; ++i) a += d.dots_q[((int64_t)i * p.T + t) * p.H + h];
-        for (int i = 0; i < d.nk; ++i) b += d.dots_k[((int64_t)i * p.T + t) * p.H + h];
+        for (int i = 0; i < d.nq; ++i) a += d.dots_q[((int64_t)i * p.H + h) * p.T + t];
+        for (int i = 0; i < d.nk; ++i) b += d.dots_k[((int64_t)i * p.H + h) * p.T + t];
         x = a - b;
         size = fabsf(a) + fabsf(b);
     };

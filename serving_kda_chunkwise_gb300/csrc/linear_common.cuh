@@ -42,7 +42,7 @@ struct Call {
     const float* seg;    // [slots][H][...] state at the other segments' edges, or nullptr
     float* S_out;        // [N][H][...] state after the sequence (reversed: before it), or nullptr
     void* out;           // [T][H][db]
-    const void* dot;     // [T][H][db] rows, or nullptr: dots[b][t][h] = sum over column block b
+    const void* dot;     // [T][H][db] rows, or nullptr: dots[b][h][t] = sum over column block b
     int64_t dot_ld;      //   of out * dot in fp32, before out is rounded
     float* dots;
 };

@@ -369,19 +369,22 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
         for (int k = 0; k < t.chunks; ++k, ++g) {
             const uint32_t last = (g - 1) & 1;
             if (which == 2 && k == 0) {  // the item's state, through its copy's buffer
-                if (states > 0 && !wait1(&bar.idle, (states - 1) & 1, err, abort)) return g;
                 const bool own = t.sg.count <= 1;
                 const CUtensorMap* m = (own ? o.edge : o.seg) + t.call;
-                if (!own || c.edge) {
-                    const int inner = c.tr ? c.da : c.db, bytes = (c.tr ? c.db : c.da) * 128;
-                    mbar_expect_tx(&bar.open, inner / 32 * bytes);
+                const int inner = c.tr ? c.da : c.db, bytes = (c.tr ? c.db : c.da) * 128;
+                const int at = (own ? t.sg.n : t.slot) * o.p.H + t.h;
+                const int boxes = own && !c.edge ? 0 : inner / 32;
+                if (states > 0) {
+                    // into L2 early: all CTAs come to their next items at about the same time
 #pragma unroll 1
-                    for (int b = 0; b < inner / 32; ++b)
-                        tma_load_3d(sm + kSS + b * bytes, m, 32 * b, 0,
-                                    (own ? t.sg.n : t.slot) * o.p.H + t.h, &bar.open);
-                } else {
-                    mbar_arrive(&bar.open);
+                    for (int b = 0; b < boxes; ++b) tma_prefetch_3d(m, 32 * b, 0, at);
+                    if (!wait1(&bar.idle, (states - 1) & 1, err, abort)) return g;
                 }
+                if (boxes) mbar_expect_tx(&bar.open, boxes * bytes);
+                else mbar_arrive(&bar.open);
+#pragma unroll 1
+                for (int b = 0; b < boxes; ++b)
+                    tma_load_3d(sm + kSS + b * bytes, m, 32 * b, 0, at, &bar.open);
                 // (it has landed before this thread can come to any way out)
                 mbar_wait(&bar.open, states & 1, nullptr);
                 ++states;
@@ -580,7 +583,7 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
             }
         }
     }
-    if (dots) c.dots[((int64_t)(col >> 5) * o.p.T + ch.t0 + row) * o.p.H + h] = acc;
+    if (dots) c.dots[((int64_t)(col >> 5) * o.p.H + h) * o.p.T + ch.t0 + row] = acc;
     __syncwarp();
     // four lanes a row; rows 4 apart share a phase, for their pieces lie in different banks
     const int r0 = (row & 96) + (lane >> 3) + (lane & 4);
