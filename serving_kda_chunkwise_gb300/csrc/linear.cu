@@ -4,10 +4,14 @@
 // three gradients are instances of one call and how sequences are cut into segments.
 //
 // Launches of a call over sequences longer than a segment:
-//   1. segment sums: each segment's own contribution to the state, and its summed log decay;
-//   2. edges: the state at every segment's edge (a scan over a sequence's segments);
-//   3. outputs: every segment from its edge state.
-// When no sequence can be longer than a segment, launch 3 alone.
+//   1. (bf16) decays: what the chunks' products need of the log decays, see linear_tc.cu;
+//   2. segment sums: each segment's own contribution to the state, and its summed log decay;
+//   3. edges: the state at every segment's edge (a scan over a sequence's segments);
+//   4. outputs: every segment from its edge state;
+//   5. (gradients) the decays'.
+// When no sequence can be longer than a segment, 2 and 3 fall away.  Each launch but the first is
+// a programmatic dependent of the one before: it is set up beside it and waits before it reads
+// what that wrote (every kernel waits, so that a launch's end is that of all before it).
 //
 // The gradient of g:  dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_out>.  Taken over
 // a long sequence that sum would gather the rounding of every later token.  At every segment's
@@ -62,6 +66,8 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
     __shared__ __align__(16) float xs[kOut ? kTile : 1][DA], ys[kTile][DA], ws[kTile][kCols];
     __shared__ float2 fs[kTile];  // how the state decays before the token: factor, near
     __shared__ float2 part[kOut ? 4 : 1][kTile][kCols / 2];
+    if (kOut) grid_dependency_wait();
+    grid_dependents_launch();
     if (kOut && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) lin::check_seqlens(p);
     const Call& c = calls.c[blockIdx.z / blocks_per_call];
     const int cb = blockIdx.z % blocks_per_call;
@@ -273,6 +279,8 @@ struct Edges {
 __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Problem p,
                                                    const __grid_constant__ Edges e) {
     constexpr int kAhead = 4;
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int dir = blockIdx.z;
     const int per_head = e.E / 4 / 256;
     const int h = blockIdx.x / per_head;
@@ -299,7 +307,7 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
             for (int u = 0; u < kAhead; ++u)
                 if (i0 + u < count - 1) {
                     in[u] = __ldcs(add + slot(i0 + u) * stride + own);
-                    d[u] = __ldg(e.dec[dir] + slot(i0 + u) * p.H + h);
+                    d[u] = __ldcg(e.dec[dir] + slot(i0 + u) * p.H + h);
                 }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
@@ -331,6 +339,8 @@ struct DecayGrad {
 __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__ Problem p,
                                                          const __grid_constant__ DecayGrad d) {
     __shared__ float red[2][8];
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Segment sg = lin::find_segment(p, (int)blockIdx.x);
     if (!sg.live) return;
@@ -416,6 +426,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
 __global__ void __launch_bounds__(256) decay_sum_kernel(const float* dg, int64_t T, int H,
                                                         float* out) {
     __shared__ float red[256];
+    grid_dependency_wait();
     const int h = blockIdx.x;
     float x = 0.f;
     for (int64_t t = threadIdx.x; t < T; t += 256) x += dg[t * H + h];
@@ -491,15 +502,24 @@ Problem problem(const LinearArgs& a, int L) {
 }
 
 template <typename IO, bool kOut>
-void launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, float* dec,
-                  const char* name, cudaStream_t s) {
+cudaError_t launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, float* dec,
+                         const char* name, cudaStream_t s) {
     const int blocks = 128 / kCols;
     const dim3 grid((unsigned)slots, p.H, n * blocks);
     bool any[2] = {};
     for (int i = 0; i < n; ++i) any[calls.c[i].da == 128] = true;
     ProfScope prof(name, s);
-    if (any[0]) token_kernel<64, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
-    if (any[1]) token_kernel<128, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
+    cudaError_t e = cudaSuccess;
+    if (!kOut) {  // (a call's first launch, one da for both directions)
+        if (any[0]) token_kernel<64, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
+        if (any[1]) token_kernel<128, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
+        return cudaGetLastError();
+    }
+    if (any[0])
+        e = launch_dependent(token_kernel<64, IO, kOut>, grid, 128, 0, s, p, calls, dec, blocks);
+    if (any[1] && e == cudaSuccess)
+        e = launch_dependent(token_kernel<128, IO, kOut>, grid, 128, 0, s, p, calls, dec, blocks);
+    return e;
 }
 
 template <bool kOut>
@@ -510,11 +530,9 @@ cudaError_t launch_calls(const LinearArgs& a, const Problem& p, const Calls& cal
     if (use_tc(a.io_bf16))
         return kOut ? lintc::launch_outputs(p, calls, n, slots, rec, name, a.stream)
                     : lintc::launch_sums(p, calls, n, slots, rec, dec, name, a.stream);
-    if (a.io_bf16)
-        launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream);
-    else
-        launch_token<float, kOut>(p, calls, n, slots, dec, name, a.stream);
-    return cudaGetLastError();
+    return a.io_bf16
+               ? launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream)
+               : launch_token<float, kOut>(p, calls, n, slots, dec, name, a.stream);
 }
 
 // Segment sums and edges of the forward states and, in a backward pass, of the reversed ones.
@@ -540,8 +558,7 @@ cudaError_t launch_segments(const LinearArgs& a, const Problem& p, const Layout&
         return err;
     ProfScope prof("linear_edge_kernel", a.stream);
     const dim3 grid(a.H * (e.E / 1024), a.N < 64 ? a.N : 64, bwd ? 2 : 1);
-    edge_kernel<<<grid, 256, 0, a.stream>>>(p, e);
-    return cudaGetLastError();
+    return launch_dependent(edge_kernel, grid, dim3(256), 0, a.stream, p, e);
 }
 
 }  // namespace
@@ -610,11 +627,17 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
         d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
         if (a.T_total > 0) {
             ProfScope prof("linear_decay_grad_kernel", a.stream);
-            decay_grad_kernel<<<dim3((unsigned)l.slots, a.H), 256, 0, a.stream>>>(p, d);
+            if (cudaError_t err = launch_dependent(decay_grad_kernel,
+                                                   dim3((unsigned)l.slots, a.H), dim3(256), 0,
+                                                   a.stream, p, d))
+                return err;
         }
         if (!a.g_per_token) {
             ProfScope prof("linear_decay_sum_kernel", a.stream);
-            decay_sum_kernel<<<a.H, 256, 0, a.stream>>>(d.dg, a.T_total, a.H, a.dg);
+            if (cudaError_t err = launch_dependent(decay_sum_kernel, dim3(a.H), dim3(256), 0,
+                                                   a.stream, (const float*)d.dg, a.T_total, a.H,
+                                                   a.dg))
+                return err;
         }
     }
     return cudaGetLastError();

@@ -200,6 +200,7 @@ __device__ __forceinline__ const float* record(const OutParams& o, const Item& t
 
 // One warp a (chunk, head); a CTA's warps take neighbouring heads, whose decays share sectors.
 __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Problem p, float* rec) {
+    grid_dependents_launch();
     const int lane = threadIdx.x & 31, per = p.L / kC;
     const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int slot = blockIdx.x / per, chunk = blockIdx.x % per;
@@ -374,6 +375,7 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
                 const int inner = c.tr ? c.da : c.db, bytes = (c.tr ? c.db : c.da) * 128;
                 const int at = (own ? t.sg.n : t.slot) * o.p.H + t.h;
                 const int boxes = own && !c.edge ? 0 : inner / 32;
+                if (states == 0) grid_dependency_wait();
                 if (states > 0) {
                     // into L2 early: all CTAs come to their next items at about the same time
 #pragma unroll 1
@@ -404,6 +406,7 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
             }
             if (which == 0) {
                 if (g > 0 && !wait1(&bar.a, last, err, abort)) return g + 1;
+                if (g == 0) grid_dependency_wait();
                 mbar_expect_tx(&bar.rec, 4 * kRDir);
                 bulk_g2s(sm + kSRec, record(o, t, ch.i) + kRCol + (c.reverse ? kRDir : 0),
                          4 * kRDir, &bar.rec);
@@ -640,6 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     tc_fence_after();
     const uint32_t items = item_count(o);
     int loads = 0;  // chunks loaded by this thread (for the way out of an abort)
+    grid_dependents_launch();
+    if (warp < 16) grid_dependency_wait();  // (X, Y and W are no earlier launch's)
 
     if (warp >= 16 && warp < 19) {
         if (lane == 0) loads = load_operand(o, bar, warp - 16, sm);
@@ -1083,6 +1088,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
+    grid_dependents_launch();
     const uint32_t items = item_count(o);
     // an item whose sum no edge needs: the last segment of a walk
     auto skip = [&](const Item& t) {
@@ -1142,6 +1148,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             }
         }
     } else if (warp >= 4) {
+        grid_dependency_wait();  // (Y and W are no earlier launch's)
         // 16 warps decay W, each 32 tokens of 32 columns (8 warps took longer than the loads)
         const int q = warp & 3, cg = (warp - 4) >> 2;
         const int row = 32 * q + lane;
@@ -1368,8 +1375,8 @@ cudaError_t launch_outputs(const Problem& p, const lin::Calls& calls, int n, int
         return e;
     const int64_t items = slots * p.H * n, sms = sm_count();
     ProfScope prof(name, s);
-    kernel<<<(unsigned)(items < sms ? items : sms), kThreads, kOutSmem, s>>>(o);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3((unsigned)(items < sms ? items : sms)), dim3(kThreads),
+                            kOutSmem, s, o);
 }
 
 cudaError_t launch_sums(const Problem& p, const lin::Calls& calls, int n, int64_t slots,
@@ -1381,8 +1388,8 @@ cudaError_t launch_sums(const Problem& p, const lin::Calls& calls, int n, int64_
         return e;
     const int64_t items = slots * p.H * n, sms = sm_count();
     ProfScope prof(name, s);
-    sum_kernel<<<(unsigned)(items < sms ? items : sms), kSumThreads, kSumSmem, s>>>(o, dec);
-    return cudaGetLastError();
+    return launch_dependent(sum_kernel, dim3((unsigned)(items < sms ? items : sms)),
+                            dim3(kSumThreads), kSumSmem, s, o, dec);
 }
 
 }  // namespace lintc

@@ -392,11 +392,7 @@ __global__ void __launch_bounds__(256) qb_hist4_kernel(const float* __restrict__
 // ---- the sampled-bracket path ----
 
 // The three kernels after the thresholds are launched as programmatic dependents of the one
-// before (their launch and setup overlap its tail); each waits here for that grid to complete
-// and its writes to be visible before it reads them.
-__device__ __forceinline__ void grid_dependency_wait() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
+// before (their launch and setup overlap its tail).
 
 // One warp: the digit whose bin of the 256 counts h holds position `rank` (a prefix scan over
 // the counts, eight bins a lane), and the count of the bins before it.  True on the one lane
@@ -822,24 +818,6 @@ static cudaError_t launch_alpha(const float* s, const float* b, int64_t m, int n
     else
         qb_alpha_kernel<32><<<grid, 256, 0, stream>>>(s, b, m, n, k, alpha);
     return cudaGetLastError();
-}
-
-// a launch that may begin while the previous kernel on the stream finishes (the kernel waits
-// for it with griddepcontrol.wait)
-template <typename... KArgs, typename... Args>
-static cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                                    cudaStream_t stream, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 static cudaError_t launch_fast(const QbFast& f, const float* s, const float* b, int64_t m,
