@@ -38,8 +38,10 @@ using lin::Segment;
 // memory, the next 16 on their way in registers meanwhile.  fp32 throughout, so that fp32 inputs
 // keep fp32 accuracy.  The state decays by S += S (e^g - 1) unless g is far below 0: e^g itself
 // rounds near 1, and one decay for all tokens would round the same way at every one of them.
-// Bound by its three (sums: two) fp32 operations per state element and token, then by the
-// instructions around them.
+// Bound by its three (sums: two) fp32 operations per state element and token: at 65,536 tokens x
+// 16 heads x 128 the outputs take 2,229 us, 62 % of the fp32 rate, the sums 1,227 us, 76 %; at
+// 2,048 + 1,531 tokens x 8 heads, 64 x 128, 45 and 30 us (with one column a lane and no tile on
+// its way: 98 and 69 us).
 constexpr int kCols = 64;
 constexpr int kDotCols = 32;
 constexpr int kTile = 16;
@@ -267,7 +269,9 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
 
 // ------------------------------------------------------------------------ edges --
 // A thread carries four state elements over a sequence's segments, the contributions loaded
-// four segments ahead.
+// four segments ahead.  Bound by that traffic, each contribution read and each edge written once,
+// and by its latency where segments are few: 20 us at 65,536 tokens x 32 heads x 128 (33 segments
+// of 2,048: 134 MB), 42 us for both directions of the gradients x 16 heads (65 of 1,024: 268 MB).
 struct Edges {
     const float* add[2];    // [slots][H][E] contributions: forward, reversed
     float* seg[2];          // [slots][H][E] edge states (written)
@@ -325,7 +329,9 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
 
 // ----------------------------------------------------------- gradient of the decay --
 // One CTA a (segment, head): the anchors <S, D> at the segment's two edges, then the suffix sums
-// of q.dq - k.dk over its tokens, 256 at a time from the end.
+// of q.dq - k.dk over its tokens, 256 at a time from the end.  Bound by reading the edge states
+// (each anchor's twice, by the segments on both sides): 72 us at 65,536 tokens x 16 heads x 128,
+// 268 MB at 3.7 TB/s.
 struct DecayGrad {
     const float *segS, *segD;   // [slots][H][E] edge states (where sequences have segments)
     const float *S0, *dS0;      // [N][H][E] at the sequences' starts; S0 may be nullptr (zeros)
@@ -449,12 +455,20 @@ bool use_tc(int io_bf16) {
     return io_bf16 && !(env && strcmp(env, "generic") == 0);
 }
 
-// Tokens a segment: short enough that the segments of all heads fill the GPU a few times, no
-// shorter than the edge states' traffic (two fp32 states a segment) is worth.
+// Tokens a segment.  On the tensor cores a segment's chunks in a row cost less than its edge states
+// (two fp32 states a segment, written, read and loaded), so segments are as long as they can be
+// with one for every SM: at 8,192 tokens x 16 heads 1,024 tokens take 83 us, 512 take 93, 256 111.
+// Not beyond 2,048, where the last round's ends cost more (65,536 x 32: 857 us, with 4,096 911, with
+// 1,024 920); in the gradients not beyond 1,024, for sums over 2,048 tokens between anchors cost
+// dg's last bits (1e-5 instead of 7e-6).  Up to 512 tokens take one launch: four chunks in a row
+// take no longer than two more launches (256 x 4: 22 against 29 us, 512 x 4: 31 against 30).
+// Token by token a segment is walked by as many CTAs as its state has blocks, and each SM needs
+// several to be busy: four segments an SM (2,048 + 1,531 tokens x 8 heads: 77 us, two 89, one 138).
 int segment_length(int64_t T, int H, bool tc, bool bwd) {
-    if (tc && T <= 512) return 512;  // one launch: four chunks take less than two more launches
+    if (tc && T <= 512) return 512;
     int L = tc ? 128 : 64;
-    while (L < (tc && !bwd ? 2048 : 1024) && T / L * H > 4 * 152) L *= 2;
+    const int most = tc && !bwd ? 2048 : 1024, fill = tc ? 152 : 4 * 152;
+    while (L < most && T / L * H > fill) L *= 2;
     return L;
 }
 
@@ -647,6 +661,8 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
 // One CTA a (request, head): a state row of dv fp32 is covered by dv / 4 lanes with a float4
 // each, the dk rows spread over 8 warps; every element is read once, updated, written once and
 // added to its column's output:  S <- e^g S + k v^T,  o = S^T q.
+// Bound by the states, once in and once out: 256 requests x 32 heads x 128 x 128 take 158 us,
+// 1.07 GB at 6.8 TB/s, the copy rate.  A few requests: 10 us, the latency of one CTA.
 namespace {
 
 template <int DK, int DV, typename IO>

@@ -199,6 +199,8 @@ __device__ __forceinline__ const float* record(const OutParams& o, const Item& t
 }
 
 // One warp a (chunk, head); a CTA's warps take neighbouring heads, whose decays share sectors.
+// Bound by writing the records (4.7 KB each): 27 us at 65,536 tokens x 32 heads, 2.9 TB/s.  (The
+// output kernel's own warps formed them before, and each chunk waited for them.)
 __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Problem p, float* rec) {
     grid_dependents_launch();
     const int lane = threadIdx.x & 31, per = p.L / kC;
@@ -264,16 +266,20 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
 
 // -------------------------------------------------------------- outputs --
 // Persistent, one CTA an SM.  Roles: warps 0..7 turn X Y^T into A (hi + lo over the product's own
-// TMEM columns, so that A never leaves tensor memory); warps 8..15 decay W, keep the state's copy
-// and write the outputs; a thread each of warps 16..18 loads X and the decays, Y, and W (as lanes
-// of one warp they held each other up by up to 2500 cycles), one of warp 19 issues the MMAs, each
-// chunk's three sets in the order in which their operands get ready.  Warp w reaches TMEM lanes 32 (w % 4) .. + 31.  The state lives in TMEM in fp32; X S reads its bf16
-// hi + lo copy in shared memory.
+// TMEM columns, so that A never leaves tensor memory) and write half of the outputs; warps 8..15
+// keep the state's copy, write the other half and decay W; a thread each of warps 16..18 loads X
+// and the decays (and finds the items), Y, and W and the items' states (as lanes of one warp they
+// held each other up by up to 2500 cycles); one of warp 19 issues the MMAs.  Warp w reaches TMEM
+// lanes 32 (w % 4) .. + 31.  The state lives in TMEM in fp32; X S reads its bf16 hi + lo copy in
+// shared memory.
 // Shared memory holds one chunk of X, Y and W (32 KB each), the decayed W and the state's copy (64
 // KB each): no second stage fits, but each operand is reloaded as soon as its last product is
 // done, and while one waits the others' products run.  (Two stages fit with 64 of the db columns
 // to a CTA; that form made A twice and its N = 64 products run at 75 % of N = 128's rate, and was
 // slower.)
+// Bound by that chain: a chunk takes 8,900 cycles, of which the products are 4,400.  Measured at
+// 65,536 tokens x 32 heads x 128: 560 us (2.2 GB at 3.9 TB/s, 7 products of 4.2 MFLOP a chunk
+// and head at 860 TFLOP/s); gradients, 65,536 x 16, three calls: 1,001 us.
 constexpr int kThreads = 640;
 constexpr int kMmaT = 19 * 32;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
@@ -1052,7 +1058,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 // of a sum is free, so the chunks run away from the edge the weights refer to, the decay between
 // the edge and the chunk carried along, and the accumulator in TMEM is never rescaled.  W is
 // decayed in place (hi over W itself, lo beside it), so two stages of all operands fit.  Bound by
-// reading Y and W.
+// reading Y and W: 215 us at 65,536 tokens x 32 heads x 128, 1.07 GB at 5.0 TB/s (without the
+// conversion 176 us; a third stage for Y and W gained nothing).
 constexpr int kSumThreads = 640;
 constexpr uint32_t kUY = 0, kUW = 32768, kULo = 65536, kUStage = 98304;  // two stages
 constexpr uint32_t kUBar = 2 * kUStage;
