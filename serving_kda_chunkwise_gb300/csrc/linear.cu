@@ -476,7 +476,7 @@ struct Layout {
     int L;
     int64_t slots;
     bool segments;  // some sequence may be longer than a segment
-    size_t rec, add[2], seg[2], dec, S_T, dS0, dots_q, dots_k, dg, bytes;
+    size_t rec, next, add[2], seg[2], dec, S_T, dS0, dots_q, dots_k, dg, bytes;
 };
 
 Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool equal) {
@@ -492,6 +492,7 @@ Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool e
         return r;
     };
     l.rec = take(tc ? lintc::record_bytes(l.slots, l.L, H) : 0);
+    l.next = take(tc ? lintc::kCounters * sizeof(unsigned) : 0);
     for (int i = 0; i < (bwd ? 2 : 1); ++i) {
         l.add[i] = take(l.segments ? (size_t)l.slots * state : 0);
         l.seg[i] = take(l.segments ? (size_t)l.slots * state : 0);
@@ -541,8 +542,9 @@ cudaError_t launch_calls(const LinearArgs& a, const Problem& p, const Calls& cal
                          const Layout& l, float* dec, const char* name) {
     const int64_t slots = l.slots;
     const float* rec = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + l.rec);
+    unsigned* next = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.workspace) + l.next);
     if (use_tc(a.io_bf16))
-        return kOut ? lintc::launch_outputs(p, calls, n, slots, rec, name, a.stream)
+        return kOut ? lintc::launch_outputs(p, calls, n, slots, rec, next, name, a.stream)
                     : lintc::launch_sums(p, calls, n, slots, rec, dec, name, a.stream);
     return a.io_bf16
                ? launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream)
@@ -591,7 +593,8 @@ cudaError_t launch_linear_fwd(const LinearArgs& a) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     if (use_tc(a.io_bf16))
         if (cudaError_t e = lintc::launch_decays(
-                p, l.slots, reinterpret_cast<float*>(ws + l.rec), a.stream))
+                p, l.slots, reinterpret_cast<float*>(ws + l.rec),
+                reinterpret_cast<unsigned*>(ws + l.next), a.stream))
             return e;
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, false)) return e;
@@ -611,7 +614,8 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
     auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
     if (use_tc(a.io_bf16))
         if (cudaError_t e = lintc::launch_decays(
-                p, l.slots, reinterpret_cast<float*>(ws + l.rec), a.stream))
+                p, l.slots, reinterpret_cast<float*>(ws + l.rec),
+                reinterpret_cast<unsigned*>(ws + l.next), a.stream))
             return e;
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, true)) return e;

@@ -151,6 +151,7 @@ struct OutParams {
     int n_calls;
     int slots;
     const float* rec;  // decay records, see decay_kernel
+    unsigned* next;    // how many items have been taken beyond the first round
 };
 
 __device__ __forceinline__ uint32_t item_count(const OutParams& o) {
@@ -201,8 +202,10 @@ __device__ __forceinline__ const float* record(const OutParams& o, const Item& t
 // One warp a (chunk, head); a CTA's warps take neighbouring heads, whose decays share sectors.
 // Bound by writing the records (4.7 KB each): 27 us at 65,536 tokens x 32 heads, 2.9 TB/s.  (The
 // output kernel's own warps formed them before, and each chunk waited for them.)
-__global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Problem p, float* rec) {
+__global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Problem p, float* rec,
+                                                    unsigned* next) {
     grid_dependents_launch();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kCounters) next[threadIdx.x] = 0u;
     const int lane = threadIdx.x & 31, per = p.L / kC;
     const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int slot = blockIdx.x / per, chunk = blockIdx.x % per;
@@ -301,7 +304,7 @@ struct OutBars {
     uint64_t read;           // the chunk's outputs read from TMEM (16 arrivals)
     uint64_t stored;         // ... and read from their stage (16 arrivals)
     uint64_t item[2];        // an item's facts are there
-    uint64_t used[2];        // ... and done with (16 arrivals)
+    uint64_t used[2];        // ... and done with (19 arrivals)
     uint64_t idle;           // the last item's state is done with (8 arrivals)
     uint64_t open, taken;    // the item's state loaded; all of it taken over (8 arrivals)
     uint64_t drain;
@@ -312,10 +315,11 @@ static_assert(sizeof(OutBars) <= 256, "barrier area");
 
 // What the warps need of an item, kept in shared memory: their registers are few, and what the
 // compiler would put into local memory comes back from L2 (shared memory takes all of L1).  One
-// thread finds it, an item ahead: by each warp for itself an item began 4000 cycles later.
+// thread finds it, an item ahead: by each warp for itself an item began 4000 cycles later.  Items
+// are taken as CTAs come to them, for their lengths differ.
 struct View {
     volatile int* v;
-    enum { kBegin, kEnd, kChunks, kCall, kH, kRev, kRecord, kZero, kFinal, kWords };
+    enum { kBegin, kEnd, kChunks, kCall, kH, kRev, kRecord, kZero, kFinal, kSeg, kState, kWords };
     __device__ __forceinline__ int chunks() const { return v[kChunks]; }
     __device__ __forceinline__ int call() const { return v[kCall]; }
     __device__ __forceinline__ int h() const { return v[kH]; }
@@ -350,6 +354,9 @@ __device__ __forceinline__ void put_item(const OutParams& o, const Item& t, View
     const bool last = t.sg.live ? (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1)
                                 : t.sg.count == 0 && t.sg.s == 0;
     w.v[View::kFinal] = last ? t.sg.n : -1;  // whose final state follows, if any
+    // the state that it starts from: a segment's edge state or the sequence's own
+    w.v[View::kSeg] = t.sg.count > 1;
+    w.v[View::kState] = (t.sg.count > 1 ? t.slot : t.sg.n) * o.p.H + t.h;
 }
 
 // One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each once
@@ -363,24 +370,31 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
     unsigned* err = o.p.err;
     const uint32_t items = item_count(o);
     int g = 0;
-    uint32_t states = 0, n = 0;
-    for (uint32_t i = blockIdx.x; i < items; i += gridDim.x, ++n) {
-        const Item t = item_at<false>(o, i);
-        const Call& c = o.calls.c[t.call];
+    uint32_t states = 0, i = blockIdx.x;
+    for (uint32_t n = 0;; ++n) {
+        const View it = view(sm, n);
         if (which == 0) {
+            if (n > 0) {
+                if (n == 1) grid_dependency_wait();
+                i = gridDim.x + atomicAdd(o.next, 1u);
+            }
             if (n > 1 && !wait1(&bar.used[n & 1], ((n >> 1) - 1) & 1, err, abort)) return g;
-            put_item(o, t, view(sm, n));
+            if (i < items) put_item(o, item_at<false>(o, i), it);
+            else it.v[View::kChunks] = -1;
             mbar_arrive(&bar.item[n & 1]);
+        } else if (!wait1(&bar.item[n & 1], (n >> 1) & 1, err, abort)) {
+            return g;
         }
+        const int chunks = it.chunks(), call = it.call(), h = it.h();
+        if (chunks < 0) return g;
+        const Call& c = o.calls.c[call];
         const int blocks = (which == 2 ? c.db : c.da) / 64;
-        for (int k = 0; k < t.chunks; ++k, ++g) {
+        for (int k = 0; k < chunks; ++k, ++g) {
             const uint32_t last = (g - 1) & 1;
             if (which == 2 && k == 0) {  // the item's state, through its copy's buffer
-                const bool own = t.sg.count <= 1;
-                const CUtensorMap* m = (own ? o.edge : o.seg) + t.call;
+                const CUtensorMap* m = (it.v[View::kSeg] ? o.seg : o.edge) + call;
                 const int inner = c.tr ? c.da : c.db, bytes = (c.tr ? c.db : c.da) * 128;
-                const int at = (own ? t.sg.n : t.slot) * o.p.H + t.h;
-                const int boxes = own && !c.edge ? 0 : inner / 32;
+                const int at = it.v[View::kState], boxes = it.v[View::kZero] ? 0 : inner / 32;
                 if (states == 0) grid_dependency_wait();
                 if (states > 0) {
                     // into L2 early: all CTAs come to their next items at about the same time
@@ -399,27 +413,27 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
             }
             if (g > 0 && !wait1(freed, last, err, abort)) return g;
             if (which == 2 && g > 0 && !wait1(&bar.wd, last, err, abort)) return g;
-            const Chunk ch = chunk_at(t, c.reverse, k);
+            const Chunk ch = it.chunk(k);
             mbar_expect_tx(full, blocks * 16384);
 #pragma unroll 1
             for (int b = 0; b < blocks; ++b)
-                tma_load_3d(dst + b * 16384, maps + t.call, 64 * b, t.h, ch.t0, full);
-            if (which == 2 && k + 1 < t.chunks) {  // its load is waited for longest: into L2 early
-                const int ahead = chunk_at(t, c.reverse, k + 1).t0;
+                tma_load_3d(dst + b * 16384, maps + call, 64 * b, h, ch.t0, full);
+            if (which == 2 && k + 1 < chunks) {  // its load is waited for longest: into L2 early
+                const int ahead = it.chunk(k + 1).t0;
 #pragma unroll 1
                 for (int b = 0; b < blocks; ++b)
-                    tma_prefetch_3d(maps + t.call, 64 * b, t.h, ahead);
+                    tma_prefetch_3d(maps + call, 64 * b, h, ahead);
             }
             if (which == 0) {
                 if (g > 0 && !wait1(&bar.a, last, err, abort)) return g + 1;
                 if (g == 0) grid_dependency_wait();
                 mbar_expect_tx(&bar.rec, 4 * kRDir);
-                bulk_g2s(sm + kSRec, record(o, t, ch.i) + kRCol + (c.reverse ? kRDir : 0),
-                         4 * kRDir, &bar.rec);
+                bulk_g2s(sm + kSRec, it.record(o, k) + kRCol + (c.reverse ? kRDir : 0), 4 * kRDir,
+                         &bar.rec);
             }
         }
+        if (which != 0) mbar_arrive(&bar.used[n & 1]);
     }
-    return g;
 }
 
 // States in memory and in TMEM, 64 columns from `col` by a warp; out of line, once an item.
@@ -633,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         mbar_init(&bar.open, 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bar.item[b], 1);
-            mbar_init(&bar.used[b], 16);
+            mbar_init(&bar.used[b], 19);
         }
         uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd, &bar.idle, &bar.taken};
         for (uint64_t* b : eight) mbar_init(b, 8);
@@ -647,7 +661,6 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t items = item_count(o);
     int loads = 0;  // chunks loaded by this thread (for the way out of an abort)
     grid_dependents_launch();
     if (warp < 16) grid_dependency_wait();  // (X, Y and W are no earlier launch's)
@@ -662,13 +675,16 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         const uint32_t lWd = dlow(sbase + kSWd, 16384), lS = dlow(sbase + kSS, 16384);
         uint32_t g = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at<false>(o, i);
-            const int da = o.calls.c[t.call].da;
-            const uint32_t n = (uint32_t)(o.calls.c[t.call].db >> 3) << 17;  // N = db
-            const uint32_t id_out = (idesc_bf16(128, 0, false, true)) | n;   // A W, X S
-            const uint32_t id_up = (idesc_bf16(128, 0, true, true)) | n;     // Y^T W
-            for (int k = 0; ok && k < t.chunks; ++k, ++g) {
+        for (uint32_t i = 0;; ++i) {
+            if (!wait1(&bar.item[i & 1], (i >> 1) & 1, p.err, abort)) break;
+            const View it = view(sm, i);
+            const int chunks = it.chunks(), call = it.call();
+            if (chunks < 0) break;
+            const int da = o.calls.c[call].da;
+            const uint32_t n = (uint32_t)(o.calls.c[call].db >> 3) << 17;   // N = db
+            const uint32_t id_out = (idesc_bf16(128, 0, false, true)) | n;  // A W, X S
+            const uint32_t id_up = (idesc_bf16(128, 0, true, true)) | n;    // Y^T W
+            for (int k = 0; ok && k < chunks; ++k, ++g) {
                 const uint32_t ph = g & 1;
                 ok = wait1(&bar.x, ph, p.err, abort) && wait1(&bar.y, ph, p.err, abort);
                 if (!ok) break;
@@ -744,6 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     }
                 }
             }
+            if (!ok) break;
+            mbar_arrive(&bar.used[i & 1]);
         }
     } else if (warp < 8) {
         // ------------------------------------------------------------ A warps
@@ -753,9 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         const int row = 32 * q + lane;
         uint32_t g = 0, n = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
+        for (; ok; ++n) {
             if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
             const View it = view(sm, n);
+            if (it.chunks() < 0) break;
             // the row's prefix sum inside its block and its sum to the edge of the block that it
             // looks to, loaded a chunk ahead (from memory they take 2500 cycles)
             float hi_next = 0.f, edge_next = 0.f;
@@ -863,9 +882,10 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         const uint32_t at = (static_cast<uint32_t>(32 * q) << 16) + 64 * wg;  // this warp's columns
         uint32_t g = 0, opened = 0, n = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
+        for (; ok; ++n) {
             if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
             const View it = view(sm, n);
+            if (it.chunks() < 0) break;
             const bool final = it.v[View::kFinal] >= 0;
             if (it.chunks() == 0) {
                 // an empty sequence owns its first slot: its final state is its initial one
@@ -1363,16 +1383,17 @@ size_t record_bytes(int64_t slots, int L, int H) {
     return (size_t)slots * (L / kC) * H * kRec * sizeof(float);
 }
 
-cudaError_t launch_decays(const Problem& p, int64_t slots, float* rec, cudaStream_t s) {
-    if (p.T == 0) return cudaSuccess;
+cudaError_t launch_decays(const Problem& p, int64_t slots, float* rec, unsigned* next,
+                          cudaStream_t s) {
     ProfScope prof("linear_decay_kernel", s);
-    decay_kernel<<<dim3((unsigned)(slots * (p.L / kC)), (p.H + 7) / 8), 256, 0, s>>>(p, rec);
+    decay_kernel<<<dim3((unsigned)(slots * (p.L / kC)), (p.H + 7) / 8), 256, 0, s>>>(p, rec, next);
     return cudaGetLastError();
 }
 
 cudaError_t launch_outputs(const Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                           const float* rec, const char* name, cudaStream_t s) {
+                           const float* rec, unsigned* next, const char* name, cudaStream_t s) {
     OutParams o{};
+    o.next = next;
     if (cudaError_t e = fill(o, p, calls, n, slots, rec, true)) return e;
     bool dots = false;
     for (int i = 0; i < n; ++i) dots = dots || calls.c[i].dot != nullptr;

@@ -8,13 +8,16 @@
 namespace kda {
 namespace lintc {
 
-// What the kernels below need of the decays, once for all calls: `rec` holds record_bytes().
+// What the kernels below need of the decays, once for all calls (`rec` holds record_bytes()), and
+// the counters of taken items, zeroed.
+constexpr int kCounters = 1;
 size_t record_bytes(int64_t slots, int L, int H);
-cudaError_t launch_decays(const lin::Problem& p, int64_t slots, float* rec, cudaStream_t s);
+cudaError_t launch_decays(const lin::Problem& p, int64_t slots, float* rec, unsigned* next,
+                          cudaStream_t s);
 
-// Every segment's outputs (and final states) from its edge state.
+// Every segment's outputs (and final states) from its edge state; `next`: a zeroed counter.
 cudaError_t launch_outputs(const lin::Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                           const float* rec, const char* name, cudaStream_t s);
+                           const float* rec, unsigned* next, const char* name, cudaStream_t s);
 
 // Every segment's own contribution to the state into calls.c[i].seg, and its summed log2 decay
 // into dec[reverse][slot][head]; states in memory are [da][db] (tr = 0).
