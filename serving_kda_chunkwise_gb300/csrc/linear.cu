@@ -18,6 +18,7 @@
 // edges it is <S, D>, from states that are at hand, so the sums run inside a segment, from the
 // anchor at its end; what they miss the anchor at its start by is their rounding, and is taken
 // back token by token in proportion to the terms' sizes.
+#include <algorithm>
 #include <cstdlib>
 #include <cstring>
 
@@ -292,11 +293,11 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
     const int64_t stride = (int64_t)p.H * (e.E / 4), own = (int64_t)h * (e.E / 4) + at;
     const float4* add = reinterpret_cast<const float4*>(e.add[dir]);
     float4* seg = reinterpret_cast<float4*>(e.seg[dir]);
-    for (int n = blockIdx.y; n < p.N; n += gridDim.y) {
+    // sequence n's edges
+    auto scan = [&](int n) {
         int64_t a, b;
         seq_range(p.cu, n, p.N, p.T, p.err, a, b);
         const int count = (int)((b - a + p.L - 1) / p.L);
-        if (count < 2) continue;
         const int64_t base = a / p.L + n;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (e.edge[dir])
@@ -324,6 +325,19 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
                     seg[slot(i0 + u + 1) * stride + own] = acc;
                 }
         }
+    };
+    __shared__ unsigned some[8];  // of the next 256 sequences of this block's, those with segments
+    for (int n0 = blockIdx.y; n0 < p.N; n0 += 256 * gridDim.y) {
+        int64_t a = 0, b = 0;
+        const int mine = n0 + threadIdx.x * gridDim.y;
+        if (mine < p.N) seq_range(p.cu, mine, p.N, p.T, p.err, a, b);
+        const unsigned found = __ballot_sync(0xffffffffu, b - a > p.L);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) some[threadIdx.x >> 5] = found;
+        __syncthreads();
+        for (int w = 0; w < 8; ++w)
+            for (unsigned mask = some[w]; mask; mask &= mask - 1)
+                scan(n0 + (32 * w + __ffs(mask) - 1) * (int)gridDim.y);
     }
 }
 
@@ -545,7 +559,7 @@ cudaError_t launch_calls(const LinearArgs& a, const Problem& p, const Calls& cal
     unsigned* next = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.workspace) + l.next);
     if (use_tc(a.io_bf16))
         return kOut ? lintc::launch_outputs(p, calls, n, slots, rec, next, name, a.stream)
-                    : lintc::launch_sums(p, calls, n, slots, rec, dec, name, a.stream);
+                    : lintc::launch_sums(p, calls, n, slots, rec, dec, next + 1, name, a.stream);
     return a.io_bf16
                ? launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream)
                : launch_token<float, kOut>(p, calls, n, slots, dec, name, a.stream);
@@ -573,7 +587,8 @@ cudaError_t launch_segments(const LinearArgs& a, const Problem& p, const Layout&
                                               "linear_segment_kernel"))
         return err;
     ProfScope prof("linear_edge_kernel", a.stream);
-    const dim3 grid(a.H * (e.E / 1024), a.N < 64 ? a.N : 64, bwd ? 2 : 1);
+    const int per_row = a.H * (e.E / 1024), most = std::max(1, 8 * 8 * 152 / per_row);
+    const dim3 grid(per_row, std::min(a.N, most), bwd ? 2 : 1);
     return launch_dependent(edge_kernel, grid, dim3(256), 0, a.stream, p, e);
 }
 
@@ -593,8 +608,7 @@ cudaError_t launch_linear_fwd(const LinearArgs& a) {
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     if (use_tc(a.io_bf16))
         if (cudaError_t e = lintc::launch_decays(
-                p, l.slots, reinterpret_cast<float*>(ws + l.rec),
-                reinterpret_cast<unsigned*>(ws + l.next), a.stream))
+                p, reinterpret_cast<float*>(ws + l.rec), reinterpret_cast<unsigned*>(ws + l.next), a.stream))
             return e;
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, false)) return e;
@@ -614,8 +628,7 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
     auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
     if (use_tc(a.io_bf16))
         if (cudaError_t e = lintc::launch_decays(
-                p, l.slots, reinterpret_cast<float*>(ws + l.rec),
-                reinterpret_cast<unsigned*>(ws + l.next), a.stream))
+                p, reinterpret_cast<float*>(ws + l.rec), reinterpret_cast<unsigned*>(ws + l.next), a.stream))
             return e;
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, true)) return e;

@@ -158,15 +158,14 @@ __device__ __forceinline__ uint32_t item_count(const OutParams& o) {
     return (uint32_t)o.slots * o.p.H * o.n_calls;
 }
 
-// Out of line: once an item and in every role.  kWarp: called by whole warps; else by one thread.
-template <bool kWarp>
+// By one thread; out of line, once an item.
 __device__ __noinline__ Item item_at(const OutParams& o, uint32_t i) {
     Item t;
     t.call = (int)(i % o.n_calls);
     i /= o.n_calls;
     t.h = (int)(i % o.p.H);
     t.slot = (int)(i / o.p.H);
-    t.sg = lin::find_segment<kWarp>(o.p, t.slot);
+    t.sg = lin::find_segment<false>(o.p, t.slot);
     t.chunks = t.sg.live ? (t.sg.end - t.sg.begin + kC - 1) / kC : 0;
     return t;
 }
@@ -175,13 +174,6 @@ __device__ __noinline__ Item item_at(const OutParams& o, uint32_t i) {
 struct Chunk {
     int i, t0, len;
 };
-__device__ __forceinline__ Chunk chunk_at(const Item& t, int reverse, int c) {
-    Chunk k;
-    k.i = reverse ? t.chunks - 1 - c : c;
-    k.t0 = t.sg.begin + k.i * kC;
-    k.len = min(t.sg.end - k.t0, kC);
-    return k;
-}
 
 // ---------------------------------------------------------------- decays --
 // What a chunk's decays are needed as, formed once for all calls and roles: a record of floats a
@@ -195,10 +187,6 @@ constexpr int kRTail = 512;           // 2^(sum to the chunk's end, exclusive)
 constexpr int kRCol = 640, kRB = 256, kRDir = 264;
 constexpr int kRec = 1184;
 
-__device__ __forceinline__ const float* record(const OutParams& o, const Item& t, int chunk) {
-    return o.rec + ((size_t)(t.slot * (o.p.L / kC) + chunk) * o.p.H + t.h) * kRec;
-}
-
 // One warp a (chunk, head); a CTA's warps take neighbouring heads, whose decays share sectors.
 // Bound by writing the records (4.7 KB each): 27 us at 65,536 tokens x 32 heads, 2.9 TB/s.  (The
 // output kernel's own warps formed them before, and each chunk waited for them.)
@@ -208,11 +196,14 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kCounters) next[threadIdx.x] = 0u;
     const int lane = threadIdx.x & 31, per = p.L / kC;
     const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
-    const int slot = blockIdx.x / per, chunk = blockIdx.x % per;
-    const Segment sg = lin::find_segment(p, slot);
-    const int t0 = sg.begin + chunk * kC;
-    if (h >= p.H || !sg.live || t0 >= sg.end) return;
-    float* r = rec + ((size_t)blockIdx.x * p.H + h) * kRec;
+    // blocks are slots of one chunk, for most of a segment's chunks may lie past a short sequence
+    Problem chunks = p;
+    chunks.L = kC;
+    const Segment sg = lin::find_segment(chunks, (int)blockIdx.x);
+    if (h >= p.H || !sg.live) return;
+    const int t0 = sg.begin;
+    const int slot = (t0 - sg.s * kC) / p.L + sg.n + sg.s / per;
+    float* r = rec + ((size_t)(slot * per + sg.s % per) * p.H + h) * kRec;
     float e[4], P[4], Plo[4], U[4], B[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -379,7 +370,7 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
                 i = gridDim.x + atomicAdd(o.next, 1u);
             }
             if (n > 1 && !wait1(&bar.used[n & 1], ((n >> 1) - 1) & 1, err, abort)) return g;
-            if (i < items) put_item(o, item_at<false>(o, i), it);
+            if (i < items) put_item(o, item_at(o, i), it);
             else it.v[View::kChunks] = -1;
             mbar_arrive(&bar.item[n & 1]);
         } else if (!wait1(&bar.item[n & 1], (n >> 1) & 1, err, abort)) {
@@ -967,9 +958,19 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.s);
                 }
-                if (k == it.chunks() && !final) {
-                    // the copy's last read is complete: the next item's state may come
+                if (k == it.chunks()) {
+                    // the copy's last read is complete: the final state may pass through its
+                    // buffer, and the next item's come
                     if (!wait(&bar.xs, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+                    if (final) {
+                        if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+                        tc_fence_after();
+                        store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg,
+                                    sm + kSS + (warp - 8) * 8192);
+                        tc_fence_before();
+                        fence_async_smem();
+                        __syncwarp();
+                    }
                     if (lane == 0) mbar_arrive(&bar.idle);
                 }
                 if (k > 0 && !write_out<kDots>(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev,
@@ -1036,16 +1037,6 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 rowf_prev = rowf;
             }
             if (!ok) break;
-            if (final) {
-                if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) break;
-                tc_fence_after();
-                store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg,
-                            sm + kSS + (warp - 8) * 8192);
-                tc_fence_before();
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.idle);
-            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.used[n & 1]);
         }
@@ -1082,11 +1073,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 // conversion 176 us; a third stage for Y and W gained nothing).
 constexpr int kSumThreads = 640;
 constexpr uint32_t kUY = 0, kUW = 32768, kULo = 65536, kUStage = 98304;  // two stages
-constexpr uint32_t kUBar = 2 * kUStage;
+constexpr uint32_t kUItem = 2 * kUStage;
+constexpr uint32_t kUBar = kUItem + 128;
 constexpr uint32_t kSumSmem = kUBar + 256;
 
 struct SumBars {
     uint64_t full[2], done[2], wd[2], stored, drain;
+    uint64_t item[2], used[2];  // as in OutBars (17 arrivals)
     uint32_t tmem;
     int abort;
 };
@@ -1104,6 +1097,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.done[i], 1);
             mbar_init(&bar.wd[i], 16);
+            mbar_init(&bar.item[i], 1);
+            mbar_init(&bar.used[i], 17);
         }
         mbar_init(&bar.stored, 16);
         mbar_init(&bar.drain, 1);
@@ -1124,42 +1119,89 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
     };
     int loads = 0;  // stages loaded by the TMA thread (for the way out of an abort)
 
-    if (tid == 0) {
-        uint32_t g = 0;
+    auto view = [&](uint32_t n) {
+        return View{reinterpret_cast<volatile int*>(sm + kUItem) + 12 * (n & 1)};
+    };
+
+    if (warp == 0) {
+        // Items are taken some at a time, as CTAs come to them: where most sequences are shorter
+        // than a segment most items have no sum, and a lane each finds that out.
+        const uint32_t some = min(32u, 1 + items / (8 * gridDim.x));
+        uint32_t g = 0, n = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at<false>(o, i);
-            if (skip(t)) continue;
-            const Call& c = o.calls.c[t.call];
-            for (int k = 0; k < t.chunks; ++k, ++g) {
-                const uint32_t st = g & 1;
-                if (g >= 2 && !wait1(&bar.done[st], ((g - 2) >> 1) & 1, p.err, abort)) {
+        for (uint32_t round = 0; ok; ++round) {
+            uint32_t base = blockIdx.x;
+            if (round > 0) {
+                if (round == 1) grid_dependency_wait();
+                if (lane == 0) base = gridDim.x + atomicAdd(o.next, 1u);
+                base = __shfl_sync(0xffffffffu, base, 0);
+            }
+            base *= some;
+            if (base >= items) break;
+            Item t{};
+            bool has = lane < some && base + lane < items;
+            if (has) {
+                t = item_at(o, base + lane);
+                has = !skip(t);
+            }
+            for (uint32_t mask = __ballot_sync(0xffffffffu, has); ok && mask; mask &= mask - 1) {
+                if (n > 1 && !wait(&bar.used[n & 1], ((n >> 1) - 1) & 1, p.err, abort)) {
                     ok = false;
                     break;
                 }
-                const Chunk ch = chunk_at(t, !c.reverse, k);
-                uint8_t* s = sm + st * kUStage;
-                mbar_expect_tx(&bar.full[st], (c.da + c.db) / 64 * 16384);
+                const View it = view(n);
+                if (lane == __ffs(mask) - 1) {
+                    put_item(o, t, it);
+                    it.v[View::kRev] = !it.v[View::kRev];  // the walk's direction here
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.item[n & 1]);
+                    const int call = it.call(), h = it.h();
+                    const Call& c = o.calls.c[call];
+                    for (int k = 0; k < it.chunks(); ++k, ++g) {
+                        const uint32_t st = g & 1;
+                        if (g >= 2 && !wait1(&bar.done[st], ((g - 2) >> 1) & 1, p.err, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        const Chunk ch = it.chunk(k);
+                        uint8_t* s = sm + st * kUStage;
+                        mbar_expect_tx(&bar.full[st], (c.da + c.db) / 64 * 16384);
 #pragma unroll 1
-                for (int b = 0; b < c.da / 64; ++b)
-                    tma_load_3d(s + kUY + b * 16384, &o.y[t.call], 64 * b, t.h, ch.t0, &bar.full[st]);
+                        for (int b = 0; b < c.da / 64; ++b)
+                            tma_load_3d(s + kUY + b * 16384, &o.y[call], 64 * b, h, ch.t0,
+                                        &bar.full[st]);
 #pragma unroll 1
-                for (int b = 0; b < c.db / 64; ++b)
-                    tma_load_3d(s + kUW + b * 16384, &o.w[t.call], 64 * b, t.h, ch.t0, &bar.full[st]);
-                loads = (int)g + 1;
+                        for (int b = 0; b < c.db / 64; ++b)
+                            tma_load_3d(s + kUW + b * 16384, &o.w[call], 64 * b, h, ch.t0,
+                                        &bar.full[st]);
+                        loads = (int)g + 1;
+                    }
+                }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                ++n;
             }
+        }
+        if (ok && (n < 2 || wait(&bar.used[n & 1], ((n >> 1) - 1) & 1, p.err, abort)) &&
+            lane == 0) {
+            view(n).v[View::kChunks] = -1;
+            mbar_arrive(&bar.item[n & 1]);
         }
     } else if (tid == 32) {
         const uint32_t lY = dlow(sbase + kUY, 16384), lHi = dlow(sbase + kUW, 16384);
         const uint32_t lLo = dlow(sbase + kULo, 16384);
         uint32_t g = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at<false>(o, i);
-            if (skip(t)) continue;
+        for (uint32_t n = 0; ok; ++n) {
+            if (!wait1(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
+            const View it = view(n);
+            const int chunks = it.chunks();
+            if (chunks < 0) break;
             const uint32_t id =
-                idesc_bf16(128, 0, true, true) | (uint32_t)(o.calls.c[t.call].db >> 3) << 17;
-            for (int k = 0; k < t.chunks; ++k, ++g) {
+                idesc_bf16(128, 0, true, true) | (uint32_t)(o.calls.c[it.call()].db >> 3) << 17;
+            mbar_arrive(&bar.used[n & 1]);
+            for (int k = 0; k < chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
                 if (!wait1(&bar.wd[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
@@ -1182,30 +1224,31 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
         uint32_t g = 0, stored = 0;
         bool ok = true;
-        for (uint32_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item t = item_at<true>(o, i);
-            if (skip(t)) continue;
-            const Call& c = o.calls.c[t.call];
+        for (uint32_t n = 0; ok; ++n) {
+            if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
+            const View it = view(n);
+            const int chunks = it.chunks();
+            if (chunks < 0) break;
+            const Call& c = o.calls.c[it.call()];
             const int rev = c.reverse;
             const bool cols = 32 * cg < c.db;
             float between = 0.f;  // log2 decay between the edge and the chunk
             const int mine = (rev ? kRHead : kRTail) + row;
-            const float* r = record(o, t, chunk_at(t, !rev, 0).i);
+            const float* r = it.record(o, 0);
             float next = __ldg(r + mine), total = __ldg(r + kRCol + kRB + 4);
 #pragma unroll 1
-            for (int k = 0; k < t.chunks; ++k, ++g) {
+            for (int k = 0; k < chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
-                const Chunk ch = chunk_at(t, !rev, k);
                 const float wf = next * ex2f(between);
                 between += total;
-                if (k + 1 < t.chunks) {  // the next chunk's, early
-                    r = record(o, t, chunk_at(t, !rev, k + 1).i);
+                if (k + 1 < chunks) {  // the next chunk's, early
+                    r = it.record(o, k + 1);
                     next = __ldg(r + mine);
                     total = __ldg(r + kRCol + kRB + 4);
                 }
                 if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 uint8_t* stage = sm + st * kUStage;
-                const bool dead = row >= ch.len;
+                const bool dead = row >= it.chunk(k).len;
                 if (cols) {
                     uint8_t* wr = stage + kUW + (cg >> 1) * 16384 + row * 128;
                     uint8_t* lr = stage + kULo + (cg >> 1) * 16384 + row * 128;
@@ -1262,7 +1305,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                         make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
                 __syncwarp();
                 float* to = const_cast<float*>(c.seg) +
-                            (((int64_t)t.slot * p.H + t.h) * c.da + 32 * q) * c.db + 32 * cg;
+                            ((int64_t)it.v[View::kState] * c.da + 32 * q) * c.db + 32 * cg;
                 if (32 * q < c.da)
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
@@ -1279,7 +1322,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             if (!wait(&bar.stored, stored & 1, p.err, abort)) { ok = false; break; }
             ++stored;
             if (warp == 4 && lane == 0)
-                dec[((int64_t)rev * o.slots + t.slot) * p.H + t.h] = between;
+                dec[(int64_t)rev * o.slots * p.H + it.v[View::kState]] = between;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.used[n & 1]);
         }
     }
 
@@ -1383,10 +1428,10 @@ size_t record_bytes(int64_t slots, int L, int H) {
     return (size_t)slots * (L / kC) * H * kRec * sizeof(float);
 }
 
-cudaError_t launch_decays(const Problem& p, int64_t slots, float* rec, unsigned* next,
-                          cudaStream_t s) {
+cudaError_t launch_decays(const Problem& p, float* rec, unsigned* next, cudaStream_t s) {
     ProfScope prof("linear_decay_kernel", s);
-    decay_kernel<<<dim3((unsigned)(slots * (p.L / kC)), (p.H + 7) / 8), 256, 0, s>>>(p, rec, next);
+    const dim3 grid((unsigned)lin::slot_count(p.T, p.N, kC), (p.H + 7) / 8);
+    decay_kernel<<<grid, 256, 0, s>>>(p, rec, next);
     return cudaGetLastError();
 }
 
@@ -1408,8 +1453,10 @@ cudaError_t launch_outputs(const Problem& p, const lin::Calls& calls, int n, int
 }
 
 cudaError_t launch_sums(const Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                        const float* rec, float* dec, const char* name, cudaStream_t s) {
+                        const float* rec, float* dec, unsigned* next, const char* name,
+                        cudaStream_t s) {
     OutParams o{};
+    o.next = next;
     if (cudaError_t e = fill(o, p, calls, n, slots, rec, false)) return e;
     if (cudaError_t e = cudaFuncSetAttribute(
             sum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSumSmem))

@@ -10,10 +10,9 @@ namespace lintc {
 
 // What the kernels below need of the decays, once for all calls (`rec` holds record_bytes()), and
 // the counters of taken items, zeroed.
-constexpr int kCounters = 1;
+constexpr int kCounters = 2;
 size_t record_bytes(int64_t slots, int L, int H);
-cudaError_t launch_decays(const lin::Problem& p, int64_t slots, float* rec, unsigned* next,
-                          cudaStream_t s);
+cudaError_t launch_decays(const lin::Problem& p, float* rec, unsigned* next, cudaStream_t s);
 
 // Every segment's outputs (and final states) from its edge state; `next`: a zeroed counter.
 cudaError_t launch_outputs(const lin::Problem& p, const lin::Calls& calls, int n, int64_t slots,
@@ -22,7 +21,8 @@ cudaError_t launch_outputs(const lin::Problem& p, const lin::Calls& calls, int n
 // Every segment's own contribution to the state into calls.c[i].seg, and its summed log2 decay
 // into dec[reverse][slot][head]; states in memory are [da][db] (tr = 0).
 cudaError_t launch_sums(const lin::Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                        const float* rec, float* dec, const char* name, cudaStream_t s);
+                        const float* rec, float* dec, unsigned* next, const char* name,
+                        cudaStream_t s);
 
 }  // namespace lintc
 }  // namespace kda
