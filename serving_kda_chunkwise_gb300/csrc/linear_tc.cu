@@ -1026,7 +1026,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                             uint4* wr = reinterpret_cast<uint4*>(sm + kSW + wg * 16384 + row * 128);
                             uint4* yr = reinterpret_cast<uint4*>(sm + kSY + wg * 16384 + row * 128);
 #pragma unroll 1
-                            for (int x = 0; x < 8; ++x) wr[x] = yr[x] = make_uint4(0u, 0u, 0u, 0u);
+                            for (int x = 0; x < 8; ++x)  // (each lane from another piece: other banks)
+                                wr[(x + lane) & 7] = yr[(x + lane) & 7] = make_uint4(0u, 0u, 0u, 0u);
                         }
                     }
                     fence_async_smem();
@@ -1279,7 +1280,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                 if (dead) {
                     uint4* yr = reinterpret_cast<uint4*>(stage + kUY + (cg >> 1) * 16384 + row * 128);
 #pragma unroll 1
-                    for (int x = 0; x < 4; ++x) yr[4 * (cg & 1) + x] = make_uint4(0u, 0u, 0u, 0u);
+                    for (int x = 0; x < 4; ++x)
+                        yr[(4 * (cg & 1) + x) ^ (row & 7)] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_smem();
                 __syncwarp();
