@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
             for (int u = 0; u < kAhead; ++u)
                 if (i0 + u < count - 1) {
                     in[u] = __ldcs(add + slot(i0 + u) * stride + own);
-                    d[u] = __ldcg(e.dec[dir] + slot(i0 + u) * p.H + h);
+                    d[u] = e.dec[dir][slot(i0 + u) * p.H + h];
                 }
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
