@@ -471,11 +471,12 @@ bool use_tc(int io_bf16) {
 
 // Tokens a segment.  On the tensor cores a segment's chunks in a row cost less than its edge states
 // (two fp32 states a segment, written, read and loaded), so segments are as long as they can be
-// with one for every SM: at 8,192 tokens x 16 heads 1,024 tokens take 83 us, 512 take 93, 256 111.
-// Not beyond 2,048, where the last round's ends cost more (65,536 x 32: 857 us, with 4,096 911, with
-// 1,024 920); in the gradients not beyond 1,024, for sums over 2,048 tokens between anchors cost
+// with one for every SM: at 8,192 tokens x 16 heads 1,024 tokens take 83 us, 512 take 89, 256 105.
+// Not beyond 2,048, where the last round's ends cost more (65,536 x 32: 838 us, with 4,096 888, with
+// 1,024 886; packed prompts up to 5,753 tokens x 16: 314, 345, 298); in the gradients not beyond 1,024, for sums over 2,048 tokens between anchors cost
 // dg's last bits (1e-5 instead of 7e-6).  Up to 512 tokens take one launch: four chunks in a row
-// take no longer than two more launches (256 x 4: 22 against 29 us, 512 x 4: 31 against 30).
+// take about as long as two more launches (256 x 4: 21 against 28 us, 512 x 4: 31 against 28, its
+// gradients 40 against 40, 512 x 32's 48 against 71).
 // Token by token a segment is walked by as many CTAs as its state has blocks, and each SM needs
 // several to be busy: four segments an SM (2,048 + 1,531 tokens x 8 heads: 77 us, two 89, one 138).
 int segment_length(int64_t T, int H, bool tc, bool bwd) {

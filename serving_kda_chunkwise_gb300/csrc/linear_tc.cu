@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
 // to a CTA; that form made A twice and its N = 64 products run at 75 % of N = 128's rate, and was
 // slower.)
 // Bound by that chain: a chunk takes 8,900 cycles, of which the products are 4,400.  Measured at
-// 65,536 tokens x 32 heads x 128: 560 us (2.2 GB at 3.9 TB/s, 7 products of 4.2 MFLOP a chunk
-// and head at 860 TFLOP/s); gradients, 65,536 x 16, three calls: 1,001 us.
+// 65,536 tokens x 32 heads x 128: 547 us (2.2 GB at 4.0 TB/s, 7 products of 4.2 MFLOP a chunk
+// and head at 880 TFLOP/s); gradients, 65,536 x 16, three calls: 954 us.  Items are taken as CTAs
+// come to them (packed prompts of 17 to 5,753 tokens x 16: 219 us, dealt out 262).
 constexpr int kThreads = 640;
 constexpr int kMmaT = 19 * 32;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
@@ -552,9 +553,9 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
     uint8_t* stage = sm + kSWd + (col >> 6) * 16384;
     const int piece = (col & 32) >> 3;  // of 16 bytes, within the 128 of a row
     float acc = 0.f;
-    // 16 columns at a time, to stay within the registers (one after the other with dots: unrolled
-    // they spilled, 1083 against 1026 us for 65536 x 16; without them unrolled, 561 against 584 us
-    // for 65536 x 32)
+    // 16 columns at a time, to stay within the registers.  With dots one after the other: unrolled
+    // they spilled (1,083 against 1,026 us at 65,536 x 16).  Without them unrolled (561 against 584
+    // us at 65,536 x 32).
 #pragma unroll (kDots ? 1 : 2)
     for (int b = 0; b < 2; ++b) {
         float o1[16];
@@ -1070,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 // of a sum is free, so the chunks run away from the edge the weights refer to, the decay between
 // the edge and the chunk carried along, and the accumulator in TMEM is never rescaled.  W is
 // decayed in place (hi over W itself, lo beside it), so two stages of all operands fit.  Bound by
-// reading Y and W: 215 us at 65,536 tokens x 32 heads x 128, 1.07 GB at 5.0 TB/s (without the
+// reading Y and W: 209 us at 65,536 tokens x 32 heads x 128, 1.07 GB at 5.1 TB/s (without the
 // conversion 176 us; a third stage for Y and W gained nothing).
 constexpr int kSumThreads = 640;
 constexpr uint32_t kUY = 0, kUW = 32768, kULo = 65536, kUStage = 98304;  // two stages
