@@ -389,3 +389,38 @@ def test_f32_fixed_decay_over_many_tokens(kda, decay):
     # fp32 sums of some hundred terms, 2^-24 each in quadrature: below 2e-6
     assert float((o.double() - ro).norm()) <= 2e-6 * float(ro.norm())
     assert float((S.double() - rS).norm()) <= 2e-6 * float(rS.norm())
+
+
+@pytest.mark.parametrize("dtype,lengths", [("bf16", [200, 52]), ("bf16", [2500, 17, 900]),
+                                           ("f32", [900, 300])])
+def test_graph_and_two_streams(kda, dtype, lengths):
+    """Replayed from a graph, and on two streams at once, the results are the same bits."""
+    import torch
+    x = _inputs(25, lengths, 4, 128, 128, dtype)
+
+    def run():
+        f = kda.linear_fwd_chunked(x["q"], x["k"], x["v"], x["g"], S0=x["S0"], cu_seqlens=x["cu"])
+        b = kda.linear_bwd(x["q"], x["k"], x["v"], x["g"], x["do"], S0=x["S0"], dS_out=x["dS"],
+                           cu_seqlens=x["cu"])
+        return list(f) + [b[n] for n in sorted(b)]
+
+    first = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(first, out):
+        assert torch.equal(a, b)
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(4):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(run())
+    torch.cuda.synchronize()
+    kda.device_status()
+    for o in outs:
+        for a, b in zip(first, o):
+            assert torch.equal(a, b)
