@@ -3,6 +3,11 @@
 Argument marshalling only -- every step of the computation runs in the library's
 CUDA kernels.  Torch is used for device memory and streams.  Importing this module
 loads ``_build/libkda.so`` and raises if it is missing: there is no fallback path.
+
+``stream`` (a ``torch.cuda.Stream``; None for the current one) is where a call's kernels run.  The
+outputs and the workspace that a call makes itself are of that stream's memory; that it waits for
+the stream that made the inputs, and that a stream that reads the outputs waits for it, is the
+caller's to arrange.
 """
 from __future__ import annotations
 
@@ -138,6 +143,31 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A new tensor that a call on `stream` may write: of that stream's memory (a block of another
+    stream's may still be in use there), and kept from reuse until the current stream, where the
+    caller reads it, has done so."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _scratch(workspace, need: int, device, stream):
+    """(workspace, its bytes): the caller's where it is large enough, else one of the memory of the
+    stream that the call runs on, for it is dropped when the call returns and a block of another
+    stream's could be handed out there while the kernels run."""
+    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        if stream is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
 def _need(t: torch.Tensor, name: str, dtype=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -157,7 +187,7 @@ def gate(z: torch.Tensor, A_log: torch.Tensor, g_min: float, g_out=None, stream=
     _need(A_log, "A_log", torch.float32)
     T, H, dk = z.shape
     if g_out is None:
-        g_out = torch.empty((T, H, dk), dtype=torch.float32, device=z.device)
+        g_out = _empty((T, H, dk), torch.float32, z.device, stream)
     _need(g_out, "g_out", torch.float32)
     _check(_lib.kda_gate(_ptr(z), _dt(z), _ptr(A_log), float(g_min), _ptr(g_out), T, H, dk,
                          _stream(stream)), "kda_gate")
@@ -191,16 +221,14 @@ def fwd_chunked(q, k, v, beta, z, A_log, g_min: float, S0=None, cu_seqlens=None,
     if S0 is not None:
         _need(S0, "S0", torch.float32)
     if o is None:
-        o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((T, H, dv), q.dtype, q.device, stream)
     _need(o, "o", q.dtype)
     if S_out is None and want_state:
-        S_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+        S_out = _empty((N, H, dk, dv), torch.float32, q.device, stream)
     if S_out is not None:
         _need(S_out, "S_out", torch.float32)
     need = workspace_size(T, N, H, dk, dv, q.dtype)
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _scratch(workspace, need, q.device, stream)
     _check(_lib.kda_fwd_chunked(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(z), _ptr(A_log),
                                 float(g_min), _ptr(S0), _ptr(S_out), _ptr(cu_seqlens), int(N),
                                 int(T), int(H), int(dk), int(dv), _dt(q), _ptr(o), _ptr(workspace),
@@ -318,15 +346,13 @@ def fwd_chunked_softplus(q, k, v, beta, z, A_log, S0=None, cu_seqlens=None, N=No
     elif N is None:
         N = 1
     if o is None:
-        o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((T, H, dv), q.dtype, q.device, stream)
     if S_out is None and want_state:
-        S_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+        S_out = _empty((N, H, dk, dv), torch.float32, q.device, stream)
     if S0 is not None:
         _need(S0, "S0", torch.float32)
     need = workspace_size(T, N, H, dk, dv, q.dtype)
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    workspace, ws_bytes = _scratch(workspace, need, q.device, stream)
     _check(_lib.kda_fwd_chunked_softplus(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(z),
                                          _ptr(A_log), _ptr(S0), _ptr(S_out), _ptr(cu_seqlens),
                                          int(N), int(T), int(H), int(dk), int(dv), _dt(q),
@@ -355,14 +381,17 @@ def bwd(q, k, v, beta, z, A_log, g_min: float, dout, S0=None, dS_out=None, cu_se
         if t is not None:
             _need(t, nm, torch.float32)
     dev = q.device
-    out = {"dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
-           "dbeta": torch.empty_like(beta), "dz": torch.empty_like(z),
-           "dA_log": torch.empty(H, dtype=torch.float32, device=dev),
-           "dS0": (torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    out = {"dq": _empty((T, H, dk), q.dtype, dev, stream),
+           "dk": _empty((T, H, dk), q.dtype, dev, stream),
+           "dv": _empty((T, H, dv), q.dtype, dev, stream),
+           "dbeta": _empty((T, H), q.dtype, dev, stream),
+           "dz": _empty((T, H, dk), q.dtype, dev, stream),
+           "dA_log": _empty(H, torch.float32, dev, stream),
+           "dS0": (_empty((N, H, dk, dv), torch.float32, dev, stream)
                    if want_dS0 else None)}
     need = int(_lib.kda_bwd_workspace_size(int(T), int(N), int(H), int(dk), int(dv)))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace, _ = _scratch(None, max(need, 16), dev, stream)
     _check(_lib.kda_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(z), _ptr(A_log),
                         float(g_min), _ptr(S0), _ptr(cu_seqlens), int(N), int(T), int(H),
                         int(dk), int(dv), _dt(q), _ptr(dout), _ptr(dS_out), _ptr(out["dq"]),
@@ -384,7 +413,7 @@ def decode_step(q, k, v, beta, z, A_log, g_min: float, S, o=None, stream=None):
     N, H, dk = q.shape
     dv = v.shape[2]
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((N, H, dv), q.dtype, q.device, stream)
     _need(o, "o", q.dtype)
     _check(_lib.kda_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(z), _ptr(A_log),
                                 float(g_min), _ptr(S), int(N), int(H), int(dk), int(dv), _dt(q),
@@ -403,7 +432,7 @@ def output_norm_gate(o, gate, norm_w=None, eps: float = 1e-6, y=None, stream=Non
         _need(norm_w, "norm_w", torch.float32)
     T, H, dv = o.shape
     if y is None:
-        y = torch.empty_like(o)
+        y = _empty(o.shape, o.dtype, o.device, stream)
     _need(y, "y", o.dtype)
     _check(_lib.kda_output_norm_gate(_ptr(o), _ptr(gate), _ptr(norm_w), float(eps), _ptr(y),
                                      int(T), int(H), int(dv), _dt(o), _stream(stream)),
@@ -423,7 +452,7 @@ def decode_step_gated(q, k, v, beta, z, A_log, g_min: float, S, gate, norm_w=Non
     N, H, dk = q.shape
     dv = v.shape[2]
     if y is None:
-        y = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        y = _empty((N, H, dv), q.dtype, q.device, stream)
     _need(y, "y", q.dtype)
     _check(_lib.kda_decode_step_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(z),
                                       _ptr(A_log), float(g_min), _ptr(S), _ptr(gate),
@@ -464,12 +493,6 @@ def _decay(g: torch.Tensor, T: int, H: int) -> int:
     return 1
 
 
-def _scratch(workspace, need: int, device):
-    if need > 0 and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
-
-
 def _packed(q, k, v, cu_seqlens, N):
     """Shared shape checks of the linear attention: (T, N, H, dk, dv)."""
     T, H, dk = q.shape
@@ -502,18 +525,18 @@ def linear_fwd_chunked(q, k, v, g, S0=None, cu_seqlens=None, N=None, o=None, S_o
     per_token = _decay(g, T, H)
     dt = _dt(q)
     if o is None:
-        o = torch.empty((T, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((T, H, dv), q.dtype, q.device, stream)
     else:
         _need(o, "o", q.dtype)
         _shape(o, "o", (T, H, dv))
     if S_out is None and want_state:
-        S_out = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+        S_out = _empty((N, H, dk, dv), torch.float32, q.device, stream)
     for t, nm in ((S0, "S0"), (S_out, "S_out")):
         if t is not None:
             _need(t, nm, torch.float32)
             _shape(t, nm, (N, H, dk, dv))
     workspace, ws_bytes = _scratch(
-        workspace, _lib.kda_linear_fwd_workspace_size(T, N, H, dk, dv, dt), q.device)
+        workspace, _lib.kda_linear_fwd_workspace_size(T, N, H, dk, dv, dt), q.device, stream)
     _check(_lib.kda_linear_fwd_chunked(_ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(g), per_token,
                                        _ptr(S0), _ptr(S_out), _ptr(cu_seqlens), N, T, H, dk, dv,
                                        dt, _ptr(o), _ptr(workspace), ws_bytes, _stream(stream)),
@@ -538,14 +561,14 @@ def linear_bwd(q, k, v, g, dout, S0=None, dS_out=None, cu_seqlens=None, N=None,
             _need(t, nm, torch.float32)
             _shape(t, nm, (N, H, dk, dv))
     dt, dev = _dt(q), q.device
-    out = {"dq": torch.empty((T, H, dk), dtype=q.dtype, device=dev),
-           "dk": torch.empty((T, H, dk), dtype=q.dtype, device=dev),
-           "dv": torch.empty((T, H, dv), dtype=q.dtype, device=dev),
-           "dg": torch.empty_like(g) if want_dg else None,
-           "dS0": (torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    out = {"dq": _empty((T, H, dk), q.dtype, dev, stream),
+           "dk": _empty((T, H, dk), q.dtype, dev, stream),
+           "dv": _empty((T, H, dv), q.dtype, dev, stream),
+           "dg": _empty(g.shape, g.dtype, g.device, stream) if want_dg else None,
+           "dS0": (_empty((N, H, dk, dv), torch.float32, dev, stream)
                    if want_dS0 else None)}
     workspace, ws_bytes = _scratch(
-        workspace, _lib.kda_linear_bwd_workspace_size(T, N, H, dk, dv, dt), dev)
+        workspace, _lib.kda_linear_bwd_workspace_size(T, N, H, dk, dv, dt), dev, stream)
     _check(_lib.kda_linear_bwd(_ptr(q), lq, _ptr(k), lk, _ptr(v), lv, _ptr(g), per_token,
                                _ptr(S0), _ptr(cu_seqlens), N, T, H, dk, dv, dt, _ptr(dout), ldo,
                                _ptr(dS_out), _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dv"]),
@@ -571,7 +594,7 @@ def linear_decode_step(q, k, v, g, S, slots=None, o=None, stream=None):
         _need(slots, "slots", torch.int32)
         _shape(slots, "slots", (N,))
     if o is None:
-        o = torch.empty((N, H, dv), dtype=q.dtype, device=q.device)
+        o = _empty((N, H, dv), q.dtype, q.device, stream)
     else:
         _need(o, "o", q.dtype)
         _shape(o, "o", (N, H, dv))
@@ -619,9 +642,9 @@ def qk_norm_rope(q, k, wq=None, wk=None, eps: float = 1e-6, cos_sin=None, positi
             _need(t, nm, q.dtype)
             _shape(t, nm, (T, H, d))
     if q_out is None:
-        q_out = torch.empty((T, Hq, d), dtype=q.dtype, device=q.device)
+        q_out = _empty((T, Hq, d), q.dtype, q.device, stream)
     if k_out is None:
-        k_out = torch.empty((T, Hk, d), dtype=q.dtype, device=q.device)
+        k_out = _empty((T, Hk, d), q.dtype, q.device, stream)
     _check(_lib.kda_qk_norm_rope(_ptr(q), lq, _ptr(k), lk, _ptr(wq), _ptr(wk), eps,
                                  _ptr(cos_sin), n_pos, _ptr(positions), rot, int(interleaved),
                                  _ptr(q_out), _ptr(k_out), T, Hq, Hk, d, _dt(q),
@@ -642,12 +665,12 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, cos_si
         _need(t, nm, q.dtype)
         _shape(t, nm, (T, H, d))
     dev = q.device
-    out = {"dq": torch.empty((T, Hq, d), dtype=q.dtype, device=dev),
-           "dk": torch.empty((T, Hk, d), dtype=q.dtype, device=dev),
-           "dwq": None if wq is None else torch.empty(d, dtype=torch.float32, device=dev),
-           "dwk": None if wk is None else torch.empty(d, dtype=torch.float32, device=dev)}
+    out = {"dq": _empty((T, Hq, d), q.dtype, dev, stream),
+           "dk": _empty((T, Hk, d), q.dtype, dev, stream),
+           "dwq": None if wq is None else _empty(d, torch.float32, dev, stream),
+           "dwk": None if wk is None else _empty(d, torch.float32, dev, stream)}
     need = 0 if wq is None and wk is None else _lib.kda_qk_norm_rope_bwd_workspace_size(d)
-    workspace, ws_bytes = _scratch(workspace, need, dev)
+    workspace, ws_bytes = _scratch(workspace, need, dev, stream)
     _check(_lib.kda_qk_norm_rope_bwd(_ptr(q), lq, _ptr(k), lk, _ptr(dyq), _ptr(dyk), _ptr(wq),
                                      _ptr(wk), eps, _ptr(cos_sin), n_pos, _ptr(positions), rot,
                                      int(interleaved), _ptr(out["dq"]), _ptr(out["dk"]),
@@ -665,12 +688,12 @@ def quantile_balance(scores, bias, k: int, want_bhat=False, want_alpha=False, wo
     _need(bias, "bias", torch.float32)
     m, n = scores.shape
     dev = scores.device
-    b_new = torch.empty(n, dtype=torch.float32, device=dev)
-    bhat = torch.empty(n, dtype=torch.float32, device=dev) if want_bhat else None
-    alpha = torch.empty(m, dtype=torch.float32, device=dev) if want_alpha else None
+    b_new = _empty(n, torch.float32, dev, stream)
+    bhat = _empty(n, torch.float32, dev, stream) if want_bhat else None
+    alpha = _empty(m, torch.float32, dev, stream) if want_alpha else None
     need = int(_lib.kda_quantile_balance_workspace_size(int(m), int(n)))
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace, _ = _scratch(None, max(need, 16), dev, stream)
     _check(_lib.kda_quantile_balance(_ptr(scores), _ptr(bias), int(m), int(n), int(k),
                                      _ptr(b_new), _ptr(bhat), _ptr(alpha), _ptr(workspace),
                                      workspace.numel(), _stream(stream)), "kda_quantile_balance")
