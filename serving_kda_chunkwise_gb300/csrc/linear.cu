@@ -13,11 +13,18 @@
 // a programmatic dependent of the one before: it is set up beside it and waits before it reads
 // what that wrote (every kernel waits, so that a launch's end is that of all before it).
 //
-// The gradient of g:  dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_out>.  Taken over
-// a long sequence that sum would gather the rounding of every later token.  At every segment's
+// The gradient of g:  dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_out>.  Both dot
+// products hold the token's own term (q_s . k_s) (v_s . do_s), the only one without a decay.  It is
+// left out of both: carried along, its rounding would drown the rest where decays are strong (dg of
+// a head is of the size of e^g; at g = -10 everywhere it came out 1 % off, a fixed decay's 100 times
+// too large).  Taken over a long sequence the sum would gather the rounding of every later token.
+// At every segment's
 // edges it is <S, D>, from states that are at hand, so the sums run inside a segment, from the
-// anchor at its end; what they miss the anchor at its start by is their rounding, and is taken
-// back token by token in proportion to the terms' sizes.
+// anchor at its start: dg_t = <S, D> - sum_{s < t} (...).  What they miss the anchor at its end by
+// is their rounding, and is taken back token by token in proportion to the squares of the terms'
+// sizes, as independent errors are best shared out.  (From the
+// end they would begin, at a sequence's last token, with <S_T, dS_out>, in which that token's own
+// k v^T has no decay either.)
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
@@ -60,13 +67,17 @@ __device__ __forceinline__ float4 load_row4(const IO* p) {
     }
 }
 
-template <int DA, typename IO, bool kOut>
+// kDots: some call wants its outputs' dot products.  Then outputs come from the decayed state of
+// before the token's own update, and its own term (x . y) w joins them after the dot product.
+template <int DA, typename IO, bool kOut, bool kDots>
 __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Problem p,
                                                     const __grid_constant__ Calls calls,
                                                     float* dec,
                                                     int blocks_per_call) {
     constexpr int R = DA / 4, kPer = kTile * DA / 4 / 128, kPerW = kTile * kCols / 4 / 128;
-    __shared__ __align__(16) float xs[kOut ? kTile : 1][DA], ys[kTile][DA], ws[kTile][kCols];
+    __shared__ __align__(16) float xs[kOut ? kTile : 1][DA], ys[kTile][DA];
+    __shared__ __align__(16) float ws[kDots ? 2 : 1][kTile][kCols];  // (kDots: the last tile's too)
+    __shared__ float xy[kTile];  // x . y
     __shared__ float2 fs[kTile];  // how the state decays before the token: factor, near
     __shared__ float2 part[kOut ? 4 : 1][kTile][kCols / 2];
     if (kOut) grid_dependency_wait();
@@ -189,12 +200,7 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
                 o.x += part[u][i][lane].x;
                 o.y += part[u][i][lane].y;
             }
-            IO* to = static_cast<IO*>(c.out) + (t * p.H + h) * c.db + col;
-            if constexpr (sizeof(IO) == 4)
-                *reinterpret_cast<float2*>(to) = o;
-            else
-                *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(o.x, o.y);
-            if (c.dot) {
+            if (kDots && c.dot) {
                 const IO* y = static_cast<const IO*>(c.dot) + t * c.dot_ld + h * c.db + col;
                 float x = fmaf(o.x, to_f32(y[0]), o.y * to_f32(y[1]));
 #pragma unroll
@@ -202,10 +208,21 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
                 if ((lane & 15) == 0)
                     c.dots[((int64_t)(col / kDotCols) * p.H + h) * p.T + t] = x;
             }
+            if (kDots) {
+                const float2 w =
+                    *reinterpret_cast<const float2*>(&ws[t0 / kTile & 1][i][2 * lane]);
+                o = fma2(make_float2(xy[i], xy[i]), w, o);
+            }
+            IO* to = static_cast<IO*>(c.out) + (t * p.H + h) * c.db + col;
+            if constexpr (sizeof(IO) == 4)
+                *reinterpret_cast<float2*>(to) = o;
+            else
+                *reinterpret_cast<__nv_bfloat162*>(to) = __floats2bfloat162_rn(o.x, o.y);
         }
     };
     load_tile(0);
     for (int t0 = 0; t0 < len; t0 += kTile) {
+        const int buf = kDots ? t0 / kTile & 1 : 0;
         __syncthreads();
         if (kOut && t0 > 0) write_out(t0 - kTile);
 #pragma unroll
@@ -214,7 +231,7 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
             reinterpret_cast<float4*>(ys)[e + 128 * j] = ny[j];
         }
 #pragma unroll
-        for (int j = 0; j < kPerW; ++j) reinterpret_cast<float4*>(ws)[e + 128 * j] = nw[j];
+        for (int j = 0; j < kPerW; ++j) reinterpret_cast<float4*>(ws[buf])[e + 128 * j] = nw[j];
         if (e < kTile) {
             fs[e] = factor(ng);
             gsum += ng;
@@ -222,27 +239,38 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
         __syncthreads();
         if (t0 + kTile < len) load_tile(t0 + kTile);
         const int m = min(kTile, len - t0);
+        if (kDots)
+            for (int i = warp; i < m; i += 4) {
+                float x = 0.f;
+#pragma unroll
+                for (int d = lane; d < DA; d += 32) x = fmaf(xs[i][d], ys[i][d], x);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+                if (lane == 0) xy[i] = x;
+            }
         for (int i = 0; i < m; ++i) {
             decay(fs[i]);
-            const float2 w = *reinterpret_cast<const float2*>(&ws[i][2 * lane]);
+            const float2 w = *reinterpret_cast<const float2*>(&ws[buf][i][2 * lane]);
             const float2 w0 = make_float2(w.x, w.x), w1 = make_float2(w.y, w.y);
             float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+            auto read = [&](int r) {
+                const float4 x = *reinterpret_cast<const float4*>(&xs[i][row0 + 4 * r]);
+                const float2 xa = make_float2(x.x, x.y), xb = make_float2(x.z, x.w);
+                a0 = fma2(xa, S[0][2 * r], a0);
+                a1 = fma2(xa, S[1][2 * r], a1);
+                a0 = fma2(xb, S[0][2 * r + 1], a0);
+                a1 = fma2(xb, S[1][2 * r + 1], a1);
+            };
 #pragma unroll
             for (int r = 0; r < R / 4; ++r) {
+                if (kDots) read(r);
                 const float4 y = *reinterpret_cast<const float4*>(&ys[i][row0 + 4 * r]);
                 const float2 ya = make_float2(y.x, y.y), yb = make_float2(y.z, y.w);
                 S[0][2 * r] = fma2(ya, w0, S[0][2 * r]);
                 S[1][2 * r] = fma2(ya, w1, S[1][2 * r]);
                 S[0][2 * r + 1] = fma2(yb, w0, S[0][2 * r + 1]);
                 S[1][2 * r + 1] = fma2(yb, w1, S[1][2 * r + 1]);
-                if (kOut) {
-                    const float4 x = *reinterpret_cast<const float4*>(&xs[i][row0 + 4 * r]);
-                    const float2 xa = make_float2(x.x, x.y), xb = make_float2(x.z, x.w);
-                    a0 = fma2(xa, S[0][2 * r], a0);
-                    a1 = fma2(xa, S[1][2 * r], a1);
-                    a0 = fma2(xb, S[0][2 * r + 1], a0);
-                    a1 = fma2(xb, S[1][2 * r + 1], a1);
-                }
+                if (kOut && !kDots) read(r);
             }
             if (kOut) part[warp][i][lane] = make_float2(a0.x + a0.y, a1.x + a1.y);
         }
@@ -342,8 +370,8 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
 }
 
 // ----------------------------------------------------------- gradient of the decay --
-// One CTA a (segment, head): the anchors <S, D> at the segment's two edges, then the suffix sums
-// of q.dq - k.dk over its tokens, 256 at a time from the end.  Bound by reading the edge states
+// One CTA a (segment, head): the anchors <S, D> at the segment's two edges, then the prefix sums
+// of q.dq - k.dk over its tokens, 256 at a time.  Bound by reading the edge states
 // (each anchor's twice, by the segments on both sides): 72 us at 65,536 tokens x 16 heads x 128,
 // 268 MB at 3.7 TB/s.
 struct DecayGrad {
@@ -399,7 +427,7 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
     block_sum(head, tail);
     auto term = [&](int64_t t, float& x, float& size) {
         x = size = 0.f;
-        if (t < sg.begin) return;
+        if (t >= sg.end) return;
         float a = 0.f, b = 0.f;
         for (int i = 0; i < d.nq; ++i) a += d.dots_q[((int64_t)i * p.H + h) * p.T + t];
         for (int i = 0; i < d.nk; ++i) b += d.dots_k[((int64_t)i * p.H + h) * p.T + t];
@@ -407,22 +435,22 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
         size = fabsf(a) + fabsf(b);
     };
     float sum = 0.f, weight = 0.f;
-    for (int64_t t0 = sg.end - 1; t0 >= sg.begin; t0 -= 256) {
+    for (int64_t t0 = sg.begin; t0 < sg.end; t0 += 256) {
         float x, size;
-        term(t0 - threadIdx.x, x, size);
+        term(t0 + threadIdx.x, x, size);
         sum += x;
-        weight += size;
+        weight = fmaf(size, size, weight);
     }
     block_sum(sum, weight);
     const float miss = (tail - head) + sum;
-    const float share = weight > 0.f ? miss / weight : 0.f;
-    float carry = tail;
-    // thread i holds the i-th token from the end, so the suffix sum is a running sum
-    for (int64_t t0 = sg.end - 1; t0 >= sg.begin; t0 -= 256) {
-        const int64_t t = t0 - threadIdx.x;
+    const float share = weight > 0.f && weight < INFINITY ? miss / weight : 0.f;
+    float carry = head;
+    // a token's sum is over those before it
+    for (int64_t t0 = sg.begin; t0 < sg.end; t0 += 256) {
+        const int64_t t = t0 + threadIdx.x;
         float x, size;
         term(t, x, size);
-        x -= share * size;
+        x = fmaf(-share * size, size, x);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const float y = __shfl_up_sync(0xffffffffu, x, off);
@@ -437,8 +465,10 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
             if (w < warp) before += red[0][w];
             all += red[0][w];
         }
-        if (t >= sg.begin) d.dg[t * p.H + h] = carry + (before + x);
-        carry += all;
+        x = __shfl_up_sync(0xffffffffu, x, 1);
+        if (lane == 0) x = 0.f;
+        if (t < sg.end) d.dg[t * p.H + h] = carry - (before + x);
+        carry -= all;
     }
 }
 
@@ -531,25 +561,34 @@ Problem problem(const LinearArgs& a, int L) {
     return p;
 }
 
-template <typename IO, bool kOut>
+template <typename IO, bool kOut, bool kDots>
 cudaError_t launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, float* dec,
                          const char* name, cudaStream_t s) {
     const int blocks = 128 / kCols;
     const dim3 grid((unsigned)slots, p.H, n * blocks);
     bool any[2] = {};
     for (int i = 0; i < n; ++i) any[calls.c[i].da == 128] = true;
+    const auto k64 = token_kernel<64, IO, kOut, kDots>, k128 = token_kernel<128, IO, kOut, kDots>;
     ProfScope prof(name, s);
     cudaError_t e = cudaSuccess;
     if (!kOut) {  // (a call's first launch, one da for both directions)
-        if (any[0]) token_kernel<64, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
-        if (any[1]) token_kernel<128, IO, kOut><<<grid, 128, 0, s>>>(p, calls, dec, blocks);
+        if (any[0]) k64<<<grid, 128, 0, s>>>(p, calls, dec, blocks);
+        if (any[1]) k128<<<grid, 128, 0, s>>>(p, calls, dec, blocks);
         return cudaGetLastError();
     }
-    if (any[0])
-        e = launch_dependent(token_kernel<64, IO, kOut>, grid, 128, 0, s, p, calls, dec, blocks);
+    if (any[0]) e = launch_dependent(k64, grid, 128, 0, s, p, calls, dec, blocks);
     if (any[1] && e == cudaSuccess)
-        e = launch_dependent(token_kernel<128, IO, kOut>, grid, 128, 0, s, p, calls, dec, blocks);
+        e = launch_dependent(k128, grid, 128, 0, s, p, calls, dec, blocks);
     return e;
+}
+
+template <typename IO, bool kOut>
+cudaError_t launch_token(const Problem& p, const Calls& calls, int n, int64_t slots, float* dec,
+                         const char* name, cudaStream_t s) {
+    bool dots = false;
+    for (int i = 0; i < n; ++i) dots = dots || calls.c[i].dot != nullptr;
+    return kOut && dots ? launch_token<IO, kOut, kOut>(p, calls, n, slots, dec, name, s)
+                        : launch_token<IO, kOut, false>(p, calls, n, slots, dec, name, s);
 }
 
 template <bool kOut>

@@ -43,8 +43,8 @@ struct Call {
     float* S_out;        // [N][H][...] state after the sequence (reversed: before it), or nullptr
     void* out;           // [T][H][db]
     const void* dot;     // [T][H][db] rows, or nullptr: dots[b][h][t] = sum over column block b
-    int64_t dot_ld;      //   of out * dot in fp32, before out is rounded
-    float* dots;
+    int64_t dot_ld;      //   of out * dot in fp32, before out is rounded and without the token's
+    float* dots;         //   own term (x_t . y_t) (w_t . dot_t)
 };
 
 constexpr int kMaxCalls = 3;

@@ -67,6 +67,9 @@ __device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
     return done != 0;
 }
 
+__device__ __forceinline__ void st_shared(float* p, float x) {
+    asm volatile("st.shared.f32 [%0], %1;" : : "r"(smem_u32(p)), "f"(x) : "memory");
+}
 // The registers of earlier TMEM loads are ready (tied to the wait, so that no use moves above it).
 __device__ __forceinline__ void landed(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -281,7 +284,8 @@ constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
 constexpr uint32_t kSWd = 98304;             // decayed W: hi, lo
 constexpr uint32_t kSS = kSWd + 65536;       // state: hi, lo
 constexpr uint32_t kSRec = kSS + 65536;      // the record's part for the call's direction
-constexpr uint32_t kSItem = kSRec + 1088;    // this item's facts and the next one's
+constexpr uint32_t kSOwn = kSRec + 1088;     // the diagonal of X Y^T, of two chunks
+constexpr uint32_t kSItem = kSOwn + 1024;    // this item's facts and the next one's
 constexpr uint32_t kSBar = kSItem + 128;
 constexpr uint32_t kOutSmem = kSBar + 256;
 static_assert(kOutSmem <= 232448, "shared-memory limit");
@@ -293,12 +297,13 @@ struct OutBars {
     uint64_t sc, a;          // X Y^T complete; A written (8 arrivals)
     uint64_t s, wd;          // state and its copy written; decayed W written (8 arrivals each)
     uint64_t upd, xs, aw;    // state update, X S, A W complete
-    uint64_t read;           // the chunk's outputs read from TMEM (16 arrivals)
+    uint64_t read;           // the chunk's outputs (dots: and W) read (16 arrivals)
     uint64_t stored;         // ... and read from their stage (16 arrivals)
     uint64_t item[2];        // an item's facts are there
     uint64_t used[2];        // ... and done with (19 arrivals)
     uint64_t idle;           // the last item's state is done with (8 arrivals)
     uint64_t open, taken;    // the item's state loaded; all of it taken over (8 arrivals)
+    uint64_t own[2];         // (dots) the chunk's diagonal of X Y^T written (4 arrivals)
     uint64_t drain;
     uint32_t tmem;
     int abort;
@@ -363,6 +368,7 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
     const uint32_t items = item_count(o);
     int g = 0;
     uint32_t states = 0, i = blockIdx.x;
+    bool dots = false;  // the last chunk's outputs take their own terms from W
     for (uint32_t n = 0;; ++n) {
         const View it = view(sm, n);
         if (which == 0) {
@@ -404,7 +410,9 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
                 ++states;
             }
             if (g > 0 && !wait1(freed, last, err, abort)) return g;
-            if (which == 2 && g > 0 && !wait1(&bar.wd, last, err, abort)) return g;
+            if (which == 2 && g > 0 && !wait1(dots ? &bar.read : &bar.wd, last, err, abort))
+                return g;
+            dots = c.dot != nullptr;
             const Chunk ch = it.chunk(k);
             mbar_expect_tx(full, blocks * 16384);
 #pragma unroll 1
@@ -522,14 +530,15 @@ __device__ __noinline__ void pass_state(const OutParams& o, int call, int n, int
 }
 
 // Outputs of one chunk, 32 columns from `col` of one row a lane: rowf (X S) + A W, and
-// their dot products with another row where wanted.  A warp's 32 rows are its TMEM lanes: stored
+// their dot products with another row where wanted.  A is then without its diagonal, and the
+// token's own term, x . y w, joins the outputs after the dot product.  A warp's 32 rows are its TMEM lanes: stored
 // from there, each access would touch 32 lines and keep the load/store unit busy for 2000 cycles,
 // so a warp passes its 2 KB through the decayed W's buffer (whose product is complete, and which
 // the next chunk's overwrites only then).  A TMA store of the whole tile kept that buffer for
 // 2200 cycles.
 template <bool kDots>
 __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint8_t* sm,
-                                          uint32_t phase, View it, int k, float rowf, int col) {
+                                          uint32_t g, View it, int k, float rowf, int col) {
     const int row = threadIdx.x & 127, lane = threadIdx.x & 31;
     const Call& c = o.calls.c[it.call()];
     const int db = c.db, h = it.h();
@@ -544,11 +553,15 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
         d[0] = __ldg(dr);
         d[1] = __ldg(dr + 1);
     }
+    const uint32_t phase = g & 1;
     if (!wait(&bar.aw, phase, o.p.err, &bar.abort) ||
         !wait(&bar.xs, phase, o.p.err, &bar.abort) ||
-        !wait(&bar.upd, phase, o.p.err, &bar.abort))
+        !wait(&bar.upd, phase, o.p.err, &bar.abort) ||
+        (kDots && !wait(&bar.own[phase], (g >> 1) & 1, o.p.err, &bar.abort)))
         return false;
     tc_fence_after();
+    const float own =
+        kDots ? reinterpret_cast<const float*>(sm + kSOwn)[128 * phase + row] : 0.f;
     const uint32_t from = (static_cast<uint32_t>(row & 96) << 16) + col;
     uint8_t* stage = sm + kSWd + (col >> 6) * 16384;
     const int piece = (col & 32) >> 3;  // of 16 bytes, within the 128 of a row
@@ -572,7 +585,35 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
 #pragma unroll
             for (int x = 0; x < 8; ++x) o1[8 + x] = fmaf(rowf, o2[x], o1[8 + x]);
         }
-        if (b == 1) {  // the accumulators may be written again
+        if (!kDots && b == 1) {  // the accumulators may be written again
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.read);
+        }
+        if (dots) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t u[4] = {d[x].x, d[x].y, d[x].z, d[x].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    acc = fmaf(o1[8 * x + 2 * y], __uint_as_float(u[y] << 16), acc);
+                    acc = fmaf(o1[8 * x + 2 * y + 1], __uint_as_float(u[y] & 0xffff0000u), acc);
+                }
+                if (b == 0) d[x] = __ldg(dr + 2 + x);
+                // the row of W, which stays in its buffer until `read`
+                const uint4 w = *reinterpret_cast<const uint4*>(
+                    sm + kSW + (col >> 6) * 16384 + row * 128 +
+                    ((piece + 2 * b + x) ^ (row & 7)) * 16);
+                const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    float &a0 = o1[8 * x + 2 * y], &a1 = o1[8 * x + 2 * y + 1];
+                    a0 = fmaf(own, __uint_as_float(v[y] << 16), a0);
+                    a1 = fmaf(own, __uint_as_float(v[y] & 0xffff0000u), a1);
+                }
+            }
+        }
+        if (kDots && b == 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.read);
@@ -580,22 +621,10 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
         if (!cols) continue;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const float* w = o1 + 8 * x;
+            const float* v = o1 + 8 * x;
             *reinterpret_cast<uint4*>(stage + row * 128 + ((piece + 2 * b + x) ^ (row & 7)) * 16) =
-                make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
-                           pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
-        }
-        if (dots) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint32_t w[4] = {d[x].x, d[x].y, d[x].z, d[x].w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    acc = fmaf(o1[8 * x + 2 * y], __uint_as_float(w[y] << 16), acc);
-                    acc = fmaf(o1[8 * x + 2 * y + 1], __uint_as_float(w[y] & 0xffff0000u), acc);
-                }
-                if (b == 0) d[x] = __ldg(dr + 2 + x);
-            }
+                make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                           pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
         }
     }
     if (dots) c.dots[((int64_t)(col >> 5) * o.p.H + h) * o.p.T + ch.t0 + row] = acc;
@@ -640,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bar.item[b], 1);
             mbar_init(&bar.used[b], 19);
+            mbar_init(&bar.own[b], 4);
         }
         uint64_t* eight[] = {&bar.a, &bar.s, &bar.wd, &bar.idle, &bar.taken};
         for (uint64_t* b : eight) mbar_init(b, 8);
@@ -779,6 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             for (int k = 0; k < it.chunks(); ++k, ++g) {
                 const int rev = it.rev();
                 const int len = it.chunk(k).len;
+                const bool strict = kDots && o.calls.c[it.call()].dot != nullptr;
                 const float p_hi = hi_next, edge = edge_next;
                 if (k + 1 < it.chunks()) {
                     const float* r = it.record(o, k + 1);
@@ -809,6 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (rev && len - 32 * j < 32)
                         in = len > 32 * j ? (1u << (len - 32 * j)) - 1u : 0u;
                     if (n == 0) in &= rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
+                    if (n == 0 && strict) in &= ~(1u << lane);
                     // The row's decay up to the block times the columns' inside it.  On the
                     // diagonal these are 2^P_r and 2^-P_i (reversed: 2^-P_r, 2^P_i), at most 2^24,
                     // whose errors (2^-23 times the exponents) stay below 2e-6.
@@ -823,6 +855,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                         float v[16];
                         tmem_ld16(at + 32 * j + 16 * hf, v);
                         landed(v);
+                        if (kDots && n == 0) {
+                            // (a store each: picked by index, the values went to local memory)
+                            float* own = reinterpret_cast<float*>(sm + kSOwn) + 128 * (g & 1) + row;
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                if (lane == 16 * hf + c) st_shared(own, v[c]);
+                        }
                         if (!strong) {
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
@@ -858,10 +897,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.a);
+                if (lane == 0) {
+                    if (kDots && wg == 0) mbar_arrive(&bar.own[g & 1]);
+                    mbar_arrive(&bar.a);
+                }
                 // the second half of its 64 output columns (the state warps write the first)
                 const float rowf = __ldg(it.record(o, k) + (it.rev() ? kRTail : kRHead) + row);
-                ok = write_out<kDots>(o, bar, sm, g & 1, it, k, rowf, 64 * wg + 32);
+                ok = write_out<kDots>(o, bar, sm, g, it, k, rowf, 64 * wg + 32);
                 if (!ok) break;
             }
             __syncwarp();
@@ -974,8 +1016,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     }
                     if (lane == 0) mbar_arrive(&bar.idle);
                 }
-                if (k > 0 && !write_out<kDots>(o, bar, sm, (g - 1) & 1, it, k - 1, rowf_prev,
-                                               64 * wg)) {
+                if (k > 0 && !write_out<kDots>(o, bar, sm, g - 1, it, k - 1, rowf_prev, 64 * wg)) {
                     ok = false;
                     break;
                 }
