@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = cb * kCols + 2 * lane, row0 = warp * R;
     const int64_t E = (int64_t)c.da * c.db;
-    const int64_t own = ((int64_t)blockIdx.x * p.H + h) * E;
+    const int64_t own = ((int64_t)sg.edge * p.H + h) * E;
     const int64_t seq = ((int64_t)sg.n * p.H + h) * E;
 
     float2 S[2][R / 2];  // [column][row pair]
@@ -287,11 +287,33 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
     float* to = kOut ? (last && c.S_out ? c.S_out + seq : nullptr)
                      : const_cast<float*>(c.seg) + own;
     if (to) store_state(to);
+    if (kDots && last && c.anchor) {
+        const float* with = c.anchor + seq;
+        float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) {
+            const int row = row0 + 2 * r;
+            if (c.tr) {
+                x = fma2(S[0][r], *reinterpret_cast<const float2*>(with + col * DA + row), x);
+                x = fma2(S[1][r], *reinterpret_cast<const float2*>(with + (col + 1) * DA + row), x);
+            } else {
+                const float2 a = *reinterpret_cast<const float2*>(with + row * c.db + col);
+                const float2 b = *reinterpret_cast<const float2*>(with + (row + 1) * c.db + col);
+                x = fma2(S[0][r], make_float2(a.x, b.x), x);
+                x = fma2(S[1][r], make_float2(a.y, b.y), x);
+            }
+        }
+        float y = x.x + x.y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
+        if (lane == 0)
+            c.anchors[((int64_t)sg.n * p.H + h) * lin::kAnchors + 4 * cb + warp] = y;
+    }
     if (!kOut && cb == 0 && warp == 0) {
 #pragma unroll
         for (int off = 8; off > 0; off >>= 1) gsum += __shfl_xor_sync(0xffffffffu, gsum, off);
         if (lane == 0)
-            dec[((int64_t)c.reverse * gridDim.x + blockIdx.x) * p.H + h] =
+            dec[((int64_t)c.reverse * p.edges + sg.edge) * p.H + h] =
                 gsum * 1.4426950408889634f;
     }
 }
@@ -302,10 +324,10 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
 // and by its latency where segments are few: 20 us at 65,536 tokens x 32 heads x 128 (33 segments
 // of 2,048: 134 MB), 42 us for both directions of the gradients x 16 heads (65 of 1,024: 268 MB).
 struct Edges {
-    const float* add[2];    // [slots][H][E] contributions: forward, reversed
-    float* seg[2];          // [slots][H][E] edge states (written)
+    const float* add[2];    // [edges][H][E] contributions: forward, reversed
+    float* seg[2];          // [edges][H][E] edge states (written)
     const float* edge[2];   // [N][H][E] or nullptr
-    const float* dec[2];    // [slots][H] summed log2 decays
+    const float* dec[2];    // [edges][H] summed log2 decays
     int E;
 };
 
@@ -326,7 +348,7 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
         int64_t a, b;
         seq_range(p.cu, n, p.N, p.T, p.err, a, b);
         const int count = (int)((b - a + p.L - 1) / p.L);
-        const int64_t base = a / p.L + n;
+        const int64_t base = lin::edge_base(p, (uint32_t)a, n);
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (e.edge[dir])
             acc = reinterpret_cast<const float4*>(e.edge[dir])[(int64_t)n * stride + own];
@@ -375,12 +397,12 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
 // (each anchor's twice, by the segments on both sides): 72 us at 65,536 tokens x 16 heads x 128,
 // 268 MB at 3.7 TB/s.
 struct DecayGrad {
-    const float *segS, *segD;   // [slots][H][E] edge states (where sequences have segments)
-    const float *S0, *dS0;      // [N][H][E] at the sequences' starts; S0 may be nullptr (zeros)
-    const float *S_T, *dS_out;  // at their ends; dS_out may be nullptr (zeros)
-    const float *dots_q, *dots_k;  // [nq][H][T], [nk][H][T]
+    const float *segS, *segD;        // [edges][H][E] edge states (where sequences have segments)
+    const float *at_start, *at_end;  // [N][H][kAnchors] partial sums of <S, D> at the sequences'
+    int n_start, n_end;              //   edges, and how many; nullptr where that is zero
+    const float *dots_q, *dots_k;    // [nq][H][T], [nk][H][T]
     int nq, nk;
-    float* dg;                  // [T][H]
+    float* dg;                       // [T][H]
     int E;
 };
 
@@ -392,17 +414,20 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
     const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Segment sg = lin::find_segment(p, (int)blockIdx.x);
     if (!sg.live) return;
-    const int64_t seq = ((int64_t)sg.n * p.H + h) * d.E;
-    const int64_t own = ((int64_t)blockIdx.x * p.H + h) * d.E, step = (int64_t)p.H * d.E;
+    const int64_t seq = ((int64_t)sg.n * p.H + h) * lin::kAnchors;
+    const int64_t own = ((int64_t)sg.edge * p.H + h) * d.E, step = (int64_t)p.H * d.E;
     auto dot = [&](const float* A, const float* B) {
         float x = 0.f;
-        if (A && B)
-            for (int i = threadIdx.x; i < d.E / 4; i += 256) {
-                const float4 u = reinterpret_cast<const float4*>(A)[i];
-                const float4 v = reinterpret_cast<const float4*>(B)[i];
-                x = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, x))));
-            }
+#pragma unroll 8
+        for (int i = threadIdx.x; i < d.E / 4; i += 256) {
+            const float4 u = reinterpret_cast<const float4*>(A)[i];
+            const float4 v = reinterpret_cast<const float4*>(B)[i];
+            x = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, x))));
+        }
         return x;
+    };
+    auto part = [&](const float* parts, int n) {
+        return parts && (int)threadIdx.x < n ? parts[seq + threadIdx.x] : 0.f;
     };
     // sums of x and of y over the block, the same in every thread
     auto block_sum = [&](float& x, float& y) {
@@ -420,10 +445,8 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
     };
     // segment s's slot holds S at its start and D at its end
     const bool first = sg.s == 0, last = sg.s == sg.count - 1;
-    float head = first ? dot(d.S0 ? d.S0 + seq : nullptr, d.dS0 + seq)
-                       : dot(d.segS + own, d.segD + own - step);
-    float tail = last ? dot(d.S_T + seq, d.dS_out ? d.dS_out + seq : nullptr)
-                      : dot(d.segS + own + step, d.segD + own);
+    float head = first ? part(d.at_start, d.n_start) : dot(d.segS + own, d.segD + own - step);
+    float tail = last ? part(d.at_end, d.n_end) : dot(d.segS + own + step, d.segD + own);
     block_sum(head, tail);
     auto term = [&](int64_t t, float& x, float& size) {
         x = size = 0.f;
@@ -519,15 +542,16 @@ int segment_length(int64_t T, int H, bool tc, bool bwd) {
 
 struct Layout {
     int L;
-    int64_t slots;
+    int64_t slots, edges;
     bool segments;  // some sequence may be longer than a segment
-    size_t rec, next, add[2], seg[2], dec, S_T, dS0, dots_q, dots_k, dg, bytes;
+    size_t rec, next, add[2], seg[2], dec, at_start, at_end, dots_q, dots_k, dg, bytes;
 };
 
 Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool equal) {
     Layout l{};
     l.L = segment_length(T, H, tc, bwd);
     l.slots = lin::slot_count(T, N, l.L);
+    l.edges = std::min(l.slots, 2 * T / l.L);
     l.segments = (equal && N > 0 ? T / N : T) > l.L;
     const size_t state = (size_t)H * dk * dv * sizeof(float);
     size_t at = 0;
@@ -536,16 +560,16 @@ Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool e
         at += align256(n);
         return r;
     };
-    l.rec = take(tc ? lintc::record_bytes(l.slots, l.L, H) : 0);
+    l.rec = take(tc ? lintc::record_bytes(T, N, H) : 0);
     l.next = take(tc ? lintc::kCounters * sizeof(unsigned) : 0);
     for (int i = 0; i < (bwd ? 2 : 1); ++i) {
-        l.add[i] = take(l.segments ? (size_t)l.slots * state : 0);
-        l.seg[i] = take(l.segments ? (size_t)l.slots * state : 0);
+        l.add[i] = take(l.segments ? (size_t)l.edges * state : 0);
+        l.seg[i] = take(l.segments ? (size_t)l.edges * state : 0);
     }
-    l.dec = take(l.segments ? (size_t)2 * l.slots * H * sizeof(float) : 0);
+    l.dec = take(l.segments ? (size_t)2 * l.edges * H * sizeof(float) : 0);
     if (bwd) {
-        l.S_T = take((size_t)N * state);
-        l.dS0 = take((size_t)N * state);
+        l.at_start = take((size_t)N * H * lin::kAnchors * sizeof(float));
+        l.at_end = take((size_t)N * H * lin::kAnchors * sizeof(float));
         l.dots_q = take((size_t)(dk / kDotCols) * T * H * sizeof(float));
         l.dots_k = take((size_t)(dk / kDotCols) * T * H * sizeof(float));
         l.dg = take((size_t)T * H * sizeof(float));
@@ -554,10 +578,11 @@ Layout layout(int64_t T, int N, int H, int dk, int dv, bool bwd, bool tc, bool e
     return l;
 }
 
-Problem problem(const LinearArgs& a, int L) {
+Problem problem(const LinearArgs& a, const Layout& l) {
     Problem p{};
     p.cu = a.cu_seqlens; p.N = a.N; p.T = a.T_total; p.H = a.H; p.g = a.g;
-    p.g_per_token = a.g_per_token; p.L = L; p.err = a.dev_err;
+    p.g_per_token = a.g_per_token; p.L = l.L; p.edges = (int)l.edges;
+    p.edges_close = l.edges < l.slots; p.err = a.dev_err;
     return p;
 }
 
@@ -620,7 +645,7 @@ cudaError_t launch_segments(const LinearArgs& a, const Problem& p, const Layout&
         e.add[i] = c.seg;
         e.seg[i] = reinterpret_cast<float*>(ws + l.seg[i]);
         e.edge[i] = i ? a.dS_out : a.S0;
-        e.dec[i] = dec + (size_t)i * l.slots * a.H;
+        e.dec[i] = dec + (size_t)i * l.edges * a.H;
     }
     e.E = a.dk * a.dv;
     if (cudaError_t err = launch_calls<false>(a, p, calls, bwd ? 2 : 1, l, dec,
@@ -644,7 +669,7 @@ size_t linear_bwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int io
 cudaError_t launch_linear_fwd(const LinearArgs& a) {
     const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, false, use_tc(a.io_bf16),
                             a.cu_seqlens == nullptr);
-    const Problem p = problem(a, l.L);
+    const Problem p = problem(a, l);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     if (use_tc(a.io_bf16))
         if (cudaError_t e = lintc::launch_decays(
@@ -663,7 +688,7 @@ cudaError_t launch_linear_fwd(const LinearArgs& a) {
 cudaError_t launch_linear_bwd(const LinearArgs& a) {
     const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, true, use_tc(a.io_bf16),
                             a.cu_seqlens == nullptr);
-    const Problem p = problem(a, l.L);
+    const Problem p = problem(a, l);
     uint8_t* ws = static_cast<uint8_t*>(a.workspace);
     auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
     if (use_tc(a.io_bf16))
@@ -672,28 +697,34 @@ cudaError_t launch_linear_bwd(const LinearArgs& a) {
             return e;
     if (l.segments)
         if (cudaError_t e = launch_segments(a, p, l, true)) return e;
-    const bool anchor = a.dg && a.dS_out;
     float* const seg[2] = {l.segments ? at(l.seg[0]) : nullptr, l.segments ? at(l.seg[1]) : nullptr};
     Calls calls{};
     Call &q = calls.c[0], &k = calls.c[1], &v = calls.c[2];
     q.x = a.dout; q.x_ld = a.dout_ld; q.y = a.v; q.y_ld = a.v_ld; q.w = a.k; q.w_ld = a.k_ld;
     q.da = a.dv; q.db = a.dk; q.tr = 1; q.edge = a.S0; q.seg = seg[0];
-    q.S_out = anchor ? at(l.S_T) : nullptr; q.out = a.dq;
-    if (a.dg) { q.dot = a.q; q.dot_ld = a.q_ld; q.dots = at(l.dots_q); }
+    q.out = a.dq;
+    if (a.dg) {
+        q.dot = a.q; q.dot_ld = a.q_ld; q.dots = at(l.dots_q);
+        q.anchor = a.dS_out; q.anchors = at(l.at_end);
+    }
     k.x = a.v; k.x_ld = a.v_ld; k.y = a.dout; k.y_ld = a.dout_ld; k.w = a.q; k.w_ld = a.q_ld;
     k.da = a.dv; k.db = a.dk; k.reverse = 1; k.tr = 1; k.edge = a.dS_out; k.seg = seg[1];
     k.out = a.dk_;
     if (a.dg) { k.dot = a.k; k.dot_ld = a.k_ld; k.dots = at(l.dots_k); }
     v.x = a.k; v.x_ld = a.k_ld; v.y = a.q; v.y_ld = a.q_ld; v.w = a.dout; v.w_ld = a.dout_ld;
     v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = seg[1];
-    v.S_out = a.dS0 ? a.dS0 : a.dg && a.S0 ? at(l.dS0) : nullptr; v.out = a.dv_;
+    v.S_out = a.dS0; v.out = a.dv_;
+    if (a.dg) { v.anchor = a.S0; v.anchors = at(l.at_start); }
     if (cudaError_t e =
             launch_calls<true>(a, p, calls, 3, l, nullptr, "linear_grad_kernel"))
         return e;
     if (a.dg) {
         DecayGrad d{};
         d.segS = seg[0]; d.segD = seg[1];
-        d.S_T = at(l.S_T); d.dS_out = a.dS_out; d.S0 = a.S0; d.dS0 = v.S_out;
+        // (the tensor cores' kernel leaves kAnchors parts, the other four a 64 columns)
+        const bool tc = use_tc(a.io_bf16);
+        d.at_start = a.S0 ? v.anchors : nullptr; d.n_start = tc ? lin::kAnchors : a.dv / kCols * 4;
+        d.at_end = a.dS_out ? q.anchors : nullptr; d.n_end = tc ? lin::kAnchors : a.dk / kCols * 4;
         d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kDotCols;
         d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
         if (a.T_total > 0) {

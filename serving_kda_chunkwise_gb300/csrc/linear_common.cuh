@@ -13,6 +13,9 @@
 // s of sequence n, with base(n) = floor(cu[n] / L) + n: consecutive bases are at least
 // ceil(len / L) apart, so a slot finds its sequence from cu_seqlens alone and no launch has to
 // lay out a table.  Slots past a sequence's last segment are empty.
+// Only sequences of more than one segment have states at segments' edges.  Where sequences are
+// many these lie more closely: from floor(2 cu[n] / L) on, for ceil(len / L) <= floor(2 len / L) where
+// len > L, so that 2 T / L slots hold them however many sequences there are.
 #pragma once
 
 #include "kda_common.cuh"
@@ -29,6 +32,8 @@ struct Problem {
     const float* g;
     int g_per_token;
     int L;
+    int edges;       // slots of edge states
+    int edges_close; // nonzero: they begin at floor(2 cu[n] / L), else at the segments' slots
     unsigned* err;
 };
 
@@ -39,25 +44,33 @@ struct Call {
     int reverse;
     int tr;              // states in memory are [db][da] instead of [da][db]
     const float* edge;   // [N][H][...] state before the first (reversed: after the last) token
-    const float* seg;    // [slots][H][...] state at the other segments' edges, or nullptr
+    const float* seg;    // [edges][H][...] state at the other segments' edges, or nullptr
     float* S_out;        // [N][H][...] state after the sequence (reversed: before it), or nullptr
+    const float* anchor; // [N][H][...] states whose dot products with those after the sequences
+    float* anchors;      //   are wanted, or nullptr: [N][H][kAnchors] partial sums
     void* out;           // [T][H][db]
     const void* dot;     // [T][H][db] rows, or nullptr: dots[b][h][t] = sum over column block b
     int64_t dot_ld;      //   of out * dot in fp32, before out is rounded and without the token's
     float* dots;         //   own term (x_t . y_t) (w_t . dot_t)
 };
 
-constexpr int kMaxCalls = 3;
+constexpr int kMaxCalls = 3, kAnchors = 8;
 struct Calls {
     Call c[kMaxCalls];
 };
 
 __host__ __device__ inline int64_t slot_count(int64_t T, int N, int L) { return T / L + N; }
 
+// the slot of the edge state of the first segment of sequence n, whose first token is a
+__device__ __forceinline__ int edge_base(const Problem& p, uint32_t a, int n) {
+    return p.edges_close ? (int)(2 * a / (uint32_t)p.L) : (int)(a / (uint32_t)p.L) + n;
+}
+
 struct Segment {
     int n;                // sequence
     int s, count;         // segment of the sequence, and how many it has
     int begin, end;       // its tokens (there are fewer than 2^31)
+    int edge;             // (where count > 1) the slot of its edge state
     bool live;
 };
 
@@ -99,6 +112,7 @@ __device__ __forceinline__ Segment find_segment(const Problem& p, int j) {
     r.live = r.s >= 0 && r.s < r.count;
     r.begin = (int)(a + (uint32_t)r.s * L);
     r.end = (int)min((uint32_t)r.begin + L, b);
+    r.edge = edge_base(p, a, lo) + r.s;
     return r;
 }
 

@@ -180,7 +180,7 @@ struct Chunk {
 
 // ---------------------------------------------------------------- decays --
 // What a chunk's decays are needed as, formed once for all calls and roles: a record of floats a
-// (chunk, head), arrays of 128 tokens.
+// (chunk, head), arrays of 128 tokens.  The records lie by slots of one chunk.
 constexpr int kRP = 0, kRPlo = 128;   // prefix sum inside the block of 32 (log2), its rounding
 constexpr int kRU = 256;              // exclusive suffix sum inside the block
 constexpr int kRHead = 384;           // 2^(sum from the chunk's start, inclusive)
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
                                                     unsigned* next) {
     grid_dependents_launch();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < kCounters) next[threadIdx.x] = 0u;
-    const int lane = threadIdx.x & 31, per = p.L / kC;
+    const int lane = threadIdx.x & 31;
     const int h = blockIdx.y * 8 + (threadIdx.x >> 5);
     // blocks are slots of one chunk, for most of a segment's chunks may lie past a short sequence
     Problem chunks = p;
@@ -205,8 +205,7 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
     const Segment sg = lin::find_segment(chunks, (int)blockIdx.x);
     if (h >= p.H || !sg.live) return;
     const int t0 = sg.begin;
-    const int slot = (t0 - sg.s * kC) / p.L + sg.n + sg.s / per;
-    float* r = rec + ((size_t)(slot * per + sg.s % per) * p.H + h) * kRec;
+    float* r = rec + ((size_t)blockIdx.x * p.H + h) * kRec;
     float e[4], P[4], Plo[4], U[4], B[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
@@ -345,7 +344,7 @@ __device__ __forceinline__ void put_item(const OutParams& o, const Item& t, View
     w.v[View::kCall] = t.call;
     w.v[View::kH] = t.h;
     w.v[View::kRev] = rev;
-    w.v[View::kRecord] = t.slot * (o.p.L / kC);
+    w.v[View::kRecord] = (t.sg.begin - t.sg.s * o.p.L) / kC + t.sg.n + t.sg.s * (o.p.L / kC);
     w.v[View::kZero] = t.sg.count <= 1 && o.calls.c[t.call].edge == nullptr;
     // (an empty sequence's first slot passes the state on: kChunks = 0, kFinal >= 0)
     const bool last = t.sg.live ? (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1)
@@ -353,7 +352,7 @@ __device__ __forceinline__ void put_item(const OutParams& o, const Item& t, View
     w.v[View::kFinal] = last ? t.sg.n : -1;  // whose final state follows, if any
     // the state that it starts from: a segment's edge state or the sequence's own
     w.v[View::kSeg] = t.sg.count > 1;
-    w.v[View::kState] = (t.sg.count > 1 ? t.slot : t.sg.n) * o.p.H + t.h;
+    w.v[View::kState] = (t.sg.count > 1 ? t.sg.edge : t.sg.n) * o.p.H + t.h;
 }
 
 // One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each once
@@ -459,12 +458,14 @@ __device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 256 + ((
 
 // The item's state from the buffer that the copy is to have, where 32-float boxes of its rows in
 // memory lie (128 bytes a row, 16-byte pieces permuted by the row), into TMEM.
-__device__ __noinline__ void load_state(const OutParams& o, int call, bool zero, int col,
-                                        const uint8_t* buf) {
-    const Call& c = o.calls.c[call];
+__device__ __noinline__ void load_state(const OutParams& o, uint8_t* sm, uint32_t n) {
+    const View it = view(sm, n);
+    const Call& c = o.calls.c[it.call()];
+    const uint8_t* buf = sm + kSS;
+    const int col = threadIdx.x >= 384 ? 64 : 0;
     const int lane = threadIdx.x & 31, row = threadIdx.x & 127;
     const uint32_t to = (static_cast<uint32_t>(row & 96) << 16) + kTS + col;
-    zero = zero || col >= c.db || (row & 96) >= c.da;
+    const bool zero = it.v[View::kZero] || col >= c.db || (row & 96) >= c.da;
 #pragma unroll 1
     for (int b = 0; b < 4; ++b) {
         uint32_t u[16];
@@ -488,41 +489,78 @@ __device__ __noinline__ void load_state(const OutParams& o, int call, bool zero,
     tmem_st_wait();
     __syncwarp();
 }
-__device__ __noinline__ void store_state(const OutParams& o, int call, int n, int h, int col,
-                                         uint8_t* stage) {
-    const Call& c = o.calls.c[call];
+// What follows from the n-th item's final state: the state in memory and, for kDots, the warp's part
+// of its dot product with another.
+template <bool kDots>
+__device__ __noinline__ void final_state(const OutParams& o, uint8_t* sm, uint32_t n) {
+    const View it = view(sm, n);
+    const Call& c = o.calls.c[it.call()];
+    const int h = it.h(), seq = it.v[View::kFinal];
     const int lane = threadIdx.x & 31, row0 = threadIdx.x & 96;
-    const bool rows = col < c.db && row0 < c.da;
-    if (c.S_out == nullptr || !rows) return;
-    const StateAt s = state_at(o, c, n, h, col);
-    const uint32_t from = (static_cast<uint32_t>(row0) << 16) + kTS + col;
+    const int col = threadIdx.x >= 384 ? 64 : 0;
+    uint8_t* stage = sm + kSS + ((threadIdx.x >> 5) - 8) * 8192;
+    const float* anchor = kDots ? c.anchor : nullptr;
+    const StateAt s = state_at(o, c, seq, h, col);
+    float dot = 0.f;
+    if (col < c.db && row0 < c.da && (c.S_out || anchor)) {
+        const uint32_t from = (static_cast<uint32_t>(row0) << 16) + kTS + col;
 #pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-        float v[16];
-        tmem_ld16(from + 16 * b, v);
-        landed(v);
-        if (c.tr) {
+        for (int b = 0; b < 4; ++b) {
+            float v[16], w[16];
+            if (c.tr && anchor)
 #pragma unroll
-            for (int x = 0; x < 16; ++x) c.S_out[s.at + (16 * b + x) * s.cs] = v[x];
-        } else {
+                for (int x = 0; x < 16; ++x) w[x] = __ldg(anchor + s.at + (16 * b + x) * s.cs);
+            tmem_ld16(from + 16 * b, v);
+            landed(v);
+            if (!c.tr) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                *reinterpret_cast<float4*>(stage + piece_at(lane, 4 * b + x)) =
-                    make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                for (int x = 0; x < 4; ++x)
+                    *reinterpret_cast<float4*>(stage + piece_at(lane, 4 * b + x)) =
+                        make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                continue;
+            }
+            if (c.S_out)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) c.S_out[s.at + (16 * b + x) * s.cs] = v[x];
+            if (anchor)
+#pragma unroll
+                for (int x = 0; x < 16; ++x) dot = fmaf(v[x], w[x], dot);
+        }
+        if (!c.tr) {
+            __syncwarp();
+            const int64_t at = s.at - (int64_t)lane * c.db + (int64_t)(lane >> 4) * c.db +
+                               4 * (lane & 15);
+            auto piece = [&](int x) {
+                return *reinterpret_cast<const float4*>(
+                    stage + piece_at(2 * x + (lane >> 4), lane & 15));
+            };
+            if (c.S_out)
+#pragma unroll 4
+                for (int x = 0; x < 16; ++x)
+                    *reinterpret_cast<float4*>(c.S_out + at + (int64_t)2 * x * c.db) = piece(x);
+            if (anchor)
+#pragma unroll 8
+                for (int x = 0; x < 16; ++x) {
+                    const float4 w = __ldg(
+                        reinterpret_cast<const float4*>(anchor + at + (int64_t)2 * x * c.db));
+                    const float4 v = piece(x);
+                    dot = fmaf(v.x, w.x, fmaf(v.y, w.y, fmaf(v.z, w.z, fmaf(v.w, w.w, dot))));
+                }
+            __syncwarp();
         }
     }
-    if (c.tr) return;
-    __syncwarp();
-    float* f = c.S_out + s.at - (int64_t)lane * c.db;
-#pragma unroll 4
-    for (int x = 0; x < 16; ++x)
-        reinterpret_cast<float4*>(f + (int64_t)(2 * x + (lane >> 4)) * c.db)[lane & 15] =
-            *reinterpret_cast<const float4*>(stage + piece_at(2 * x + (lane >> 4), lane & 15));
-    __syncwarp();
+    if (anchor) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+        if (lane == 0)
+            c.anchors[((int64_t)seq * o.p.H + h) * lin::kAnchors + 2 * (row0 >> 5) + (col >> 6)] =
+                dot;
+    }
 }
-__device__ __noinline__ void pass_state(const OutParams& o, int call, int n, int h, int col) {
-    const Call& c = o.calls.c[call];
-    const StateAt s = state_at(o, c, n, h, col);
+__device__ __noinline__ void pass_state(const OutParams& o, uint8_t* sm, uint32_t n) {
+    const View it = view(sm, n);
+    const Call& c = o.calls.c[it.call()];
+    const StateAt s = state_at(o, c, it.v[View::kFinal], it.h(), threadIdx.x >= 384 ? 64 : 0);
     if (c.S_out && s.holds)
 #pragma unroll 1
         for (int x = 0; x < 64; ++x)
@@ -923,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             const bool final = it.v[View::kFinal] >= 0;
             if (it.chunks() == 0) {
                 // an empty sequence owns its first slot: its final state is its initial one
-                if (final) pass_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg);
+                if (final) pass_state(o, sm, n);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.used[n & 1]);
                 continue;
@@ -939,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             }
             if (!wait(&bar.open, opened & 1, p.err, abort)) { ok = false; break; }
             tc_fence_after();
-            load_state(o, it.call(), it.v[View::kZero], 64 * wg, sm + kSS);
+            load_state(o, sm, n);
             // no warp writes the copy while another still reads the buffer
             if (lane == 0) mbar_arrive(&bar.taken);
             if (!wait(&bar.taken, opened & 1, p.err, abort)) { ok = false; break; }
@@ -1008,8 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (final) {
                         if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
                         tc_fence_after();
-                        store_state(o, it.call(), it.v[View::kFinal], it.h(), 64 * wg,
-                                    sm + kSS + (warp - 8) * 8192);
+                        final_state<kDots>(o, sm, n);
                         tc_fence_before();
                         fence_async_smem();
                         __syncwarp();
@@ -1366,7 +1403,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             if (!wait(&bar.stored, stored & 1, p.err, abort)) { ok = false; break; }
             ++stored;
             if (warp == 4 && lane == 0)
-                dec[(int64_t)rev * o.slots * p.H + it.v[View::kState]] = between;
+                dec[(int64_t)rev * p.edges * p.H + it.v[View::kState]] = between;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.used[n & 1]);
         }
@@ -1458,7 +1495,7 @@ cudaError_t fill(OutParams& o, const Problem& p, const lin::Calls& calls, int n,
             !make_map(&o.w[i], c.w, p.T, p.H, c.db, c.w_ld))
             return cudaErrorInvalidValue;
         const int rows = c.tr ? c.db : c.da, inner = c.tr ? c.da : c.db;
-        if (out && ((c.seg && !make_state_map(&o.seg[i], c.seg, slots * p.H, rows, inner)) ||
+        if (out && ((c.seg && !make_state_map(&o.seg[i], c.seg, (int64_t)p.edges * p.H, rows, inner)) ||
                     (c.edge && !make_state_map(&o.edge[i], c.edge, (int64_t)p.N * p.H, rows,
                                                inner))))
             return cudaErrorInvalidValue;
@@ -1468,8 +1505,8 @@ cudaError_t fill(OutParams& o, const Problem& p, const lin::Calls& calls, int n,
 
 }  // namespace
 
-size_t record_bytes(int64_t slots, int L, int H) {
-    return (size_t)slots * (L / kC) * H * kRec * sizeof(float);
+size_t record_bytes(int64_t T, int N, int H) {
+    return (size_t)lin::slot_count(T, N, kC) * H * kRec * sizeof(float);
 }
 
 cudaError_t launch_decays(const Problem& p, float* rec, unsigned* next, cudaStream_t s) {

@@ -11,7 +11,7 @@ namespace lintc {
 // What the kernels below need of the decays, once for all calls (`rec` holds record_bytes()), and
 // the counters of taken items, zeroed.
 constexpr int kCounters = 2;
-size_t record_bytes(int64_t slots, int L, int H);
+size_t record_bytes(int64_t T, int N, int H);
 cudaError_t launch_decays(const lin::Problem& p, float* rec, unsigned* next, cudaStream_t s);
 
 // Every segment's outputs (and final states) from its edge state; `next`: a zeroed counter.
