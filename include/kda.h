@@ -256,6 +256,7 @@ kda_status_t kda_linear_fwd_chunked(const void *q, int64_t q_ld, const void *k, 
  *   dq = S_t do_t, dk = D_t v_t : [T_total, H, dk] io_dt      dv = D_t^T k_t : [T_total, H, dv]
  *   dg  : fp32, [T_total, H] when g_per_token, else [H] (summed over all tokens), or NULL
  *   dS0 : [N, H, dk, dv] fp32, or NULL when not wanted
+ * N = 0 (no sequences) is a batch like any other.
  * Deterministic.  Gradients with respect to g = -inf are computed as for any other g.  Inputs
  * that are not finite spoil their own sequence only (and dg [H], which sums over all).
  */

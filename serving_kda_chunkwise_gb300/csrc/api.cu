@@ -510,7 +510,13 @@ kda_status_t kda_linear_bwd(const void* q, int64_t q_ld, const void* k, int64_t 
     KDA_REQUIRE(dout_ld >= (int64_t)H * dv && dout_ld % per16 == 0,
                 "dout_ld=%lld must be a multiple of %d and at least H dv", (long long)dout_ld,
                 per16);
-    KDA_REQUIRE(N > 0, "N=%d must be positive", N);
+    if (dg) KDA_REQUIRE_WORDS(dg, "dg");
+    if (N == 0) {  // (a decay that all tokens share has a gradient all the same)
+        if (dg == nullptr || g_per_token) return KDA_OK;
+        cudaError_t e =
+            cudaMemsetAsync(dg, 0, H * sizeof(float), reinterpret_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, "kda_linear_bwd");
+    }
     if (T_total > 0) {
         KDA_REQUIRE_PTR(q, "q");
         KDA_REQUIRE_PTR(k, "k");
@@ -523,7 +529,6 @@ kda_status_t kda_linear_bwd(const void* q, int64_t q_ld, const void* k, int64_t 
     }
     KDA_OPTIONAL_PTR(S0, "S0");
     KDA_OPTIONAL_PTR(dS_out, "dS_out");
-    if (dg) KDA_REQUIRE_WORDS(dg, "dg");
     KDA_OPTIONAL_PTR(dS0, "dS0");
     const size_t need = kda_linear_bwd_workspace_size(T_total, N, H, dk, dv, io_dt);
     if (need > 0) {
