@@ -457,41 +457,51 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
         x = a - b;
         size = fabsf(a) + fabsf(b);
     };
-    float sum = 0.f, weight = 0.f;
-    for (int64_t t0 = sg.begin; t0 < sg.end; t0 += 256) {
-        float x, size;
-        term(t0 + threadIdx.x, x, size);
-        sum += x;
-        weight = fmaf(size, size, weight);
-    }
-    block_sum(sum, weight);
-    const float miss = (tail - head) + sum;
-    const float share = weight > 0.f && weight < INFINITY ? miss / weight : 0.f;
-    float carry = head;
-    // a token's sum is over those before it
-    for (int64_t t0 = sg.begin; t0 < sg.end; t0 += 256) {
-        const int64_t t = t0 + threadIdx.x;
-        float x, size;
-        term(t, x, size);
-        x = fmaf(-share * size, size, x);
+    // the sum over the block's threads before this one, and over all
+    auto scan = [&](float x, float (&warps)[8], float& before, float& all) {
+        float y = x;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, x, off);
-            if (lane >= off) x += y;
+            const float z = __shfl_up_sync(0xffffffffu, y, off);
+            if (lane >= off) y += z;
         }
+        if (lane == 31) warps[warp] = y;
         __syncthreads();
-        if (lane == 31) red[0][warp] = x;
-        __syncthreads();
-        float before = 0.f, all = 0.f;
+        before = all = 0.f;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-            if (w < warp) before += red[0][w];
-            all += red[0][w];
+            if (w < warp) before += warps[w];
+            all += warps[w];
         }
-        x = __shfl_up_sync(0xffffffffu, x, 1);
-        if (lane == 0) x = 0.f;
-        if (t < sg.end) d.dg[t * p.H + h] = carry - (before + x);
-        carry -= all;
+        y = __shfl_up_sync(0xffffffffu, y, 1);
+        if (lane > 0) before += y;
+    };
+    // The miss is that of the sums as they will be taken: added up in another order, they would end
+    // elsewhere by their rounding.
+    float sum = 0.f, weight = 0.f;
+    for (int64_t t0 = sg.begin; t0 < sg.end; t0 += 256) {
+        float x, size, before, all;
+        term(t0 + threadIdx.x, x, size);
+        __syncthreads();
+        scan(x, red[0], before, all);
+        sum += all;
+        weight = fmaf(size, size, weight);
+    }
+    float none = 0.f;
+    block_sum(weight, none);
+    const float miss = (tail - head) + sum;
+    const float share = weight > 0.f && weight < INFINITY ? miss / weight : 0.f;
+    sum = weight = 0.f;
+    for (int64_t t0 = sg.begin; t0 < sg.end; t0 += 256) {
+        const int64_t t = t0 + threadIdx.x;
+        float x, size, before, all, back, backs;
+        term(t, x, size);
+        __syncthreads();
+        scan(x, red[0], before, all);
+        scan(size * size, red[1], back, backs);
+        if (t < sg.end) d.dg[t * p.H + h] = head - ((sum + before) - share * (weight + back));
+        sum += all;
+        weight += backs;
     }
 }
 

@@ -250,8 +250,11 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
         r[kRHead + i] = ex2f(P[b] + before[b]);
         r[kRTail + i] = ex2f(U[b] + after[b]);
         r[kRCol + i] = ex2f(U[b]);
-        r[kRCol + 128 + i] = ex2f(-P[b]);
-        r[kRCol + kRDir + i] = r[kRCol + kRDir + 128 + i] = ex2f(P[b]);
+        // (2^-lo and 2^lo: a factor of the diagonal block is up to 2^24 and its product with a row's
+        // about 1, so that the rounding of P would be seen)
+        const float lo = 0.6931471805599453f * Plo[b];
+        r[kRCol + 128 + i] = ex2f(-P[b]) * (1.f - lo);
+        r[kRCol + kRDir + i] = r[kRCol + kRDir + 128 + i] = ex2f(P[b]) * (1.f + lo);
     }
     if (lane < 2) {
         float* s = r + kRCol + lane * kRDir + kRB;
@@ -835,12 +838,13 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
             const View it = view(sm, n);
             if (it.chunks() < 0) break;
-            // the row's prefix sum inside its block and its sum to the edge of the block that it
-            // looks to, loaded a chunk ahead (from memory they take 2500 cycles)
-            float hi_next = 0.f, edge_next = 0.f;
+            // the row's factor in the diagonal block, which is a column's of the other direction, and
+            // its sum to the edge of the block that it looks to, loaded a chunk ahead (from memory
+            // they take 2500 cycles)
+            float diag_next = 0.f, edge_next = 0.f;
             if (it.chunks()) {
                 const float* r = it.record(o, 0);
-                hi_next = __ldg(r + kRP + row);
+                diag_next = __ldg(r + kRCol + (it.rev() ? 0 : kRDir) + 128 + row);
                 edge_next = __ldg(r + (it.rev() ? kRU : kRP) + row);
             }
 #pragma unroll 1
@@ -848,10 +852,10 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 const int rev = it.rev();
                 const int len = it.chunk(k).len;
                 const bool strict = kDots && o.calls.c[it.call()].dot != nullptr;
-                const float p_hi = hi_next, edge = edge_next;
+                const float diag = diag_next, edge = edge_next;
                 if (k + 1 < it.chunks()) {
                     const float* r = it.record(o, k + 1);
-                    hi_next = __ldg(r + kRP + row);
+                    diag_next = __ldg(r + kRCol + (rev ? 0 : kRDir) + 128 + row);
                     edge_next = __ldg(r + (rev ? kRU : kRP) + row);
                 }
                 if (!wait(&bar.rec, g & 1, p.err, abort) || !wait(&bar.sc, g & 1, p.err, abort)) {
@@ -881,12 +885,12 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (n == 0 && strict) in &= ~(1u << lane);
                     // The row's decay up to the block times the columns' inside it.  On the
                     // diagonal these are 2^P_r and 2^-P_i (reversed: 2^-P_r, 2^P_i), at most 2^24,
-                    // whose errors (2^-23 times the exponents) stay below 2e-6.
+                    // formed from sums kept in two floats.
                     const bool strong = n == 0 && !(rCol[kRB + q] > -24.f);
-                    float x = n == 0 ? (rev ? -p_hi : p_hi) : edge;
+                    float x = edge;
                     if (n > 1) x += rCol[kRB + (rev ? q + 1 : q - 1)];
                     if (n > 2) x += rCol[kRB + (rev ? q + 2 : q - 2)];
-                    const float rf = ex2f(x);
+                    const float rf = n == 0 ? diag : ex2f(x);
                     const float* cf = rCol + (n == 0 ? 128 : 0) + 32 * j;
 #pragma unroll 1
                     for (int hf = 0; hf < 2; ++hf) {  // 16 columns, a step of A W
@@ -912,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                         } else {
                             // strong decays: the difference of the prefix sums, kept in two floats
                             const float sgn = rev ? -1.f : 1.f;
+                            const float p_hi = __ldg(it.record(o, k) + kRP + row);
                             const float p_lo = __ldg(it.record(o, k) + kRPlo + row);
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
