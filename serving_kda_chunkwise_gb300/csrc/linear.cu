@@ -320,7 +320,8 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
 
 // ------------------------------------------------------------------------ edges --
 // A thread carries four state elements over a sequence's segments, the contributions loaded
-// four segments ahead.  Bound by that traffic, each contribution read and each edge written once,
+// four segments ahead, and on to the state after the sequence where the last segment's contribution
+// is there (the token kernels form that state themselves).  Bound by that traffic, each contribution read and each edge written once,
 // and by its latency where segments are few: 20 us at 65,536 tokens x 32 heads x 128 (33 segments
 // of 2,048: 134 MB), 42 us for both directions of the gradients x 16 heads (65 of 1,024: 268 MB).
 struct Edges {
@@ -328,6 +329,9 @@ struct Edges {
     float* seg[2];          // [edges][H][E] edge states (written)
     const float* edge[2];   // [N][H][E] or nullptr
     const float* dec[2];    // [edges][H] summed log2 decays
+    float* S_out[2];        // [N][H][E] states after the sequences, or nullptr
+    const float* anchor[2];  // as in Call
+    float* anchors[2];
     int E;
 };
 
@@ -343,6 +347,7 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
     const int64_t stride = (int64_t)p.H * (e.E / 4), own = (int64_t)h * (e.E / 4) + at;
     const float4* add = reinterpret_cast<const float4*>(e.add[dir]);
     float4* seg = reinterpret_cast<float4*>(e.seg[dir]);
+    __shared__ float part[8];
     // sequence n's edges
     auto scan = [&](int n) {
         int64_t a, b;
@@ -375,6 +380,32 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
                     seg[slot(i0 + u + 1) * stride + own] = acc;
                 }
         }
+        if (e.S_out[dir] == nullptr && e.anchor[dir] == nullptr) return;
+        const float4 in = __ldcs(add + slot(count - 1) * stride + own);
+        const float f = exp2f(e.dec[dir][slot(count - 1) * p.H + h]);
+        acc.x = fmaf(f, acc.x, in.x);
+        acc.y = fmaf(f, acc.y, in.y);
+        acc.z = fmaf(f, acc.z, in.z);
+        acc.w = fmaf(f, acc.w, in.w);
+        const int64_t at_seq = (int64_t)n * stride + own;
+        if (e.S_out[dir]) reinterpret_cast<float4*>(e.S_out[dir])[at_seq] = acc;
+        if (e.anchor[dir] == nullptr) return;
+        const float4 with = __ldg(reinterpret_cast<const float4*>(e.anchor[dir]) + at_seq);
+        float x = fmaf(acc.x, with.x, fmaf(acc.y, with.y, fmaf(acc.z, with.z, acc.w * with.w)));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+        __syncthreads();
+        // parts by this block and, where a state has fewer blocks than parts, zeros
+        float* to = e.anchors[dir] + ((int64_t)n * p.H + h) * lin::kAnchors;
+        for (int i = blockIdx.x % per_head; i < lin::kAnchors; i += per_head)
+            if (threadIdx.x == 0) {
+                x = 0.f;
+                if (i < per_head)
+                    for (int w = 0; w < 8; ++w) x += part[w];
+                to[i] = x;
+            }
     };
     __shared__ unsigned some[8];  // of the next 256 sequences of this block's, those with segments
     for (int n0 = blockIdx.y; n0 < p.N; n0 += 256 * gridDim.y) {
@@ -626,45 +657,67 @@ cudaError_t launch_token(const Problem& p, const Calls& calls, int n, int64_t sl
                         : launch_token<IO, kOut, false>(p, calls, n, slots, dec, name, s);
 }
 
-template <bool kOut>
-cudaError_t launch_calls(const LinearArgs& a, const Problem& p, const Calls& calls, int n,
-                         const Layout& l, float* dec, const char* name) {
-    const int64_t slots = l.slots;
-    const float* rec = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + l.rec);
-    unsigned* next = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(a.workspace) + l.next);
+struct Scratch {  // of the workspace
+    uint8_t* ws;
+    Layout l;
+    float* at(size_t off) const { return reinterpret_cast<float*>(ws + off); }
+    const float* rec() const { return at(l.rec); }
+    unsigned* next(int i) const { return reinterpret_cast<unsigned*>(ws + l.next) + i; }
+};
+
+// The outputs of some calls.
+cudaError_t launch_out(const LinearArgs& a, const Problem& p, const Scratch& w, const Calls& calls,
+                       int n, const char* name) {
     if (use_tc(a.io_bf16))
-        return kOut ? lintc::launch_outputs(p, calls, n, slots, rec, next, name, a.stream)
-                    : lintc::launch_sums(p, calls, n, slots, rec, dec, next + 1, name, a.stream);
-    return a.io_bf16
-               ? launch_token<__nv_bfloat16, kOut>(p, calls, n, slots, dec, name, a.stream)
-               : launch_token<float, kOut>(p, calls, n, slots, dec, name, a.stream);
+        return lintc::launch_outputs(p, calls, n, w.l.slots, w.rec(), w.next(0), name, a.stream);
+    return a.io_bf16 ? launch_token<__nv_bfloat16, true>(p, calls, n, w.l.slots, nullptr, name,
+                                                         a.stream)
+                     : launch_token<float, true>(p, calls, n, w.l.slots, nullptr, name, a.stream);
 }
 
-// Segment sums and edges of the forward states and, in a backward pass, of the reversed ones.
-cudaError_t launch_segments(const LinearArgs& a, const Problem& p, const Layout& l, bool bwd) {
-    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    float* dec = reinterpret_cast<float*>(ws + l.dec);
-    Calls calls{};
+// Segment sums, edge states and (on the tensor cores) final states of the forward states and, in a
+// backward pass, of the reversed ones; `calls` has their rows and what is wanted at the end.
+cudaError_t launch_states(const LinearArgs& a, const Problem& p, const Scratch& w, Calls calls,
+                          int n, int sums, int counter) {
+    const bool tc = use_tc(a.io_bf16);
+    bool final = false;
+    for (int i = 0; i < n; ++i) final = final || calls.c[i].S_out || calls.c[i].anchor;
+    if (!w.l.segments) sums &= ~lintc::kSegments;
+    if (!tc || !final) sums &= ~lintc::kSingles;
+    if (sums == 0) return cudaSuccess;
+    float* dec = w.at(w.l.dec);
     Edges e{};
-    for (int i = 0; i < (bwd ? 2 : 1); ++i) {
+    for (int i = 0; i < n; ++i) {
         Call& c = calls.c[i];
-        c.y = i ? a.q : a.k; c.y_ld = i ? a.q_ld : a.k_ld;
-        c.w = i ? a.dout : a.v; c.w_ld = i ? a.dout_ld : a.v_ld;
-        c.da = a.dk; c.db = a.dv; c.reverse = i;
-        c.seg = reinterpret_cast<float*>(ws + l.add[i]);
+        c.seg = w.at(w.l.add[i]);
         e.add[i] = c.seg;
-        e.seg[i] = reinterpret_cast<float*>(ws + l.seg[i]);
-        e.edge[i] = i ? a.dS_out : a.S0;
-        e.dec[i] = dec + (size_t)i * l.edges * a.H;
+        e.seg[i] = w.at(w.l.seg[i]);
+        e.edge[i] = c.edge;
+        e.dec[i] = dec + (size_t)i * w.l.edges * a.H;
+        if (tc) {
+            e.S_out[i] = c.S_out;
+            e.anchor[i] = c.anchor;
+            e.anchors[i] = c.anchors;
+        }
     }
     e.E = a.dk * a.dv;
-    if (cudaError_t err = launch_calls<false>(a, p, calls, bwd ? 2 : 1, l, dec,
-                                              "linear_segment_kernel"))
-        return err;
+    const char* name = sums & lintc::kSegments ? "linear_segment_kernel" : "linear_state_kernel";
+    cudaError_t err =
+        tc ? lintc::launch_sums(p, calls, n, w.l.slots, w.rec(), dec, w.next(counter), sums, name,
+                                a.stream)
+        : a.io_bf16
+            ? launch_token<__nv_bfloat16, false>(p, calls, n, w.l.slots, dec, name, a.stream)
+            : launch_token<float, false>(p, calls, n, w.l.slots, dec, name, a.stream);
+    if (err != cudaSuccess || !(sums & lintc::kSegments)) return err;
     ProfScope prof("linear_edge_kernel", a.stream);
     const int per_row = a.H * (e.E / 1024), most = std::max(1, 8 * 8 * 152 / per_row);
-    const dim3 grid(per_row, std::min(a.N, most), bwd ? 2 : 1);
+    const dim3 grid(per_row, std::min(a.N, most), n);
     return launch_dependent(edge_kernel, grid, dim3(256), 0, a.stream, p, e);
+}
+
+cudaError_t launch_decays(const LinearArgs& a, const Problem& p, const Scratch& w) {
+    if (!use_tc(a.io_bf16)) return cudaSuccess;
+    return lintc::launch_decays(p, w.at(w.l.rec), w.next(0), a.stream);
 }
 
 }  // namespace
@@ -677,66 +730,72 @@ size_t linear_bwd_workspace_size(int64_t T, int N, int H, int dk, int dv, int io
 }
 
 cudaError_t launch_linear_fwd(const LinearArgs& a) {
-    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, false, use_tc(a.io_bf16),
-                            a.cu_seqlens == nullptr);
-    const Problem p = problem(a, l);
-    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    if (use_tc(a.io_bf16))
-        if (cudaError_t e = lintc::launch_decays(
-                p, reinterpret_cast<float*>(ws + l.rec), reinterpret_cast<unsigned*>(ws + l.next), a.stream))
-            return e;
-    if (l.segments)
-        if (cudaError_t e = launch_segments(a, p, l, false)) return e;
+    const Scratch w{static_cast<uint8_t*>(a.workspace),
+                    layout(a.T_total, a.N, a.H, a.dk, a.dv, false, use_tc(a.io_bf16),
+                           a.cu_seqlens == nullptr)};
+    const Problem p = problem(a, w.l);
+    if (cudaError_t e = launch_decays(a, p, w)) return e;
     Calls calls{};
     Call& c = calls.c[0];
     c.x = a.q; c.x_ld = a.q_ld; c.y = a.k; c.y_ld = a.k_ld; c.w = a.v; c.w_ld = a.v_ld;
     c.da = a.dk; c.db = a.dv; c.edge = a.S0; c.S_out = a.S_out; c.out = a.o;
-    c.seg = l.segments ? reinterpret_cast<float*>(ws + l.seg[0]) : nullptr;
-    return launch_calls<true>(a, p, calls, 1, l, nullptr, "linear_out_kernel");
+    // With S_out in S0's place the states after sequences of one segment come after the outputs,
+    // which read S0 itself there.
+    const bool in_place = a.S_out != nullptr && a.S_out == a.S0;
+    const int first = lintc::kSegments | (in_place ? 0 : lintc::kSingles);
+    if (cudaError_t e = launch_states(a, p, w, calls, 1, first, 1)) return e;
+    c.seg = w.l.segments ? w.at(w.l.seg[0]) : nullptr;
+    if (cudaError_t e = launch_out(a, p, w, calls, 1, "linear_out_kernel")) return e;
+    return in_place ? launch_states(a, p, w, calls, 1, lintc::kSingles, 2) : cudaSuccess;
 }
 
 cudaError_t launch_linear_bwd(const LinearArgs& a) {
-    const Layout l = layout(a.T_total, a.N, a.H, a.dk, a.dv, true, use_tc(a.io_bf16),
-                            a.cu_seqlens == nullptr);
+    const Scratch w{static_cast<uint8_t*>(a.workspace),
+                    layout(a.T_total, a.N, a.H, a.dk, a.dv, true, use_tc(a.io_bf16),
+                           a.cu_seqlens == nullptr)};
+    const Layout& l = w.l;
     const Problem p = problem(a, l);
-    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-    auto at = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
-    if (use_tc(a.io_bf16))
-        if (cudaError_t e = lintc::launch_decays(
-                p, reinterpret_cast<float*>(ws + l.rec), reinterpret_cast<unsigned*>(ws + l.next), a.stream))
-            return e;
-    if (l.segments)
-        if (cudaError_t e = launch_segments(a, p, l, true)) return e;
-    float* const seg[2] = {l.segments ? at(l.seg[0]) : nullptr, l.segments ? at(l.seg[1]) : nullptr};
+    if (cudaError_t e = launch_decays(a, p, w)) return e;
+    Calls states{};  // S from the starts, D from the ends
+    Call &S = states.c[0], &D = states.c[1];
+    S.y = a.k; S.y_ld = a.k_ld; S.w = a.v; S.w_ld = a.v_ld; S.edge = a.S0;
+    D.y = a.q; D.y_ld = a.q_ld; D.w = a.dout; D.w_ld = a.dout_ld; D.edge = a.dS_out;
+    S.da = D.da = a.dk; S.db = D.db = a.dv; D.reverse = 1; D.S_out = a.dS0;
+    if (a.dg) {
+        S.anchor = a.dS_out; S.anchors = w.at(l.at_end);
+        D.anchor = a.S0; D.anchors = w.at(l.at_start);
+    }
+    if (cudaError_t e =
+            launch_states(a, p, w, states, 2, lintc::kSegments | lintc::kSingles, 1))
+        return e;
+    float* const seg[2] = {l.segments ? w.at(l.seg[0]) : nullptr,
+                           l.segments ? w.at(l.seg[1]) : nullptr};
     Calls calls{};
     Call &q = calls.c[0], &k = calls.c[1], &v = calls.c[2];
     q.x = a.dout; q.x_ld = a.dout_ld; q.y = a.v; q.y_ld = a.v_ld; q.w = a.k; q.w_ld = a.k_ld;
-    q.da = a.dv; q.db = a.dk; q.tr = 1; q.edge = a.S0; q.seg = seg[0];
-    q.out = a.dq;
-    if (a.dg) {
-        q.dot = a.q; q.dot_ld = a.q_ld; q.dots = at(l.dots_q);
-        q.anchor = a.dS_out; q.anchors = at(l.at_end);
-    }
+    q.da = a.dv; q.db = a.dk; q.tr = 1; q.edge = a.S0; q.seg = seg[0]; q.out = a.dq;
     k.x = a.v; k.x_ld = a.v_ld; k.y = a.dout; k.y_ld = a.dout_ld; k.w = a.q; k.w_ld = a.q_ld;
     k.da = a.dv; k.db = a.dk; k.reverse = 1; k.tr = 1; k.edge = a.dS_out; k.seg = seg[1];
     k.out = a.dk_;
-    if (a.dg) { k.dot = a.k; k.dot_ld = a.k_ld; k.dots = at(l.dots_k); }
     v.x = a.k; v.x_ld = a.k_ld; v.y = a.q; v.y_ld = a.q_ld; v.w = a.dout; v.w_ld = a.dout_ld;
-    v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = seg[1];
-    v.S_out = a.dS0; v.out = a.dv_;
-    if (a.dg) { v.anchor = a.S0; v.anchors = at(l.at_start); }
-    if (cudaError_t e =
-            launch_calls<true>(a, p, calls, 3, l, nullptr, "linear_grad_kernel"))
-        return e;
+    v.da = a.dk; v.db = a.dv; v.reverse = 1; v.edge = a.dS_out; v.seg = seg[1]; v.out = a.dv_;
+    v.S_out = a.dS0;
+    if (a.dg) {
+        q.dot = a.q; q.dot_ld = a.q_ld; q.dots = w.at(l.dots_q);
+        k.dot = a.k; k.dot_ld = a.k_ld; k.dots = w.at(l.dots_k);
+        q.anchor = S.anchor; q.anchors = S.anchors;
+        v.anchor = D.anchor; v.anchors = D.anchors;
+    }
+    if (cudaError_t e = launch_out(a, p, w, calls, 3, "linear_grad_kernel")) return e;
     if (a.dg) {
         DecayGrad d{};
         d.segS = seg[0]; d.segD = seg[1];
-        // (the tensor cores' kernel leaves kAnchors parts, the other four a 64 columns)
+        // (the tensor cores' kernels leave 16 parts, the other four a 64 columns)
         const bool tc = use_tc(a.io_bf16);
-        d.at_start = a.S0 ? v.anchors : nullptr; d.n_start = tc ? lin::kAnchors : a.dv / kCols * 4;
-        d.at_end = a.dS_out ? q.anchors : nullptr; d.n_end = tc ? lin::kAnchors : a.dk / kCols * 4;
-        d.dots_q = at(l.dots_q); d.dots_k = at(l.dots_k); d.nq = d.nk = a.dk / kDotCols;
-        d.dg = a.g_per_token ? a.dg : at(l.dg); d.E = a.dk * a.dv;
+        d.at_start = a.S0 ? D.anchors : nullptr; d.n_start = tc ? lin::kAnchors : a.dv / kCols * 4;
+        d.at_end = a.dS_out ? S.anchors : nullptr; d.n_end = tc ? lin::kAnchors : a.dk / kCols * 4;
+        d.dots_q = q.dots; d.dots_k = k.dots; d.nq = d.nk = a.dk / kDotCols;
+        d.dg = a.g_per_token ? a.dg : w.at(l.dg); d.E = a.dk * a.dv;
         if (a.T_total > 0) {
             ProfScope prof("linear_decay_grad_kernel", a.stream);
             if (cudaError_t err = launch_dependent(decay_grad_kernel,

@@ -54,7 +54,7 @@ struct Call {
     float* dots;         //   own term (x_t . y_t) (w_t . dot_t)
 };
 
-constexpr int kMaxCalls = 3, kAnchors = 8;
+constexpr int kMaxCalls = 3, kAnchors = 16;
 struct Calls {
     Call c[kMaxCalls];
 };

@@ -1,5 +1,5 @@
 // linear_tc.cu -- the per-head-decay linear attention of bf16 inputs on the tcgen05 tensor
-// cores: the segment sums and the outputs of a call (linear_common.cuh).
+// cores: the segment sums, the outputs and the final states of a call (linear_common.cuh).
 //
 // Chunks of C = 128 tokens.  With X, Y [C, da] and W [C, db] the chunk's rows, S the state at
 // its start and G the running sum of g inside it (forward; reversed in brackets):
@@ -8,9 +8,11 @@
 //     S  <- e^{G_C} S + Y^T Diag(e^{G_C - G_i}) W             [e^{G_i}]
 // (reversed chunks run from the last to the first, S is then the state at the chunk's end).
 //
-// Precision.  X, Y, W are bf16 as given, so X Y^T is exact up to its fp32 accumulation.  A, S
-// and the decayed W are held as bf16 hi + lo (16 bits of mantissa, 2^-17) in two products each:
-// with hi alone the fp32 state and the decay's gradient would carry bf16's 2^-9.
+// Precision.  X, Y, W are bf16 as given, so X Y^T is exact up to its fp32 accumulation.  In the
+// outputs A, S and the decayed W are held as bf16 hi + lo (16 bits of mantissa, 2^-17) in two
+// products each: with hi alone the decay's gradient would carry bf16's 2^-9.  States that are
+// results, or that segments start from, are formed by the segment sums, whose decayed W has a third
+// part, fp32's 24 bits: 2e-7 to 5e-7 off, with two parts 2.5e-6.
 // No decay is formed as a quotient or as a difference of long sums: with P and U a token's
 // prefix and suffix sums inside its block of 32 tokens and B the blocks' sums, every exponent is
 // a sum of terms of one sign except inside a diagonal block, where the difference of prefix sums
@@ -54,6 +56,16 @@ __device__ __noinline__ bool wait1(uint64_t* bar, uint32_t parity, unsigned* err
     return mbar_wait_ab(bar, parity, err, abort);
 }
 
+// hi, lo and what these leave of (a0, a1), in bf16
+__device__ __forceinline__ void split3(float a0, float a1, uint32_t& hi, uint32_t& lo,
+                                       uint32_t& rest) {
+    hi = pack_bf16x2(a0, a1);
+    a0 -= __uint_as_float(hi << 16);
+    a1 -= __uint_as_float(hi & 0xffff0000u);
+    lo = pack_bf16x2(a0, a1);
+    rest = pack_bf16x2(a0 - __uint_as_float(lo << 16), a1 - __uint_as_float(lo & 0xffff0000u));
+}
+
 // Whether the phase is complete, without waiting.
 __device__ __forceinline__ bool test(uint64_t* bar, uint32_t parity) {
     uint32_t done;
@@ -95,17 +107,6 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
                  : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void landed(float (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
-                   "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
-                   "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
-                   "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
-                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
-                 :
-                 : "memory");
-    asm volatile("" : "+f"(v[30]), "+f"(v[31]) : : "memory");
 }
 
 // ---------------------------------------------------------- descriptors --
@@ -155,6 +156,7 @@ struct OutParams {
     int slots;
     const float* rec;  // decay records, see decay_kernel
     unsigned* next;    // how many items have been taken beyond the first round
+    int sums;          // which (kSegments, kSingles)
 };
 
 __device__ __forceinline__ uint32_t item_count(const OutParams& o) {
@@ -318,7 +320,7 @@ static_assert(sizeof(OutBars) <= 256, "barrier area");
 // are taken as CTAs come to them, for their lengths differ.
 struct View {
     volatile int* v;
-    enum { kBegin, kEnd, kChunks, kCall, kH, kRev, kRecord, kZero, kFinal, kSeg, kState, kWords };
+    enum { kBegin, kEnd, kChunks, kCall, kH, kRev, kRecord, kZero, kN, kSeg, kState, kWords };
     __device__ __forceinline__ int chunks() const { return v[kChunks]; }
     __device__ __forceinline__ int call() const { return v[kCall]; }
     __device__ __forceinline__ int h() const { return v[kH]; }
@@ -349,10 +351,7 @@ __device__ __forceinline__ void put_item(const OutParams& o, const Item& t, View
     w.v[View::kRev] = rev;
     w.v[View::kRecord] = (t.sg.begin - t.sg.s * o.p.L) / kC + t.sg.n + t.sg.s * (o.p.L / kC);
     w.v[View::kZero] = t.sg.count <= 1 && o.calls.c[t.call].edge == nullptr;
-    // (an empty sequence's first slot passes the state on: kChunks = 0, kFinal >= 0)
-    const bool last = t.sg.live ? (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1)
-                                : t.sg.count == 0 && t.sg.s == 0;
-    w.v[View::kFinal] = last ? t.sg.n : -1;  // whose final state follows, if any
+    w.v[View::kN] = t.sg.n;
     // the state that it starts from: a segment's edge state or the sequence's own
     w.v[View::kSeg] = t.sg.count > 1;
     w.v[View::kState] = (t.sg.count > 1 ? t.sg.edge : t.sg.n) * o.p.H + t.h;
@@ -438,27 +437,6 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
     }
 }
 
-// States in memory and in TMEM, 64 columns from `col` by a warp; out of line, once an item.
-struct StateAt {
-    int64_t at, cs;  // this lane's row from column col, the step between columns
-    bool holds;
-};
-__device__ __forceinline__ StateAt state_at(const OutParams& o, const Call& c, int which, int h,
-                                            int col) {
-    const int row = threadIdx.x & 127;
-    StateAt s;
-    s.cs = c.tr ? c.da : 1;
-    s.at = ((int64_t)which * o.p.H + h) * c.da * c.db + (int64_t)row * (c.tr ? 1 : c.db) +
-           col * s.cs;
-    s.holds = col < c.db && row < c.da;
-    return s;
-}
-// A [da][db] state's rows lie 4 db bytes apart, one a lane: written from the lanes, each access
-// would touch 32 lines.  The warp's 32 x 64 piece goes through 8 KB of shared memory instead,
-// 16-byte pieces permuted by the row.  (States are read by TMA: by the warps themselves an item's
-// 64 KB took 15,000 cycles.)
-__device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 256 + ((c ^ (r & 15)) << 4); }
-
 // The item's state from the buffer that the copy is to have, where 32-float boxes of its rows in
 // memory lie (128 bytes a row, 16-byte pieces permuted by the row), into TMEM.
 __device__ __noinline__ void load_state(const OutParams& o, uint8_t* sm, uint32_t n) {
@@ -491,83 +469,6 @@ __device__ __noinline__ void load_state(const OutParams& o, uint8_t* sm, uint32_
     }
     tmem_st_wait();
     __syncwarp();
-}
-// What follows from the n-th item's final state: the state in memory and, for kDots, the warp's part
-// of its dot product with another.
-template <bool kDots>
-__device__ __noinline__ void final_state(const OutParams& o, uint8_t* sm, uint32_t n) {
-    const View it = view(sm, n);
-    const Call& c = o.calls.c[it.call()];
-    const int h = it.h(), seq = it.v[View::kFinal];
-    const int lane = threadIdx.x & 31, row0 = threadIdx.x & 96;
-    const int col = threadIdx.x >= 384 ? 64 : 0;
-    uint8_t* stage = sm + kSS + ((threadIdx.x >> 5) - 8) * 8192;
-    const float* anchor = kDots ? c.anchor : nullptr;
-    const StateAt s = state_at(o, c, seq, h, col);
-    float dot = 0.f;
-    if (col < c.db && row0 < c.da && (c.S_out || anchor)) {
-        const uint32_t from = (static_cast<uint32_t>(row0) << 16) + kTS + col;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-            float v[16], w[16];
-            if (c.tr && anchor)
-#pragma unroll
-                for (int x = 0; x < 16; ++x) w[x] = __ldg(anchor + s.at + (16 * b + x) * s.cs);
-            tmem_ld16(from + 16 * b, v);
-            landed(v);
-            if (!c.tr) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    *reinterpret_cast<float4*>(stage + piece_at(lane, 4 * b + x)) =
-                        make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                continue;
-            }
-            if (c.S_out)
-#pragma unroll
-                for (int x = 0; x < 16; ++x) c.S_out[s.at + (16 * b + x) * s.cs] = v[x];
-            if (anchor)
-#pragma unroll
-                for (int x = 0; x < 16; ++x) dot = fmaf(v[x], w[x], dot);
-        }
-        if (!c.tr) {
-            __syncwarp();
-            const int64_t at = s.at - (int64_t)lane * c.db + (int64_t)(lane >> 4) * c.db +
-                               4 * (lane & 15);
-            auto piece = [&](int x) {
-                return *reinterpret_cast<const float4*>(
-                    stage + piece_at(2 * x + (lane >> 4), lane & 15));
-            };
-            if (c.S_out)
-#pragma unroll 4
-                for (int x = 0; x < 16; ++x)
-                    *reinterpret_cast<float4*>(c.S_out + at + (int64_t)2 * x * c.db) = piece(x);
-            if (anchor)
-#pragma unroll 8
-                for (int x = 0; x < 16; ++x) {
-                    const float4 w = __ldg(
-                        reinterpret_cast<const float4*>(anchor + at + (int64_t)2 * x * c.db));
-                    const float4 v = piece(x);
-                    dot = fmaf(v.x, w.x, fmaf(v.y, w.y, fmaf(v.z, w.z, fmaf(v.w, w.w, dot))));
-                }
-            __syncwarp();
-        }
-    }
-    if (anchor) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-        if (lane == 0)
-            c.anchors[((int64_t)seq * o.p.H + h) * lin::kAnchors + 2 * (row0 >> 5) + (col >> 6)] =
-                dot;
-    }
-}
-__device__ __noinline__ void pass_state(const OutParams& o, uint8_t* sm, uint32_t n) {
-    const View it = view(sm, n);
-    const Call& c = o.calls.c[it.call()];
-    const StateAt s = state_at(o, c, it.v[View::kFinal], it.h(), threadIdx.x >= 384 ? 64 : 0);
-    if (c.S_out && s.holds)
-#pragma unroll 1
-        for (int x = 0; x < 64; ++x)
-            c.S_out[s.at + x * s.cs] = c.edge ? c.edge[s.at + x * s.cs] : 0.f;
 }
 
 // Outputs of one chunk, 32 columns from `col` of one row a lane: rowf (X S) + A W, and
@@ -963,11 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
             const View it = view(sm, n);
             if (it.chunks() < 0) break;
-            const bool final = it.v[View::kFinal] >= 0;
             if (it.chunks() == 0) {
-                // an empty sequence owns its first slot: its final state is its initial one
-                if (final) pass_state(o, sm, n);
-                __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.used[n & 1]);
                 continue;
             }
@@ -1045,17 +942,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (lane == 0) mbar_arrive(&bar.s);
                 }
                 if (k == it.chunks()) {
-                    // the copy's last read is complete: the final state may pass through its
-                    // buffer, and the next item's come
+                    // the copy's last read is complete: the next item's state may come
                     if (!wait(&bar.xs, (g - 1) & 1, p.err, abort)) { ok = false; break; }
-                    if (final) {
-                        if (!wait(&bar.upd, (g - 1) & 1, p.err, abort)) { ok = false; break; }
-                        tc_fence_after();
-                        final_state<kDots>(o, sm, n);
-                        tc_fence_before();
-                        fence_async_smem();
-                        __syncwarp();
-                    }
                     if (lane == 0) mbar_arrive(&bar.idle);
                 }
                 if (k > 0 && !write_out<kDots>(o, bar, sm, g - 1, it, k - 1, rowf_prev, 64 * wg)) {
@@ -1150,17 +1038,27 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 }
 
 // --------------------------------------------------------- segment sums --
-// sum_i e^{G_end - G_i} y_i w_i^T over a segment [reversed: e^{G_i} from its start].  The order
-// of a sum is free, so the chunks run away from the edge the weights refer to, the decay between
-// the edge and the chunk carried along, and the accumulator in TMEM is never rescaled.  W is
-// decayed in place (hi over W itself, lo beside it), so two stages of all operands fit.  Bound by
-// reading Y and W: 209 us at 65,536 tokens x 32 heads x 128, 1.07 GB at 5.1 TB/s (without the
+// sum_i e^{G_end - G_i} y_i w_i^T over a segment [reversed: e^{G_i} from its start]: for the scan over
+// a sequence's segments, or of a sequence that is one segment (or empty), which with the state before
+// it is the state after it.  W is decayed in
+// place (hi over W itself, lo and the third part beside it); two stages of all operands fit but for
+// the third part, which waits until the last chunk's products are done with its buffer.
+// A tensor core adds to its accumulator by truncation, 4e-8 of it a step: the small parts have an
+// accumulator of their own, the chunks take turns at three for hi, and the walk is towards the edge
+// that the weights refer to, so that what counts most comes last.  (Away from it, into one accumulator
+// for all parts, with two parts of W: <S, D> of heads that remember a thousand tokens was 1e-5 off.)
+// Bound by reading Y and W: 209 us at 65,536 tokens x 32 heads x 128, 1.07 GB at 5.1 TB/s (without the
 // conversion 176 us; a third stage for Y and W gained nothing).
 constexpr int kSumThreads = 640;
 constexpr uint32_t kUY = 0, kUW = 32768, kULo = 65536, kUStage = 98304;  // two stages
-constexpr uint32_t kUItem = 2 * kUStage;
+constexpr uint32_t kUThird = 2 * kUStage;
+constexpr uint32_t kUItem = kUThird + 32768;
 constexpr uint32_t kUBar = kUItem + 128;
 constexpr uint32_t kSumSmem = kUBar + 256;
+static_assert(kSumSmem <= 232448, "shared-memory limit");
+// TMEM columns (all 512): three accumulators of hi, one of lo and the third part
+constexpr uint32_t kUSmall = 384;
+constexpr int kUTurns = 3;
 
 struct SumBars {
     uint64_t full[2], done[2], wd[2], stored, drain;
@@ -1190,17 +1088,21 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         fence_mbar_init();
         bar.abort = 0;
     }
-    if (warp == 0) tmem_alloc(&bar.tmem, 128);
+    if (warp == 0) tmem_alloc(&bar.tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = bar.tmem;
     grid_dependents_launch();
     const uint32_t items = item_count(o);
-    // an item whose sum no edge needs: the last segment of a walk
+    // an item whose sum nothing needs, or none in this launch (a walk's last segment is needed only
+    // for the state after the sequence; an empty sequence owns its first slot)
     auto skip = [&](const Item& t) {
-        const int rev = o.calls.c[t.call].reverse;
-        return !t.sg.live || (rev ? t.sg.s == 0 : t.sg.s == t.sg.count - 1);
+        const Call& c = o.calls.c[t.call];
+        const bool final = c.S_out || c.anchor;
+        if (t.sg.count <= 1)
+            return !(o.sums & kSingles) || !final || (t.sg.count == 0 ? t.sg.s != 0 : !t.sg.live);
+        const bool last = c.reverse ? t.sg.s == 0 : t.sg.s == t.sg.count - 1;
+        return !(o.sums & kSegments) || !t.sg.live || (last && !final);
     };
     int loads = 0;  // stages loaded by the TMA thread (for the way out of an abort)
 
@@ -1235,10 +1137,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                     break;
                 }
                 const View it = view(n);
-                if (lane == __ffs(mask) - 1) {
-                    put_item(o, t, it);
-                    it.v[View::kRev] = !it.v[View::kRev];  // the walk's direction here
-                }
+                if (lane == __ffs(mask) - 1) put_item(o, t, it);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bar.item[n & 1]);
@@ -1262,6 +1161,15 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                             tma_load_3d(s + kUW + b * 16384, &o.w[call], 64 * b, h, ch.t0,
                                         &bar.full[st]);
                         loads = (int)g + 1;
+                        if (k + 2 < it.chunks()) {  // its stage comes free late: into L2 early
+                            const int ahead = it.chunk(k + 2).t0;
+#pragma unroll 1
+                            for (int b = 0; b < c.da / 64; ++b)
+                                tma_prefetch_3d(&o.y[call], 64 * b, h, ahead);
+#pragma unroll 1
+                            for (int b = 0; b < c.db / 64; ++b)
+                                tma_prefetch_3d(&o.w[call], 64 * b, h, ahead);
+                        }
                     }
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -1275,7 +1183,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         }
     } else if (tid == 32) {
         const uint32_t lY = dlow(sbase + kUY, 16384), lHi = dlow(sbase + kUW, 16384);
-        const uint32_t lLo = dlow(sbase + kULo, 16384);
+        const uint32_t lLo = dlow(sbase + kULo, 16384), lThird = dlow(sbase + kUThird, 16384);
         uint32_t g = 0;
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
@@ -1290,13 +1198,14 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                 const uint32_t st = g & 1;
                 if (!wait1(&bar.wd[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t at = st * kUStage >> 4;
+                const uint32_t at = st * kUStage >> 4, turn = 128 * (k % kUTurns);
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks) {
-                    mma_bf16(tmem, desc(lY + at + (ks * 2048 >> 4)),
-                             desc(lHi + at + (ks * 2048 >> 4)), id, k + ks > 0);
-                    mma_bf16(tmem, desc(lY + at + (ks * 2048 >> 4)),
-                             desc(lLo + at + (ks * 2048 >> 4)), id, 1);
+                    const uint32_t step = ks * 2048 >> 4;
+                    mma_bf16(turn, desc(lY + at + step), desc(lHi + at + step), id,
+                             k >= kUTurns || ks > 0);
+                    mma_bf16(kUSmall, desc(lY + at + step), desc(lLo + at + step), id, k + ks > 0);
+                    mma_bf16(kUSmall, desc(lY + at + step), desc(lThird + step), id, 1);
                 }
                 mma_commit(&bar.done[st]);
             }
@@ -1317,48 +1226,50 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             const Call& c = o.calls.c[it.call()];
             const int rev = c.reverse;
             const bool cols = 32 * cg < c.db;
-            float between = 0.f;  // log2 decay between the edge and the chunk
+            // log2 decays between the edge and the walk's chunks, chunk k's in lane k (a segment has
+            // at most 16), and over all of them
+            float between = lane < chunks ? __ldg(it.record(o, lane) + kRCol + kRB + 4) : 0.f;
             const int mine = (rev ? kRHead : kRTail) + row;
-            const float* r = it.record(o, 0);
-            float next = __ldg(r + mine), total = __ldg(r + kRCol + kRB + 4);
+            float next = chunks > 0 ? __ldg(it.record(o, 0) + mine) : 0.f;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const float x = __shfl_down_sync(0xffffffffu, between, off);
+                if (lane + off < 32) between += x;
+            }
+            const float whole = __shfl_sync(0xffffffffu, between, 0);
+            between = __shfl_down_sync(0xffffffffu, between, 1);  // (lane 31's is none's)
 #pragma unroll 1
             for (int k = 0; k < chunks; ++k, ++g) {
                 const uint32_t st = g & 1;
-                const float wf = next * ex2f(between);
-                between += total;
-                if (k + 1 < chunks) {  // the next chunk's, early
-                    r = it.record(o, k + 1);
-                    next = __ldg(r + mine);
-                    total = __ldg(r + kRCol + kRB + 4);
-                }
+                const float wf = next * ex2f(__shfl_sync(0xffffffffu, between, k));
+                if (k + 1 < chunks) next = __ldg(it.record(o, k + 1) + mine);  // early
                 if (!wait(&bar.full[st], (g >> 1) & 1, p.err, abort)) { ok = false; break; }
                 uint8_t* stage = sm + st * kUStage;
                 const bool dead = row >= it.chunk(k).len;
+                const uint32_t own = (cg >> 1) * 16384 + row * 128;
+                auto at = [&](int x) { return own + (((4 * (cg & 1) + x) ^ (row & 7)) << 4); };
+                uint4 rest[4];
                 if (cols) {
-                    uint8_t* wr = stage + kUW + (cg >> 1) * 16384 + row * 128;
-                    uint8_t* lr = stage + kULo + (cg >> 1) * 16384 + row * 128;
-                    uint4 in[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        in[x] = *reinterpret_cast<const uint4*>(
-                            wr + (((4 * (cg & 1) + x) ^ (row & 7)) << 4));
-                    if (dead)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) in[x] = make_uint4(0u, 0u, 0u, 0u);
+                        rest[x] = *reinterpret_cast<const uint4*>(stage + kUW + at(x));
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
+                        uint32_t w[4] = {rest[x].x, rest[x].y, rest[x].z, rest[x].w};
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
+                            if (dead) w[y] = 0u;
                             float a0 = __uint_as_float(w[y] << 16);
                             float a1 = __uint_as_float(w[y] & 0xffff0000u);
                             mul2(a0, a1, wf, wf);
-                            split2(a0, a1, hi[y], lo[y]);
+                            split3(a0, a1, hi[y], lo[y], w[y]);
                         }
-                        const uint32_t to = ((4 * (cg & 1) + x) ^ (row & 7)) << 4;
-                        *reinterpret_cast<uint4*>(wr + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(lr + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4*>(stage + kUW + at(x)) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(stage + kULo + at(x)) =
+                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        rest[x] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 if (dead) {
@@ -1367,39 +1278,102 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                     for (int x = 0; x < 4; ++x)
                         yr[(4 * (cg & 1) + x) ^ (row & 7)] = make_uint4(0u, 0u, 0u, 0u);
                 }
+                // the last chunk's products have read their third part
+                if (g > 0 && !wait(&bar.done[st ^ 1], ((g - 1) >> 1) & 1, p.err, abort)) {
+                    ok = false;
+                    break;
+                }
+                if (cols)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<uint4*>(sm + kUThird + at(x)) = rest[x];
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.wd[st]);
             }
             if (!ok) break;
-            // the accumulator is complete with the item's last chunk; the next item's first MMA
+            // the accumulators are complete with the item's last chunk; the next item's first MMA
             // follows this warp's next arrival
             const uint32_t gl = g - 1;
-            if (!wait(&bar.done[gl & 1], (gl >> 1) & 1, p.err, abort)) { ok = false; break; }
+            if (chunks > 0 && !wait(&bar.done[gl & 1], (gl >> 1) & 1, p.err, abort)) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
+            float dot = 0.f;
             if (cols) {
-                // (through shared memory, as in load_state(): both lo buffers are free now, for
-                // every product is complete and these warps write them next)
-                float v[32];
-                tmem_ld32(tmem + lb + 32 * cg, v);
-                landed(v);
+                // (through shared memory, for a state's rows lie 4 db bytes apart, one a lane: both lo
+                // buffers are free now, for every product is complete and these warps write them next)
                 const int w16 = warp - 4;
                 uint8_t* own = sm + (w16 >> 3) * kUStage + kULo + (w16 & 7) * 4096;
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    *reinterpret_cast<float4*>(own + lane * 128 + ((x ^ (lane & 7)) << 4)) =
-                        make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
-                __syncwarp();
-                float* to = const_cast<float*>(c.seg) +
-                            ((int64_t)it.v[View::kState] * c.da + 32 * q) * c.db + 32 * cg;
-                if (32 * q < c.da)
+                for (int b = 0; b < 2; ++b) {
+                    float v[16];
+                    if (chunks > 0) {
+                        tmem_ld16(lb + kUSmall + 32 * cg + 16 * b, v);
+                        landed(v);
+                    } else {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const int r8 = 4 * x + (lane >> 3), c8 = lane & 7;
-                        reinterpret_cast<float4*>(to + (int64_t)r8 * c.db)[c8] =
-                            *reinterpret_cast<const float4*>(own + r8 * 128 +
-                                                             ((c8 ^ (r8 & 7)) << 4));
+                        for (int x = 0; x < 16; ++x) v[x] = 0.f;
                     }
+#pragma unroll 1
+                    for (int turn = 0; turn < min(chunks, kUTurns); ++turn) {
+                        float u[16];
+                        tmem_ld16(lb + 128 * turn + 32 * cg + 16 * b, u);
+                        landed(u);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) v[x] += u[x];
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        *reinterpret_cast<float4*>(own + lane * 128 +
+                                                   (((4 * b + x) ^ (lane & 7)) << 4)) =
+                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                }
+                __syncwarp();
+                // a lane's first float4 of the piece, in a state and in those at hand
+                const int64_t first = (int64_t)(32 * q + (lane >> 3)) * c.db + 32 * cg + 4 * (lane & 7);
+                const int64_t E = (int64_t)c.da * c.db, state = it.v[View::kState] * E + first;
+                const int64_t seq = ((int64_t)it.v[View::kN] * p.H + it.h()) * E + first;
+                auto sum = [&](int x) {
+                    const int r8 = 4 * x + (lane >> 3), c8 = lane & 7;
+                    return *reinterpret_cast<const float4*>(own + r8 * 128 +
+                                                            ((c8 ^ (r8 & 7)) << 4));
+                };
+                const bool rows = 32 * q < c.da;
+                if (rows && it.v[View::kSeg]) {
+                    float* to = const_cast<float*>(c.seg) + state;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        *reinterpret_cast<float4*>(to + (int64_t)4 * x * c.db) = sum(x);
+                } else if (rows) {
+                    const float f = ex2f(whole);
+#pragma unroll 4
+                    for (int x = 0; x < 8; ++x) {
+                        const int64_t to = (int64_t)4 * x * c.db;
+                        float4 v = sum(x);
+                        if (c.edge) {  // (which S_out may be)
+                            const float4 u = *reinterpret_cast<const float4*>(c.edge + seq + to);
+                            v.x = fmaf(f, u.x, v.x);
+                            v.y = fmaf(f, u.y, v.y);
+                            v.z = fmaf(f, u.z, v.z);
+                            v.w = fmaf(f, u.w, v.w);
+                        }
+                        if (c.S_out) *reinterpret_cast<float4*>(c.S_out + seq + to) = v;
+                        if (c.anchor) {
+                            const float4 u =
+                                __ldg(reinterpret_cast<const float4*>(c.anchor + seq + to));
+                            dot = fmaf(v.x, u.x, fmaf(v.y, u.y, fmaf(v.z, u.z, fmaf(v.w, u.w, dot))));
+                        }
+                    }
+                }
+            }
+            if (c.anchor && !it.v[View::kSeg]) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                if (lane == 0)
+                    c.anchors[((int64_t)it.v[View::kN] * p.H + it.h()) * lin::kAnchors + warp - 4] =
+                        dot;
             }
             tc_fence_before();
             // no warp decays the next item's W over another's sums
@@ -1407,8 +1381,8 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             if (lane == 0) mbar_arrive(&bar.stored);
             if (!wait(&bar.stored, stored & 1, p.err, abort)) { ok = false; break; }
             ++stored;
-            if (warp == 4 && lane == 0)
-                dec[(int64_t)rev * p.edges * p.H + it.v[View::kState]] = between;
+            if (it.v[View::kSeg] && warp == 4 && lane == 0)
+                dec[(int64_t)rev * p.edges * p.H + it.v[View::kState]] = whole;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.used[n & 1]);
         }
@@ -1428,7 +1402,7 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 128);
+        tmem_dealloc(0, 512);
     }
 }
 
@@ -1539,10 +1513,11 @@ cudaError_t launch_outputs(const Problem& p, const lin::Calls& calls, int n, int
 }
 
 cudaError_t launch_sums(const Problem& p, const lin::Calls& calls, int n, int64_t slots,
-                        const float* rec, float* dec, unsigned* next, const char* name,
-                        cudaStream_t s) {
+                        const float* rec, float* dec, unsigned* next, int sums,
+                        const char* name, cudaStream_t s) {
     OutParams o{};
     o.next = next;
+    o.sums = sums;
     if (cudaError_t e = fill(o, p, calls, n, slots, rec, false)) return e;
     if (cudaError_t e = cudaFuncSetAttribute(
             sum_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSumSmem))
