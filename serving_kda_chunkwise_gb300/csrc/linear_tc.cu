@@ -1061,7 +1061,7 @@ constexpr uint32_t kUSmall = 384;
 constexpr int kUTurns = 3;
 
 struct SumBars {
-    uint64_t full[2], done[2], wd[2], stored, drain;
+    uint64_t full[2], done[2], wd[2], drain;
     uint64_t item[2], used[2];  // as in OutBars (17 arrivals)
     uint32_t tmem;
     int abort;
@@ -1083,7 +1083,6 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             mbar_init(&bar.item[i], 1);
             mbar_init(&bar.used[i], 17);
         }
-        mbar_init(&bar.stored, 16);
         mbar_init(&bar.drain, 1);
         fence_mbar_init();
         bar.abort = 0;
@@ -1143,6 +1142,10 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                     mbar_arrive(&bar.item[n & 1]);
                     const int call = it.call(), h = it.h();
                     const Call& c = o.calls.c[call];
+                    if (c.edge && !it.v[View::kSeg]) {  // read at the item's end: into L2 early
+                        const int64_t E = (int64_t)c.da * c.db;
+                        l2_prefetch(c.edge + ((int64_t)it.v[View::kN] * p.H + h) * E, 4 * E);
+                    }
                     for (int k = 0; k < it.chunks(); ++k, ++g) {
                         const uint32_t st = g & 1;
                         if (g >= 2 && !wait1(&bar.done[st], ((g - 2) >> 1) & 1, p.err, abort)) {
@@ -1216,21 +1219,31 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
         const int q = warp & 3, cg = (warp - 4) >> 2;
         const int row = 32 * q + lane;
         const uint32_t lb = static_cast<uint32_t>(32 * q) << 16;
-        uint32_t g = 0, stored = 0;
-        bool ok = true;
+        uint32_t g = 0;
+        // An item's first loads from the decays' records, before the item before it is stored: the
+        // chunks' summed log2 decays, chunk k's in lane k (a segment has at most 16), and the row's
+        // factor in the first chunk.
+        float total = 0.f, first = 0.f;
+        auto open = [&](uint32_t n) {
+            if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) return false;
+            const View it = view(n);
+            const int chunks = it.chunks();
+            const int mine = (it.rev() ? kRHead : kRTail) + row;
+            total = lane < chunks ? __ldg(it.record(o, lane) + kRCol + kRB + 4) : 0.f;
+            first = chunks > 0 ? __ldg(it.record(o, 0) + mine) : 0.f;
+            return true;
+        };
+        bool ok = open(0);
         for (uint32_t n = 0; ok; ++n) {
-            if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
             const View it = view(n);
             const int chunks = it.chunks();
             if (chunks < 0) break;
             const Call& c = o.calls.c[it.call()];
             const int rev = c.reverse;
             const bool cols = 32 * cg < c.db;
-            // log2 decays between the edge and the walk's chunks, chunk k's in lane k (a segment has
-            // at most 16), and over all of them
-            float between = lane < chunks ? __ldg(it.record(o, lane) + kRCol + kRB + 4) : 0.f;
             const int mine = (rev ? kRHead : kRTail) + row;
-            float next = chunks > 0 ? __ldg(it.record(o, 0) + mine) : 0.f;
+            // log2 decays between the edge and the walk's chunks, and over all of them
+            float between = total, next = first;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const float x = __shfl_down_sync(0xffffffffu, between, off);
@@ -1291,7 +1304,20 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.wd[st]);
             }
-            if (!ok) break;
+            if (!ok || !(ok = open(n + 1))) break;
+            // The warp's piece of the state: 32 rows x 32 columns, a row a lane in TMEM, four rows an
+            // access in memory (where rows lie 4 db bytes apart).  It passes through what the warp
+            // itself writes of both stages' lo buffers, 64 bytes of its rows in each.
+            const bool piece = cols && 32 * q < c.da, single = !it.v[View::kSeg];
+            const int64_t E = (int64_t)c.da * c.db;
+            const int64_t at0 = (int64_t)(32 * q + (lane >> 3)) * c.db + 32 * cg + 4 * (lane & 7);
+            const int64_t seq = ((int64_t)it.v[View::kN] * p.H + it.h()) * E + at0;
+            float4 before[8];  // the state before the segment (S_out may be in its place)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                before[x] = piece && single && c.edge
+                                ? *reinterpret_cast<const float4*>(c.edge + seq + 4 * x * c.db)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
             // the accumulators are complete with the item's last chunk; the next item's first MMA
             // follows this warp's next arrival
             const uint32_t gl = g - 1;
@@ -1301,88 +1327,69 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
             }
             tc_fence_after();
             float dot = 0.f;
-            if (cols) {
-                // (through shared memory, for a state's rows lie 4 db bytes apart, one a lane: both lo
-                // buffers are free now, for every product is complete and these warps write them next)
-                const int w16 = warp - 4;
-                uint8_t* own = sm + (w16 >> 3) * kUStage + kULo + (w16 & 7) * 4096;
+            auto stage_at = [&](int r, int c16) {
+                return reinterpret_cast<float4*>(sm + (c16 >> 2) * kUStage + kULo +
+                                                 (cg >> 1) * 16384 + (32 * q + r) * 128 +
+                                                 (((4 * (cg & 1) + (c16 & 3)) ^ (r & 7)) << 4));
+            };
+            if (piece) {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float v[16];
-                    if (chunks > 0) {
-                        tmem_ld16(lb + kUSmall + 32 * cg + 16 * b, v);
-                        landed(v);
-                    } else {
+                for (int b = 0; b < 4; ++b) {
+                    float v[8], w[kUTurns][8];
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) v[x] = 0.f;
-                    }
-#pragma unroll 1
-                    for (int turn = 0; turn < min(chunks, kUTurns); ++turn) {
-                        float u[16];
-                        tmem_ld16(lb + 128 * turn + 32 * cg + 16 * b, u);
-                        landed(u);
+                    for (int x = 0; x < 8; ++x) v[x] = w[0][x] = w[1][x] = w[2][x] = 0.f;
+                    const uint32_t from = lb + 32 * cg + 8 * b;
+                    if (chunks > 0) tmem_ld8(from + kUSmall, v);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) v[x] += u[x];
-                    }
+                    for (int turn = 0; turn < kUTurns; ++turn)
+                        if (chunks > turn) tmem_ld8(from + 128 * turn, w[turn]);
+                    landed(v);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        *reinterpret_cast<float4*>(own + lane * 128 +
-                                                   (((4 * b + x) ^ (lane & 7)) << 4)) =
-                            make_float4(v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+                    for (int turn = 0; turn < kUTurns; ++turn) landed(w[turn]);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) v[x] += w[0][x] + (w[1][x] + w[2][x]);
+                    *stage_at(lane, 2 * b) = make_float4(v[0], v[1], v[2], v[3]);
+                    *stage_at(lane, 2 * b + 1) = make_float4(v[4], v[5], v[6], v[7]);
                 }
                 __syncwarp();
-                // a lane's first float4 of the piece, in a state and in those at hand
-                const int64_t first = (int64_t)(32 * q + (lane >> 3)) * c.db + 32 * cg + 4 * (lane & 7);
-                const int64_t E = (int64_t)c.da * c.db, state = it.v[View::kState] * E + first;
-                const int64_t seq = ((int64_t)it.v[View::kN] * p.H + it.h()) * E + first;
-                auto sum = [&](int x) {
-                    const int r8 = 4 * x + (lane >> 3), c8 = lane & 7;
-                    return *reinterpret_cast<const float4*>(own + r8 * 128 +
-                                                            ((c8 ^ (r8 & 7)) << 4));
-                };
-                const bool rows = 32 * q < c.da;
-                if (rows && it.v[View::kSeg]) {
-                    float* to = const_cast<float*>(c.seg) + state;
+                auto sum = [&](int x) { return *stage_at(4 * x + (lane >> 3), lane & 7); };
+                if (!single) {
+                    float* to = const_cast<float*>(c.seg) + it.v[View::kState] * E + at0;
 #pragma unroll
                     for (int x = 0; x < 8; ++x)
-                        *reinterpret_cast<float4*>(to + (int64_t)4 * x * c.db) = sum(x);
-                } else if (rows) {
+                        *reinterpret_cast<float4*>(to + 4 * x * c.db) = sum(x);
+                } else {
                     const float f = ex2f(whole);
-#pragma unroll 4
+#pragma unroll
+                    for (int x = 4; x < 8; ++x)
+                        before[x] = c.edge ? *reinterpret_cast<const float4*>(c.edge + seq +
+                                                                              4 * x * c.db)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        const int64_t to = (int64_t)4 * x * c.db;
                         float4 v = sum(x);
-                        if (c.edge) {  // (which S_out may be)
-                            const float4 u = *reinterpret_cast<const float4*>(c.edge + seq + to);
-                            v.x = fmaf(f, u.x, v.x);
-                            v.y = fmaf(f, u.y, v.y);
-                            v.z = fmaf(f, u.z, v.z);
-                            v.w = fmaf(f, u.w, v.w);
-                        }
-                        if (c.S_out) *reinterpret_cast<float4*>(c.S_out + seq + to) = v;
+                        v.x = fmaf(f, before[x].x, v.x);
+                        v.y = fmaf(f, before[x].y, v.y);
+                        v.z = fmaf(f, before[x].z, v.z);
+                        v.w = fmaf(f, before[x].w, v.w);
+                        if (c.S_out) *reinterpret_cast<float4*>(c.S_out + seq + 4 * x * c.db) = v;
                         if (c.anchor) {
                             const float4 u =
-                                __ldg(reinterpret_cast<const float4*>(c.anchor + seq + to));
+                                __ldg(reinterpret_cast<const float4*>(c.anchor + seq + 4 * x * c.db));
                             dot = fmaf(v.x, u.x, fmaf(v.y, u.y, fmaf(v.z, u.z, fmaf(v.w, u.w, dot))));
                         }
                     }
                 }
             }
-            if (c.anchor && !it.v[View::kSeg]) {
+            if (c.anchor && single) {
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
                 if (lane == 0)
-                    c.anchors[((int64_t)it.v[View::kN] * p.H + it.h()) * lin::kAnchors + warp - 4] =
-                        dot;
+                    c.anchors[((int64_t)it.v[View::kN] * p.H + it.h()) * lin::kAnchors + warp - 4] = dot;
             }
-            tc_fence_before();
-            // no warp decays the next item's W over another's sums
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.stored);
-            if (!wait(&bar.stored, stored & 1, p.err, abort)) { ok = false; break; }
-            ++stored;
-            if (it.v[View::kSeg] && warp == 4 && lane == 0)
+            if (!single && warp == 4 && lane == 0)
                 dec[(int64_t)rev * p.edges * p.H + it.v[View::kState]] = whole;
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.used[n & 1]);
         }
