@@ -27,7 +27,8 @@ def sizes():
 def test_grows_by_what_can_exist(sizes, T, N, H, dk, dv, dt):
     """Two arrays (gradients: four) of at most 2 T / L edge states, where segments are at least 64
     (bf16: 128) tokens and there is about one a SM at most (bf16; gradients up to 1,024 tokens,
-    forward 2,048; fp32 four); the chunks' decays (bf16: 4.7 KB each); dot products."""
+    forward 2,048; fp32 four); the chunks' decays (bf16: 4.7 KB each); dot products; 16 parts of
+    <S, D> at both ends of a sequence."""
     state = H * dk * dv * 4
     for bwd, size in enumerate(sizes):
         L = 128 if dt else 64
@@ -36,7 +37,7 @@ def test_grows_by_what_can_exist(sizes, T, N, H, dk, dv, dt):
         edges = 2 * T // L
         chunks = T // 128 + N
         most = (4 if bwd else 2) * edges * state + (chunks * H * 4736 if dt else 0)
-        most += 2 * edges * H * 4 + (bwd and 2 * (dk // 32) * T * H * 4 + T * H * 4 + N * H * 64)
+        most += 2 * edges * H * 4 + (bwd and 2 * (dk // 32) * T * H * 4 + T * H * 4 + N * H * 2 * 16 * 4)
         assert size(T, N, H, dk, dv, dt) <= most + 4096 + (1 << 20)
 
 
