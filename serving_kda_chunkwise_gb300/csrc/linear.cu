@@ -668,8 +668,20 @@ struct Scratch {  // of the workspace
 // The outputs of some calls.
 cudaError_t launch_out(const LinearArgs& a, const Problem& p, const Scratch& w, const Calls& calls,
                        int n, const char* name) {
-    if (use_tc(a.io_bf16))
-        return lintc::launch_outputs(p, calls, n, w.l.slots, w.rec(), w.next(0), name, a.stream);
+    if (use_tc(a.io_bf16)) {
+        // (calls with dot products and the others are kernels of their own)
+        int m = 0;
+        while (m < n && calls.c[m].dot) ++m;
+        Calls rest{};
+        for (int i = m; i < n; ++i) rest.c[i - m] = calls.c[i];
+        if (m > 0)
+            if (cudaError_t e = lintc::launch_outputs(p, calls, m, w.l.slots, w.rec(), w.next(0),
+                                                      name, a.stream))
+                return e;
+        return m == n ? cudaSuccess
+                      : lintc::launch_outputs(p, rest, n - m, w.l.slots, w.rec(),
+                                              w.next(m > 0 ? 2 : 0), name, a.stream);
+    }
     return a.io_bf16 ? launch_token<__nv_bfloat16, true>(p, calls, n, w.l.slots, nullptr, name,
                                                          a.stream)
                      : launch_token<float, true>(p, calls, n, w.l.slots, nullptr, name, a.stream);

@@ -10,9 +10,12 @@
 //
 // Precision.  X, Y, W are bf16 as given, so X Y^T is exact up to its fp32 accumulation.  In the
 // outputs A, S and the decayed W are held as bf16 hi + lo (16 bits of mantissa, 2^-17) in two
-// products each: with hi alone the decay's gradient would carry bf16's 2^-9.  States that are
-// results, or that segments start from, are formed by the segment sums, whose decayed W has a third
-// part, fp32's 24 bits: 2e-7 to 5e-7 off, with two parts 2.5e-6.
+// products each, which is lost in the rounding of the outputs to bf16.  Where fp32 results come of
+// them there is a third part, for fp32's 24 bits: of S and the decayed W in the calls whose dot
+// products make up the decay's gradient (dg of 65,536 x 16: 2.0e-6 off, with two parts 4.3e-6; a third
+// part of A finds no room, and costs heads of short memory 3e-6), and of the decayed W in the segment
+// sums, which form all states that are results or that segments start from (2e-7 off; with two
+// parts 2.5e-6).
 // No decay is formed as a quotient or as a difference of long sums: with P and U a token's
 // prefix and suffix sums inside its block of 32 tokens and B the blocks' sums, every exponent is
 // a sum of terms of one sign except inside a diagonal block, where the difference of prefix sums
@@ -359,6 +362,7 @@ __device__ __forceinline__ void put_item(const OutParams& o, const Item& t, View
 
 // One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each once
 // the last chunk's buffer has been read.  Returns the number of chunks loaded.
+template <bool kDots>
 __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int which, uint8_t* sm) {
     const CUtensorMap* maps = which == 0 ? o.x : which == 1 ? o.y : o.w;
     uint8_t* dst = sm + (which == 0 ? kSX : which == 1 ? kSY : kSW);
@@ -369,7 +373,6 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
     const uint32_t items = item_count(o);
     int g = 0;
     uint32_t states = 0, i = blockIdx.x;
-    bool dots = false;  // the last chunk's outputs take their own terms from W
     for (uint32_t n = 0;; ++n) {
         const View it = view(sm, n);
         if (which == 0) {
@@ -411,9 +414,9 @@ __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int w
                 ++states;
             }
             if (g > 0 && !wait1(freed, last, err, abort)) return g;
-            if (which == 2 && g > 0 && !wait1(dots ? &bar.read : &bar.wd, last, err, abort))
+            // (dots: the outputs take their own terms from W)
+            if (which == 2 && g > 0 && !wait1(kDots ? &bar.read : &bar.wd, last, err, abort))
                 return g;
-            dots = c.dot != nullptr;
             const Chunk ch = it.chunk(k);
             mbar_expect_tx(full, blocks * 16384);
 #pragma unroll 1
@@ -471,9 +474,9 @@ __device__ __noinline__ void load_state(const OutParams& o, uint8_t* sm, uint32_
     __syncwarp();
 }
 
-// Outputs of one chunk, 32 columns from `col` of one row a lane: rowf (X S) + A W, and
-// their dot products with another row where wanted.  A is then without its diagonal, and the
-// token's own term, x . y w, joins the outputs after the dot product.  A warp's 32 rows are its TMEM lanes: stored
+// Outputs of one chunk, 32 columns from `col` of one row a lane: rowf (X S) + A W, and for kDots
+// their dot products with another row.  A is then without its diagonal, and the token's own term,
+// x . y w, joins the outputs after the dot product.  A warp's 32 rows are its TMEM lanes: stored
 // from there, each access would touch 32 lines and keep the load/store unit busy for 2000 cycles,
 // so a warp passes its 2 KB through the decayed W's buffer (whose product is complete, and which
 // the next chunk's overwrites only then).  A TMA store of the whole tile kept that buffer for
@@ -485,7 +488,7 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
     const Call& c = o.calls.c[it.call()];
     const int db = c.db, h = it.h();
     const Chunk ch = it.chunk(k);
-    const bool cols = col < db, dots = kDots && cols && row < ch.len && c.dot != nullptr;
+    const bool cols = col < db, dots = kDots && cols && row < ch.len;
     // (the other rows' first pieces early, while the products are waited for)
     const uint4* dr = nullptr;
     uint4 d[2];
@@ -594,7 +597,10 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
     return true;
 }
 
-// kDots: some call wants its outputs' dot products (a forward has the registers they take to spare).
+// kDots: the calls want their outputs' dot products, and have third parts of the state's copy and of
+// the decayed W.  Those have no buffers of their own: the copy's lies in the decayed W's lo part's
+// until X S is done, W's then in the copy's.  (Calls without them are launched on their own: in one
+// kernel for both, 1,319 us against 1,130 for the gradients of 65,536 x 16.)
 template <bool kDots>
 __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant__ OutParams o) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -630,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
     if (warp < 16) grid_dependency_wait();  // (X, Y and W are no earlier launch's)
 
     if (warp >= 16 && warp < 19) {
-        if (lane == 0) loads = load_operand(o, bar, warp - 16, sm);
+        if (lane == 0) loads = load_operand<kDots>(o, bar, warp - 16, sm);
     } else if (tid == kMmaT) {
         // ------------------------------------------------------- MMA thread
         constexpr uint32_t id_sc = idesc_bf16(128, 128, false, false);  // X Y^T
@@ -698,6 +704,11 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                             for (int part = 0; part < 2; ++part)
                                 mma_bf16(kTS, desc(lYm + (ks * 2048 >> 4)),
                                          desc(lWd + ((part * 32768 + ks * 2048) >> 4)), id_up, 1);
+                        if (kDots)  // (the third part from the state's copy's buffer)
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks)
+                                mma_bf16(kTS, desc(lYm + (ks * 2048 >> 4)),
+                                         desc(lS + (ks * 2048 >> 4)), id_up, 1);
                         mma_commit(&bar.upd);
                     } else if (now == 2) {
                         // X S
@@ -711,6 +722,14 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                                          desc(lS + ((part * 32768 + ks * 2048) >> 4)), id_out,
                                          ks + part > 0);
                         }
+                        if (kDots)  // (from the decayed W's lo part's buffer)
+#pragma unroll
+                            for (int ks = 0; ks < 8; ++ks) {
+                                if (ks == 4 && da == 64) break;
+                                mma_bf16(kTO2,
+                                         desc(lX + (((ks >> 2) * 16384 + (ks & 3) * 32) >> 4)),
+                                         desc(lWd + ((32768 + ks * 2048) >> 4)), id_out, 1);
+                            }
                         mma_commit(&bar.xs);
                     } else {
                         // A W: A's 16-token steps are 8 columns of hi and 8 of lo
@@ -752,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             for (int k = 0; k < it.chunks(); ++k, ++g) {
                 const int rev = it.rev();
                 const int len = it.chunk(k).len;
-                const bool strict = kDots && o.calls.c[it.call()].dot != nullptr;
                 const float diag = diag_next, edge = edge_next;
                 if (k + 1 < it.chunks()) {
                     const float* r = it.record(o, k + 1);
@@ -783,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (rev && len - 32 * j < 32)
                         in = len > 32 * j ? (1u << (len - 32 * j)) - 1u : 0u;
                     if (n == 0) in &= rev ? ~((1u << lane) - 1u) : (2u << lane) - 1u;
-                    if (n == 0 && strict) in &= ~(1u << lane);
+                    if (n == 0 && kDots) in &= ~(1u << lane);
                     // The row's decay up to the block times the columns' inside it.  On the
                     // diagonal these are 2^P_r and 2^-P_i (reversed: 2^-P_r, 2^P_i), at most 2^24,
                     // formed from sums kept in two floats.
@@ -908,31 +926,41 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     tc_fence_after();
                     if (cols) {
                         uint8_t* sr = sm + kSS + wg * 16384 + row * 128;
+                        // (few columns at a time, to stay within the registers)
+                        constexpr int kN = kDots ? 8 : 16;
 #pragma unroll 1
-                        for (int b = 0; b < 4; ++b) {
-                            float S[16];
-                            tmem_ld16(at + kTS + 16 * b, S);
+                        for (int b = 0; b < 64 / kN; ++b) {
+                            float S[kN];
+                            if constexpr (kDots) tmem_ld8(at + kTS + kN * b, S);
+                            else tmem_ld16(at + kTS + kN * b, S);
                             landed(S);
                             if (holds)
 #pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    uint4 hi, lo;
-                                    split2(S[8 * x], S[8 * x + 1], hi.x, lo.x);
-                                    split2(S[8 * x + 2], S[8 * x + 3], hi.y, lo.y);
-                                    split2(S[8 * x + 4], S[8 * x + 5], hi.z, lo.z);
-                                    split2(S[8 * x + 6], S[8 * x + 7], hi.w, lo.w);
-                                    const uint32_t to = ((2 * b + x) ^ (row & 7)) << 4;
-                                    *reinterpret_cast<uint4*>(sr + to) = hi;
-                                    *reinterpret_cast<uint4*>(sr + 32768 + to) = lo;
-                                }
-                            uint32_t u[16];
+                                for (int x = 0; x < kN / 8; ++x) {
+                                    const float* v = S + 8 * x;
+                                    const uint32_t to = ((kN / 8 * b + x) ^ (row & 7)) << 4;
+                                    uint32_t hi[4], lo[4], rest[4];
 #pragma unroll
-                            for (int x = 0; x < 16; x += 2) {
+                                    for (int y = 0; y < 4; ++y)
+                                        if (kDots) split3(v[2 * y], v[2 * y + 1], hi[y], lo[y], rest[y]);
+                                        else split2(v[2 * y], v[2 * y + 1], hi[y], lo[y]);
+                                    *reinterpret_cast<uint4*>(sr + to) =
+                                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                                    *reinterpret_cast<uint4*>(sr + 32768 + to) =
+                                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                                    if (kDots)  // (in the decayed W's lo part's buffer)
+                                        *reinterpret_cast<uint4*>(sr + (kSWd + 32768 - kSS) + to) =
+                                            make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                                }
+                            uint32_t u[kN];
+#pragma unroll
+                            for (int x = 0; x < kN; x += 2) {
                                 mul2(S[x], S[x + 1], all, all);
                                 u[x] = __float_as_uint(S[x]);
                                 u[x + 1] = __float_as_uint(S[x + 1]);
                             }
-                            tmem_st16(at + kTS + 16 * b, u);
+                            if constexpr (kDots) tmem_st8(at + kTS + kN * b, u);
+                            else tmem_st16(at + kTS + kN * b, u);
                         }
                         tmem_st_wait();
                         fence_async_smem();
@@ -942,8 +970,12 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (lane == 0) mbar_arrive(&bar.s);
                 }
                 if (k == it.chunks()) {
-                    // the copy's last read is complete: the next item's state may come
-                    if (!wait(&bar.xs, (g - 1) & 1, p.err, abort)) { ok = false; break; }
+                    // the last reads of the copy's buffer are complete: the next item's state may come
+                    if (!wait(&bar.xs, (g - 1) & 1, p.err, abort) ||
+                        (kDots && !wait(&bar.upd, (g - 1) & 1, p.err, abort))) {
+                        ok = false;
+                        break;
+                    }
                     if (lane == 0) mbar_arrive(&bar.idle);
                 }
                 if (k > 0 && !write_out<kDots>(o, bar, sm, g - 1, it, k - 1, rowf_prev, 64 * wg)) {
@@ -952,7 +984,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                 }
                 if (k < it.chunks()) {
                     if (!wait(&bar.w, g & 1, p.err, abort) ||
-                        (g > 0 && !wait(&bar.stored, (g - 1) & 1, p.err, abort))) {
+                        (g > 0 && !wait(&bar.stored, (g - 1) & 1, p.err, abort)) ||
+                        (kDots && !wait(&bar.xs, g & 1, p.err, abort))) {
                         ok = false;
                         break;
                     }
@@ -961,32 +994,37 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (cols) {
                         const uint8_t* wr = sm + kSW + wg * 16384 + row * 128;
                         uint8_t* wd = sm + kSWd + wg * 16384 + row * 128;
+                        constexpr int kN = kDots ? 2 : 4;
 #pragma unroll 1
-                        for (int b = 0; b < 2; ++b) {
-                            uint4 in[4];
+                        for (int b = 0; b < 8 / kN; ++b) {
+                            uint4 in[kN];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
+                            for (int x = 0; x < kN; ++x)
                                 in[x] = *reinterpret_cast<const uint4*>(
-                                    wr + (((4 * b + x) ^ (row & 7)) << 4));
+                                    wr + (((kN * b + x) ^ (row & 7)) << 4));
                             if (dead)
 #pragma unroll
-                                for (int x = 0; x < 4; ++x) in[x] = make_uint4(0u, 0u, 0u, 0u);
+                                for (int x = 0; x < kN; ++x) in[x] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
+                            for (int x = 0; x < kN; ++x) {
                                 const uint32_t w[4] = {in[x].x, in[x].y, in[x].z, in[x].w};
-                                uint32_t hi[4], lo[4];
+                                uint32_t hi[4], lo[4], rest[4];
 #pragma unroll
                                 for (int y = 0; y < 4; ++y) {
                                     float a0 = __uint_as_float(w[y] << 16);
                                     float a1 = __uint_as_float(w[y] & 0xffff0000u);
                                     mul2(a0, a1, wf, wf);
-                                    split2(a0, a1, hi[y], lo[y]);
+                                    if (kDots) split3(a0, a1, hi[y], lo[y], rest[y]);
+                                    else split2(a0, a1, hi[y], lo[y]);
                                 }
-                                const uint32_t to = ((4 * b + x) ^ (row & 7)) << 4;
+                                const uint32_t to = ((kN * b + x) ^ (row & 7)) << 4;
                                 *reinterpret_cast<uint4*>(wd + to) =
                                     make_uint4(hi[0], hi[1], hi[2], hi[3]);
                                 *reinterpret_cast<uint4*>(wd + 32768 + to) =
                                     make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                                if (kDots)  // (in the state's copy's buffer, which has been read)
+                                    *reinterpret_cast<uint4*>(wd + (kSS - kSWd) + to) =
+                                        make_uint4(rest[0], rest[1], rest[2], rest[3]);
                             }
                         }
                     }
@@ -1507,9 +1545,7 @@ cudaError_t launch_outputs(const Problem& p, const lin::Calls& calls, int n, int
     OutParams o{};
     o.next = next;
     if (cudaError_t e = fill(o, p, calls, n, slots, rec, true)) return e;
-    bool dots = false;
-    for (int i = 0; i < n; ++i) dots = dots || calls.c[i].dot != nullptr;
-    const auto kernel = dots ? out_kernel<true> : out_kernel<false>;
+    const auto kernel = calls.c[0].dot ? out_kernel<true> : out_kernel<false>;
     if (cudaError_t e = cudaFuncSetAttribute(
             kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kOutSmem))
         return e;

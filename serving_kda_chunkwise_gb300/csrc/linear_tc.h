@@ -14,7 +14,8 @@ constexpr int kCounters = 3;
 size_t record_bytes(int64_t T, int N, int H);
 cudaError_t launch_decays(const lin::Problem& p, float* rec, unsigned* next, cudaStream_t s);
 
-// Every segment's outputs from its edge state; `next`: a zeroed counter.
+// Every segment's outputs from its edge state, of calls that all or none want dot products; `next`: a
+// zeroed counter.
 cudaError_t launch_outputs(const lin::Problem& p, const lin::Calls& calls, int n, int64_t slots,
                            const float* rec, unsigned* next, const char* name, cudaStream_t s);
 
