@@ -564,17 +564,20 @@ bool use_tc(int io_bf16) {
 }
 
 // Tokens a segment.  On the tensor cores a segment's chunks in a row cost less than its edge states
-// (two fp32 states a segment, written, read and loaded), so segments are as long as they can be
-// with one for every SM: at 8,192 tokens x 16 heads 1,024 tokens take 83 us, 512 take 89, 256 105.
-// Not beyond 2,048, where the last round's ends cost more (65,536 x 32: 838 us, with 4,096 888, with
-// 1,024 886; packed prompts up to 5,753 tokens x 16: 314, 345, 298); in the gradients not beyond 1,024, for sums over 2,048 tokens between anchors cost
-// dg's last bits (1e-5 instead of 7e-6).  Up to 512 tokens take one launch: four chunks in a row
-// take about as long as two more launches (256 x 4: 21 against 28 us, 512 x 4: 31 against 28, its
-// gradients 40 against 40, 512 x 32's 48 against 71).
+// (two fp32 states a segment, written, read and loaded), so segments are as long as they can be and
+// still be one for every SM, or for half of the SMs where the next length down would give more than
+// one to each: at 8,192 tokens x 16 heads 128 segments of 1,024 tokens take 89 us, 256 of 512 take 95,
+// 512 of 256 take 110; x 10 heads 80 of 1,024 take 79, 160 of 512 take 87.  Not beyond 2,048 tokens,
+// where the last round's ends cost more (65,536 x 32: 824 us, with 4,096 882, with 1,024 892; packed
+// prompts up to 5,753 tokens x 16, whose lengths the rule does not know: 353, 403, 337); in the
+// gradients not beyond 1,024, for the rounding between two anchors adds up in dg (65,536 x 16: 2.0e-6
+// off, with 2,048 2.4e-6 and 1,455 instead of 1,515 us).  Up to 256 tokens take no segments: two chunks
+// in a row take about as long as the edges' launch (256 x 4: 30 against 28 us, and one launch less for
+// the host; 512 x 4 in one piece 42 against 30, its gradients 71 against 50).
 // Token by token a segment is walked by as many CTAs as its state has blocks, and each SM needs
 // several to be busy: four segments an SM (2,048 + 1,531 tokens x 8 heads: 77 us, two 89, one 138).
 int segment_length(int64_t T, int H, bool tc, bool bwd) {
-    if (tc && T <= 512) return 512;
+    if (tc && T <= 256) return 256;
     int L = tc ? 128 : 64;
     const int most = tc && !bwd ? 2048 : 1024, fill = tc ? 152 : 4 * 152;
     while (L < most && T / L * H > fill) L *= 2;
