@@ -5,26 +5,28 @@
 //
 // Launches of a call over sequences longer than a segment:
 //   1. (bf16) decays: what the chunks' products need of the log decays, see linear_tc.cu;
-//   2. segment sums: each segment's own contribution to the state, and its summed log decay;
-//   3. edges: the state at every segment's edge (a scan over a sequence's segments);
-//   4. outputs: every segment from its edge state;
+//   2. segment sums: each segment's own contribution to the state, and its summed log decay; for
+//      bf16 also the states after sequences of one segment;
+//   3. edges: the state at every segment's edge (a scan over a sequence's segments) and, for bf16,
+//      after the sequence;
+//   4. outputs: every segment from its edge state (fp32: and the states after the sequences);
 //   5. (gradients) the decays'.
-// When no sequence can be longer than a segment, 2 and 3 fall away.  Each launch but the first is
-// a programmatic dependent of the one before: it is set up beside it and waits before it reads
-// what that wrote (every kernel waits, so that a launch's end is that of all before it).
+// When no sequence can be longer than a segment, 3 falls away, and 2 where no state is wanted.  With
+// S_out in S0's place the states of bf16 sequences of one segment come last, for the outputs read S0.
+// Each launch but the first is a programmatic dependent of the one before: it is set up beside it and
+// waits before it reads what that wrote (every kernel waits, so that a launch's end is that of all
+// before it).
 //
 // The gradient of g:  dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_out>.  Both dot
 // products hold the token's own term (q_s . k_s) (v_s . do_s), the only one without a decay.  It is
 // left out of both: carried along, its rounding would drown the rest where decays are strong (dg of
 // a head is of the size of e^g; at g = -10 everywhere it came out 1 % off, a fixed decay's 100 times
 // too large).  Taken over a long sequence the sum would gather the rounding of every later token.
-// At every segment's
-// edges it is <S, D>, from states that are at hand, so the sums run inside a segment, from the
-// anchor at its start: dg_t = <S, D> - sum_{s < t} (...).  What they miss the anchor at its end by
-// is their rounding, and is taken back token by token in proportion to the squares of the terms'
-// sizes, as independent errors are best shared out.  (From the
-// end they would begin, at a sequence's last token, with <S_T, dS_out>, in which that token's own
-// k v^T has no decay either.)
+// At every segment's edges it is <S, D>, from states that are at hand, so the sums run inside a
+// segment, from the anchor at its start: dg_t = <S, D> - sum_{s < t} (...).  What they miss the anchor
+// at its end by is their rounding, and is taken back token by token in proportion to the squares of
+// the terms' sizes, as independent errors are best shared out.  (From the end they would begin, at a
+// sequence's last token, with <S_T, dS_out>, in which that token's own k v^T has no decay either.)
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
@@ -47,9 +49,9 @@ using lin::Segment;
 // keep fp32 accuracy.  The state decays by S += S (e^g - 1) unless g is far below 0: e^g itself
 // rounds near 1, and one decay for all tokens would round the same way at every one of them.
 // Bound by its three (sums: two) fp32 operations per state element and token: at 65,536 tokens x
-// 16 heads x 128 the outputs take 2,229 us, 62 % of the fp32 rate, the sums 1,227 us, 76 %; at
-// 2,048 + 1,531 tokens x 8 heads, 64 x 128, 45 and 30 us (with one column a lane and no tile on
-// its way: 98 and 69 us).
+// 16 heads x 128 the outputs take 2,163 us, 64 % of the fp32 rate, the sums 1,207 us, 77 %, the three
+// of the gradients 7,543 us; at 2,048 + 1,531 tokens x 8 heads, 64 x 128, 45, 30 and 143 us (with one
+// column a lane and no tile on its way outputs and sums took 98 and 69 us).
 constexpr int kCols = 64;
 constexpr int kDotCols = 32;
 constexpr int kTile = 16;
@@ -321,9 +323,10 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
 // ------------------------------------------------------------------------ edges --
 // A thread carries four state elements over a sequence's segments, the contributions loaded
 // four segments ahead, and on to the state after the sequence where the last segment's contribution
-// is there (the token kernels form that state themselves).  Bound by that traffic, each contribution read and each edge written once,
-// and by its latency where segments are few: 20 us at 65,536 tokens x 32 heads x 128 (33 segments
-// of 2,048: 134 MB), 42 us for both directions of the gradients x 16 heads (65 of 1,024: 268 MB).
+// is there (the token kernels form that state themselves).  Bound by that traffic, each contribution
+// read and each edge written once, and by its latency where segments are few: 22 us at 65,536 tokens x
+// 32 heads x 128 (32 segments of 2,048: 134 MB), 43 us for both directions of the gradients x 16 heads
+// (64 of 1,024: 268 MB).
 struct Edges {
     const float* add[2];    // [edges][H][E] contributions: forward, reversed
     float* seg[2];          // [edges][H][E] edge states (written)
@@ -425,8 +428,8 @@ __global__ void __launch_bounds__(256) edge_kernel(const __grid_constant__ Probl
 // ----------------------------------------------------------- gradient of the decay --
 // One CTA a (segment, head): the anchors <S, D> at the segment's two edges, then the prefix sums
 // of q.dq - k.dk over its tokens, 256 at a time.  Bound by reading the edge states
-// (each anchor's twice, by the segments on both sides): 72 us at 65,536 tokens x 16 heads x 128,
-// 268 MB at 3.7 TB/s.
+// (each anchor's twice, by the segments on both sides): 57 us at 65,536 tokens x 16 heads x 128,
+// 268 MB at 4.7 TB/s.
 struct DecayGrad {
     const float *segS, *segD;        // [edges][H][E] edge states (where sequences have segments)
     const float *at_start, *at_end;  // [N][H][kAnchors] partial sums of <S, D> at the sequences'
@@ -536,7 +539,8 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
     }
 }
 
-// dg of a decay that all tokens of a head share: the sum over tokens, in a fixed order.
+// dg of a decay that all tokens of a head share: the sum over tokens, in a fixed order, by one CTA a
+// head.  Bound by its rounds' latency: 24 us at 65,536 tokens x 16 heads, 2 % of the gradients.
 __global__ void __launch_bounds__(256) decay_sum_kernel(const float* dg, int64_t T, int H,
                                                         float* out) {
     __shared__ float red[256];

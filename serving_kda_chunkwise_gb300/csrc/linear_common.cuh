@@ -45,6 +45,8 @@ struct Call {
     int tr;              // states in memory are [db][da] instead of [da][db]
     const float* edge;   // [N][H][...] state before the first (reversed: after the last) token
     const float* seg;    // [edges][H][...] state at the other segments' edges, or nullptr
+    // what follows at a sequence's end (token by token in the outputs' kernel, on the tensor cores in
+    // the segment sums' and the edges'):
     float* S_out;        // [N][H][...] state after the sequence (reversed: before it), or nullptr
     const float* anchor; // [N][H][...] states whose dot products with those after the sequences
     float* anchors;      //   are wanted, or nullptr: [N][H][kAnchors] partial sums

@@ -283,8 +283,9 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
 // slower.)
 // Bound by that chain: a chunk takes 8,900 cycles, of which the products are 4,400.  Measured at
 // 65,536 tokens x 32 heads x 128: 547 us (2.2 GB at 4.0 TB/s, 7 products of 4.2 MFLOP a chunk
-// and head at 880 TFLOP/s); gradients, 65,536 x 16, three calls: 954 us.  Items are taken as CTAs
-// come to them (packed prompts of 17 to 5,753 tokens x 16: 219 us, dealt out 262).
+// and head at 880 TFLOP/s); gradients, 65,536 x 16: 1,130 us, dq and dk with dot products and third
+// parts (9 products) and dv without.  Items are taken as CTAs come to them (packed prompts of 17 to
+// 5,753 tokens x 16: 215 us; dealt out they took a fifth longer).
 constexpr int kThreads = 640;
 constexpr int kMmaT = 19 * 32;
 constexpr uint32_t kSX = 0, kSY = 32768, kSW = 65536;
@@ -1078,15 +1079,17 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 // --------------------------------------------------------- segment sums --
 // sum_i e^{G_end - G_i} y_i w_i^T over a segment [reversed: e^{G_i} from its start]: for the scan over
 // a sequence's segments, or of a sequence that is one segment (or empty), which with the state before
-// it is the state after it.  W is decayed in
-// place (hi over W itself, lo and the third part beside it); two stages of all operands fit but for
-// the third part, which waits until the last chunk's products are done with its buffer.
+// it is the state after it.  W is decayed in place (hi over W itself, lo and the third part beside it);
+// two stages of all operands fit but for the third part, which waits until the last chunk's products
+// are done with its buffer.
 // A tensor core adds to its accumulator by truncation, 4e-8 of it a step: the small parts have an
 // accumulator of their own, the chunks take turns at three for hi, and the walk is towards the edge
 // that the weights refer to, so that what counts most comes last.  (Away from it, into one accumulator
 // for all parts, with two parts of W: <S, D> of heads that remember a thousand tokens was 1e-5 off.)
-// Bound by reading Y and W: 209 us at 65,536 tokens x 32 heads x 128, 1.07 GB at 5.1 TB/s (without the
-// conversion 176 us; a third stage for Y and W gained nothing).
+// Bound by reading Y and W, and by the conversion of W between a stage's load and its products: 241 us
+// at 65,536 tokens x 32 heads x 128, 1.07 GB at 4.5 TB/s (with two parts of W 209 us, without the
+// conversion 176); packed prompts with states 108 us; 256 x 300 tokens x 32 heads with states, where
+// an item is three chunks and a state in and out, 541 us, 2.3 GB at 4.3 TB/s.
 constexpr int kSumThreads = 640;
 constexpr uint32_t kUY = 0, kUW = 32768, kULo = 65536, kUStage = 98304;  // two stages
 constexpr uint32_t kUThird = 2 * kUStage;

@@ -15,8 +15,9 @@
 // groups of 1 or 2 times that many rows, the next group's rows on their way while one is worked
 // on: the token's position and its row of the table, two dependent loads, are then paid once a
 // task.
-// Bound by memory and, next, by the instructions (2.6 issued a cycle): 65,536 tokens x 40 heads x
-// 128 in bf16 253 us, 1.34 GB at 5.3 TB/s; gradients, 32,768 x 32 heads, 184 us, 0.8 GB at 4.4.
+// Bound by memory and, next, by the instructions (2.5 issued a cycle): 65,536 tokens x 40 heads x
+// 128 in bf16 253 us, 1.34 GB at 5.3 TB/s, in fp32 414 us at 6.5.  The gradients by the loads' latency
+// (126 registers: a quarter of the warps): 32,768 x 32 heads 184 us, 0.8 GB at 4.4; fp32 289 us at 5.6.
 // All sums and the rotation are fp32; the only rounding to fewer bits is that of the result.
 // y may be x: a lane reads its 8 channels before it writes them and no other lane reads them.
 #include "kda_common.cuh"
