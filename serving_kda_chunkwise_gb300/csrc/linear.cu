@@ -11,22 +11,23 @@
 //      after the sequence;
 //   4. outputs: every segment from its edge state (fp32: and the states after the sequences);
 //   5. (gradients) the decays'.
-// When no sequence can be longer than a segment, 3 falls away, and 2 where no state is wanted.  With
-// S_out in S0's place the states of bf16 sequences of one segment come last, for the outputs read S0.
-// Each launch but the first is a programmatic dependent of the one before: it is set up beside it and
-// waits before it reads what that wrote (every kernel waits, so that a launch's end is that of all
-// before it).
+// When no sequence can be longer than a segment, 3 falls away, and 2 where no state is wanted.
+// With S_out in S0's place the states of bf16 sequences of one segment come last, for the outputs
+// read S0. Each launch but the first is a programmatic dependent of the one before: it is set up
+// beside it and waits before it reads what that wrote (every kernel waits, so that a launch's end
+// is that of all before it).
 //
 // The gradient of g:  dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, dS_out>.  Both dot
 // products hold the token's own term (q_s . k_s) (v_s . do_s), the only one without a decay.  It is
 // left out of both: carried along, its rounding would drown the rest where decays are strong (dg of
-// a head is of the size of e^g; at g = -10 everywhere it came out 1 % off, a fixed decay's 100 times
-// too large).  Taken over a long sequence the sum would gather the rounding of every later token.
-// At every segment's edges it is <S, D>, from states that are at hand, so the sums run inside a
-// segment, from the anchor at its start: dg_t = <S, D> - sum_{s < t} (...).  What they miss the anchor
-// at its end by is their rounding, and is taken back token by token in proportion to the squares of
-// the terms' sizes, as independent errors are best shared out.  (From the end they would begin, at a
-// sequence's last token, with <S_T, dS_out>, in which that token's own k v^T has no decay either.)
+// a head is of the size of e^g; at g = -10 everywhere it came out 1 % off, a fixed decay's 100
+// times too large).  Taken over a long sequence the sum would gather the rounding of every later
+// token. At every segment's edges it is <S, D>, from states that are at hand, so the sums run
+// inside a segment, from the anchor at its start: dg_t = <S, D> - sum_{s < t} (...).  What they
+// miss the anchor at its end by is their rounding, and is taken back token by token in proportion
+// to the squares of the terms' sizes, as independent errors are best shared out.  (From the end
+// they would begin, at a sequence's last token, with <S_T, dS_out>, in which that token's own k v^T
+// has no decay either.)
 #include <algorithm>
 #include <cstdlib>
 #include <cstring>
@@ -47,10 +48,10 @@ using lin::Segment;
 // a quarter of the rows, in pairs) and walks the segment's tokens, 16 at a time through shared
 // memory, the next 16 on their way in registers meanwhile.  fp32 throughout, so that fp32 inputs
 // keep fp32 accuracy.  The state decays by S += S (e^g - 1) unless g is far below 0: e^g itself
-// rounds near 1, and one decay for all tokens would round the same way at every one of them.
-// Bound by its three (sums: two) fp32 operations per state element and token: at 65,536 tokens x
-// 16 heads x 128 the outputs take 2,163 us, 64 % of the fp32 rate, the sums 1,207 us, 77 %, the three
-// of the gradients 7,543 us; at 2,048 + 1,531 tokens x 8 heads, 64 x 128, 45, 30 and 143 us (with one
+// rounds near 1, and one decay for all tokens would round the same way at every one of them. Bound
+// by its three (sums: two) fp32 operations per state element and token: at 65,536 tokens x 16 heads
+// x 128 the outputs take 2,163 us, 64 % of the fp32 rate, the sums 1,207 us, 77 %, the three of the
+// gradients 7,543 us; at 2,048 + 1,531 tokens x 8 heads, 64 x 128, 45, 30 and 143 us (with one
 // column a lane and no tile on its way outputs and sums took 98 and 69 us).
 constexpr int kCols = 64;
 constexpr int kDotCols = 32;
@@ -321,12 +322,12 @@ __global__ void __launch_bounds__(128) token_kernel(const __grid_constant__ Prob
 }
 
 // ------------------------------------------------------------------------ edges --
-// A thread carries four state elements over a sequence's segments, the contributions loaded
-// four segments ahead, and on to the state after the sequence where the last segment's contribution
-// is there (the token kernels form that state themselves).  Bound by that traffic, each contribution
-// read and each edge written once, and by its latency where segments are few: 22 us at 65,536 tokens x
-// 32 heads x 128 (32 segments of 2,048: 134 MB), 43 us for both directions of the gradients x 16 heads
-// (64 of 1,024: 268 MB).
+// A thread carries four state elements over a sequence's segments, the contributions loaded four
+// segments ahead, and on to the state after the sequence where the last segment's contribution is
+// there (the token kernels form that state themselves).  Bound by that traffic, each contribution
+// read and each edge written once, and by its latency where segments are few: 22 us at 65,536
+// tokens x 32 heads x 128 (32 segments of 2,048: 134 MB), 43 us for both directions of the
+// gradients x 16 heads (64 of 1,024: 268 MB).
 struct Edges {
     const float* add[2];    // [edges][H][E] contributions: forward, reversed
     float* seg[2];          // [edges][H][E] edge states (written)
@@ -539,8 +540,8 @@ __global__ void __launch_bounds__(256) decay_grad_kernel(const __grid_constant__
     }
 }
 
-// dg of a decay that all tokens of a head share: the sum over tokens, in a fixed order, by one CTA a
-// head.  Bound by its rounds' latency: 24 us at 65,536 tokens x 16 heads, 2 % of the gradients.
+// dg of a decay that all tokens of a head share: the sum over tokens, in a fixed order, by one CTA
+// a head.  Bound by its rounds' latency: 24 us at 65,536 tokens x 16 heads, 2 % of the gradients.
 __global__ void __launch_bounds__(256) decay_sum_kernel(const float* dg, int64_t T, int H,
                                                         float* out) {
     __shared__ float red[256];
@@ -570,16 +571,17 @@ bool use_tc(int io_bf16) {
 // Tokens a segment.  On the tensor cores a segment's chunks in a row cost less than its edge states
 // (two fp32 states a segment, written, read and loaded), so segments are as long as they can be and
 // still be one for every SM, or for half of the SMs where the next length down would give more than
-// one to each: at 8,192 tokens x 16 heads 128 segments of 1,024 tokens take 89 us, 256 of 512 take 95,
-// 512 of 256 take 110; x 10 heads 80 of 1,024 take 79, 160 of 512 take 87.  Not beyond 2,048 tokens,
-// where the last round's ends cost more (65,536 x 32: 824 us, with 4,096 882, with 1,024 892; packed
-// prompts up to 5,753 tokens x 16, whose lengths the rule does not know: 353, 403, 337); in the
-// gradients not beyond 1,024, for the rounding between two anchors adds up in dg (65,536 x 16: 2.0e-6
-// off, with 2,048 2.4e-6 and 1,455 instead of 1,515 us).  Up to 256 tokens take no segments: two chunks
-// in a row take about as long as the edges' launch (256 x 4: 30 against 28 us, and one launch less for
-// the host; 512 x 4 in one piece 42 against 30, its gradients 71 against 50).
-// Token by token a segment is walked by as many CTAs as its state has blocks, and each SM needs
-// several to be busy: four segments an SM (2,048 + 1,531 tokens x 8 heads: 77 us, two 89, one 138).
+// one to each: at 8,192 tokens x 16 heads 128 segments of 1,024 tokens take 89 us, 256 of 512 take
+// 95, 512 of 256 take 110; x 10 heads 80 of 1,024 take 79, 160 of 512 take 87.  Not beyond 2,048
+// tokens, where the last round's ends cost more (65,536 x 32: 824 us, with 4,096 882, with 1,024
+// 892; packed prompts up to 5,753 tokens x 16, whose lengths the rule does not know: 353, 403,
+// 337); in the gradients not beyond 1,024, for the rounding between two anchors adds up in dg
+// (65,536 x 16: 2.0e-6 off, with 2,048 2.4e-6 and 1,455 instead of 1,515 us).  Up to 256 tokens
+// take no segments: two chunks in a row take about as long as the edges' launch (256 x 4: 30
+// against 28 us, and one launch less for the host; 512 x 4 in one piece 42 against 30, its
+// gradients 71 against 50). Token by token a segment is walked by as many CTAs as its state has
+// blocks, and each SM needs several to be busy: four segments an SM (2,048 + 1,531 tokens x 8
+// heads: 77 us, two 89, one 138).
 int segment_length(int64_t T, int H, bool tc, bool bwd) {
     if (tc && T <= 256) return 256;
     int L = tc ? 128 : 64;

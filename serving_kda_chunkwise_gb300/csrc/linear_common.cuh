@@ -8,14 +8,14 @@
 //   o  = forward (x, y, w) = (q, k, v)          dq = forward (do, v, k)  (states transposed)
 //   dv = reversed (k, q, do)                    dk = reversed (v, do, q) (states transposed)
 //
-// Segments.  The recurrence is linear, so a sequence is cut into segments of L tokens that run
-// in parallel once the state at each segment's edge is known.  Slot base(n) + s holds segment
-// s of sequence n, with base(n) = floor(cu[n] / L) + n: consecutive bases are at least
-// ceil(len / L) apart, so a slot finds its sequence from cu_seqlens alone and no launch has to
-// lay out a table.  Slots past a sequence's last segment are empty.
-// Only sequences of more than one segment have states at segments' edges.  Where sequences are
-// many these lie more closely: from floor(2 cu[n] / L) on, for ceil(len / L) <= floor(2 len / L) where
-// len > L, so that 2 T / L slots hold them however many sequences there are.
+// Segments.  The recurrence is linear, so a sequence is cut into segments of L tokens that run in
+// parallel once the state at each segment's edge is known.  Slot base(n) + s holds segment s of
+// sequence n, with base(n) = floor(cu[n] / L) + n: consecutive bases are at least ceil(len / L)
+// apart, so a slot finds its sequence from cu_seqlens alone and no launch has to lay out a table.
+// Slots past a sequence's last segment are empty. Only sequences of more than one segment have
+// states at segments' edges.  Where sequences are many these lie more closely: from floor(2 cu[n] /
+// L) on, for ceil(len / L) <= floor(2 len / L) where len > L, so that 2 T / L slots hold them
+// however many sequences there are.
 #pragma once
 
 #include "kda_common.cuh"
@@ -45,8 +45,8 @@ struct Call {
     int tr;              // states in memory are [db][da] instead of [da][db]
     const float* edge;   // [N][H][...] state before the first (reversed: after the last) token
     const float* seg;    // [edges][H][...] state at the other segments' edges, or nullptr
-    // what follows at a sequence's end (token by token in the outputs' kernel, on the tensor cores in
-    // the segment sums' and the edges'):
+    // what follows at a sequence's end (token by token in the outputs' kernel, on the tensor cores
+    // in the segment sums' and the edges'):
     float* S_out;        // [N][H][...] state after the sequence (reversed: before it), or nullptr
     const float* anchor; // [N][H][...] states whose dot products with those after the sequences
     float* anchors;      //   are wanted, or nullptr: [N][H][kAnchors] partial sums

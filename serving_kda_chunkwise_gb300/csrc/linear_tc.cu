@@ -12,16 +12,15 @@
 // outputs A, S and the decayed W are held as bf16 hi + lo (16 bits of mantissa, 2^-17) in two
 // products each, which is lost in the rounding of the outputs to bf16.  Where fp32 results come of
 // them there is a third part, for fp32's 24 bits: of S and the decayed W in the calls whose dot
-// products make up the decay's gradient (dg of 65,536 x 16: 2.0e-6 off, with two parts 4.3e-6; a third
-// part of A finds no room, and costs heads of short memory 3e-6), and of the decayed W in the segment
-// sums, which form all states that are results or that segments start from (2e-7 off; with two
-// parts 2.5e-6).
-// No decay is formed as a quotient or as a difference of long sums: with P and U a token's
-// prefix and suffix sums inside its block of 32 tokens and B the blocks' sums, every exponent is
-// a sum of terms of one sign except inside a diagonal block, where the difference of prefix sums
-// is taken on sums kept in two floats.  So nothing overflows, strong decays underflow to zero,
-// and a strong token does not cost the weak ones behind it their precision.  A log2 decay below
-// -2000 is taken as -2000 (2^-2000 is zero in fp32), which makes g = -inf an exact reset.
+// products make up the decay's gradient (dg of 65,536 x 16: 2.0e-6 off, with two parts 4.3e-6; a
+// third part of A finds no room, and costs heads of short memory 3e-6), and of the decayed W in the
+// segment sums, which form all states that are results or that segments start from (2e-7 off; with
+// two parts 2.5e-6). No decay is formed as a quotient or as a difference of long sums: with P and U
+// a token's prefix and suffix sums inside its block of 32 tokens and B the blocks' sums, every
+// exponent is a sum of terms of one sign except inside a diagonal block, where the difference of
+// prefix sums is taken on sums kept in two floats.  So nothing overflows, strong decays underflow
+// to zero, and a strong token does not cost the weak ones behind it their precision.  A log2 decay
+// below -2000 is taken as -2000 (2^-2000 is zero in fp32), which makes g = -inf an exact reset.
 #include <cuda.h>
 
 #include "linear_common.cuh"
@@ -255,8 +254,8 @@ __global__ void __launch_bounds__(256) decay_kernel(const __grid_constant__ Prob
         r[kRHead + i] = ex2f(P[b] + before[b]);
         r[kRTail + i] = ex2f(U[b] + after[b]);
         r[kRCol + i] = ex2f(U[b]);
-        // (2^-lo and 2^lo: a factor of the diagonal block is up to 2^24 and its product with a row's
-        // about 1, so that the rounding of P would be seen)
+        // (2^-lo and 2^lo: a factor of the diagonal block is up to 2^24 and its product with a
+        // row's about 1, so that the rounding of P would be seen)
         const float lo = 0.6931471805599453f * Plo[b];
         r[kRCol + 128 + i] = ex2f(-P[b]) * (1.f - lo);
         r[kRCol + kRDir + i] = r[kRCol + kRDir + 128 + i] = ex2f(P[b]) * (1.f + lo);
@@ -361,8 +360,8 @@ __device__ __forceinline__ void put_item(const OutParams& o, const Item& t, View
     w.v[View::kState] = (t.sg.count > 1 ? t.sg.edge : t.sg.n) * o.p.H + t.h;
 }
 
-// One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each once
-// the last chunk's buffer has been read.  Returns the number of chunks loaded.
+// One operand's loads (0: X and the decays, 1: Y, 2: W), by one thread: chunk after chunk, each
+// once the last chunk's buffer has been read.  Returns the number of chunks loaded.
 template <bool kDots>
 __device__ __noinline__ int load_operand(const OutParams& o, OutBars& bar, int which, uint8_t* sm) {
     const CUtensorMap* maps = which == 0 ? o.x : which == 1 ? o.y : o.w;
@@ -598,10 +597,10 @@ __device__ __forceinline__ bool write_out(const OutParams& o, OutBars& bar, uint
     return true;
 }
 
-// kDots: the calls want their outputs' dot products, and have third parts of the state's copy and of
-// the decayed W.  Those have no buffers of their own: the copy's lies in the decayed W's lo part's
-// until X S is done, W's then in the copy's.  (Calls without them are launched on their own: in one
-// kernel for both, 1,319 us against 1,130 for the gradients of 65,536 x 16.)
+// kDots: the calls want their outputs' dot products, and have third parts of the state's copy and
+// of the decayed W.  Those have no buffers of their own: the copy's lies in the decayed W's lo
+// part's until X S is done, W's then in the copy's.  (Calls without them are launched on their own:
+// in one kernel for both, 1,319 us against 1,130 for the gradients of 65,536 x 16.)
 template <bool kDots>
 __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant__ OutParams o) {
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -759,9 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
             if (!wait(&bar.item[n & 1], (n >> 1) & 1, p.err, abort)) break;
             const View it = view(sm, n);
             if (it.chunks() < 0) break;
-            // the row's factor in the diagonal block, which is a column's of the other direction, and
-            // its sum to the edge of the block that it looks to, loaded a chunk ahead (from memory
-            // they take 2500 cycles)
+            // the row's factor in the diagonal block, which is a column's of the other direction,
+            // and its sum to the edge of the block that it looks to, loaded a chunk ahead (from
+            // memory they take 2500 cycles)
             float diag_next = 0.f, edge_next = 0.f;
             if (it.chunks()) {
                 const float* r = it.record(o, 0);
@@ -971,7 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
                     if (lane == 0) mbar_arrive(&bar.s);
                 }
                 if (k == it.chunks()) {
-                    // the last reads of the copy's buffer are complete: the next item's state may come
+                    // the last reads of the copy's buffer are complete: the next item's state may
+                    // come
                     if (!wait(&bar.xs, (g - 1) & 1, p.err, abort) ||
                         (kDots && !wait(&bar.upd, (g - 1) & 1, p.err, abort))) {
                         ok = false;
@@ -1077,19 +1077,19 @@ __global__ void __launch_bounds__(kThreads, 1) out_kernel(const __grid_constant_
 }
 
 // --------------------------------------------------------- segment sums --
-// sum_i e^{G_end - G_i} y_i w_i^T over a segment [reversed: e^{G_i} from its start]: for the scan over
-// a sequence's segments, or of a sequence that is one segment (or empty), which with the state before
-// it is the state after it.  W is decayed in place (hi over W itself, lo and the third part beside it);
-// two stages of all operands fit but for the third part, which waits until the last chunk's products
-// are done with its buffer.
-// A tensor core adds to its accumulator by truncation, 4e-8 of it a step: the small parts have an
-// accumulator of their own, the chunks take turns at three for hi, and the walk is towards the edge
-// that the weights refer to, so that what counts most comes last.  (Away from it, into one accumulator
-// for all parts, with two parts of W: <S, D> of heads that remember a thousand tokens was 1e-5 off.)
-// Bound by reading Y and W, and by the conversion of W between a stage's load and its products: 241 us
-// at 65,536 tokens x 32 heads x 128, 1.07 GB at 4.5 TB/s (with two parts of W 209 us, without the
-// conversion 176); packed prompts with states 108 us; 256 x 300 tokens x 32 heads with states, where
-// an item is three chunks and a state in and out, 541 us, 2.3 GB at 4.3 TB/s.
+// sum_i e^{G_end - G_i} y_i w_i^T over a segment [reversed: e^{G_i} from its start]: for the scan
+// over a sequence's segments, or of a sequence that is one segment (or empty), which with the state
+// before it is the state after it.  W is decayed in place (hi over W itself, lo and the third part
+// beside it); two stages of all operands fit but for the third part, which waits until the last
+// chunk's products are done with its buffer. A tensor core adds to its accumulator by truncation,
+// 4e-8 of it a step: the small parts have an accumulator of their own, the chunks take turns at
+// three for hi, and the walk is towards the edge that the weights refer to, so that what counts
+// most comes last.  (Away from it, into one accumulator for all parts, with two parts of W: <S, D>
+// of heads that remember a thousand tokens was 1e-5 off.) Bound by reading Y and W, and by the
+// conversion of W between a stage's load and its products: 241 us at 65,536 tokens x 32 heads x
+// 128, 1.07 GB at 4.5 TB/s (with two parts of W 209 us, without the conversion 176); packed prompts
+// with states 108 us; 256 x 300 tokens x 32 heads with states, where an item is three chunks and a
+// state in and out, 541 us, 2.3 GB at 4.3 TB/s.
 constexpr int kSumThreads = 640;
 constexpr uint32_t kUY = 0, kUW = 32768, kULo = 65536, kUStage = 98304;  // two stages
 constexpr uint32_t kUThird = 2 * kUStage;
@@ -1346,9 +1346,9 @@ __global__ void __launch_bounds__(kSumThreads, 1) sum_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(&bar.wd[st]);
             }
             if (!ok || !(ok = open(n + 1))) break;
-            // The warp's piece of the state: 32 rows x 32 columns, a row a lane in TMEM, four rows an
-            // access in memory (where rows lie 4 db bytes apart).  It passes through what the warp
-            // itself writes of both stages' lo buffers, 64 bytes of its rows in each.
+            // The warp's piece of the state: 32 rows x 32 columns, a row a lane in TMEM, four rows
+            // an access in memory (where rows lie 4 db bytes apart).  It passes through what the
+            // warp itself writes of both stages' lo buffers, 64 bytes of its rows in each.
             const bool piece = cols && 32 * q < c.da, single = !it.v[View::kSeg];
             const int64_t E = (int64_t)c.da * c.db;
             const int64_t at0 = (int64_t)(32 * q + (lane >> 3)) * c.db + 32 * cg + 4 * (lane & 7);

@@ -1,15 +1,15 @@
 """The decay's gradient of the linear attention, head by head: a head whose decay is strong has a
 gradient of the size of e^g, far below the others', so one norm over all heads would not see it.
 
-Tolerances, relative to the head's 2-norm.  dg is a running sum over up to 1,024 tokens of the
+Tolerances, relative to the head's 2-norm. dg is a running sum over up to 1,024 tokens of the
 difference of two dot products, each a sum of terms of dg's own size, pinned to the right value at
 both ends; of independent errors of such a sum, sqrt(1024 / 6) = 13 times one term's remains on
-average.  bf16: a term carries up to three operands held to 2^-17 (2.4e-6 in the mean each, 4e-6 together), two
-dot products: 13 * 1.4 * 4e-6 = 7.5e-5, taken as 1e-4.  fp32: 1e-7 a dot product of 128 terms, 2e-6, and
-as much again for the running sum in fp32: taken as 1e-5.  A fixed decay's gradient is the sum over
-T tokens of these: the errors of neighbours are alike, and 1024^1.5 / sqrt(12) / sqrt(1024) = 300 times
-a term's remains beside the norm: bf16 300 * 1.4 * 4e-6 = 1.7e-3, taken as 2e-3; fp32 4e-5, taken as 1e-4.
-"""
+average. bf16: a term carries up to three operands held to 2^-17 (2.4e-6 in the mean each, 4e-6
+together), two dot products: 13 * 1.4 * 4e-6 = 7.5e-5, taken as 1e-4. fp32: 1e-7 a dot product of
+128 terms, 2e-6, and as much again for the running sum in fp32: taken as 1e-5. A fixed decay's
+gradient is the sum over T tokens of these: the errors of neighbours are alike, and 1024^1.5 /
+sqrt(12) / sqrt(1024) = 300 times a term's remains beside the norm: bf16 300 * 1.4 * 4e-6 = 1.7e-3,
+taken as 2e-3; fp32 4e-5, taken as 1e-4."""
 import pytest
 
 pytestmark = pytest.mark.gpu

@@ -1,11 +1,11 @@
-"""The decay's gradient of bf16 inputs is an fp32 result: each head within 4e-6 of 64 bits (2-norm), over
-memories from a few tokens to some hundreds.
+"""The decay's gradient of bf16 inputs is an fp32 result: each head within 4e-6 of 64 bits (2-norm),
+over memories from a few tokens to some hundreds.
 
-What is held in fewer bits than fp32 is A, as bf16 hi + lo, 2.4e-6 of a term in the mean; a gradient of a
-head that remembers few tokens is made of few terms, so that this stays (with the decays' 2^-22, 3e-6),
-and averages out where it is made of many.  There the tensor core's truncated additions count: 4.3e-8
-of a state each, 24 a chunk of 128 tokens; over a memory of 300 tokens half of 56 of them, 1.2e-6, in S and
-in D: 1.7e-6.  Both together 3.5e-6."""
+What is held in fewer bits than fp32 is A, as bf16 hi + lo, 2.4e-6 of a term in the mean; a
+gradient of a head that remembers few tokens is made of few terms, so that this stays (with the
+decays' 2^-22, 3e-6), and averages out where it is made of many. There the tensor core's truncated
+additions count: 4.3e-8 of a state each, 24 a chunk of 128 tokens; over a memory of 300 tokens half
+of 56 of them, 1.2e-6, in S and in D: 1.7e-6. Both together 3.5e-6."""
 import pytest
 
 pytestmark = pytest.mark.gpu

@@ -1,12 +1,12 @@
 """States of bf16 inputs are fp32 results: S_out and dS0 within 1e-6 of 64 bits (2-norm), however long
 the sequence and however weak the decay.
 
-A product of two bf16 numbers is exact in fp32; each decay carries about 2e-7 (2^x to 2^-22), different
-for every token.  A tensor core's addition truncates, 4.3e-8 of the sum in the mean, towards zero; a
-segment of 2,048 tokens is 128 such additions in turns to three accumulators, 43 each, at which a sum
-of random terms has half its final size in the mean square: 43 / 2 * 4.3e-8 = 9e-7 where nothing decays,
-less where it does.  Segments are joined by rounding fp32 operations (6e-8 each, either way).
-"""
+A product of two bf16 numbers is exact in fp32; each decay carries about 2e-7 (2^x to 2^-22),
+different for every token. A tensor core's addition truncates, 4.3e-8 of the sum in the mean,
+towards zero; a segment of 2,048 tokens is 128 such additions in turns to three accumulators, 43
+each, at which a sum of random terms has half its final size in the mean square: 43 / 2 * 4.3e-8 =
+9e-7 where nothing decays, less where it does. Segments are joined by rounding fp32 operations
+(6e-8 each, either way)."""
 import pytest
 
 pytestmark = pytest.mark.gpu
