@@ -336,6 +336,146 @@ kda_status_t kda_qk_norm_rope_bwd(const void *q, int64_t q_ld, const void *k, in
                                   kda_stream_t stream);
 
 /*
+ * The gated recurrence of single channels (the sibling of KDA whose state is one number a channel),
+ * per sequence and channel c, with KDA's lower-bounded gate:
+ *     g_t = g_min Sigmoid(e^{A_log[c]} z_t)
+ *     h_t = e^{g_t} h_{t-1} + sqrt(1 - e^{2 g_t}) Sigmoid(i_t) x_t          y_t = h_t
+ * Additional conventions of these entry points:
+ *   - x, z, i and dy are [T, D] io_dt with a token stride of ld elements (ld >= D, a multiple of 16
+ *     bytes), so views of a fused projection's output can be passed as they are; every tensor
+ *     written is contiguous.  D is a multiple of 8 (KDA_ERR_UNSUPPORTED otherwise).
+ *   - A_log [D], the states [N, D] and the edges are fp32.
+ *   - z = -inf leaves the state as it is (for finite x), z = +inf decays it by e^{g_min}.  A token
+ *     whose input is not finite spoils its channel of its sequence from there on (the gradients also
+ *     before it), and nothing else but the sum dA_log.
+ *   - slots need 4-byte alignment only.
+ *   - No output may overlap an input, except h_out, which may be the same buffer as h0.
+ */
+
+/*
+ * kda_recurrence_fwd -- the forward over N packed sequences.
+ *   h0     : [N, D] initial states, or NULL for zeros
+ *   h_out  : [N, D] final states (written), or NULL
+ *   cu_seqlens, N, T_total : as kda_fwd_chunked (a sequence may be empty: its h_out is its h0)
+ *   y      : [T_total, D] io_dt (written)
+ *   edges  : [ceil(T_total / 64), D] (written), or NULL: row j is the state that token 64 j starts
+ *            from.  kda_recurrence_bwd takes it and is then spared a pass over the inputs.
+ *   workspace : device scratch of kda_recurrence_fwd_workspace_size(...) bytes (NULL when 0)
+ */
+size_t kda_recurrence_fwd_workspace_size(int64_t T_total, int N, int D);
+kda_status_t kda_recurrence_fwd(const void *x, int64_t x_ld, const void *z, int64_t z_ld,
+                                const void *i, int64_t i_ld, const float *A_log, float g_min,
+                                const float *h0, float *h_out, const int32_t *cu_seqlens, int N,
+                                int64_t T_total, int D, kda_dtype_t io_dt, void *y, float *edges,
+                                void *workspace, size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * kda_recurrence_bwd -- gradients of kda_recurrence_fwd's outputs.  For a loss with gradient
+ * dy [T_total, D] io_dt on y and dh_out [N, D] (or NULL) on h_out, with
+ * l_t = dL/dh_t running backwards (l_t = dy_t + e^{g_{t+1}} l_{t+1}, dh_out added at the end) and
+ * m = sqrt(1 - e^{2g}), writes
+ *   dx = l m Sigmoid(i),  di = dx x (1 - Sigmoid(i)),
+ *   dz = l (e^g h_{t-1} - e^{2g} / m Sigmoid(i) x) g (1 - Sigmoid(e^A z)) e^A
+ *            : [T_total, D] io_dt
+ *   dA_log   : [D] (summed over all tokens), or NULL when not wanted
+ *   dh0      : [N, D], or NULL when not wanted
+ *   edges    : what the forward of the same inputs wrote, or NULL (formed again from x, z and i)
+ * N = 0 (no sequences) is a batch like any other.  Deterministic.
+ */
+size_t kda_recurrence_bwd_workspace_size(int64_t T_total, int N, int D);
+kda_status_t kda_recurrence_bwd(const void *x, int64_t x_ld, const void *z, int64_t z_ld,
+                                const void *i, int64_t i_ld, const float *A_log, float g_min,
+                                const float *h0, const int32_t *cu_seqlens, int N,
+                                int64_t T_total, int D, kda_dtype_t io_dt, const void *dy,
+                                int64_t dy_ld, const float *dh_out, const float *edges, void *dx,
+                                void *dz, void *di, float *dA_log, float *dh0, void *workspace,
+                                size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * kda_recurrence_bwd_packed -- the same gradients from inputs that were kept by
+ * kda_checkpoint_pack: what kda_recurrence_bwd gives (without edges) for x, z and i brought back
+ * in fp32.  io_dt is the type of dy and of the gradients.
+ */
+kda_status_t kda_recurrence_bwd_packed(const int8_t *x_codes, const int8_t *x_exps,
+                                       const int8_t *z_codes, const int8_t *z_exps,
+                                       const int8_t *i_codes, const int8_t *i_exps,
+                                       const float *A_log, float g_min, const float *h0,
+                                       const int32_t *cu_seqlens, int N, int64_t T_total, int D,
+                                       kda_dtype_t io_dt, const void *dy, int64_t dy_ld,
+                                       const float *dh_out, void *dx, void *dz, void *di,
+                                       float *dA_log, float *dh0, void *workspace,
+                                       size_t ws_bytes, kda_stream_t stream);
+
+/*
+ * kda_recurrence_step -- one token of the recurrence for N requests, states in place.
+ *   x, z, i : one token a request ([N, D] with token strides)
+ *   h      : [n_slots, D] fp32 pool of states, read and overwritten
+ *   slots, n_slots : as kda_linear_decode_step (a negative slot marks an unused row: its y is zero)
+ *   y      : [N, D] io_dt (written)
+ */
+kda_status_t kda_recurrence_step(const void *x, int64_t x_ld, const void *z, int64_t z_ld,
+                                 const void *i, int64_t i_ld, const float *A_log, float g_min,
+                                 float *h, const int32_t *slots, int n_slots, int N, int D,
+                                 kda_dtype_t io_dt, void *y, kda_stream_t stream);
+
+/*
+ * kda_checkpoint_pack -- keeps an activation in 8 bits for the backward pass.  The 64 channels
+ * 64 j .. 64 j + 63 of a token (fewer at the end) share an exponent: the smallest e in [-127, 121]
+ * with max |x| 2^-e < 127.5, and each is kept as the integer next to x 2^-e (halves to even, limited
+ * to [-127, 127]).  Each step is exact in binary, so codes and exponents are those of the formula.
+ *   x     : [T, D] io_dt with a token stride of x_ld elements (a multiple of 16 bytes, >= D)
+ *   codes : [T, D] int8 (written)       exps : [ceil(D / 64), T] int8 (written)
+ * A group of zeros has e = -127; one that holds an infinity or a NaN has e = -128, which stands for
+ * NaN in all its channels (its codes are 0).  D is a multiple of 8.
+ */
+kda_status_t kda_checkpoint_pack(const void *x, int64_t x_ld, int64_t T, int D,
+                                 kda_dtype_t io_dt, int8_t *codes, int8_t *exps,
+                                 kda_stream_t stream);
+
+/*
+ * kda_checkpoint_unpack -- the values that codes and exponents stand for:
+ *   x : [T, D] io_dt, contiguous (written) = codes 2^e, exact in either type
+ */
+kda_status_t kda_checkpoint_unpack(const int8_t *codes, const int8_t *exps, int64_t T, int D,
+                                   kda_dtype_t io_dt, void *x, kda_stream_t stream);
+
+/*
+ * kda_block_norm -- what stands between a block's output y and the next block's input, in one pass:
+ *     n  = w_post y / sqrt(mean(y^2) + eps)          (n = y when post_norm is zero)
+ *     r' = r + scale Sigmoid(gate) n                  x' = w_pre r' / sqrt(mean(r'^2) + eps)
+ * with the means over the D channels of a token.
+ *   y, gate : [T, D] io_dt; gate may be NULL (no gate)
+ *   r       : [T, D] r_dt, the residual stream: io_dt, or KDA_F32 beside bf16 blocks
+ *   scale, w_post, w_pre : [D] fp32, or NULL for ones (w_post must be NULL when post_norm is zero)
+ *   r_out   : [T, D] r_dt (written); may be r       x_out : [T, D] io_dt (written); may be y
+ * x' is formed from r' before it is rounded to r_dt.  All tensors are contiguous.  D is a multiple
+ * of 8, at most 8192 (KDA_ERR_UNSUPPORTED otherwise).  T = 0 is a no-op.
+ */
+kda_status_t kda_block_norm(const void *y, const void *gate, const void *r, const float *scale,
+                            const float *w_post, const float *w_pre, int post_norm, float eps,
+                            void *r_out, void *x_out, int64_t T, int D, kda_dtype_t io_dt,
+                            kda_dtype_t r_dt, kda_stream_t stream);
+
+/*
+ * kda_block_norm_bwd -- its gradients, from y, gate, the residual r_out that the forward left and
+ * the gradients dx [T, D] io_dt on x_out and dr [T, D] r_dt (or NULL) on r_out:
+ *   dr_in  : [T, D] r_dt (written): the gradient of r           dy : [T, D] io_dt (written)
+ *   dgate  : [T, D] io_dt (written); NULL exactly when gate is
+ *   dscale, dw_post, dw_pre : [D] fp32, summed over tokens, or NULL when not wanted
+ *   workspace : device scratch of kda_block_norm_bwd_workspace_size(D) bytes; not needed when none
+ *            of the three sums is wanted
+ * No output may overlap an input.  Deterministic.
+ */
+size_t kda_block_norm_bwd_workspace_size(int D);
+kda_status_t kda_block_norm_bwd(const void *y, const void *gate, const void *r_out,
+                                const void *dx, const void *dr, const float *scale,
+                                const float *w_post, const float *w_pre, int post_norm, float eps,
+                                void *dr_in, void *dy, void *dgate, float *dscale, float *dw_post,
+                                float *dw_pre, int64_t T, int D, kda_dtype_t io_dt,
+                                kda_dtype_t r_dt, void *workspace, size_t ws_bytes,
+                                kda_stream_t stream);
+
+/*
  * kda_quantile_balance -- quantile-balancing update of a mixture-of-experts router's expert
  * biases ([blog] section "Quantile Balancing (QB)"; [guide] section 4.2):
  *     alpha_i   = the (k+1)-th largest of scores[i,:] + bias          (token threshold)

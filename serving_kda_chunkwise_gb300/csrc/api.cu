@@ -99,7 +99,7 @@ kda_status_t set_last_error(kda_status_t s, const char* msg) {
 
 extern "C" {
 
-int kda_version(void) { return 300; /* 0.3.0: per-head-decay linear attention, query/key norm with rotation */ }
+int kda_version(void) { return 400; /* 0.4.0: channel recurrence, 8-bit checkpoints, norms around a block */ }
 
 const char* kda_status_string(kda_status_t s) {
     switch (s) {
@@ -678,6 +678,312 @@ kda_status_t kda_qk_norm_rope_bwd(const void* q, int64_t q_ld, const void* k, in
     if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
     cudaError_t e = kda::launch_qk_norm_bwd(a);
     if (e != cudaSuccess) return cuda_fail(e, "kda_qk_norm_rope_bwd launch");
+    return KDA_OK;
+}
+
+// ------------------------------------- recurrence of single channels --
+
+static kda_status_t check_width(int D) {
+    KDA_REQUIRE(D > 0, "D=%d must be positive", D);
+    if (D % 8 != 0) return fail(KDA_ERR_UNSUPPORTED, "D=%d: only multiples of 8 are supported", D);
+    return KDA_OK;
+}
+
+static kda_status_t check_ld(int64_t ld, int D, int per16, const char* name) {
+    KDA_REQUIRE(ld >= D && ld % per16 == 0, "%s=%lld must be a multiple of %d and at least D", name,
+                (long long)ld, per16);
+    return KDA_OK;
+}
+
+// What the forward and both backward entries share, the workspace excepted.
+static kda_status_t check_recurrence(const kda::RecurrenceArgs& a, kda_dtype_t io_dt) {
+    KDA_REQUIRE(io_dt == KDA_F32 || io_dt == KDA_BF16, "io_dt=%d is not a kda_dtype_t", (int)io_dt);
+    if (kda_status_t s = check_width(a.D)) return s;
+    if (kda_status_t s = check_gmin(a.g_min)) return s;
+    if (kda_status_t s = check_packed(a.T_total, a.N, a.D, a.cu_seqlens)) return s;
+    const int per16 = io_dt == KDA_BF16 ? 8 : 4;
+    if (!a.packed) {
+        if (kda_status_t s = check_ld(a.x_ld, a.D, per16, "x_ld")) return s;
+        if (kda_status_t s = check_ld(a.z_ld, a.D, per16, "z_ld")) return s;
+        if (kda_status_t s = check_ld(a.i_ld, a.D, per16, "i_ld")) return s;
+    }
+    if (a.T_total > 0) {
+        KDA_REQUIRE_PTR(a.x, a.packed ? "x_codes" : "x");
+        KDA_REQUIRE_PTR(a.z, a.packed ? "z_codes" : "z");
+        KDA_REQUIRE_PTR(a.i, a.packed ? "i_codes" : "i");
+        if (a.packed) {
+            KDA_REQUIRE(a.x_exps != nullptr, "x_exps is NULL");
+            KDA_REQUIRE(a.z_exps != nullptr, "z_exps is NULL");
+            KDA_REQUIRE(a.i_exps != nullptr, "i_exps is NULL");
+        }
+        KDA_REQUIRE_PTR(a.A_log, "A_log");
+    }
+    KDA_OPTIONAL_PTR(a.h0, "h0");
+    KDA_OPTIONAL_PTR(a.edges, "edges");
+    return KDA_OK;
+}
+
+static kda_status_t check_workspace(const void* workspace, size_t ws_bytes, size_t need) {
+    if (need == 0) return KDA_OK;
+    KDA_REQUIRE_PTR(workspace, "workspace");
+    KDA_REQUIRE(ws_bytes >= need, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes,
+                need);
+    return KDA_OK;
+}
+
+size_t kda_recurrence_fwd_workspace_size(int64_t T_total, int N, int D) {
+    if (T_total < 0 || N <= 0 || D <= 0 || D % 8 != 0) return 0;
+    return kda::recurrence_fwd_workspace_size(T_total, N, D);
+}
+
+size_t kda_recurrence_bwd_workspace_size(int64_t T_total, int N, int D) {
+    if (T_total < 0 || N <= 0 || D <= 0 || D % 8 != 0) return 0;
+    return kda::recurrence_bwd_workspace_size(T_total, N, D);
+}
+
+kda_status_t kda_recurrence_fwd(const void* x, int64_t x_ld, const void* z, int64_t z_ld,
+                                const void* i, int64_t i_ld, const float* A_log, float g_min,
+                                const float* h0, float* h_out, const int32_t* cu_seqlens, int N,
+                                int64_t T_total, int D, kda_dtype_t io_dt, void* y, float* edges,
+                                void* workspace, size_t ws_bytes, kda_stream_t stream) {
+    t_last_error.clear();
+    kda::RecurrenceArgs a{};
+    a.x = x; a.x_ld = x_ld; a.z = z; a.z_ld = z_ld; a.i = i; a.i_ld = i_ld; a.A_log = A_log;
+    a.g_min = g_min; a.h0 = h0; a.h_out = h_out; a.cu_seqlens = cu_seqlens; a.N = N;
+    a.T_total = T_total; a.D = D; a.io_bf16 = io_dt == KDA_BF16; a.y = y; a.edges = edges;
+    a.workspace = workspace; a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (kda_status_t s = check_recurrence(a, io_dt)) return s;
+    if (N == 0) return KDA_OK;
+    if (T_total > 0) KDA_REQUIRE_PTR(y, "y");
+    KDA_OPTIONAL_PTR(h_out, "h_out");
+    if (kda_status_t s = check_workspace(workspace, ws_bytes,
+                                         kda_recurrence_fwd_workspace_size(T_total, N, D)))
+        return s;
+    a.dev_err = device_error_ptr();
+    if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_recurrence_fwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_recurrence_fwd launch");
+    return KDA_OK;
+}
+
+static kda_status_t recurrence_bwd(kda::RecurrenceArgs& a, kda_dtype_t io_dt, size_t ws_bytes,
+                                   const char* where) {
+    if (kda_status_t s = check_recurrence(a, io_dt)) return s;
+    if (kda_status_t s = check_ld(a.dy_ld, a.D, io_dt == KDA_BF16 ? 8 : 4, "dy_ld")) return s;
+    if (a.T_total > 0) {
+        KDA_REQUIRE_PTR(a.dy, "dy");
+        KDA_REQUIRE_PTR(a.dx, "dx");
+        KDA_REQUIRE_PTR(a.dz, "dz");
+        KDA_REQUIRE_PTR(a.di, "di");
+    }
+    KDA_OPTIONAL_PTR(a.dh_out, "dh_out");
+    KDA_OPTIONAL_PTR(a.dA_log, "dA_log");
+    KDA_OPTIONAL_PTR(a.dh0, "dh0");
+    if (a.N == 0) {  // (A_log, which all tokens share, has a gradient all the same)
+        if (a.dA_log == nullptr) return KDA_OK;
+        cudaError_t e = cudaMemsetAsync(a.dA_log, 0, a.D * sizeof(float), a.stream);
+        return e == cudaSuccess ? KDA_OK : cuda_fail(e, where);
+    }
+    if (kda_status_t s = check_workspace(
+            a.workspace, ws_bytes, kda_recurrence_bwd_workspace_size(a.T_total, a.N, a.D)))
+        return s;
+    a.dev_err = device_error_ptr();
+    if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_recurrence_bwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, where);
+    return KDA_OK;
+}
+
+kda_status_t kda_recurrence_bwd(const void* x, int64_t x_ld, const void* z, int64_t z_ld,
+                                const void* i, int64_t i_ld, const float* A_log, float g_min,
+                                const float* h0, const int32_t* cu_seqlens, int N,
+                                int64_t T_total, int D, kda_dtype_t io_dt, const void* dy,
+                                int64_t dy_ld, const float* dh_out, const float* edges, void* dx,
+                                void* dz, void* di, float* dA_log, float* dh0, void* workspace,
+                                size_t ws_bytes, kda_stream_t stream) {
+    t_last_error.clear();
+    kda::RecurrenceArgs a{};
+    a.x = x; a.x_ld = x_ld; a.z = z; a.z_ld = z_ld; a.i = i; a.i_ld = i_ld; a.A_log = A_log;
+    a.g_min = g_min; a.h0 = h0; a.cu_seqlens = cu_seqlens; a.N = N; a.T_total = T_total; a.D = D;
+    a.io_bf16 = io_dt == KDA_BF16; a.dy = dy; a.dy_ld = dy_ld; a.dh_out = dh_out;
+    a.edges = const_cast<float*>(edges); a.dx = dx; a.dz = dz; a.di = di; a.dA_log = dA_log;
+    a.dh0 = dh0; a.workspace = workspace; a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return recurrence_bwd(a, io_dt, ws_bytes, "kda_recurrence_bwd launch");
+}
+
+kda_status_t kda_recurrence_bwd_packed(const int8_t* x_codes, const int8_t* x_exps,
+                                       const int8_t* z_codes, const int8_t* z_exps,
+                                       const int8_t* i_codes, const int8_t* i_exps,
+                                       const float* A_log, float g_min, const float* h0,
+                                       const int32_t* cu_seqlens, int N, int64_t T_total, int D,
+                                       kda_dtype_t io_dt, const void* dy, int64_t dy_ld,
+                                       const float* dh_out, void* dx, void* dz, void* di,
+                                       float* dA_log, float* dh0, void* workspace,
+                                       size_t ws_bytes, kda_stream_t stream) {
+    t_last_error.clear();
+    kda::RecurrenceArgs a{};
+    a.x = x_codes; a.z = z_codes; a.i = i_codes; a.x_ld = a.z_ld = a.i_ld = D; a.packed = 1;
+    a.x_exps = x_exps; a.z_exps = z_exps; a.i_exps = i_exps; a.A_log = A_log; a.g_min = g_min;
+    a.h0 = h0; a.cu_seqlens = cu_seqlens; a.N = N; a.T_total = T_total; a.D = D;
+    a.io_bf16 = io_dt == KDA_BF16; a.dy = dy; a.dy_ld = dy_ld; a.dh_out = dh_out; a.dx = dx;
+    a.dz = dz; a.di = di; a.dA_log = dA_log; a.dh0 = dh0; a.workspace = workspace;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    return recurrence_bwd(a, io_dt, ws_bytes, "kda_recurrence_bwd_packed launch");
+}
+
+kda_status_t kda_recurrence_step(const void* x, int64_t x_ld, const void* z, int64_t z_ld,
+                                 const void* i, int64_t i_ld, const float* A_log, float g_min,
+                                 float* h, const int32_t* slots, int n_slots, int N, int D,
+                                 kda_dtype_t io_dt, void* y, kda_stream_t stream) {
+    t_last_error.clear();
+    KDA_REQUIRE(io_dt == KDA_F32 || io_dt == KDA_BF16, "io_dt=%d is not a kda_dtype_t", (int)io_dt);
+    if (kda_status_t s = check_width(D)) return s;
+    if (kda_status_t s = check_gmin(g_min)) return s;
+    const int per16 = io_dt == KDA_BF16 ? 8 : 4;
+    if (kda_status_t s = check_ld(x_ld, D, per16, "x_ld")) return s;
+    if (kda_status_t s = check_ld(z_ld, D, per16, "z_ld")) return s;
+    if (kda_status_t s = check_ld(i_ld, D, per16, "i_ld")) return s;
+    KDA_REQUIRE(N >= 0, "N=%d must be >= 0", N);
+    KDA_REQUIRE((int64_t)N * D < (int64_t)1 << 36, "N*D=%lld is too large", (long long)N * D);
+    KDA_REQUIRE(n_slots >= 0, "n_slots=%d must be >= 0", n_slots);
+    KDA_REQUIRE(slots != nullptr || n_slots >= N, "n_slots=%d must be at least N=%d without slots",
+                n_slots, N);
+    if (N == 0) return KDA_OK;
+    KDA_REQUIRE_PTR(x, "x");
+    KDA_REQUIRE_PTR(z, "z");
+    KDA_REQUIRE_PTR(i, "i");
+    KDA_REQUIRE_PTR(A_log, "A_log");
+    KDA_REQUIRE_PTR(h, "h");
+    KDA_REQUIRE_PTR(y, "y");
+    if (slots) KDA_REQUIRE_WORDS(slots, "slots");
+    unsigned* err = device_error_ptr();
+    if (err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
+    cudaError_t e = kda::launch_recurrence_step(x, x_ld, z, z_ld, i, i_ld, A_log, g_min, h, slots,
+                                                n_slots, N, D, io_dt == KDA_BF16, y, err,
+                                                reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kda_recurrence_step launch");
+    return KDA_OK;
+}
+
+// --------------------------------------------- activations in 8 bits --
+
+static kda_status_t check_checkpoint(int64_t T, int D, kda_dtype_t io_dt) {
+    KDA_REQUIRE(io_dt == KDA_F32 || io_dt == KDA_BF16, "io_dt=%d is not a kda_dtype_t", (int)io_dt);
+    KDA_REQUIRE(T >= 0 && T < (int64_t)1 << 31, "T=%lld must be in [0, 2^31)", (long long)T);
+    return check_width(D);
+}
+
+kda_status_t kda_checkpoint_pack(const void* x, int64_t x_ld, int64_t T, int D,
+                                 kda_dtype_t io_dt, int8_t* codes, int8_t* exps,
+                                 kda_stream_t stream) {
+    t_last_error.clear();
+    if (kda_status_t s = check_checkpoint(T, D, io_dt)) return s;
+    if (kda_status_t s = check_ld(x_ld, D, io_dt == KDA_BF16 ? 8 : 4, "x_ld")) return s;
+    if (T == 0) return KDA_OK;
+    KDA_REQUIRE_PTR(x, "x");
+    KDA_REQUIRE_PTR(codes, "codes");
+    KDA_REQUIRE(exps != nullptr, "exps is NULL");
+    cudaError_t e = kda::launch_checkpoint_pack(x, x_ld, T, D, io_dt == KDA_BF16, codes, exps,
+                                                reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kda_checkpoint_pack launch");
+    return KDA_OK;
+}
+
+kda_status_t kda_checkpoint_unpack(const int8_t* codes, const int8_t* exps, int64_t T, int D,
+                                   kda_dtype_t io_dt, void* x, kda_stream_t stream) {
+    t_last_error.clear();
+    if (kda_status_t s = check_checkpoint(T, D, io_dt)) return s;
+    if (T == 0) return KDA_OK;
+    KDA_REQUIRE_PTR(codes, "codes");
+    KDA_REQUIRE(exps != nullptr, "exps is NULL");
+    KDA_REQUIRE_PTR(x, "x");
+    cudaError_t e = kda::launch_checkpoint_unpack(codes, exps, T, D, io_dt == KDA_BF16, x,
+                                                  reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kda_checkpoint_unpack launch");
+    return KDA_OK;
+}
+
+// ---------------------------------------------- norms around a block --
+
+static kda_status_t check_block_norm(const kda::BlockNormArgs& a, kda_dtype_t io_dt,
+                                     kda_dtype_t r_dt) {
+    KDA_REQUIRE(io_dt == KDA_F32 || io_dt == KDA_BF16, "io_dt=%d is not a kda_dtype_t", (int)io_dt);
+    KDA_REQUIRE(r_dt == KDA_F32 || r_dt == io_dt, "r_dt=%d must be io_dt or KDA_F32", (int)r_dt);
+    KDA_REQUIRE(a.T >= 0 && a.T < (int64_t)1 << 31, "T=%lld must be in [0, 2^31)", (long long)a.T);
+    if (kda_status_t s = check_width(a.D)) return s;
+    if (a.D > kda::kMaxBlockNormD)
+        return fail(KDA_ERR_UNSUPPORTED, "D=%d: at most %d is supported", a.D, kda::kMaxBlockNormD);
+    KDA_REQUIRE(a.eps >= 0.f && std::isfinite(a.eps), "eps=%g must be finite and >= 0",
+                (double)a.eps);
+    KDA_REQUIRE(a.post_norm || a.w_post == nullptr, "w_post must be NULL without a post-norm");
+    KDA_OPTIONAL_PTR(a.gate, "gate");
+    KDA_OPTIONAL_PTR(a.scale, "scale");
+    KDA_OPTIONAL_PTR(a.w_post, "w_post");
+    KDA_OPTIONAL_PTR(a.w_pre, "w_pre");
+    return KDA_OK;
+}
+
+kda_status_t kda_block_norm(const void* y, const void* gate, const void* r, const float* scale,
+                            const float* w_post, const float* w_pre, int post_norm, float eps,
+                            void* r_out, void* x_out, int64_t T, int D, kda_dtype_t io_dt,
+                            kda_dtype_t r_dt, kda_stream_t stream) {
+    t_last_error.clear();
+    kda::BlockNormArgs a{};
+    a.y = y; a.gate = gate; a.r = r; a.scale = scale; a.w_post = w_post; a.w_pre = w_pre;
+    a.post_norm = post_norm != 0; a.eps = eps; a.r_out = r_out; a.x_out = x_out; a.T = T; a.D = D;
+    a.io_bf16 = io_dt == KDA_BF16; a.r_bf16 = r_dt == KDA_BF16;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (kda_status_t s = check_block_norm(a, io_dt, r_dt)) return s;
+    if (T == 0) return KDA_OK;
+    KDA_REQUIRE_PTR(y, "y");
+    KDA_REQUIRE_PTR(r, "r");
+    KDA_REQUIRE_PTR(r_out, "r_out");
+    KDA_REQUIRE_PTR(x_out, "x_out");
+    cudaError_t e = kda::launch_block_norm(a);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_block_norm launch");
+    return KDA_OK;
+}
+
+size_t kda_block_norm_bwd_workspace_size(int D) {
+    if (D <= 0 || D % 8 != 0 || D > kda::kMaxBlockNormD) return 0;
+    return kda::block_norm_bwd_workspace_size(D);
+}
+
+kda_status_t kda_block_norm_bwd(const void* y, const void* gate, const void* r_out,
+                                const void* dx, const void* dr, const float* scale,
+                                const float* w_post, const float* w_pre, int post_norm, float eps,
+                                void* dr_in, void* dy, void* dgate, float* dscale, float* dw_post,
+                                float* dw_pre, int64_t T, int D, kda_dtype_t io_dt,
+                                kda_dtype_t r_dt, void* workspace, size_t ws_bytes,
+                                kda_stream_t stream) {
+    t_last_error.clear();
+    kda::BlockNormArgs a{};
+    a.y = y; a.gate = gate; a.r = r_out; a.dx = dx; a.dr = dr; a.scale = scale; a.w_post = w_post;
+    a.w_pre = w_pre; a.post_norm = post_norm != 0; a.eps = eps; a.dr_in = dr_in; a.dy = dy;
+    a.dgate = dgate; a.dscale = dscale; a.dw_post = dw_post; a.dw_pre = dw_pre; a.T = T; a.D = D;
+    a.io_bf16 = io_dt == KDA_BF16; a.r_bf16 = r_dt == KDA_BF16; a.workspace = workspace;
+    a.stream = reinterpret_cast<cudaStream_t>(stream);
+    if (kda_status_t s = check_block_norm(a, io_dt, r_dt)) return s;
+    KDA_REQUIRE(post_norm || dw_post == nullptr, "dw_post must be NULL without a post-norm");
+    if (T > 0) {
+        KDA_REQUIRE_PTR(y, "y");
+        KDA_REQUIRE_PTR(r_out, "r_out");
+        KDA_REQUIRE_PTR(dx, "dx");
+        KDA_OPTIONAL_PTR(dr, "dr");
+        KDA_REQUIRE_PTR(dr_in, "dr_in");
+        KDA_REQUIRE_PTR(dy, "dy");
+        if (gate) KDA_REQUIRE_PTR(dgate, "dgate");
+        KDA_REQUIRE(gate || dgate == nullptr, "dgate must be NULL without a gate");
+    }
+    KDA_OPTIONAL_PTR(dscale, "dscale");
+    KDA_OPTIONAL_PTR(dw_post, "dw_post");
+    KDA_OPTIONAL_PTR(dw_pre, "dw_pre");
+    if (dscale || dw_post || dw_pre)
+        if (kda_status_t s =
+                check_workspace(workspace, ws_bytes, kda::block_norm_bwd_workspace_size(D)))
+            return s;
+    cudaError_t e = kda::launch_block_norm_bwd(a);
+    if (e != cudaSuccess) return cuda_fail(e, "kda_block_norm_bwd launch");
     return KDA_OK;
 }
 

@@ -147,6 +147,69 @@ size_t qk_norm_bwd_workspace_size(int d);
 cudaError_t launch_qk_norm(const QkNormArgs& a);
 cudaError_t launch_qk_norm_bwd(const QkNormArgs& a);
 
+// The gated recurrence of single channels (recurrence.cu).
+struct RecurrenceArgs {
+    const void *x, *z, *i;                       // io_dt, or codes when packed
+    int64_t x_ld, z_ld, i_ld;
+    const int8_t *x_exps, *z_exps, *i_exps;      // packed inputs only
+    int packed;
+    const float* A_log;
+    float g_min;
+    const float* h0;
+    float* h_out;  // backward: unused
+    const int32_t* cu_seqlens;
+    int N;
+    int64_t T_total;
+    int D;
+    int io_bf16;
+    void* y;       // forward: nullptr when only the edges are wanted
+    float* edges;  // forward: written, or nullptr; backward: read, or nullptr
+    // backward only
+    const void* dy;
+    int64_t dy_ld;
+    const float* dh_out;
+    void *dx, *dz, *di;
+    float *dA_log, *dh0;
+    void* workspace;
+    unsigned* dev_err;
+    cudaStream_t stream;
+};
+size_t recurrence_fwd_workspace_size(int64_t T_total, int N, int D);
+size_t recurrence_bwd_workspace_size(int64_t T_total, int N, int D);
+cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a);
+cudaError_t launch_recurrence_bwd(const RecurrenceArgs& a);
+cudaError_t launch_recurrence_step(const void* x, int64_t x_ld, const void* z, int64_t z_ld,
+                                   const void* i, int64_t i_ld, const float* A_log, float g_min,
+                                   float* h, const int32_t* slots, int n_slots, int N, int D,
+                                   int io_bf16, void* y, unsigned* dev_err, cudaStream_t stream);
+
+// Activations in 8 bits (checkpoint.cu).
+cudaError_t launch_checkpoint_pack(const void* x, int64_t x_ld, int64_t T, int D, int io_bf16,
+                                   int8_t* codes, int8_t* exps, cudaStream_t stream);
+cudaError_t launch_checkpoint_unpack(const int8_t* codes, const int8_t* exps, int64_t T, int D,
+                                     int io_bf16, void* x, cudaStream_t stream);
+
+// Norms before and after a block, with its gate and residual (block_norm.cu).
+struct BlockNormArgs {
+    const void *y, *gate, *r;  // r: the residual before the block (forward) or after it (backward)
+    const float *scale, *w_post, *w_pre;
+    int post_norm;
+    float eps;
+    void *r_out, *x_out;       // forward only
+    const void *dx, *dr;       // backward only, as the rest
+    void *dr_in, *dy, *dgate;
+    float *dscale, *dw_post, *dw_pre;
+    int64_t T;
+    int D;
+    int io_bf16, r_bf16;
+    void* workspace;
+    cudaStream_t stream;
+};
+constexpr int kMaxBlockNormD = 8192;
+size_t block_norm_bwd_workspace_size(int D);
+cudaError_t launch_block_norm(const BlockNormArgs& a);
+cudaError_t launch_block_norm_bwd(const BlockNormArgs& a);
+
 // Chunked forward on CUDA cores in fp32 (any dtype, dk/dv in {64,128}).
 cudaError_t launch_fwd_generic(const FwdArgs& a);
 

@@ -100,6 +100,33 @@ def _load():
     lib.kda_qk_norm_rope_bwd.restype = ctypes.c_int
     lib.kda_qk_norm_rope_bwd.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, f32, vp, i64, vp, i32,
                                          i32, vp, vp, vp, vp, i64, i32, i32, i32, i32, vp, sz, vp]
+    rows = [vp, i64]  # a pointer and a token stride
+    lib.kda_recurrence_fwd_workspace_size.restype = sz
+    lib.kda_recurrence_fwd_workspace_size.argtypes = [i64, i32, i32]
+    lib.kda_recurrence_fwd.restype = ctypes.c_int
+    lib.kda_recurrence_fwd.argtypes = 3 * rows + [vp, f32, vp, vp, vp, i32, i64, i32, i32, vp, vp,
+                                                  vp, sz, vp]
+    lib.kda_recurrence_bwd_workspace_size.restype = sz
+    lib.kda_recurrence_bwd_workspace_size.argtypes = [i64, i32, i32]
+    lib.kda_recurrence_bwd.restype = ctypes.c_int
+    lib.kda_recurrence_bwd.argtypes = 3 * rows + [vp, f32, vp, vp, i32, i64, i32, i32, vp, i64, vp,
+                                                  vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_recurrence_bwd_packed.restype = ctypes.c_int
+    lib.kda_recurrence_bwd_packed.argtypes = 6 * [vp] + [vp, f32, vp, vp, i32, i64, i32, i32, vp,
+                                                         i64, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.kda_recurrence_step.restype = ctypes.c_int
+    lib.kda_recurrence_step.argtypes = 3 * rows + [vp, f32, vp, vp, i32, i32, i32, i32, vp, vp]
+    lib.kda_checkpoint_pack.restype = ctypes.c_int
+    lib.kda_checkpoint_pack.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp]
+    lib.kda_checkpoint_unpack.restype = ctypes.c_int
+    lib.kda_checkpoint_unpack.argtypes = [vp, vp, i64, i32, i32, vp, vp]
+    lib.kda_block_norm.restype = ctypes.c_int
+    lib.kda_block_norm.argtypes = 6 * [vp] + [i32, f32, vp, vp, i64, i32, i32, i32, vp]
+    lib.kda_block_norm_bwd_workspace_size.restype = sz
+    lib.kda_block_norm_bwd_workspace_size.argtypes = [i32]
+    lib.kda_block_norm_bwd.restype = ctypes.c_int
+    lib.kda_block_norm_bwd.argtypes = 8 * [vp] + [i32, f32] + 6 * [vp] + [i64, i32, i32, i32, vp,
+                                                                          sz, vp]
     lib.kda_selftest_timeout.restype = ctypes.c_int
     lib.kda_selftest_timeout.argtypes = [ctypes.c_uint, vp]
     lib.kda_device_status.restype = ctypes.c_int
@@ -677,6 +704,290 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, cos_si
                                      _ptr(out["dwq"]), _ptr(out["dwk"]), T, Hq, Hk, d, _dt(q),
                                      _ptr(workspace), ws_bytes, _stream(stream)),
            "kda_qk_norm_rope_bwd")
+    return out
+
+
+EDGE = 64   # tokens from one edge state to the next
+GROUP = 64  # channels that share an exponent of a checkpoint
+
+
+def _device(t: torch.Tensor, *others):
+    """The device of a call: its tensors' only one, and the current one, where kernels are
+    launched."""
+    d = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != d:
+            raise ValueError(f"tensors are on different devices ({d} and {o.get_device()})")
+    if t.is_cuda and d >= 0 and d != torch.cuda.current_device():
+        raise ValueError(f"tensors are on device {d}, which is not the current one")
+    return t.device
+
+
+def _tokens(t: torch.Tensor, name: str, dtype, shape=None) -> int:
+    """Token stride of a [T, D] tensor (T may be a strided view)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, D = t.shape
+    ld, one = t.stride()
+    if T <= 1 or D == 0:
+        ld = D
+    if one != 1 and D > 1 and T > 0:
+        raise ValueError(f"{name} must have contiguous channels")
+    return ld
+
+
+def _f32(t, name: str, shape):
+    """An optional contiguous fp32 tensor."""
+    if t is not None:
+        _need(t, name, torch.float32)
+        _shape(t, name, shape)
+
+
+def _sequences(cu_seqlens, N) -> int:
+    if cu_seqlens is None:
+        return 1 if N is None else N
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    n = cu_seqlens.numel() - 1
+    if N is not None and N != n:
+        raise ValueError(f"N={N} does not match cu_seqlens of {n} sequences")
+    return n
+
+
+def recurrence_edges(x):
+    """An empty fp32 [ceil(T/64), D] for the edge states of x [T, D] (see recurrence_fwd)."""
+    T, D = x.shape
+    return torch.empty((-(-T // EDGE), D), dtype=torch.float32, device=x.device)
+
+
+def recurrence_fwd(x, z, i, A_log, g_min: float, h0=None, cu_seqlens=None, N=None, y=None,
+                   h_out=None, want_state: bool = True, edges=None, workspace=None, stream=None):
+    """Gated recurrence of single channels over packed sequences:
+    g = g_min sigmoid(exp(A_log) z), h_t = e^g h_{t-1} + sqrt(1 - e^{2g}) sigmoid(i_t) x_t, y = h.
+
+    x, z, i: [T, D] (bf16 or fp32; the token stride is free); A_log: fp32 [D]; h0: fp32 [N, D] or
+    None; cu_seqlens: int32 [N+1] on the device, or None with N equal sequences (N defaults to 1).
+    edges (from recurrence_edges) receives the state that every 64th token starts from, which spares
+    recurrence_bwd a pass.  Returns (y [T, D], h_out [N, D] or None); h_out may be h0.
+    """
+    lx = _tokens(x, "x", x.dtype)
+    T, D = shape = x.shape
+    lz, li = _tokens(z, "z", x.dtype, shape), _tokens(i, "i", x.dtype, shape)
+    N = _sequences(cu_seqlens, N)
+    _f32(A_log, "A_log", (D,))
+    _f32(h0, "h0", (N, D))
+    _f32(h_out, "h_out", (N, D))
+    _f32(edges, "edges", (-(-T // EDGE), D))
+    dt, dev = _dt(x), _device(x, z, i, A_log, h0, cu_seqlens, y, h_out, edges)
+    if y is None:
+        y = _empty((T, D), x.dtype, dev, stream)
+    else:
+        _need(y, "y", x.dtype)
+        _shape(y, "y", (T, D))
+    if h_out is None and want_state:
+        h_out = _empty((N, D), torch.float32, dev, stream)
+    workspace, ws_bytes = _scratch(
+        workspace, _lib.kda_recurrence_fwd_workspace_size(T, N, D), dev, stream)
+    _check(_lib.kda_recurrence_fwd(_ptr(x), lx, _ptr(z), lz, _ptr(i), li, _ptr(A_log), g_min,
+                                   _ptr(h0), _ptr(h_out), _ptr(cu_seqlens), N, T, D, dt, _ptr(y),
+                                   _ptr(edges), _ptr(workspace), ws_bytes, _stream(stream)),
+           "kda_recurrence_fwd")
+    return y, h_out
+
+
+def _checkpoint(c, name: str, shape):
+    """The codes and exponents of a packed [T, D] input."""
+    codes, exps = c
+    T, D = shape
+    _need(codes, f"{name}'s codes", torch.int8)
+    _shape(codes, f"{name}'s codes", (T, D))
+    _need(exps, f"{name}'s exponents", torch.int8)
+    _shape(exps, f"{name}'s exponents", (-(-D // GROUP), T))
+    return codes, exps
+
+
+def recurrence_bwd(x, z, i, A_log, g_min: float, dy, h0=None, dh_out=None, cu_seqlens=None, N=None,
+                   edges=None, want_dA: bool = True, want_dh0: bool = True, workspace=None,
+                   stream=None):
+    """Gradients of recurrence_fwd's (y, h_out) for upstream gradients dy (and dh_out).
+
+    x, z, i: as recurrence_fwd, or all three as checkpoint_pack returned them (then without edges;
+    the gradients are of dy's type).  Returns a dict: dx, dz, di, dA_log [D] and dh0 [N, D] (fp32;
+    None where not wanted).
+    """
+    ldy = _tokens(dy, "dy", dy.dtype)
+    T, D = shape = dy.shape
+    N = _sequences(cu_seqlens, N)
+    _f32(A_log, "A_log", (D,))
+    _f32(h0, "h0", (N, D))
+    _f32(dh_out, "dh_out", (N, D))
+    _f32(edges, "edges", (-(-T // EDGE), D))
+    packed = isinstance(x, (tuple, list))
+    if packed:
+        if not (isinstance(z, (tuple, list)) and isinstance(i, (tuple, list))):
+            raise TypeError("x, z and i must all be checkpoints, or none")
+        if edges is not None:
+            raise ValueError("edges go with whole inputs only")
+        tensors = [t for c, nm in ((x, "x"), (z, "z"), (i, "i")) for t in _checkpoint(c, nm, shape)]
+        inputs = [_ptr(t) for t in tensors]
+    else:
+        tensors = [x, z, i]
+        inputs = []
+        for t, nm in ((x, "x"), (z, "z"), (i, "i")):
+            ld = _tokens(t, nm, dy.dtype, shape)
+            inputs += [_ptr(t), ld]
+    dt, dev = _dt(dy), _device(dy, A_log, h0, dh_out, cu_seqlens, edges, *tensors)
+    out = {"dx": _empty((T, D), dy.dtype, dev, stream),
+           "dz": _empty((T, D), dy.dtype, dev, stream),
+           "di": _empty((T, D), dy.dtype, dev, stream),
+           "dA_log": _empty((D,), torch.float32, dev, stream) if want_dA else None,
+           "dh0": _empty((N, D), torch.float32, dev, stream) if want_dh0 else None}
+    workspace, ws_bytes = _scratch(
+        workspace, _lib.kda_recurrence_bwd_workspace_size(T, N, D), dev, stream)
+    head = [*inputs, _ptr(A_log), g_min, _ptr(h0), _ptr(cu_seqlens), N, T, D, dt, _ptr(dy), ldy,
+            _ptr(dh_out)]
+    tail = [_ptr(t) for t in out.values()] + [_ptr(workspace), ws_bytes, _stream(stream)]
+    if packed:
+        _check(_lib.kda_recurrence_bwd_packed(*head, *tail), "kda_recurrence_bwd_packed")
+    else:
+        _check(_lib.kda_recurrence_bwd(*head, _ptr(edges), *tail), "kda_recurrence_bwd")
+    return out
+
+
+def recurrence_step(x, z, i, A_log, g_min: float, h, slots=None, y=None, stream=None):
+    """One token of recurrence_fwd's recurrence for N requests, states updated in place.
+
+    x, z, i: [N, D]; h: fp32 pool [n_slots, D]; slots: int32 [N], each request's row of the pool
+    (negative: unused, its y is zero), or None for row n.  Returns y [N, D].
+    """
+    lx = _tokens(x, "x", x.dtype)
+    N, D = shape = x.shape
+    lz, li = _tokens(z, "z", x.dtype, shape), _tokens(i, "i", x.dtype, shape)
+    _f32(A_log, "A_log", (D,))
+    n_slots = h.shape[0]
+    _f32(h, "h", (n_slots, D))
+    if slots is not None:
+        _need(slots, "slots", torch.int32)
+        _shape(slots, "slots", (N,))
+    dt, dev = _dt(x), _device(x, z, i, A_log, h, slots, y)
+    if y is None:
+        y = _empty((N, D), x.dtype, dev, stream)
+    else:
+        _need(y, "y", x.dtype)
+        _shape(y, "y", (N, D))
+    _check(_lib.kda_recurrence_step(_ptr(x), lx, _ptr(z), lz, _ptr(i), li, _ptr(A_log), g_min,
+                                    _ptr(h), _ptr(slots), n_slots, N, D, dt, _ptr(y),
+                                    _stream(stream)), "kda_recurrence_step")
+    return y
+
+
+def checkpoint_pack(x, codes=None, exps=None, stream=None):
+    """Keeps an activation x [T, D] (bf16 or fp32; the token stride is free) in 8 bits: 64 channels
+    of a token share the smallest exponent e with max|x| 2^-e < 127.5, each is the integer next to
+    x 2^-e.  Returns (codes int8 [T, D], exps int8 [ceil(D/64), T])."""
+    lx = _tokens(x, "x", x.dtype)
+    T, D = x.shape
+    groups = -(-D // GROUP)
+    dt, dev = _dt(x), _device(x, codes, exps)
+    if codes is None:
+        codes = _empty((T, D), torch.int8, dev, stream)
+    if exps is None:
+        exps = _empty((groups, T), torch.int8, dev, stream)
+    _checkpoint((codes, exps), "x", (T, D))
+    _check(_lib.kda_checkpoint_pack(_ptr(x), lx, T, D, dt, _ptr(codes), _ptr(exps),
+                                    _stream(stream)), "kda_checkpoint_pack")
+    return codes, exps
+
+
+def checkpoint_unpack(codes, exps, dtype=torch.bfloat16, out=None, stream=None):
+    """The activation [T, D] that checkpoint_pack's codes and exponents stand for."""
+    T, D = codes.shape
+    _checkpoint((codes, exps), "x", (T, D))
+    dev = _device(codes, exps, out)
+    if out is None:
+        out = _empty((T, D), dtype, dev, stream)
+    else:
+        _need(out, "out", dtype)
+        _shape(out, "out", (T, D))
+    _check(_lib.kda_checkpoint_unpack(_ptr(codes), _ptr(exps), T, D, _dt(out), _ptr(out),
+                                      _stream(stream)), "kda_checkpoint_unpack")
+    return out
+
+
+def _block(y, r, gate, scale, w_post, w_pre, others=()):
+    """Shared checks of the norms around a block: (T, D, io dtype, residual dtype, device)."""
+    _need(y, "y")
+    if y.dim() != 2:
+        raise ValueError(f"y must have two dimensions, got {y.dim()}")
+    T, D = y.shape
+    _need(r, "r")
+    _shape(r, "r", (T, D))
+    if gate is not None:
+        _need(gate, "gate", y.dtype)
+        _shape(gate, "gate", (T, D))
+    for t, nm in ((scale, "scale"), (w_post, "w_post"), (w_pre, "w_pre")):
+        _f32(t, nm, (D,))
+    for t, nm, dtype in others:
+        if t is not None:
+            _need(t, nm, dtype)
+            _shape(t, nm, (T, D))
+    dev = _device(y, r, gate, scale, w_post, w_pre, *(t for t, _, _ in others))
+    return T, D, _dt(y), _dt(r), dev
+
+
+def block_norm(y, r, gate=None, scale=None, w_post=None, w_pre=None, post_norm: bool = True,
+               eps: float = 1e-6, r_out=None, x_out=None, stream=None):
+    """What stands between a block's output y and the next block's input, in one pass:
+    n = w_post y / rms(y) (n = y without post_norm), r' = r + scale sigmoid(gate) n,
+    x' = w_pre r' / rms(r').
+
+    y, gate: [T, D] (bf16 or fp32, contiguous); r: [T, D] of y's type or fp32; scale, w_post, w_pre:
+    fp32 [D] or None for ones.  Returns (r', x'); they may be r and y.
+    """
+    T, D, dt, rdt, dev = _block(y, r, gate, scale, w_post, w_pre,
+                                ((r_out, "r_out", r.dtype), (x_out, "x_out", y.dtype)))
+    if r_out is None:
+        r_out = _empty((T, D), r.dtype, dev, stream)
+    if x_out is None:
+        x_out = _empty((T, D), y.dtype, dev, stream)
+    _check(_lib.kda_block_norm(_ptr(y), _ptr(gate), _ptr(r), _ptr(scale), _ptr(w_post),
+                               _ptr(w_pre), int(post_norm), eps, _ptr(r_out), _ptr(x_out), T, D,
+                               dt, rdt, _stream(stream)), "kda_block_norm")
+    return r_out, x_out
+
+
+def block_norm_bwd(y, r_out, dx, dr=None, gate=None, scale=None, w_post=None, w_pre=None,
+                   post_norm: bool = True, eps: float = 1e-6, workspace=None, stream=None):
+    """Gradients of block_norm from y, the residual r' that it returned and the gradients dx on x'
+    and dr (or None) on r'.
+
+    Returns a dict: dr (of r), dy, dgate (None without a gate), dscale, dw_post, dw_pre ([D] fp32,
+    None where the parameter is None).
+    """
+    T, D, dt, rdt, dev = _block(y, r_out, gate, scale, w_post, w_pre,
+                                ((dx, "dx", y.dtype), (dr, "dr", r_out.dtype)))
+
+    def sums(w):
+        return None if w is None else _empty((D,), torch.float32, dev, stream)
+
+    out = {"dr": _empty((T, D), r_out.dtype, dev, stream),
+           "dy": _empty((T, D), y.dtype, dev, stream),
+           "dgate": None if gate is None else _empty((T, D), y.dtype, dev, stream),
+           "dscale": sums(scale), "dw_post": sums(w_post), "dw_pre": sums(w_pre)}
+    need = 0
+    if scale is not None or w_post is not None or w_pre is not None:
+        need = _lib.kda_block_norm_bwd_workspace_size(D)
+    workspace, ws_bytes = _scratch(workspace, need, dev, stream)
+    _check(_lib.kda_block_norm_bwd(_ptr(y), _ptr(gate), _ptr(r_out), _ptr(dx), _ptr(dr),
+                                   _ptr(scale), _ptr(w_post), _ptr(w_pre), int(post_norm), eps,
+                                   *(_ptr(t) for t in out.values()), T, D, dt, rdt,
+                                   _ptr(workspace), ws_bytes, _stream(stream)),
+           "kda_block_norm_bwd")
     return out
 
 
