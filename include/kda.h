@@ -358,7 +358,7 @@ kda_status_t kda_qk_norm_rope_bwd(const void *q, int64_t q_ld, const void *k, in
  *   h_out  : [N, D] final states (written), or NULL
  *   cu_seqlens, N, T_total : as kda_fwd_chunked (a sequence may be empty: its h_out is its h0)
  *   y      : [T_total, D] io_dt (written)
- *   edges  : [ceil(T_total / 64), D] (written), or NULL: row j is the state that token 64 j starts
+ *   edges  : [ceil(T_total / 8), D] (written), or NULL: row j is the state that token 8 j starts
  *            from.  kda_recurrence_bwd takes it and is then spared a pass over the inputs.
  *   workspace : device scratch of kda_recurrence_fwd_workspace_size(...) bytes (NULL when 0)
  */

@@ -67,9 +67,10 @@ __device__ __forceinline__ float recurrence_next(float c, float b, float h) {
     return h + fmaf(c, h, b);
 }
 
-// The factors of l_t = dL/dh_t in the gradients of one element, for the state h before it.
+// c, and the factors of l_t = dL/dh_t in the gradients of one element, for the state h before it
+// (that of dx is b / x).
 struct StepGrad {
-    float dx, di, dz;
+    float c, dx, di, dz;
 };
 __device__ __forceinline__ StepGrad recurrence_grad(float x, float z, float i, float rate,
                                                     float neg_log2, float g_min, float h) {
@@ -83,6 +84,7 @@ __device__ __forceinline__ StepGrad recurrence_grad(float x, float z, float i, f
     const float q = m2 > 1e-37f ? rsqrt_approx(m2) : m2 * 0.f;  // 1 / m
     const float u = si * x;
     StepGrad r;
+    r.c = c;
     r.dx = m2 * q * si;
     r.di = m2 * q * u * oi;
     r.dz = rate * oz * g * a * (h - a * q * u);

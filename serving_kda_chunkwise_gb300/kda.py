@@ -707,7 +707,7 @@ def qk_norm_rope_bwd(q, k, dyq, dyk, wq=None, wk=None, eps: float = 1e-6, cos_si
     return out
 
 
-EDGE = 64   # tokens from one edge state to the next
+EDGE = 8    # tokens from one edge state to the next
 GROUP = 64  # channels that share an exponent of a checkpoint
 
 
@@ -760,7 +760,7 @@ def _sequences(cu_seqlens, N) -> int:
 
 
 def recurrence_edges(x):
-    """An empty fp32 [ceil(T/64), D] for the edge states of x [T, D] (see recurrence_fwd)."""
+    """An empty fp32 [ceil(T/8), D] for the edge states of x [T, D] (see recurrence_fwd)."""
     T, D = x.shape
     return torch.empty((-(-T // EDGE), D), dtype=torch.float32, device=x.device)
 
@@ -772,7 +772,7 @@ def recurrence_fwd(x, z, i, A_log, g_min: float, h0=None, cu_seqlens=None, N=Non
 
     x, z, i: [T, D] (bf16 or fp32; the token stride is free); A_log: fp32 [D]; h0: fp32 [N, D] or
     None; cu_seqlens: int32 [N+1] on the device, or None with N equal sequences (N defaults to 1).
-    edges (from recurrence_edges) receives the state that every 64th token starts from, which spares
+    edges (from recurrence_edges) receives the state that every 8th token starts from, which spares
     recurrence_bwd a pass.  Returns (y [T, D], h_out [N, D] or None); h_out may be h0.
     """
     lx = _tokens(x, "x", x.dtype)

@@ -54,7 +54,7 @@ def recurrence(x, z, i, A, g_min, h0, lengths, dy=None, dh=None):
             h[t], E[t] = s, err
         end[n], end_E[n] = s, err
     before_E = torch.cat([torch.zeros_like(E[:1]), E[:-1]])
-    out = dict(y=(h, E), h=(end, end_E), edges=(before[::64], before_E[::64]))
+    out = dict(y=(h, E), h=(end, end_E), edges=(before[::8], before_E[::8]))
     if dy is None:
         return out
     dy = dy.double()

@@ -399,7 +399,7 @@ def test_binding_refusals(kda):
     with pytest.raises(ValueError):
         fwd(**args, h0=s["h0"])  # of two sequences, without offsets
     with pytest.raises(ValueError):
-        fwd(**args, edges=torch.empty(2, 64, device="cuda"))
+        fwd(**args, edges=torch.empty(1, 64, device="cuda"))
     with pytest.raises(ValueError):
         fwd(**args, cu_seqlens=s["cu"], N=3)
     with pytest.raises(kda.KdaError) as e:
