@@ -4,29 +4,22 @@
 //   h_t = a_t h_{t-1} + b_t,   a = e^g, b = sqrt(1 - e^{2g}) s(i) x          (recurrence_math.cuh)
 //   l_t = dy_t + a_{t+1} l_{t+1}, backwards, for the gradients
 //
-// Both are scans of affine maps (P, H): h -> P h + H, and both run in one pass over the data.  A tile
-// is 64 channels x 64 or 128 tokens: a warp holds 8 or 16 tokens, a lane two channels.  The warps
-// compose their tokens' maps, one warp composes the tile's, publishes it and looks back for the
-// state the tile starts from: the nearest tile before it whose end state is published, from which
-// it applies the published maps in between.  Whatever it finds, the state is the same fused
-// multiply-adds in the same order, P_j (... P_0 h + H_0 ...) + H_j, so results do not depend on
-// timing.  Then every warp goes over its tokens again, in registers, and writes.
-//   A map or state is published as 64-bit messages, a channel's (P, H) with P's sign bit (P >= 0) or
-// (state, 1), which are read whole or not at all: to wait for one is to read it until it is there,
-// without a flag of its own to be read before it.
-//   A CTA takes tiles by tickets, the columns of one row of tiles after the other, so a tile waits
-// only for tiles that running CTAs have begun (however many CTAs are resident), and loads the next
-// tiles' inputs (cp.async) while it waits.  A tile in which a sequence starts ends in a state that
-// depends on nothing before it: its end state is published at once.
+// Both are scans of affine maps (P, H): h -> P h + H.  A CTA takes W channels along a run, some
+// consecutive sequences, tile by tile, and carries their state in registers.  In a tile a thread
+// holds 8 tokens of two channels; a warp's threads compose their maps by shuffles, the warps' maps
+// meet in shared memory (two buffers, so one barrier a tile), and every thread applies those before
+// it to the carried state, goes over its tokens again and writes.  So inputs are read once, results
+// written once, and no CTA waits for another.
 //
-// The gradients go over the tiles backwards.  A warp's states come from the edges, the state that
+// The gradients go over the tiles backwards.  A thread's states come from the edges, the state that
 // every 8th token starts from, which the forward writes on request; without them a forward that
 // writes nothing else runs first.  So the factors of l_t in the gradients are formed once, before
 // the scan, and stay in registers until l_t is known.
 //
-// Sequences: every tile has the sequences that touch it (a setup launch finds them, which also
-// clears the messages); where one starts, the map is constant (selected, not multiplied by zero, so
-// that nothing that is not finite crosses).
+// Sequences: a setup launch finds the tokens with which sequences start and end, 8 at a time, and
+// cuts the batch into runs (one sequence needs none of it).  Where a sequence starts, a map is
+// constant: P's sign bit says so (P >= 0 otherwise), and it is selected, not multiplied by zero, so
+// that nothing that is not finite crosses.
 #include <algorithm>
 
 #include "kda_internal.h"
@@ -38,45 +31,53 @@ namespace {
 
 using namespace tc;
 
+constexpr int kTok = 8;     // tokens a thread holds, and from one edge to the next
+constexpr int kGroup = 64;  // channels that share an exponent of packed inputs
 constexpr int kWarps = 8;
-constexpr int kC = 64;    // channels of a tile, and of an exponent of packed inputs
-constexpr int kEdge = 8;  // tokens from one edge to the next
 constexpr int kThreads = 32 * kWarps;
 
-// What the CTAs of a launch share, in the workspace.
-struct Shared {
-    uint32_t* counter;  // tickets; next to it the abort flag of waits that ran out
-    int2* seqs;         // [rows] first and last sequence that may start or end in the tiles of a row,
-                        // {0, -1} where none does; nullptr: one row, every sequence may
-    ulonglong2* mail;   // [rows][cols][map, state][32] messages of a lane's two channels
-    float* part;        // [rows][D] dA_log of the tiles
-    int rows, cols;
+// What the setup launch leaves for the scan.
+struct Plan {
+    int* run;            // [runs + 1] first tokens; nullptr, as all here: one sequence
+    uint32_t* marks;     // [ceil(T / 8)] bits of tokens that start (0..7) and end (8..15) a sequence
+    int *start_seq, *end_seq;  // [T] whose sequence, at such tokens
+    int runs, cols;
 };
 
 // ---------------------------------------------------------------- inputs --
 
-// A stage of the ring: the inputs of a tile.
-template <typename In, typename IO, bool kBwd, int kTok>
+// A stage of the ring: the inputs of a tile of kT tokens x W channels.  Where a row has less than 128
+// bytes, the places of token k of a group of 8 are permuted with the group, which keeps a warp's
+// groups in different banks.
+template <typename In, typename IO, bool kBwd, int W>
 struct Stage {
-    static constexpr int kT = kTok * kWarps;  // tokens of a tile
-    static constexpr int kIn = kT * kC * (int)sizeof(In);
+    static constexpr int kLanes = W / 2;               // of a row
+    static constexpr int kSplit = 32 / kLanes;         // groups of 8 tokens in a warp
+    static constexpr int kGroups = kWarps * kSplit;
+    static constexpr int kT = kGroups * kTok;
+    static constexpr int kIn = kT * W * (int)sizeof(In);
     static constexpr int kDy = 3 * kIn;
-    static constexpr int kEdges = kDy + (kBwd ? kT * kC * (int)sizeof(IO) : 0);
-    static constexpr int kExps = kEdges + (kBwd ? kT / kEdge * kC * 4 : 0);
-    static constexpr int kSeqs = kExps + (sizeof(In) == 1 ? 3 * kT : 0);
-    static constexpr int kBytes = kSeqs + 16;
+    static constexpr int kEdges = kDy + (kBwd ? kT * W * (int)sizeof(IO) : 0);
+    static constexpr int kMarks = kEdges + (kBwd ? kGroups * W * 4 : 0);
+    static constexpr int kExps = kMarks + kGroups * 4;
+    static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT : 0) + 127) / 128 * 128;
     static constexpr int kExpsEach = (3 * kT + kThreads - 1) / kThreads;  // a thread's
-    static_assert(kIn % 16 == 0 && kDy % 16 == 0 && kEdges % 16 == 0 && kBytes % 16 == 0, "");
-    static_assert(!kBwd || kTok == kEdge, "a warp's states come from its edge");
+    static_assert(kIn % 128 == 0 && kEdges % 128 == 0 && kMarks % 16 == 0, "");
 };
+
+// The place of token k of a group, for rows of `bytes` bytes: k with some bits of the group's number.
+__device__ __forceinline__ constexpr int place_bits(int bytes) {
+    return bytes >= 128 ? 0 : 128 / bytes - 1 > kTok - 1 ? kTok - 1 : 128 / bytes - 1;
+}
 
 template <int kBytes>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool live) {
     const int n = live ? kBytes : 0;
-    if (kBytes == 16)
+    if constexpr (kBytes == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n));
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n),
+                     "n"(kBytes));
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;"); }
 template <int n>
@@ -84,24 +85,26 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-// kT tokens x 64 channels of a tensor; rows and channels past its end become zeros.
-template <typename In, int kT>
+// kT tokens x W channels of a tensor; rows and channels past its end become zeros.
+template <typename In, int W, int kT>
 __device__ __forceinline__ void load_tile(char* dst, const void* src, int64_t ld, int64_t t0, int c0,
                                           int64_t T, int D) {
     // (rows of codes begin on 8 bytes only)
     constexpr int kPiece = sizeof(In) == 1 ? 8 : 16, kElems = kPiece / (int)sizeof(In);
-    constexpr int kPer = kC / kElems, kRows = kThreads / kPer;
+    constexpr int kPer = W / kElems, kStep = kThreads / kPer;
     const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * kElems;
     const int left = (int)min((int64_t)kT, T - t0) - row;  // rows left from this thread's first
     const bool in = c0 + c < D;
     const In* s = static_cast<const In*>(src) + (t0 + row) * ld + c0 + c;
-    uint32_t d = smem_u32(dst) + (row * kC + c) * (int)sizeof(In);
+    const uint32_t d = smem_u32(dst);
 #pragma unroll
-    for (int k = 0; k < kT / kRows; ++k) {
-        const bool live = in && k * kRows < left;
-        copy_async<kPiece>(d, live ? s : src, live);
-        s += kRows * ld;
-        d += kRows * kC * (int)sizeof(In);
+    for (int k = 0; k < (kT + kStep - 1) / kStep; ++k) {
+        const int r = row + k * kStep;
+        if (kT % kStep != 0 && r >= kT) break;
+        const bool live = in && k * kStep < left;
+        const int at = r ^ (r / kTok & place_bits(W * (int)sizeof(In)));
+        copy_async<kPiece>(d + (at * W + c) * (int)sizeof(In), live ? s : src, live);
+        s += kStep * ld;
     }
 }
 
@@ -111,40 +114,43 @@ struct Exps {
     int8_t e[n];
 };
 
-// Starts the loads of a tile.
-template <typename S, typename In, typename IO, bool kBwd>
-__device__ __forceinline__ void load_stage(const RecurrenceArgs& a, const Shared& w, char* st,
-                                           int row, int col, Exps<S::kExpsEach>& exps) {
-    const int64_t t0 = (int64_t)row * S::kT;
-    const int c0 = col * kC;
-    load_tile<In, S::kT>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D);
-    load_tile<In, S::kT>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D);
-    load_tile<In, S::kT>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D);
+// Starts the loads of the tile from token t0 and channel c0.
+template <typename S, typename In, typename IO, bool kBwd, int W>
+__device__ __forceinline__ void load_stage(const RecurrenceArgs& a, const Plan& w, char* st,
+                                           int64_t t0, int c0, Exps<S::kExpsEach>& exps) {
+    load_tile<In, W, S::kT>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D);
+    load_tile<In, W, S::kT>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D);
+    load_tile<In, W, S::kT>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D);
     if (kBwd) {
-        load_tile<IO, S::kT>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D);
-        if (threadIdx.x < S::kT / kEdge * kC / 4) {
-            const int e = threadIdx.x / (kC / 4), c = threadIdx.x % (kC / 4) * 4;
-            const bool live = t0 + e * kEdge < a.T_total && c0 + c < a.D;
-            copy_async<16>(smem_u32(st + S::kEdges) + (e * kC + c) * 4,
-                           a.edges + (live ? (t0 / kEdge + e) * a.D + c0 + c : 0), live);
+        load_tile<IO, W, S::kT>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D);
+        constexpr int kPer = W / 4;
+        for (int n = threadIdx.x; n < S::kGroups * kPer; n += kThreads) {
+            const int e = n / kPer, c = n % kPer * 4;
+            const bool live = t0 + e * kTok < a.T_total && c0 + c < a.D;
+            copy_async<16>(smem_u32(st + S::kEdges) + (e * W + c) * 4,
+                           a.edges + (live ? (t0 / kTok + e) * a.D + c0 + c : 0), live);
         }
     }
-    if (w.seqs && threadIdx.x == kThreads - 1)
-        copy_async<8>(smem_u32(st + S::kSeqs), w.seqs + row, true);
-    if (sizeof(In) == 1) {
+    // (a group's marks by the thread that looks at them before the barrier)
+    if (w.marks && threadIdx.x % S::kLanes == 0) {
+        const int g = threadIdx.x / S::kLanes;
+        const bool live = t0 + g * kTok < a.T_total;
+        copy_async<4>(smem_u32(st + S::kMarks) + g * 4, w.marks + (live ? t0 / kTok + g : 0), live);
+    }
+    if constexpr (sizeof(In) == 1) {
 #pragma unroll
         for (int j = 0; j < S::kExpsEach; ++j) {
             const int n = j * kThreads + threadIdx.x, k = n / S::kT, t = n % S::kT;
             const int8_t* e = k == 0 ? a.x_exps : k == 1 ? a.z_exps : a.i_exps;
             exps.e[j] = 0;
             if (n < 3 * S::kT && t0 + t < a.T_total)
-                exps.e[j] = __ldg(e + (int64_t)col * a.T_total + t0 + t);
+                exps.e[j] = __ldg(e + (int64_t)(c0 / kGroup) * a.T_total + t0 + t);
         }
     }
 }
 template <typename S, typename In>
 __device__ __forceinline__ void put_exps(char* st, const Exps<S::kExpsEach>& exps) {
-    if (sizeof(In) == 1) {
+    if constexpr (sizeof(In) == 1) {
 #pragma unroll
         for (int j = 0; j < S::kExpsEach; ++j)
             if (j * kThreads + threadIdx.x < 3 * S::kT)
@@ -160,20 +166,41 @@ __device__ __forceinline__ float2 pair(const float* p) {
     return *reinterpret_cast<const float2*>(p);
 }
 
-// The values of token t of the tile and the lane's channels of input k (x, z, i) of a stage.
-template <typename S, typename In>
-__device__ __forceinline__ float2 input(const char* st, int k, int t, int lane) {
-    const In* p = reinterpret_cast<const In*>(st + k * S::kIn) + t * kC + 2 * lane;
-    if constexpr (sizeof(In) == 1) {
-        const char2 q = *reinterpret_cast<const char2*>(p);
-        const int e = reinterpret_cast<const int8_t*>(st)[S::kExps + k * S::kT + t];
-        // 2^e, denormal at -127; -128 stands for NaN
-        const float s = __int_as_float(e > -127 ? (e + 127) << 23 : e == -127 ? 1 << 22 : 0x7fc00000);
-        return make_float2((float)(signed char)q.x * s, (float)(signed char)q.y * s);
-    } else {
-        return pair(p);
+// A thread's view of a stage: token k of its group, its two channels.
+template <typename S, typename In, typename IO, int W>
+struct View {
+    const char* st;
+    int group, lane;  // group of 8 tokens, lane of the row
+    template <typename E>
+    __device__ __forceinline__ const E* at(int part, int k) const {
+        constexpr int kRow = W * (int)sizeof(E);
+        const int base = group * kTok * kRow + (group & place_bits(kRow)) * kRow + 2 * lane * (int)sizeof(E);
+        return reinterpret_cast<const E*>(st + part + (base ^ k * kRow));
     }
-}
+    __device__ __forceinline__ float2 input(int which, int k) const {
+        const In* p = at<In>(which * S::kIn, k);
+        if constexpr (sizeof(In) == 1) {
+            const char2 q = *reinterpret_cast<const char2*>(p);
+            const int e =
+                reinterpret_cast<const int8_t*>(st)[S::kExps + which * S::kT + group * kTok + k];
+            // 2^e, denormal at -127; -128 stands for NaN
+            const float s =
+                __int_as_float(e > -127 ? (e + 127) << 23 : e == -127 ? 1 << 22 : 0x7fc00000);
+            return make_float2((float)(signed char)q.x * s, (float)(signed char)q.y * s);
+        } else {
+            return pair(p);
+        }
+    }
+    __device__ __forceinline__ float2 dy(int k) const { return pair(at<IO>(S::kDy, k)); }
+    __device__ __forceinline__ float2 edge() const {
+        return pair(reinterpret_cast<const float*>(st + S::kEdges) + group * W + 2 * lane);
+    }
+    // the marks of the group whose first token is t, of a batch of T tokens
+    __device__ __forceinline__ uint32_t marks(const Plan& w, int64_t t, int64_t T) const {
+        if (w.marks) return reinterpret_cast<const uint32_t*>(st + S::kMarks)[group];
+        return (t == 0 ? 1u : 0u) | (T > t && T <= t + kTok ? 256u << (T - 1 - t) : 0u);
+    }
+};
 
 __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
     *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
@@ -181,585 +208,442 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
 __device__ __forceinline__ void store_pair(float* p, float2 v) {
     *reinterpret_cast<float2*>(p) = v;
 }
-// The lane's channels of row n of an fp32 [N, D] tensor.
-__device__ __forceinline__ float2 state_row(const float* p, int n, int D, int c0) {
-    return *reinterpret_cast<const float2*>(p + (int64_t)n * D + c0);
+// Two channels of row n of an fp32 [N, D] tensor.
+__device__ __forceinline__ float2 state_row(const float* p, int n, int D, int c) {
+    return *reinterpret_cast<const float2*>(p + (int64_t)n * D + c);
 }
 
 // ------------------------------------------------------------- sequences --
 
-// Where sequences start and end in a tile: bits of a warp's tokens, and of the warps that have one.
-template <int kT>
-struct Marks {
-    unsigned starts[kWarps], ends[kWarps], start_warps, end_warps;
-    int start_seq[kT], end_seq[kT];  // valid where the token's bit is set
-};
-
-// Marks the sequences lo .. hi; called by all threads.
-template <int kT>
-__device__ __forceinline__ void mark(const RecurrenceArgs& a, Marks<kT>& m, int64_t t0, int lo,
-                                     int hi) {
-    constexpr int kTok = kT / kWarps;
-    if (threadIdx.x < kWarps) m.starts[threadIdx.x] = m.ends[threadIdx.x] = 0u;
-    if (threadIdx.x == 0) m.start_warps = m.end_warps = 0u;
-    __syncthreads();
-    for (int n = lo + threadIdx.x; n <= hi; n += kThreads) {
-        int64_t b, e;
-        seq_range(a.cu_seqlens, n, a.N, a.T_total, nullptr, b, e);
-        if (b >= e) continue;
-        if (b >= t0 && b < t0 + kT) {
-            const int t = (int)(b - t0);
-            m.start_seq[t] = n;
-            atomicOr(&m.starts[t / kTok], 1u << t % kTok);
-            atomicOr(&m.start_warps, 1u << t / kTok);
-        }
-        if (e > t0 && e <= t0 + kT) {
-            const int t = (int)(e - 1 - t0);
-            m.end_seq[t] = n;
-            atomicOr(&m.ends[t / kTok], 1u << t % kTok);
-            atomicOr(&m.end_warps, 1u << t / kTok);
-        }
-    }
-    __syncthreads();
-}
-
 // What becomes of a sequence without tokens: its state (or the state's gradient) as it is.
-__device__ __forceinline__ void pass_empty(const RecurrenceArgs& a, int n, int c, const float* from,
+__device__ __forceinline__ void pass_empty(const RecurrenceArgs& a, int n, const float* from,
                                            float* to) {
-    if (to) to[(int64_t)n * a.D + c] = from ? from[(int64_t)n * a.D + c] : 0.f;
+    if (to)
+        for (int c = threadIdx.x & 31; c < a.D; c += 32)
+            to[(int64_t)n * a.D + c] = from ? from[(int64_t)n * a.D + c] : 0.f;
 }
 
-// Checks the sequences and passes on the states of empty ones (from -> to), for a column of
-// channels; called by all threads where there is no setup launch.
-__device__ __forceinline__ void check_sequences(const RecurrenceArgs& a, int c, const float* from,
-                                                float* to) {
-    for (int n = threadIdx.x >> 5; n < a.N; n += kWarps) {
-        int64_t b, e;
-        seq_range(a.cu_seqlens, n, a.N, a.T_total, (threadIdx.x & 31) == 0 ? a.dev_err : nullptr, b,
-                  e);
-        if (b >= e && c < a.D) {
-            pass_empty(a, n, c, from, to);
-            pass_empty(a, n, c + 1, from, to);
-        }
-    }
-}
-
-// Clears what the scan's CTAs share, finds the sequences of every row of tiles, checks the sequences
-// and passes on the states of empty ones (from -> to).
-__global__ void __launch_bounds__(256) setup_kernel(const RecurrenceArgs a, const Shared w, int kT,
+// Finds where sequences start and end and the runs, checks the sequences and passes on the states
+// of empty ones (from -> to).
+__global__ void __launch_bounds__(256) setup_kernel(const RecurrenceArgs a, const Plan w,
                                                     const float* from, float* to) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
     grid_dependents_launch();
-    if (id < 2) w.counter[id] = 0u;
-    for (int64_t k = id; k < (int64_t)w.rows * w.cols * 64; k += all)
-        w.mail[k] = make_ulonglong2(0ull, 0ull);
+    auto first = [&](int n) {
+        return a.cu_seqlens ? (int64_t)__ldg(a.cu_seqlens + n) : n * (a.T_total / a.N);
+    };
     // the last sequence that starts at or before token t
     auto at = [&](int64_t t) {
-        if (a.cu_seqlens == nullptr) return (int)min(t / (a.T_total / a.N), (int64_t)a.N - 1);
         int lo = 0, hi = a.N - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (__ldg(a.cu_seqlens + mid) <= t) lo = mid;
+            if (first(mid) <= t) lo = mid;
             else hi = mid - 1;
         }
         return lo;
     };
-    for (int64_t k = id; k < w.rows; k += all) {
-        const int64_t t0 = k * kT, t1 = min(t0 + kT, a.T_total);
-        const int lo = at(t0), hi = at(t1 - 1);
-        int64_t b, e;
-        seq_range(a.cu_seqlens, lo, a.N, a.T_total, nullptr, b, e);
-        w.seqs[k] = lo == hi && b != t0 && e > t1 ? make_int2(0, -1) : make_int2(lo, hi);
+    for (int64_t g = id; g * kTok < a.T_total; g += all) {
+        const int64_t t0 = g * kTok;
+        uint32_t bits = 0;
+        for (int n = at(t0); n < a.N && (bits == 0 || first(n) < t0 + kTok); ++n) {
+            int64_t b, e;
+            seq_range(a.cu_seqlens, n, a.N, a.T_total, nullptr, b, e);
+            if (b >= e) {
+                if (first(n) >= t0 + kTok) break;
+                continue;
+            }
+            if (b >= t0 && b < t0 + kTok) {
+                bits |= 1u << (b - t0);
+                w.start_seq[b] = n;
+            }
+            if (e > t0 && e <= t0 + kTok) {
+                bits |= 256u << (e - 1 - t0);
+                w.end_seq[e - 1] = n;
+            }
+            if (e > t0 + kTok - 1 || b >= t0 + kTok) break;
+        }
+        w.marks[g] = bits;
     }
-    const int lane = threadIdx.x & 31;
+    // a run has the sequences that start in its part of the tokens
+    for (int64_t r = id; r <= w.runs; r += all) {
+        int64_t t = a.T_total * r / w.runs;
+        if (r > 0 && r < w.runs) {
+            const int n = at(t - 1) + 1;  // the first that starts at or after t
+            t = n < a.N ? min(max(first(n), (int64_t)0), a.T_total) : a.T_total;
+        }
+        w.run[r] = (int)t;
+    }
     for (int64_t n = id / 32; n < a.N; n += all / 32) {
         int64_t b, e;
-        seq_range(a.cu_seqlens, (int)n, a.N, a.T_total, lane == 0 ? a.dev_err : nullptr, b, e);
-        if (b >= e)
-            for (int c = lane; c < a.D; c += 32) pass_empty(a, (int)n, c, from, to);
+        seq_range(a.cu_seqlens, (int)n, a.N, a.T_total,
+                  (threadIdx.x & 31) == 0 ? a.dev_err : nullptr, b, e);
+        if (b >= e) pass_empty(a, (int)n, from, to);
     }
 }
 
-// ------------------------------------------------------------- messages --
+// ------------------------------------------------------------------ scan --
 
-__device__ __forceinline__ ulonglong2 read_mail(const ulonglong2* p) {
-    ulonglong2 v;
-    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
-                 : "=l"(v.x), "=l"(v.y)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-__device__ __forceinline__ void send_mail(ulonglong2* p, ulonglong2 v) {
-    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(v.x), "l"(v.y)
-                 : "memory");
-}
-__device__ __forceinline__ unsigned long long message(uint32_t lo, float hi) {
-    return (unsigned long long)__float_as_uint(hi) << 32 | lo;
-}
-__device__ __forceinline__ float high(unsigned long long m) {
-    return __uint_as_float((uint32_t)(m >> 32));
-}
-__device__ __forceinline__ float factor(unsigned long long m) {
-    return __uint_as_float((uint32_t)m & 0x7fffffffu);
-}
+// The maps of a thread's two channels: (P.x, P.y, H.x, H.y), P's sign bit set where the map is
+// constant.  kCut: some may be.
+__device__ __forceinline__ bool constant(float P) { return __float_as_int(P) < 0; }
 
-// A lane's maps (P, H) of its two channels.
-__device__ __forceinline__ void send_map(ulonglong2* at, float2 P, float2 H) {
-    send_mail(at, make_ulonglong2(message(__float_as_uint(P.x) | 0x80000000u, H.x),
-                                  message(__float_as_uint(P.y) | 0x80000000u, H.y)));
+template <bool kCut>
+__device__ __forceinline__ float2 apply(float4 m, float2 h) {
+    const float2 r = fma2(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
+    if (kCut && constant(m.x)) return make_float2(m.z, m.w);
+    return r;
 }
-__device__ __forceinline__ void send_state(ulonglong2* at, float2 h) {
-    send_mail(at + 32, make_ulonglong2(message(1u, h.x), message(1u, h.y)));
+// The map that applies `before` and then m.
+template <bool kCut>
+__device__ __forceinline__ float4 after(float4 m, float4 before) {
+    const float2 P = mul2(make_float2(m.x, m.y), make_float2(before.x, before.y));
+    const float2 H = fma2(make_float2(m.x, m.y), make_float2(before.z, before.w),
+                          make_float2(m.z, m.w));
+    if (kCut && constant(m.x)) return m;
+    if (kCut && constant(before.x)) return make_float4(-0.f, -0.f, H.x, H.y);
+    return make_float4(P.x, P.y, H.x, H.y);
 }
-__device__ __forceinline__ bool has_map(ulonglong2 m) {
-    return ((uint32_t)m.x & (uint32_t)m.y & 0x80000000u) != 0u;
-}
-__device__ __forceinline__ bool has_state(ulonglong2 m) {
-    return ((uint32_t)m.x & (uint32_t)m.y & 1u) != 0u;
-}
-__device__ __forceinline__ float2 apply(ulonglong2 m, float2 h) {
-    return make_float2(fmaf(factor(m.x), h.x, high(m.x)), fmaf(factor(m.y), h.y, high(m.y)));
+template <int kUp>
+__device__ __forceinline__ float4 shift(float4 m) {
+    constexpr unsigned kAll = 0xffffffffu;
+    if (kUp > 0)
+        return make_float4(__shfl_up_sync(kAll, m.x, kUp), __shfl_up_sync(kAll, m.y, kUp),
+                           __shfl_up_sync(kAll, m.z, kUp), __shfl_up_sync(kAll, m.w, kUp));
+    return make_float4(__shfl_down_sync(kAll, m.x, -kUp), __shfl_down_sync(kAll, m.y, -kUp),
+                       __shfl_down_sync(kAll, m.z, -kUp), __shfl_down_sync(kAll, m.w, -kUp));
 }
 
-// Bounds a wait of a whole warp: true once it has to be given up.
-struct Patience {
-    uint64_t since = 0;
-    int spins = 0;
-    __device__ __forceinline__ bool over(const Shared& w, unsigned* err, int lane) {
-        if (++spins < 16) return false;
-        int stop = 0;
-        if (lane == 0) {
-            const uint64_t now = globaltimer();
-            if (since == 0) since = now;
-            stop = *reinterpret_cast<volatile uint32_t*>(w.counter + 1) != 0u;
-            if (!stop && now - since > kWaitLimitNs) {
-                atomicOr(err, kDevErrTimeout);
-                atomicExch(w.counter + 1, 1u);
-                stop = 1;
-            }
-        }
-        return __shfl_sync(0xffffffffu, stop, 0) != 0;
+// In a warp: m becomes the map of the groups of tokens before the thread's (in the scan's order: rank
+// 0 first), and the warp's whole map goes to *out.
+template <bool kCut, bool kBwd, int kLanes>
+__device__ __forceinline__ void scan_warp(float4& m, int rank, float4* out) {
+    constexpr int kSplit = 32 / kLanes, kDir = kBwd ? -1 : 1;
+#define KDA_SCAN_STEP(o)                                        \
+    if constexpr (kSplit > o) {                                 \
+        const float4 b = shift<kDir * kLanes * o>(m);           \
+        if (rank >= o) m = after<kCut>(m, b);                   \
     }
-};
+    KDA_SCAN_STEP(1)
+    KDA_SCAN_STEP(2)
+    KDA_SCAN_STEP(4)
+#undef KDA_SCAN_STEP
+    if (rank == kSplit - 1) *out = m;
+    if constexpr (kSplit > 1) m = shift<kDir * kLanes>(m);
+    if (rank == 0) m = make_float4(1.f, 1.f, 0.f, 0.f);
+}
 
-// The state before row p of a column (rows in the scan's order); called by a whole warp, a lane for
-// its two channels.
-__device__ __forceinline__ float2 look_back(const Shared& w, int p, int col, int lane, unsigned* err) {
-    const int64_t step = (int64_t)w.cols * 64;
-    const ulonglong2* at = w.mail + ((int64_t)(p - 1) * w.cols + col) * 64 + lane;  // row p - 1
-    Patience wait;
-    constexpr int kNear = 4;
-    for (;;) {
-        if (wait.over(w, err, lane)) return make_float2(0.f, 0.f);
-        // the nearest rows, maps and states at once: one round trip once they are there
-        ulonglong2 m[kNear], s[kNear];
+// From the state before the tile, that before the thread's tokens; carry: the state after the tile.
+template <bool kCut, int kLanes>
+__device__ __forceinline__ float2 scan_tile(const float4 (*maps)[kLanes], int turn, int lane,
+                                            float4 before, float2& carry) {
+    float2 h = carry, mine = carry;
 #pragma unroll
-        for (int k = 0; k < kNear; ++k) {
-            if (k >= p) continue;
-            m[k] = read_mail(at - k * step);
-            s[k] = read_mail(at - k * step + 32);
-        }
-        int from = -1;       // rows back to a state
-        bool maps = true;    // all maps on the way are there
-#pragma unroll
-        for (int k = 0; k < kNear; ++k) {
-            if (from >= 0) continue;
-            if (k >= p || has_state(s[k])) from = k;
-            else maps = maps && has_map(m[k]);
-        }
-        float2 h = make_float2(0.f, 0.f);
-        if (__all_sync(0xffffffffu, from >= 0 && maps)) {
-#pragma unroll
-            for (int k = kNear - 1; k >= 0; --k) {
-                if (k == from && k < p) h = make_float2(high(s[k].x), high(s[k].y));
-                if (k < from && k < p) h = apply(m[k], h);
-            }
-            return h;
-        }
-        if (!__all_sync(0xffffffffu, from < 0 && maps)) continue;
-        // farther: the nearest state of the 32 rows before, then the maps from there
-        const int q = p - 1 - lane;
-        const bool some =
-            q < 0 || has_state(read_mail(w.mail + ((int64_t)q * w.cols + col) * 64 + 32));
-        const unsigned v = __ballot_sync(0xffffffffu, some);
-        if (v == 0u) continue;
-        int k = min(__ffs(v) - 1, p);
-        if (k < p) {
-            const ulonglong2 t = read_mail(at - k * step + 32);
-            if (!__all_sync(0xffffffffu, has_state(t))) continue;
-            h = make_float2(high(t.x), high(t.y));
-        }
-        for (--k; k >= 0;) {
-            ulonglong2 g[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j <= k) g[j] = read_mail(at - (k - j) * step);
-            int taken = 0;
-            bool go = true;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j > k) continue;
-                go = go && __all_sync(0xffffffffu, has_map(g[j]));
-                if (go) {
-                    h = apply(g[j], h);
-                    ++taken;
-                }
-            }
-            k -= taken;
-            if (!go) break;
-        }
-        // (a row whose map has not come may come with its state alone: from the start)
-        if (k < 0) return h;
+    for (int j = 0; j < kWarps; ++j) {
+        if (j == turn) mine = h;
+        h = apply<kCut>(maps[j][lane], h);
     }
+    carry = h;
+    return apply<kCut>(before, mine);
 }
 
-// The warps' maps of a tile (P, H of a lane's two channels), and the state that it starts from.
-struct Compose {
-    float4 map[kWarps][32];
-    float2 in[32];
-};
+// ------------------------------------------------------------- the loop --
 
-// Called by one warp with all maps there: the tile's map (cut: a bit for every warp whose map is
-// constant, in the scan's order), its publication, and the state the tile starts from (zero for a
-// fresh one, with whose first token a sequence starts).
-__device__ __forceinline__ void compose(const Shared& w, Compose& s, unsigned cut, bool fresh, int p,
-                                        int col, int lane, unsigned* err) {
-    if (w.seqs == nullptr) {  // one row of tiles: a state of zero, and none that waits for this one
-        s.in[lane] = make_float2(0.f, 0.f);
-        return;
-    }
-    float4 m = s.map[0][lane];
-#pragma unroll
-    for (int j = 1; j < kWarps; ++j) {
-        const float4 g = s.map[j][lane];
-        if (cut >> j & 1)
-            m = g;
-        else
-            m = make_float4(m.x * g.x, m.y * g.y, fmaf(g.x, m.z, g.z), fmaf(g.y, m.w, g.w));
-    }
-    ulonglong2* at = w.mail + ((int64_t)p * w.cols + col) * 64 + lane;
-    const bool last = p == w.rows - 1;  // nobody waits for it
-    if (!last) {
-        if (cut) send_state(at, make_float2(m.z, m.w));
-        else if (p > 0) send_map(at, make_float2(m.x, m.y), make_float2(m.z, m.w));
-    }
-    float2 h = make_float2(0.f, 0.f);
-    if (!fresh) {
-        h = look_back(w, p, col, lane, err);
-        if (!cut && !last)
-            send_state(at, make_float2(fmaf(m.x, h.x, m.z), fmaf(m.y, h.y, m.w)));
-    }
-    s.in[lane] = h;
-}
-
-// The state that warp `warp` (in the scan's order) starts from.
-__device__ __forceinline__ float2 warp_state(const Compose& s, unsigned cut, int warp, int lane) {
-    float2 h = s.in[lane];
-#pragma unroll
-    for (int j = 0; j < kWarps - 1; ++j) {
-        if (j < warp) {
-            const float4 g = s.map[j][lane];
-            h = cut >> j & 1 ? make_float2(g.z, g.w)
-                             : make_float2(fmaf(g.x, h.x, g.z), fmaf(g.y, h.y, g.w));
-        }
-    }
-    return h;
-}
-
-// ------------------------------------------------------------- the loops --
-
-// Runs body(stage, p, row, col) over a CTA's tiles (p: the row in the scan's order), their inputs
-// loaded ahead.
-template <typename S, typename In, typename IO, bool kBwd, int kStages, typename Body>
-__device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Shared& w, char* ring,
-                                          Body&& body) {
-    __shared__ int2 tile[kStages];  // (p, column) of the tile in each stage; p = rows: none left
-    auto place = [&](uint32_t id) {
-        const uint32_t p = id / (uint32_t)w.cols;
-        return make_int2((int)min(p, (uint32_t)w.rows), (int)(id - p * (uint32_t)w.cols));
-    };
-    auto load = [&](int s, Exps<S::kExpsEach>& e) {
-        const int2 t = tile[s];
-        if (t.x < w.rows)
-            load_stage<S, In, IO, kBwd>(a, w, ring + s * S::kBytes, kBwd ? w.rows - 1 - t.x : t.x, t.y,
-                                        e);
+// Runs first(view, t0, marks, marked, buf), a barrier and second(..) over the tiles of a CTA's run,
+// their inputs loaded ahead.  marked: some token of the tile starts or ends a sequence; buf
+// alternates.  kHeld: second() reads the stage too.
+template <typename S, typename In, typename IO, bool kBwd, int W, int kStages, bool kHeld,
+          typename First, typename Second>
+__device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w, char* ring, int begin,
+                                          int end, int c0, First&& first, Second&& second) {
+    // Loads go out right after the barrier, into the stage that is free then: the tile's own, or where
+    // that is still read, the one before it.
+    constexpr int kAhead = kHeld ? kStages - 1 : kStages;  // tiles from the one worked on
+    static_assert(kAhead >= 2, "the next tile is on its way before the barrier");
+    const int base = begin / kTok * kTok, n = (end - base + S::kT - 1) / S::kT;
+    auto first_token = [&](int k) { return base + (kBwd ? n - 1 - k : k) * S::kT; };
+    Exps<S::kExpsEach> exps;
+    auto load = [&](int k, int s) {
+        if (k < n) load_stage<S, In, IO, kBwd, W>(a, w, ring + s * S::kBytes, first_token(k), c0, exps);
         copy_commit();
     };
-    const uint32_t none = 0xffffffffu;
-    if (threadIdx.x == 0) {
+    const int group = threadIdx.x / S::kLanes, lane = threadIdx.x % S::kLanes;
+    // whether tile k, in stage s, has marks that this thread has copied (or its run ends in it)
+    auto look = [&](int k, int s) {
+        if (k >= n) return false;
+        const int t0 = first_token(k);
+        if (t0 < begin || t0 + S::kT > end || (w.marks == nullptr && (t0 == 0 || t0 + S::kT == end)))
+            return true;
+        return w.marks != nullptr && lane == 0 &&
+               reinterpret_cast<const uint32_t*>(ring + s * S::kBytes + S::kMarks)[group] != 0u;
+    };
 #pragma unroll
-        for (int s = 0; s < kStages; ++s)
-            tile[s] = w.seqs ? place(atomicAdd(w.counter, 1u))
-                             : s == 0 ? make_int2(0, blockIdx.x) : make_int2(w.rows, 0);
+    for (int k = 0; k < kAhead; ++k) {
+        load(k, k);
+        put_exps<S, In>(ring + k * S::kBytes, exps);
     }
-    __syncthreads();
-    Exps<S::kExpsEach> exps;
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        load(s, exps);
-        put_exps<S, In>(ring + s * S::kBytes, exps);
-    }
-    for (int s = 0;;) {
-        copy_wait<kStages - 2>();
-        __syncthreads();  // the stage is there, and the one before it free
-        const int2 t = tile[s];
-        if (t.x >= w.rows) break;
-        const int free = s == 0 ? kStages - 1 : s - 1;
-        load(free, exps);
-        uint32_t next = none;  // (on its way while this tile is worked on)
-        if (threadIdx.x == 0 && w.seqs) next = atomicAdd(w.counter, 1u);
-        body(ring + s * S::kBytes, t.x, kBwd ? w.rows - 1 - t.x : t.x, t.y);
-        put_exps<S, In>(ring + free * S::kBytes, exps);
-        // (every thread has read this stage's place before the body's barriers)
-        if (threadIdx.x == 0) tile[s] = next == none ? make_int2(w.rows, 0) : place(next);
-        s = s + 1 == kStages ? 0 : s + 1;
+    copy_wait<kAhead - 1>();
+    bool marked = __syncthreads_or(look(0, 0));
+    for (int k = 0, s = 0; k < n; ++k) {
+        const View<S, In, IO, W> v{ring + s * S::kBytes, group, lane};
+        const int64_t t = first_token(k) + group * kTok;
+        const uint32_t marks = marked ? v.marks(w, t, a.T_total) : 0u;
+        first(v, t, marks, marked, k & 1);
+        const int next = s + 1 == kStages ? 0 : s + 1;
+        copy_wait<kAhead - 2>();
+        const bool coming = __syncthreads_or(look(k + 1, next));
+        const int free = !kHeld ? s : s == 0 ? kStages - 1 : s - 1;
+        load(k + kAhead, free);
+        second(v, t, marks, marked, k & 1);
+        if (k + kAhead < n) put_exps<S, In>(ring + free * S::kBytes, exps);
+        marked = coming;
+        s = next;
     }
     copy_wait<0>();
 }
 
-// Marks a tile's sequences, if any may start or end there.
-template <typename S>
-__device__ __forceinline__ bool find_marks(const RecurrenceArgs& a, const Shared& w, const char* st,
-                                           int row, Marks<S::kT>& marks) {
-    const int2 q = w.seqs ? *reinterpret_cast<const int2*>(st + S::kSeqs) : make_int2(0, a.N - 1);
-    if (q.x > q.y) return false;
-    mark<S::kT>(a, marks, (int64_t)row * S::kT, q.x, q.y);
+// The CTA's run and first channel; false where it has nothing to do.
+__device__ __forceinline__ bool find_run(const RecurrenceArgs& a, const Plan& w, int W, int& begin,
+                                         int& end, int& c0) {
+    const int r = blockIdx.x / w.cols;
+    c0 = (int)(blockIdx.x - r * w.cols) * W;
+    if (w.run) {
+        begin = w.run[r];
+        end = w.run[r + 1];
+        return begin < end;
+    }
+    begin = 0;
+    end = (int)a.T_total;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {  // no setup launch: its check here
+        int64_t b, e;
+        seq_range(a.cu_seqlens, 0, 1, a.T_total, a.dev_err, b, e);
+    }
     return true;
+}
+// The sequence that starts, or ends, with token t.
+__device__ __forceinline__ int start_at(const Plan& w, int64_t t) {
+    return w.start_seq ? w.start_seq[t] : 0;
+}
+__device__ __forceinline__ int end_at(const Plan& w, int64_t t) {
+    return w.end_seq ? w.end_seq[t] : 0;
 }
 
 // ---------------------------------------------------------------- forward --
 
-template <typename In, typename IO, int kTok, int kStages, int kCtas>
-__global__ void __launch_bounds__(kThreads, kCtas) scan_kernel(
-    const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Shared w,
+template <typename In, typename IO, int W, int kStages>
+__global__ void __launch_bounds__(kThreads, 2) scan_kernel(
+    const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
     const __grid_constant__ GateBound gb) {
-    using S = Stage<In, IO, false, kTok>;
+    using S = Stage<In, IO, false, W>;
+    using V = View<S, In, IO, W>;
     extern __shared__ __align__(128) char ring[];
-    __shared__ Compose comp;
-    __shared__ Marks<S::kT> marks;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float4 maps[2][kWarps][S::kLanes];
+    const int lane = threadIdx.x % S::kLanes, warp = threadIdx.x >> 5;
+    const int rank = threadIdx.x % 32 / S::kLanes;
     grid_dependency_wait();
     grid_dependents_launch();
-    if (w.seqs == nullptr) check_sequences(a, blockIdx.x * kC + 2 * lane, a.h0, a.h_out);
-    for_tiles<S, In, IO, false, kStages>(a, w, ring, [&](const char* st, int p, int row, int col) {
-        const int64_t t0 = (int64_t)row * S::kT;
-        const int c0 = col * kC + 2 * lane;
-        const bool live = c0 < a.D;
-        unsigned starts = 0, ends = 0, cut = 0;
-        bool fresh = false;
-        if (find_marks<S>(a, w, st, row, marks)) {
-            starts = marks.starts[warp];
-            ends = marks.ends[warp];
-            cut = marks.start_warps;
-            fresh = marks.starts[0] & 1;
-        }
-        const float2 nl =
-            channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + c0) : both(0.f), 0.f)
-                .neg_log2;
-
-        float2 c[kTok], nb[kTok];
-#pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-            const int t = warp * kTok + k;
-            const Step u = recurrence_step(input<S, In>(st, 0, t, lane), input<S, In>(st, 1, t, lane),
-                                           input<S, In>(st, 2, t, lane), nl, gb);
-            c[k] = u.c;
-            nb[k] = u.nb;
-            if (k % 2 == 1) asm volatile("" ::: "memory");  // (later tokens' loads would take registers)
-        }
-        if (starts && a.h0) {  // initial states: into the first tokens' input terms
-#pragma unroll
-            for (int k = 0; k < kTok; k += 4) {
-                float2 h0[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    h0[j] = starts >> (k + j) & 1 && live
-                                ? state_row(a.h0, marks.start_seq[warp * kTok + k + j], a.D, c0)
-                                : both(0.f);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (starts >> (k + j) & 1)
-                        nb[k + j] = mul2(recurrence_next(c[k + j], nb[k + j], h0[j]), both(-1.f));
-            }
-        }
-        float2 P = both(1.f), H = both(0.f);
-        if (starts == 0) {
+    int begin, end, c0;
+    if (!find_run(a, w, W, begin, end, c0)) return;
+    const int ch = c0 + 2 * lane;
+    const bool live = ch < a.D;
+    const float2 nl =
+        channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
+    float2 carry = both(0.f);
+    float2 c[kTok], nb[kTok];
+    float2 opening = both(0.f);  // the initial state of a sequence that starts with the first token
+    float4 before;
+    for_tiles<S, In, IO, false, W, kStages, false>(
+        a, w, ring, begin, end, c0,
+        [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
+            float2 P = both(1.f), H = both(0.f);
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
-                P = fma2(c[k], P, P);
-                H = recurrence_next(c[k], nb[k], H);
+                const Step u = recurrence_step(v.input(0, k), v.input(1, k), v.input(2, k), nl, gb);
+                c[k] = u.c;
+                nb[k] = u.nb;
             }
-        } else {
+            if ((marks & 0xffu) == 0u) {
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+                    P = fma2(c[k], P, P);
+                    H = recurrence_next(c[k], nb[k], H);
+                }
+            } else {
+                if (a.h0) {  // initial states: into the first tokens' input terms
+                    float2 h0[kTok];
+#pragma unroll
+                    for (int k = 0; k < kTok; ++k)
+                        h0[k] = marks >> k & 1 && live ? state_row(a.h0, start_at(w, t + k), a.D, ch)
+                                                       : both(0.f);
+                    opening = h0[0];
+#pragma unroll
+                    for (int k = 0; k < kTok; ++k)
+                        if (marks >> k & 1)
+                            nb[k] = mul2(recurrence_next(c[k], nb[k], h0[k]), both(-1.f));
+                }
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+                    if (marks >> k & 1) H = both(0.f);
+                    H = recurrence_next(c[k], nb[k], H);
+                }
+                P = both(-0.f);
+            }
+            before = make_float4(P.x, P.y, H.x, H.y);
+            if (marked)
+                scan_warp<true, false, S::kLanes>(before, rank, &maps[buf][warp][lane]);
+            else
+                scan_warp<false, false, S::kLanes>(before, rank, &maps[buf][warp][lane]);
+        },
+        [&](const V&, int64_t t, uint32_t marks, bool marked, int buf) {
+            float2 h = marked ? scan_tile<true, S::kLanes>(maps[buf], warp, lane, before, carry)
+                              : scan_tile<false, S::kLanes>(maps[buf], warp, lane, before, carry);
+            if (!live) return;
+            IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
+            float* edge = a.edges + t / kTok * a.D + ch;
+            if (!marked) {
+                if (a.edges) store_pair(edge, h);
+#pragma unroll
+                for (int k = 0; k < kTok; ++k) {
+                    h = recurrence_next(c[k], nb[k], h);
+                    if (a.y) store_pair(y + (int64_t)k * a.D, h);
+                }
+                return;
+            }
+            if (a.edges && t >= begin && t < end)
+                store_pair(edge, marks & 1 ? opening : h);
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
-                if (starts >> k & 1) H = both(0.f);
-                H = recurrence_next(c[k], nb[k], H);
-            }
-        }
-        comp.map[warp][lane] = make_float4(P.x, P.y, H.x, H.y);
-        __syncthreads();
-        if (warp == 0) compose(w, comp, cut, fresh, p, col, lane, a.dev_err);
-        __syncthreads();
-        float2 h = warp_state(comp, cut, warp, lane);
-        if (!live) return;
-        const int64_t t = t0 + warp * kTok;
-        const int left = (int)min((int64_t)kTok, a.T_total - t);
-        IO* y = static_cast<IO*>(a.y) + t * a.D + c0;
-        float* edge = a.edges + t / kEdge * a.D + c0;
-        if ((starts | ends) == 0 && left == kTok) {
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-                if (k % kEdge == 0 && a.edges) store_pair(edge + (int64_t)(k / kEdge) * a.D, h);
+                if (marks >> k & 1) h = both(0.f);
                 h = recurrence_next(c[k], nb[k], h);
-                if (a.y) store_pair(y, h);
-                y += a.D;
+                if (t + k < begin || t + k >= end) continue;
+                if (a.y) store_pair(y + (int64_t)k * a.D, h);
+                if (marks >> (8 + k) & 1 && a.h_out)
+                    store_pair(a.h_out + (int64_t)end_at(w, t + k) * a.D + ch, h);
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-                const bool start = starts >> k & 1;
-                const int at = warp * kTok + k;
-                if (k % kEdge == 0 && a.edges && k < left)
-                    store_pair(edge + (int64_t)(k / kEdge) * a.D,
-                               !start  ? h
-                               : a.h0 ? state_row(a.h0, marks.start_seq[at], a.D, c0)
-                                      : both(0.f));
-                if (start) h = both(0.f);
-                h = recurrence_next(c[k], nb[k], h);
-                if (k < left && a.y) store_pair(y, h);
-                y += a.D;
-                if (k < left && ends >> k & 1 && a.h_out)
-                    store_pair(a.h_out + (int64_t)marks.end_seq[at] * a.D + c0, h);
-            }
-        }
-    });
+        });
 }
 
 // -------------------------------------------------------------- gradients --
 
-template <typename In, typename IO, int kTok, int kStages, int kCtas>
-__global__ void __launch_bounds__(kThreads, kCtas) scan_bwd_kernel(
-    const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Shared w,
-    const __grid_constant__ GateBound gb) {
-    using S = Stage<In, IO, true, kTok>;
+template <typename In, typename IO, int W, int kStages>
+__global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
+    const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
+    const __grid_constant__ GateBound gb, float* part) {
+    using S = Stage<In, IO, true, W>;
+    using V = View<S, In, IO, W>;
     extern __shared__ __align__(128) char ring[];
-    __shared__ Compose comp;
-    __shared__ Marks<S::kT> marks;
-    __shared__ float2 sums[kWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float4 maps[2][kWarps][S::kLanes];
+    const int lane = threadIdx.x % S::kLanes, warp = threadIdx.x >> 5;
+    // in the scan's order, backwards
+    const int rank = S::kSplit - 1 - (int)threadIdx.x % 32 / S::kLanes, turn = kWarps - 1 - warp;
     grid_dependency_wait();
     grid_dependents_launch();
-    if (w.seqs == nullptr) check_sequences(a, blockIdx.x * kC + 2 * lane, a.dh_out, a.dh0);
-    for_tiles<S, In, IO, true, kStages>(a, w, ring, [&](const char* st, int p, int row, int col) {
-        const int64_t t0 = (int64_t)row * S::kT;
-        const int c0 = col * kC + 2 * lane;
-        const bool live = c0 < a.D;
-        unsigned starts = 0, ends = 0, cut = 0;
-        bool fresh = false;
-        if (find_marks<S>(a, w, st, row, marks)) {
-            starts = marks.starts[warp];
-            ends = marks.ends[warp];
-            cut = __brev(marks.end_warps) >> (32 - kWarps);  // in the scan's order
-            fresh = marks.ends[kWarps - 1] >> (kTok - 1) & 1;
-        }
+    int begin, end, c0;
+    const bool any = find_run(a, w, W, begin, end, c0);
+    const int ch = c0 + 2 * lane;
+    const bool live = ch < a.D;
+    float2 dA = both(0.f);
+    if (any) {
         const ChannelRate r = channel_rate(
-            live ? *reinterpret_cast<const float2*>(a.A_log + c0) : both(0.f), gb.g_min);
-
-        // the negated factors of l in the gradients, from the states, and -dy
-        float2 c[kTok], fx[kTok], fz[kTok], fi[kTok], dy[kTok];
-        float2 h = *reinterpret_cast<const float2*>(st + S::kEdges + (warp * kC + 2 * lane) * 4);
+            live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), gb.g_min);
+        float2 carry = both(0.f);  // -r, what -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
+        float2 c[kTok], fx[kTok], fz[kTok], fi[kTok];
+        float4 before;
+        for_tiles<S, In, IO, true, W, kStages, true>(
+            a, w, ring, begin, end, c0,
+            [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
+                // the negated factors of l in the gradients, from the states
+                float2 h = v.edge();
 #pragma unroll
-        for (int k = 0; k < kTok; ++k) {
-            const int t = warp * kTok + k;
-            if (starts >> k & 1)
-                h = a.h0 && live ? state_row(a.h0, marks.start_seq[t], a.D, c0) : both(0.f);
-            const float2 x = input<S, In>(st, 0, t, lane);
-            const StepGrad u = recurrence_grad(x, input<S, In>(st, 1, t, lane),
-                                               input<S, In>(st, 2, t, lane), r, gb, h);
-            c[k] = u.c;
-            fx[k] = u.dx;
-            fz[k] = u.dz;
-            fi[k] = u.di;
-            h = recurrence_next(u.c, mul2(u.dx, x), h);
-            dy[k] = mul2(pair(reinterpret_cast<const IO*>(st + S::kDy) + t * kC + 2 * lane), both(-1.f));
-            if (k % 2 == 1) asm volatile("" ::: "memory");
-        }
-        if (ends && a.dh_out) {
-            float2 d[kTok];
+                for (int k = 0; k < kTok; ++k) {
+                    if (marks >> k & 1)
+                        h = a.h0 && live ? state_row(a.h0, start_at(w, t + k), a.D, ch) : both(0.f);
+                    const float2 x = v.input(0, k);
+                    const StepGrad u = recurrence_grad(x, v.input(1, k), v.input(2, k), r, gb, h);
+                    c[k] = u.c;
+                    fx[k] = u.dx;
+                    fz[k] = u.dz;
+                    fi[k] = u.di;
+                    h = recurrence_next(u.c, mul2(u.dx, x), h);
+                }
+                float2 P = both(1.f), H = both(0.f);
+                if ((marks & 0xff00u) == 0u) {
 #pragma unroll
-            for (int k = 0; k < kTok; ++k)
-                d[k] = ends >> k & 1 && live
-                           ? state_row(a.dh_out, marks.end_seq[warp * kTok + k], a.D, c0)
-                           : both(0.f);
+                    for (int k = kTok - 1; k >= 0; --k) {
+                        P = fma2(c[k], P, P);
+                        const float2 l = fma2(v.dy(k), both(-1.f), H);
+                        H = fma2(c[k], l, l);
+                    }
+                } else {
 #pragma unroll
-            for (int k = 0; k < kTok; ++k) dy[k] = fma2(d[k], both(-1.f), dy[k]);
-        }
-        // -r, what -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
-        float2 P = both(1.f), H = both(0.f);
+                    for (int k = kTok - 1; k >= 0; --k) {
+                        if (marks >> (8 + k) & 1)
+                            H = a.dh_out && live
+                                    ? mul2(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
+                                    : both(0.f);
+                        const float2 l = fma2(v.dy(k), both(-1.f), H);
+                        H = fma2(c[k], l, l);
+                    }
+                    P = both(-0.f);
+                }
+                before = make_float4(P.x, P.y, H.x, H.y);
+                if (marked)
+                    scan_warp<true, true, S::kLanes>(before, rank, &maps[buf][turn][lane]);
+                else
+                    scan_warp<false, true, S::kLanes>(before, rank, &maps[buf][turn][lane]);
+            },
+            [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
+                float2 nr = marked ? scan_tile<true, S::kLanes>(maps[buf], turn, lane, before, carry)
+                                   : scan_tile<false, S::kLanes>(maps[buf], turn, lane, before, carry);
+                if (!live) return;
+                const int64_t at = t * a.D + ch;
+                IO* dx = static_cast<IO*>(a.dx) + at;
+                IO* dz = static_cast<IO*>(a.dz) + at;
+                IO* di = static_cast<IO*>(a.di) + at;
 #pragma unroll
-        for (int k = kTok - 1; k >= 0; --k) {
-            if (ends >> k & 1) H = both(0.f);
-            P = fma2(c[k], P, P);
-            const float2 l = add2(dy[k], H);
-            H = fma2(c[k], l, l);
-        }
-        const int turn = kWarps - 1 - warp;  // the warp's place in the scan
-        comp.map[turn][lane] = make_float4(P.x, P.y, H.x, H.y);
-        __syncthreads();
-        if (warp == 0) compose(w, comp, cut, fresh, p, col, lane, a.dev_err);
-        __syncthreads();
-        float2 nr = warp_state(comp, cut, turn, lane);
-        const int64_t t = t0 + warp * kTok;
-        const int64_t at = t * a.D + c0;
-        const int left = live ? (int)min((int64_t)kTok, a.T_total - t) : 0;
-        IO* dx = static_cast<IO*>(a.dx) + at;
-        IO* dz = static_cast<IO*>(a.dz) + at;
-        IO* di = static_cast<IO*>(a.di) + at;
-        float2 dA = both(0.f);
-#pragma unroll
-        for (int k = kTok - 1; k >= 0; --k) {
-            if (ends >> k & 1) nr = both(0.f);
-            const float2 l = add2(dy[k], nr);
-            nr = fma2(c[k], l, l);
-            if (k < left) {
-                const int64_t o = (int64_t)k * a.D;
-                const float2 v = mul2(l, fz[k]);
-                store_pair(dx + o, mul2(l, fx[k]));
-                store_pair(dz + o, v);
-                store_pair(di + o, mul2(l, fi[k]));
-                // (an infinite z has a gradient of zero)
-                const float2 z = input<S, In>(st, 1, warp * kTok + k, lane);
-                dA.x += v.x == 0.f ? 0.f : v.x * z.x;
-                dA.y += v.y == 0.f ? 0.f : v.y * z.y;
-                if (starts >> k & 1 && a.dh0)
-                    store_pair(a.dh0 + (int64_t)marks.start_seq[warp * kTok + k] * a.D + c0,
-                               mul2(nr, both(-1.f)));
-            }
-        }
-        if (a.dA_log) {
-            sums[warp][lane] = dA;
-            __syncthreads();
-            if (warp == 0 && live) {
-                float2 s = sums[0][lane];
-#pragma unroll
-                for (int j = 1; j < kWarps; ++j) s = add2(s, sums[j][lane]);
-                *reinterpret_cast<float2*>(w.part + (int64_t)row * a.D + c0) = s;
-            }
-        }
-    });
+                for (int k = kTok - 1; k >= 0; --k) {
+                    if (marks >> (8 + k) & 1)
+                        nr = a.dh_out ? mul2(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
+                                      : both(0.f);
+                    const float2 l = fma2(v.dy(k), both(-1.f), nr);
+                    nr = fma2(c[k], l, l);
+                    if (marked && (t + k < begin || t + k >= end)) continue;
+                    const int64_t o = (int64_t)k * a.D;
+                    const float2 g = mul2(l, fz[k]), z = v.input(1, k);
+                    store_pair(dx + o, mul2(l, fx[k]));
+                    store_pair(dz + o, g);
+                    store_pair(di + o, mul2(l, fi[k]));
+                    // (an infinite z has a gradient of zero)
+                    dA.x += g.x == 0.f ? 0.f : g.x * z.x;
+                    dA.y += g.y == 0.f ? 0.f : g.y * z.y;
+                    if (marks >> k & 1 && a.dh0)
+                        store_pair(a.dh0 + (int64_t)start_at(w, t + k) * a.D + ch, mul2(nr, both(-1.f)));
+                }
+            });
+    }
+    if (part == nullptr) return;
+    // the run's dA_log: over the threads of a channel, in a fixed order
+    float2* sums = reinterpret_cast<float2*>(ring);
+    __syncthreads();
+    sums[threadIdx.x] = dA;
+    __syncthreads();
+    if (threadIdx.x < S::kLanes && live) {
+        float2 s = both(0.f);
+#pragma unroll 8
+        for (int g = 0; g < S::kGroups; ++g) s = add2(s, sums[g * S::kLanes + lane]);
+        *reinterpret_cast<float2*>(part + (int64_t)(blockIdx.x / w.cols) * a.D + ch) = s;
+    }
 }
 
-// dA_log[c] = the sum of the tiles' parts in a fixed order: a CTA takes 32 channels, its 32 warps
-// every 32nd tile.
-__global__ void __launch_bounds__(1024) rate_kernel(const float* part, int tiles, int D, float* dA) {
+// dA_log[c] = the sum of the runs' parts in a fixed order: a CTA takes 32 channels, its 32 warps every
+// 32nd run.
+__global__ void __launch_bounds__(1024) rate_kernel(const float* part, int runs, int D, float* dA) {
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     grid_dependency_wait();
     float x = 0.f;
     if (c < D) {
 #pragma unroll 4
-        for (int b = warp; b < tiles; b += 32) x += part[(int64_t)b * D + c];
+        for (int b = warp; b < runs; b += 32) x += part[(int64_t)b * D + c];
     }
     red[warp][lane] = x;
     __syncthreads();
@@ -832,114 +716,148 @@ __global__ void __launch_bounds__(128) step_kernel(const IO* x, int64_t x_ld, co
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// The parts of a workspace for rows of tiles of kT tokens; w may be nullptr.
-size_t lay_out(char* ws, int64_t T, int D, int kT, bool bwd, Shared* w, float** edges) {
-    const size_t rows = (size_t)((T + kT - 1) / kT), cols = (D + kC - 1) / kC;
+// Runs are as many as sequences, but of 1,024 tokens on average at least, and 8 times the CTAs
+// that the GPU holds at most.
+int count_runs(int64_t T, int N, int cols) {
+    const int64_t most = std::max<int64_t>(1, 152 * 2 * 8 / cols);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(N, T / 1024), most));
+}
+
+// The parts of a workspace; w may be nullptr.
+size_t lay_out(char* ws, int64_t T, int N, int D, int W, bool bwd, Plan* w, float** edges,
+               float** part) {
     size_t n = 0;
     auto take = [&](size_t bytes) {
         char* p = ws ? ws + n : nullptr;
         n += up(bytes);
         return p;
     };
-    Shared s{};
-    s.rows = (int)rows;
-    s.cols = (int)cols;
-    if (bwd) {  // (first, so that a forward before the gradients does not touch them)
-        char* e = take((size_t)((T + kEdge - 1) / kEdge) * D * 4);
-        if (edges) *edges = reinterpret_cast<float*>(e);
-        s.part = reinterpret_cast<float*>(take(rows * D * 4));
+    Plan s{};
+    s.cols = (D + W - 1) / W;
+    s.runs = count_runs(T, N, s.cols);
+    if (N != 1) {
+        s.run = reinterpret_cast<int*>(take((s.runs + 1) * 4));
+        s.marks = reinterpret_cast<uint32_t*>(take((T + kTok - 1) / kTok * 4));
+        s.start_seq = reinterpret_cast<int*>(take(T * 4));
+        s.end_seq = reinterpret_cast<int*>(take(T * 4));
     }
-    if (rows != 1) {
-        s.counter = reinterpret_cast<uint32_t*>(take(8));
-        s.seqs = reinterpret_cast<int2*>(take(rows * sizeof(int2)));
-        s.mail = reinterpret_cast<ulonglong2*>(take(rows * cols * 64 * sizeof(ulonglong2)));
+    if (bwd) {
+        char* p = take((size_t)s.runs * D * 4);
+        char* e = take((size_t)((T + kTok - 1) / kTok) * D * 4);
+        if (part) *part = reinterpret_cast<float*>(p);
+        if (edges) *edges = reinterpret_cast<float*>(e);
     }
     if (w) *w = s;
     return n;
 }
 
-template <typename S, typename Kernel>
-cudaError_t launch_scan(Kernel kernel, const char* name, int smem, int ctas, const RecurrenceArgs& a,
-                        const Shared& w, const float* from, float* to) {
-    if (w.rows != 1) {
-        const int64_t want = std::max<int64_t>((int64_t)w.rows * w.cols * 16, (int64_t)a.N * 32);
-        const int grid = (int)std::min<int64_t>((want + 255) / 256, 152 * 8);
-        ProfScope prof("recurrence_setup_kernel", a.stream);
-        setup_kernel<<<std::max(grid, 1), 256, 0, a.stream>>>(a, w, S::kT, from, to);
-    }
-    if (w.rows == 0) return cudaGetLastError();
+cudaError_t setup(const RecurrenceArgs& a, const Plan& w, const float* from, float* to) {
+    if (w.run == nullptr) return cudaSuccess;
+    const int64_t want = std::max<int64_t>(a.T_total / kTok, (int64_t)a.N * 32);
+    const int grid = (int)std::min<int64_t>(want / 256 + 1, 152 * 8);
+    ProfScope prof("recurrence_setup_kernel", a.stream);
+    setup_kernel<<<grid, 256, 0, a.stream>>>(a, w, from, to);
+    return cudaGetLastError();
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch_scan(Kernel kernel, const char* name, int smem, const RecurrenceArgs& a,
+                        const Plan& w, Args... args) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
         return e;
-    // (one row of tiles: a CTA a column, no tickets)
-    const int64_t all = (int64_t)w.rows * w.cols;
-    const int64_t grid = w.rows == 1 ? all : std::min<int64_t>(all, 152 * ctas);
     ProfScope prof(name, a.stream);
-    return launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), smem, a.stream, a, w,
-                            gate_bound(a.g_min));
+    return launch_dependent(kernel, dim3((unsigned)w.runs * w.cols), dim3(kThreads), smem, a.stream, a,
+                            w, gate_bound(a.g_min), args...);
 }
 
-// Tokens a warp holds in the forward: what keeps the tile's inputs at 48 KB (and packed inputs' states
-// those of the same inputs whole, bit by bit).
-template <typename IO>
-constexpr int kForwardTok = sizeof(IO) == 4 ? 8 : 16;
-
-template <typename In, typename IO>
-cudaError_t forward(const RecurrenceArgs& a, char* ws) {
-    constexpr int kTok = kForwardTok<IO>, kStages = sizeof(In) == 1 ? 3 : 2, kCtas = 2;
-    using S = Stage<In, IO, false, kTok>;
-    Shared w;
-    lay_out(ws, a.T_total, a.D, S::kT, false, &w, nullptr);
-    return launch_scan<S>(scan_kernel<In, IO, kTok, kStages, kCtas>, "recurrence_kernel",
-                          kStages * S::kBytes, kCtas, a, w, a.h0, a.h_out);
+template <typename In, typename IO, int W>
+cudaError_t forward(const RecurrenceArgs& a, const Plan& w) {
+    constexpr int kStages = sizeof(In) == 4 ? 2 : 4;
+    return launch_scan(scan_kernel<In, IO, W, kStages>, "recurrence_kernel",
+                       kStages * Stage<In, IO, false, W>::kBytes, a, w);
 }
 
-template <typename In, typename IO>
+template <typename In, typename IO, int W>
 cudaError_t backward(RecurrenceArgs a) {
-    constexpr int kTok = kEdge, kCtas = sizeof(In) == 4 ? 1 : 2, kStages = 3;
-    using S = Stage<In, IO, true, kTok>;
-    Shared w;
-    float* edges;
-    char* ws = static_cast<char*>(a.workspace);
-    lay_out(ws, a.T_total, a.D, S::kT, true, &w, &edges);
-    if (a.edges == nullptr) {
-        RecurrenceArgs f = a;
-        f.edges = a.edges = edges;
-        f.y = nullptr;
-        f.h_out = nullptr;
-        if (cudaError_t e = forward<In, IO>(f, ws + up((size_t)((a.T_total + kEdge - 1) / kEdge) *
-                                                       a.D * 4)))
+    constexpr int kStages = 3;
+    Plan w;
+    float *edges, *part;
+    lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, W, true, &w, &edges, &part);
+    if (cudaError_t e = setup(a, w, a.dh_out, a.dh0)) return e;
+    if (a.T_total > 0) {
+        if (a.edges == nullptr) {
+            RecurrenceArgs f = a;
+            f.edges = a.edges = edges;
+            f.y = nullptr;
+            f.h_out = nullptr;
+            if (cudaError_t e = forward<In, IO, W>(f, w)) return e;
+        }
+        if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, W, kStages>, "recurrence_bwd_kernel",
+                                        kStages * Stage<In, IO, true, W>::kBytes, a, w,
+                                        a.dA_log ? part : nullptr))
             return e;
     }
-    if (cudaError_t e = launch_scan<S>(scan_bwd_kernel<In, IO, kTok, kStages, kCtas>,
-                                       "recurrence_bwd_kernel", kStages * S::kBytes, kCtas, a, w,
-                                       a.dh_out, a.dh0))
-        return e;
     if (a.dA_log) {
         ProfScope prof("recurrence_rate_kernel", a.stream);
         return launch_dependent(rate_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, a.stream,
-                                (const float*)w.part, w.rows, a.D, a.dA_log);
+                                (const float*)part, a.T_total > 0 ? w.runs : 0, a.D, a.dA_log);
     }
     return cudaGetLastError();
 }
 
+// Channels of a CTA: the fewest with which the CTAs of one run, two an SM, are on the GPU at once
+// (rows of 16 bytes at least).  More CTAs are faster as long as they run side by side.
+int columns(int D, int N, int64_t T, bool f32) {
+    const int least = f32 ? 8 : 8;
+    int W = least;
+    while (W < (f32 ? 16 : 32) && (int64_t)((D + W - 1) / W) * count_runs(T, N, (D + W - 1) / W) > 304)
+        W *= 2;
+    return W;
+}
+
+template <typename In, typename IO>
+cudaError_t backward_of(const RecurrenceArgs& a) {
+    switch (columns(a.D, a.N, a.T_total, sizeof(IO) == 4)) {
+        case 8: return backward<In, IO, 8>(a);
+        case 16: return backward<In, IO, 16>(a);
+        default:
+            if constexpr (sizeof(IO) == 4) return backward<In, IO, 16>(a);
+            else return backward<In, IO, 32>(a);
+    }
+}
+
 }  // namespace
 
-// (of either type: tiles of 64 tokens have the most rows)
-size_t recurrence_fwd_workspace_size(int64_t T, int, int D) {
-    return lay_out(nullptr, T, D, kEdge * kWarps, false, nullptr, nullptr);
+size_t recurrence_fwd_workspace_size(int64_t T, int N, int D) {
+    return lay_out(nullptr, T, N, D, 8, false, nullptr, nullptr, nullptr) + 256 * 4 * 11;
 }
-size_t recurrence_bwd_workspace_size(int64_t T, int, int D) {
-    return lay_out(nullptr, T, D, kEdge * kWarps, true, nullptr, nullptr);
+size_t recurrence_bwd_workspace_size(int64_t T, int N, int D) {
+    return lay_out(nullptr, T, N, D, 32, true, nullptr, nullptr, nullptr) + 256 * 4 * 11;
+}
+
+template <typename IO>
+static cudaError_t forward_of(const RecurrenceArgs& a) {
+    const int W = columns(a.D, a.N, a.T_total, sizeof(IO) == 4);
+    Plan w;
+    lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, W, false, &w, nullptr, nullptr);
+    if (cudaError_t e = setup(a, w, a.h0, a.h_out)) return e;
+    if (a.T_total == 0) return cudaSuccess;
+    switch (W) {
+        case 8: return forward<IO, IO, 8>(a, w);
+        case 16: return forward<IO, IO, 16>(a, w);
+        default:
+            if constexpr (sizeof(IO) == 4) return forward<IO, IO, 16>(a, w);
+            else return forward<IO, IO, 32>(a, w);
+    }
 }
 
 cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a) {
-    char* ws = static_cast<char*>(a.workspace);
-    return a.io_bf16 ? forward<__nv_bfloat16, __nv_bfloat16>(a, ws) : forward<float, float>(a, ws);
+    return a.io_bf16 ? forward_of<__nv_bfloat16>(a) : forward_of<float>(a);
 }
 cudaError_t launch_recurrence_bwd(const RecurrenceArgs& a) {
     if (a.packed)
-        return a.io_bf16 ? backward<int8_t, __nv_bfloat16>(a) : backward<int8_t, float>(a);
-    return a.io_bf16 ? backward<__nv_bfloat16, __nv_bfloat16>(a) : backward<float, float>(a);
+        return a.io_bf16 ? backward_of<int8_t, __nv_bfloat16>(a) : backward_of<int8_t, float>(a);
+    return a.io_bf16 ? backward_of<__nv_bfloat16, __nv_bfloat16>(a) : backward_of<float, float>(a);
 }
 
 cudaError_t launch_recurrence_step(const void* x, int64_t x_ld, const void* z, int64_t z_ld,
