@@ -289,15 +289,15 @@ __device__ __forceinline__ bool constant(float P) { return __float_as_int(P) < 0
 
 template <bool kCut>
 __device__ __forceinline__ float2 apply(float4 m, float2 h) {
-    const float2 r = fma2(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
+    const float2 r = fma_pair(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
     if (kCut && constant(m.x)) return make_float2(m.z, m.w);
     return r;
 }
 // The map that applies `before` and then m.
 template <bool kCut>
 __device__ __forceinline__ float4 after(float4 m, float4 before) {
-    const float2 P = mul2(make_float2(m.x, m.y), make_float2(before.x, before.y));
-    const float2 H = fma2(make_float2(m.x, m.y), make_float2(before.z, before.w),
+    const float2 P = mul_pair(make_float2(m.x, m.y), make_float2(before.x, before.y));
+    const float2 H = fma_pair(make_float2(m.x, m.y), make_float2(before.z, before.w),
                           make_float2(m.z, m.w));
     if (kCut && constant(m.x)) return m;
     if (kCut && constant(before.x)) return make_float4(-0.f, -0.f, H.x, H.y);
@@ -455,16 +455,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         a, w, ring, begin, end, c0,
         [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
             float2 P = both(1.f), H = both(0.f);
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-                const Step u = recurrence_step(v.input(0, k), v.input(1, k), v.input(2, k), nl, gb);
-                c[k] = u.c;
-                nb[k] = u.nb;
-            }
+            recurrence_steps([&](int which, int k) { return v.input(which, k); }, nl, gb, c, nb);
             if ((marks & 0xffu) == 0u) {
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) {
-                    P = fma2(c[k], P, P);
+                    P = fma_pair(c[k], P, P);
                     H = recurrence_next(c[k], nb[k], H);
                 }
             } else {
@@ -478,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
 #pragma unroll
                     for (int k = 0; k < kTok; ++k)
                         if (marks >> k & 1)
-                            nb[k] = mul2(recurrence_next(c[k], nb[k], h0[k]), both(-1.f));
+                            nb[k] = mul_pair(recurrence_next(c[k], nb[k], h0[k]), both(-1.f));
                 }
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) {
@@ -552,36 +547,31 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             a, w, ring, begin, end, c0,
             [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
                 // the negated factors of l in the gradients, from the states
-                float2 h = v.edge();
-#pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                    if (marks >> k & 1)
-                        h = a.h0 && live ? state_row(a.h0, start_at(w, t + k), a.D, ch) : both(0.f);
-                    const float2 x = v.input(0, k);
-                    const StepGrad u = recurrence_grad(x, v.input(1, k), v.input(2, k), r, gb, h);
-                    c[k] = u.c;
-                    fx[k] = u.dx;
-                    fz[k] = u.dz;
-                    fi[k] = u.di;
-                    h = recurrence_next(u.c, mul2(u.dx, x), h);
-                }
+                recurrence_grads(
+                    [&](int which, int k) { return v.input(which, k); }, r, gb, v.edge(),
+                    [&](int k, float2 h) {
+                        if (marks >> k & 1)
+                            h = a.h0 && live ? state_row(a.h0, start_at(w, t + k), a.D, ch) : both(0.f);
+                        return h;
+                    },
+                    c, fx, fz, fi);
                 float2 P = both(1.f), H = both(0.f);
                 if ((marks & 0xff00u) == 0u) {
 #pragma unroll
                     for (int k = kTok - 1; k >= 0; --k) {
-                        P = fma2(c[k], P, P);
-                        const float2 l = fma2(v.dy(k), both(-1.f), H);
-                        H = fma2(c[k], l, l);
+                        P = fma_pair(c[k], P, P);
+                        const float2 l = fma_pair(v.dy(k), both(-1.f), H);
+                        H = fma_pair(c[k], l, l);
                     }
                 } else {
 #pragma unroll
                     for (int k = kTok - 1; k >= 0; --k) {
                         if (marks >> (8 + k) & 1)
                             H = a.dh_out && live
-                                    ? mul2(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
+                                    ? mul_pair(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
                                     : both(0.f);
-                        const float2 l = fma2(v.dy(k), both(-1.f), H);
-                        H = fma2(c[k], l, l);
+                        const float2 l = fma_pair(v.dy(k), both(-1.f), H);
+                        H = fma_pair(c[k], l, l);
                     }
                     P = both(-0.f);
                 }
@@ -602,21 +592,21 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
 #pragma unroll
                 for (int k = kTok - 1; k >= 0; --k) {
                     if (marks >> (8 + k) & 1)
-                        nr = a.dh_out ? mul2(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
+                        nr = a.dh_out ? mul_pair(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
                                       : both(0.f);
-                    const float2 l = fma2(v.dy(k), both(-1.f), nr);
-                    nr = fma2(c[k], l, l);
+                    const float2 l = fma_pair(v.dy(k), both(-1.f), nr);
+                    nr = fma_pair(c[k], l, l);
                     if (marked && (t + k < begin || t + k >= end)) continue;
                     const int64_t o = (int64_t)k * a.D;
-                    const float2 g = mul2(l, fz[k]), z = v.input(1, k);
-                    store_pair(dx + o, mul2(l, fx[k]));
+                    const float2 g = mul_pair(l, fz[k]), z = v.input(1, k);
+                    store_pair(dx + o, mul_pair(l, fx[k]));
                     store_pair(dz + o, g);
-                    store_pair(di + o, mul2(l, fi[k]));
+                    store_pair(di + o, mul_pair(l, fi[k]));
                     // (an infinite z has a gradient of zero)
                     dA.x += g.x == 0.f ? 0.f : g.x * z.x;
                     dA.y += g.y == 0.f ? 0.f : g.y * z.y;
                     if (marks >> k & 1 && a.dh0)
-                        store_pair(a.dh0 + (int64_t)start_at(w, t + k) * a.D + ch, mul2(nr, both(-1.f)));
+                        store_pair(a.dh0 + (int64_t)start_at(w, t + k) * a.D + ch, mul_pair(nr, both(-1.f)));
                 }
             });
     }
@@ -629,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     if (threadIdx.x < S::kLanes && live) {
         float2 s = both(0.f);
 #pragma unroll 8
-        for (int g = 0; g < S::kGroups; ++g) s = add2(s, sums[g * S::kLanes + lane]);
+        for (int g = 0; g < S::kGroups; ++g) s = add_pair(s, sums[g * S::kLanes + lane]);
         *reinterpret_cast<float2*>(part + (int64_t)(blockIdx.x / w.cols) * a.D + ch) = s;
     }
 }
@@ -698,14 +688,17 @@ __global__ void __launch_bounds__(128) step_kernel(const IO* x, int64_t x_ld, co
     if (slot >= 0) {
         float4* hp = reinterpret_cast<float4*>(h + slot * D + c);
         v = *hp;
-        auto next = [&](float2 xe, float2 ze, float2 ie, float2 Ae, float2 he) {
-            const Step s = recurrence_step(xe, ze, ie, channel_rate(Ae, 0.f).neg_log2, gb);
-            return recurrence_next(s.c, s.nb, he);
+        const float2 in[3][2] = {{make_float2(xv.x, xv.y), make_float2(xv.z, xv.w)},
+                                 {make_float2(zv.x, zv.y), make_float2(zv.z, zv.w)},
+                                 {make_float2(iv.x, iv.y), make_float2(iv.z, iv.w)}};
+        auto next = [&](int j, float2 Ae, float2 he) {
+            float2 cc[1], nb[1];
+            recurrence_steps([&](int which, int) { return in[which][j]; },
+                             channel_rate(Ae, 0.f).neg_log2, gb, cc, nb);
+            return recurrence_next(cc[0], nb[0], he);
         };
-        const float2 a = next(make_float2(xv.x, xv.y), make_float2(zv.x, zv.y),
-                              make_float2(iv.x, iv.y), make_float2(A.x, A.y), make_float2(v.x, v.y));
-        const float2 b = next(make_float2(xv.z, xv.w), make_float2(zv.z, zv.w),
-                              make_float2(iv.z, iv.w), make_float2(A.z, A.w), make_float2(v.z, v.w));
+        const float2 a = next(0, make_float2(A.x, A.y), make_float2(v.x, v.y));
+        const float2 b = next(1, make_float2(A.z, A.w), make_float2(v.z, v.w));
         v = make_float4(a.x, a.y, b.x, b.y);
         *hp = v;
     }

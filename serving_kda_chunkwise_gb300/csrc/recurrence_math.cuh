@@ -30,13 +30,17 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Pairs of numbers in one instruction.
+__device__ __forceinline__ float2 add_pair(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 ex2_pair(float2 x) {
     return make_float2(ex2_approx(x.x), ex2_approx(x.y));
 }
 // 1 / (1 + e)
 __device__ __forceinline__ float2 rcp1_pair(float2 e) {
-    e = add2(e, both(1.f));
+    e = add_pair(e, both(1.f));
     return make_float2(rcp_approx(e.x), rcp_approx(e.y));
 }
 
@@ -51,18 +55,18 @@ inline GateBound gate_bound(float g_min) {
     return b;
 }
 
-// e^g - 1 for g = w 2^doublings, w in [-1.25, 0].
-__device__ __forceinline__ float2 expm1_pair(float2 w, int doublings) {
-    float2 p = fma2(w, both(1.1634889e-4f), both(1.2614741e-3f));
-    p = fma2(w, p, both(8.2301879e-3f));
-    p = fma2(w, p, both(4.1622911e-2f));
-    p = fma2(w, p, both(1.6665773e-1f));
-    p = fma2(w, p, both(4.9999931e-1f));
-    p = fma2(w, p, both(1.f));
-    float2 c = mul2(w, p);
-    for (; doublings > 0; --doublings) c = fma2(c, c, add2(c, c));
-    return c;
+// e^w - 1 for w in [-1.25, 0].
+__device__ __forceinline__ float2 expm1_near(float2 w) {
+    float2 p = fma_pair(w, both(1.1634889e-4f), both(1.2614741e-3f));
+    p = fma_pair(w, p, both(8.2301879e-3f));
+    p = fma_pair(w, p, both(4.1622911e-2f));
+    p = fma_pair(w, p, both(1.6665773e-1f));
+    p = fma_pair(w, p, both(4.9999931e-1f));
+    p = fma_pair(w, p, both(1.f));
+    return mul_pair(w, p);
 }
+// e^{2w} - 1 from e^w - 1
+__device__ __forceinline__ float2 twice(float2 c) { return fma_pair(c, c, add_pair(c, c)); }
 
 // Per pair of channels: what turns z into exponents of two (-e^A log2(e)), and e^A g_min.
 struct ChannelRate {
@@ -70,51 +74,76 @@ struct ChannelRate {
 };
 __device__ __forceinline__ ChannelRate channel_rate(float2 A_log, float g_min) {
     const float2 r = make_float2(expf(A_log.x), expf(A_log.y));
-    return ChannelRate{mul2(r, both(-kLog2e)), mul2(r, both(g_min))};
+    return ChannelRate{mul_pair(r, both(-kLog2e)), mul_pair(r, both(g_min))};
 }
 
-// c and the negated input term -b.
-struct Step {
-    float2 c, nb;
-};
-__device__ __forceinline__ Step recurrence_step(float2 x, float2 z, float2 i, float2 neg_log2,
-                                                const GateBound& gb) {
-    const float2 sz = rcp1_pair(ex2_pair(mul2(z, neg_log2)));
-    const float2 si = rcp1_pair(ex2_pair(mul2(i, both(-kLog2e))));
-    const float2 c = expm1_pair(mul2(sz, both(gb.scaled)), gb.doublings);
-    const float2 d = fma2(c, c, add2(c, c));  // -m^2
-    // (below 1e-37, where the root would be of a denormal number, the factor is next to nothing)
-    const float2 q = make_float2(rsqrt_approx(fmaxf(-d.x, 1e-37f)), rsqrt_approx(fmaxf(-d.y, 1e-37f)));
-    return Step{c, mul2(mul2(d, q), mul2(si, x))};
+// 1 / sqrt(-d).  (Below 1e-37, where the root would be of a denormal number, what is multiplied by it
+// is next to nothing.)
+__device__ __forceinline__ float2 rsqrt_pair(float2 d) {
+    return make_float2(rsqrt_approx(fmaxf(-d.x, 1e-37f)), rsqrt_approx(fmaxf(-d.y, 1e-37f)));
+}
+
+// n tokens in steps that leave the tokens independent of each other: c[k], and the negated input
+// terms nb[k] = -b.  in(which, k): input x, z or i (0, 1, 2) of token k.
+template <int n, typename In>
+__device__ __forceinline__ void recurrence_steps(In&& in, float2 neg_log2, const GateBound& gb,
+                                                 float2 (&c)[n], float2 (&nb)[n]) {
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+        const float2 sz = rcp1_pair(ex2_pair(mul_pair(in(1, k), neg_log2)));
+        const float2 si = rcp1_pair(ex2_pair(mul_pair(in(2, k), both(-kLog2e))));
+        c[k] = expm1_near(mul_pair(sz, both(gb.scaled)));
+        nb[k] = mul_pair(si, in(0, k));
+    }
+    for (int j = gb.doublings; j > 0; --j)
+#pragma unroll
+        for (int k = 0; k < n; ++k) c[k] = twice(c[k]);
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+        const float2 d = twice(c[k]);  // -m^2
+        nb[k] = mul_pair(mul_pair(d, rsqrt_pair(d)), nb[k]);
+    }
 }
 // h_t from h_{t-1}
 __device__ __forceinline__ float2 recurrence_next(float2 c, float2 nb, float2 h) {
-    return fma2(nb, both(-1.f), fma2(c, h, h));
+    return fma_pair(nb, both(-1.f), fma_pair(c, h, h));
 }
 
-// c, and the negated factors of l_t = dL/dh_t in the gradients, for the state h before the token
-// (that of dx is -b / x).
-struct StepGrad {
-    float2 c, dx, di, dz;
-};
-__device__ __forceinline__ StepGrad recurrence_grad(float2 x, float2 z, float2 i,
-                                                    const ChannelRate& r, const GateBound& gb,
-                                                    float2 h) {
-    const float2 ez = ex2_pair(mul2(z, r.neg_log2)), ei = ex2_pair(mul2(i, both(-kLog2e)));
-    const float2 sz = rcp1_pair(ez), si = rcp1_pair(ei);
-    // 1 - s = e^{-..} s, the exponential limited so that it stays a number where s is zero
-    const float2 oz = mul2(make_float2(fminf(ez.x, 3e38f), fminf(ez.y, 3e38f)), sz);
-    const float2 oi = mul2(make_float2(fminf(ei.x, 3e38f), fminf(ei.y, 3e38f)), si);
-    StepGrad o;
-    o.c = expm1_pair(mul2(sz, both(gb.scaled)), gb.doublings);
-    const float2 d = fma2(o.c, o.c, add2(o.c, o.c));
-    const float2 q = make_float2(rsqrt_approx(fmaxf(-d.x, 1e-37f)), rsqrt_approx(fmaxf(-d.y, 1e-37f)));
-    const float2 a = add2(o.c, both(1.f)), m = mul2(d, q), u = mul2(si, x);
-    o.dx = mul2(m, si);
-    o.di = mul2(mul2(m, u), oi);
-    // e^A g (1 - s(e^A z)) e^g (e^g / m s(i) x - h)
-    o.dz = mul2(mul2(mul2(r.rate_g, sz), mul2(oz, a)), fma2(h, both(-1.f), mul2(a, mul2(q, u))));
-    return o;
+// The same for the gradients: c[k], and the negated factors of l_t = dL/dh_t in those of x, z and i.
+// before(k, h): the state before token k, where h follows from the tokens before it.
+template <int n, typename In, typename Before>
+__device__ __forceinline__ void recurrence_grads(In&& in, const ChannelRate& r, const GateBound& gb,
+                                                 float2 h, Before&& before, float2 (&c)[n],
+                                                 float2 (&fx)[n], float2 (&fz)[n], float2 (&fi)[n]) {
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+        const float2 ez = ex2_pair(mul_pair(in(1, k), r.neg_log2));
+        const float2 ei = ex2_pair(mul_pair(in(2, k), both(-kLog2e)));
+        const float2 sz = rcp1_pair(ez), si = rcp1_pair(ei);
+        // 1 - s = e^{-..} s, the exponential limited so that it stays a number where s is zero
+        const float2 oz = mul_pair(make_float2(fminf(ez.x, 3e38f), fminf(ez.y, 3e38f)), sz);
+        const float2 oi = mul_pair(make_float2(fminf(ei.x, 3e38f), fminf(ei.y, 3e38f)), si);
+        c[k] = expm1_near(mul_pair(sz, both(gb.scaled)));
+        fx[k] = si;
+        fz[k] = mul_pair(mul_pair(r.rate_g, sz), oz);
+        fi[k] = oi;
+    }
+    for (int j = gb.doublings; j > 0; --j)
+#pragma unroll
+        for (int k = 0; k < n; ++k) c[k] = twice(c[k]);
+#pragma unroll
+    for (int k = 0; k < n; ++k) {
+        const float2 d = twice(c[k]), q = rsqrt_pair(d);  // -m^2, 1 / m
+        const float2 a = add_pair(c[k], both(1.f)), m = mul_pair(d, q);
+        const float2 u = mul_pair(fx[k], in(0, k)), mu = mul_pair(m, u);
+        fx[k] = mul_pair(m, fx[k]);
+        fi[k] = mul_pair(mu, fi[k]);
+        // e^A g (1 - s(e^A z)) e^g (e^g / m s(i) x - h)
+        h = before(k, h);
+        fz[k] = mul_pair(mul_pair(fz[k], a),
+                         fma_pair(h, both(-1.f), mul_pair(a, mul_pair(q, u))));
+        h = recurrence_next(c[k], mu, h);
+    }
 }
 
 }  // namespace kda
