@@ -4,12 +4,14 @@
 //   h_t = a_t h_{t-1} + b_t,   a = e^g, b = sqrt(1 - e^{2g}) s(i) x          (recurrence_math.cuh)
 //   l_t = dy_t + a_{t+1} l_{t+1}, backwards, for the gradients
 //
-// Both are scans of affine maps (P, H): h -> P h + H.  A CTA takes W channels along a run, some
-// consecutive sequences, tile by tile, and carries their state in registers.  In a tile a thread
-// holds 8 tokens of two channels; a warp's threads compose their maps by shuffles, the warps' maps
-// meet in shared memory (two buffers, so one barrier a tile), and every thread applies those before
-// it to the carried state, goes over its tokens again and writes.  So inputs are read once, results
-// written once, and no CTA waits for another.
+// Both are scans of affine maps (P, H): h -> P h + H.  A cluster of CTAs takes 64 channels along a
+// run, some consecutive sequences, and carries their state in registers.  In a step each of its CTAs
+// has a tile of 64 tokens: a warp holds 8 tokens, a lane two channels.  The warps' maps meet in
+// shared memory; the tile's map is sent to every CTA of the cluster (distributed shared memory, two
+// buffers, one cluster barrier a step); every thread applies the maps before it to the carried
+// state, goes over its tokens again, in registers, and writes.  So inputs are read once, results
+// written once, in rows of 128 bytes (bf16), and no cluster waits for another.  (Narrower columns
+// instead of clusters cost more in the loads and stores of short rows than the barrier does.)
 //
 // The gradients go over the tiles backwards.  A thread's states come from the edges, the state that
 // every 8th token starts from, which the forward writes on request; without them a forward that
@@ -32,8 +34,10 @@ namespace {
 using namespace tc;
 
 constexpr int kTok = 8;     // tokens a thread holds, and from one edge to the next
-constexpr int kGroup = 64;  // channels that share an exponent of packed inputs
+constexpr int kC = 64;      // channels of a tile, and of an exponent of packed inputs
 constexpr int kWarps = 8;
+constexpr int kT = kTok * kWarps;  // tokens of a tile
+constexpr int kMaxCluster = 8;
 constexpr int kThreads = 32 * kWarps;
 
 // What the setup launch leaves for the scan.
@@ -46,29 +50,15 @@ struct Plan {
 
 // ---------------------------------------------------------------- inputs --
 
-// A stage of the ring: the inputs of a tile of kT tokens x W channels.  Where a row has less than 128
-// bytes, the places of token k of a group of 8 are permuted with the group, which keeps a warp's
-// groups in different banks.
-template <typename In, typename IO, bool kBwd, int W>
+// A stage of the ring: the inputs of a tile.
+template <typename In, typename IO, bool kBwd>
 struct Stage {
-    static constexpr int kLanes = W / 2;               // of a row
-    static constexpr int kSplit = 32 / kLanes;         // groups of 8 tokens in a warp
-    static constexpr int kGroups = kWarps * kSplit;
-    static constexpr int kT = kGroups * kTok;
-    static constexpr int kIn = kT * W * (int)sizeof(In);
+    static constexpr int kIn = kT * kC * (int)sizeof(In);
     static constexpr int kDy = 3 * kIn;
-    static constexpr int kEdges = kDy + (kBwd ? kT * W * (int)sizeof(IO) : 0);
-    static constexpr int kMarks = kEdges + (kBwd ? kGroups * W * 4 : 0);
-    static constexpr int kExps = kMarks + kGroups * 4;
-    static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT : 0) + 127) / 128 * 128;
-    static constexpr int kExpsEach = (3 * kT + kThreads - 1) / kThreads;  // a thread's
-    static_assert(kIn % 128 == 0 && kEdges % 128 == 0 && kMarks % 16 == 0, "");
+    static constexpr int kMarks = kDy + (kBwd ? kT * kC * (int)sizeof(IO) : 0);
+    static constexpr int kExps = kMarks + kWarps * 4;
+    static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT : 0) + 15) / 16 * 16;
 };
-
-// The place of token k of a group, for rows of `bytes` bytes: k with some bits of the group's number.
-__device__ __forceinline__ constexpr int place_bits(int bytes) {
-    return bytes >= 128 ? 0 : 128 / bytes - 1 > kTok - 1 ? kTok - 1 : 128 / bytes - 1;
-}
 
 template <int kBytes>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool live) {
@@ -85,77 +75,52 @@ __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-// kT tokens x W channels of a tensor; rows and channels past its end become zeros.
-template <typename In, int W, int kT>
+// 64 tokens x 64 channels of a tensor; rows and channels past its end become zeros.
+template <typename In>
 __device__ __forceinline__ void load_tile(char* dst, const void* src, int64_t ld, int64_t t0, int c0,
                                           int64_t T, int D) {
     // (rows of codes begin on 8 bytes only)
     constexpr int kPiece = sizeof(In) == 1 ? 8 : 16, kElems = kPiece / (int)sizeof(In);
-    constexpr int kPer = W / kElems, kStep = kThreads / kPer;
+    constexpr int kPer = kC / kElems, kStep = kThreads / kPer;
     const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * kElems;
     const int left = (int)min((int64_t)kT, T - t0) - row;  // rows left from this thread's first
     const bool in = c0 + c < D;
     const In* s = static_cast<const In*>(src) + (t0 + row) * ld + c0 + c;
-    const uint32_t d = smem_u32(dst);
+    const uint32_t d = smem_u32(dst) + (row * kC + c) * (int)sizeof(In);
 #pragma unroll
-    for (int k = 0; k < (kT + kStep - 1) / kStep; ++k) {
-        const int r = row + k * kStep;
-        if (kT % kStep != 0 && r >= kT) break;
+    for (int k = 0; k < kT / kStep; ++k) {
         const bool live = in && k * kStep < left;
-        const int at = r ^ (r / kTok & place_bits(W * (int)sizeof(In)));
-        copy_async<kPiece>(d + (at * W + c) * (int)sizeof(In), live ? s : src, live);
+        copy_async<kPiece>(d + k * kStep * kC * (int)sizeof(In), live ? s : src, live);
         s += kStep * ld;
     }
 }
 
-// The exponents of packed inputs that a thread has to put into a stage.
-template <int n>
-struct Exps {
-    int8_t e[n];
-};
-
-// Starts the loads of the tile from token t0 and channel c0.
-template <typename S, typename In, typename IO, bool kBwd, int W>
-__device__ __forceinline__ void load_stage(const RecurrenceArgs& a, const Plan& w, char* st,
-                                           int64_t t0, int c0, Exps<S::kExpsEach>& exps) {
-    load_tile<In, W, S::kT>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D);
-    load_tile<In, W, S::kT>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D);
-    load_tile<In, W, S::kT>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D);
-    if (kBwd) {
-        load_tile<IO, W, S::kT>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D);
-        constexpr int kPer = W / 4;
-        for (int n = threadIdx.x; n < S::kGroups * kPer; n += kThreads) {
-            const int e = n / kPer, c = n % kPer * 4;
-            const bool live = t0 + e * kTok < a.T_total && c0 + c < a.D;
-            copy_async<16>(smem_u32(st + S::kEdges) + (e * W + c) * 4,
-                           a.edges + (live ? (t0 / kTok + e) * a.D + c0 + c : 0), live);
-        }
-    }
-    // (a group's marks by the thread that looks at them before the barrier)
-    if (w.marks && threadIdx.x % S::kLanes == 0) {
-        const int g = threadIdx.x / S::kLanes;
+// Starts the loads of the tile from token t0 and channel c0.  Of packed inputs, the exponent that
+// this thread has to put into the stage is returned.
+template <typename S, typename In, typename IO, bool kBwd>
+__device__ __forceinline__ int load_stage(const RecurrenceArgs& a, const Plan& w, char* st,
+                                          int64_t t0, int c0) {
+    load_tile<In>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D);
+    load_tile<In>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D);
+    load_tile<In>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D);
+    if (kBwd) load_tile<IO>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D);
+    // (a warp's marks by the thread that looks at them before the barrier)
+    if (w.marks && threadIdx.x % 32 == 0) {
+        const int g = threadIdx.x / 32;
         const bool live = t0 + g * kTok < a.T_total;
         copy_async<4>(smem_u32(st + S::kMarks) + g * 4, w.marks + (live ? t0 / kTok + g : 0), live);
     }
-    if constexpr (sizeof(In) == 1) {
-#pragma unroll
-        for (int j = 0; j < S::kExpsEach; ++j) {
-            const int n = j * kThreads + threadIdx.x, k = n / S::kT, t = n % S::kT;
-            const int8_t* e = k == 0 ? a.x_exps : k == 1 ? a.z_exps : a.i_exps;
-            exps.e[j] = 0;
-            if (n < 3 * S::kT && t0 + t < a.T_total)
-                exps.e[j] = __ldg(e + (int64_t)(c0 / kGroup) * a.T_total + t0 + t);
-        }
+    if (sizeof(In) == 1 && threadIdx.x < 3 * kT) {
+        const int k = threadIdx.x / kT, t = threadIdx.x % kT;
+        const int8_t* e = k == 0 ? a.x_exps : k == 1 ? a.z_exps : a.i_exps;
+        if (t0 + t < a.T_total) return __ldg(e + (int64_t)(c0 / kC) * a.T_total + t0 + t);
     }
+    return 0;
 }
 template <typename S, typename In>
-__device__ __forceinline__ void put_exps(char* st, const Exps<S::kExpsEach>& exps) {
-    if constexpr (sizeof(In) == 1) {
-#pragma unroll
-        for (int j = 0; j < S::kExpsEach; ++j)
-            if (j * kThreads + threadIdx.x < 3 * S::kT)
-                reinterpret_cast<int8_t*>(st)[S::kExps + j * kThreads + threadIdx.x] = exps.e[j];
-    }
+__device__ __forceinline__ void put_exps(char* st, int e) {
+    if (sizeof(In) == 1 && threadIdx.x < 3 * kT)
+        reinterpret_cast<int8_t*>(st)[S::kExps + threadIdx.x] = (int8_t)e;
 }
 
 __device__ __forceinline__ float2 pair(const __nv_bfloat16* p) {
@@ -166,23 +131,21 @@ __device__ __forceinline__ float2 pair(const float* p) {
     return *reinterpret_cast<const float2*>(p);
 }
 
-// A thread's view of a stage: token k of its group, its two channels.
-template <typename S, typename In, typename IO, int W>
+// A thread's view of a stage: token k of its warp, its two channels.
+template <typename S, typename In, typename IO>
 struct View {
     const char* st;
-    int group, lane;  // group of 8 tokens, lane of the row
+    int warp, lane;
+    float2 edge;  // (gradients) the state before the warp's tokens
     template <typename E>
     __device__ __forceinline__ const E* at(int part, int k) const {
-        constexpr int kRow = W * (int)sizeof(E);
-        const int base = group * kTok * kRow + (group & place_bits(kRow)) * kRow + 2 * lane * (int)sizeof(E);
-        return reinterpret_cast<const E*>(st + part + (base ^ k * kRow));
+        return reinterpret_cast<const E*>(st + part) + (warp * kTok + k) * kC + 2 * lane;
     }
     __device__ __forceinline__ float2 input(int which, int k) const {
         const In* p = at<In>(which * S::kIn, k);
         if constexpr (sizeof(In) == 1) {
             const char2 q = *reinterpret_cast<const char2*>(p);
-            const int e =
-                reinterpret_cast<const int8_t*>(st)[S::kExps + which * S::kT + group * kTok + k];
+            const int e = reinterpret_cast<const int8_t*>(st)[S::kExps + which * kT + warp * kTok + k];
             // 2^e, denormal at -127; -128 stands for NaN
             const float s =
                 __int_as_float(e > -127 ? (e + 127) << 23 : e == -127 ? 1 << 22 : 0x7fc00000);
@@ -192,12 +155,9 @@ struct View {
         }
     }
     __device__ __forceinline__ float2 dy(int k) const { return pair(at<IO>(S::kDy, k)); }
-    __device__ __forceinline__ float2 edge() const {
-        return pair(reinterpret_cast<const float*>(st + S::kEdges) + group * W + 2 * lane);
-    }
-    // the marks of the group whose first token is t, of a batch of T tokens
+    // the marks of the warp's tokens, the first of which is t, of a batch of T tokens
     __device__ __forceinline__ uint32_t marks(const Plan& w, int64_t t, int64_t T) const {
-        if (w.marks) return reinterpret_cast<const uint32_t*>(st + S::kMarks)[group];
+        if (w.marks) return reinterpret_cast<const uint32_t*>(st + S::kMarks)[warp];
         return (t == 0 ? 1u : 0u) | (T > t && T <= t + kTok ? 256u << (T - 1 - t) : 0u);
     }
 };
@@ -303,109 +263,155 @@ __device__ __forceinline__ float4 after(float4 m, float4 before) {
     if (kCut && constant(before.x)) return make_float4(-0.f, -0.f, H.x, H.y);
     return make_float4(P.x, P.y, H.x, H.y);
 }
-template <int kUp>
-__device__ __forceinline__ float4 shift(float4 m) {
-    constexpr unsigned kAll = 0xffffffffu;
-    if (kUp > 0)
-        return make_float4(__shfl_up_sync(kAll, m.x, kUp), __shfl_up_sync(kAll, m.y, kUp),
-                           __shfl_up_sync(kAll, m.z, kUp), __shfl_up_sync(kAll, m.w, kUp));
-    return make_float4(__shfl_down_sync(kAll, m.x, -kUp), __shfl_down_sync(kAll, m.y, -kUp),
-                       __shfl_down_sync(kAll, m.z, -kUp), __shfl_down_sync(kAll, m.w, -kUp));
+__device__ __forceinline__ float4 identity() { return make_float4(1.f, 1.f, 0.f, 0.f); }
+
+// What a CTA keeps of a step's maps.
+struct Maps {
+    float4 warps[kWarps][32];             // of its own tile
+    float4 tiles[2][kMaxCluster][32];     // of the cluster's, in the scan's order; alternating
+};
+
+__device__ __forceinline__ unsigned cluster_rank() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+    unsigned r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Writes v to p's place in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_remote(float4* p, unsigned rank, float4 v) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// In a warp: m becomes the map of the groups of tokens before the thread's (in the scan's order: rank
-// 0 first), and the warp's whole map goes to *out.
-template <bool kCut, bool kBwd, int kLanes>
-__device__ __forceinline__ void scan_warp(float4& m, int rank, float4* out) {
-    constexpr int kSplit = 32 / kLanes, kDir = kBwd ? -1 : 1;
-#define KDA_SCAN_STEP(o)                                        \
-    if constexpr (kSplit > o) {                                 \
-        const float4 b = shift<kDir * kLanes * o>(m);           \
-        if (rank >= o) m = after<kCut>(m, b);                   \
-    }
-    KDA_SCAN_STEP(1)
-    KDA_SCAN_STEP(2)
-    KDA_SCAN_STEP(4)
-#undef KDA_SCAN_STEP
-    if (rank == kSplit - 1) *out = m;
-    if constexpr (kSplit > 1) m = shift<kDir * kLanes>(m);
-    if (rank == 0) m = make_float4(1.f, 1.f, 0.f, 0.f);
-}
-
-// From the state before the tile, that before the thread's tokens; carry: the state after the tile.
-template <bool kCut, int kLanes>
-__device__ __forceinline__ float2 scan_tile(const float4 (*maps)[kLanes], int turn, int lane,
-                                            float4 before, float2& carry) {
-    float2 h = carry, mine = carry;
+// With the warps' maps there: the map of those before `turn` (in the scan's order), and the tile's
+// map to the CTAs of the cluster (one each, by as many warps).
+template <bool kCut>
+__device__ __forceinline__ float4 compose(Maps& m, int buf, int turn, int lane, unsigned rank,
+                                          unsigned ctas) {
+    float4 all = identity(), before = all;
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) {
-        if (j == turn) mine = h;
-        h = apply<kCut>(maps[j][lane], h);
+        if (j == turn) before = all;
+        if (j < turn || (unsigned)turn < ctas) all = after<kCut>(m.warps[j][lane], all);
+    }
+    if ((unsigned)turn < ctas) store_remote(&m.tiles[buf][rank][lane], turn, all);
+    return before;
+}
+
+// The state before the thread's tokens; carry: from before the step's tiles to after them.
+__device__ __forceinline__ float2 start_state(const Maps& m, int buf, int lane, float4 before,
+                                              unsigned rank, unsigned ctas, bool marked,
+                                              float2& carry) {
+    float2 h = carry, mine = carry;
+#pragma unroll
+    for (unsigned j = 0; j < kMaxCluster; ++j) {
+        if (j >= ctas) break;
+        if (j == rank) mine = h;
+        h = apply<true>(m.tiles[buf][j][lane], h);
     }
     carry = h;
-    return apply<kCut>(before, mine);
+    return marked ? apply<true>(before, mine) : apply<false>(before, mine);
 }
 
 // ------------------------------------------------------------- the loop --
 
-// Runs first(view, t0, marks, marked, buf), a barrier and second(..) over the tiles of a CTA's run,
-// their inputs loaded ahead.  marked: some token of the tile starts or ends a sequence; buf
-// alternates.  kHeld: second() reads the stage too.
-template <typename S, typename In, typename IO, bool kBwd, int W, int kStages, bool kHeld,
-          typename First, typename Second>
-__device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w, char* ring, int begin,
-                                          int end, int c0, First&& first, Second&& second) {
-    // Loads go out right after the barrier, into the stage that is free then: the tile's own, or where
+// Runs first(view, t0, marks), which leaves the warp's map, and second(view, t0, marks, marked, state
+// before the warp's tokens) over the tiles of a CTA in its cluster's run, their inputs loaded ahead.
+// marked: some token of the tile starts or ends a sequence.  kHeld: second() reads the stage too.
+template <typename S, typename In, typename IO, bool kBwd, int kStages, bool kHeld, typename First,
+          typename Second>
+__device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w, char* ring, Maps& maps,
+                                          int begin, int end, int c0, First&& first, Second&& second) {
+    // Loads go out after the CTA's barrier, into the stage that is free then: the tile's own, or where
     // that is still read, the one before it.
     constexpr int kAhead = kHeld ? kStages - 1 : kStages;  // tiles from the one worked on
     static_assert(kAhead >= 2, "the next tile is on its way before the barrier");
-    const int base = begin / kTok * kTok, n = (end - base + S::kT - 1) / S::kT;
-    auto first_token = [&](int k) { return base + (kBwd ? n - 1 - k : k) * S::kT; };
-    Exps<S::kExpsEach> exps;
+    const unsigned rank = cluster_rank(), ctas = cluster_size();
+    const int base = begin / kTok * kTok, n = (end - base + kT - 1) / kT;
+    const int steps = (n + (int)ctas - 1) / (int)ctas;
+    // step k's tile, in the scan's order; there may be none left for this CTA
+    auto place = [&](int k) { return k * (int)ctas + (int)rank; };
+    auto first_token = [&](int k) { return base + (kBwd ? n - 1 - place(k) : place(k)) * kT; };
     auto load = [&](int k, int s) {
-        if (k < n) load_stage<S, In, IO, kBwd, W>(a, w, ring + s * S::kBytes, first_token(k), c0, exps);
+        int e = 0;
+        if (place(k) < n)
+            e = load_stage<S, In, IO, kBwd>(a, w, ring + s * S::kBytes, first_token(k), c0);
         copy_commit();
+        return e;
     };
-    const int group = threadIdx.x / S::kLanes, lane = threadIdx.x % S::kLanes;
-    // whether tile k, in stage s, has marks that this thread has copied (or its run ends in it)
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int turn = kBwd ? kWarps - 1 - warp : warp;  // in the scan's order
+    // whether step k's tile, in stage s, has marks that this thread has copied (or its run ends in it)
     auto look = [&](int k, int s) {
-        if (k >= n) return false;
+        if (place(k) >= n) return false;
         const int t0 = first_token(k);
-        if (t0 < begin || t0 + S::kT > end || (w.marks == nullptr && (t0 == 0 || t0 + S::kT == end)))
+        if (t0 < begin || t0 + kT > end || (w.marks == nullptr && (t0 == 0 || t0 + kT == end)))
             return true;
         return w.marks != nullptr && lane == 0 &&
-               reinterpret_cast<const uint32_t*>(ring + s * S::kBytes + S::kMarks)[group] != 0u;
+               reinterpret_cast<const uint32_t*>(ring + s * S::kBytes + S::kMarks)[warp] != 0u;
     };
+    // step k's edge, one step ahead
+    auto edge_of = [&](int k) {
+        const int64_t t = first_token(k) + warp * kTok;
+        const int c = c0 + 2 * lane;
+        return kBwd && place(k) < n && t < a.T_total && c < a.D
+                   ? __ldg(reinterpret_cast<const float2*>(a.edges + t / kTok * a.D + c))
+                   : both(0.f);
+    };
+    float2 edge = edge_of(0);
+    cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-        load(k, k);
-        put_exps<S, In>(ring + k * S::kBytes, exps);
-    }
+    for (int k = 0; k < kAhead; ++k) put_exps<S, In>(ring + k * S::kBytes, load(k, k));
     copy_wait<kAhead - 1>();
     bool marked = __syncthreads_or(look(0, 0));
-    for (int k = 0, s = 0; k < n; ++k) {
-        const View<S, In, IO, W> v{ring + s * S::kBytes, group, lane};
-        const int64_t t = first_token(k) + group * kTok;
+    float2 carry = both(0.f);
+    __syncwarp();
+    cluster_wait();
+    for (int k = 0, s = 0; k < steps; ++k) {
+        const View<S, In, IO> v{ring + s * S::kBytes, warp, lane, edge};
+        const int64_t t = first_token(k) + warp * kTok;
+        const bool some = place(k) < n;
         const uint32_t marks = marked ? v.marks(w, t, a.T_total) : 0u;
-        first(v, t, marks, marked, k & 1);
-        const int next = s + 1 == kStages ? 0 : s + 1;
+        maps.warps[turn][lane] = some ? first(v, t, marks) : identity();
+        const int next = s + 1 == kStages ? 0 : s + 1, buf = k & 1;
         copy_wait<kAhead - 2>();
         const bool coming = __syncthreads_or(look(k + 1, next));
+        const float4 before = marked ? compose<true>(maps, buf, turn, lane, rank, ctas)
+                                     : compose<false>(maps, buf, turn, lane, rank, ctas);
+        __syncwarp();
+        cluster_arrive();
         const int free = !kHeld ? s : s == 0 ? kStages - 1 : s - 1;
-        load(k + kAhead, free);
-        second(v, t, marks, marked, k & 1);
-        if (k + kAhead < n) put_exps<S, In>(ring + free * S::kBytes, exps);
+        const int e = load(k + kAhead, free);
+        edge = edge_of(k + 1);
+        __syncwarp();
+        cluster_wait();
+        const float2 h = start_state(maps, buf, lane, before, rank, ctas, marked, carry);
+        if (some) second(v, t, marks, marked, h);
+        if (place(k + kAhead) < n) put_exps<S, In>(ring + free * S::kBytes, e);
         marked = coming;
         s = next;
     }
     copy_wait<0>();
 }
 
-// The CTA's run and first channel; false where it has nothing to do.
-__device__ __forceinline__ bool find_run(const RecurrenceArgs& a, const Plan& w, int W, int& begin,
-                                         int& end, int& c0) {
-    const int r = blockIdx.x / w.cols;
-    c0 = (int)(blockIdx.x - r * w.cols) * W;
+// The cluster's run and first channel; false where it has nothing to do.
+__device__ __forceinline__ bool find_run(const RecurrenceArgs& a, const Plan& w, int& begin, int& end,
+                                         int& c0) {
+    const int id = blockIdx.x / cluster_size(), r = id / w.cols;
+    c0 = (id - r * w.cols) * kC;
     if (w.run) {
         begin = w.run[r];
         end = w.run[r + 1];
@@ -429,33 +435,28 @@ __device__ __forceinline__ int end_at(const Plan& w, int64_t t) {
 
 // ---------------------------------------------------------------- forward --
 
-template <typename In, typename IO, int W, int kStages>
+template <typename In, typename IO, int kStages>
 __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
     const __grid_constant__ GateBound gb) {
-    using S = Stage<In, IO, false, W>;
-    using V = View<S, In, IO, W>;
+    using S = Stage<In, IO, false>;
+    using V = View<S, In, IO>;
     extern __shared__ __align__(128) char ring[];
-    __shared__ float4 maps[2][kWarps][S::kLanes];
-    const int lane = threadIdx.x % S::kLanes, warp = threadIdx.x >> 5;
-    const int rank = threadIdx.x % 32 / S::kLanes;
+    __shared__ Maps maps;
     grid_dependency_wait();
-    grid_dependents_launch();
     int begin, end, c0;
-    if (!find_run(a, w, W, begin, end, c0)) return;
-    const int ch = c0 + 2 * lane;
+    if (!find_run(a, w, begin, end, c0)) return;
+    const int ch = c0 + 2 * (threadIdx.x % 32);
     const bool live = ch < a.D;
     const float2 nl =
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
-    float2 carry = both(0.f);
     float2 c[kTok], nb[kTok];
     float2 opening = both(0.f);  // the initial state of a sequence that starts with the first token
-    float4 before;
-    for_tiles<S, In, IO, false, W, kStages, false>(
-        a, w, ring, begin, end, c0,
-        [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
-            float2 P = both(1.f), H = both(0.f);
+    for_tiles<S, In, IO, false, kStages, false>(
+        a, w, ring, maps, begin, end, c0,
+        [&](const V& v, int64_t t, uint32_t marks) {
             recurrence_steps([&](int which, int k) { return v.input(which, k); }, nl, gb, c, nb);
+            float2 P = both(1.f), H = both(0.f);
             if ((marks & 0xffu) == 0u) {
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) {
@@ -482,15 +483,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                 }
                 P = both(-0.f);
             }
-            before = make_float4(P.x, P.y, H.x, H.y);
-            if (marked)
-                scan_warp<true, false, S::kLanes>(before, rank, &maps[buf][warp][lane]);
-            else
-                scan_warp<false, false, S::kLanes>(before, rank, &maps[buf][warp][lane]);
+            return make_float4(P.x, P.y, H.x, H.y);
         },
-        [&](const V&, int64_t t, uint32_t marks, bool marked, int buf) {
-            float2 h = marked ? scan_tile<true, S::kLanes>(maps[buf], warp, lane, before, carry)
-                              : scan_tile<false, S::kLanes>(maps[buf], warp, lane, before, carry);
+        [&](const V&, int64_t t, uint32_t marks, bool marked, float2 h) {
             if (!live) return;
             IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
             float* edge = a.edges + t / kTok * a.D + ch;
@@ -503,8 +498,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                 }
                 return;
             }
-            if (a.edges && t >= begin && t < end)
-                store_pair(edge, marks & 1 ? opening : h);
+            if (a.edges && t >= begin && t < end) store_pair(edge, marks & 1 ? opening : h);
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
                 if (marks >> k & 1) h = both(0.f);
@@ -519,36 +513,31 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
 
 // -------------------------------------------------------------- gradients --
 
-template <typename In, typename IO, int W, int kStages>
+template <typename In, typename IO, int kStages>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
     const __grid_constant__ GateBound gb, float* part) {
-    using S = Stage<In, IO, true, W>;
-    using V = View<S, In, IO, W>;
+    using S = Stage<In, IO, true>;
+    using V = View<S, In, IO>;
     extern __shared__ __align__(128) char ring[];
-    __shared__ float4 maps[2][kWarps][S::kLanes];
-    const int lane = threadIdx.x % S::kLanes, warp = threadIdx.x >> 5;
-    // in the scan's order, backwards
-    const int rank = S::kSplit - 1 - (int)threadIdx.x % 32 / S::kLanes, turn = kWarps - 1 - warp;
+    __shared__ Maps maps;
     grid_dependency_wait();
-    grid_dependents_launch();
     int begin, end, c0;
-    const bool any = find_run(a, w, W, begin, end, c0);
-    const int ch = c0 + 2 * lane;
+    const bool any = find_run(a, w, begin, end, c0);
+    const int lane = threadIdx.x % 32, ch = c0 + 2 * lane;
     const bool live = ch < a.D;
     float2 dA = both(0.f);
     if (any) {
         const ChannelRate r = channel_rate(
             live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), gb.g_min);
-        float2 carry = both(0.f);  // -r, what -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
         float2 c[kTok], fx[kTok], fz[kTok], fi[kTok];
-        float4 before;
-        for_tiles<S, In, IO, true, W, kStages, true>(
-            a, w, ring, begin, end, c0,
-            [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
+        // the scan's state is -r, what -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
+        for_tiles<S, In, IO, true, kStages, true>(
+            a, w, ring, maps, begin, end, c0,
+            [&](const V& v, int64_t t, uint32_t marks) {
                 // the negated factors of l in the gradients, from the states
                 recurrence_grads(
-                    [&](int which, int k) { return v.input(which, k); }, r, gb, v.edge(),
+                    [&](int which, int k) { return v.input(which, k); }, r, gb, v.edge,
                     [&](int k, float2 h) {
                         if (marks >> k & 1)
                             h = a.h0 && live ? state_row(a.h0, start_at(w, t + k), a.D, ch) : both(0.f);
@@ -575,15 +564,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                     }
                     P = both(-0.f);
                 }
-                before = make_float4(P.x, P.y, H.x, H.y);
-                if (marked)
-                    scan_warp<true, true, S::kLanes>(before, rank, &maps[buf][turn][lane]);
-                else
-                    scan_warp<false, true, S::kLanes>(before, rank, &maps[buf][turn][lane]);
+                return make_float4(P.x, P.y, H.x, H.y);
             },
-            [&](const V& v, int64_t t, uint32_t marks, bool marked, int buf) {
-                float2 nr = marked ? scan_tile<true, S::kLanes>(maps[buf], turn, lane, before, carry)
-                                   : scan_tile<false, S::kLanes>(maps[buf], turn, lane, before, carry);
+            [&](const V& v, int64_t t, uint32_t marks, bool marked, float2 nr) {
                 if (!live) return;
                 const int64_t at = t * a.D + ch;
                 IO* dx = static_cast<IO*>(a.dx) + at;
@@ -611,29 +594,31 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             });
     }
     if (part == nullptr) return;
-    // the run's dA_log: over the threads of a channel, in a fixed order
+    // the CTA's dA_log: over the warps, in a fixed order
     float2* sums = reinterpret_cast<float2*>(ring);
     __syncthreads();
     sums[threadIdx.x] = dA;
     __syncthreads();
-    if (threadIdx.x < S::kLanes && live) {
-        float2 s = both(0.f);
-#pragma unroll 8
-        for (int g = 0; g < S::kGroups; ++g) s = add_pair(s, sums[g * S::kLanes + lane]);
-        *reinterpret_cast<float2*>(part + (int64_t)(blockIdx.x / w.cols) * a.D + ch) = s;
+    if (threadIdx.x < 32 && live) {
+        float2 s = sums[lane];
+#pragma unroll
+        for (int j = 1; j < kWarps; ++j) s = add_pair(s, sums[j * 32 + lane]);
+        const unsigned ctas = cluster_size();
+        const int64_t row = (int64_t)(blockIdx.x / ctas / w.cols) * ctas + cluster_rank();
+        *reinterpret_cast<float2*>(part + row * a.D + ch) = s;
     }
 }
 
-// dA_log[c] = the sum of the runs' parts in a fixed order: a CTA takes 32 channels, its 32 warps every
-// 32nd run.
-__global__ void __launch_bounds__(1024) rate_kernel(const float* part, int runs, int D, float* dA) {
+// dA_log[c] = the sum of the CTAs' parts in a fixed order: a CTA takes 32 channels, its 32 warps every
+// 32nd part.
+__global__ void __launch_bounds__(1024) rate_kernel(const float* part, int parts, int D, float* dA) {
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     grid_dependency_wait();
     float x = 0.f;
     if (c < D) {
 #pragma unroll 4
-        for (int b = warp; b < runs; b += 32) x += part[(int64_t)b * D + c];
+        for (int b = warp; b < parts; b += 32) x += part[(int64_t)b * D + c];
     }
     red[warp][lane] = x;
     __syncthreads();
@@ -709,16 +694,25 @@ __global__ void __launch_bounds__(128) step_kernel(const IO* x, int64_t x_ld, co
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// Runs are as many as sequences, but of 1,024 tokens on average at least, and 8 times the CTAs
-// that the GPU holds at most.
+// Runs are as many as sequences, but of 1,024 tokens on average at least, and 8 times what the GPU
+// holds at most.
 int count_runs(int64_t T, int N, int cols) {
     const int64_t most = std::max<int64_t>(1, 152 * 2 * 8 / cols);
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(N, T / 1024), most));
 }
 
+// CTAs of a cluster: as many as keep all of them on the GPU at once, two an SM; with several runs,
+// that a run has 8 steps on average.
+int count_ctas(int64_t T, int runs, int cols, int most) {
+    int n = 1;
+    while (2 * n <= most && T / runs > kT * n &&
+           ((int64_t)runs * cols * 2 * n <= 304 || (runs > 1 && T / runs >= (int64_t)kT * 2 * n * 8)))
+        n *= 2;
+    return n;
+}
+
 // The parts of a workspace; w may be nullptr.
-size_t lay_out(char* ws, int64_t T, int N, int D, int W, bool bwd, Plan* w, float** edges,
-               float** part) {
+size_t lay_out(char* ws, int64_t T, int N, int D, bool bwd, Plan* w, float** edges, float** part) {
     size_t n = 0;
     auto take = [&](size_t bytes) {
         char* p = ws ? ws + n : nullptr;
@@ -726,7 +720,7 @@ size_t lay_out(char* ws, int64_t T, int N, int D, int W, bool bwd, Plan* w, floa
         return p;
     };
     Plan s{};
-    s.cols = (D + W - 1) / W;
+    s.cols = (D + kC - 1) / kC;
     s.runs = count_runs(T, N, s.cols);
     if (N != 1) {
         s.run = reinterpret_cast<int*>(take((s.runs + 1) * 4));
@@ -735,7 +729,7 @@ size_t lay_out(char* ws, int64_t T, int N, int D, int W, bool bwd, Plan* w, floa
         s.end_seq = reinterpret_cast<int*>(take(T * 4));
     }
     if (bwd) {
-        char* p = take((size_t)s.runs * D * 4);
+        char* p = take((size_t)s.runs * kMaxCluster * D * 4);
         char* e = take((size_t)((T + kTok - 1) / kTok) * D * 4);
         if (part) *part = reinterpret_cast<float*>(p);
         if (edges) *edges = reinterpret_cast<float*>(e);
@@ -753,95 +747,80 @@ cudaError_t setup(const RecurrenceArgs& a, const Plan& w, const float* from, flo
     return cudaGetLastError();
 }
 
-template <typename Kernel, typename... Args>
-cudaError_t launch_scan(Kernel kernel, const char* name, int smem, const RecurrenceArgs& a,
-                        const Plan& w, Args... args) {
+template <typename... KArgs, typename... Args>
+cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int smem, int ctas,
+                        const RecurrenceArgs& a, const Plan& w, Args... args) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
         return e;
     ProfScope prof(name, a.stream);
-    return launch_dependent(kernel, dim3((unsigned)w.runs * w.cols), dim3(kThreads), smem, a.stream, a,
-                            w, gate_bound(a.g_min), args...);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)w.runs * w.cols * ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, w, gate_bound(a.g_min), args...);
 }
 
-template <typename In, typename IO, int W>
+template <typename In, typename IO>
 cudaError_t forward(const RecurrenceArgs& a, const Plan& w) {
-    constexpr int kStages = sizeof(In) == 4 ? 2 : 4;
-    return launch_scan(scan_kernel<In, IO, W, kStages>, "recurrence_kernel",
-                       kStages * Stage<In, IO, false, W>::kBytes, a, w);
+    constexpr int kStages = sizeof(In) == 4 ? 2 : 3;
+    const int ctas = count_ctas(a.T_total, w.runs, w.cols, kMaxCluster);
+    return launch_scan(scan_kernel<In, IO, kStages>, "recurrence_kernel",
+                       kStages * Stage<In, IO, false>::kBytes, ctas, a, w);
 }
 
-template <typename In, typename IO, int W>
+template <typename In, typename IO>
 cudaError_t backward(RecurrenceArgs a) {
     constexpr int kStages = 3;
     Plan w;
     float *edges, *part;
-    lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, W, true, &w, &edges, &part);
+    lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, true, &w, &edges, &part);
     if (cudaError_t e = setup(a, w, a.dh_out, a.dh0)) return e;
+    const int ctas = count_ctas(a.T_total, w.runs, w.cols, kMaxCluster);
     if (a.T_total > 0) {
         if (a.edges == nullptr) {
             RecurrenceArgs f = a;
             f.edges = a.edges = edges;
             f.y = nullptr;
             f.h_out = nullptr;
-            if (cudaError_t e = forward<In, IO, W>(f, w)) return e;
+            if (cudaError_t e = forward<In, IO>(f, w)) return e;
         }
-        if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, W, kStages>, "recurrence_bwd_kernel",
-                                        kStages * Stage<In, IO, true, W>::kBytes, a, w,
+        if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, kStages>, "recurrence_bwd_kernel",
+                                        kStages * Stage<In, IO, true>::kBytes, ctas, a, w,
                                         a.dA_log ? part : nullptr))
             return e;
     }
     if (a.dA_log) {
         ProfScope prof("recurrence_rate_kernel", a.stream);
         return launch_dependent(rate_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, a.stream,
-                                (const float*)part, a.T_total > 0 ? w.runs : 0, a.D, a.dA_log);
+                                (const float*)part, a.T_total > 0 ? w.runs * ctas : 0, a.D, a.dA_log);
     }
     return cudaGetLastError();
 }
 
-// Channels of a CTA: the fewest with which the CTAs of one run, two an SM, are on the GPU at once
-// (rows of 16 bytes at least).  More CTAs are faster as long as they run side by side.
-int columns(int D, int N, int64_t T, bool f32) {
-    const int least = f32 ? 8 : 8;
-    int W = least;
-    while (W < (f32 ? 16 : 32) && (int64_t)((D + W - 1) / W) * count_runs(T, N, (D + W - 1) / W) > 304)
-        W *= 2;
-    return W;
-}
-
-template <typename In, typename IO>
-cudaError_t backward_of(const RecurrenceArgs& a) {
-    switch (columns(a.D, a.N, a.T_total, sizeof(IO) == 4)) {
-        case 8: return backward<In, IO, 8>(a);
-        case 16: return backward<In, IO, 16>(a);
-        default:
-            if constexpr (sizeof(IO) == 4) return backward<In, IO, 16>(a);
-            else return backward<In, IO, 32>(a);
-    }
+template <typename IO>
+cudaError_t forward_of(const RecurrenceArgs& a) {
+    Plan w;
+    lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, false, &w, nullptr, nullptr);
+    if (cudaError_t e = setup(a, w, a.h0, a.h_out)) return e;
+    return a.T_total == 0 ? cudaSuccess : forward<IO, IO>(a, w);
 }
 
 }  // namespace
 
 size_t recurrence_fwd_workspace_size(int64_t T, int N, int D) {
-    return lay_out(nullptr, T, N, D, 8, false, nullptr, nullptr, nullptr) + 256 * 4 * 11;
+    return lay_out(nullptr, T, N, D, false, nullptr, nullptr, nullptr);
 }
 size_t recurrence_bwd_workspace_size(int64_t T, int N, int D) {
-    return lay_out(nullptr, T, N, D, 32, true, nullptr, nullptr, nullptr) + 256 * 4 * 11;
-}
-
-template <typename IO>
-static cudaError_t forward_of(const RecurrenceArgs& a) {
-    const int W = columns(a.D, a.N, a.T_total, sizeof(IO) == 4);
-    Plan w;
-    lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, W, false, &w, nullptr, nullptr);
-    if (cudaError_t e = setup(a, w, a.h0, a.h_out)) return e;
-    if (a.T_total == 0) return cudaSuccess;
-    switch (W) {
-        case 8: return forward<IO, IO, 8>(a, w);
-        case 16: return forward<IO, IO, 16>(a, w);
-        default:
-            if constexpr (sizeof(IO) == 4) return forward<IO, IO, 16>(a, w);
-            else return forward<IO, IO, 32>(a, w);
-    }
+    return lay_out(nullptr, T, N, D, true, nullptr, nullptr, nullptr);
 }
 
 cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a) {
@@ -849,8 +828,8 @@ cudaError_t launch_recurrence_fwd(const RecurrenceArgs& a) {
 }
 cudaError_t launch_recurrence_bwd(const RecurrenceArgs& a) {
     if (a.packed)
-        return a.io_bf16 ? backward_of<int8_t, __nv_bfloat16>(a) : backward_of<int8_t, float>(a);
-    return a.io_bf16 ? backward_of<__nv_bfloat16, __nv_bfloat16>(a) : backward_of<float, float>(a);
+        return a.io_bf16 ? backward<int8_t, __nv_bfloat16>(a) : backward<int8_t, float>(a);
+    return a.io_bf16 ? backward<__nv_bfloat16, __nv_bfloat16>(a) : backward<float, float>(a);
 }
 
 cudaError_t launch_recurrence_step(const void* x, int64_t x_ld, const void* z, int64_t z_ld,
