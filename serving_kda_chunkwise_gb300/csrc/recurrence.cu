@@ -22,6 +22,9 @@
 // cuts the batch into runs (one sequence needs none of it).  Where a sequence starts, a map is
 // constant: P's sign bit says so (P >= 0 otherwise), and it is selected, not multiplied by zero, so
 // that nothing that is not finite crosses.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 
 #include "kda_internal.h"
@@ -50,65 +53,72 @@ struct Plan {
 
 // ---------------------------------------------------------------- inputs --
 
-// A stage of the ring: the inputs of a tile.
-template <typename In, typename IO, bool kBwd>
-struct Stage {
-    static constexpr int kIn = kT * kC * (int)sizeof(In);
-    static constexpr int kDy = 3 * kIn;
-    static constexpr int kMarks = kDy + (kBwd ? kT * kC * (int)sizeof(IO) : 0);
-    static constexpr int kExps = kMarks + kWarps * 4;
-    static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT : 0) + 15) / 16 * 16;
+// The tensors as the copy engine sees them, boxes of 64 tokens x 64 channels: inputs x, z, i, dy and
+// outputs y, or dx, dz and di.
+struct Tensors {
+    CUtensorMap in[4], out[3];
+    int plain;  // inputs by plain copies: rows of codes that begin on 8 bytes only
 };
 
-template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool live) {
-    const int n = live ? kBytes : 0;
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n));
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n),
-                     "n"(kBytes));
+// A stage of the ring: the inputs of a tile.  A tile's results leave from where its inputs were, or
+// from a place of their own where these have fewer bytes.
+template <typename In, typename IO, bool kBwd>
+struct Stage {
+    static constexpr int kIn = kT * kC * (int)sizeof(In), kOut = kT * kC * (int)sizeof(IO);
+    static constexpr int kDy = 3 * kIn;
+    static constexpr int kExps = kDy + (kBwd ? kOut : 0);
+    static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT : 0) + 127) / 128 * 128;
+    static constexpr bool kInPlace = sizeof(In) == sizeof(IO);
+    static constexpr int kOuts = kInPlace ? 0 : (kBwd ? 3 : 1) * kOut;  // bytes of that place
+};
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;"); }
-template <int n>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
 }
 
-// 64 tokens x 64 channels of a tensor; rows and channels past its end become zeros.
+// 64 tokens x 64 channels of a tensor by plain copies; rows and channels past its end become zeros.
 template <typename In>
-__device__ __forceinline__ void load_tile(char* dst, const void* src, int64_t ld, int64_t t0, int c0,
+__device__ __forceinline__ void copy_tile(char* dst, const void* src, int64_t ld, int64_t t0, int c0,
                                           int64_t T, int D) {
-    // (rows of codes begin on 8 bytes only)
-    constexpr int kPiece = sizeof(In) == 1 ? 8 : 16, kElems = kPiece / (int)sizeof(In);
-    constexpr int kPer = kC / kElems, kStep = kThreads / kPer;
-    const int row = threadIdx.x / kPer, c = threadIdx.x % kPer * kElems;
-    const int left = (int)min((int64_t)kT, T - t0) - row;  // rows left from this thread's first
-    const bool in = c0 + c < D;
-    const In* s = static_cast<const In*>(src) + (t0 + row) * ld + c0 + c;
-    const uint32_t d = smem_u32(dst) + (row * kC + c) * (int)sizeof(In);
-#pragma unroll
-    for (int k = 0; k < kT / kStep; ++k) {
-        const bool live = in && k * kStep < left;
-        copy_async<kPiece>(d + k * kStep * kC * (int)sizeof(In), live ? s : src, live);
-        s += kStep * ld;
+    constexpr int kElems = 8 / (int)sizeof(In);
+    for (int p = threadIdx.x; p < kT * kC / kElems; p += kThreads) {
+        const int row = p * kElems / kC, c = p * kElems % kC;
+        const bool live = t0 + row < T && c0 + c < D;
+        const In* s = static_cast<const In*>(src) + (live ? (t0 + row) * ld + c0 + c : 0);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(
+                         smem_u32(dst) + (row * kC + c) * (int)sizeof(In)),
+                     "l"(s), "r"(live ? 8 : 0));
     }
 }
 
-// Starts the loads of the tile from token t0 and channel c0.  Of packed inputs, the exponent that
-// this thread has to put into the stage is returned.
+// Starts the loads of the tile from token t0 and channel c0; called by all threads.  Of packed
+// inputs, the exponent that this thread has to put into the stage is returned.
 template <typename S, typename In, typename IO, bool kBwd>
-__device__ __forceinline__ int load_stage(const RecurrenceArgs& a, const Plan& w, char* st,
-                                          int64_t t0, int c0) {
-    load_tile<In>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D);
-    load_tile<In>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D);
-    load_tile<In>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D);
-    if (kBwd) load_tile<IO>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D);
-    // (a warp's marks by the thread that looks at them before the barrier)
-    if (w.marks && threadIdx.x % 32 == 0) {
-        const int g = threadIdx.x / 32;
-        const bool live = t0 + g * kTok < a.T_total;
-        copy_async<4>(smem_u32(st + S::kMarks) + g * 4, w.marks + (live ? t0 / kTok + g : 0), live);
+__device__ __forceinline__ int load_stage(const RecurrenceArgs& a, const Tensors& m, char* st,
+                                          uint64_t* full, int t0, int c0) {
+    if (sizeof(In) == 1 && m.plain) {
+        copy_tile<In>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D);
+        copy_tile<In>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D);
+        copy_tile<In>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D);
+        if (kBwd) copy_tile<IO>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full))
+                     : "memory");
+    } else if (threadIdx.x == 0) {
+        mbar_expect_tx(full, S::kExps);
+        tma_load(st, &m.in[0], c0, t0, full);
+        tma_load(st + S::kIn, &m.in[1], c0, t0, full);
+        tma_load(st + 2 * S::kIn, &m.in[2], c0, t0, full);
+        if (kBwd) tma_load(st + S::kDy, &m.in[3], c0, t0, full);
     }
     if (sizeof(In) == 1 && threadIdx.x < 3 * kT) {
         const int k = threadIdx.x / kT, t = threadIdx.x % kT;
@@ -124,7 +134,9 @@ __device__ __forceinline__ void put_exps(char* st, int e) {
 }
 
 __device__ __forceinline__ float2 pair(const __nv_bfloat16* p) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    // (read as what it is: results are written to the same places)
+    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(p);
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 __device__ __forceinline__ float2 pair(const float* p) {
@@ -134,7 +146,7 @@ __device__ __forceinline__ float2 pair(const float* p) {
 // A thread's view of a stage: token k of its warp, its two channels.
 template <typename S, typename In, typename IO>
 struct View {
-    const char* st;
+    char* st;
     int warp, lane;
     float2 edge;  // (gradients) the state before the warp's tokens
     template <typename E>
@@ -155,10 +167,10 @@ struct View {
         }
     }
     __device__ __forceinline__ float2 dy(int k) const { return pair(at<IO>(S::kDy, k)); }
-    // the marks of the warp's tokens, the first of which is t, of a batch of T tokens
-    __device__ __forceinline__ uint32_t marks(const Plan& w, int64_t t, int64_t T) const {
-        if (w.marks) return reinterpret_cast<const uint32_t*>(st + S::kMarks)[warp];
-        return (t == 0 ? 1u : 0u) | (T > t && T <= t + kTok ? 256u << (T - 1 - t) : 0u);
+    // the place of output `which` of token k
+    char* outs;
+    __device__ __forceinline__ IO* out(int which, int k) const {
+        return reinterpret_cast<IO*>(outs + which * S::kOut) + (warp * kTok + k) * kC + 2 * lane;
     }
 };
 
@@ -267,8 +279,9 @@ __device__ __forceinline__ float4 identity() { return make_float4(1.f, 1.f, 0.f,
 
 // What a CTA keeps of a step's maps.
 struct Maps {
-    float4 warps[kWarps][32];             // of its own tile
-    float4 tiles[2][kMaxCluster][32];     // of the cluster's, in the scan's order; alternating
+    float4 warps[kWarps][32];          // of its own tile
+    float4 tiles[2][kMaxCluster][32];  // of the cluster's, in the scan's order; alternating
+    uint64_t there[2];                 // those have arrived
 };
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -281,13 +294,16 @@ __device__ __forceinline__ unsigned cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-// Writes v to p's place in the shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_remote(float4* p, unsigned rank, float4 v) {
-    uint32_t at;
+// Writes v to p's place in the shared memory of CTA `rank` of the cluster, and counts its bytes on the
+// barrier in bar's place there.
+__device__ __forceinline__ void send(float4* p, uint64_t* bar, unsigned rank, float4 v) {
+    uint32_t at, done;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
-                 : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(done) : "r"(smem_u32(bar)), "r"(rank));
+    asm volatile(
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+        "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(done)
+        : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -296,18 +312,20 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// With the warps' maps there: the map of those before `turn` (in the scan's order), and the tile's
-// map to the CTAs of the cluster (one each, by as many warps).
+// With the warps' maps there: the map of those before `turn` (in the scan's order); the last one
+// sends the tile's map to the CTAs of the cluster.
 template <bool kCut>
 __device__ __forceinline__ float4 compose(Maps& m, int buf, int turn, int lane, unsigned rank,
                                           unsigned ctas) {
-    float4 all = identity(), before = all;
+    float4 before = identity();
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) {
-        if (j == turn) before = all;
-        if (j < turn || (unsigned)turn < ctas) all = after<kCut>(m.warps[j][lane], all);
+    for (int j = 0; j < kWarps - 1; ++j)
+        if (j < turn) before = after<kCut>(m.warps[j][lane], before);
+    if (turn == kWarps - 1) {
+        const float4 all = after<kCut>(m.warps[turn][lane], before);
+        for (unsigned j = 0; j < ctas; ++j)
+            send(&m.tiles[buf][rank][lane], &m.there[buf], j, all);
     }
-    if ((unsigned)turn < ctas) store_remote(&m.tiles[buf][rank][lane], turn, all);
     return before;
 }
 
@@ -328,83 +346,106 @@ __device__ __forceinline__ float2 start_state(const Maps& m, int buf, int lane, 
 
 // ------------------------------------------------------------- the loop --
 
-// Runs first(view, t0, marks), which leaves the warp's map, and second(view, t0, marks, marked, state
+// The marks of tokens t .. t + 7.
+__device__ __forceinline__ uint32_t marks_of(const Plan& w, int64_t t, int64_t T) {
+    if (w.marks) return t < T ? __ldg(w.marks + t / kTok) : 0u;
+    return (t == 0 ? 1u : 0u) | (T > t && T <= t + kTok ? 256u << (T - 1 - t) : 0u);
+}
+
+// Runs first(view, t0, marks), which returns the warp's map, and second(view, t0, marks, whole, state
 // before the warp's tokens) over the tiles of a CTA in its cluster's run, their inputs loaded ahead.
-// marked: some token of the tile starts or ends a sequence.  kHeld: second() reads the stage too.
-template <typename S, typename In, typename IO, bool kBwd, int kStages, bool kHeld, typename First,
+// whole: the tile lies in the run, and second() leaves its results in the view's places for kOutputs
+// outputs; otherwise it stores those of the run itself.
+template <typename S, typename In, typename IO, bool kBwd, int kStages, int kOutputs, typename First,
           typename Second>
-__device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w, char* ring, Maps& maps,
-                                          int begin, int end, int c0, First&& first, Second&& second) {
-    // Loads go out after the CTA's barrier, into the stage that is free then: the tile's own, or where
-    // that is still read, the one before it.
-    constexpr int kAhead = kHeld ? kStages - 1 : kStages;  // tiles from the one worked on
-    static_assert(kAhead >= 2, "the next tile is on its way before the barrier");
+__device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w, const Tensors& m,
+                                          char* ring, Maps& maps, int begin, int end, int c0,
+                                          First&& first, Second&& second) {
+    __shared__ uint64_t full[kStages];
+    constexpr int kAhead = kStages - 1;  // tiles from the one worked on to the one loaded
     const unsigned rank = cluster_rank(), ctas = cluster_size();
     const int base = begin / kTok * kTok, n = (end - base + kT - 1) / kT;
     const int steps = (n + (int)ctas - 1) / (int)ctas;
     // step k's tile, in the scan's order; there may be none left for this CTA
     auto place = [&](int k) { return k * (int)ctas + (int)rank; };
     auto first_token = [&](int k) { return base + (kBwd ? n - 1 - place(k) : place(k)) * kT; };
-    auto load = [&](int k, int s) {
-        int e = 0;
-        if (place(k) < n)
-            e = load_stage<S, In, IO, kBwd>(a, w, ring + s * S::kBytes, first_token(k), c0);
-        copy_commit();
-        return e;
-    };
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int turn = kBwd ? kWarps - 1 - warp : warp;  // in the scan's order
-    // whether step k's tile, in stage s, has marks that this thread has copied (or its run ends in it)
-    auto look = [&](int k, int s) {
-        if (place(k) >= n) return false;
-        const int t0 = first_token(k);
-        if (t0 < begin || t0 + kT > end || (w.marks == nullptr && (t0 == 0 || t0 + kT == end)))
-            return true;
-        return w.marks != nullptr && lane == 0 &&
-               reinterpret_cast<const uint32_t*>(ring + s * S::kBytes + S::kMarks)[warp] != 0u;
+    char* const outs = ring + kStages * S::kBytes;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kStages; ++k) mbar_init(&full[k], sizeof(In) == 1 && m.plain ? kThreads : 1);
+        for (int k = 0; k < 2; ++k) mbar_init(&maps.there[k], 1);
+        fence_mbar_init();
+        for (int k = 0; k < 2; ++k) mbar_expect_tx(&maps.there[k], ctas * 32 * sizeof(float4));
+    }
+    __syncthreads();
+    cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
+    auto load = [&](int k, int s) {
+        return place(k) < n ? load_stage<S, In, IO, kBwd>(a, m, ring + s * S::kBytes, &full[s],
+                                                          first_token(k), c0)
+                            : 0;
     };
-    // step k's edge, one step ahead
-    auto edge_of = [&](int k) {
+    // a warp's marks and edge of step k's tile
+    auto marks_at = [&](int k) {
+        return place(k) < n ? marks_of(w, first_token(k) + warp * kTok, a.T_total) : 0u;
+    };
+    auto edge_at = [&](int k) {
         const int64_t t = first_token(k) + warp * kTok;
         const int c = c0 + 2 * lane;
         return kBwd && place(k) < n && t < a.T_total && c < a.D
                    ? __ldg(reinterpret_cast<const float2*>(a.edges + t / kTok * a.D + c))
                    : both(0.f);
     };
-    float2 edge = edge_of(0);
-    cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) put_exps<S, In>(ring + k * S::kBytes, load(k, k));
-    copy_wait<kAhead - 1>();
-    bool marked = __syncthreads_or(look(0, 0));
-    float2 carry = both(0.f);
-    __syncwarp();
+    float2 edge = edge_at(0), carry = both(0.f);
+    uint32_t marks = marks_at(0), coming = marks_at(1);
+    bool marked = __syncthreads_or(marks != 0u), broken = false;
     cluster_wait();
     for (int k = 0, s = 0; k < steps; ++k) {
-        const View<S, In, IO> v{ring + s * S::kBytes, warp, lane, edge};
-        const int64_t t = first_token(k) + warp * kTok;
-        const bool some = place(k) < n;
-        const uint32_t marks = marked ? v.marks(w, t, a.T_total) : 0u;
+        char* const st = ring + s * S::kBytes;
+        const View<S, In, IO> v{st, warp, lane, edge, S::kInPlace ? st : outs};
+        const int t0 = first_token(k);
+        const int64_t t = t0 + warp * kTok;
+        const bool some = place(k) < n, whole = some && t0 >= begin && t0 + kT <= end;
+        if (some && !broken) broken = !mbar_wait(&full[s], k / kStages & 1, a.dev_err);
         maps.warps[turn][lane] = some ? first(v, t, marks) : identity();
-        const int next = s + 1 == kStages ? 0 : s + 1, buf = k & 1;
-        copy_wait<kAhead - 2>();
-        const bool coming = __syncthreads_or(look(k + 1, next));
+        const int buf = k & 1, before_s = s == 0 ? kStages - 1 : s - 1;
+        if (kOutputs && threadIdx.x == 0) bulk_wait_read0();  // (the stage before this one is free)
+        const bool next_marked = __syncthreads_or(coming != 0u);
         const float4 before = marked ? compose<true>(maps, buf, turn, lane, rank, ctas)
                                      : compose<false>(maps, buf, turn, lane, rank, ctas);
-        __syncwarp();
-        cluster_arrive();
-        const int free = !kHeld ? s : s == 0 ? kStages - 1 : s - 1;
-        const int e = load(k + kAhead, free);
-        edge = edge_of(k + 1);
-        __syncwarp();
-        cluster_wait();
+        const int e = load(k + kAhead, before_s);
+        edge = edge_at(k + 1);
+        const uint32_t later = marks_at(k + 2);
+        // (the next maps for this buffer are sent when this CTA's of the next step are there, which
+        // its barrier of that step precedes)
+        if (!broken) broken = !mbar_wait(&maps.there[buf], k / 2 & 1, a.dev_err);
+        if (threadIdx.x == 0) mbar_expect_tx(&maps.there[buf], ctas * 32 * sizeof(float4));
         const float2 h = start_state(maps, buf, lane, before, rank, ctas, marked, carry);
-        if (some) second(v, t, marks, marked, h);
-        if (place(k + kAhead) < n) put_exps<S, In>(ring + free * S::kBytes, e);
-        marked = coming;
-        s = next;
+        if (some) second(v, t, marks, whole, h);
+        if (kOutputs && whole) {
+            fence_async_smem();
+            if (warp > 0) {
+                asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+            } else {
+                asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+                if (lane == 0) {
+#pragma unroll
+                    for (int o = 0; o < kOutputs; ++o)
+                        tma_store(&m.out[o], v.outs + o * S::kOut, c0, t0);
+                    bulk_commit();
+                }
+                __syncwarp();
+            }
+        }
+        if (place(k + kAhead) < n) put_exps<S, In>(ring + before_s * S::kBytes, e);
+        marked = next_marked;
+        marks = coming;
+        coming = later;
+        s = s + 1 == kStages ? 0 : s + 1;
     }
-    copy_wait<0>();
+    if (kOutputs && threadIdx.x == 0) bulk_wait0();
 }
 
 // The cluster's run and first channel; false where it has nothing to do.
@@ -435,10 +476,10 @@ __device__ __forceinline__ int end_at(const Plan& w, int64_t t) {
 
 // ---------------------------------------------------------------- forward --
 
-template <typename In, typename IO, int kStages>
+template <typename In, typename IO, int kStages, bool kOnlyEdges>
 __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
-    const __grid_constant__ GateBound gb) {
+    const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m) {
     using S = Stage<In, IO, false>;
     using V = View<S, In, IO>;
     extern __shared__ __align__(128) char ring[];
@@ -452,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
     float2 c[kTok], nb[kTok];
     float2 opening = both(0.f);  // the initial state of a sequence that starts with the first token
-    for_tiles<S, In, IO, false, kStages, false>(
-        a, w, ring, maps, begin, end, c0,
+    for_tiles<S, In, IO, false, kStages, kOnlyEdges ? 0 : 1>(
+        a, w, m, ring, maps, begin, end, c0,
         [&](const V& v, int64_t t, uint32_t marks) {
             recurrence_steps([&](int which, int k) { return v.input(which, k); }, nl, gb, c, nb);
             float2 P = both(1.f), H = both(0.f);
@@ -485,27 +526,27 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
             }
             return make_float4(P.x, P.y, H.x, H.y);
         },
-        [&](const V&, int64_t t, uint32_t marks, bool marked, float2 h) {
-            if (!live) return;
-            IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
-            float* edge = a.edges + t / kTok * a.D + ch;
-            if (!marked) {
-                if (a.edges) store_pair(edge, h);
+        [&](const V& v, int64_t t, uint32_t marks, bool whole, float2 h) {
+            if (live && a.edges && t >= begin && t < end)
+                store_pair(a.edges + t / kTok * a.D + ch, marks & 1 ? opening : h);
+            if (whole && marks == 0u) {
+                if (kOnlyEdges) return;
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) {
                     h = recurrence_next(c[k], nb[k], h);
-                    if (a.y) store_pair(y + (int64_t)k * a.D, h);
+                    store_pair(v.out(0, k), h);
                 }
                 return;
             }
-            if (a.edges && t >= begin && t < end) store_pair(edge, marks & 1 ? opening : h);
+            IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
                 if (marks >> k & 1) h = both(0.f);
                 h = recurrence_next(c[k], nb[k], h);
-                if (t + k < begin || t + k >= end) continue;
-                if (a.y) store_pair(y + (int64_t)k * a.D, h);
-                if (marks >> (8 + k) & 1 && a.h_out)
+                if (kOnlyEdges) continue;
+                if (whole) store_pair(v.out(0, k), h);
+                else if (live && t + k >= begin && t + k < end) store_pair(y + (int64_t)k * a.D, h);
+                if (live && marks >> (8 + k) & 1 && t + k >= begin && t + k < end && a.h_out)
                     store_pair(a.h_out + (int64_t)end_at(w, t + k) * a.D + ch, h);
             }
         });
@@ -516,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
 template <typename In, typename IO, int kStages>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
-    const __grid_constant__ GateBound gb, float* part) {
+    const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m, float* part) {
     using S = Stage<In, IO, true>;
     using V = View<S, In, IO>;
     extern __shared__ __align__(128) char ring[];
@@ -532,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), gb.g_min);
         float2 c[kTok], fx[kTok], fz[kTok], fi[kTok];
         // the scan's state is -r, what -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
-        for_tiles<S, In, IO, true, kStages, true>(
-            a, w, ring, maps, begin, end, c0,
+        for_tiles<S, In, IO, true, kStages, 3>(
+            a, w, m, ring, maps, begin, end, c0,
             [&](const V& v, int64_t t, uint32_t marks) {
                 // the negated factors of l in the gradients, from the states
                 recurrence_grads(
@@ -566,29 +607,43 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                 }
                 return make_float4(P.x, P.y, H.x, H.y);
             },
-            [&](const V& v, int64_t t, uint32_t marks, bool marked, float2 nr) {
-                if (!live) return;
+            [&](const V& v, int64_t t, uint32_t marks, bool whole, float2 nr) {
                 const int64_t at = t * a.D + ch;
-                IO* dx = static_cast<IO*>(a.dx) + at;
-                IO* dz = static_cast<IO*>(a.dz) + at;
-                IO* di = static_cast<IO*>(a.di) + at;
-#pragma unroll
-                for (int k = kTok - 1; k >= 0; --k) {
-                    if (marks >> (8 + k) & 1)
-                        nr = a.dh_out ? mul_pair(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
-                                      : both(0.f);
-                    const float2 l = fma_pair(v.dy(k), both(-1.f), nr);
-                    nr = fma_pair(c[k], l, l);
-                    if (marked && (t + k < begin || t + k >= end)) continue;
-                    const int64_t o = (int64_t)k * a.D;
+                // a token's gradients but for the state's
+                auto take = [&](int k, float2 l, IO* dx, IO* dz, IO* di) {
                     const float2 g = mul_pair(l, fz[k]), z = v.input(1, k);
-                    store_pair(dx + o, mul_pair(l, fx[k]));
-                    store_pair(dz + o, g);
-                    store_pair(di + o, mul_pair(l, fi[k]));
+                    store_pair(dx, mul_pair(l, fx[k]));
+                    store_pair(dz, g);
+                    store_pair(di, mul_pair(l, fi[k]));
                     // (an infinite z has a gradient of zero)
                     dA.x += g.x == 0.f ? 0.f : g.x * z.x;
                     dA.y += g.y == 0.f ? 0.f : g.y * z.y;
-                    if (marks >> k & 1 && a.dh0)
+                };
+                if (whole && marks == 0u) {
+#pragma unroll
+                    for (int k = kTok - 1; k >= 0; --k) {
+                        const float2 l = fma_pair(v.dy(k), both(-1.f), nr);
+                        nr = fma_pair(c[k], l, l);
+                        take(k, l, v.out(0, k), v.out(1, k), v.out(2, k));
+                    }
+                    return;
+                }
+#pragma unroll
+                for (int k = kTok - 1; k >= 0; --k) {
+                    if (marks >> (8 + k) & 1)
+                        nr = a.dh_out && live
+                                 ? mul_pair(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
+                                 : both(0.f);
+                    const float2 l = fma_pair(v.dy(k), both(-1.f), nr);
+                    nr = fma_pair(c[k], l, l);
+                    const bool mine = live && t + k >= begin && t + k < end;
+                    const int64_t o = at + (int64_t)k * a.D;
+                    if (whole)
+                        take(k, l, v.out(0, k), v.out(1, k), v.out(2, k));
+                    else if (mine)
+                        take(k, l, static_cast<IO*>(a.dx) + o, static_cast<IO*>(a.dz) + o,
+                             static_cast<IO*>(a.di) + o);
+                    if (mine && marks >> k & 1 && a.dh0)
                         store_pair(a.dh0 + (int64_t)start_at(w, t + k) * a.D + ch, mul_pair(nr, both(-1.f)));
                 }
             });
@@ -747,6 +802,55 @@ cudaError_t setup(const RecurrenceArgs& a, const Plan& w, const float* from, flo
     return cudaGetLastError();
 }
 
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                             const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                             const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                             &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// [T][D] of E with a token stride of ld elements.
+template <typename E>
+bool make_map(CUtensorMap* m, const void* base, int64_t T, int D, int64_t ld) {
+    EncodeFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)T};
+    const cuuint64_t stride = (cuuint64_t)ld * sizeof(E);
+    const cuuint32_t box[2] = {kC, kT}, estr[2] = {1, 1};
+    return fn(m,
+              sizeof(E) == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+              : sizeof(E) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+              2, const_cast<void*>(base), dims, &stride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename In, typename IO>
+bool make_maps(Tensors& m, const RecurrenceArgs& a, bool bwd) {
+    const int64_t T = a.T_total;
+    m.plain = sizeof(In) == 1 && a.D % 16 != 0;
+    if (!m.plain && (!make_map<In>(&m.in[0], a.x, T, a.D, a.x_ld) ||
+                     !make_map<In>(&m.in[1], a.z, T, a.D, a.z_ld) ||
+                     !make_map<In>(&m.in[2], a.i, T, a.D, a.i_ld)))
+        return false;
+    if (!bwd) return a.y == nullptr || make_map<IO>(&m.out[0], a.y, T, a.D, a.D);
+    return (m.plain || make_map<IO>(&m.in[3], a.dy, T, a.D, a.dy_ld)) &&
+           make_map<IO>(&m.out[0], a.dx, T, a.D, a.D) && make_map<IO>(&m.out[1], a.dz, T, a.D, a.D) &&
+           make_map<IO>(&m.out[2], a.di, T, a.D, a.D);
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int smem, int ctas,
                         const RecurrenceArgs& a, const Plan& w, Args... args) {
@@ -769,17 +873,21 @@ cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int smem, in
     return cudaLaunchKernelEx(&cfg, kernel, a, w, gate_bound(a.g_min), args...);
 }
 
-template <typename In, typename IO>
+constexpr int kStages = 3;
+
+template <typename In, typename IO, bool kOnlyEdges>
 cudaError_t forward(const RecurrenceArgs& a, const Plan& w) {
-    constexpr int kStages = sizeof(In) == 4 ? 2 : 3;
+    using S = Stage<In, IO, false>;
+    Tensors m{};
+    if (!make_maps<In, IO>(m, a, false)) return cudaErrorInvalidValue;
     const int ctas = count_ctas(a.T_total, w.runs, w.cols, kMaxCluster);
-    return launch_scan(scan_kernel<In, IO, kStages>, "recurrence_kernel",
-                       kStages * Stage<In, IO, false>::kBytes, ctas, a, w);
+    return launch_scan(scan_kernel<In, IO, kStages, kOnlyEdges>, "recurrence_kernel",
+                       kStages * S::kBytes + (kOnlyEdges ? 0 : S::kOuts), ctas, a, w, m);
 }
 
 template <typename In, typename IO>
 cudaError_t backward(RecurrenceArgs a) {
-    constexpr int kStages = 3;
+    using S = Stage<In, IO, true>;
     Plan w;
     float *edges, *part;
     lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, true, &w, &edges, &part);
@@ -791,10 +899,12 @@ cudaError_t backward(RecurrenceArgs a) {
             f.edges = a.edges = edges;
             f.y = nullptr;
             f.h_out = nullptr;
-            if (cudaError_t e = forward<In, IO>(f, w)) return e;
+            if (cudaError_t e = forward<In, IO, true>(f, w)) return e;
         }
+        Tensors m{};
+        if (!make_maps<In, IO>(m, a, true)) return cudaErrorInvalidValue;
         if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, kStages>, "recurrence_bwd_kernel",
-                                        kStages * Stage<In, IO, true>::kBytes, ctas, a, w,
+                                        kStages * S::kBytes + S::kOuts, ctas, a, w, m,
                                         a.dA_log ? part : nullptr))
             return e;
     }
@@ -811,7 +921,7 @@ cudaError_t forward_of(const RecurrenceArgs& a) {
     Plan w;
     lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, false, &w, nullptr, nullptr);
     if (cudaError_t e = setup(a, w, a.h0, a.h_out)) return e;
-    return a.T_total == 0 ? cudaSuccess : forward<IO, IO>(a, w);
+    return a.T_total == 0 ? cudaSuccess : forward<IO, IO, false>(a, w);
 }
 
 }  // namespace
