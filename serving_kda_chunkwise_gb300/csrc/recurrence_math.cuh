@@ -85,15 +85,17 @@ __device__ __forceinline__ float2 rsqrt_pair(float2 d) {
 
 // n tokens in steps that leave the tokens independent of each other: c[k], and the negated input
 // terms nb[k] = -b.  in(which, k): input x, z or i (0, 1, 2) of token k.
+//   b = m s(i) x = m^2 x / sqrt(m^2 (1 + e^-i)^2): one root for m's and s(i)'s reciprocal.  (1e-37 next
+// to m^2 keeps it from zero, so that the root of 0 times infinity is not taken; an m below 3e-19 is
+// lost in it, and a s(i) below 2^-64 in the square's overflow.)
 template <int n, typename In>
 __device__ __forceinline__ void recurrence_steps(In&& in, float2 neg_log2, const GateBound& gb,
                                                  float2 (&c)[n], float2 (&nb)[n]) {
 #pragma unroll
     for (int k = 0; k < n; ++k) {
         const float2 sz = rcp1_pair(ex2_pair(mul_pair(in(1, k), neg_log2)));
-        const float2 si = rcp1_pair(ex2_pair(mul_pair(in(2, k), both(-kLog2e))));
         c[k] = expm1_near(mul_pair(sz, both(gb.scaled)));
-        nb[k] = mul_pair(si, in(0, k));
+        nb[k] = add_pair(ex2_pair(mul_pair(in(2, k), both(-kLog2e))), both(1.f));
     }
     for (int j = gb.doublings; j > 0; --j)
 #pragma unroll
@@ -101,7 +103,9 @@ __device__ __forceinline__ void recurrence_steps(In&& in, float2 neg_log2, const
 #pragma unroll
     for (int k = 0; k < n; ++k) {
         const float2 d = twice(c[k]);  // -m^2
-        nb[k] = mul_pair(mul_pair(d, rsqrt_pair(d)), nb[k]);
+        const float2 y = mul_pair(mul_pair(add_pair(d, both(-1e-37f)), nb[k]), nb[k]);
+        const float2 q = make_float2(rsqrt_approx(-y.x), rsqrt_approx(-y.y));
+        nb[k] = mul_pair(mul_pair(d, q), in(0, k));
     }
 }
 // h_t from h_{t-1}
