@@ -362,7 +362,9 @@ __device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w
                                           char* ring, Maps& maps, int begin, int end, int c0,
                                           First&& first, Second&& second) {
     __shared__ uint64_t full[kStages];
-    constexpr int kAhead = kStages - 1;  // tiles from the one worked on to the one loaded
+    // Loads go out after the CTA's barrier, into the stage that is free then: the tile's own, or where
+    // its results leave from there, the one before it.
+    constexpr int kAhead = kOutputs ? kStages - 1 : kStages;
     const unsigned rank = cluster_rank(), ctas = cluster_size();
     const int base = begin / kTok * kTok, n = (end - base + kT - 1) / kT;
     const int steps = (n + (int)ctas - 1) / (int)ctas;
@@ -415,7 +417,8 @@ __device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w
         const bool next_marked = __syncthreads_or(coming != 0u);
         const float4 before = marked ? compose<true>(maps, buf, turn, lane, rank, ctas)
                                      : compose<false>(maps, buf, turn, lane, rank, ctas);
-        const int e = load(k + kAhead, before_s);
+        const int free = kOutputs ? before_s : s;
+        const int e = load(k + kAhead, free);
         edge = edge_at(k + 1);
         const uint32_t later = marks_at(k + 2);
         // (the next maps for this buffer are sent when this CTA's of the next step are there, which
@@ -439,7 +442,7 @@ __device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w
                 __syncwarp();
             }
         }
-        if (place(k + kAhead) < n) put_exps<S, In>(ring + before_s * S::kBytes, e);
+        if (place(k + kAhead) < n) put_exps<S, In>(ring + free * S::kBytes, e);
         marked = next_marked;
         marks = coming;
         coming = later;
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
     float2 c[kTok], nb[kTok];
     float2 opening = both(0.f);  // the initial state of a sequence that starts with the first token
-    for_tiles<S, In, IO, false, kStages, kOnlyEdges ? 0 : 1>(
+    for_tiles<S, In, IO, false, kStages, 0>(
         a, w, m, ring, maps, begin, end, c0,
         [&](const V& v, int64_t t, uint32_t marks) {
             recurrence_steps([&](int which, int k) { return v.input(which, k); }, nl, gb, c, nb);
@@ -529,25 +532,27 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         [&](const V& v, int64_t t, uint32_t marks, bool whole, float2 h) {
             if (live && a.edges && t >= begin && t < end)
                 store_pair(a.edges + t / kTok * a.D + ch, marks & 1 ? opening : h);
+            if (kOnlyEdges || !live) return;
+            IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
             if (whole && marks == 0u) {
-                if (kOnlyEdges) return;
 #pragma unroll
                 for (int k = 0; k < kTok; ++k) {
                     h = recurrence_next(c[k], nb[k], h);
-                    store_pair(v.out(0, k), h);
+                    store_pair(y, h);
+                    y += a.D;
                 }
                 return;
             }
-            IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
 #pragma unroll
             for (int k = 0; k < kTok; ++k) {
                 if (marks >> k & 1) h = both(0.f);
                 h = recurrence_next(c[k], nb[k], h);
-                if (kOnlyEdges) continue;
-                if (whole) store_pair(v.out(0, k), h);
-                else if (live && t + k >= begin && t + k < end) store_pair(y + (int64_t)k * a.D, h);
-                if (live && marks >> (8 + k) & 1 && t + k >= begin && t + k < end && a.h_out)
-                    store_pair(a.h_out + (int64_t)end_at(w, t + k) * a.D + ch, h);
+                if (t + k >= begin && t + k < end) {
+                    store_pair(y, h);
+                    if (marks >> (8 + k) & 1 && a.h_out)
+                        store_pair(a.h_out + (int64_t)end_at(w, t + k) * a.D + ch, h);
+                }
+                y += a.D;
             }
         });
 }
@@ -845,7 +850,7 @@ bool make_maps(Tensors& m, const RecurrenceArgs& a, bool bwd) {
                      !make_map<In>(&m.in[1], a.z, T, a.D, a.z_ld) ||
                      !make_map<In>(&m.in[2], a.i, T, a.D, a.i_ld)))
         return false;
-    if (!bwd) return a.y == nullptr || make_map<IO>(&m.out[0], a.y, T, a.D, a.D);
+    if (!bwd) return true;
     return (m.plain || make_map<IO>(&m.in[3], a.dy, T, a.D, a.dy_ld)) &&
            make_map<IO>(&m.out[0], a.dx, T, a.D, a.D) && make_map<IO>(&m.out[1], a.dz, T, a.D, a.D) &&
            make_map<IO>(&m.out[2], a.di, T, a.D, a.D);
@@ -882,7 +887,7 @@ cudaError_t forward(const RecurrenceArgs& a, const Plan& w) {
     if (!make_maps<In, IO>(m, a, false)) return cudaErrorInvalidValue;
     const int ctas = count_ctas(a.T_total, w.runs, w.cols, kMaxCluster);
     return launch_scan(scan_kernel<In, IO, kStages, kOnlyEdges>, "recurrence_kernel",
-                       kStages * S::kBytes + (kOnlyEdges ? 0 : S::kOuts), ctas, a, w, m);
+                       kStages * S::kBytes, ctas, a, w, m);
 }
 
 template <typename In, typename IO>
