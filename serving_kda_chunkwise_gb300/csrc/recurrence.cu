@@ -5,13 +5,15 @@
 //   l_t = dy_t + a_{t+1} l_{t+1}, backwards, for the gradients
 //
 // Both are scans of affine maps (P, H): h -> P h + H.  A cluster of CTAs takes 64 channels along a
-// run, some consecutive sequences, and carries their state in registers.  In a step each of its CTAs
-// has a tile of 64 tokens: a warp holds 8 tokens, a lane two channels.  The warps' maps meet in
-// shared memory; the tile's map is sent to every CTA of the cluster (distributed shared memory, two
-// buffers, one cluster barrier a step); every thread applies the maps before it to the carried
-// state, goes over its tokens again, in registers, and writes.  So inputs are read once, results
-// written once, in rows of 128 bytes (bf16), and no cluster waits for another.  (Narrower columns
-// instead of clusters cost more in the loads and stores of short rows than the barrier does.)
+// run, some consecutive sequences.  In a step each of its CTAs has a tile of 64 tokens: each of eight
+// warps holds 8 tokens, a lane two channels, and leaves its tokens' map in shared memory.  The maps
+// are composed, the tile's map is sent to every CTA of the cluster (stores into distributed shared
+// memory that count their bytes on a barrier there), and the state is carried over the cluster's
+// maps; then every warp goes over its tokens again, in registers, and writes.  So inputs are read
+// once, results written once, in rows of 128 bytes (bf16), and no cluster waits for another.
+// (Narrower columns instead of clusters cost more in the copies of short rows.)
+//   The forward has two warps more, one that composes and sends, one that carries the state, and its
+// eight form the next tile's maps before they write this one's: the exchange takes as long as that.
 //
 // The gradients go over the tiles backwards.  A thread's states come from the edges, the state that
 // every 8th token starts from, which the forward writes on request; without them a forward that
@@ -41,7 +43,8 @@ constexpr int kC = 64;      // channels of a tile, and of an exponent of packed 
 constexpr int kWarps = 8;
 constexpr int kT = kTok * kWarps;  // tokens of a tile
 constexpr int kMaxCluster = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kThreads = 32 * kWarps;         // of the gradients' CTAs
+constexpr int kFwdThreads = 32 * (kWarps + 2);  // of the forward's
 
 // What the setup launch leaves for the scan.
 struct Plan {
@@ -86,12 +89,13 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* sr
                  : "memory");
 }
 
-// 64 tokens x 64 channels of a tensor by plain copies; rows and channels past its end become zeros.
+// 64 tokens x 64 channels of a tensor by a warp's plain copies; rows and channels past its end become
+// zeros.
 template <typename In>
 __device__ __forceinline__ void copy_tile(char* dst, const void* src, int64_t ld, int64_t t0, int c0,
-                                          int64_t T, int D) {
+                                          int64_t T, int D, int lane) {
     constexpr int kElems = 8 / (int)sizeof(In);
-    for (int p = threadIdx.x; p < kT * kC / kElems; p += kThreads) {
+    for (int p = lane; p < kT * kC / kElems; p += 32) {
         const int row = p * kElems / kC, c = p * kElems % kC;
         const bool live = t0 + row < T && c0 + c < D;
         const In* s = static_cast<const In*>(src) + (live ? (t0 + row) * ld + c0 + c : 0);
@@ -101,36 +105,54 @@ __device__ __forceinline__ void copy_tile(char* dst, const void* src, int64_t ld
     }
 }
 
-// Starts the loads of the tile from token t0 and channel c0; called by all threads.  Of packed
-// inputs, the exponent that this thread has to put into the stage is returned.
+// Arrivals that fill a stage: the copies' (every lane's where they are plain ones), and for packed
+// inputs that of the exponents.
+template <typename In>
+__device__ __forceinline__ int fill_count(const Tensors& m) {
+    return sizeof(In) == 1 ? 1 + (m.plain ? 32 : 1) : 1;
+}
+// A lane's share of a tile's exponents, on their way.
+struct Exps {
+    int8_t e[3 * kT / 32];
+};
+
+// Starts the loads of the tile from token t0 and channel c0; called by a warp.
 template <typename S, typename In, typename IO, bool kBwd>
-__device__ __forceinline__ int load_stage(const RecurrenceArgs& a, const Tensors& m, char* st,
-                                          uint64_t* full, int t0, int c0) {
+__device__ __forceinline__ void load_stage(const RecurrenceArgs& a, const Tensors& m, char* st,
+                                           uint64_t* full, int t0, int c0, int lane, Exps& exps) {
     if (sizeof(In) == 1 && m.plain) {
-        copy_tile<In>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D);
-        copy_tile<In>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D);
-        copy_tile<In>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D);
-        if (kBwd) copy_tile<IO>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D);
+        copy_tile<In>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D, lane);
+        copy_tile<In>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D, lane);
+        copy_tile<In>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D, lane);
+        if (kBwd) copy_tile<IO>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D, lane);
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full))
                      : "memory");
-    } else if (threadIdx.x == 0) {
+    } else if (lane == 0) {
         mbar_expect_tx(full, S::kExps);
         tma_load(st, &m.in[0], c0, t0, full);
         tma_load(st + S::kIn, &m.in[1], c0, t0, full);
         tma_load(st + 2 * S::kIn, &m.in[2], c0, t0, full);
         if (kBwd) tma_load(st + S::kDy, &m.in[3], c0, t0, full);
     }
-    if (sizeof(In) == 1 && threadIdx.x < 3 * kT) {
-        const int k = threadIdx.x / kT, t = threadIdx.x % kT;
-        const int8_t* e = k == 0 ? a.x_exps : k == 1 ? a.z_exps : a.i_exps;
-        if (t0 + t < a.T_total) return __ldg(e + (int64_t)(c0 / kC) * a.T_total + t0 + t);
+    if (sizeof(In) == 1) {
+#pragma unroll
+        for (int j = 0; j < 3 * kT / 32; ++j) {
+            const int n = j * 32 + lane, t = n % kT;
+            const int8_t* e = n < kT ? a.x_exps : n < 2 * kT ? a.z_exps : a.i_exps;
+            exps.e[j] = t0 + t < a.T_total ? __ldg(e + (int64_t)(c0 / kC) * a.T_total + t0 + t) : 0;
+        }
     }
-    return 0;
 }
+// Puts the exponents into the stage that load_stage was called for.
 template <typename S, typename In>
-__device__ __forceinline__ void put_exps(char* st, int e) {
-    if (sizeof(In) == 1 && threadIdx.x < 3 * kT)
-        reinterpret_cast<int8_t*>(st)[S::kExps + threadIdx.x] = (int8_t)e;
+__device__ __forceinline__ void put_exps(char* st, uint64_t* full, int lane, const Exps& exps) {
+    if (sizeof(In) == 1) {
+#pragma unroll
+        for (int j = 0; j < 3 * kT / 32; ++j)
+            reinterpret_cast<int8_t*>(st)[S::kExps + j * 32 + lane] = exps.e[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+    }
 }
 
 __device__ __forceinline__ float2 pair(const __nv_bfloat16* p) {
@@ -148,7 +170,7 @@ template <typename S, typename In, typename IO>
 struct View {
     char* st;
     int warp, lane;
-    float2 edge;  // (gradients) the state before the warp's tokens
+    char* outs = nullptr;
     template <typename E>
     __device__ __forceinline__ const E* at(int part, int k) const {
         return reinterpret_cast<const E*>(st + part) + (warp * kTok + k) * kC + 2 * lane;
@@ -167,8 +189,7 @@ struct View {
         }
     }
     __device__ __forceinline__ float2 dy(int k) const { return pair(at<IO>(S::kDy, k)); }
-    // the place of output `which` of token k
-    char* outs;
+    // the place of result `which` of token k
     __device__ __forceinline__ IO* out(int which, int k) const {
         return reinterpret_cast<IO*>(outs + which * S::kOut) + (warp * kTok + k) * kC + 2 * lane;
     }
@@ -277,13 +298,6 @@ __device__ __forceinline__ float4 after(float4 m, float4 before) {
 }
 __device__ __forceinline__ float4 identity() { return make_float4(1.f, 1.f, 0.f, 0.f); }
 
-// What a CTA keeps of a step's maps.
-struct Maps {
-    float4 warps[kWarps][32];          // of its own tile
-    float4 tiles[2][kMaxCluster][32];  // of the cluster's, in the scan's order; alternating
-    uint64_t there[2];                 // those have arrived
-};
-
 __device__ __forceinline__ unsigned cluster_rank() {
     unsigned r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -294,12 +308,14 @@ __device__ __forceinline__ unsigned cluster_size() {
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
-// Writes v to p's place in the shared memory of CTA `rank` of the cluster, and counts its bytes on the
-// barrier in bar's place there.
-__device__ __forceinline__ void send(float4* p, uint64_t* bar, unsigned rank, float4 v) {
-    uint32_t at, done;
+// p's place in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t place_in(const void* p, unsigned rank) {
+    uint32_t at;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(done) : "r"(smem_u32(bar)), "r"(rank));
+    return at;
+}
+// Writes v there, and counts its bytes on a barrier there.
+__device__ __forceinline__ void send(uint32_t at, uint32_t done, float4 v) {
     asm volatile(
         "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
         "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(done)
@@ -312,38 +328,6 @@ __device__ __forceinline__ void cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// With the warps' maps there: the map of those before `turn` (in the scan's order); the last one
-// sends the tile's map to the CTAs of the cluster.
-template <bool kCut>
-__device__ __forceinline__ float4 compose(Maps& m, int buf, int turn, int lane, unsigned rank,
-                                          unsigned ctas) {
-    float4 before = identity();
-#pragma unroll
-    for (int j = 0; j < kWarps - 1; ++j)
-        if (j < turn) before = after<kCut>(m.warps[j][lane], before);
-    if (turn == kWarps - 1) {
-        const float4 all = after<kCut>(m.warps[turn][lane], before);
-        for (unsigned j = 0; j < ctas; ++j)
-            send(&m.tiles[buf][rank][lane], &m.there[buf], j, all);
-    }
-    return before;
-}
-
-// The state before the thread's tokens; carry: from before the step's tiles to after them.
-__device__ __forceinline__ float2 start_state(const Maps& m, int buf, int lane, float4 before,
-                                              unsigned rank, unsigned ctas, bool marked,
-                                              float2& carry) {
-    float2 h = carry, mine = carry;
-#pragma unroll
-    for (unsigned j = 0; j < kMaxCluster; ++j) {
-        if (j >= ctas) break;
-        if (j == rank) mine = h;
-        h = apply<true>(m.tiles[buf][j][lane], h);
-    }
-    carry = h;
-    return marked ? apply<true>(before, mine) : apply<false>(before, mine);
-}
-
 // ------------------------------------------------------------- the loop --
 
 // The marks of tokens t .. t + 7.
@@ -352,103 +336,37 @@ __device__ __forceinline__ uint32_t marks_of(const Plan& w, int64_t t, int64_t T
     return (t == 0 ? 1u : 0u) | (T > t && T <= t + kTok ? 256u << (T - 1 - t) : 0u);
 }
 
-// Runs first(view, t0, marks), which returns the warp's map, and second(view, t0, marks, whole, state
-// before the warp's tokens) over the tiles of a CTA in its cluster's run, their inputs loaded ahead.
-// whole: the tile lies in the run, and second() leaves its results in the view's places for kOutputs
-// outputs; otherwise it stores those of the run itself.
-template <typename S, typename In, typename IO, bool kBwd, int kStages, int kOutputs, typename First,
-          typename Second>
-__device__ __forceinline__ void for_tiles(const RecurrenceArgs& a, const Plan& w, const Tensors& m,
-                                          char* ring, Maps& maps, int begin, int end, int c0,
-                                          First&& first, Second&& second) {
-    __shared__ uint64_t full[kStages];
-    // Loads go out after the CTA's barrier, into the stage that is free then: the tile's own, or where
-    // its results leave from there, the one before it.
-    constexpr int kAhead = kOutputs ? kStages - 1 : kStages;
-    const unsigned rank = cluster_rank(), ctas = cluster_size();
-    const int base = begin / kTok * kTok, n = (end - base + kT - 1) / kT;
-    const int steps = (n + (int)ctas - 1) / (int)ctas;
-    // step k's tile, in the scan's order; there may be none left for this CTA
-    auto place = [&](int k) { return k * (int)ctas + (int)rank; };
-    auto first_token = [&](int k) { return base + (kBwd ? n - 1 - place(k) : place(k)) * kT; };
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int turn = kBwd ? kWarps - 1 - warp : warp;  // in the scan's order
-    char* const outs = ring + kStages * S::kBytes;
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < kStages; ++k) mbar_init(&full[k], sizeof(In) == 1 && m.plain ? kThreads : 1);
-        for (int k = 0; k < 2; ++k) mbar_init(&maps.there[k], 1);
-        fence_mbar_init();
-        for (int k = 0; k < 2; ++k) mbar_expect_tx(&maps.there[k], ctas * 32 * sizeof(float4));
+// A CTA's tiles in its cluster's run.  Step k's is the `place(k)`-th in the scan's order; there may be
+// none left for this CTA.
+template <bool kBwd>
+struct Steps {
+    int begin, end, base, tiles, count, rank, ctas;
+    __device__ __forceinline__ Steps(int b, int e)
+        : begin(b), end(e), base(b / kTok * kTok), rank((int)cluster_rank()), ctas((int)cluster_size()) {
+        tiles = (end - base + kT - 1) / kT;
+        count = (tiles + ctas - 1) / ctas;
     }
-    __syncthreads();
-    cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
-    auto load = [&](int k, int s) {
-        return place(k) < n ? load_stage<S, In, IO, kBwd>(a, m, ring + s * S::kBytes, &full[s],
-                                                          first_token(k), c0)
-                            : 0;
-    };
-    // a warp's marks and edge of step k's tile
-    auto marks_at = [&](int k) {
-        return place(k) < n ? marks_of(w, first_token(k) + warp * kTok, a.T_total) : 0u;
-    };
-    auto edge_at = [&](int k) {
-        const int64_t t = first_token(k) + warp * kTok;
-        const int c = c0 + 2 * lane;
-        return kBwd && place(k) < n && t < a.T_total && c < a.D
-                   ? __ldg(reinterpret_cast<const float2*>(a.edges + t / kTok * a.D + c))
-                   : both(0.f);
-    };
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) put_exps<S, In>(ring + k * S::kBytes, load(k, k));
-    float2 edge = edge_at(0), carry = both(0.f);
-    uint32_t marks = marks_at(0), coming = marks_at(1);
-    bool marked = __syncthreads_or(marks != 0u), broken = false;
-    cluster_wait();
-    for (int k = 0, s = 0; k < steps; ++k) {
-        char* const st = ring + s * S::kBytes;
-        const View<S, In, IO> v{st, warp, lane, edge, S::kInPlace ? st : outs};
-        const int t0 = first_token(k);
-        const int64_t t = t0 + warp * kTok;
-        const bool some = place(k) < n, whole = some && t0 >= begin && t0 + kT <= end;
-        if (some && !broken) broken = !mbar_wait(&full[s], k / kStages & 1, a.dev_err);
-        maps.warps[turn][lane] = some ? first(v, t, marks) : identity();
-        const int buf = k & 1, before_s = s == 0 ? kStages - 1 : s - 1;
-        if (kOutputs && threadIdx.x == 0) bulk_wait_read0();  // (the stage before this one is free)
-        const bool next_marked = __syncthreads_or(coming != 0u);
-        const float4 before = marked ? compose<true>(maps, buf, turn, lane, rank, ctas)
-                                     : compose<false>(maps, buf, turn, lane, rank, ctas);
-        const int free = kOutputs ? before_s : s;
-        const int e = load(k + kAhead, free);
-        edge = edge_at(k + 1);
-        const uint32_t later = marks_at(k + 2);
-        // (the next maps for this buffer are sent when this CTA's of the next step are there, which
-        // its barrier of that step precedes)
-        if (!broken) broken = !mbar_wait(&maps.there[buf], k / 2 & 1, a.dev_err);
-        if (threadIdx.x == 0) mbar_expect_tx(&maps.there[buf], ctas * 32 * sizeof(float4));
-        const float2 h = start_state(maps, buf, lane, before, rank, ctas, marked, carry);
-        if (some) second(v, t, marks, whole, h);
-        if (kOutputs && whole) {
-            fence_async_smem();
-            if (warp > 0) {
-                asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
-            } else {
-                asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
-                if (lane == 0) {
-#pragma unroll
-                    for (int o = 0; o < kOutputs; ++o)
-                        tma_store(&m.out[o], v.outs + o * S::kOut, c0, t0);
-                    bulk_commit();
-                }
-                __syncwarp();
-            }
-        }
-        if (place(k + kAhead) < n) put_exps<S, In>(ring + free * S::kBytes, e);
-        marked = next_marked;
-        marks = coming;
-        coming = later;
-        s = s + 1 == kStages ? 0 : s + 1;
+    __device__ __forceinline__ bool some(int k) const { return k * ctas + rank < tiles; }
+    // the bytes of a step's maps from the cluster
+    __device__ __forceinline__ uint32_t bytes() const { return ctas * 32 * (uint32_t)sizeof(float4); }
+    __device__ __forceinline__ int first_token(int k) const {
+        const int p = k * ctas + rank;
+        return base + (kBwd ? tiles - 1 - p : p) * kT;
     }
-    if (kOutputs && threadIdx.x == 0) bulk_wait0();
+};
+
+// The state that a CTA's tile starts from; carry: from before the step's tiles to after them.
+__device__ __forceinline__ float2 carry_over(const float4 (*tiles)[32], int lane, int rank, int ctas,
+                                             float2& carry) {
+    float2 h = carry, mine = carry;
+#pragma unroll
+    for (int j = 0; j < kMaxCluster; ++j) {
+        if (j >= ctas) break;
+        if (j == rank) mine = h;
+        h = apply<true>(tiles[j][lane], h);
+    }
+    carry = h;
+    return mine;
 }
 
 // The cluster's run and first channel; false where it has nothing to do.
@@ -479,179 +397,428 @@ __device__ __forceinline__ int end_at(const Plan& w, int64_t t) {
 
 // ---------------------------------------------------------------- forward --
 
+// What a CTA keeps of its steps' maps, in the scan's order.  (Another CTA may send its map of three
+// steps on before this one has carried the state over this step's; for the fourth it needs this
+// one's of the second, formed after the states of this one.)
+constexpr int kTurns = 4;
+template <int kStages>
+struct Exchange {
+    float4 warps[2][kWarps][32];            // its warps'; then, of the warps before each
+    float4 tiles[kTurns][kMaxCluster][32];  // the cluster's tiles'
+    float2 mine[2][32];                     // the state that its tile starts from
+    uint64_t maps[2], there[kTurns], states[2], full[kStages];  // barriers: those are there
+};
+
+// The warp that composes a step's maps, sends the tile's, and issues the loads of later tiles.  (Of
+// waits that ran out, here and below: the ones after are not taken, so that everything ends.)
+template <typename S, typename In, typename IO, int kStages>
+__device__ __forceinline__ void send_maps(const RecurrenceArgs& a, const Tensors& m,
+                                          Exchange<kStages>& x, char* ring, const Steps<false>& steps,
+                                          int c0, int lane) {
+    Exps exps;
+    auto load = [&](int k) {
+        if (steps.some(k))
+            load_stage<S, In, IO, false>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
+                                         steps.first_token(k), c0, lane, exps);
+    };
+    auto put = [&](int k) {
+        if (steps.some(k))
+            put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
+    };
+    for (int k = 0; k < kStages; ++k) {
+        load(k);
+        put(k);
+    }
+    // the places of `tiles` and `there` in the cluster's CTAs
+    uint32_t tiles[kMaxCluster], there[kMaxCluster];
+#pragma unroll
+    for (int j = 0; j < kMaxCluster; ++j) {
+        const unsigned to = j < steps.ctas ? j : 0;
+        tiles[j] = place_in(&x.tiles[0][steps.rank][lane], to);
+        there[j] = place_in(&x.there[0], to);
+    }
+    bool broken = false;
+    for (int k = 0; k < steps.count; ++k) {
+        const int buf = k & 1, turn = k % kTurns;
+        if (!broken) broken = !mbar_wait(&x.maps[buf], k / 2 & 1, a.dev_err);
+        float4 own[kWarps], before[kWarps], all;
+#pragma unroll
+        for (int j = 0; j < kWarps; ++j) own[j] = x.warps[buf][j][lane];
+        all = own[0];
+        before[0] = identity();
+#pragma unroll
+        for (int j = 1; j < kWarps; ++j) {
+            before[j] = all;
+            all = after<true>(own[j], all);
+        }
+#pragma unroll
+        for (int j = 0; j < kMaxCluster; ++j)
+            if (j < steps.ctas)
+                send(tiles[j] + turn * (uint32_t)sizeof x.tiles[0], there[j] + turn * 8u, all);
+#pragma unroll
+        for (int j = 0; j < kWarps; ++j) x.warps[buf][j][lane] = before[j];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.states[buf]);
+        if (!broken) {
+            load(k + kStages);
+            put(k + kStages);
+        }
+    }
+}
+
+// The warp that carries the state over the cluster's tiles.
+template <int kStages>
+__device__ __forceinline__ void carry_states(const RecurrenceArgs& a, Exchange<kStages>& x,
+                                             const Steps<false>& steps, int lane) {
+    float2 carry = both(0.f);
+    bool broken = false;
+    for (int k = 0; k < steps.count; ++k) {
+        const int turn = k % kTurns;
+        if (!broken) broken = !mbar_wait(&x.there[turn], k / kTurns & 1, a.dev_err);
+        if (lane == 0) mbar_expect_tx(&x.there[turn], steps.bytes());
+        x.mine[k & 1][lane] = carry_over(x.tiles[turn], lane, steps.rank, steps.ctas, carry);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.states[k & 1]);
+    }
+}
+
 template <typename In, typename IO, int kStages, bool kOnlyEdges>
-__global__ void __launch_bounds__(kThreads, 2) scan_kernel(
+__global__ void __launch_bounds__(kFwdThreads, 2) scan_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
     const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m) {
     using S = Stage<In, IO, false>;
-    using V = View<S, In, IO>;
     extern __shared__ __align__(128) char ring[];
-    __shared__ Maps maps;
+    __shared__ Exchange<kStages> x;
     grid_dependency_wait();
     int begin, end, c0;
     if (!find_run(a, w, begin, end, c0)) return;
-    const int ch = c0 + 2 * (threadIdx.x % 32);
+    const Steps<false> steps(begin, end);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kStages; ++k) mbar_init(&x.full[k], fill_count<In>(m));
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(&x.maps[k], kWarps);
+            mbar_init(&x.states[k], 2);
+        }
+        for (int k = 0; k < kTurns; ++k) mbar_init(&x.there[k], 1);
+        fence_mbar_init();
+        for (int k = 0; k < kTurns; ++k) mbar_expect_tx(&x.there[k], steps.bytes());
+    }
+    __syncthreads();
+    cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
+    cluster_wait();
+    if (warp >= kWarps) {
+        if (warp == kWarps) send_maps<S, In, IO, kStages>(a, m, x, ring, steps, c0, lane);
+        else carry_states(a, x, steps, lane);
+        __syncwarp();
+        cluster_arrive();  // (a CTA stays until nobody can send to it)
+        cluster_wait();
+        return;
+    }
+    const int ch = c0 + 2 * lane;
     const bool live = ch < a.D;
     const float2 nl =
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
-    float2 c[kTok], nb[kTok];
-    float2 opening = both(0.f);  // the initial state of a sequence that starts with the first token
-    for_tiles<S, In, IO, false, kStages, 0>(
-        a, w, m, ring, maps, begin, end, c0,
-        [&](const V& v, int64_t t, uint32_t marks) {
-            recurrence_steps([&](int which, int k) { return v.input(which, k); }, nl, gb, c, nb);
-            float2 P = both(1.f), H = both(0.f);
-            if ((marks & 0xffu) == 0u) {
+    bool broken = false;
+    struct Held {  // tokens of a step: c, -b
+        float2 c[kTok], nb[kTok];
+        uint32_t marks;
+    };
+    uint32_t coming = marks_of(w, steps.first_token(0) + warp * kTok, a.T_total);
+    // Step k's tokens and their map.
+    auto first = [&](int k, Held& o) {
+        const int buf = k & 1, s = k % kStages;
+        const int64_t t = steps.first_token(k) + warp * kTok;
+        o.marks = coming;
+        coming = marks_of(w, steps.first_token(k + 1) + warp * kTok, a.T_total);
+        float2 P = both(1.f), H = both(0.f);
+        if (steps.some(k)) {
+            if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
+            const View<S, In, IO> v{ring + s * S::kBytes, warp, lane};
+            recurrence_steps([&](int which, int j) { return v.input(which, j); }, nl, gb, o.c, o.nb);
+            if ((o.marks & 0xffu) == 0u) {
 #pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                    P = fma_pair(c[k], P, P);
-                    H = recurrence_next(c[k], nb[k], H);
+                for (int j = 0; j < kTok; ++j) {
+                    P = fma_pair(o.c[j], P, P);
+                    H = recurrence_next(o.c[j], o.nb[j], H);
                 }
             } else {
-                if (a.h0) {  // initial states: into the first tokens' input terms
-                    float2 h0[kTok];
+                // initial states: into the first tokens' input terms
+                float2 opening = both(0.f);
+                if (a.h0) {
 #pragma unroll
-                    for (int k = 0; k < kTok; ++k)
-                        h0[k] = marks >> k & 1 && live ? state_row(a.h0, start_at(w, t + k), a.D, ch)
-                                                       : both(0.f);
-                    opening = h0[0];
+                    for (int j = 0; j < kTok; j += 2) {
+                        float2 h0[2];
 #pragma unroll
-                    for (int k = 0; k < kTok; ++k)
-                        if (marks >> k & 1)
-                            nb[k] = mul_pair(recurrence_next(c[k], nb[k], h0[k]), both(-1.f));
+                        for (int i = 0; i < 2; ++i)
+                            h0[i] = o.marks >> (j + i) & 1 && live
+                                        ? state_row(a.h0, start_at(w, t + j + i), a.D, ch)
+                                        : both(0.f);
+                        if (j == 0) opening = h0[0];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            if (o.marks >> (j + i) & 1)
+                                o.nb[j + i] =
+                                    mul_pair(recurrence_next(o.c[j + i], o.nb[j + i], h0[i]), both(-1.f));
+                    }
                 }
+                if (o.marks & 1 && a.edges && live && t >= begin && t < end)
+                    store_pair(a.edges + t / kTok * a.D + ch, opening);
 #pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                    if (marks >> k & 1) H = both(0.f);
-                    H = recurrence_next(c[k], nb[k], H);
+                for (int j = 0; j < kTok; ++j) {
+                    if (o.marks >> j & 1) H = both(0.f);
+                    H = recurrence_next(o.c[j], o.nb[j], H);
                 }
                 P = both(-0.f);
             }
-            return make_float4(P.x, P.y, H.x, H.y);
-        },
-        [&](const V& v, int64_t t, uint32_t marks, bool whole, float2 h) {
-            if (live && a.edges && t >= begin && t < end)
-                store_pair(a.edges + t / kTok * a.D + ch, marks & 1 ? opening : h);
-            if (kOnlyEdges || !live) return;
-            IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
-            if (whole && marks == 0u) {
+        }
+        x.warps[buf][warp][lane] = make_float4(P.x, P.y, H.x, H.y);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&x.maps[buf]);
+    };
+    // Step k's results, from the state that its tokens start from.
+    auto second = [&](int k, const Held& o) {
+        const int buf = k & 1;
+        const int64_t t = steps.first_token(k) + warp * kTok;
+        if (!broken) broken = !mbar_wait(&x.states[buf], k / 2 & 1, a.dev_err);
+        float2 h = apply<true>(x.warps[buf][warp][lane], x.mine[buf][lane]);
+        if (!steps.some(k) || !live || t + kTok <= begin || t >= end) return;
+        if (a.edges && t >= begin && !(o.marks & 1)) store_pair(a.edges + t / kTok * a.D + ch, h);
+        IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
+        if (o.marks == 0u) {
+            if (kOnlyEdges) return;
 #pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                    h = recurrence_next(c[k], nb[k], h);
-                    store_pair(y, h);
-                    y += a.D;
-                }
-                return;
-            }
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-                if (marks >> k & 1) h = both(0.f);
-                h = recurrence_next(c[k], nb[k], h);
-                if (t + k >= begin && t + k < end) {
-                    store_pair(y, h);
-                    if (marks >> (8 + k) & 1 && a.h_out)
-                        store_pair(a.h_out + (int64_t)end_at(w, t + k) * a.D + ch, h);
-                }
+            for (int j = 0; j < kTok; ++j) {
+                h = recurrence_next(o.c[j], o.nb[j], h);
+                store_pair(y, h);
                 y += a.D;
             }
-        });
+            return;
+        }
+        if (kOnlyEdges) return;
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+            if (o.marks >> j & 1) h = both(0.f);
+            h = recurrence_next(o.c[j], o.nb[j], h);
+            if (t + j >= begin && t + j < end) {
+                store_pair(y, h);
+                if (o.marks >> (8 + j) & 1 && a.h_out)
+                    store_pair(a.h_out + (int64_t)end_at(w, t + j) * a.D + ch, h);
+            }
+            y += a.D;
+        }
+    };
+    Held even, odd;
+    for (int k = 0; k <= steps.count; k += 2) {
+        if (k < steps.count) first(k, even);
+        if (k >= 1) second(k - 1, odd);
+        if (k + 1 < steps.count) first(k + 1, odd);
+        if (k < steps.count) second(k, even);
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
 }
 
 // -------------------------------------------------------------- gradients --
+
+// What a CTA keeps of a step's maps, in the scan's order.
+template <int kStages>
+struct Maps {
+    float4 warps[kWarps][32];          // its warps'
+    float4 tiles[2][kMaxCluster][32];  // the cluster's tiles'; of two steps in turn
+    uint64_t there[2], full[kStages];  // barriers: those are there
+};
+
+// With the warps' maps there: the map of those before `turn`; the last one sends the tile's map to
+// the CTAs of the cluster.
+template <bool kCut, int kStages>
+__device__ __forceinline__ float4 compose(Maps<kStages>& x, int buf, int turn, int lane,
+                                          const Steps<true>& steps) {
+    float4 before = identity();
+#pragma unroll
+    for (int j = 0; j < kWarps - 1; ++j)
+        if (j < turn) before = after<kCut>(x.warps[j][lane], before);
+    if (turn == kWarps - 1) {
+        const float4 all = after<kCut>(x.warps[turn][lane], before);
+        for (int j = 0; j < steps.ctas; ++j)
+            send(place_in(&x.tiles[buf][steps.rank][lane], j), place_in(&x.there[buf], j), all);
+    }
+    return before;
+}
 
 template <typename In, typename IO, int kStages>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
     const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m, float* part) {
     using S = Stage<In, IO, true>;
-    using V = View<S, In, IO>;
+    constexpr int kAhead = kStages - 1;  // steps from the one at hand to the one loaded
     extern __shared__ __align__(128) char ring[];
-    __shared__ Maps maps;
+    __shared__ Maps<kStages> x;
     grid_dependency_wait();
     int begin, end, c0;
     const bool any = find_run(a, w, begin, end, c0);
-    const int lane = threadIdx.x % 32, ch = c0 + 2 * lane;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, ch = c0 + 2 * lane;
+    const int turn = kWarps - 1 - warp;  // in the scan's order
     const bool live = ch < a.D;
     float2 dA = both(0.f);
     if (any) {
+        const Steps<true> steps(begin, end);
+        if (threadIdx.x == 0) {
+            for (int k = 0; k < kStages; ++k) mbar_init(&x.full[k], fill_count<In>(m));
+            for (int k = 0; k < 2; ++k) mbar_init(&x.there[k], 1);
+            fence_mbar_init();
+            for (int k = 0; k < 2; ++k) mbar_expect_tx(&x.there[k], steps.bytes());
+        }
+        __syncthreads();
+        cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
+        Exps exps;
+        auto load = [&](int k) {
+            if (warp == 0 && steps.some(k))
+                load_stage<S, In, IO, true>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
+                                            steps.first_token(k), c0, lane, exps);
+        };
+        auto put = [&](int k) {
+            if (warp == 0 && steps.some(k))
+                put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
+        };
+        // a step's marks, and the state that the warp's tokens start from
+        auto marks_at = [&](int k) {
+            return steps.some(k) ? marks_of(w, steps.first_token(k) + warp * kTok, a.T_total) : 0u;
+        };
+        auto edge_at = [&](int k) {
+            const int64_t t = steps.first_token(k) + warp * kTok;
+            return steps.some(k) && t < a.T_total && live
+                       ? __ldg(reinterpret_cast<const float2*>(a.edges + t / kTok * a.D + ch))
+                       : both(0.f);
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            load(k);
+            put(k);
+        }
         const ChannelRate r = channel_rate(
             live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), gb.g_min);
-        float2 c[kTok], fx[kTok], fz[kTok], fi[kTok];
-        // the scan's state is -r, what -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
-        for_tiles<S, In, IO, true, kStages, 3>(
-            a, w, m, ring, maps, begin, end, c0,
-            [&](const V& v, int64_t t, uint32_t marks) {
-                // the negated factors of l in the gradients, from the states
+        float2 edge = edge_at(0), carry = both(0.f);
+        uint32_t marks = marks_at(0), coming = marks_at(1);
+        bool marked = __syncthreads_or(marks != 0u), broken = false;
+        cluster_wait();
+        for (int k = 0; k < steps.count; ++k) {
+            const int buf = k & 1, s = k % kStages;
+            char* const st = ring + s * S::kBytes;
+            const View<S, In, IO> v{st, warp, lane, S::kInPlace ? st : ring + kStages * S::kBytes};
+            const int t0 = steps.first_token(k);
+            const int64_t t = t0 + warp * kTok;
+            const bool some = steps.some(k), whole = some && t0 >= begin && t0 + kT <= end;
+            // the negated factors of l in the gradients, from the states; the scan's state is -r, what
+            // -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
+            float2 c[kTok], fx[kTok], fz[kTok], fi[kTok];
+            float2 P = both(1.f), H = both(0.f);
+            if (some) {
+                if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
                 recurrence_grads(
-                    [&](int which, int k) { return v.input(which, k); }, r, gb, v.edge,
-                    [&](int k, float2 h) {
-                        if (marks >> k & 1)
-                            h = a.h0 && live ? state_row(a.h0, start_at(w, t + k), a.D, ch) : both(0.f);
+                    [&](int which, int j) { return v.input(which, j); }, r, gb, edge,
+                    [&](int j, float2 h) {
+                        if (marks >> j & 1)
+                            h = a.h0 && live ? state_row(a.h0, start_at(w, t + j), a.D, ch) : both(0.f);
                         return h;
                     },
                     c, fx, fz, fi);
-                float2 P = both(1.f), H = both(0.f);
                 if ((marks & 0xff00u) == 0u) {
 #pragma unroll
-                    for (int k = kTok - 1; k >= 0; --k) {
-                        P = fma_pair(c[k], P, P);
-                        const float2 l = fma_pair(v.dy(k), both(-1.f), H);
-                        H = fma_pair(c[k], l, l);
+                    for (int j = kTok - 1; j >= 0; --j) {
+                        P = fma_pair(c[j], P, P);
+                        const float2 l = fma_pair(v.dy(j), both(-1.f), H);
+                        H = fma_pair(c[j], l, l);
                     }
                 } else {
 #pragma unroll
-                    for (int k = kTok - 1; k >= 0; --k) {
-                        if (marks >> (8 + k) & 1)
+                    for (int j = kTok - 1; j >= 0; --j) {
+                        if (marks >> (8 + j) & 1)
                             H = a.dh_out && live
-                                    ? mul_pair(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
+                                    ? mul_pair(state_row(a.dh_out, end_at(w, t + j), a.D, ch), both(-1.f))
                                     : both(0.f);
-                        const float2 l = fma_pair(v.dy(k), both(-1.f), H);
-                        H = fma_pair(c[k], l, l);
+                        const float2 l = fma_pair(v.dy(j), both(-1.f), H);
+                        H = fma_pair(c[j], l, l);
                     }
                     P = both(-0.f);
                 }
-                return make_float4(P.x, P.y, H.x, H.y);
-            },
-            [&](const V& v, int64_t t, uint32_t marks, bool whole, float2 nr) {
+            }
+            x.warps[turn][lane] = make_float4(P.x, P.y, H.x, H.y);
+            if (threadIdx.x == 0) bulk_wait_read0();  // (the stage before this one is free)
+            const bool next_marked = __syncthreads_or(coming != 0u);
+            const float4 before = marked ? compose<true>(x, buf, turn, lane, steps)
+                                         : compose<false>(x, buf, turn, lane, steps);
+            load(k + kAhead);
+            edge = edge_at(k + 1);
+            const uint32_t later = marks_at(k + 2);
+            // (the next maps for this buffer are sent when this CTA's of the next step are there, which
+            // its barrier of that step precedes)
+            if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, a.dev_err);
+            if (threadIdx.x == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
+            const float2 mine = carry_over(x.tiles[buf], lane, steps.rank, steps.ctas, carry);
+            float2 nr = marked ? apply<true>(before, mine) : apply<false>(before, mine);
+            // a token's gradients but for the state's
+            auto take = [&](int j, float2 l, IO* dx, IO* dz, IO* di) {
+                const float2 g = mul_pair(l, fz[j]), z = v.input(1, j);
+                store_pair(dx, mul_pair(l, fx[j]));
+                store_pair(dz, g);
+                store_pair(di, mul_pair(l, fi[j]));
+                // (an infinite z has a gradient of zero)
+                dA.x += g.x == 0.f ? 0.f : g.x * z.x;
+                dA.y += g.y == 0.f ? 0.f : g.y * z.y;
+            };
+            if (whole && marks == 0u) {
+#pragma unroll
+                for (int j = kTok - 1; j >= 0; --j) {
+                    const float2 l = fma_pair(v.dy(j), both(-1.f), nr);
+                    nr = fma_pair(c[j], l, l);
+                    take(j, l, v.out(0, j), v.out(1, j), v.out(2, j));
+                }
+            } else if (some) {
                 const int64_t at = t * a.D + ch;
-                // a token's gradients but for the state's
-                auto take = [&](int k, float2 l, IO* dx, IO* dz, IO* di) {
-                    const float2 g = mul_pair(l, fz[k]), z = v.input(1, k);
-                    store_pair(dx, mul_pair(l, fx[k]));
-                    store_pair(dz, g);
-                    store_pair(di, mul_pair(l, fi[k]));
-                    // (an infinite z has a gradient of zero)
-                    dA.x += g.x == 0.f ? 0.f : g.x * z.x;
-                    dA.y += g.y == 0.f ? 0.f : g.y * z.y;
-                };
-                if (whole && marks == 0u) {
 #pragma unroll
-                    for (int k = kTok - 1; k >= 0; --k) {
-                        const float2 l = fma_pair(v.dy(k), both(-1.f), nr);
-                        nr = fma_pair(c[k], l, l);
-                        take(k, l, v.out(0, k), v.out(1, k), v.out(2, k));
-                    }
-                    return;
-                }
-#pragma unroll
-                for (int k = kTok - 1; k >= 0; --k) {
-                    if (marks >> (8 + k) & 1)
+                for (int j = kTok - 1; j >= 0; --j) {
+                    if (marks >> (8 + j) & 1)
                         nr = a.dh_out && live
-                                 ? mul_pair(state_row(a.dh_out, end_at(w, t + k), a.D, ch), both(-1.f))
+                                 ? mul_pair(state_row(a.dh_out, end_at(w, t + j), a.D, ch), both(-1.f))
                                  : both(0.f);
-                    const float2 l = fma_pair(v.dy(k), both(-1.f), nr);
-                    nr = fma_pair(c[k], l, l);
-                    const bool mine = live && t + k >= begin && t + k < end;
-                    const int64_t o = at + (int64_t)k * a.D;
+                    const float2 l = fma_pair(v.dy(j), both(-1.f), nr);
+                    nr = fma_pair(c[j], l, l);
+                    const bool mine_too = live && t + j >= begin && t + j < end;
+                    const int64_t o = at + (int64_t)j * a.D;
                     if (whole)
-                        take(k, l, v.out(0, k), v.out(1, k), v.out(2, k));
-                    else if (mine)
-                        take(k, l, static_cast<IO*>(a.dx) + o, static_cast<IO*>(a.dz) + o,
+                        take(j, l, v.out(0, j), v.out(1, j), v.out(2, j));
+                    else if (mine_too)
+                        take(j, l, static_cast<IO*>(a.dx) + o, static_cast<IO*>(a.dz) + o,
                              static_cast<IO*>(a.di) + o);
-                    if (mine && marks >> k & 1 && a.dh0)
-                        store_pair(a.dh0 + (int64_t)start_at(w, t + k) * a.D + ch, mul_pair(nr, both(-1.f)));
+                    if (mine_too && marks >> j & 1 && a.dh0)
+                        store_pair(a.dh0 + (int64_t)start_at(w, t + j) * a.D + ch, mul_pair(nr, both(-1.f)));
                 }
-            });
+            }
+            if (whole) {  // the tile's results leave when all warps' are there
+                fence_async_smem();
+                if (warp > 0) {
+                    asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+                } else {
+                    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+                    if (lane == 0) {
+#pragma unroll
+                        for (int o = 0; o < 3; ++o) tma_store(&m.out[o], v.outs + o * S::kOut, c0, t0);
+                        bulk_commit();
+                    }
+                    __syncwarp();
+                }
+            }
+            put(k + kAhead);
+            marked = next_marked;
+            marks = coming;
+            coming = later;
+        }
+        if (threadIdx.x == 0) bulk_wait0();
+        __syncwarp();
+        cluster_arrive();  // (a CTA stays until nobody can send to it)
+        cluster_wait();
     }
     if (part == nullptr) return;
     // the CTA's dA_log: over the warps, in a fixed order
@@ -857,14 +1024,14 @@ bool make_maps(Tensors& m, const RecurrenceArgs& a, bool bwd) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int smem, int ctas,
+cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int threads, int smem, int ctas,
                         const RecurrenceArgs& a, const Plan& w, Args... args) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
         return e;
     ProfScope prof(name, a.stream);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)w.runs * w.cols * ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
@@ -886,7 +1053,7 @@ cudaError_t forward(const RecurrenceArgs& a, const Plan& w) {
     Tensors m{};
     if (!make_maps<In, IO>(m, a, false)) return cudaErrorInvalidValue;
     const int ctas = count_ctas(a.T_total, w.runs, w.cols, kMaxCluster);
-    return launch_scan(scan_kernel<In, IO, kStages, kOnlyEdges>, "recurrence_kernel",
+    return launch_scan(scan_kernel<In, IO, kStages, kOnlyEdges>, "recurrence_kernel", kFwdThreads,
                        kStages * S::kBytes, ctas, a, w, m);
 }
 
@@ -908,7 +1075,7 @@ cudaError_t backward(RecurrenceArgs a) {
         }
         Tensors m{};
         if (!make_maps<In, IO>(m, a, true)) return cudaErrorInvalidValue;
-        if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, kStages>, "recurrence_bwd_kernel",
+        if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, kStages>, "recurrence_bwd_kernel", kThreads,
                                         kStages * S::kBytes + S::kOuts, ctas, a, w, m,
                                         a.dA_log ? part : nullptr))
             return e;
