@@ -5,15 +5,13 @@
 //   l_t = dy_t + a_{t+1} l_{t+1}, backwards, for the gradients
 //
 // Both are scans of affine maps (P, H): h -> P h + H.  A cluster of CTAs takes 64 channels along a
-// run, some consecutive sequences.  In a step each of its CTAs has a tile of 64 tokens: each of eight
-// warps holds 8 tokens, a lane two channels, and leaves its tokens' map in shared memory.  The maps
+// run, some consecutive sequences.  In a step each of its CTAs has a tile of 64 or 128 tokens: each of
+// eight warps holds 8 or 16 tokens, a lane two channels, and leaves its tokens' map in shared memory.  The maps
 // are composed, the tile's map is sent to every CTA of the cluster (stores into distributed shared
 // memory that count their bytes on a barrier there), and the state is carried over the cluster's
 // maps; then every warp goes over its tokens again, in registers, and writes.  So inputs are read
 // once, results written once, in rows of 128 bytes (bf16), and no cluster waits for another.
 // (Narrower columns instead of clusters cost more in the copies of short rows.)
-//   The forward has two warps more, one that composes and sends, one that carries the state, and its
-// eight form the next tile's maps before they write this one's: the exchange takes as long as that.
 //
 // The gradients go over the tiles backwards.  A thread's states come from the edges, the state that
 // every 8th token starts from, which the forward writes on request; without them a forward that
@@ -38,13 +36,11 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTok = 8;     // tokens a thread holds, and from one edge to the next
+constexpr int kEdge = 8;    // tokens from one edge to the next, and of a word of marks
 constexpr int kC = 64;      // channels of a tile, and of an exponent of packed inputs
 constexpr int kWarps = 8;
-constexpr int kT = kTok * kWarps;  // tokens of a tile
 constexpr int kMaxCluster = 8;
-constexpr int kThreads = 32 * kWarps;         // of the gradients' CTAs
-constexpr int kFwdThreads = 32 * (kWarps + 2);  // of the forward's
+constexpr int kThreads = 32 * kWarps;
 
 // What the setup launch leaves for the scan.
 struct Plan {
@@ -56,23 +52,24 @@ struct Plan {
 
 // ---------------------------------------------------------------- inputs --
 
-// The tensors as the copy engine sees them, boxes of 64 tokens x 64 channels: inputs x, z, i, dy and
+// The tensors as the copy engine sees them, boxes of a tile's tokens x 64 channels: inputs x, z, i, dy and
 // outputs y, or dx, dz and di.
 struct Tensors {
     CUtensorMap in[4], out[3];
     int plain;  // inputs by plain copies: rows of codes that begin on 8 bytes only
 };
 
-// A stage of the ring: the inputs of a tile.  A tile's results leave from where its inputs were, or
+// A stage of the ring: the inputs of a tile, kTok tokens a warp.  The gradients' results leave from where its inputs were, or
 // from a place of their own where these have fewer bytes.
-template <typename In, typename IO, bool kBwd>
+template <typename In, typename IO, bool kBwd, int kTok_>
 struct Stage {
+    static constexpr int kTok = kTok_, kT = kTok * kWarps;
     static constexpr int kIn = kT * kC * (int)sizeof(In), kOut = kT * kC * (int)sizeof(IO);
     static constexpr int kDy = 3 * kIn;
     static constexpr int kExps = kDy + (kBwd ? kOut : 0);
     static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT : 0) + 127) / 128 * 128;
     static constexpr bool kInPlace = sizeof(In) == sizeof(IO);
-    static constexpr int kOuts = kInPlace ? 0 : (kBwd ? 3 : 1) * kOut;  // bytes of that place
+    static constexpr int kOuts = kInPlace ? 0 : 3 * kOut;  // bytes of that place
 };
 
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y,
@@ -89,9 +86,9 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* sr
                  : "memory");
 }
 
-// 64 tokens x 64 channels of a tensor by a warp's plain copies; rows and channels past its end become
+// kT tokens x 64 channels of a tensor by a warp's plain copies; rows and channels past its end become
 // zeros.
-template <typename In>
+template <typename In, int kT>
 __device__ __forceinline__ void copy_tile(char* dst, const void* src, int64_t ld, int64_t t0, int c0,
                                           int64_t T, int D, int lane) {
     constexpr int kElems = 8 / (int)sizeof(In);
@@ -112,6 +109,7 @@ __device__ __forceinline__ int fill_count(const Tensors& m) {
     return sizeof(In) == 1 ? 1 + (m.plain ? 32 : 1) : 1;
 }
 // A lane's share of a tile's exponents, on their way.
+template <int kT>
 struct Exps {
     int8_t e[3 * kT / 32];
 };
@@ -119,12 +117,13 @@ struct Exps {
 // Starts the loads of the tile from token t0 and channel c0; called by a warp.
 template <typename S, typename In, typename IO, bool kBwd>
 __device__ __forceinline__ void load_stage(const RecurrenceArgs& a, const Tensors& m, char* st,
-                                           uint64_t* full, int t0, int c0, int lane, Exps& exps) {
+                                           uint64_t* full, int t0, int c0, int lane,
+                                           Exps<S::kT>& exps) {
     if (sizeof(In) == 1 && m.plain) {
-        copy_tile<In>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D, lane);
-        copy_tile<In>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D, lane);
-        copy_tile<In>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D, lane);
-        if (kBwd) copy_tile<IO>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D, lane);
+        copy_tile<In, S::kT>(st, a.x, a.x_ld, t0, c0, a.T_total, a.D, lane);
+        copy_tile<In, S::kT>(st + S::kIn, a.z, a.z_ld, t0, c0, a.T_total, a.D, lane);
+        copy_tile<In, S::kT>(st + 2 * S::kIn, a.i, a.i_ld, t0, c0, a.T_total, a.D, lane);
+        if (kBwd) copy_tile<IO, S::kT>(st + S::kDy, a.dy, a.dy_ld, t0, c0, a.T_total, a.D, lane);
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(full))
                      : "memory");
     } else if (lane == 0) {
@@ -136,19 +135,20 @@ __device__ __forceinline__ void load_stage(const RecurrenceArgs& a, const Tensor
     }
     if (sizeof(In) == 1) {
 #pragma unroll
-        for (int j = 0; j < 3 * kT / 32; ++j) {
-            const int n = j * 32 + lane, t = n % kT;
-            const int8_t* e = n < kT ? a.x_exps : n < 2 * kT ? a.z_exps : a.i_exps;
+        for (int j = 0; j < 3 * S::kT / 32; ++j) {
+            const int n = j * 32 + lane, t = n % S::kT;
+            const int8_t* e = n < S::kT ? a.x_exps : n < 2 * S::kT ? a.z_exps : a.i_exps;
             exps.e[j] = t0 + t < a.T_total ? __ldg(e + (int64_t)(c0 / kC) * a.T_total + t0 + t) : 0;
         }
     }
 }
 // Puts the exponents into the stage that load_stage was called for.
 template <typename S, typename In>
-__device__ __forceinline__ void put_exps(char* st, uint64_t* full, int lane, const Exps& exps) {
+__device__ __forceinline__ void put_exps(char* st, uint64_t* full, int lane,
+                                         const Exps<S::kT>& exps) {
     if (sizeof(In) == 1) {
 #pragma unroll
-        for (int j = 0; j < 3 * kT / 32; ++j)
+        for (int j = 0; j < 3 * S::kT / 32; ++j)
             reinterpret_cast<int8_t*>(st)[S::kExps + j * 32 + lane] = exps.e[j];
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
@@ -168,18 +168,17 @@ __device__ __forceinline__ float2 pair(const float* p) {
 // A thread's view of a stage: token k of its warp, its two channels.
 template <typename S, typename In, typename IO>
 struct View {
-    char* st;
+    char *st, *outs;
     int warp, lane;
-    char* outs = nullptr;
     template <typename E>
     __device__ __forceinline__ const E* at(int part, int k) const {
-        return reinterpret_cast<const E*>(st + part) + (warp * kTok + k) * kC + 2 * lane;
+        return reinterpret_cast<const E*>(st + part) + (warp * S::kTok + k) * kC + 2 * lane;
     }
     __device__ __forceinline__ float2 input(int which, int k) const {
         const In* p = at<In>(which * S::kIn, k);
         if constexpr (sizeof(In) == 1) {
             const char2 q = *reinterpret_cast<const char2*>(p);
-            const int e = reinterpret_cast<const int8_t*>(st)[S::kExps + which * kT + warp * kTok + k];
+            const int e = reinterpret_cast<const int8_t*>(st)[S::kExps + which * S::kT + warp * S::kTok + k];
             // 2^e, denormal at -127; -128 stands for NaN
             const float s =
                 __int_as_float(e > -127 ? (e + 127) << 23 : e == -127 ? 1 << 22 : 0x7fc00000);
@@ -191,7 +190,7 @@ struct View {
     __device__ __forceinline__ float2 dy(int k) const { return pair(at<IO>(S::kDy, k)); }
     // the place of result `which` of token k
     __device__ __forceinline__ IO* out(int which, int k) const {
-        return reinterpret_cast<IO*>(outs + which * S::kOut) + (warp * kTok + k) * kC + 2 * lane;
+        return reinterpret_cast<IO*>(outs + which * S::kOut) + (warp * S::kTok + k) * kC + 2 * lane;
     }
 };
 
@@ -235,25 +234,25 @@ __global__ void __launch_bounds__(256) setup_kernel(const RecurrenceArgs a, cons
         }
         return lo;
     };
-    for (int64_t g = id; g * kTok < a.T_total; g += all) {
-        const int64_t t0 = g * kTok;
+    for (int64_t g = id; g * kEdge < a.T_total; g += all) {
+        const int64_t t0 = g * kEdge;
         uint32_t bits = 0;
-        for (int n = at(t0); n < a.N && (bits == 0 || first(n) < t0 + kTok); ++n) {
+        for (int n = at(t0); n < a.N && (bits == 0 || first(n) < t0 + kEdge); ++n) {
             int64_t b, e;
             seq_range(a.cu_seqlens, n, a.N, a.T_total, nullptr, b, e);
             if (b >= e) {
-                if (first(n) >= t0 + kTok) break;
+                if (first(n) >= t0 + kEdge) break;
                 continue;
             }
-            if (b >= t0 && b < t0 + kTok) {
+            if (b >= t0 && b < t0 + kEdge) {
                 bits |= 1u << (b - t0);
                 w.start_seq[b] = n;
             }
-            if (e > t0 && e <= t0 + kTok) {
+            if (e > t0 && e <= t0 + kEdge) {
                 bits |= 256u << (e - 1 - t0);
                 w.end_seq[e - 1] = n;
             }
-            if (e > t0 + kTok - 1 || b >= t0 + kTok) break;
+            if (e > t0 + kEdge - 1 || b >= t0 + kEdge) break;
         }
         w.marks[g] = bits;
     }
@@ -332,17 +331,28 @@ __device__ __forceinline__ void cluster_wait() {
 
 // The marks of tokens t .. t + 7.
 __device__ __forceinline__ uint32_t marks_of(const Plan& w, int64_t t, int64_t T) {
-    if (w.marks) return t < T ? __ldg(w.marks + t / kTok) : 0u;
-    return (t == 0 ? 1u : 0u) | (T > t && T <= t + kTok ? 256u << (T - 1 - t) : 0u);
+    if (w.marks) return t < T ? __ldg(w.marks + t / kEdge) : 0u;
+    return (t == 0 ? 1u : 0u) | (T > t && T <= t + kEdge ? 256u << (T - 1 - t) : 0u);
+}
+// Of kTok tokens: those that start a sequence, and from bit 16 those that end one.
+template <int kTok>
+__device__ __forceinline__ uint32_t marks_of(const Plan& w, int64_t t, int64_t T) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kTok; j += kEdge) {
+        const uint32_t v = marks_of(w, t + j, T);
+        m |= (v & 0xffu) << j | (v >> 8) << (16 + j);
+    }
+    return m;
 }
 
 // A CTA's tiles in its cluster's run.  Step k's is the `place(k)`-th in the scan's order; there may be
 // none left for this CTA.
-template <bool kBwd>
+template <bool kBwd, int kT>
 struct Steps {
     int begin, end, base, tiles, count, rank, ctas;
     __device__ __forceinline__ Steps(int b, int e)
-        : begin(b), end(e), base(b / kTok * kTok), rank((int)cluster_rank()), ctas((int)cluster_size()) {
+        : begin(b), end(e), base(b / kEdge * kEdge), rank((int)cluster_rank()), ctas((int)cluster_size()) {
         tiles = (end - base + kT - 1) / kT;
         count = (tiles + ctas - 1) / ctas;
     }
@@ -367,6 +377,45 @@ __device__ __forceinline__ float2 carry_over(const float4 (*tiles)[32], int lane
     }
     carry = h;
     return mine;
+}
+
+// What a CTA keeps of a step's maps, in the scan's order.
+template <int kStages>
+struct Maps {
+    float4 warps[kWarps][32];          // its warps'
+    float4 tiles[2][kMaxCluster][32];  // the cluster's tiles'; of two steps in turn
+    uint64_t there[2], full[kStages];  // barriers: those are there
+};
+
+// With the warps' maps there: the map of those before `turn`; the last one sends the tile's map to
+// the CTAs of the cluster.
+template <bool kCut, int kStages, typename Steps>
+__device__ __forceinline__ float4 compose(Maps<kStages>& x, int buf, int turn, int lane,
+                                          const Steps& steps) {
+    float4 before = identity();
+#pragma unroll
+    for (int j = 0; j < kWarps - 1; ++j)
+        if (j < turn) before = after<kCut>(x.warps[j][lane], before);
+    if (turn == kWarps - 1) {
+        const float4 all = after<kCut>(x.warps[turn][lane], before);
+        for (int j = 0; j < steps.ctas; ++j)
+            send(place_in(&x.tiles[buf][steps.rank][lane], j), place_in(&x.there[buf], j), all);
+    }
+    return before;
+}
+
+// Before anything else: the barriers, by all threads; the caller waits for the cluster
+// (cluster_wait) before it sends.
+template <typename In, int kStages>
+__device__ __forceinline__ void open_maps(Maps<kStages>& x, const Tensors& m, uint32_t bytes) {
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kStages; ++k) mbar_init(&x.full[k], fill_count<In>(m));
+        for (int k = 0; k < 2; ++k) mbar_init(&x.there[k], 1);
+        fence_mbar_init();
+        for (int k = 0; k < 2; ++k) mbar_expect_tx(&x.there[k], bytes);
+    }
+    __syncthreads();
+    cluster_arrive();
 }
 
 // The cluster's run and first channel; false where it has nothing to do.
@@ -397,261 +446,135 @@ __device__ __forceinline__ int end_at(const Plan& w, int64_t t) {
 
 // ---------------------------------------------------------------- forward --
 
-// What a CTA keeps of its steps' maps, in the scan's order.  (Another CTA may send its map of three
-// steps on before this one has carried the state over this step's; for the fourth it needs this
-// one's of the second, formed after the states of this one.)
-constexpr int kTurns = 4;
-template <int kStages>
-struct Exchange {
-    float4 warps[2][kWarps][32];            // its warps'; then, of the warps before each
-    float4 tiles[kTurns][kMaxCluster][32];  // the cluster's tiles'
-    float2 mine[2][32];                     // the state that its tile starts from
-    uint64_t maps[2], there[kTurns], states[2], full[kStages];  // barriers: those are there
-};
-
-// The warp that composes a step's maps, sends the tile's, and issues the loads of later tiles.  (Of
-// waits that ran out, here and below: the ones after are not taken, so that everything ends.)
-template <typename S, typename In, typename IO, int kStages>
-__device__ __forceinline__ void send_maps(const RecurrenceArgs& a, const Tensors& m,
-                                          Exchange<kStages>& x, char* ring, const Steps<false>& steps,
-                                          int c0, int lane) {
-    Exps exps;
+template <typename In, typename IO, int kTok, int kStages, bool kOnlyEdges>
+__global__ void __launch_bounds__(kThreads, 2) scan_kernel(
+    const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
+    const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m) {
+    using S = Stage<In, IO, false, kTok>;
+    extern __shared__ __align__(128) char ring[];
+    __shared__ Maps<kStages> x;
+    grid_dependency_wait();
+    int begin, end, c0;
+    if (!find_run(a, w, begin, end, c0)) return;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, ch = c0 + 2 * lane;
+    const bool live = ch < a.D;
+    const Steps<false, S::kT> steps(begin, end);
+    open_maps<In>(x, m, steps.bytes());
+    Exps<S::kT> exps;
     auto load = [&](int k) {
-        if (steps.some(k))
+        if (warp == 0 && steps.some(k))
             load_stage<S, In, IO, false>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
                                          steps.first_token(k), c0, lane, exps);
     };
     auto put = [&](int k) {
-        if (steps.some(k))
+        if (warp == 0 && steps.some(k))
             put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
     };
+    auto marks_at = [&](int k) {
+        return steps.some(k) ? marks_of<kTok>(w, steps.first_token(k) + warp * kTok, a.T_total) : 0u;
+    };
+#pragma unroll
     for (int k = 0; k < kStages; ++k) {
         load(k);
         put(k);
     }
-    // the places of `tiles` and `there` in the cluster's CTAs
-    uint32_t tiles[kMaxCluster], there[kMaxCluster];
-#pragma unroll
-    for (int j = 0; j < kMaxCluster; ++j) {
-        const unsigned to = j < steps.ctas ? j : 0;
-        tiles[j] = place_in(&x.tiles[0][steps.rank][lane], to);
-        there[j] = place_in(&x.there[0], to);
-    }
-    bool broken = false;
-    for (int k = 0; k < steps.count; ++k) {
-        const int buf = k & 1, turn = k % kTurns;
-        if (!broken) broken = !mbar_wait(&x.maps[buf], k / 2 & 1, a.dev_err);
-        float4 own[kWarps], before[kWarps], all;
-#pragma unroll
-        for (int j = 0; j < kWarps; ++j) own[j] = x.warps[buf][j][lane];
-        all = own[0];
-        before[0] = identity();
-#pragma unroll
-        for (int j = 1; j < kWarps; ++j) {
-            before[j] = all;
-            all = after<true>(own[j], all);
-        }
-#pragma unroll
-        for (int j = 0; j < kMaxCluster; ++j)
-            if (j < steps.ctas)
-                send(tiles[j] + turn * (uint32_t)sizeof x.tiles[0], there[j] + turn * 8u, all);
-#pragma unroll
-        for (int j = 0; j < kWarps; ++j) x.warps[buf][j][lane] = before[j];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x.states[buf]);
-        if (!broken) {
-            load(k + kStages);
-            put(k + kStages);
-        }
-    }
-}
-
-// The warp that carries the state over the cluster's tiles.
-template <int kStages>
-__device__ __forceinline__ void carry_states(const RecurrenceArgs& a, Exchange<kStages>& x,
-                                             const Steps<false>& steps, int lane) {
-    float2 carry = both(0.f);
-    bool broken = false;
-    for (int k = 0; k < steps.count; ++k) {
-        const int turn = k % kTurns;
-        if (!broken) broken = !mbar_wait(&x.there[turn], k / kTurns & 1, a.dev_err);
-        if (lane == 0) mbar_expect_tx(&x.there[turn], steps.bytes());
-        x.mine[k & 1][lane] = carry_over(x.tiles[turn], lane, steps.rank, steps.ctas, carry);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x.states[k & 1]);
-    }
-}
-
-template <typename In, typename IO, int kStages, bool kOnlyEdges>
-__global__ void __launch_bounds__(kFwdThreads, 2) scan_kernel(
-    const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
-    const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m) {
-    using S = Stage<In, IO, false>;
-    extern __shared__ __align__(128) char ring[];
-    __shared__ Exchange<kStages> x;
-    grid_dependency_wait();
-    int begin, end, c0;
-    if (!find_run(a, w, begin, end, c0)) return;
-    const Steps<false> steps(begin, end);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (threadIdx.x == 0) {
-        for (int k = 0; k < kStages; ++k) mbar_init(&x.full[k], fill_count<In>(m));
-        for (int k = 0; k < 2; ++k) {
-            mbar_init(&x.maps[k], kWarps);
-            mbar_init(&x.states[k], 2);
-        }
-        for (int k = 0; k < kTurns; ++k) mbar_init(&x.there[k], 1);
-        fence_mbar_init();
-        for (int k = 0; k < kTurns; ++k) mbar_expect_tx(&x.there[k], steps.bytes());
-    }
-    __syncthreads();
-    cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
-    cluster_wait();
-    if (warp >= kWarps) {
-        if (warp == kWarps) send_maps<S, In, IO, kStages>(a, m, x, ring, steps, c0, lane);
-        else carry_states(a, x, steps, lane);
-        __syncwarp();
-        cluster_arrive();  // (a CTA stays until nobody can send to it)
-        cluster_wait();
-        return;
-    }
-    const int ch = c0 + 2 * lane;
-    const bool live = ch < a.D;
     const float2 nl =
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
-    bool broken = false;
-    struct Held {  // tokens of a step: c, -b
-        float2 c[kTok], nb[kTok];
-        uint32_t marks;
-    };
-    uint32_t coming = marks_of(w, steps.first_token(0) + warp * kTok, a.T_total);
-    // Step k's tokens and their map.
-    auto first = [&](int k, Held& o) {
+    float2 carry = both(0.f);
+    uint32_t marks = marks_at(0), coming = marks_at(1);
+    bool marked = __syncthreads_or(marks != 0u), broken = false;
+    cluster_wait();
+    for (int k = 0; k < steps.count; ++k) {
         const int buf = k & 1, s = k % kStages;
+        const View<S, In, IO> v{ring + s * S::kBytes, nullptr, warp, lane};
         const int64_t t = steps.first_token(k) + warp * kTok;
-        o.marks = coming;
-        coming = marks_of(w, steps.first_token(k + 1) + warp * kTok, a.T_total);
+        const bool some = steps.some(k);
+        float2 c[kTok], nb[kTok], opening[kTok / kEdge] = {};
         float2 P = both(1.f), H = both(0.f);
-        if (steps.some(k)) {
+        if (some) {
             if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
-            const View<S, In, IO> v{ring + s * S::kBytes, warp, lane};
-            recurrence_steps([&](int which, int j) { return v.input(which, j); }, nl, gb, o.c, o.nb);
-            if ((o.marks & 0xffu) == 0u) {
+            recurrence_steps([&](int which, int j) { return v.input(which, j); }, nl, gb, c, nb);
+            if ((marks & 0xffffu) == 0u) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
-                    P = fma_pair(o.c[j], P, P);
-                    H = recurrence_next(o.c[j], o.nb[j], H);
+                    P = fma_pair(c[j], P, P);
+                    H = recurrence_next(c[j], nb[j], H);
                 }
             } else {
-                // initial states: into the first tokens' input terms
-                float2 opening = both(0.f);
-                if (a.h0) {
-#pragma unroll
-                    for (int j = 0; j < kTok; j += 2) {
-                        float2 h0[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            h0[i] = o.marks >> (j + i) & 1 && live
-                                        ? state_row(a.h0, start_at(w, t + j + i), a.D, ch)
-                                        : both(0.f);
-                        if (j == 0) opening = h0[0];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            if (o.marks >> (j + i) & 1)
-                                o.nb[j + i] =
-                                    mul_pair(recurrence_next(o.c[j + i], o.nb[j + i], h0[i]), both(-1.f));
-                    }
-                }
-                if (o.marks & 1 && a.edges && live && t >= begin && t < end)
-                    store_pair(a.edges + t / kTok * a.D + ch, opening);
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
-                    if (o.marks >> j & 1) H = both(0.f);
-                    H = recurrence_next(o.c[j], o.nb[j], H);
+                    if (marks >> j & 1) {  // the initial state: into the first token's input term
+                        H = both(0.f);
+                        if (a.h0 && live) {
+                            const float2 h0 = state_row(a.h0, start_at(w, t + j), a.D, ch);
+                            if (j % kEdge == 0) opening[j / kEdge] = h0;
+                            nb[j] = mul_pair(recurrence_next(c[j], nb[j], h0), both(-1.f));
+                        }
+                    }
+                    H = recurrence_next(c[j], nb[j], H);
                 }
                 P = both(-0.f);
             }
         }
-        x.warps[buf][warp][lane] = make_float4(P.x, P.y, H.x, H.y);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x.maps[buf]);
-    };
-    // Step k's results, from the state that its tokens start from.
-    auto second = [&](int k, const Held& o) {
-        const int buf = k & 1;
-        const int64_t t = steps.first_token(k) + warp * kTok;
-        if (!broken) broken = !mbar_wait(&x.states[buf], k / 2 & 1, a.dev_err);
-        float2 h = apply<true>(x.warps[buf][warp][lane], x.mine[buf][lane]);
-        if (!steps.some(k) || !live || t + kTok <= begin || t >= end) return;
-        if (a.edges && t >= begin && !(o.marks & 1)) store_pair(a.edges + t / kTok * a.D + ch, h);
-        IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
-        if (o.marks == 0u) {
-            if (kOnlyEdges) return;
+        x.warps[warp][lane] = make_float4(P.x, P.y, H.x, H.y);
+        const bool next_marked = __syncthreads_or(coming != 0u);
+        const float4 before = marked ? compose<true>(x, buf, warp, lane, steps)
+                                     : compose<false>(x, buf, warp, lane, steps);
+        load(k + kStages);  // (the stage has been read)
+        const uint32_t later = marks_at(k + 2);
+        // (the next maps for this buffer are sent when this CTA's of the next step are there, which
+        // its barrier of that step precedes)
+        if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, a.dev_err);
+        if (threadIdx.x == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
+        const float2 mine = carry_over(x.tiles[buf], lane, steps.rank, steps.ctas, carry);
+        float2 h = marked ? apply<true>(before, mine) : apply<false>(before, mine);
+        if (some && live) {
+            IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
+            float* edge = a.edges + t / kEdge * a.D + ch;
+            if (marks == 0u && t >= begin && t + kTok <= end) {
 #pragma unroll
-            for (int j = 0; j < kTok; ++j) {
-                h = recurrence_next(o.c[j], o.nb[j], h);
-                store_pair(y, h);
-                y += a.D;
-            }
-            return;
-        }
-        if (kOnlyEdges) return;
+                for (int j = 0; j < kTok; ++j) {
+                    if (j % kEdge == 0 && a.edges) store_pair(edge + j / kEdge * (int64_t)a.D, h);
+                    h = recurrence_next(c[j], nb[j], h);
+                    if (!kOnlyEdges) store_pair(y, h);
+                    y += a.D;
+                }
+            } else {
 #pragma unroll
-        for (int j = 0; j < kTok; ++j) {
-            if (o.marks >> j & 1) h = both(0.f);
-            h = recurrence_next(o.c[j], o.nb[j], h);
-            if (t + j >= begin && t + j < end) {
-                store_pair(y, h);
-                if (o.marks >> (8 + j) & 1 && a.h_out)
-                    store_pair(a.h_out + (int64_t)end_at(w, t + j) * a.D + ch, h);
+                for (int j = 0; j < kTok; ++j) {
+                    const bool in = t + j >= begin && t + j < end;
+                    if (j % kEdge == 0 && a.edges && in)
+                        store_pair(edge + j / kEdge * (int64_t)a.D,
+                                   marks >> j & 1 ? opening[j / kEdge] : h);
+                    if (marks >> j & 1) h = both(0.f);
+                    h = recurrence_next(c[j], nb[j], h);
+                    if (!kOnlyEdges && in) {
+                        store_pair(y, h);
+                        if (marks >> (16 + j) & 1 && a.h_out)
+                            store_pair(a.h_out + (int64_t)end_at(w, t + j) * a.D + ch, h);
+                    }
+                    y += a.D;
+                }
             }
-            y += a.D;
         }
-    };
-    Held even, odd;
-    for (int k = 0; k <= steps.count; k += 2) {
-        if (k < steps.count) first(k, even);
-        if (k >= 1) second(k - 1, odd);
-        if (k + 1 < steps.count) first(k + 1, odd);
-        if (k < steps.count) second(k, even);
+        put(k + kStages);
+        marked = next_marked;
+        marks = coming;
+        coming = later;
     }
     __syncwarp();
-    cluster_arrive();
+    cluster_arrive();  // (a CTA stays until nobody can send to it)
     cluster_wait();
 }
 
 // -------------------------------------------------------------- gradients --
 
-// What a CTA keeps of a step's maps, in the scan's order.
-template <int kStages>
-struct Maps {
-    float4 warps[kWarps][32];          // its warps'
-    float4 tiles[2][kMaxCluster][32];  // the cluster's tiles'; of two steps in turn
-    uint64_t there[2], full[kStages];  // barriers: those are there
-};
-
-// With the warps' maps there: the map of those before `turn`; the last one sends the tile's map to
-// the CTAs of the cluster.
-template <bool kCut, int kStages>
-__device__ __forceinline__ float4 compose(Maps<kStages>& x, int buf, int turn, int lane,
-                                          const Steps<true>& steps) {
-    float4 before = identity();
-#pragma unroll
-    for (int j = 0; j < kWarps - 1; ++j)
-        if (j < turn) before = after<kCut>(x.warps[j][lane], before);
-    if (turn == kWarps - 1) {
-        const float4 all = after<kCut>(x.warps[turn][lane], before);
-        for (int j = 0; j < steps.ctas; ++j)
-            send(place_in(&x.tiles[buf][steps.rank][lane], j), place_in(&x.there[buf], j), all);
-    }
-    return before;
-}
-
 template <typename In, typename IO, int kStages>
 __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
     const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m, float* part) {
-    using S = Stage<In, IO, true>;
+    constexpr int kTok = kEdge;  // (a warp's states come from its edge)
+    using S = Stage<In, IO, true, kTok>;
     constexpr int kAhead = kStages - 1;  // steps from the one at hand to the one loaded
     extern __shared__ __align__(128) char ring[];
     __shared__ Maps<kStages> x;
@@ -663,16 +586,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     const bool live = ch < a.D;
     float2 dA = both(0.f);
     if (any) {
-        const Steps<true> steps(begin, end);
-        if (threadIdx.x == 0) {
-            for (int k = 0; k < kStages; ++k) mbar_init(&x.full[k], fill_count<In>(m));
-            for (int k = 0; k < 2; ++k) mbar_init(&x.there[k], 1);
-            fence_mbar_init();
-            for (int k = 0; k < 2; ++k) mbar_expect_tx(&x.there[k], steps.bytes());
-        }
-        __syncthreads();
-        cluster_arrive();  // (the cluster's CTAs are there before any writes into another)
-        Exps exps;
+        const Steps<true, S::kT> steps(begin, end);
+        open_maps<In>(x, m, steps.bytes());
+        Exps<S::kT> exps;
         auto load = [&](int k) {
             if (warp == 0 && steps.some(k))
                 load_stage<S, In, IO, true>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
@@ -684,12 +600,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
         };
         // a step's marks, and the state that the warp's tokens start from
         auto marks_at = [&](int k) {
-            return steps.some(k) ? marks_of(w, steps.first_token(k) + warp * kTok, a.T_total) : 0u;
+            return steps.some(k) ? marks_of<kTok>(w, steps.first_token(k) + warp * kTok, a.T_total) : 0u;
         };
         auto edge_at = [&](int k) {
             const int64_t t = steps.first_token(k) + warp * kTok;
             return steps.some(k) && t < a.T_total && live
-                       ? __ldg(reinterpret_cast<const float2*>(a.edges + t / kTok * a.D + ch))
+                       ? __ldg(reinterpret_cast<const float2*>(a.edges + t / kEdge * a.D + ch))
                        : both(0.f);
         };
 #pragma unroll
@@ -706,10 +622,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
         for (int k = 0; k < steps.count; ++k) {
             const int buf = k & 1, s = k % kStages;
             char* const st = ring + s * S::kBytes;
-            const View<S, In, IO> v{st, warp, lane, S::kInPlace ? st : ring + kStages * S::kBytes};
+            const View<S, In, IO> v{st, S::kInPlace ? st : ring + kStages * S::kBytes, warp, lane};
             const int t0 = steps.first_token(k);
             const int64_t t = t0 + warp * kTok;
-            const bool some = steps.some(k), whole = some && t0 >= begin && t0 + kT <= end;
+            const bool some = steps.some(k), whole = some && t0 >= begin && t0 + S::kT <= end;
             // the negated factors of l in the gradients, from the states; the scan's state is -r, what
             // -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
             float2 c[kTok], fx[kTok], fz[kTok], fi[kTok];
@@ -724,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                         return h;
                     },
                     c, fx, fz, fi);
-                if ((marks & 0xff00u) == 0u) {
+                if (marks >> 16 == 0u) {
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
                         P = fma_pair(c[j], P, P);
@@ -734,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                 } else {
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
-                        if (marks >> (8 + j) & 1)
+                        if (marks >> (16 + j) & 1)
                             H = a.dh_out && live
                                     ? mul_pair(state_row(a.dh_out, end_at(w, t + j), a.D, ch), both(-1.f))
                                     : both(0.f);
@@ -779,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                 const int64_t at = t * a.D + ch;
 #pragma unroll
                 for (int j = kTok - 1; j >= 0; --j) {
-                    if (marks >> (8 + j) & 1)
+                    if (marks >> (16 + j) & 1)
                         nr = a.dh_out && live
                                  ? mul_pair(state_row(a.dh_out, end_at(w, t + j), a.D, ch), both(-1.f))
                                  : both(0.f);
@@ -930,9 +846,9 @@ int count_runs(int64_t T, int N, int cols) {
 
 // CTAs of a cluster: as many as keep all of them on the GPU at once, two an SM; with several runs,
 // that a run has 8 steps on average.
-int count_ctas(int64_t T, int runs, int cols, int most) {
+int count_ctas(int64_t T, int runs, int cols, int kT) {
     int n = 1;
-    while (2 * n <= most && T / runs > kT * n &&
+    while (2 * n <= kMaxCluster && T / runs > kT * n &&
            ((int64_t)runs * cols * 2 * n <= 304 || (runs > 1 && T / runs >= (int64_t)kT * 2 * n * 8)))
         n *= 2;
     return n;
@@ -951,13 +867,13 @@ size_t lay_out(char* ws, int64_t T, int N, int D, bool bwd, Plan* w, float** edg
     s.runs = count_runs(T, N, s.cols);
     if (N != 1) {
         s.run = reinterpret_cast<int*>(take((s.runs + 1) * 4));
-        s.marks = reinterpret_cast<uint32_t*>(take((T + kTok - 1) / kTok * 4));
+        s.marks = reinterpret_cast<uint32_t*>(take((T + kEdge - 1) / kEdge * 4));
         s.start_seq = reinterpret_cast<int*>(take(T * 4));
         s.end_seq = reinterpret_cast<int*>(take(T * 4));
     }
     if (bwd) {
         char* p = take((size_t)s.runs * kMaxCluster * D * 4);
-        char* e = take((size_t)((T + kTok - 1) / kTok) * D * 4);
+        char* e = take((size_t)((T + kEdge - 1) / kEdge) * D * 4);
         if (part) *part = reinterpret_cast<float*>(p);
         if (edges) *edges = reinterpret_cast<float*>(e);
     }
@@ -967,7 +883,7 @@ size_t lay_out(char* ws, int64_t T, int N, int D, bool bwd, Plan* w, float** edg
 
 cudaError_t setup(const RecurrenceArgs& a, const Plan& w, const float* from, float* to) {
     if (w.run == nullptr) return cudaSuccess;
-    const int64_t want = std::max<int64_t>(a.T_total / kTok, (int64_t)a.N * 32);
+    const int64_t want = std::max<int64_t>(a.T_total / kEdge, (int64_t)a.N * 32);
     const int grid = (int)std::min<int64_t>(want / 256 + 1, 152 * 8);
     ProfScope prof("recurrence_setup_kernel", a.stream);
     setup_kernel<<<grid, 256, 0, a.stream>>>(a, w, from, to);
@@ -994,12 +910,12 @@ EncodeFn encode_fn() {
 
 // [T][D] of E with a token stride of ld elements.
 template <typename E>
-bool make_map(CUtensorMap* m, const void* base, int64_t T, int D, int64_t ld) {
+bool make_map(CUtensorMap* m, const void* base, int64_t T, int D, int64_t ld, int kT) {
     EncodeFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)T};
     const cuuint64_t stride = (cuuint64_t)ld * sizeof(E);
-    const cuuint32_t box[2] = {kC, kT}, estr[2] = {1, 1};
+    const cuuint32_t box[2] = {kC, (cuuint32_t)kT}, estr[2] = {1, 1};
     return fn(m,
               sizeof(E) == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
               : sizeof(E) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -1009,29 +925,33 @@ bool make_map(CUtensorMap* m, const void* base, int64_t T, int D, int64_t ld) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename In, typename IO>
+template <typename S, typename In, typename IO>
 bool make_maps(Tensors& m, const RecurrenceArgs& a, bool bwd) {
     const int64_t T = a.T_total;
+    auto of = [&](auto* type, int which, const void* base, int64_t ld, bool out) {
+        using E = std::remove_pointer_t<decltype(type)>;
+        return make_map<E>(out ? &m.out[which] : &m.in[which], base, T, a.D, ld, S::kT);
+    };
+    In* in = nullptr;
+    IO* io = nullptr;
     m.plain = sizeof(In) == 1 && a.D % 16 != 0;
-    if (!m.plain && (!make_map<In>(&m.in[0], a.x, T, a.D, a.x_ld) ||
-                     !make_map<In>(&m.in[1], a.z, T, a.D, a.z_ld) ||
-                     !make_map<In>(&m.in[2], a.i, T, a.D, a.i_ld)))
+    if (!m.plain && !(of(in, 0, a.x, a.x_ld, false) && of(in, 1, a.z, a.z_ld, false) &&
+                      of(in, 2, a.i, a.i_ld, false)))
         return false;
     if (!bwd) return true;
-    return (m.plain || make_map<IO>(&m.in[3], a.dy, T, a.D, a.dy_ld)) &&
-           make_map<IO>(&m.out[0], a.dx, T, a.D, a.D) && make_map<IO>(&m.out[1], a.dz, T, a.D, a.D) &&
-           make_map<IO>(&m.out[2], a.di, T, a.D, a.D);
+    return (m.plain || of(io, 3, a.dy, a.dy_ld, false)) && of(io, 0, a.dx, a.D, true) &&
+           of(io, 1, a.dz, a.D, true) && of(io, 2, a.di, a.D, true);
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int threads, int smem, int ctas,
+cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int smem, int ctas,
                         const RecurrenceArgs& a, const Plan& w, Args... args) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
         return e;
     ProfScope prof(name, a.stream);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)w.runs * w.cols * ctas);
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
@@ -1045,26 +965,32 @@ cudaError_t launch_scan(void (*kernel)(KArgs...), const char* name, int threads,
     return cudaLaunchKernelEx(&cfg, kernel, a, w, gate_bound(a.g_min), args...);
 }
 
-constexpr int kStages = 3;
+// A warp's tokens in the forward: 16 of them halve what the steps cost beside the tokens' arithmetic;
+// 8 of fp32, whose tiles would leave one CTA an SM.  (Of the gradients' type where only edges are
+// wanted, so that these are the same for packed inputs and the values they stand for.)
+template <typename IO>
+constexpr int kForwardTok = sizeof(IO) == 4 ? 8 : 16;
 
 template <typename In, typename IO, bool kOnlyEdges>
 cudaError_t forward(const RecurrenceArgs& a, const Plan& w) {
-    using S = Stage<In, IO, false>;
+    constexpr int kTok = kForwardTok<IO>, kStages = 2;
+    using S = Stage<In, IO, false, kTok>;
     Tensors m{};
-    if (!make_maps<In, IO>(m, a, false)) return cudaErrorInvalidValue;
-    const int ctas = count_ctas(a.T_total, w.runs, w.cols, kMaxCluster);
-    return launch_scan(scan_kernel<In, IO, kStages, kOnlyEdges>, "recurrence_kernel", kFwdThreads,
+    if (!make_maps<S, In, IO>(m, a, false)) return cudaErrorInvalidValue;
+    const int ctas = count_ctas(a.T_total, w.runs, w.cols, S::kT);
+    return launch_scan(scan_kernel<In, IO, kTok, kStages, kOnlyEdges>, "recurrence_kernel",
                        kStages * S::kBytes, ctas, a, w, m);
 }
 
 template <typename In, typename IO>
 cudaError_t backward(RecurrenceArgs a) {
-    using S = Stage<In, IO, true>;
+    constexpr int kStages = 3;
+    using S = Stage<In, IO, true, kEdge>;
     Plan w;
     float *edges, *part;
     lay_out(static_cast<char*>(a.workspace), a.T_total, a.N, a.D, true, &w, &edges, &part);
     if (cudaError_t e = setup(a, w, a.dh_out, a.dh0)) return e;
-    const int ctas = count_ctas(a.T_total, w.runs, w.cols, kMaxCluster);
+    const int ctas = count_ctas(a.T_total, w.runs, w.cols, S::kT);
     if (a.T_total > 0) {
         if (a.edges == nullptr) {
             RecurrenceArgs f = a;
@@ -1074,8 +1000,8 @@ cudaError_t backward(RecurrenceArgs a) {
             if (cudaError_t e = forward<In, IO, true>(f, w)) return e;
         }
         Tensors m{};
-        if (!make_maps<In, IO>(m, a, true)) return cudaErrorInvalidValue;
-        if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, kStages>, "recurrence_bwd_kernel", kThreads,
+        if (!make_maps<S, In, IO>(m, a, true)) return cudaErrorInvalidValue;
+        if (cudaError_t e = launch_scan(scan_bwd_kernel<In, IO, kStages>, "recurrence_bwd_kernel",
                                         kStages * S::kBytes + S::kOuts, ctas, a, w, m,
                                         a.dA_log ? part : nullptr))
             return e;
