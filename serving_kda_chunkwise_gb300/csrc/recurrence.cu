@@ -67,7 +67,7 @@ struct Stage {
     static constexpr int kIn = kT * kC * (int)sizeof(In), kOut = kT * kC * (int)sizeof(IO);
     static constexpr int kDy = 3 * kIn;
     static constexpr int kExps = kDy + (kBwd ? kOut : 0);
-    static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT : 0) + 127) / 128 * 128;
+    static constexpr int kBytes = (kExps + (sizeof(In) == 1 ? 3 * kT * 4 : 0) + 127) / 128 * 128;
     static constexpr bool kInPlace = sizeof(In) == sizeof(IO);
     static constexpr int kOuts = kInPlace ? 0 : 3 * kOut;  // bytes of that place
 };
@@ -142,24 +142,28 @@ __device__ __forceinline__ void load_stage(const RecurrenceArgs& a, const Tensor
         }
     }
 }
-// Puts the exponents into the stage that load_stage was called for.
+// Puts the powers of two into the stage that load_stage was called for.
 template <typename S, typename In>
 __device__ __forceinline__ void put_exps(char* st, uint64_t* full, int lane,
                                          const Exps<S::kT>& exps) {
     if (sizeof(In) == 1) {
 #pragma unroll
         for (int j = 0; j < 3 * S::kT / 32; ++j)
-            reinterpret_cast<int8_t*>(st)[S::kExps + j * 32 + lane] = exps.e[j];
+            // 2^e, denormal at -127; -128 stands for NaN
+            reinterpret_cast<float*>(st + S::kExps)[j * 32 + lane] = __int_as_float(
+                exps.e[j] > -127 ? (exps.e[j] + 127) << 23 : exps.e[j] == -127 ? 1 << 22 : 0x7fc00000);
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
     }
 }
 
-__device__ __forceinline__ float2 pair(const __nv_bfloat16* p) {
-    // (read as what it is: results are written to the same places)
-    const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(p);
+__device__ __forceinline__ float2 bits(__nv_bfloat162 v) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(&v);
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair(const __nv_bfloat16* p) {
+    // (read as what it is: results are written to the same places)
+    return bits(*reinterpret_cast<const __nv_bfloat162*>(p));
 }
 __device__ __forceinline__ float2 pair(const float* p) {
     return *reinterpret_cast<const float2*>(p);
@@ -177,14 +181,32 @@ struct View {
     __device__ __forceinline__ float2 input(int which, int k) const {
         const In* p = at<In>(which * S::kIn, k);
         if constexpr (sizeof(In) == 1) {
-            const char2 q = *reinterpret_cast<const char2*>(p);
-            const int e = reinterpret_cast<const int8_t*>(st)[S::kExps + which * S::kT + warp * S::kTok + k];
-            // 2^e, denormal at -127; -128 stands for NaN
             const float s =
-                __int_as_float(e > -127 ? (e + 127) << 23 : e == -127 ? 1 << 22 : 0x7fc00000);
-            return make_float2((float)(signed char)q.x * s, (float)(signed char)q.y * s);
+                reinterpret_cast<const float*>(st + S::kExps)[which * S::kT + warp * S::kTok + k];
+            // a byte with its sign flipped, code + 128, as the last of a number of 2^23 and more
+            const uint32_t q = *reinterpret_cast<const uint16_t*>(p) ^ 0x8080u;
+            return mul_pair(add_pair(make_float2(__uint_as_float(__byte_perm(q, 0x4b000000u, 0x7440)),
+                                                 __uint_as_float(__byte_perm(q, 0x4b000000u, 0x7441))),
+                                     both(-8388736.f)),
+                            both(s));
         } else {
             return pair(p);
+        }
+    }
+    // The same, infinities as the largest numbers (beside a gradient of zero: its share is zero).
+    __device__ __forceinline__ float2 finite(int which, int k) const {
+        if constexpr (sizeof(In) == 1) {
+            return input(which, k);
+        } else if constexpr (sizeof(In) == 2) {
+            const __nv_bfloat162 top = __floats2bfloat162_rn(3.3e38f, 3.3e38f);
+            const __nv_bfloat162 v =
+                __hmin2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(at<In>(which * S::kIn, k)),
+                                __hneg2(top)),
+                        top);
+            return bits(v);
+        } else {
+            const float2 v = input(which, k);
+            return make_float2(fminf(fmaxf(v.x, -3e38f), 3e38f), fminf(fmaxf(v.y, -3e38f), 3e38f));
         }
     }
     __device__ __forceinline__ float2 dy(int k) const { return pair(at<IO>(S::kDy, k)); }
@@ -489,6 +511,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         const View<S, In, IO> v{ring + s * S::kBytes, nullptr, warp, lane};
         const int64_t t = steps.first_token(k) + warp * kTok;
         const bool some = steps.some(k);
+        // of every token: the decay from before the warp's tokens to after it, and the state after it
+        // if that before them were zero
         float2 c[kTok], nb[kTok], opening[kTok / kEdge] = {};
         float2 P = both(1.f), H = both(0.f);
         if (some) {
@@ -499,21 +523,23 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                 for (int j = 0; j < kTok; ++j) {
                     P = fma_pair(c[j], P, P);
                     H = recurrence_next(c[j], nb[j], H);
+                    c[j] = P;
+                    nb[j] = H;
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
-                    if (marks >> j & 1) {  // the initial state: into the first token's input term
+                    if (marks >> j & 1) {
+                        P = both(-0.f);  // (constant from here on)
                         H = both(0.f);
-                        if (a.h0 && live) {
-                            const float2 h0 = state_row(a.h0, start_at(w, t + j), a.D, ch);
-                            if (j % kEdge == 0) opening[j / kEdge] = h0;
-                            nb[j] = mul_pair(recurrence_next(c[j], nb[j], h0), both(-1.f));
-                        }
+                        if (a.h0 && live) H = state_row(a.h0, start_at(w, t + j), a.D, ch);
+                        if (j % kEdge == 0) opening[j / kEdge] = H;
                     }
+                    if (!constant(P.x)) P = fma_pair(c[j], P, P);
                     H = recurrence_next(c[j], nb[j], H);
+                    c[j] = P;
+                    nb[j] = H;
                 }
-                P = both(-0.f);
             }
         }
         x.warps[warp][lane] = make_float4(P.x, P.y, H.x, H.y);
@@ -534,24 +560,25 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
             if (marks == 0u && t >= begin && t + kTok <= end) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
-                    if (j % kEdge == 0 && a.edges) store_pair(edge + j / kEdge * (int64_t)a.D, h);
-                    h = recurrence_next(c[j], nb[j], h);
-                    if (!kOnlyEdges) store_pair(y, h);
+                    if (j % kEdge == 0 && a.edges)
+                        store_pair(edge + j / kEdge * (int64_t)a.D,
+                                   j == 0 ? h : fma_pair(c[j - 1], h, nb[j - 1]));
+                    if (!kOnlyEdges) store_pair(y, fma_pair(c[j], h, nb[j]));
                     y += a.D;
                 }
             } else {
+                float2 last = h;
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
                     const bool in = t + j >= begin && t + j < end;
                     if (j % kEdge == 0 && a.edges && in)
                         store_pair(edge + j / kEdge * (int64_t)a.D,
-                                   marks >> j & 1 ? opening[j / kEdge] : h);
-                    if (marks >> j & 1) h = both(0.f);
-                    h = recurrence_next(c[j], nb[j], h);
+                                   marks >> j & 1 ? opening[j / kEdge] : last);
+                    last = constant(c[j].x) ? nb[j] : fma_pair(c[j], h, nb[j]);
                     if (!kOnlyEdges && in) {
-                        store_pair(y, h);
+                        store_pair(y, last);
                         if (marks >> (16 + j) & 1 && a.h_out)
-                            store_pair(a.h_out + (int64_t)end_at(w, t + j) * a.D + ch, h);
+                            store_pair(a.h_out + (int64_t)end_at(w, t + j) * a.D + ch, last);
                     }
                     y += a.D;
                 }
@@ -632,14 +659,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             float2 P = both(1.f), H = both(0.f);
             if (some) {
                 if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
-                recurrence_grads(
-                    [&](int which, int j) { return v.input(which, j); }, r, gb, edge,
-                    [&](int j, float2 h) {
-                        if (marks >> j & 1)
-                            h = a.h0 && live ? state_row(a.h0, start_at(w, t + j), a.D, ch) : both(0.f);
-                        return h;
-                    },
-                    c, fx, fz, fi);
+                auto in = [&](int which, int j) { return v.input(which, j); };
+                if ((marks & 0xffffu) == 0u)
+                    recurrence_grads(in, r, gb, edge, [](int, float2 h) { return h; }, c, fx, fz, fi);
+                else
+                    recurrence_grads(
+                        in, r, gb, edge,
+                        [&](int j, float2 h) {
+                            if (marks >> j & 1)
+                                h = a.h0 && live ? state_row(a.h0, start_at(w, t + j), a.D, ch)
+                                                 : both(0.f);
+                            return h;
+                        },
+                        c, fx, fz, fi);
                 if (marks >> 16 == 0u) {
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
@@ -676,13 +708,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             float2 nr = marked ? apply<true>(before, mine) : apply<false>(before, mine);
             // a token's gradients but for the state's
             auto take = [&](int j, float2 l, IO* dx, IO* dz, IO* di) {
-                const float2 g = mul_pair(l, fz[j]), z = v.input(1, j);
+                const float2 g = mul_pair(l, fz[j]), z = v.finite(1, j);
                 store_pair(dx, mul_pair(l, fx[j]));
                 store_pair(dz, g);
                 store_pair(di, mul_pair(l, fi[j]));
-                // (an infinite z has a gradient of zero)
-                dA.x += g.x == 0.f ? 0.f : g.x * z.x;
-                dA.y += g.y == 0.f ? 0.f : g.y * z.y;
+                dA = fma_pair(g, z, dA);
             };
             if (whole && marks == 0u) {
 #pragma unroll
