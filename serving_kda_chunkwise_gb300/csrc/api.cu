@@ -982,6 +982,8 @@ kda_status_t kda_block_norm_bwd(const void* y, const void* gate, const void* r_o
         if (kda_status_t s =
                 check_workspace(workspace, ws_bytes, kda::block_norm_bwd_workspace_size(D)))
             return s;
+    a.dev_err = device_error_ptr();
+    if (a.dev_err == nullptr) return fail(KDA_ERR_CUDA, "no CUDA device is usable");
     cudaError_t e = kda::launch_block_norm_bwd(a);
     if (e != cudaSuccess) return cuda_fail(e, "kda_block_norm_bwd launch");
     return KDA_OK;

@@ -6,25 +6,28 @@
 //   dn = f G,  dy = (w_post dn - y^ mean(w_post dn y^)) / rms(y),  dgate = G f n (1 - s(gate))
 //   dscale = sum G s(gate) n,  dw_post = sum dn y^,  dw_pre = sum dx r^
 //
-// Streaming work: every tensor is read once and written once.  A CTA holds a row at a time in
-// registers, 8 channels a thread (16 bytes of bf16), and goes over its rows with the next one on its
-// way; weights, and the sums for their gradients, stay in registers.  The forward's two means are
-// two sums over the CTA one after the other (r' is what the second is of).  The gradients' are taken
-// together: with q = f w_post y,
+// Streaming work: every tensor is read once and written once.  A CTA holds a row at a time, 8 channels
+// a thread (16 bytes of bf16), weights and the sums for their gradients in registers.
+//   The forward keeps the row in registers, the next one on its way.  Its two means are two sums over
+// the CTA one after the other (r' is what the second is of).
+//   The gradients read five tensors twice over (before and after the sums): bulk copies bring the next
+// rows into shared memory, as many as fit.  Their means are taken together: with q = f w_post y,
 //   mean(w_post dn y^) rms(y) D = sum G q = sum dr q + (sum u q - mean(u r^) sum r^ q) / rms(r'),
 // u = w_pre dx, so that six sums of one pass give all, and a row costs one barrier.
 // All sums are fp32; the only rounding to fewer bits is that of the results.
 #include "kda_common.cuh"
 #include "kda_internal.h"
+#include "tc_util.cuh"
 
 namespace kda {
 namespace {
 
+using namespace tc;
+
 constexpr int kV = 8;          // channels a thread
 constexpr int kMaxWarps = 32;  // of a CTA: kMaxBlockNormD / kV threads
-constexpr int kMaxBlocks = 152 * 8;
-// rows wider than this keep the gradients' sums in shared memory: 1,024 threads have no registers
-constexpr int kWide = 4096;
+constexpr int kWide = 4096;    // the gradients of wider rows take 16 channels a thread
+constexpr int kMaxStages = 8;
 
 template <typename T>
 struct Raw;  // 8 values as they are in memory
@@ -202,133 +205,241 @@ __global__ void __launch_bounds__(1024) norm_kernel(const BlockNormArgs a) {
     }
 }
 
-// kWideRows: rows of more than kWide channels, whose sums are kept in shared memory ([3][D]).
-template <typename IO, typename R, bool kWideRows>
-__global__ void __launch_bounds__(kWideRows ? 1024 : 512, 1) norm_bwd_kernel(const BlockNormArgs a,
-                                                                            float* part) {
+// Pairs of numbers in one instruction.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 mul_pair(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma_pair(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+
+constexpr int kPairs = kV / 2;
+__device__ __forceinline__ void read(const __nv_bfloat16* p, float2 (&f)[kPairs]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e)
+        f[e] = make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+}
+__device__ __forceinline__ void read(const float* p, float2 (&f)[kPairs]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = make_float2(a.x, a.y); f[1] = make_float2(a.z, a.w);
+    f[2] = make_float2(b.x, b.y); f[3] = make_float2(b.z, b.w);
+}
+template <typename T>
+__device__ __forceinline__ void store(T* p, const float2 (&f)[kPairs]) {
+    const float v[kV] = {f[0].x, f[0].y, f[1].x, f[1].y, f[2].x, f[2].y, f[3].x, f[3].y};
+    store(p, v);
+}
+__device__ __forceinline__ void weights(const float* w, int c, bool live, float2 (&f)[kPairs]) {
+    float v[kV];
+    weights(w, c, live, v);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) f[e] = make_float2(v[2 * e], v[2 * e + 1]);
+}
+
+// Where a row's tensors are in a stage; those that are not used have no place.
+struct Places {
+    int y, gate, dx, r, dr, bytes;
+};
+template <typename IO, typename R>
+__host__ __device__ inline Places places(int D, bool y, bool gate, bool dr) {
+    Places p{};
+    int at = 0;
+    auto take = [&](bool used, int elem) {
+        const int here = at;
+        at += used ? D * elem : 0;
+        return here;
+    };
+    p.y = take(y, sizeof(IO));
+    p.gate = take(gate, sizeof(IO));
+    p.dx = take(true, sizeof(IO));
+    p.r = take(true, sizeof(R));
+    p.dr = take(dr, sizeof(R));
+    p.bytes = at;
+    return p;
+}
+
+// kG: groups of 8 channels of a thread, blockDim.x groups apart.  With one, the weights stay in
+// registers.
+template <typename IO, typename R, int kG>
+__global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const __grid_constant__ BlockNormArgs a,
+                                                          float* part, int stages, unsigned* err) {
     __shared__ __align__(16) Sums<6> sums;
-    extern __shared__ __align__(16) float kept[];
-    clear(sums);
-    const int D = a.D, c = threadIdx.x * kV;
-    const bool live = c < D;
+    __shared__ uint64_t full[kMaxStages];
+    extern __shared__ __align__(128) char ring[];
+    const int D = a.D;
     const float over_D = 1.f / D;
     // without a norm, gate and scale the block's output is not looked at
     const bool use_y = a.post_norm || a.gate || a.dscale;
-    float wn[kV], ws[kV], wx[kV], dwn[kV], dws[kV], dwx[kV];
-    auto read_weights = [&] {
-        weights(a.w_post, c, live, wn);
-        weights(a.scale, c, live, ws);
-        weights(a.w_pre, c, live, wx);
-    };
-    if (!kWideRows) read_weights();
-#pragma unroll
-    for (int e = 0; e < kV; ++e) {
-        dwn[e] = dws[e] = dwx[e] = 0.f;
-        if (kWideRows && live) kept[c + e] = kept[D + c + e] = kept[2 * D + c + e] = 0.f;
+    const Places at = places<IO, R>(D, use_y, a.gate, a.dr);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        fence_mbar_init();
     }
-    Raw<IO> yr, gr, xr;
-    Raw<R> rr, dr;
-    auto fetch = [&](int64_t t) {
-        yr.zero();
-        gr.zero();
-        xr.zero();
-        rr.zero();
-        dr.zero();
-        if (t < a.T && live) {
-            const int64_t at = t * D + c;
-            if (use_y) yr.load(static_cast<const IO*>(a.y) + at);
-            if (a.gate) gr.load(static_cast<const IO*>(a.gate) + at);
-            xr.load(static_cast<const IO*>(a.dx) + at);
-            rr.load(static_cast<const R*>(a.r) + at);
-            if (a.dr) dr.load(static_cast<const R*>(a.dr) + at);
-        }
+    clear(sums);
+    auto load = [&](int64_t t, int s) {
+        if (threadIdx.x != 0 || t >= a.T) return;
+        char* st = ring + s * at.bytes;
+        mbar_expect_tx(&full[s], at.bytes);
+        const int64_t o = t * D;
+        const int io = D * (int)sizeof(IO), re = D * (int)sizeof(R);
+        if (use_y) bulk_g2s(st + at.y, static_cast<const IO*>(a.y) + o, io, &full[s]);
+        if (a.gate) bulk_g2s(st + at.gate, static_cast<const IO*>(a.gate) + o, io, &full[s]);
+        bulk_g2s(st + at.dx, static_cast<const IO*>(a.dx) + o, io, &full[s]);
+        bulk_g2s(st + at.r, static_cast<const R*>(a.r) + o, re, &full[s]);
+        if (a.dr) bulk_g2s(st + at.dr, static_cast<const R*>(a.dr) + o, re, &full[s]);
     };
-    fetch(blockIdx.x);
-    int buf = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
-        const Raw<IO> y_ = yr, g_ = gr, x_ = xr;
-        const Raw<R> r_ = rr, d_ = dr;
-        fetch(t + gridDim.x);
-        float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (kWideRows) read_weights();
-        {
-            float y[kV], g[kV], x[kV], r[kV], d[kV];
-            y_.get(y);
-            g_.get(g);
-            x_.get(x);
-            r_.get(r);
-            d_.get(d);
+    for (int s = 0; s < stages; ++s) load(blockIdx.x + (int64_t)s * gridDim.x, s);
+
+    float2 wn[kPairs], ws[kPairs], wx[kPairs], dwn[kG][kPairs], dws[kG][kPairs], dwx[kG][kPairs];
+    auto channel = [&](int g) { return ((int)threadIdx.x + g * (int)blockDim.x) * kV; };
+    auto read_weights = [&](int g) {
+        const int c = channel(g);
+        weights(a.w_post, c, c < D, wn);
+        weights(a.scale, c, c < D, ws);
+        weights(a.w_pre, c, c < D, wx);
+    };
+    if (kG == 1) read_weights(0);
 #pragma unroll
-            for (int e = 0; e < kV; ++e) {
-                const float u = x[e] * wx[e];
-                v[1] = fmaf(r[e], r[e], v[1]);
-                v[2] = fmaf(u, r[e], v[2]);
-                if (a.post_norm) {
-                    const float q = y[e] * wn[e] * ws[e] * (a.gate ? gate_of(g[e]).s : 1.f);
-                    v[0] = fmaf(y[e], y[e], v[0]);
-                    v[3] = fmaf(d[e], q, v[3]);
-                    v[4] = fmaf(u, q, v[4]);
-                    v[5] = fmaf(r[e], q, v[5]);
-                }
+    for (int g = 0; g < kG; ++g)
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) dwn[g][e] = dws[g][e] = dwx[g][e] = both(0.f);
+
+    int buf = 0, s = 0, turn = 0;
+    bool broken = false;  // (a wait that ran out: the others are not waited for)
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
+        const char* st = ring + s * at.bytes;
+        const IO* const yp = reinterpret_cast<const IO*>(st + at.y);
+        const IO* const gp = reinterpret_cast<const IO*>(st + at.gate);
+        const IO* const xp = reinterpret_cast<const IO*>(st + at.dx);
+        const R* const rp = reinterpret_cast<const R*>(st + at.r);
+        const R* const dp = reinterpret_cast<const R*>(st + at.dr);
+        if (!broken) broken = !mbar_wait(&full[s], turn, err);
+        float2 v2[6];
+#pragma unroll
+        for (int k = 0; k < 6; ++k) v2[k] = both(0.f);
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+            const int c = channel(g);
+            if (c >= D) break;
+            if (kG > 1) read_weights(g);
+            float2 x[kPairs], r[kPairs];
+            read(xp + c, x);
+            read(rp + c, r);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                x[e] = mul_pair(x[e], wx[e]);  // u
+                v2[1] = fma_pair(r[e], r[e], v2[1]);
+                v2[2] = fma_pair(x[e], r[e], v2[2]);
+            }
+            if (!a.post_norm) continue;
+            float2 q[kPairs], d[kPairs];
+            read(yp + c, q);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                v2[0] = fma_pair(q[e], q[e], v2[0]);
+                q[e] = mul_pair(mul_pair(q[e], wn[e]), ws[e]);
+            }
+            if (a.gate) {
+                read(gp + c, d);
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e)
+                    q[e] = mul_pair(q[e], make_float2(gate_of(d[e].x).s, gate_of(d[e].y).s));
+            }
+            if (a.dr) {
+                read(dp + c, d);
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) v2[3] = fma_pair(d[e], q[e], v2[3]);
+            }
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                v2[4] = fma_pair(x[e], q[e], v2[4]);
+                v2[5] = fma_pair(r[e], q[e], v2[5]);
             }
         }
+        float v[6];
+#pragma unroll
+        for (int k = 0; k < 6; ++k) v[k] = v2[k].x + v2[k].y;
         sum_all(sums, buf, v);
+        // (every thread is done with the row before this one: its place is free)
+        if (t > blockIdx.x && stages > 1 && !broken)
+            load(t + (int64_t)(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
         const float inv_y = a.post_norm ? rsqrtf(v[0] * over_D + a.eps) : 1.f;
         const float inv_r = rsqrtf(v[1] * over_D + a.eps);
         // G = dr + inv_r u - back r
         const float back = inv_r * inv_r * inv_r * (v[2] * over_D);
-        const float dot = a.post_norm ? inv_y * inv_y * over_D * (v[3] + inv_r * v[4] - back * v[5]) : 0.f;
-        if (!live) continue;
-        if (kWideRows) {
-            asm volatile("" ::: "memory");  // (read again, not kept)
-            read_weights();
-        }
-        float y[kV], x[kV], r[kV], G[kV];
-        y_.get(y);
-        x_.get(x);
-        r_.get(r);
-        d_.get(G);
+        const float dot =
+            a.post_norm ? -inv_y * inv_y * inv_y * over_D * (v[3] + inv_r * v[4] - back * v[5]) : 0.f;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) G[e] = fmaf(-back, r[e], fmaf(inv_r, x[e] * wx[e], G[e]));
-        const int64_t at = t * D + c;
-        store(static_cast<R*>(a.dr_in) + at, G);
+        for (int g = 0; g < kG; ++g) {
+            const int c = channel(g);
+            if (c >= D) break;
+            if (kG > 1) read_weights(g);
+            const int64_t o = t * D + c;
+            float2 G[kPairs], x[kPairs], r[kPairs];
+            if (a.dr) {
+                read(dp + c, G);
+            } else {
 #pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            r[e] = x[e] * r[e] * inv_r;  // dw_pre's
-            dwx[e] += r[e];
-        }
-        float g[kV], dy[kV];
-        g_.get(g);
-#pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            const Gate s = a.gate ? gate_of(g[e]) : Gate{1.f, 0.f};
-            const float yh = y[e] * inv_y, gs = G[e] * s.s, dn = gs * ws[e];
-            dy[e] = inv_y * (dn * wn[e]) - y[e] * (inv_y * dot);
-            if (!a.post_norm) dy[e] = dn;
-            g[e] = dn * yh * wn[e] * s.other;
-            x[e] = gs * yh * wn[e];  // dscale's
-            y[e] = dn * yh;          // dw_post's
-            dws[e] += x[e];
-            dwn[e] += y[e];
-        }
-        store(static_cast<IO*>(a.dy) + at, dy);
-        if (a.gate) store(static_cast<IO*>(a.dgate) + at, g);
-        if (kWideRows) {
-#pragma unroll
-            for (int e = 0; e < kV; ++e) {
-                kept[c + e] += x[e];
-                kept[D + c + e] += y[e];
-                kept[2 * D + c + e] += r[e];
+                for (int e = 0; e < kPairs; ++e) G[e] = both(0.f);
             }
+            read(xp + c, x);
+            read(rp + c, r);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                const float2 u = mul_pair(x[e], wx[e]);
+                G[e] = fma_pair(r[e], both(-back), fma_pair(u, both(inv_r), G[e]));
+                dwx[g][e] = fma_pair(mul_pair(x[e], r[e]), both(inv_r), dwx[g][e]);
+            }
+            store(static_cast<R*>(a.dr_in) + o, G);
+            float2 y[kPairs];
+            if (use_y) {
+                read(yp + c, y);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) y[e] = both(0.f);
+            }
+            float2 other[kPairs];  // 1 - s(gate)
+            if (a.gate) {
+                read(gp + c, x);
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) {
+                    const Gate p = gate_of(x[e].x), q = gate_of(x[e].y);
+                    G[e] = mul_pair(G[e], make_float2(p.s, q.s));
+                    other[e] = make_float2(p.other, q.other);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                const float2 yh = mul_pair(y[e], both(inv_y)), n = mul_pair(yh, wn[e]);
+                const float2 dn = mul_pair(G[e], ws[e]);
+                dws[g][e] = fma_pair(G[e], n, dws[g][e]);
+                dwn[g][e] = fma_pair(dn, yh, dwn[g][e]);
+                if (a.gate) x[e] = mul_pair(mul_pair(dn, n), other[e]);
+                G[e] = a.post_norm ? fma_pair(y[e], both(dot), mul_pair(mul_pair(dn, wn[e]), both(inv_y)))
+                                   : dn;
+            }
+            store(static_cast<IO*>(a.dy) + o, G);
+            if (a.gate) store(static_cast<IO*>(a.dgate) + o, x);
+        }
+        if (stages == 1) {
+            __syncthreads();
+            if (!broken) load(t + gridDim.x, 0);
+        }
+        if (++s == stages) {
+            s = 0;
+            turn ^= 1;
         }
     }
-    if (part && live) {
+    if (part == nullptr) return;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+        const int c = channel(g);
+        if (c >= D) break;
         float* out = part + (int64_t)blockIdx.x * 3 * D + c;
 #pragma unroll
-        for (int e = 0; e < kV; ++e) {
-            out[e] = kWideRows ? kept[c + e] : dws[e];
-            out[D + e] = kWideRows ? kept[D + c + e] : dwn[e];
-            out[2 * D + e] = kWideRows ? kept[2 * D + c + e] : dwx[e];
+        for (int e = 0; e < kPairs; ++e) {
+            reinterpret_cast<float2*>(out)[e] = dws[g][e];
+            reinterpret_cast<float2*>(out + D)[e] = dwn[g][e];
+            reinterpret_cast<float2*>(out + 2 * D)[e] = dwx[g][e];
         }
     }
 }
@@ -358,7 +469,10 @@ __global__ void __launch_bounds__(1024) norm_sums_kernel(const float* part, int 
     }
 }
 
-int threads_for(int D) { return (D / kV + 31) / 32 * 32; }
+// For `groups` groups of 8 channels a thread.
+int threads_for(int D, int groups = 1) {
+    return ((D / kV + groups - 1) / groups + 31) / 32 * 32;
+}
 
 // CTAs that fill the GPU, two rows' loads of every thread on their way.
 int blocks_for(int64_t T, int threads, int regs_threads) {
@@ -376,23 +490,36 @@ cudaError_t forward(const BlockNormArgs& a) {
     return cudaGetLastError();
 }
 
+// CTAs of the gradients, 128 registers a thread and up to four an SM, and their threads.
+int bwd_threads(int D) { return threads_for(D, D > kWide ? 2 : 1); }
+int bwd_blocks(int64_t T, int D) { return blocks_for(T, bwd_threads(D), 512); }
+
+template <typename IO, typename R, int kG>
+cudaError_t backward_of(const BlockNormArgs& a, float* part, int grid) {
+    const int threads = bwd_threads(a.D);
+    const Places at = places<IO, R>(a.D, a.post_norm || a.gate || a.dscale, a.gate, a.dr);
+    // the rows that an SM's shared memory holds, in equal parts
+    const int per_sm = (grid + 151) / 152;
+    int stages = (227 * 1024 / per_sm - 3 * 1024) / at.bytes;
+    if (stages > kMaxStages) stages = kMaxStages;
+    if (stages < 1) return cudaErrorInvalidValue;
+    const int smem = stages * at.bytes;
+    auto kernel = norm_bwd_kernel<IO, R, kG>;
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+        return e;
+    ProfScope prof("block_norm_bwd_kernel", a.stream);
+    kernel<<<grid, threads, smem, a.stream>>>(a, part, stages, a.dev_err);
+    return cudaGetLastError();
+}
+
 template <typename IO, typename R>
 cudaError_t backward(const BlockNormArgs& a) {
     float* part = a.dscale || a.dw_post || a.dw_pre ? static_cast<float*>(a.workspace) : nullptr;
-    const int threads = threads_for(a.D);
-    int grid = blocks_for(a.T, threads, 512);
-    if (grid > kMaxBlocks) grid = kMaxBlocks;
+    const int grid = bwd_blocks(a.T, a.D);
     if (grid > 0) {
-        ProfScope prof("block_norm_bwd_kernel", a.stream);
-        if (a.D > kWide) {
-            const int smem = 3 * a.D * (int)sizeof(float);
-            if (cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<IO, R, true>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
-                return e;
-            norm_bwd_kernel<IO, R, true><<<grid, threads, smem, a.stream>>>(a, part);
-        } else {
-            norm_bwd_kernel<IO, R, false><<<grid, threads, 0, a.stream>>>(a, part);
-        }
+        const cudaError_t e = a.D > kWide ? backward_of<IO, R, 2>(a, part, grid)
+                                          : backward_of<IO, R, 1>(a, part, grid);
+        if (e != cudaSuccess) return e;
     }
     if (part) {
         ProfScope prof("block_norm_sums_kernel", a.stream);
@@ -405,7 +532,7 @@ cudaError_t backward(const BlockNormArgs& a) {
 }  // namespace
 
 size_t block_norm_bwd_workspace_size(int D) {
-    return (size_t)blocks_for(kMaxBlocks, threads_for(D), 512) * 3 * D * sizeof(float);
+    return (size_t)bwd_blocks((int64_t)1 << 31, D) * 3 * D * sizeof(float);
 }
 
 cudaError_t launch_block_norm(const BlockNormArgs& a) {

@@ -203,6 +203,7 @@ struct BlockNormArgs {
     int D;
     int io_bf16, r_bf16;
     void* workspace;
+    unsigned* dev_err;  // backward only
     cudaStream_t stream;
 };
 constexpr int kMaxBlockNormD = 8192;
