@@ -87,31 +87,53 @@ __device__ __forceinline__ void weights(const float* w, int c, bool live, float 
 }
 
 // Sums over the CTA's threads, the same in all of them.  buf: alternates from one call to the next, so
-// that a call needs one barrier.
+// that a call needs one barrier.  (Of six numbers half go to each half of a warp after the first
+// step, and the warps' sums are read four at a time by a lane each: 45 instructions, not 170.)
 template <int n>
 struct Sums {
+    static_assert(n == 1 || n == 6, "");
     float part[2][n][kMaxWarps];
 };
 template <int n>
 __device__ __forceinline__ void sum_all(Sums<n>& s, int buf, float (&v)[n]) {
+    constexpr unsigned kAll = 0xffffffffu;
+    constexpr int kEach = n == 1 ? 1 : n / 2;  // numbers of a half
+    const int lane = threadIdx.x & 31, warps = blockDim.x / 32;
+    float h[kEach];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-        for (int k = 0; k < n; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], off);
-    const int warps = blockDim.x / 32;
-    if (warps == 1) return;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int k = 0; k < n; ++k) s.part[buf][k][threadIdx.x >> 5] = v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < n; ++k) v[k] = 0.f;
-    for (int w = 0; w < warps; w += 4)  // (the unused ones are zeros)
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            const float4 p = *reinterpret_cast<const float4*>(&s.part[buf][k][w]);
-            v[k] += (p.x + p.y) + (p.z + p.w);
+    for (int k = 0; k < kEach; ++k) {
+        if (n == 1) {
+            h[k] = v[k] + __shfl_xor_sync(kAll, v[k], 16);
+        } else {
+            const float keep = lane < 16 ? v[k] : v[n - kEach + k];
+            h[k] = keep + __shfl_xor_sync(kAll, lane < 16 ? v[n - kEach + k] : v[k], 16);
         }
+    }
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1)
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) h[k] += __shfl_xor_sync(kAll, h[k], off);
+    if (warps == 1) {
+#pragma unroll
+        for (int k = 0; k < n; ++k) v[k] = __shfl_sync(kAll, h[k % kEach], k / kEach * 16);
+        return;
+    }
+    if (lane % 16 == 0 && (n > 1 || lane == 0))
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) s.part[buf][lane / 16 * kEach + k][threadIdx.x >> 5] = h[k];
+    __syncthreads();
+    // four warps' sums of one number a lane (of warps that are not there, zeros)
+    constexpr int kLanes = n == 1 ? kMaxWarps / 4 : 4;
+    const int k = lane / kLanes;
+    float x = 0.f;
+    if (k < n) {
+        const float4 p = *reinterpret_cast<const float4*>(&s.part[buf][k][lane % kLanes * 4]);
+        x = (p.x + p.y) + (p.z + p.w);
+    }
+#pragma unroll
+    for (int off = 1; off < kLanes; off <<= 1) x += __shfl_xor_sync(kAll, x, off);
+#pragma unroll
+    for (int j = 0; j < n; ++j) v[j] = __shfl_sync(kAll, x, j * kLanes);
 }
 template <int n>
 __device__ __forceinline__ void clear(Sums<n>& s) {
