@@ -356,7 +356,8 @@ kda_status_t kda_qk_norm_rope_bwd(const void *q, int64_t q_ld, const void *k, in
  * kda_recurrence_fwd -- the forward over N packed sequences.
  *   h0     : [N, D] initial states, or NULL for zeros
  *   h_out  : [N, D] final states (written), or NULL
- *   cu_seqlens, N, T_total : as kda_fwd_chunked (a sequence may be empty: its h_out is its h0)
+ *   cu_seqlens, N, T_total : as kda_fwd_chunked (a sequence may be empty: its h_out is its h0);
+ *            T_total < 2^31 - 2048
  *   y      : [T_total, D] io_dt (written)
  *   edges  : [ceil(T_total / 8), D] (written), or NULL: row j is the state that token 8 j starts
  *            from.  kda_recurrence_bwd takes it and is then spared a pass over the inputs.

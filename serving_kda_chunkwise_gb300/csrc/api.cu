@@ -701,6 +701,9 @@ static kda_status_t check_recurrence(const kda::RecurrenceArgs& a, kda_dtype_t i
     if (kda_status_t s = check_width(a.D)) return s;
     if (kda_status_t s = check_gmin(a.g_min)) return s;
     if (kda_status_t s = check_packed(a.T_total, a.N, a.D, a.cu_seqlens)) return s;
+    // (tokens are counted in 32 bits, those of tiles behind the last one too)
+    KDA_REQUIRE(a.T_total < ((int64_t)1 << 31) - 2048, "T_total=%lld must be below 2^31 - 2048",
+                (long long)a.T_total);
     const int per16 = io_dt == KDA_BF16 ? 8 : 4;
     if (!a.packed) {
         if (kda_status_t s = check_ld(a.x_ld, a.D, per16, "x_ld")) return s;

@@ -1,22 +1,30 @@
 // recurrence.cu -- the gated recurrence of single channels (declared in include/kda.h): packed
 // forward, gradients (from whole or 8-bit inputs) and the single-token step.
 //
-//   h_t = a_t h_{t-1} + b_t,   a = e^g, b = sqrt(1 - e^{2g}) s(i) x          (recurrence_math.cuh)
+//   h_t = a_t h_{t-1} + b_t,   a = e^g, b = sqrt(1 - e^{2g}) s(i) x           (recurrence_math.cuh)
 //   l_t = dy_t + a_{t+1} l_{t+1}, backwards, for the gradients
 //
 // Both are scans of affine maps (P, H): h -> P h + H.  A cluster of CTAs takes 64 channels along a
 // run, some consecutive sequences.  In a step each of its CTAs has a tile of 64 or 128 tokens: each of
-// eight warps holds 8 or 16 tokens, a lane two channels, and leaves its tokens' map in shared memory.  The maps
-// are composed, the tile's map is sent to every CTA of the cluster (stores into distributed shared
-// memory that count their bytes on a barrier there), and the state is carried over the cluster's
+// eight warps holds 8 or 16 tokens, a lane two channels, and leaves its tokens' map in shared memory.
+// One warp composes the maps, sends the tile's to every CTA of the cluster (stores into distributed
+// shared memory that count their bytes on a barrier there) and carries the state over the cluster's
 // maps; then every warp goes over its tokens again, in registers, and writes.  So inputs are read
-// once, results written once, in rows of 128 bytes (bf16), and no cluster waits for another.
-// (Narrower columns instead of clusters cost more in the copies of short rows.)
+// once (by the copy engine, steps ahead), results written once, in rows of 128 bytes (bf16), and no
+// cluster waits for another.  Ways that were slower at 65,536 x 4096 (now 436 us): a look-back over
+// tiles by messages in memory, 890 us; columns of 16 channels without clusters, 715 us, for the copies
+// of 32-byte rows; 8 tokens a warp instead of 16, 531 us; CTAs of 4 or 16 warps, 580 and 880 us.
 //
 // The gradients go over the tiles backwards.  A thread's states come from the edges, the state that
 // every 8th token starts from, which the forward writes on request; without them a forward that
 // writes nothing else runs first.  So the factors of l_t in the gradients are formed once, before
-// the scan, and stay in registers until l_t is known.
+// the scan, and stay in registers until l_t is known (which is why a warp has 8 tokens).
+//
+// Bound by instructions, and by the clusters' being 256 CTAs for 152 SMs: the forward of 65,536 x 4096
+// in bf16 436 us, 4.9 TB/s (its special functions alone would be 190 us, its memory 322); gradients
+// from edges of 32,768 x 4096 455 us, 120 instructions for two channels of a token; from 8-bit inputs
+// of 65,536 x 2048 255 us for the edges and 545 us (1,610 with 12 bytes of spilled registers: tiles
+// leave the first-level cache nothing, so no kernel here may spill).
 //
 // Sequences: a setup launch finds the tokens with which sequences start and end, 8 at a time, and
 // cuts the batch into runs (one sequence needs none of it).  Where a sequence starts, a map is
@@ -298,23 +306,20 @@ __global__ void __launch_bounds__(256) setup_kernel(const RecurrenceArgs a, cons
 // ------------------------------------------------------------------ scan --
 
 // The maps of a thread's two channels: (P.x, P.y, H.x, H.y), P's sign bit set where the map is
-// constant.  kCut: some may be.
+// constant.
 __device__ __forceinline__ bool constant(float P) { return __float_as_int(P) < 0; }
 
-template <bool kCut>
 __device__ __forceinline__ float2 apply(float4 m, float2 h) {
     const float2 r = fma_pair(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
-    if (kCut && constant(m.x)) return make_float2(m.z, m.w);
-    return r;
+    return constant(m.x) ? make_float2(m.z, m.w) : r;
 }
 // The map that applies `before` and then m.
-template <bool kCut>
 __device__ __forceinline__ float4 after(float4 m, float4 before) {
     const float2 P = mul_pair(make_float2(m.x, m.y), make_float2(before.x, before.y));
     const float2 H = fma_pair(make_float2(m.x, m.y), make_float2(before.z, before.w),
                           make_float2(m.z, m.w));
-    if (kCut && constant(m.x)) return m;
-    if (kCut && constant(before.x)) return make_float4(-0.f, -0.f, H.x, H.y);
+    if (constant(m.x)) return m;
+    if (constant(before.x)) return make_float4(-0.f, -0.f, H.x, H.y);
     return make_float4(P.x, P.y, H.x, H.y);
 }
 __device__ __forceinline__ float4 identity() { return make_float4(1.f, 1.f, 0.f, 0.f); }
@@ -387,43 +392,53 @@ struct Steps {
     }
 };
 
-// The state that a CTA's tile starts from; carry: from before the step's tiles to after them.
-__device__ __forceinline__ float2 carry_over(const float4 (*tiles)[32], int lane, int rank, int ctas,
-                                             float2& carry) {
-    float2 h = carry, mine = carry;
-#pragma unroll
-    for (int j = 0; j < kMaxCluster; ++j) {
-        if (j >= ctas) break;
-        if (j == rank) mine = h;
-        h = apply<true>(tiles[j][lane], h);
-    }
-    carry = h;
-    return mine;
-}
-
 // What a CTA keeps of a step's maps, in the scan's order.
 template <int kStages>
 struct Maps {
     float4 warps[kWarps][32];          // its warps'
     float4 tiles[2][kMaxCluster][32];  // the cluster's tiles'; of two steps in turn
-    uint64_t there[2], full[kStages];  // barriers: those are there
+    float2 start[kWarps][32];          // the states that its warps' tokens start from
+    float2 carry[32];                  // from step to step
+    uint64_t there[2], states, full[kStages];  // barriers: the tiles', the states, inputs are there
 };
 
-// With the warps' maps there: the map of those before `turn`; the last one sends the tile's map to
-// the CTAs of the cluster.
-template <bool kCut, int kStages, typename Steps>
-__device__ __forceinline__ float4 compose(Maps<kStages>& x, int buf, int turn, int lane,
-                                          const Steps& steps) {
-    float4 before = identity();
+// By one warp, with the warps' maps there: sends the tile's map to the CTAs of the cluster, calls
+// meanwhile(), carries the state over the cluster's maps and leaves the warps' starts.  (Every warp
+// for itself would read most of the maps again: some 800 instructions a step more with 8 CTAs.)
+template <int kStages, typename Steps, typename Meanwhile>
+__device__ __forceinline__ void exchange(Maps<kStages>& x, const Steps& steps, int k, int lane,
+                                         bool& broken, unsigned* err, Meanwhile&& meanwhile) {
+    const int buf = k & 1;
+    float4 own[kWarps], all;
 #pragma unroll
-    for (int j = 0; j < kWarps - 1; ++j)
-        if (j < turn) before = after<kCut>(x.warps[j][lane], before);
-    if (turn == kWarps - 1) {
-        const float4 all = after<kCut>(x.warps[turn][lane], before);
-        for (int j = 0; j < steps.ctas; ++j)
-            send(place_in(&x.tiles[buf][steps.rank][lane], j), place_in(&x.there[buf], j), all);
+    for (int j = 0; j < kWarps; ++j) own[j] = x.warps[j][lane];
+    all = own[0];
+    own[0] = identity();
+#pragma unroll
+    for (int j = 1; j < kWarps; ++j) {  // own becomes the map of the warps before
+        const float4 next = after(own[j], all);
+        own[j] = all;
+        all = next;
     }
-    return before;
+    for (int j = 0; j < steps.ctas; ++j)
+        send(place_in(&x.tiles[buf][steps.rank][lane], j), place_in(&x.there[buf], j), all);
+    meanwhile();
+    // (the next maps for this buffer are sent when this CTA's of the next step are there, which its
+    // barrier of that step precedes)
+    if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, err);
+    if (lane == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
+    float2 h = k == 0 ? both(0.f) : x.carry[lane], mine = h;
+#pragma unroll
+    for (int j = 0; j < kMaxCluster; ++j) {
+        if (j >= steps.ctas) break;
+        if (j == steps.rank) mine = h;
+        h = apply(x.tiles[buf][j][lane], h);
+    }
+    x.carry[lane] = h;
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) x.start[j][lane] = apply(own[j], mine);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&x.states);
 }
 
 // Before anything else: the barriers, by all threads; the caller waits for the cluster
@@ -433,6 +448,7 @@ __device__ __forceinline__ void open_maps(Maps<kStages>& x, const Tensors& m, ui
     if (threadIdx.x == 0) {
         for (int k = 0; k < kStages; ++k) mbar_init(&x.full[k], fill_count<In>(m));
         for (int k = 0; k < 2; ++k) mbar_init(&x.there[k], 1);
+        mbar_init(&x.states, 1);
         fence_mbar_init();
         for (int k = 0; k < 2; ++k) mbar_expect_tx(&x.there[k], bytes);
     }
@@ -502,12 +518,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     }
     const float2 nl =
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
-    float2 carry = both(0.f);
-    uint32_t marks = marks_at(0), coming = marks_at(1);
-    bool marked = __syncthreads_or(marks != 0u), broken = false;
+    uint32_t marks = marks_at(0);
+    bool broken = false;  // (a wait that ran out: the ones after are not taken, so that all ends)
+    __syncwarp();
     cluster_wait();
     for (int k = 0; k < steps.count; ++k) {
-        const int buf = k & 1, s = k % kStages;
+        const int s = k % kStages;
         const View<S, In, IO> v{ring + s * S::kBytes, nullptr, warp, lane};
         const int64_t t = steps.first_token(k) + warp * kTok;
         const bool some = steps.some(k);
@@ -543,17 +559,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
             }
         }
         x.warps[warp][lane] = make_float4(P.x, P.y, H.x, H.y);
-        const bool next_marked = __syncthreads_or(coming != 0u);
-        const float4 before = marked ? compose<true>(x, buf, warp, lane, steps)
-                                     : compose<false>(x, buf, warp, lane, steps);
-        load(k + kStages);  // (the stage has been read)
-        const uint32_t later = marks_at(k + 2);
-        // (the next maps for this buffer are sent when this CTA's of the next step are there, which
-        // its barrier of that step precedes)
-        if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, a.dev_err);
-        if (threadIdx.x == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
-        const float2 mine = carry_over(x.tiles[buf], lane, steps.rank, steps.ctas, carry);
-        float2 h = marked ? apply<true>(before, mine) : apply<false>(before, mine);
+        __syncthreads();
+        // (the stage has been read)
+        if (warp == 0) {
+            exchange(x, steps, k, lane, broken, a.dev_err, [&] { load(k + kStages); });
+            put(k + kStages);
+        }
+        const uint32_t coming = marks_at(k + 1);
+        if (!broken) broken = !mbar_wait(&x.states, k & 1, a.dev_err);
+        const float2 h = x.start[warp][lane];
         if (some && live) {
             IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
             float* edge = a.edges + t / kEdge * a.D + ch;
@@ -584,10 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                 }
             }
         }
-        put(k + kStages);
-        marked = next_marked;
         marks = coming;
-        coming = later;
     }
     __syncwarp();
     cluster_arrive();  // (a CTA stays until nobody can send to it)
@@ -642,12 +653,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
         }
         const ChannelRate r = channel_rate(
             live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), gb.g_min);
-        float2 edge = edge_at(0), carry = both(0.f);
-        uint32_t marks = marks_at(0), coming = marks_at(1);
-        bool marked = __syncthreads_or(marks != 0u), broken = false;
+        float2 edge = edge_at(0);
+        uint32_t marks = marks_at(0);
+        bool broken = false;
+        __syncwarp();
         cluster_wait();
         for (int k = 0; k < steps.count; ++k) {
-            const int buf = k & 1, s = k % kStages;
+            const int s = k % kStages;
             char* const st = ring + s * S::kBytes;
             const View<S, In, IO> v{st, S::kInPlace ? st : ring + kStages * S::kBytes, warp, lane};
             const int t0 = steps.first_token(k);
@@ -694,18 +706,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             }
             x.warps[turn][lane] = make_float4(P.x, P.y, H.x, H.y);
             if (threadIdx.x == 0) bulk_wait_read0();  // (the stage before this one is free)
-            const bool next_marked = __syncthreads_or(coming != 0u);
-            const float4 before = marked ? compose<true>(x, buf, turn, lane, steps)
-                                         : compose<false>(x, buf, turn, lane, steps);
-            load(k + kAhead);
+            __syncthreads();
+            if (warp == 0) {
+                exchange(x, steps, k, lane, broken, a.dev_err, [&] { load(k + kAhead); });
+                put(k + kAhead);
+            }
             edge = edge_at(k + 1);
-            const uint32_t later = marks_at(k + 2);
-            // (the next maps for this buffer are sent when this CTA's of the next step are there, which
-            // its barrier of that step precedes)
-            if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, a.dev_err);
-            if (threadIdx.x == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
-            const float2 mine = carry_over(x.tiles[buf], lane, steps.rank, steps.ctas, carry);
-            float2 nr = marked ? apply<true>(before, mine) : apply<false>(before, mine);
+            const uint32_t coming = marks_at(k + 1);
+            if (!broken) broken = !mbar_wait(&x.states, k & 1, a.dev_err);
+            float2 nr = x.start[turn][lane];
             // a token's gradients but for the state's
             auto take = [&](int j, float2 l, IO* dx, IO* dz, IO* di) {
                 const float2 g = mul_pair(l, fz[j]), z = v.finite(1, j);
@@ -756,10 +765,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                     __syncwarp();
                 }
             }
-            put(k + kAhead);
-            marked = next_marked;
             marks = coming;
-            coming = later;
         }
         if (threadIdx.x == 0) bulk_wait0();
         __syncwarp();
@@ -874,12 +880,13 @@ int count_runs(int64_t T, int N, int cols) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(N, T / 1024), most));
 }
 
-// CTAs of a cluster: as many as keep all of them on the GPU at once, two an SM; with several runs,
-// that a run has 8 steps on average.
+// CTAs of a cluster, for tiles of kT tokens: as many as keep all of them on the GPU at once, two an SM;
+// with several runs, one for every 1,024 tokens that a run has on average (24 sequences, 47,139 tokens
+// x 2560: 186 us with two, 197 with one, 199 with four).
 int count_ctas(int64_t T, int runs, int cols, int kT) {
     int n = 1;
-    while (2 * n <= kMaxCluster && T / runs > kT * n &&
-           ((int64_t)runs * cols * 2 * n <= 304 || (runs > 1 && T / runs >= (int64_t)kT * 2 * n * 8)))
+    while (2 * n <= kMaxCluster && T > (int64_t)kT * n * runs &&
+           ((int64_t)runs * cols * 2 * n <= 304 || (runs > 1 && T >= (int64_t)1024 * n * runs)))
         n *= 2;
     return n;
 }

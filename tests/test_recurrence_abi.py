@@ -36,6 +36,7 @@ PACKED = [
     (dict(g_min=f(float("nan"))), 1, "g_min"), (dict(D=0), 1, "D=0"),
     (dict(D=60), 2, "multiples of 8"), (dict(dt=2), 1, "kda_dtype_t"),
     (dict(T=i64(-1)), 1, "T_total"), (dict(T=i64(1 << 31)), 1, "T_total"),
+    (dict(T=i64((1 << 31) - 2048)), 1, "T_total"),
     (dict(N=-1), 1, "N=-1"), (dict(N=3), 1, "multiple of N"), (dict(N=0), 1, "N=0"),
     (dict(cu=vp(0x10004)), 1, "cu_seqlens is not 16-byte"),
     (dict(h0=vp(0x10004)), 1, "h0 is not 16-byte"),
