@@ -27,9 +27,9 @@
 // leave the first-level cache nothing, so no kernel here may spill).
 //
 // Sequences: a setup launch finds the tokens with which sequences start and end, 8 at a time, and
-// cuts the batch into runs (one sequence needs none of it).  Where a sequence starts, a map is
-// constant: P's sign bit says so (P >= 0 otherwise), and it is selected, not multiplied by zero, so
-// that nothing that is not finite crosses.
+// cuts the batch into runs (one sequence needs none of it, and short forwards of a few do it
+// themselves).  Where a sequence starts, a map is constant: P's sign bit says so (P >= 0 otherwise), and
+// it is selected, not multiplied by zero, so that nothing that is not finite crosses.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -50,12 +50,16 @@ constexpr int kWarps = 8;
 constexpr int kMaxCluster = 8;
 constexpr int kThreads = 32 * kWarps;
 
+// Sequences that a CTA of the scan finds its way through by itself, a lane of a warp each.
+constexpr int kFew = 32, kNone = 0x7fffffff;
+
 // What the setup launch leaves for the scan.
 struct Plan {
-    int* run;            // [runs + 1] first tokens; nullptr, as all here: one sequence
+    int* run;            // [runs + 1] first tokens; nullptr, as all here, without it
     uint32_t* marks;     // [ceil(T / 8)] bits of tokens that start (0..7) and end (8..15) a sequence
     int *start_seq, *end_seq;  // [T] whose sequence, at such tokens
     int runs, cols;
+    bool few;  // a few sequences, without a setup launch
 };
 
 // ---------------------------------------------------------------- inputs --
@@ -356,21 +360,29 @@ __device__ __forceinline__ void cluster_wait() {
 
 // ------------------------------------------------------------- the loop --
 
-// The marks of tokens t .. t + 7.
-__device__ __forceinline__ uint32_t marks_of(const Plan& w, int64_t t, int64_t T) {
-    if (w.marks) return t < T ? __ldg(w.marks + t / kEdge) : 0u;
-    return (t == 0 ? 1u : 0u) | (T > t && T <= t + kEdge ? 256u << (T - 1 - t) : 0u);
-}
-// Of kTok tokens: those that start a sequence, and from bit 16 those that end one.
+// Of tokens t .. t + kTok - 1: those that start a sequence, and from bit 16 those that end one.  By a
+// whole warp.
 template <int kTok>
-__device__ __forceinline__ uint32_t marks_of(const Plan& w, int64_t t, int64_t T) {
+__device__ __forceinline__ uint32_t marks_of(const Plan& w, const int2* few, int lane, int t,
+                                             int64_t T) {
     uint32_t m = 0;
+    if (few == nullptr && w.marks) {
 #pragma unroll
-    for (int j = 0; j < kTok; j += kEdge) {
-        const uint32_t v = marks_of(w, t + j, T);
-        m |= (v & 0xffu) << j | (v >> 8) << (16 + j);
+        for (int j = 0; j < kTok; j += kEdge) {
+            const uint32_t v = t + j < T ? __ldg(w.marks + (t + j) / kEdge) : 0u;
+            m |= (v & 0xffu) << j | (v >> 8) << (16 + j);
+        }
+        return m;
     }
-    return m;
+    if (few == nullptr) {  // one sequence
+        if (t == 0) m = 1u;
+        if (T > t && T <= t + kTok) m |= 0x10000u << (int)(T - 1 - t);
+        return m;
+    }
+    const unsigned first = few[lane].x - t, last = few[lane].y - t;
+    if (first < kTok) m = 1u << first;
+    if (last < kTok) m |= 0x10000u << last;
+    return __reduce_or_sync(~0u, m);
 }
 
 // A CTA's tiles in its cluster's run.  Step k's is the `place(k)`-th in the scan's order; there may be
@@ -399,6 +411,7 @@ struct Maps {
     float4 tiles[2][kMaxCluster][32];  // the cluster's tiles'; of two steps in turn
     float2 start[kWarps][32];          // the states that its warps' tokens start from
     float2 carry[32];                  // from step to step
+    int2 few[kFew];                    // a few sequences' first and last tokens (kNone: empty)
     uint64_t there[2], states, full[kStages];  // barriers: the tiles', the states, inputs are there
 };
 
@@ -456,35 +469,69 @@ __device__ __forceinline__ void open_maps(Maps<kStages>& x, const Tensors& m, ui
     cluster_arrive();
 }
 
-// The cluster's run and first channel; false where it has nothing to do.
-__device__ __forceinline__ bool find_run(const RecurrenceArgs& a, const Plan& w, int& begin, int& end,
+// The cluster's run and first channel; false where it has nothing to do.  With `few` a CTA reads the
+// offsets itself, a lane of every warp one sequence, and takes on what the setup launch does.
+__device__ __forceinline__ bool find_run(const RecurrenceArgs& a, const Plan& w, int2* few, int lane,
+                                         const float* from, float* to, int& begin, int& end,
                                          int& c0) {
     const int id = blockIdx.x / cluster_size(), r = id / w.cols;
     c0 = (id - r * w.cols) * kC;
-    if (w.run) {
+    if (few == nullptr && w.run) {
         begin = w.run[r];
         end = w.run[r + 1];
         return begin < end;
     }
-    begin = 0;
-    end = (int)a.T_total;
-    if (blockIdx.x == 0 && threadIdx.x == 0) {  // no setup launch: its check here
-        int64_t b, e;
-        seq_range(a.cu_seqlens, 0, 1, a.T_total, a.dev_err, b, e);
+    if (few == nullptr) {
+        begin = 0;
+        end = (int)a.T_total;
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            int64_t b, e;
+            seq_range(a.cu_seqlens, 0, 1, a.T_total, a.dev_err, b, e);
+        }
+        return true;
     }
-    return true;
+    const bool mine = lane < a.N;
+    int64_t b = 0, e = 0;
+    if (mine)
+        seq_range(a.cu_seqlens, lane, a.N, a.T_total, blockIdx.x == 0 ? a.dev_err : nullptr, b, e);
+    if (threadIdx.x < 32)
+        few[lane] = b < e ? make_int2((int)b, (int)e - 1) : make_int2(kNone, kNone);
+    const bool passes = mine && b >= e && to && r == 0 && cluster_rank() == 0 && threadIdx.x < 32;
+    for (unsigned empty = __ballot_sync(~0u, passes); empty; empty &= empty - 1) {
+        const int n = __ffs(empty) - 1;
+        if (c0 + 2 * lane < a.D) {
+            const int64_t at = (int64_t)n * a.D + c0 + 2 * lane;
+            store_pair(to + at, from ? pair(from + at) : both(0.f));
+        }
+    }
+    // a run has the sequences that start in its part of the tokens
+    auto bound = [&](int j) {
+        const int t = (int)(a.T_total * j / w.runs);
+        return j == 0 ? 0
+               : j == w.runs
+                   ? t
+                   : __reduce_min_sync(~0u, b < e && b >= t ? (int)b : (int)a.T_total);
+    };
+    begin = bound(r);
+    end = bound(r + 1);
+    return begin < end;
 }
 // The sequence that starts, or ends, with token t.
-__device__ __forceinline__ int start_at(const Plan& w, int64_t t) {
-    return w.start_seq ? w.start_seq[t] : 0;
+__device__ __forceinline__ int find_few(const int* first_or_last, int t) {
+    int n = 0;
+    while (n < kFew - 1 && first_or_last[2 * n] != t) ++n;
+    return n;
 }
-__device__ __forceinline__ int end_at(const Plan& w, int64_t t) {
-    return w.end_seq ? w.end_seq[t] : 0;
+__device__ __forceinline__ int start_at(const Plan& w, const int2* few, int64_t t) {
+    return few ? find_few(&few[0].x, (int)t) : w.start_seq ? w.start_seq[t] : 0;
+}
+__device__ __forceinline__ int end_at(const Plan& w, const int2* few, int64_t t) {
+    return few ? find_few(&few[0].y, (int)t) : w.end_seq ? w.end_seq[t] : 0;
 }
 
 // ---------------------------------------------------------------- forward --
 
-template <typename In, typename IO, int kTok, int kStages, bool kOnlyEdges>
+template <typename In, typename IO, int kTok, int kStages, bool kOnlyEdges, bool kFewOnes>
 __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     const __grid_constant__ RecurrenceArgs a, const __grid_constant__ Plan w,
     const __grid_constant__ GateBound gb, const __grid_constant__ Tensors m) {
@@ -493,8 +540,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     __shared__ Maps<kStages> x;
     grid_dependency_wait();
     int begin, end, c0;
-    if (!find_run(a, w, begin, end, c0)) return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, ch = c0 + 2 * lane;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int2* const few = kFewOnes ? x.few : nullptr;
+    if (!find_run(a, w, few, lane, a.h0, a.h_out, begin, end, c0)) return;
+    const int ch = c0 + 2 * lane;
     const bool live = ch < a.D;
     const Steps<false, S::kT> steps(begin, end);
     open_maps<In>(x, m, steps.bytes());
@@ -509,7 +558,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
             put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
     };
     auto marks_at = [&](int k) {
-        return steps.some(k) ? marks_of<kTok>(w, steps.first_token(k) + warp * kTok, a.T_total) : 0u;
+        return steps.some(k)
+                   ? marks_of<kTok>(w, few, lane, steps.first_token(k) + warp * kTok, a.T_total)
+                   : 0u;
     };
 #pragma unroll
     for (int k = 0; k < kStages; ++k) {
@@ -518,10 +569,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     }
     const float2 nl =
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
-    uint32_t marks = marks_at(0);
     bool broken = false;  // (a wait that ran out: the ones after are not taken, so that all ends)
     __syncwarp();
     cluster_wait();
+    uint32_t marks = marks_at(0);
     for (int k = 0; k < steps.count; ++k) {
         const int s = k % kStages;
         const View<S, In, IO> v{ring + s * S::kBytes, nullptr, warp, lane};
@@ -548,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                     if (marks >> j & 1) {
                         P = both(-0.f);  // (constant from here on)
                         H = both(0.f);
-                        if (a.h0 && live) H = state_row(a.h0, start_at(w, t + j), a.D, ch);
+                        if (a.h0 && live) H = state_row(a.h0, start_at(w, few, t + j), a.D, ch);
                         if (j % kEdge == 0) opening[j / kEdge] = H;
                     }
                     if (!constant(P.x)) P = fma_pair(c[j], P, P);
@@ -592,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                     if (!kOnlyEdges && in) {
                         store_pair(y, last);
                         if (marks >> (16 + j) & 1 && a.h_out)
-                            store_pair(a.h_out + (int64_t)end_at(w, t + j) * a.D + ch, last);
+                            store_pair(a.h_out + (int64_t)end_at(w, few, t + j) * a.D + ch, last);
                     }
                     y += a.D;
                 }
@@ -618,8 +669,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     __shared__ Maps<kStages> x;
     grid_dependency_wait();
     int begin, end, c0;
-    const bool any = find_run(a, w, begin, end, c0);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, ch = c0 + 2 * lane;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const bool any = find_run(a, w, nullptr, lane, nullptr, nullptr, begin, end, c0);
+    const int ch = c0 + 2 * lane;
     const int turn = kWarps - 1 - warp;  // in the scan's order
     const bool live = ch < a.D;
     float2 dA = both(0.f);
@@ -638,7 +690,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
         };
         // a step's marks, and the state that the warp's tokens start from
         auto marks_at = [&](int k) {
-            return steps.some(k) ? marks_of<kTok>(w, steps.first_token(k) + warp * kTok, a.T_total) : 0u;
+            return steps.some(k)
+                       ? marks_of<kTok>(w, nullptr, lane, steps.first_token(k) + warp * kTok, a.T_total)
+                       : 0u;
         };
         auto edge_at = [&](int k) {
             const int64_t t = steps.first_token(k) + warp * kTok;
@@ -654,10 +708,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
         const ChannelRate r = channel_rate(
             live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), gb.g_min);
         float2 edge = edge_at(0);
-        uint32_t marks = marks_at(0);
         bool broken = false;
         __syncwarp();
         cluster_wait();
+        uint32_t marks = marks_at(0);
         for (int k = 0; k < steps.count; ++k) {
             const int s = k % kStages;
             char* const st = ring + s * S::kBytes;
@@ -679,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                         in, r, gb, edge,
                         [&](int j, float2 h) {
                             if (marks >> j & 1)
-                                h = a.h0 && live ? state_row(a.h0, start_at(w, t + j), a.D, ch)
+                                h = a.h0 && live ? state_row(a.h0, start_at(w, nullptr, t + j), a.D, ch)
                                                  : both(0.f);
                             return h;
                         },
@@ -696,7 +750,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                     for (int j = kTok - 1; j >= 0; --j) {
                         if (marks >> (16 + j) & 1)
                             H = a.dh_out && live
-                                    ? mul_pair(state_row(a.dh_out, end_at(w, t + j), a.D, ch), both(-1.f))
+                                    ? mul_pair(state_row(a.dh_out, end_at(w, nullptr, t + j), a.D, ch),
+                                               both(-1.f))
                                     : both(0.f);
                         const float2 l = fma_pair(v.dy(j), both(-1.f), H);
                         H = fma_pair(c[j], l, l);
@@ -736,7 +791,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                 for (int j = kTok - 1; j >= 0; --j) {
                     if (marks >> (16 + j) & 1)
                         nr = a.dh_out && live
-                                 ? mul_pair(state_row(a.dh_out, end_at(w, t + j), a.D, ch), both(-1.f))
+                                 ? mul_pair(state_row(a.dh_out, end_at(w, nullptr, t + j), a.D, ch),
+                                            both(-1.f))
                                  : both(0.f);
                     const float2 l = fma_pair(v.dy(j), both(-1.f), nr);
                     nr = fma_pair(c[j], l, l);
@@ -748,7 +804,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                         take(j, l, static_cast<IO*>(a.dx) + o, static_cast<IO*>(a.dz) + o,
                              static_cast<IO*>(a.di) + o);
                     if (mine_too && marks >> j & 1 && a.dh0)
-                        store_pair(a.dh0 + (int64_t)start_at(w, t + j) * a.D + ch, mul_pair(nr, both(-1.f)));
+                        store_pair(a.dh0 + (int64_t)start_at(w, nullptr, t + j) * a.D + ch,
+                                   mul_pair(nr, both(-1.f)));
                 }
             }
             if (whole) {  // the tile's results leave when all warps' are there
@@ -891,6 +948,15 @@ int count_ctas(int64_t T, int runs, int cols, int kT) {
     return n;
 }
 
+// Whether the forward's CTAs find their way through the sequences by themselves, without the setup
+// launch and its workspace: where a call's latency counts more than the scan's, which this makes 10 to
+// 20 % longer.  Calls without and with a setup launch: 252 tokens x 1024 in 4 sequences 21 and 28 us,
+// 2,048 x 1024 21 and 27, 512 x 4096 in 32 20 and 27, but 8,192 x 1024 in 24 26 either way (as graphs
+// 26 and 22) and 8,192 x 2560 69 and 60.  (The gradients have no registers left for it.)
+bool few_ones(int64_t T, int N, int cols) {
+    return T > 0 && N > 1 && N <= kFew && T * cols <= 65536;
+}
+
 // The parts of a workspace; w may be nullptr.
 size_t lay_out(char* ws, int64_t T, int N, int D, bool bwd, Plan* w, float** edges, float** part) {
     size_t n = 0;
@@ -902,7 +968,8 @@ size_t lay_out(char* ws, int64_t T, int N, int D, bool bwd, Plan* w, float** edg
     Plan s{};
     s.cols = (D + kC - 1) / kC;
     s.runs = count_runs(T, N, s.cols);
-    if (N != 1) {
+    s.few = !bwd && few_ones(T, N, s.cols);
+    if ((N > 1 && !s.few) || T == 0) {  // (a setup launch; without tokens it passes the states on)
         s.run = reinterpret_cast<int*>(take((s.runs + 1) * 4));
         s.marks = reinterpret_cast<uint32_t*>(take((T + kEdge - 1) / kEdge * 4));
         s.start_seq = reinterpret_cast<int*>(take(T * 4));
@@ -1015,8 +1082,10 @@ cudaError_t forward(const RecurrenceArgs& a, const Plan& w) {
     Tensors m{};
     if (!make_maps<S, In, IO>(m, a, false)) return cudaErrorInvalidValue;
     const int ctas = count_ctas(a.T_total, w.runs, w.cols, S::kT);
-    return launch_scan(scan_kernel<In, IO, kTok, kStages, kOnlyEdges>, "recurrence_kernel",
-                       kStages * S::kBytes, ctas, a, w, m);
+    auto kernel = scan_kernel<In, IO, kTok, kStages, kOnlyEdges, false>;
+    if constexpr (!kOnlyEdges)
+        if (w.few) kernel = scan_kernel<In, IO, kTok, kStages, false, true>;
+    return launch_scan(kernel, "recurrence_kernel", kStages * S::kBytes, ctas, a, w, m);
 }
 
 template <typename In, typename IO>

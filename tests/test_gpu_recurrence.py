@@ -151,6 +151,37 @@ def test_no_tokens(kda, N, T):
     assert torch.equal(got["dh0"], s["dh"]) and float(got["dA_log"].abs().sum()) == 0.0
 
 
+@pytest.mark.parametrize("lengths", [
+    [0, 3] * 15 + [7], [0, 3] * 16, [0, 3] * 16 + [7], [5] * 31 + [0], [5] * 32 + [0],
+    [1500, 0, 1200, 900, 0, 2000], [0] * 30 + [4000, 1], [1200] * 33])
+def test_few_and_more_sequences(kda, lengths):
+    """On both sides of the numbers that the forward finds its way through by itself, in several runs
+    and in one, with empty sequences anywhere."""
+    _check(kda, _inputs(24, lengths, 72, "bf16"))
+
+
+@pytest.mark.parametrize("N", [2, 32, 33])
+def test_equal_sequences(kda, N):
+    import torch
+    s = _inputs(25, [40] * N, 64, "f32")
+    want = [*_fwd(kda, s), *_bwd(kda, s).values()]
+    s["cu"] = None
+    got = [*_fwd(kda, s, N=N), *_bwd(kda, s, N=N).values()]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_one_sequence_without_tokens(kda):
+    import torch
+    s = _inputs(8, [0], 64, "bf16")
+    for cu in (s["cu"], None):
+        s["cu"] = cu
+        y, h = _fwd(kda, s)
+        assert y.shape == (0, 64) and torch.equal(h, s["h0"])
+        got = _bwd(kda, s)
+        assert torch.equal(got["dh0"], s["dh"]) and float(got["dA_log"].abs().sum()) == 0.0
+
+
 def test_infinite_gates(kda):
     """z = -inf keeps the state, z = +inf decays it by e^g_min, i = -inf takes nothing in."""
     import recurrence_ref as R
