@@ -28,8 +28,12 @@
 //
 // Sequences: a setup launch finds the tokens with which sequences start and end, 8 at a time, and
 // cuts the batch into runs (one sequence needs none of it, and short forwards of a few do it
-// themselves).  Where a sequence starts, a map is constant: P's sign bit says so (P >= 0 otherwise), and
-// it is selected, not multiplied by zero, so that nothing that is not finite crosses.
+// themselves).  Where a sequence starts, a map is constant, which is said by a P that is none, and
+// selected, not multiplied by zero, so that nothing that is not finite crosses.
+//
+// Of several tokens' decay P next to one, P - 1 is kept and composed (a number <= 0), from the tokens'
+// summed gates: P's rounding, the same again and again under gates that are alike, would add up over
+// the memory (5.7e-6 of a state that remembers 1,600 tokens, now WITHP).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -309,24 +313,24 @@ __global__ void __launch_bounds__(256) setup_kernel(const RecurrenceArgs a, cons
 
 // ------------------------------------------------------------------ scan --
 
-// The maps of a thread's two channels: (P.x, P.y, H.x, H.y), P's sign bit set where the map is
-// constant.
-__device__ __forceinline__ bool constant(float P) { return __float_as_int(P) < 0; }
-
-__device__ __forceinline__ float2 apply(float4 m, float2 h) {
-    const float2 r = fma_pair(make_float2(m.x, m.y), h, make_float2(m.z, m.w));
-    return constant(m.x) ? make_float2(m.z, m.w) : r;
+// A channel's map (p, H).  p stands for P: P - 1 where that is -1/2 or more, P itself, or the next to
+// nothing in place of zero, below; kConstant where the map is constant.
+constexpr float kConstant = 2.f, kNothing = 1.2e-38f;
+__device__ __forceinline__ bool constant(float p) { return p > 1.f; }
+__device__ __forceinline__ float apply(float2 m, float h) {
+    float r = m.y;
+    if (!constant(m.x)) r = fmaf(m.x, h, m.y);
+    if (m.x <= 0.f) r += h;
+    return r;
 }
-// The map that applies `before` and then m.
-__device__ __forceinline__ float4 after(float4 m, float4 before) {
-    const float2 P = mul_pair(make_float2(m.x, m.y), make_float2(before.x, before.y));
-    const float2 H = fma_pair(make_float2(m.x, m.y), make_float2(before.z, before.w),
-                          make_float2(m.z, m.w));
-    if (constant(m.x)) return m;
-    if (constant(before.x)) return make_float4(-0.f, -0.f, H.x, H.y);
-    return make_float4(P.x, P.y, H.x, H.y);
+// p of tokens without a cut, whose gates add up to w.
+__device__ __forceinline__ float decay(float w, float near) {
+    return w >= -0.6f ? near : fmaxf(ex2_approx(w * kLog2e), kNothing);
 }
-__device__ __forceinline__ float4 identity() { return make_float4(1.f, 1.f, 0.f, 0.f); }
+__device__ __forceinline__ float2 decay(float2 w) {
+    const float2 near = expm1_near(w);
+    return make_float2(decay(w.x, near.x), decay(w.y, near.y));
+}
 
 __device__ __forceinline__ unsigned cluster_rank() {
     unsigned r;
@@ -345,11 +349,10 @@ __device__ __forceinline__ uint32_t place_in(const void* p, unsigned rank) {
     return at;
 }
 // Writes v there, and counts its bytes on a barrier there.
-__device__ __forceinline__ void send(uint32_t at, uint32_t done, float4 v) {
-    asm volatile(
-        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
-        "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(done)
-        : "memory");
+__device__ __forceinline__ void send(uint32_t at, uint32_t done, float2 v) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::
+                     "r"(at), "f"(v.x), "f"(v.y), "r"(done)
+                 : "memory");
 }
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -397,61 +400,72 @@ struct Steps {
     }
     __device__ __forceinline__ bool some(int k) const { return k * ctas + rank < tiles; }
     // the bytes of a step's maps from the cluster
-    __device__ __forceinline__ uint32_t bytes() const { return ctas * 32 * (uint32_t)sizeof(float4); }
+    __device__ __forceinline__ uint32_t bytes() const { return ctas * kC * (uint32_t)sizeof(float2); }
     __device__ __forceinline__ int first_token(int k) const {
         const int p = k * ctas + rank;
         return base + (kBwd ? tiles - 1 - p : p) * kT;
     }
 };
 
-// What a CTA keeps of a step's maps, in the scan's order.
+// What a CTA keeps of a step's maps, in the scan's order, by channels.
 template <int kStages>
 struct Maps {
-    float4 warps[kWarps][32];          // its warps'
-    float4 tiles[2][kMaxCluster][32];  // the cluster's tiles'; of two steps in turn
-    float2 start[kWarps][32];          // the states that its warps' tokens start from
-    float2 carry[32];                  // from step to step
+    float2 warps[kWarps][kC];          // its warps'
+    float2 tiles[2][kMaxCluster][kC];  // the cluster's tiles'; of two steps in turn
+    float start[kWarps][kC];           // the sums of its warps' gates, then the states they start from
+    float carry[kC];                   // from step to step
     int2 few[kFew];                    // a few sequences' first and last tokens (kNone: empty)
     uint64_t there[2], states, full[kStages];  // barriers: the tiles', the states, inputs are there
-};
 
-// By one warp, with the warps' maps there: sends the tile's map to the CTAs of the cluster, calls
-// meanwhile(), carries the state over the cluster's maps and leaves the warps' starts.  (Every warp
-// for itself would read most of the maps again: some 800 instructions a step more with 8 CTAs.)
-template <int kStages, typename Steps, typename Meanwhile>
-__device__ __forceinline__ void exchange(Maps<kStages>& x, const Steps& steps, int k, int lane,
-                                         bool& broken, unsigned* err, Meanwhile&& meanwhile) {
-    const int buf = k & 1;
-    float4 own[kWarps], all;
-#pragma unroll
-    for (int j = 0; j < kWarps; ++j) own[j] = x.warps[j][lane];
-    all = own[0];
-    own[0] = identity();
-#pragma unroll
-    for (int j = 1; j < kWarps; ++j) {  // own becomes the map of the warps before
-        const float4 next = after(own[j], all);
-        own[j] = all;
-        all = next;
+    // a thread's two channels of them
+    __device__ __forceinline__ void put(int turn, int lane, float2 p, float2 H) {
+        *reinterpret_cast<float4*>(&warps[turn][2 * lane]) = make_float4(p.x, H.x, p.y, H.y);
     }
+    __device__ __forceinline__ float2& states_of(int turn, int lane) {
+        return *reinterpret_cast<float2*>(&start[turn][2 * lane]);
+    }
+};
+constexpr int kCarriers = kC / 32;  // warps that exchange, a lane a channel
+
+// By the first kCarriers warps, with the warps' maps there: sends the tile's map to the CTAs of the
+// cluster, carries the state over the cluster's maps and leaves the warps' starts.  (Every warp for
+// itself would read most of the maps again, some 800 instructions a step more with 8 CTAs; by one
+// warp, two channels a lane, 65,536 x 4096 took 464 us instead of FWDUS.)
+template <int kUnroll, int kStages, typename Steps>
+__device__ __forceinline__ void exchange(Maps<kStages>& x, const Steps& steps, int k, int c,
+                                         bool& broken, unsigned* err) {
+    const int buf = k & 1;
+    float H = 0.f, sum = 0.f;
+    bool cut = false;
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) {
+        const float2 m = x.warps[j][c];
+        H = apply(m, H);
+        sum += x.start[j][c];
+        cut |= constant(m.x);
+    }
+    const float2 all = make_float2(cut ? kConstant : decay(sum, expm1_near(both(sum)).x), H);
     for (int j = 0; j < steps.ctas; ++j)
-        send(place_in(&x.tiles[buf][steps.rank][lane], j), place_in(&x.there[buf], j), all);
-    meanwhile();
+        send(place_in(&x.tiles[buf][steps.rank][c], j), place_in(&x.there[buf], j), all);
     // (the next maps for this buffer are sent when this CTA's of the next step are there, which its
     // barrier of that step precedes)
     if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, err);
-    if (lane == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
-    float2 h = k == 0 ? both(0.f) : x.carry[lane], mine = h;
-#pragma unroll
+    if (c == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
+    float h = k == 0 ? 0.f : x.carry[c], mine = h;
+#pragma unroll(kUnroll)
     for (int j = 0; j < kMaxCluster; ++j) {
         if (j >= steps.ctas) break;
         if (j == steps.rank) mine = h;
-        h = apply(x.tiles[buf][j][lane], h);
+        h = apply(x.tiles[buf][j][c], h);
     }
-    x.carry[lane] = h;
+    x.carry[c] = h;
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) x.start[j][lane] = apply(own[j], mine);
+    for (int j = 0; j < kWarps; ++j) {
+        x.start[j][c] = mine;
+        mine = apply(x.warps[j][c], mine);
+    }
     __syncwarp();
-    if (lane == 0) mbar_arrive(&x.states);
+    if (c % 32 == 0) mbar_arrive(&x.states);
 }
 
 // Before anything else: the barriers, by all threads; the caller waits for the cluster
@@ -461,7 +475,7 @@ __device__ __forceinline__ void open_maps(Maps<kStages>& x, const Tensors& m, ui
     if (threadIdx.x == 0) {
         for (int k = 0; k < kStages; ++k) mbar_init(&x.full[k], fill_count<In>(m));
         for (int k = 0; k < 2; ++k) mbar_init(&x.there[k], 1);
-        mbar_init(&x.states, 1);
+        mbar_init(&x.states, kCarriers);
         fence_mbar_init();
         for (int k = 0; k < 2; ++k) mbar_expect_tx(&x.there[k], bytes);
     }
@@ -549,12 +563,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     open_maps<In>(x, m, steps.bytes());
     Exps<S::kT> exps;
     auto load = [&](int k) {
-        if (warp == 0 && steps.some(k))
+        if (warp == kCarriers && steps.some(k))
             load_stage<S, In, IO, false>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
                                          steps.first_token(k), c0, lane, exps);
     };
     auto put = [&](int k) {
-        if (warp == 0 && steps.some(k))
+        if (warp == kCarriers && steps.some(k))
             put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
     };
     auto marks_at = [&](int k) {
@@ -582,9 +596,16 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         // if that before them were zero
         float2 c[kTok], nb[kTok], opening[kTok / kEdge] = {};
         float2 P = both(1.f), H = both(0.f);
-        if (some) {
+        if (!some) {
+            x.states_of(warp, lane) = both(0.f);
+            x.put(warp, lane, both(0.f), both(0.f));  // (what leaves a state as it is)
+        } else {
             if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
-            recurrence_steps([&](int which, int j) { return v.input(which, j); }, nl, gb, c, nb);
+            recurrence_steps([&](int which, int j) { return v.input(which, j); }, nl, gb, c, nb,
+                             [&](float2 sum) {
+                                 sum = mul_pair(sum, both(gb.g_min));
+                                 x.states_of(warp, lane) = sum;
+                             });
             if ((marks & 0xffffu) == 0u) {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
@@ -593,11 +614,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                     c[j] = P;
                     nb[j] = H;
                 }
+                x.put(warp, lane, decay(x.states_of(warp, lane)), H);
             } else {
 #pragma unroll
                 for (int j = 0; j < kTok; ++j) {
                     if (marks >> j & 1) {
-                        P = both(-0.f);  // (constant from here on)
+                        P = both(kConstant);  // (from here on)
                         H = both(0.f);
                         if (a.h0 && live) H = state_row(a.h0, start_at(w, few, t + j), a.D, ch);
                         if (j % kEdge == 0) opening[j / kEdge] = H;
@@ -607,18 +629,16 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                     c[j] = P;
                     nb[j] = H;
                 }
+                x.put(warp, lane, both(kConstant), H);
             }
         }
-        x.warps[warp][lane] = make_float4(P.x, P.y, H.x, H.y);
         __syncthreads();
-        // (the stage has been read)
-        if (warp == 0) {
-            exchange(x, steps, k, lane, broken, a.dev_err, [&] { load(k + kStages); });
-            put(k + kStages);
-        }
+        if (warp < kCarriers) exchange<kMaxCluster>(x, steps, k, threadIdx.x, broken, a.dev_err);
+        load(k + kStages);  // (the stage has been read; by another warp)
+        put(k + kStages);
         const uint32_t coming = marks_at(k + 1);
         if (!broken) broken = !mbar_wait(&x.states, k & 1, a.dev_err);
-        const float2 h = x.start[warp][lane];
+        const float2 h = x.states_of(warp, lane);
         if (some && live) {
             IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
             float* edge = a.edges + t / kEdge * a.D + ch;
@@ -674,18 +694,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     const int ch = c0 + 2 * lane;
     const int turn = kWarps - 1 - warp;  // in the scan's order
     const bool live = ch < a.D;
-    float2 dA = both(0.f);
+    __shared__ float2 sums[kThreads];  // dA_log, a thread's tokens so far (steps' sums are added up)
+    sums[threadIdx.x] = both(0.f);
     if (any) {
         const Steps<true, S::kT> steps(begin, end);
         open_maps<In>(x, m, steps.bytes());
         Exps<S::kT> exps;
         auto load = [&](int k) {
-            if (warp == 0 && steps.some(k))
+            if (warp == kCarriers && steps.some(k))
                 load_stage<S, In, IO, true>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
                                             steps.first_token(k), c0, lane, exps);
         };
         auto put = [&](int k) {
-            if (warp == 0 && steps.some(k))
+            if (warp == kCarriers && steps.some(k))
                 put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
         };
         // a step's marks, and the state that the warp's tokens start from
@@ -722,12 +743,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             // the negated factors of l in the gradients, from the states; the scan's state is -r, what
             // -l_t has from later tokens: r_{t-1} = a_t (dy_t + r_t)
             float2 c[kTok], fx[kTok], fz[kTok], fi[kTok];
-            float2 P = both(1.f), H = both(0.f);
-            if (some) {
+            float2 H = both(0.f);
+            if (!some) {
+                x.states_of(turn, lane) = both(0.f);
+                x.put(turn, lane, both(0.f), both(0.f));
+            } else {
                 if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
                 auto in = [&](int which, int j) { return v.input(which, j); };
+                auto summed = [&](float2 sum) {
+                    sum = mul_pair(sum, both(gb.g_min));
+                    x.states_of(turn, lane) = sum;
+                };
                 if ((marks & 0xffffu) == 0u)
-                    recurrence_grads(in, r, gb, edge, [](int, float2 h) { return h; }, c, fx, fz, fi);
+                    recurrence_grads(in, r, gb, edge, [](int, float2 h) { return h; }, c, fx, fz, fi, summed);
                 else
                     recurrence_grads(
                         in, r, gb, edge,
@@ -737,14 +765,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                                                  : both(0.f);
                             return h;
                         },
-                        c, fx, fz, fi);
+                        c, fx, fz, fi, summed);
                 if (marks >> 16 == 0u) {
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
-                        P = fma_pair(c[j], P, P);
                         const float2 l = fma_pair(v.dy(j), both(-1.f), H);
                         H = fma_pair(c[j], l, l);
                     }
+                    x.put(turn, lane, decay(x.states_of(turn, lane)), H);
                 } else {
 #pragma unroll
                     for (int j = kTok - 1; j >= 0; --j) {
@@ -756,20 +784,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                         const float2 l = fma_pair(v.dy(j), both(-1.f), H);
                         H = fma_pair(c[j], l, l);
                     }
-                    P = both(-0.f);
+                    x.put(turn, lane, both(kConstant), H);
                 }
             }
-            x.warps[turn][lane] = make_float4(P.x, P.y, H.x, H.y);
             if (threadIdx.x == 0) bulk_wait_read0();  // (the stage before this one is free)
             __syncthreads();
-            if (warp == 0) {
-                exchange(x, steps, k, lane, broken, a.dev_err, [&] { load(k + kAhead); });
-                put(k + kAhead);
-            }
+            if (warp < kCarriers) exchange<4>(x, steps, k, threadIdx.x, broken, a.dev_err);
+            load(k + kAhead);  // (by another warp)
+            put(k + kAhead);
             edge = edge_at(k + 1);
             const uint32_t coming = marks_at(k + 1);
             if (!broken) broken = !mbar_wait(&x.states, k & 1, a.dev_err);
-            float2 nr = x.start[turn][lane];
+            float2 nr = x.states_of(turn, lane), dA = both(0.f);
             // a token's gradients but for the state's
             auto take = [&](int j, float2 l, IO* dx, IO* dz, IO* di) {
                 const float2 g = mul_pair(l, fz[j]), z = v.finite(1, j);
@@ -808,6 +834,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                                    mul_pair(nr, both(-1.f)));
                 }
             }
+            sums[threadIdx.x] = add_pair(sums[threadIdx.x], dA);
             if (whole) {  // the tile's results leave when all warps' are there
                 fence_async_smem();
                 if (warp > 0) {
@@ -831,9 +858,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     }
     if (part == nullptr) return;
     // the CTA's dA_log: over the warps, in a fixed order
-    float2* sums = reinterpret_cast<float2*>(ring);
-    __syncthreads();
-    sums[threadIdx.x] = dA;
     __syncthreads();
     if (threadIdx.x < 32 && live) {
         float2 s = sums[lane];
@@ -915,7 +939,7 @@ __global__ void __launch_bounds__(128) step_kernel(const IO* x, int64_t x_ld, co
         auto next = [&](int j, float2 Ae, float2 he) {
             float2 cc[1], nb[1];
             recurrence_steps([&](int which, int) { return in[which][j]; },
-                             channel_rate(Ae, 0.f).neg_log2, gb, cc, nb);
+                             channel_rate(Ae, 0.f).neg_log2, gb, cc, nb, [](float2) {});
             return recurrence_next(cc[0], nb[0], he);
         };
         const float2 a = next(0, make_float2(A.x, A.y), make_float2(v.x, v.y));

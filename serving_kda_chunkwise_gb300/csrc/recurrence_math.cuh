@@ -83,19 +83,22 @@ __device__ __forceinline__ float2 rsqrt_pair(float2 d) {
 }
 
 // n tokens in steps that leave the tokens independent of each other: c[k], and the negated input
-// terms nb[k] = -b.  in(which, k): input x, z or i (0, 1, 2) of token k.
+// terms nb[k] = -b.  in(which, k): input x, z or i (0, 1, 2) of token k.  summed(the sum of the s(e^A z)).
 //   b = m s(i) x = m^2 x / sqrt(m^2 (1 + e^-i)^2): one root for m's and s(i)'s reciprocal.  (1e-37 next
 // to m^2 keeps it from zero, so that the root of 0 times infinity is not taken; an m below 3e-19 is
 // lost in it, and a s(i) below 2^-64 in the square's overflow.)
-template <int n, typename In>
+template <int n, typename In, typename Sum>
 __device__ __forceinline__ void recurrence_steps(In&& in, float2 neg_log2, const GateBound& gb,
-                                                 float2 (&c)[n], float2 (&nb)[n]) {
+                                                 float2 (&c)[n], float2 (&nb)[n], Sum&& summed) {
+    float2 sum;
 #pragma unroll
     for (int k = 0; k < n; ++k) {
         const float2 sz = rcp1_pair(ex2_pair(mul_pair(in(1, k), neg_log2)));
+        sum = k == 0 ? sz : add_pair(sum, sz);
         c[k] = expm1_near(mul_pair(sz, both(gb.scaled)));
         nb[k] = add_pair(ex2_pair(mul_pair(in(2, k), both(-kLog2e))), both(1.f));
     }
+    summed(sum);
     for (int j = gb.doublings; j > 0; --j)
 #pragma unroll
         for (int k = 0; k < n; ++k) c[k] = twice(c[k]);
@@ -114,10 +117,12 @@ __device__ __forceinline__ float2 recurrence_next(float2 c, float2 nb, float2 h)
 
 // The same for the gradients: c[k], and the negated factors of l_t = dL/dh_t in those of x, z and i.
 // before(k, h): the state before token k, where h follows from the tokens before it.
-template <int n, typename In, typename Before>
+template <int n, typename In, typename Before, typename Sum>
 __device__ __forceinline__ void recurrence_grads(In&& in, const ChannelRate& r, const GateBound& gb,
                                                  float2 h, Before&& before, float2 (&c)[n],
-                                                 float2 (&fx)[n], float2 (&fz)[n], float2 (&fi)[n]) {
+                                                 float2 (&fx)[n], float2 (&fz)[n], float2 (&fi)[n],
+                                                 Sum&& summed) {
+    float2 sum;
 #pragma unroll
     for (int k = 0; k < n; ++k) {
         const float2 ez = ex2_pair(mul_pair(in(1, k), r.neg_log2));
@@ -126,11 +131,13 @@ __device__ __forceinline__ void recurrence_grads(In&& in, const ChannelRate& r, 
         // 1 - s = e^{-..} s, the exponential limited so that it stays a number where s is zero
         const float2 oz = mul_pair(make_float2(fminf(ez.x, 3e38f), fminf(ez.y, 3e38f)), sz);
         const float2 oi = mul_pair(make_float2(fminf(ei.x, 3e38f), fminf(ei.y, 3e38f)), si);
+        sum = k == 0 ? sz : add_pair(sum, sz);
         c[k] = expm1_near(mul_pair(sz, both(gb.scaled)));
         fx[k] = si;
         fz[k] = mul_pair(mul_pair(r.rate_g, sz), oz);
         fi[k] = oi;
     }
+    summed(sum);
     for (int j = gb.doublings; j > 0; --j)
 #pragma unroll
         for (int k = 0; k < n; ++k) c[k] = twice(c[k]);

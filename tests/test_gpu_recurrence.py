@@ -171,6 +171,56 @@ def test_equal_sequences(kda, N):
         assert torch.equal(a, b)
 
 
+def test_long_memory_of_alike_gates(kda):
+    """Gates that are alike make the same rounding again and again: a state that remembers 600 to 1,600
+    tokens is as exact as its gates.  c = e^g - 1 is off by 3.3e-7 (polynomial) + 2.4e-7 (exponential
+    and reciprocal) + 6.6e-7 (the exponential's argument, up to 13 with a step of 2^-20, and the factor
+    log2(e)) at most, the state by one and a half times that, and its own roundings, which are not
+    alike, by 6e-8 sqrt(1600 / 16): 2.5e-6 (one rounding of the decay every 8 tokens: 5e-6)."""
+    import torch
+    T, D = 8192, 128
+    z = torch.linspace(-9, -8, D, device="cuda").expand(T, D).contiguous()
+    x = torch.randn(T, D, generator=torch.Generator("cuda").manual_seed(26), device="cuda")
+    i, A = torch.zeros_like(x), torch.zeros(D, device="cuda")
+    y, _ = kda.recurrence_fwd(x, z, i, A, G_MIN)
+    g = G_MIN * torch.sigmoid(z[0].double())
+    a, b = g.exp(), (-torch.expm1(2 * g)).sqrt() * 0.5
+    want, h = torch.empty(T, D, dtype=torch.float64, device="cuda"), 0.0
+    for t in range(T):
+        want[t] = h = a * h + b * x[t].double()
+    off = (y.double() - want).norm(dim=0) / want.norm(dim=0)
+    assert float(off.max()) <= 2.5e-6
+    # and the rate's gradient, a sum with a hundredth of its terms' size left
+    dy = torch.randn(T, D, generator=torch.Generator("cuda").manual_seed(27), device="cuda")
+    got = kda.recurrence_bwd(x, z, i, A, G_MIN, dy)
+    before = torch.cat([torch.zeros(1, D, dtype=torch.float64, device="cuda"), want[:-1]])
+    lam, total = torch.zeros(D, dtype=torch.float64, device="cuda"), 0.0
+    s = torch.sigmoid(z[0].double())
+    size = 0.0
+    for t in range(T - 1, -1, -1):
+        lam = dy[t].double() + lam
+        dz = lam * (a * before[t] - a * a / (2 * b) * 0.5 * x[t].double()) * g * (1 - s)
+        total, size = total + dz * z[t].double(), size + (dz * z[t].double()).abs()
+        lam = a * lam
+    assert float(((got["dA_log"].double() - total).abs() / size).max()) <= 2.5e-6
+
+
+def test_outlier_decays(kda):
+    """After a token of 1e6 that a fast channel forgets at once, the state is as exact as without it."""
+    import torch
+    T, D = 200, 64
+    x = torch.randn(T, D, generator=torch.Generator("cuda").manual_seed(28), device="cuda")
+    z, i, A = torch.full_like(x, 3.0), torch.zeros_like(x), torch.zeros(D, device="cuda")
+    big = x.clone()
+    big[[5, 70, 127, 130]] = 1e6
+    want, h = kda.recurrence_fwd(x, z, i, A, G_MIN)
+    got, h2 = kda.recurrence_fwd(big, z, i, A, G_MIN)
+    # e^-4.76 a token: 1e6 is below 2^-24 after seven
+    for t in (*range(14, 70), *range(79, 127), *range(139, T)):
+        assert float((got[t] - want[t]).abs().max()) <= 1e-6
+    assert float((h - h2).abs().max()) <= 1e-6
+
+
 def test_one_sequence_without_tokens(kda):
     import torch
     s = _inputs(8, [0], 64, "bf16")
