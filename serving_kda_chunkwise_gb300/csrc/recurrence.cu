@@ -7,24 +7,25 @@
 // Both are scans of affine maps (P, H): h -> P h + H.  A cluster of CTAs takes 64 channels along a
 // run, some consecutive sequences.  In a step each of its CTAs has a tile of 64 or 128 tokens: each of
 // eight warps holds 8 or 16 tokens, a lane two channels, and leaves its tokens' map in shared memory.
-// One warp composes the maps, sends the tile's to every CTA of the cluster (stores into distributed
-// shared memory that count their bytes on a barrier there) and carries the state over the cluster's
-// maps; then every warp goes over its tokens again, in registers, and writes.  So inputs are read
-// once (by the copy engine, steps ahead), results written once, in rows of 128 bytes (bf16), and no
-// cluster waits for another.  Ways that were slower at 65,536 x 4096 (now 436 us): a look-back over
-// tiles by messages in memory, 890 us; columns of 16 channels without clusters, 715 us, for the copies
-// of 32-byte rows; 8 tokens a warp instead of 16, 531 us; CTAs of 4 or 16 warps, 580 and 880 us.
+// Two warps, a lane a channel, compose the maps, send the tile's to every CTA of the cluster (stores
+// into distributed shared memory that count their bytes on a barrier there) and carry the state over
+// the cluster's maps; then every warp goes over its tokens again, in registers, and writes.  So inputs
+// are read once (by the copy engine, steps ahead), results written once, in rows of 128 bytes (bf16),
+// and no cluster waits for another.  Ways that were slower at 65,536 x 4096 (now 449 us): a look-back
+// over tiles by messages in memory, 890 us; columns of 16 channels without clusters, 715 us, for the
+// copies of 32-byte rows; 8 tokens a warp instead of 16, 531 us; CTAs of 4 or 16 warps, 580 and 880 us.
 //
 // The gradients go over the tiles backwards.  A thread's states come from the edges, the state that
 // every 8th token starts from, which the forward writes on request; without them a forward that
 // writes nothing else runs first.  So the factors of l_t in the gradients are formed once, before
 // the scan, and stay in registers until l_t is known (which is why a warp has 8 tokens).
 //
-// Bound by instructions, and by the clusters' being 256 CTAs for 152 SMs: the forward of 65,536 x 4096
-// in bf16 436 us, 4.9 TB/s (its special functions alone would be 190 us, its memory 322); gradients
-// from edges of 32,768 x 4096 455 us, 120 instructions for two channels of a token; from 8-bit inputs
-// of 65,536 x 2048 255 us for the edges and 545 us (1,610 with 12 bytes of spilled registers: tiles
-// leave the first-level cache nothing, so no kernel here may spill).
+// Bound by instructions (two a cycle and SM, of which the pairs' take two cycles), by the exchange
+// between a step's two passes, and by the clusters' being 256 CTAs for 152 SMs: the forward of
+// 65,536 x 4096 in bf16 449 us, 4.8 TB/s (its special functions alone would be 190 us, its memory 322);
+// gradients from edges of 32,768 x 4096 435 us, 120 instructions for two channels of a token; from
+// 8-bit inputs of 65,536 x 2048 260 us for the edges and 525 us (1,610 with 12 bytes of spilled
+// registers: tiles leave the first-level cache nothing, so no kernel here may spill).
 //
 // Sequences: a setup launch finds the tokens with which sequences start and end, 8 at a time, and
 // cuts the batch into runs (one sequence needs none of it, and short forwards of a few do it
@@ -33,7 +34,7 @@
 //
 // Of several tokens' decay P next to one, P - 1 is kept and composed (a number <= 0), from the tokens'
 // summed gates: P's rounding, the same again and again under gates that are alike, would add up over
-// the memory (5.7e-6 of a state that remembers 1,600 tokens, now WITHP).
+// the memory (5.7e-6 of a state that remembers 1,600 tokens, now 1e-6; that is 4 % of the forward's time).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -430,8 +431,8 @@ constexpr int kCarriers = kC / 32;  // warps that exchange, a lane a channel
 // By the first kCarriers warps, with the warps' maps there: sends the tile's map to the CTAs of the
 // cluster, carries the state over the cluster's maps and leaves the warps' starts.  (Every warp for
 // itself would read most of the maps again, some 800 instructions a step more with 8 CTAs; by one
-// warp, two channels a lane, 65,536 x 4096 took 464 us instead of FWDUS.)
-template <int kUnroll, int kStages, typename Steps>
+// warp, two channels a lane, 65,536 x 4096 took 464 us instead of 449.)
+template <int kStages, typename Steps>
 __device__ __forceinline__ void exchange(Maps<kStages>& x, const Steps& steps, int k, int c,
                                          bool& broken, unsigned* err) {
     const int buf = k & 1;
@@ -452,7 +453,7 @@ __device__ __forceinline__ void exchange(Maps<kStages>& x, const Steps& steps, i
     if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, err);
     if (c == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
     float h = k == 0 ? 0.f : x.carry[c], mine = h;
-#pragma unroll(kUnroll)
+#pragma unroll 4
     for (int j = 0; j < kMaxCluster; ++j) {
         if (j >= steps.ctas) break;
         if (j == steps.rank) mine = h;
@@ -633,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
             }
         }
         __syncthreads();
-        if (warp < kCarriers) exchange<kMaxCluster>(x, steps, k, threadIdx.x, broken, a.dev_err);
+        if (warp < kCarriers) exchange(x, steps, k, threadIdx.x, broken, a.dev_err);
         load(k + kStages);  // (the stage has been read; by another warp)
         put(k + kStages);
         const uint32_t coming = marks_at(k + 1);
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             }
             if (threadIdx.x == 0) bulk_wait_read0();  // (the stage before this one is free)
             __syncthreads();
-            if (warp < kCarriers) exchange<4>(x, steps, k, threadIdx.x, broken, a.dev_err);
+            if (warp < kCarriers) exchange(x, steps, k, threadIdx.x, broken, a.dev_err);
             load(k + kAhead);  // (by another warp)
             put(k + kAhead);
             edge = edge_at(k + 1);
@@ -870,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
 }
 
 // dA_log[c] = the sum of the CTAs' parts in a fixed order: a CTA takes 32 channels, its 32 warps every
-// 32nd part.
+// 32nd part (4 us, latency).
 __global__ void __launch_bounds__(1024) rate_kernel(const float* part, int parts, int D, float* dA) {
     __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
@@ -892,7 +893,8 @@ __global__ void __launch_bounds__(1024) rate_kernel(const float* part, int parts
 
 // ------------------------------------------------------- the single token --
 
-// Four channels a thread.
+// Four channels a thread; bound by memory, or by its launch: 256 requests x 4096 3.4 us, 4.9 TB/s with
+// the states in the second-level cache, of a call of 14.
 __device__ __forceinline__ float4 four(const __nv_bfloat16* p) {
     const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
