@@ -25,7 +25,7 @@
 // 65,536 x 4096 in bf16 449 us, 4.8 TB/s (its special functions alone would be 190 us, its memory 322);
 // gradients from edges of 32,768 x 4096 435 us, 120 instructions for two channels of a token; from
 // 8-bit inputs of 65,536 x 2048 260 us for the edges and 525 us (1,610 with 12 bytes of spilled
-// registers: tiles leave the first-level cache nothing, so no kernel here may spill).
+// registers: tiles leave the first-level cache nothing, so nothing may spill within the steps).
 //
 // Sequences: a setup launch finds the tokens with which sequences start and end, 8 at a time, and
 // cuts the batch into runs (one sequence needs none of it, and short forwards of a few do it
@@ -276,11 +276,15 @@ __global__ void __launch_bounds__(256) setup_kernel(const RecurrenceArgs a, cons
     for (int64_t g = id; g * kEdge < a.T_total; g += all) {
         const int64_t t0 = g * kEdge;
         uint32_t bits = 0;
-        for (int n = at(t0); n < a.N && (bits == 0 || first(n) < t0 + kEdge); ++n) {
+        // (of empty sequences at a token the search passes to the last; so a token takes two turns at most)
+        int n = at(t0);
+        for (int turn = 0; turn < 3 * kEdge && n < a.N && (bits == 0 || first(n) < t0 + kEdge);
+             ++turn, ++n) {
             int64_t b, e;
             seq_range(a.cu_seqlens, n, a.N, a.T_total, nullptr, b, e);
             if (b >= e) {
                 if (first(n) >= t0 + kEdge) break;
+                n = max(n, at(first(n)) - 1);
                 continue;
             }
             if (b >= t0 && b < t0 + kEdge) {
@@ -400,6 +404,8 @@ struct Steps {
         count = (tiles + ctas - 1) / ctas;
     }
     __device__ __forceinline__ bool some(int k) const { return k * ctas + rank < tiles; }
+    // this CTA's tiles
+    __device__ __forceinline__ int own() const { return (tiles - rank + ctas - 1) / ctas; }
     // the bytes of a step's maps from the cluster
     __device__ __forceinline__ uint32_t bytes() const { return ctas * kC * (uint32_t)sizeof(float2); }
     __device__ __forceinline__ int first_token(int k) const {
@@ -482,6 +488,17 @@ __device__ __forceinline__ void open_maps(Maps<kStages>& x, const Tensors& m, ui
     }
     __syncthreads();
     cluster_arrive();
+}
+
+// After the last step, by all threads: where a wait ran out, for the copies on their way all the same
+// (with a limit), and until nobody in the cluster can send here.
+template <int kStages>
+__device__ __forceinline__ void close_maps(Maps<kStages>& x, int loads, bool broken, unsigned* err) {
+    if (__syncthreads_or(broken) && threadIdx.x < kStages && loads > (int)threadIdx.x)
+        mbar_wait(&x.full[threadIdx.x], (loads - 1 - (int)threadIdx.x) / kStages & 1, err);
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
 }
 
 // The cluster's run and first channel; false where it has nothing to do.  With `few` a CTA reads the
@@ -672,9 +689,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         }
         marks = coming;
     }
-    __syncwarp();
-    cluster_arrive();  // (a CTA stays until nobody can send to it)
-    cluster_wait();
+    close_maps(x, steps.own(), broken, a.dev_err);
 }
 
 // -------------------------------------------------------------- gradients --
@@ -853,9 +868,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             marks = coming;
         }
         if (threadIdx.x == 0) bulk_wait0();
-        __syncwarp();
-        cluster_arrive();  // (a CTA stays until nobody can send to it)
-        cluster_wait();
+        close_maps(x, steps.own(), broken, a.dev_err);
     }
     if (part == nullptr) return;
     // the CTA's dA_log: over the warps, in a fixed order

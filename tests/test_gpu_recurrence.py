@@ -160,6 +160,31 @@ def test_few_and_more_sequences(kda, lengths):
     _check(kda, _inputs(24, lengths, 72, "bf16"))
 
 
+def test_very_many_empty_sequences(kda):
+    """300,000 empty sequences at a token, in front of the first and behind the last one."""
+    import torch
+    s, n = _inputs(29, [40, 9, 25], 72, "f32"), 300000
+    want = [*_fwd(kda, s), *_bwd(kda, s).values()]
+    some = torch.tensor([n, 2 * n + 1, 3 * n + 2], device="cuda")
+    lengths = torch.zeros(4 * n + 3, dtype=torch.int64, device="cuda")
+    lengths[some] = torch.tensor(s["lengths"], device="cuda")
+    cu = torch.cat([lengths[:1] * 0, lengths.cumsum(0)]).to(torch.int32)
+    states = [torch.randn(4 * n + 3, 72, device="cuda") for _ in range(2)]
+    for t, part in zip(states, (s["h0"], s["dh"])):
+        t[some] = part
+    s.update(cu=cu, h0=states[0], dh=states[1])
+    got = [*_fwd(kda, s), *_bwd(kda, s).values()]
+    kda.device_status()
+    for k, (a, b) in enumerate(zip(got, want)):
+        empty = dict(((1, 0), (6, 1))).get(k)  # final states, and the first ones' gradients
+        if empty is None:
+            assert torch.equal(a, b), k
+        else:
+            assert torch.equal(a[some], b), k
+            states[empty][some] = a[some]
+            assert torch.equal(a, states[empty]), k
+
+
 @pytest.mark.parametrize("N", [2, 32, 33])
 def test_equal_sequences(kda, N):
     import torch
