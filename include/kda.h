@@ -425,7 +425,7 @@ kda_status_t kda_recurrence_step(const void *x, int64_t x_ld, const void *z, int
  * with max |x| 2^-e < 127.5, and each is kept as the integer next to x 2^-e (halves to even, limited
  * to [-127, 127]).  Each step is exact in binary, so codes and exponents are those of the formula.
  *   x     : [T, D] io_dt with a token stride of x_ld elements (a multiple of 16 bytes, >= D)
- *   codes : [T, D] int8 (written)       exps : [ceil(D / 64), T] int8 (written)
+ *   codes : [T, D] int8 (written)       exps : [ceil(D / 64), T] int8 (written; no alignment)
  * A group of zeros has e = -127; one that holds an infinity or a NaN has e = -128, which stands for
  * NaN in all its channels (its codes are 0).  D is a multiple of 8.
  */
