@@ -11,6 +11,7 @@ relative of each product's terms).  Where 1 - e^{2g} is below 1e-37, next to fp3
 number 1.2e-38, its root m is taken as zero; so is a gate's value below 2^-126, where 1 - e^{2g} is
 below 2 |g_min| 2^-126 (1.2e-37 for g_min = -5).  So m is off by at most the root of the larger of the
 two, which every product with m (or with g / m, which is -m / 2 there) inherits.
+e^g is one plus e^g - 1, off by 2^-24 too: within eps of itself down to e^-5, so for g_min >= -5.
 """
 import torch
 
