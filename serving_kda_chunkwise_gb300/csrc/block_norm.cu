@@ -391,10 +391,11 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const __grid_constant_
             load(t + (int64_t)(stages - 1) * gridDim.x, s == 0 ? stages - 1 : s - 1);
         const float inv_y = a.post_norm ? rsqrtf(v[0] * over_D + a.eps) : 1.f;
         const float inv_r = rsqrtf(v[1] * over_D + a.eps);
-        // G = dr + inv_r u - back r
-        const float back = inv_r * inv_r * inv_r * (v[2] * over_D);
-        const float dot =
-            a.post_norm ? -inv_y * inv_y * inv_y * over_D * (v[3] + inv_r * v[4] - back * v[5]) : 0.f;
+        // the mean of u r^, and the sum of G q and then the mean of w_post dn y^ from it (each factor next
+        // to the sum that it brings to size: a power of inv alone would leave fp32's range)
+        const float mean_r = inv_r * over_D * v[2];
+        const float mean_y =
+            a.post_norm ? inv_y * over_D * (v[3] + inv_r * (v[4] - mean_r * (inv_r * v[5]))) : 0.f;
 #pragma unroll
         for (int g = 0; g < kG; ++g) {
             const int c = channel(g);
@@ -412,9 +413,9 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const __grid_constant_
             read(rp + c, r);
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) {
-                const float2 u = mul_pair(x[e], wx[e]);
-                G[e] = fma_pair(r[e], both(-back), fma_pair(u, both(inv_r), G[e]));
-                dwx[g][e] = fma_pair(mul_pair(x[e], r[e]), both(inv_r), dwx[g][e]);
+                const float2 u = mul_pair(x[e], wx[e]), rh = mul_pair(r[e], both(inv_r));
+                G[e] = fma_pair(fma_pair(rh, both(-mean_r), u), both(inv_r), G[e]);
+                dwx[g][e] = fma_pair(x[e], rh, dwx[g][e]);
             }
             store(static_cast<R*>(a.dr_in) + o, G);
             float2 y[kPairs];
@@ -441,8 +442,9 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const __grid_constant_
                 dws[g][e] = fma_pair(G[e], n, dws[g][e]);
                 dwn[g][e] = fma_pair(dn, yh, dwn[g][e]);
                 if (a.gate) x[e] = mul_pair(mul_pair(dn, n), other[e]);
-                G[e] = a.post_norm ? fma_pair(y[e], both(dot), mul_pair(mul_pair(dn, wn[e]), both(inv_y)))
-                                   : dn;
+                G[e] = a.post_norm
+                           ? mul_pair(fma_pair(yh, both(-mean_y), mul_pair(dn, wn[e])), both(inv_y))
+                           : dn;
             }
             store(static_cast<IO*>(a.dy) + o, G);
             if (a.gate) store(static_cast<IO*>(a.dgate) + o, x);
