@@ -467,9 +467,10 @@ kda_status_t kda_block_norm(const void *y, const void *gate, const void *r, cons
  *   dscale, dw_post, dw_pre : [D] fp32, summed over tokens, or NULL when not wanted
  *   workspace : device scratch of kda_block_norm_bwd_workspace_size(D) bytes; not needed when none
  *            of the three sums is wanted
- * A row's magnitude is free as long as the sums of y^2, r_out^2 and (scale Sigmoid(gate) w_post y)^2 over
- * it, and of the last one's root times r_out, are normal numbers of fp32 or zero (the first two in
- * kda_block_norm as well): from about 1e-17 to 1e17.  eps = 0 is allowed; a row of zeros then has no norm.
+ * A row's magnitude is free as long as the sums over it of y^2, r_out^2, q^2 and q r_out, with
+ * q = scale Sigmoid(gate) w_post y, are normal numbers of fp32 or zero (the first two in
+ * kda_block_norm as well): from about 1e-17 to 1e17.  eps = 0 is allowed; a row of zeros then has
+ * no norm.
  * No output may overlap an input.  Deterministic.
  */
 size_t kda_block_norm_bwd_workspace_size(int D);

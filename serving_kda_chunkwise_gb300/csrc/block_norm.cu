@@ -302,8 +302,10 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const __grid_constant_
         fence_mbar_init();
     }
     clear(sums);
+    int loads = 0;  // thread 0's
     auto load = [&](int64_t t, int s) {
         if (threadIdx.x != 0 || t >= a.T) return;
+        ++loads;
         char* st = ring + s * at.bytes;
         mbar_expect_tx(&full[s], at.bytes);
         const int64_t o = t * D;
@@ -458,6 +460,11 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const __grid_constant_
             turn ^= 1;
         }
     }
+    // a wait that ran out: the copies that are still on their way come first (with a limit), for the
+    // shared memory is another kernel's afterwards
+    if (threadIdx.x == 0 && broken)
+        for (s = 0; s < stages; ++s)
+            if (const int fills = ring_fills(loads, s, stages)) mbar_wait(&full[s], fills - 1 & 1, err);
     if (part == nullptr) return;
 #pragma unroll
     for (int g = 0; g < kG; ++g) {

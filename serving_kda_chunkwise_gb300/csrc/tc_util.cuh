@@ -78,6 +78,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, unsign
     return true;
 }
 
+// Copies that went into one stage of a ring that `loads` copies have gone into in turn.  The last of
+// them completes the phase of parity (fills - 1) & 1 of that stage's barrier.
+__host__ __device__ inline int ring_fills(int loads, int stage, int stages) {
+    return (loads - stage + stages - 1) / stages;
+}
+
 // As mbar_wait, but also gives up (returning false) once *abort is set by another thread;
 // a wait that runs out sets *abort itself.
 __device__ __forceinline__ bool mbar_wait_ab(uint64_t* bar, uint32_t parity, unsigned* err,
