@@ -456,8 +456,10 @@ __device__ __forceinline__ void exchange(Maps<kStages>& x, const Steps& steps, i
         send(place_in(&x.tiles[buf][steps.rank][c], j), place_in(&x.there[buf], j), all);
     // (the next maps for this buffer are sent when this CTA's of the next step are there, which its
     // barrier of that step precedes)
-    if (!broken) broken = !mbar_wait(&x.there[buf], k / 2 & 1, err);
-    if (c == 0) mbar_expect_tx(&x.there[buf], steps.bytes());
+    if (!mbar_wait(&x.there[buf], k / 2 & 1, err))
+        broken = true;
+    else if (c == 0)
+        mbar_expect_tx(&x.there[buf], steps.bytes());
     float h = k == 0 ? 0.f : x.carry[c], mine = h;
 #pragma unroll 4
     for (int j = 0; j < kMaxCluster; ++j) {
@@ -490,12 +492,23 @@ __device__ __forceinline__ void open_maps(Maps<kStages>& x, const Tensors& m, ui
     cluster_arrive();
 }
 
-// After the last step, by all threads: where a wait ran out, for the copies on their way all the same
-// (with a limit), and until nobody in the cluster can send here.
-template <int kStages>
-__device__ __forceinline__ void close_maps(Maps<kStages>& x, int loads, bool broken, unsigned* err) {
-    if (__syncthreads_or(broken) && threadIdx.x < kStages && loads > (int)threadIdx.x)
-        mbar_wait(&x.full[threadIdx.x], (loads - 1 - (int)threadIdx.x) / kStages & 1, err);
+// After the last step, by all threads, until nobody in the cluster can send here.  Where a wait ran out,
+// a CTA leaves the steps at the next barrier, step k (it fills no stage and arms no barrier whose phase it
+// has not seen end), and waits first for what is on its way all the same, with limits: the last fills
+// of the stages, and the maps of step k, which is the last that other CTAs can send without its own.
+template <int kStages, typename Steps>
+__device__ __forceinline__ void close_maps(Maps<kStages>& x, const Steps& steps, int k, int ahead,
+                                           bool broken, unsigned* err) {
+    if (__syncthreads_or(broken)) {
+        const int s = threadIdx.x;
+        if (s < kStages) {
+            if (const int fills = ring_fills(min(k + ahead, steps.own()), s, kStages))
+                mbar_wait(&x.full[s], fills - 1 & 1, err);
+        } else if (s == 32) {
+            for (int j = max(k - 1, 0); j <= k && j < steps.count; ++j)
+                mbar_wait(&x.there[j & 1], j / 2 & 1, err);
+        }
+    }
     __syncthreads();
     cluster_arrive();
     cluster_wait();
@@ -579,15 +592,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
     const bool live = ch < a.D;
     const Steps<false, S::kT> steps(begin, end);
     open_maps<In>(x, m, steps.bytes());
-    Exps<S::kT> exps;
-    auto load = [&](int k) {
-        if (warp == kCarriers && steps.some(k))
-            load_stage<S, In, IO, false>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
-                                         steps.first_token(k), c0, lane, exps);
-    };
-    auto put = [&](int k) {
-        if (warp == kCarriers && steps.some(k))
-            put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
+    bool broken = false;  // (a wait that ran out)
+    auto fill = [&](int k) {
+        if (warp != kCarriers || !steps.some(k)) return;
+        char* const st = ring + k % kStages * S::kBytes;
+        uint64_t* const full = &x.full[k % kStages];
+        Exps<S::kT> exps;
+        load_stage<S, In, IO, false>(a, m, st, full, steps.first_token(k), c0, lane, exps);
+        put_exps<S, In>(st, full, lane, exps);
     };
     auto marks_at = [&](int k) {
         return steps.some(k)
@@ -595,17 +607,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                    : 0u;
     };
 #pragma unroll
-    for (int k = 0; k < kStages; ++k) {
-        load(k);
-        put(k);
-    }
+    for (int k = 0; k < kStages; ++k) fill(k);
     const float2 nl =
         channel_rate(live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), 0.f).neg_log2;
-    bool broken = false;  // (a wait that ran out: the ones after are not taken, so that all ends)
     __syncwarp();
     cluster_wait();
     uint32_t marks = marks_at(0);
-    for (int k = 0; k < steps.count; ++k) {
+    int k = 0;
+    for (; k < steps.count; ++k) {
         const int s = k % kStages;
         const View<S, In, IO> v{ring + s * S::kBytes, nullptr, warp, lane};
         const int64_t t = steps.first_token(k) + warp * kTok;
@@ -618,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
             x.states_of(warp, lane) = both(0.f);
             x.put(warp, lane, both(0.f), both(0.f));  // (what leaves a state as it is)
         } else {
-            if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
+            if (!mbar_wait(&x.full[s], k / kStages & 1, a.dev_err)) broken = true;
             recurrence_steps([&](int which, int j) { return v.input(which, j); }, nl, gb, c, nb,
                              [&](float2 sum) {
                                  sum = mul_pair(sum, both(gb.g_min));
@@ -650,12 +659,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
                 x.put(warp, lane, both(kConstant), H);
             }
         }
-        __syncthreads();
+        if (__syncthreads_or(broken)) break;
         if (warp < kCarriers) exchange(x, steps, k, threadIdx.x, broken, a.dev_err);
-        load(k + kStages);  // (the stage has been read; by another warp)
-        put(k + kStages);
+        fill(k + kStages);  // (the stage has been read; by another warp)
         const uint32_t coming = marks_at(k + 1);
-        if (!broken) broken = !mbar_wait(&x.states, k & 1, a.dev_err);
+        if (!mbar_wait(&x.states, k & 1, a.dev_err)) broken = true;
         const float2 h = x.states_of(warp, lane);
         if (some && live) {
             IO* y = static_cast<IO*>(a.y) + t * a.D + ch;
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(
         }
         marks = coming;
     }
-    close_maps(x, steps.own(), broken, a.dev_err);
+    close_maps(x, steps, k, kStages, broken, a.dev_err);
 }
 
 // -------------------------------------------------------------- gradients --
@@ -715,15 +723,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
     if (any) {
         const Steps<true, S::kT> steps(begin, end);
         open_maps<In>(x, m, steps.bytes());
-        Exps<S::kT> exps;
-        auto load = [&](int k) {
-            if (warp == kCarriers && steps.some(k))
-                load_stage<S, In, IO, true>(a, m, ring + k % kStages * S::kBytes, &x.full[k % kStages],
-                                            steps.first_token(k), c0, lane, exps);
-        };
-        auto put = [&](int k) {
-            if (warp == kCarriers && steps.some(k))
-                put_exps<S, In>(ring + k % kStages * S::kBytes, &x.full[k % kStages], lane, exps);
+        bool broken = false;
+        auto fill = [&](int k) {
+            if (warp != kCarriers || !steps.some(k)) return;
+            char* const st = ring + k % kStages * S::kBytes;
+            uint64_t* const full = &x.full[k % kStages];
+            Exps<S::kT> exps;
+            load_stage<S, In, IO, true>(a, m, st, full, steps.first_token(k), c0, lane, exps);
+            put_exps<S, In>(st, full, lane, exps);
         };
         // a step's marks, and the state that the warp's tokens start from
         auto marks_at = [&](int k) {
@@ -738,18 +745,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                        : both(0.f);
         };
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            load(k);
-            put(k);
-        }
+        for (int k = 0; k < kAhead; ++k) fill(k);
         const ChannelRate r = channel_rate(
             live ? *reinterpret_cast<const float2*>(a.A_log + ch) : both(0.f), gb.g_min);
         float2 edge = edge_at(0);
-        bool broken = false;
         __syncwarp();
         cluster_wait();
         uint32_t marks = marks_at(0);
-        for (int k = 0; k < steps.count; ++k) {
+        int k = 0;
+        for (; k < steps.count; ++k) {
             const int s = k % kStages;
             char* const st = ring + s * S::kBytes;
             const View<S, In, IO> v{st, S::kInPlace ? st : ring + kStages * S::kBytes, warp, lane};
@@ -764,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                 x.states_of(turn, lane) = both(0.f);
                 x.put(turn, lane, both(0.f), both(0.f));
             } else {
-                if (!broken) broken = !mbar_wait(&x.full[s], k / kStages & 1, a.dev_err);
+                if (!mbar_wait(&x.full[s], k / kStages & 1, a.dev_err)) broken = true;
                 auto in = [&](int which, int j) { return v.input(which, j); };
                 auto summed = [&](float2 sum) {
                     sum = mul_pair(sum, both(gb.g_min));
@@ -804,13 +808,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
                 }
             }
             if (threadIdx.x == 0) bulk_wait_read0();  // (the stage before this one is free)
-            __syncthreads();
+            if (__syncthreads_or(broken)) break;
             if (warp < kCarriers) exchange(x, steps, k, threadIdx.x, broken, a.dev_err);
-            load(k + kAhead);  // (by another warp)
-            put(k + kAhead);
+            fill(k + kAhead);  // (by another warp)
             edge = edge_at(k + 1);
             const uint32_t coming = marks_at(k + 1);
-            if (!broken) broken = !mbar_wait(&x.states, k & 1, a.dev_err);
+            if (!mbar_wait(&x.states, k & 1, a.dev_err)) broken = true;
             float2 nr = x.states_of(turn, lane), dA = both(0.f);
             // a token's gradients but for the state's
             auto take = [&](int j, float2 l, IO* dx, IO* dz, IO* di) {
@@ -868,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_bwd_kernel(
             marks = coming;
         }
         if (threadIdx.x == 0) bulk_wait0();
-        close_maps(x, steps.own(), broken, a.dev_err);
+        close_maps(x, steps, k, kAhead, broken, a.dev_err);
     }
     if (part == nullptr) return;
     // the CTA's dA_log: over the warps, in a fixed order

@@ -59,3 +59,24 @@ def test_every_copy_on_its_way_is_waited_for(fills, stages):
                     # one copy of a stage at most is not waited for yet, the last: its phase's parity
                     late = [k for k in mine if k >= waited]
                     assert len(late) <= 1 and late == mine[len(mine) - len(late):]
+
+
+@pytest.mark.parametrize("stages,ahead", [(2, 2), (3, 2)])
+def test_fills_of_a_scan_that_leaves_its_steps(fills, stages, ahead):
+    """The scans of the channel recurrence fill a stage behind the barrier of every step that they stay
+    in; one that leaves at step k has started min(k + ahead, its tiles) fills.  All of those whose phase
+    no step before k has seen end are the last ones of their stages, and no stage has two."""
+    for tiles in range(0, 30):
+        for steps in range(tiles, tiles + 2):  # (a step at the end may have no tile for this CTA)
+            for k in range(steps + 1):
+                started = list(range(min(ahead, tiles)))
+                for step in range(k):
+                    if step + ahead < tiles:
+                        started.append(step + ahead)
+                loads = min(k + ahead, tiles)
+                assert started == list(range(loads))
+                for s in range(stages):
+                    mine = [t for t in started if t % stages == s]
+                    late = [t for t in mine if t >= k]
+                    assert fills[stages, loads, s] == len(mine)
+                    assert len(late) <= 1 and late == mine[len(mine) - len(late):]
