@@ -33,6 +33,7 @@ constexpr int kV = 8;          // channels a thread
 constexpr int kMaxWarps = 32;  // of a CTA: kMaxBlockNormD / kV threads
 constexpr int kWide = 4096;    // the gradients of wider rows take 16 channels a thread
 constexpr int kMaxStages = 8;
+constexpr int kSmem = 227 * 1024, kStatic = 3 * 1024;  // an SM's shared memory, a CTA's beside its ring
 
 template <typename T>
 struct Raw;  // 8 values as they are in memory
@@ -536,12 +537,14 @@ cudaError_t backward_of(const BlockNormArgs& a, float* part, int grid) {
     const Places at = places<IO, R>(a.D, a.post_norm || a.gate || a.dscale, a.gate, a.dr);
     // the rows that an SM's shared memory holds, in equal parts
     const int per_sm = (grid + 151) / 152;
-    int stages = (227 * 1024 / per_sm - 3 * 1024) / at.bytes;
+    int stages = (kSmem / per_sm - kStatic) / at.bytes;
     if (stages > kMaxStages) stages = kMaxStages;
     if (stages < 1) return cudaErrorInvalidValue;
     const int smem = stages * at.bytes;
     auto kernel = norm_bwd_kernel<IO, R, kG>;
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem))
+    // (the same limit whatever the size: another thread may be between this and its launch)
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmem - kStatic))
         return e;
     ProfScope prof("block_norm_bwd_kernel", a.stream);
     kernel<<<grid, threads, smem, a.stream>>>(a, part, stages, a.dev_err);
