@@ -344,7 +344,7 @@ kda_status_t kda_qk_norm_rope_bwd(const void *q, int64_t q_ld, const void *k, in
  *   - x, z, i and dy are [T, D] io_dt with a token stride of ld elements (ld >= D, a multiple of 16
  *     bytes), so views of a fused projection's output can be passed as they are; every tensor
  *     written is contiguous.  D is a multiple of 8 (KDA_ERR_UNSUPPORTED otherwise).
- *   - A_log [D], the states [N, D] and the edges are fp32.
+ *   - A_log [D], the states [N, D] and the edges are fp32.  N D is below 2^36.
  *   - 1 - e^{g_t} is exact to 4e-7 of itself, e^{g_t} to 2^-24: of decays below 1e-3, with a g_min
  *     below -7, what is left of a state has fewer exact digits.
  *   - z = -inf leaves the state as it is (for finite x), z = +inf decays it by e^{g_min}.  A token

@@ -432,7 +432,7 @@ static kda_status_t check_linear(int H, int dk, int dv, kda_dtype_t io_dt, int64
     return KDA_OK;
 }
 
-static kda_status_t check_packed(int64_t T_total, int N, int H, const int32_t* cu_seqlens) {
+static kda_status_t check_sequences(int64_t T_total, int N, const int32_t* cu_seqlens) {
     KDA_REQUIRE(N >= 0, "N=%d must be >= 0", N);
     KDA_REQUIRE(T_total >= 0 && T_total < (int64_t)1 << 31, "T_total=%lld must be in [0, 2^31)",
                 (long long)T_total);
@@ -440,9 +440,13 @@ static kda_status_t check_packed(int64_t T_total, int N, int H, const int32_t* c
     KDA_REQUIRE(cu_seqlens != nullptr || N == 0 || T_total % N == 0,
                 "without cu_seqlens T_total=%lld must be a multiple of N=%d", (long long)T_total,
                 N);
+    KDA_OPTIONAL_PTR(cu_seqlens, "cu_seqlens");
+    return KDA_OK;
+}
+static kda_status_t check_packed(int64_t T_total, int N, int H, const int32_t* cu_seqlens) {
+    if (kda_status_t s = check_sequences(T_total, N, cu_seqlens)) return s;
     KDA_REQUIRE((int64_t)N * H * 4 < (int64_t)1 << 31, "N*H=%lld is too large",
                 (long long)N * H);
-    KDA_OPTIONAL_PTR(cu_seqlens, "cu_seqlens");
     return KDA_OK;
 }
 
@@ -695,12 +699,19 @@ static kda_status_t check_ld(int64_t ld, int D, int per16, const char* name) {
     return KDA_OK;
 }
 
+// (rows of states are addressed in 64 bits)
+static kda_status_t check_states(int N, int D) {
+    KDA_REQUIRE((int64_t)N * D < (int64_t)1 << 36, "N*D=%lld is too large", (long long)N * D);
+    return KDA_OK;
+}
+
 // What the forward and both backward entries share, the workspace excepted.
 static kda_status_t check_recurrence(const kda::RecurrenceArgs& a, kda_dtype_t io_dt) {
     KDA_REQUIRE(io_dt == KDA_F32 || io_dt == KDA_BF16, "io_dt=%d is not a kda_dtype_t", (int)io_dt);
     if (kda_status_t s = check_width(a.D)) return s;
     if (kda_status_t s = check_gmin(a.g_min)) return s;
-    if (kda_status_t s = check_packed(a.T_total, a.N, a.D, a.cu_seqlens)) return s;
+    if (kda_status_t s = check_sequences(a.T_total, a.N, a.cu_seqlens)) return s;
+    if (kda_status_t s = check_states(a.N, a.D)) return s;
     // (tokens are counted in 32 bits, those of tiles behind the last one too)
     KDA_REQUIRE(a.T_total < ((int64_t)1 << 31) - 2048, "T_total=%lld must be below 2^31 - 2048",
                 (long long)a.T_total);
@@ -847,7 +858,7 @@ kda_status_t kda_recurrence_step(const void* x, int64_t x_ld, const void* z, int
     if (kda_status_t s = check_ld(z_ld, D, per16, "z_ld")) return s;
     if (kda_status_t s = check_ld(i_ld, D, per16, "i_ld")) return s;
     KDA_REQUIRE(N >= 0, "N=%d must be >= 0", N);
-    KDA_REQUIRE((int64_t)N * D < (int64_t)1 << 36, "N*D=%lld is too large", (long long)N * D);
+    if (kda_status_t s = check_states(N, D)) return s;
     KDA_REQUIRE(n_slots >= 0, "n_slots=%d must be >= 0", n_slots);
     KDA_REQUIRE(slots != nullptr || n_slots >= N, "n_slots=%d must be at least N=%d without slots",
                 n_slots, N);
