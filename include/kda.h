@@ -345,8 +345,10 @@ kda_status_t kda_qk_norm_rope_bwd(const void *q, int64_t q_ld, const void *k, in
  *     bytes), so views of a fused projection's output can be passed as they are; every tensor
  *     written is contiguous.  D is a multiple of 8 (KDA_ERR_UNSUPPORTED otherwise).
  *   - A_log [D], the states [N, D] and the edges are fp32.  N D is below 2^36.
- *   - 1 - e^{g_t} is exact to 4e-7 of itself, e^{g_t} to 2^-24: of decays below 1e-3, with a g_min
- *     below -7, what is left of a state has fewer exact digits.
+ *   - 1 - e^{g_t} is off by at most 1e-6 + 2.6e-7 |e^{A_log} z_t| of itself (a gate below 2^-126 is
+ *     zero), e^{g_t} by at most 6e-7 + 1e-7 |e^{A_log} z_t|: an absolute bound, so what a decay far
+ *     below one leaves of a state, and the gradient that z gets from it, have fewer exact digits (a
+ *     decay of 7e-3, which g_min = -5 reaches, about four).
  *   - z = -inf leaves the state as it is (for finite x), z = +inf decays it by e^{g_min}.  A token
  *     whose input is not finite spoils its channel of its sequence from there on (the gradients also
  *     before it), and nothing else but the sum dA_log.
