@@ -844,9 +844,7 @@ static cudaError_t launch_fast(const QbFast& f, const float* s, const float* b, 
     if (e == cudaSuccess) e = launch_alpha(s, b, m, n, k, alpha, sms, stream);
     if (e != cudaSuccess) return e;
     {
-        const int smem = f.S * 4;
-        e = cudaFuncSetAttribute(qb_bracket_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+        const int smem = f.S * 4;  // (below 16 KiB: within every kernel's limit as it is)
         ProfScope prof("qb_bracket_kernel", stream);
         e = launch_dependent(qb_bracket_kernel, dim3(n), dim3(256), smem, stream, s,
                              (const float*)alpha, n, f.sshift, f.S, r_hi, r_lo, brk);
