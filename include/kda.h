@@ -344,7 +344,8 @@ kda_status_t kda_qk_norm_rope_bwd(const void *q, int64_t q_ld, const void *k, in
  *   - x, z, i and dy are [T, D] io_dt with a token stride of ld elements (ld >= D, a multiple of 16
  *     bytes), so views of a fused projection's output can be passed as they are; every tensor
  *     written is contiguous.  D is a multiple of 8 (KDA_ERR_UNSUPPORTED otherwise).
- *   - A_log [D], the states [N, D] and the edges are fp32.  N D is below 2^36.
+ *   - A_log [D], the states [N, D] and the edges are fp32.  N D is below 2^36.  e^{A_log} g_min is a
+ *     finite number of fp32.
  *   - 1 - e^{g_t} is off by at most 1e-6 + 2.6e-7 |e^{A_log} z_t| of itself (a gate below 2^-126 is
  *     zero), e^{g_t} by at most 6e-7 + 1e-7 |e^{A_log} z_t|: an absolute bound, so what a decay far
  *     below one leaves of a state, and the gradient that z gets from it, have fewer exact digits (a

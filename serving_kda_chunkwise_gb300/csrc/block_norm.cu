@@ -17,9 +17,10 @@
 // All sums are fp32; the only rounding to fewer bits is that of the results.
 //   Bound by memory: 32,768 x 4096 in bf16 with gate, scale and both norms 201 us, 6.7 TB/s, the copy
 // rate (rows read a second time after the first mean: 1,112 us); gradients with the residual stream in
-// fp32 440 us, 6.7 TB/s (plain loads instead of bulk copies 703; six sums by six shuffle reductions
-// 532), all in bf16 396 us, 5.4 TB/s, and of rows of 8192 451 us (16,384 rows), 4.8 TB/s: one CTA an SM,
-// whose barrier a row no other covers.
+// fp32 437 us, 6.8 TB/s (plain loads instead of bulk copies 703; six sums by six shuffle reductions
+// 532), all in bf16 395 us, 5.4 TB/s, and of rows of 8192 459 us (16,384 rows), 4.7 TB/s: one CTA an SM,
+// whose barrier a row no other covers.  With an fp32 residual 298 us (6.3 TB/s), in fp32 227 us (16,384 x
+// 4096, 5.9 TB/s): there the 64 registers that 1,024 threads leave spill 4 and 12 bytes.
 #include "kda_common.cuh"
 #include "kda_internal.h"
 #include "tc_util.cuh"
@@ -527,7 +528,7 @@ cudaError_t forward(const BlockNormArgs& a) {
     return cudaGetLastError();
 }
 
-// CTAs of the gradients, 128 registers a thread and up to four an SM, and their threads.
+// CTAs of the gradients, 128 registers a thread and 512 threads an SM, and their threads.
 int bwd_threads(int D) { return threads_for(D, D > kWide ? 2 : 1); }
 int bwd_blocks(int64_t T, int D) { return blocks_for(T, bwd_threads(D), 512); }
 

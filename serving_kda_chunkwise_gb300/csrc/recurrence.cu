@@ -11,7 +11,7 @@
 // into distributed shared memory that count their bytes on a barrier there) and carry the state over
 // the cluster's maps; then every warp goes over its tokens again, in registers, and writes.  So inputs
 // are read once (by the copy engine, steps ahead), results written once, in rows of 128 bytes (bf16),
-// and no cluster waits for another.  Ways that were slower at 65,536 x 4096 (now 449 us): a look-back
+// and no cluster waits for another.  Ways that were slower at 65,536 x 4096 (now 443 us): a look-back
 // over tiles by messages in memory, 890 us; columns of 16 channels without clusters, 715 us, for the
 // copies of 32-byte rows; 8 tokens a warp instead of 16, 531 us; CTAs of 4 or 16 warps, 580 and 880 us.
 //
@@ -22,10 +22,11 @@
 //
 // Bound by instructions (two a cycle and SM, of which the pairs' take two cycles), by the exchange
 // between a step's two passes, and by the clusters' being 256 CTAs for 152 SMs: the forward of
-// 65,536 x 4096 in bf16 449 us, 4.8 TB/s (its special functions alone would be 190 us, its memory 322);
-// gradients from edges of 32,768 x 4096 435 us, 120 instructions for two channels of a token; from
-// 8-bit inputs of 65,536 x 2048 260 us for the edges and 525 us (1,610 with 12 bytes of spilled
-// registers: tiles leave the first-level cache nothing, so nothing may spill within the steps).
+// 65,536 x 4096 in bf16 443 us, 4.8 TB/s (its special functions alone would be 190 us, its memory 322);
+// gradients from edges of 32,768 x 4096 430 us, 120 instructions for two channels of a token; from
+// 8-bit inputs of 65,536 x 2048 257 us for the edges and 522 us.  (Spills within the steps cost much,
+// for tiles leave the first-level cache nothing: 12 bytes 1,610 us.  The 4 bytes that the compiler
+// spills of the gradients from 8-bit inputs do not show: without them 524 us.)
 //
 // Sequences: a setup launch finds the tokens with which sequences start and end, 8 at a time, and
 // cuts the batch into runs (one sequence needs none of it, and short forwards of a few do it
@@ -979,9 +980,10 @@ int count_runs(int64_t T, int N, int cols) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(N, T / 1024), most));
 }
 
-// CTAs of a cluster, for tiles of kT tokens: as many as keep all of them on the GPU at once, two an SM;
-// with several runs, one for every 1,024 tokens that a run has on average (24 sequences, 47,139 tokens
-// x 2560: 186 us with two, 197 with one, 199 with four).
+// CTAs of a cluster, for tiles of kT tokens: as many as keep all of them on the GPU at once, counted as
+// two an SM (the gradients into fp32 have one there at a time); with several runs, one for every 1,024
+// tokens that a run has on average.  (That number comes from 24 sequences, 47,139 tokens x 2560: 186 us
+// with two, 197 with one, 199 with four.  Batches much unlike it were not tuned for.)
 int count_ctas(int64_t T, int runs, int cols, int kT) {
     int n = 1;
     while (2 * n <= kMaxCluster && T > (int64_t)kT * n * runs &&
